@@ -28,12 +28,13 @@ __all__ = [
     "DartError", "build", "lib", "NGramTable", "num_nodes", "mask_words", "workspace_bytes",
     "tree_build", "tree_build_noalloc", "tree_from_topk", "tree_from_rows", "row_topk", "mask_pack", "tree_select", "set_wait_limit", "device_error", "noalloc_device_error",
     "TreeBuilder",
+    "adjust_logits", "kv_append", "tree_attention", "attention_workspace_bytes", "Rotary", "rotary_frequencies",
     "DTYPE_CODES",
 ]
 
 DART_OK = 0
 DEVERR = {1: "bulk-copy wait timeout", 2: "row max mismatch", 4: "tree selection", 8: "bad parent",
-          16: "score rises from a parent"}
+          16: "score rises from a parent", 32: "a cache length, slot or page id out of range"}
 
 
 class DartError(RuntimeError):
@@ -119,6 +120,7 @@ def _declare(L):
     L.dart_noalloc_device_error.restype = i32
     L.dart_status_string.argtypes = [i32]
     L.dart_status_string.restype = C.c_char_p
+    _steps.declare(L)
     return L
 
 
@@ -739,3 +741,8 @@ class TreeBuilder:
                                        self.ws.numel(), _stream_ptr(stream, self.device))
         _check(rc, "dart_tree_build")
         return self.out
+
+
+from . import _steps  # noqa: E402  (it builds on the helpers above)
+from ._steps import (Rotary, adjust_logits, attention_workspace_bytes, kv_append, rotary_frequencies,  # noqa: E402
+                     tree_attention)

@@ -1,0 +1,387 @@
+"""The steps around a draft tree: logit adjustment, cache append, tree attention.
+
+Bindings of dart_logits_adjust, dart_kv_append and dart_tree_attention
+(include/darttree.h); the package exports the public names.
+"""
+from __future__ import annotations
+
+import contextlib
+import ctypes as C
+import math
+
+import numpy as np
+
+from . import (DTYPE_CODES, DartError, _check, _check_error_word, _check_tensor, _check_workspace, _device_of,
+               _mask_dtypes, _on_device, _ptr, _row_stride, _stream_ptr, _torch, lib)
+
+
+class _Adjust(C.Structure):
+    _fields_ = [("history", C.c_void_p), ("history_stride", C.c_int64), ("history_width", C.c_int32),
+                ("bias_count", C.c_int32), ("history_len", C.c_void_p), ("repetition", C.c_void_p),
+                ("presence", C.c_void_p), ("frequency", C.c_void_p), ("bias_ids", C.c_void_p),
+                ("bias_vals", C.c_void_p), ("allowed", C.c_void_p), ("allowed_seq_stride", C.c_int64),
+                ("allowed_row_stride", C.c_int64), ("tokens", C.c_void_p), ("mask", C.c_void_p),
+                ("N", C.c_int32), ("reserved", C.c_int32)]
+
+
+class _Cache(C.Structure):
+    _fields_ = [("k", C.c_void_p), ("v", C.c_void_p),
+                *((f"{x}_{y}_stride", C.c_int64) for x in "kv" for y in ("page", "row", "head")),
+                ("table", C.c_void_p), ("table_stride", C.c_int64), ("table_width", C.c_int32), ("pages", C.c_int32),
+                ("page", C.c_int32), ("heads", C.c_int32), ("dim", C.c_int32), ("dtype", C.c_int32)]
+
+
+class _Rotary(C.Structure):
+    _fields_ = [("turns", C.c_void_p), ("magnitude", C.c_float), ("rot", C.c_int32), ("interleaved", C.c_int32),
+                ("reserved", C.c_int32)]
+
+
+def declare(L):
+    P, i32, i64, f32, sz = C.c_void_p, C.c_int, C.c_int64, C.c_float, C.c_size_t
+    L.dart_logits_adjust.argtypes = [P, i32, i32, i32, i64, i32, C.POINTER(_Adjust), P, i64, P]
+    L.dart_logits_adjust.restype = i32
+    L.dart_rotary_pack_host.argtypes = [P, i32, P]
+    L.dart_rotary_pack_host.restype = i32
+    L.dart_kv_append.argtypes = [P, i64, i64, i32, P, i64, i64, P, i64, i64, i32, i32, P, P, P, C.POINTER(_Rotary),
+                                 P, P, f32, C.POINTER(_Cache), P, i64, i64, P, P]
+    L.dart_kv_append.restype = i32
+    L.dart_attention_workspace_bytes.argtypes = [i32, i32, i32, i32, i32]
+    L.dart_attention_workspace_bytes.restype = sz
+    L.dart_tree_attention.argtypes = [P, i64, i64, i32, i32, i32, P, P, P, i32, f32, C.POINTER(_Cache), P, i64, i64,
+                                      P, P, sz, P]
+    L.dart_tree_attention.restype = i32
+
+
+def _strides(t):
+    """Element strides, 0 for a dimension that is never stepped along."""
+    return [st if size > 1 else 0 for size, st in zip(t.shape, t.stride())]
+
+
+@contextlib.contextmanager
+def _launching(dev, stream):
+    """The tensors' device, and the stream that the call launches on: what the
+    call allocates and clears itself is ordered with its kernels there."""
+    with _on_device(dev):
+        _stream_ptr(stream, dev)
+        with _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+            yield
+
+
+def _check_inner(t, name):
+    if t.shape[-1] > 1 and t.stride(-1) != 1:
+        raise DartError(f"{name} must have unit stride in its last dimension")
+
+
+# --------------------------------------------------------- logit adjustment
+
+def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presence=None, frequency=None, bias=None,
+                  allowed=None, tokens=None, mask=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and a grammar mask (dart_logits_adjust).
+
+    logits: CUDA [B, R, V] float32/float16/bfloat16, rows evenly spaced (a view
+    of a padded vocabulary serves): draft rows, or the verified rows of a tree.
+    history: int32 [B, H], of which lengths (int32 [B]) entries count; ids
+    outside [0, V) do not.  repetition, presence, frequency: float32 [B].
+    bias: (ids int32 [B, K], values float32 [B, K]).  allowed: packed bits,
+    int32 (or uint32) [B, ceil(V/32)] or [B, R, ceil(V/32)].  tokens (int32
+    [B, N]) and mask (int32 [B, N, ceil(N/32)]) of a tree, as tree_build
+    returns them, let row R - N + i count the tokens on node i's path too; R
+    is N or N + 1.  Returns the adjusted logits: out, which may be logits
+    itself, or a new [B, R, V] tensor with evenly spaced rows."""
+    torch = _torch()
+    ids, vals = bias if bias is not None else (None, None)
+    dev = _device_of(("logits", logits), ("history", history), ("lengths", lengths), ("repetition", repetition),
+                     ("presence", presence), ("frequency", frequency), ("bias ids", ids), ("bias values", vals),
+                     ("allowed", allowed), ("tokens", tokens), ("mask", mask), ("out", out))
+    codes = DTYPE_CODES()
+    if logits.dtype not in codes or logits.dim() != 3:
+        raise DartError("logits must be [B, R, V] float32, float16 or bfloat16")
+    B, R, V = logits.shape
+    if V < 1:
+        raise DartError("logits must have at least one token")
+    stride = _row_stride(logits)
+    a = _Adjust()
+    if history is not None:
+        if history.dim() != 2 or history.shape[0] != B:
+            raise DartError(f"history must be [{B}, H]")
+        _check_tensor(history, "history", torch.int32, contiguous=False)
+        _check_inner(history, "history")
+        a.history, a.history_width = _ptr(history), history.shape[1]
+        a.history_stride = history.stride(0) if B > 1 else history.shape[1]
+        if B > 1 and a.history_stride < history.shape[1]:
+            raise DartError("history rows overlap")
+    elif lengths is not None:
+        raise DartError("lengths are given without a history")
+    _check_tensor(lengths, "lengths", torch.int32, (B,))
+    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
+        _check_tensor(t, name, torch.float32, (B,))
+    a.history_len = _ptr(lengths)
+    a.repetition, a.presence, a.frequency = _ptr(repetition), _ptr(presence), _ptr(frequency)
+    if ids is not None:
+        if vals is None or ids.dim() != 2 or ids.shape[0] != B:
+            raise DartError(f"bias must be (ids [{B}, K], values [{B}, K])")
+        _check_tensor(ids, "bias ids", torch.int32)
+        _check_tensor(vals, "bias values", torch.float32, tuple(ids.shape))
+        a.bias_ids, a.bias_vals, a.bias_count = _ptr(ids), _ptr(vals), ids.shape[1]
+    if allowed is not None:
+        words = (V + 31) // 32
+        if tuple(allowed.shape) not in ((B, words), (B, R, words)):
+            raise DartError(f"allowed must be [{B}, {words}] or [{B}, {R}, {words}], got {tuple(allowed.shape)}")
+        _check_tensor(allowed, "allowed", _mask_dtypes(), contiguous=False)
+        _check_inner(allowed, "allowed")
+        st = _strides(allowed)
+        a.allowed, a.allowed_seq_stride = _ptr(allowed), st[0]
+        a.allowed_row_stride = st[1] if allowed.dim() == 3 else 0
+    if (tokens is None) != (mask is None):
+        raise DartError("a tree needs both its tokens and its mask")
+    if tokens is not None:
+        if tokens.dim() != 2 or tokens.shape[0] != B:
+            raise DartError(f"tokens must be [{B}, N]")
+        N = tokens.shape[1]
+        _check_tensor(tokens, "tokens", torch.int32)
+        _check_tensor(mask, "mask", _mask_dtypes(), (B, N, (N + 31) // 32))
+        if R not in (N, N + 1):
+            raise DartError(f"a tree of {N} nodes needs {N} or {N + 1} rows of logits, got {R}")
+        a.tokens, a.mask, a.N = _ptr(tokens), _ptr(mask), N
+    if out is not None:
+        _check_tensor(out, "out", logits.dtype, (B, R, V), contiguous=False)
+        out_stride = _row_stride(out)
+        if out.data_ptr() == logits.data_ptr() and out_stride != stride and B * R > 1:
+            raise DartError("out shares its first element with logits, but not its rows")
+    with _launching(dev, stream):
+        if out is None:
+            # rows that keep the input's alignment take whole vectors from end to end
+            out_stride = V + (stride - V) % (16 // logits.element_size())
+            out = torch.empty((B, R, out_stride), dtype=logits.dtype, device=dev)[..., :V]
+        rc = lib().dart_logits_adjust(_ptr(logits), B, R, V, stride, codes[logits.dtype], C.byref(a), _ptr(out),
+                                      out_stride, _stream_ptr(stream, dev))
+    _check(rc, "dart_logits_adjust")
+    return out
+
+
+# ------------------------------------------------------------- paged caches
+
+def _cache(k_cache, v_cache, pages, B):
+    """The descriptor of caches [P, page, heads, dim] with a page table [B, width]."""
+    torch = _torch()
+    if k_cache.dim() != 4 or v_cache.dim() != 4 or tuple(k_cache.shape) != tuple(v_cache.shape):
+        raise DartError("k_cache and v_cache must both be [pages, page, heads, dim]")
+    if k_cache.dtype not in (torch.float16, torch.bfloat16) or v_cache.dtype != k_cache.dtype:
+        raise DartError("k_cache and v_cache must both be float16 or bfloat16")
+    if pages.dim() != 2 or pages.shape[0] != B:
+        raise DartError(f"pages must be [{B}, width]")
+    _check_tensor(pages, "pages", torch.int32, contiguous=False)
+    _check_inner(pages, "pages")
+    c = _Cache()
+    for t, x in ((k_cache, "k"), (v_cache, "v")):
+        _check_inner(t, f"{x}_cache")
+        setattr(c, x, t.data_ptr())
+        for name, st in zip(("page", "row", "head"), _strides(t)):
+            if st % 8:
+                raise DartError(f"{x}_cache strides must be multiples of 8 elements")
+            setattr(c, f"{x}_{name}_stride", st)
+    c.pages, c.page, c.heads, c.dim = k_cache.shape
+    if c.page < 8 or c.page % 8:
+        raise DartError(f"pages must hold a multiple of 8 positions, got {c.page}")
+    if not 8 <= c.dim <= 128 or c.dim % 8:
+        raise DartError(f"heads must have a multiple of 8 elements, 8 to 128, got {c.dim}")
+    c.dtype = DTYPE_CODES()[k_cache.dtype]
+    c.table, c.table_width = _ptr(pages), pages.shape[1]
+    c.table_stride = pages.stride(0) if B > 1 else pages.shape[1]
+    if B > 1 and c.table_stride < pages.shape[1]:
+        raise DartError("the rows of pages overlap")
+    return c
+
+
+def _heads(t, name, T, heads, dim, dtype):
+    """A [T, heads, dim] tensor of vectors: its (token, head) strides."""
+    _check_tensor(t, name, dtype, (T, heads, dim), contiguous=False)
+    _check_inner(t, name)
+    st = _strides(t)
+    if st[0] % 8 or st[1] % 8 or t.data_ptr() % 16:
+        raise DartError(f"{name} must be 16-byte aligned, with strides of multiples of 8 elements")
+    return st[0], st[1]
+
+
+def _no_overlap(t, name):
+    """Outputs whose elements share memory (an expanded tensor) are refused."""
+    if t.numel() > 1 and any(size > 1 and st == 0 for size, st in zip(t.shape, t.stride())):
+        raise DartError(f"{name} must not be an expanded tensor")
+
+
+def _sequences(lengths, starts):
+    torch = _torch()
+    if lengths.dim() != 1:
+        raise DartError("lengths must be [B]")
+    B = lengths.shape[0]
+    _check_tensor(lengths, "lengths", torch.int32)
+    _check_tensor(starts, "starts", torch.int32, (B + 1,))
+    return B
+
+
+class Rotary:
+    """Rotary positions for kv_append: pair j of a head turns by position * freqs[j].
+
+    freqs: rot / 2 radians per position (float64; see rotary_frequencies), rot
+    the elements of each head that turn, the rest staying as they are.
+    magnitude scales the turned elements.  interleaved: pairs (2j, 2j + 1)
+    instead of (j, j + rot / 2)."""
+
+    def __init__(self, freqs, magnitude: float = 1.0, interleaved: bool = False, device="cuda"):
+        freqs = np.ascontiguousarray(freqs, dtype=np.float64).reshape(-1)
+        if freqs.size < 8 or freqs.size % 8 or freqs.size > 64:
+            raise DartError("freqs must hold 8, 16, .. 64 values (rot / 2, rot a multiple of 16)")
+        if not math.isfinite(magnitude):
+            raise DartError("magnitude must be finite")
+        turns = np.empty(freqs.size, dtype=np.uint64)
+        _check(lib().dart_rotary_pack_host(freqs.ctypes.data_as(C.c_void_p), freqs.size,
+                                           turns.ctypes.data_as(C.c_void_p)), "dart_rotary_pack_host")
+        self.freqs, self.magnitude, self.interleaved = freqs, float(magnitude), bool(interleaved)
+        self.rot = 2 * freqs.size
+        self.turns = _torch().from_numpy(turns.view(np.int64)).to(device)
+        self.desc = _Rotary(self.turns.data_ptr(), self.magnitude, self.rot, int(self.interleaved), 0)
+
+
+def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, original: int | None = None,
+                       fast: float = 32.0, slow: float = 1.0):
+    """(freqs float64 [rot / 2], magnitude) of rotary positions: base^(-2j / rot).
+
+    factor > 1 stretches them for contexts that are `factor` times longer:
+    without `original` every frequency is divided by factor (magnitude 1); with
+    it (the length that the model was trained on), a pair that turns more than
+    `fast` times within `original` positions keeps its frequency, one that turns
+    less than `slow` times is divided by factor, those between are blended
+    linearly in their number of turns, and the magnitude is 0.1 ln(factor) + 1."""
+    if rot < 2 or rot % 2 or not base > 0 or not factor >= 1:
+        raise DartError("rot must be even, base > 0 and factor >= 1")
+    f = float(base) ** (-np.arange(rot // 2, dtype=np.float64) / (rot // 2))
+    if factor == 1.0 or original is None:
+        return f / factor, 1.0
+    if not fast > slow:
+        raise DartError("fast must exceed slow")
+    keep = np.clip((original * f / (2 * math.pi) - slow) / (fast - slow), 0.0, 1.0)
+    return f * keep + f / factor * (1.0 - keep), 0.1 * math.log(factor) + 1.0
+
+
+def kv_append(q, k, v, k_cache, v_cache, pages, lengths, starts, *, rotary: Rotary | None = None, offsets=None,
+              q_weight=None, k_weight=None, eps: float = 1e-6, out=None, device_err=None, stream=None):
+    """Appends a chunk's keys and values to a paged cache (dart_kv_append).
+
+    q: CUDA [T, q_heads, dim] or None; k, v: [T, heads, dim] (views of one
+    projection's output serve); k_cache, v_cache: [pages, page, heads, dim],
+    float16 or bfloat16 like q, k and v, written in place; pages: int32 [B,
+    width], the page of each sequence's positions; lengths: int32 [B] tokens in
+    the cache before the chunk; starts: int32 [B + 1], sequence b's tokens being
+    rows starts[b] .. starts[b + 1] (rows outside are left alone).  q_weight,
+    k_weight ([dim]) apply the norm of each head, rotary the turn by position
+    lengths[b] + index in the chunk, or lengths[b] + offsets[row] (int32 [T]; a
+    tree's nodes: 1 + their lead's last offset, counted by tree_build's pos).
+    Returns the finished queries: out, which may be q itself, or a new tensor
+    whose rows outside every sequence are unset (None without q).  device_err (int32 [>= 1], zeroed by the caller) collects
+    the error bits of tokens that do not fit in their pages."""
+    torch = _torch()
+    dev = _device_of(("k", k), ("v", v), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("pages", pages),
+                     ("lengths", lengths), ("starts", starts), ("rotary", rotary.turns if rotary is not None else None),
+                     ("offsets", offsets), ("q_weight", q_weight), ("k_weight", k_weight), ("out", out),
+                     ("device_err", device_err))
+    B = _sequences(lengths, starts)
+    c = _cache(k_cache, v_cache, pages, B)
+    _no_overlap(k_cache, "k_cache")
+    _no_overlap(v_cache, "v_cache")
+    if k.dim() != 3:
+        raise DartError("k must be [T, heads, dim]")
+    T, dt = k.shape[0], k_cache.dtype
+    ks, vs = _heads(k, "k", T, c.heads, c.dim, dt), _heads(v, "v", T, c.heads, c.dim, dt)
+    qs = os = (0, 0)
+    Hq = 0
+    if q is not None:
+        if q.dim() != 3:
+            raise DartError("q must be [T, q_heads, dim]")
+        Hq = q.shape[1]
+        qs = _heads(q, "q", T, Hq, c.dim, dt)
+        if out is not None:
+            os = _heads(out, "out", T, Hq, c.dim, dt)
+            _no_overlap(out, "out")
+            if out.data_ptr() == q.data_ptr() and os != qs:
+                raise DartError("out shares its first element with q, but not its strides")
+    elif out is not None or q_weight is not None:
+        raise DartError("out or q_weight is given without q")
+    _check_tensor(offsets, "offsets", torch.int32, (T,))
+    _check_tensor(q_weight, "q_weight", dt, (c.dim,))
+    _check_tensor(k_weight, "k_weight", dt, (c.dim,))
+    if rotary is not None and rotary.rot > c.dim:
+        raise DartError(f"rotary turns {rotary.rot} elements of heads of {c.dim}")
+    _check_error_word(device_err)
+    with _launching(dev, stream):
+        if q is not None and out is None:
+            out = torch.empty((T, Hq, c.dim), dtype=dt, device=dev)
+            os = _heads(out, "out", T, Hq, c.dim, dt)
+        rc = lib().dart_kv_append(_ptr(q), *qs, Hq, _ptr(k), *ks, _ptr(v), *vs, T, B, _ptr(lengths), _ptr(starts),
+                                  _ptr(offsets), C.byref(rotary.desc) if rotary is not None else None,
+                                  _ptr(q_weight), _ptr(k_weight), float(eps), C.byref(c), _ptr(out), *os,
+                                  _ptr(device_err), _stream_ptr(stream, dev))
+    _check(rc, "dart_kv_append")
+    return out
+
+
+# ------------------------------------------------------------ tree attention
+
+def attention_workspace_bytes(T: int, B: int, q_heads: int, heads: int, dim: int) -> int:
+    return lib().dart_attention_workspace_bytes(T, B, q_heads, heads, dim)
+
+
+def tree_attention(q, k_cache, v_cache, pages, lengths, starts, *, mask=None, scale: float | None = None, out=None,
+                   lse: bool = False, workspace=None, stream=None) -> dict:
+    """Attention of a chunk over the paged cache that holds it (dart_tree_attention).
+
+    q: CUDA [T, q_heads, dim] float16 or bfloat16 like the caches (as kv_append
+    returns it); k_cache, v_cache, pages, lengths, starts as for kv_append,
+    which has written the chunk's own keys and values.  Without a mask every
+    token sees the positions up to its own.  mask (int32 [B, N, ceil(N/32)], as
+    tree_build returns it) makes the last N tokens of each chunk a tree, each
+    node seeing the context, the tokens before the tree and its own path.
+    scale defaults to 1 / sqrt(dim).  Returns out [T, q_heads, dim] (a new
+    tensor's rows outside every sequence are unset), lse (float32 [T, q_heads]
+    with lse=True, else None) and the workspace, whose error bits device_error
+    reads.  A workspace is reused by calls in order on one stream; calls that
+    may overlap need one each."""
+    torch = _torch()
+    dev = _device_of(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("pages", pages), ("lengths", lengths),
+                     ("starts", starts), ("mask", mask), ("out", out), ("workspace", workspace))
+    B = _sequences(lengths, starts)
+    c = _cache(k_cache, v_cache, pages, B)
+    if q.dim() != 3:
+        raise DartError("q must be [T, q_heads, dim]")
+    T, Hq = q.shape[:2]
+    qs = _heads(q, "q", T, Hq, c.dim, k_cache.dtype)
+    if Hq < 1 or Hq % c.heads:
+        raise DartError(f"{Hq} query heads do not share {c.heads} key heads evenly")
+    N = 0
+    if mask is not None:
+        if mask.dim() != 3 or mask.shape[0] != B or mask.shape[2] != (mask.shape[1] + 31) // 32:
+            raise DartError(f"mask must be [{B}, N, ceil(N / 32)]")
+        N = mask.shape[1]
+        _check_tensor(mask, "mask", _mask_dtypes())
+    if out is not None:
+        os = _heads(out, "out", T, Hq, c.dim, q.dtype)
+        _no_overlap(out, "out")
+        if out.numel() and out.data_ptr() == q.data_ptr():
+            raise DartError("out must not be q")
+    need = attention_workspace_bytes(T, B, Hq, c.heads, c.dim)
+    if workspace is not None:
+        _check_workspace(workspace, need)
+    with _launching(dev, stream):
+        if out is None:
+            out = torch.empty((T, Hq, c.dim), dtype=q.dtype, device=dev)
+            os = _heads(out, "out", T, Hq, c.dim, q.dtype)
+        ws = workspace
+        if ws is None:
+            ws = torch.empty(need, dtype=torch.uint8, device=dev)
+            ws[:256].zero_()
+        sums = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse else None
+        rc = lib().dart_tree_attention(_ptr(q), *qs, Hq, T, B, _ptr(lengths), _ptr(starts), _ptr(mask), N,
+                                       1.0 / math.sqrt(c.dim) if scale is None else float(scale), C.byref(c),
+                                       _ptr(out), *os, _ptr(sums), _ptr(ws), ws.numel() * ws.element_size(),
+                                       _stream_ptr(stream, dev))
+    _check(rc, "dart_tree_attention")
+    return dict(out=out, lse=sums, workspace=ws)

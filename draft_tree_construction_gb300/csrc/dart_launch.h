@@ -60,4 +60,7 @@ cudaError_t launch_ngram_lookup(const void* slots, unsigned long long capacity, 
                                 const int32_t* keys, long long Q, float* vals, int32_t* found,
                                 cudaStream_t stream);
 
+// Argument checks of a paged cache shared by B sequences.
+int check_cache(const dart_cache_t* c, int B);
+
 }  // namespace dart

@@ -77,8 +77,10 @@ enum {
   DART_DEVERR_ROW_MAX = 1u << 1,       /* a row's maximum and its best candidate disagreed */
   DART_DEVERR_SELECT = 1u << 2,        /* the tree selection produced an invalid candidate */
   DART_DEVERR_PARENT = 1u << 3,        /* dart_mask_pack / dart_tree_select: a parent index was not below its child */
-  DART_DEVERR_SCORE_RISES = 1u << 4    /* dart_tree_select: a node outscored its parent (the result is the M best,
+  DART_DEVERR_SCORE_RISES = 1u << 4,   /* dart_tree_select: a node outscored its parent (the result is the M best,
                                           which best-first need not take) */
+  DART_DEVERR_CACHE = 1u << 5          /* dart_kv_append / dart_tree_attention: a length, slot or page id is out of
+                                          range (the access is left out) */
 };
 
 /* An n-gram model in device memory: a two-choice bucketed hash table.
@@ -354,6 +356,159 @@ int dart_tree_select(const int32_t* tokens, const int32_t* parents, const int32_
                      const float* scores, int B, int N, int M, int32_t* out_index,
                      int32_t* out_tokens, int32_t* out_parents, int32_t* out_pos,
                      uint32_t* out_mask, float* out_scores, uint32_t* device_err, void* stream);
+
+/* ---------------------------------------------------------------- around the tree
+ * The steps that a serving loop takes before a tree is built and after it:
+ * logits are adjusted (dart_logits_adjust), a chunk's keys and values enter
+ * a paged cache (dart_kv_append), and the chunk attends to that cache with
+ * the tree's ancestor masks (dart_tree_attention; DART, Figure 3 caption:
+ * "verify them in target model with Tree Attention").
+ *
+ * A chunk is a sequence's new tokens, sequence b's being rows starts[b] ..
+ * starts[b+1] of a [T] axis; rows outside every sequence are left untouched.
+ * Its last N tokens may be a tree of N nodes in dart_tree_build's order; the
+ * lead before them (lead = max(length - N, 0) tokens, say the root) is
+ * causal.  A chunk shorter than N holds the tree's first nodes. */
+
+/* What dart_logits_adjust does to the logits; NULL / 0 leaves a part out. */
+typedef struct {
+  const int32_t* history;        /* device [B][history_width], rows history_stride apart: tokens so far; ids outside
+                                    [0, V) (padding) are not counted */
+  int64_t history_stride;
+  int32_t history_width;
+  int32_t bias_count;            /* entries per sequence, 0..1024 */
+  const int32_t* history_len;    /* device [B]: entries in use (limited to 0..history_width), or NULL for all */
+  const float* repetition;       /* device [B], > 0: a counted token's z becomes z / r if z > 0, else z * r */
+  const float* presence;         /* device [B]: subtracted once from a counted token */
+  const float* frequency;        /* device [B]: subtracted as many times as the token is counted */
+  const int32_t* bias_ids;       /* device [B][bias_count]; ids outside [0, V) are ignored */
+  const float* bias_vals;        /* device [B][bias_count]; the values of a repeated id add up, in their order */
+  const uint32_t* allowed;       /* device: bit (v & 31) of word (v >> 5) clears token v to keep its logit */
+  int64_t allowed_seq_stride;    /* words from one sequence's masks to the next (0: one for all) */
+  int64_t allowed_row_stride;    /* words from one row's mask to the next (0: one per sequence) */
+  const int32_t* tokens;         /* device [B][N]: a tree's tokens, so that row lead + i also counts node i's path */
+  const uint32_t* mask;          /* device [B][N][ceil(N/32)]: the tree's ancestor-or-self masks (bits from N up and
+                                    tokens outside [0, V) are not counted) */
+  int32_t N;                     /* 0..1024; with a tree R is N (the nodes' rows) or N + 1 (the root's row first) */
+  int32_t reserved;              /* must be 0 */
+} dart_adjust_t;
+
+/* Penalties for repeated tokens, biases and grammar masks on logits: draft
+ * rows before dart_tree_build, or the verified rows of a tree.  For row r of
+ * sequence b and token v, with cnt its occurrences in the history and on the
+ * row's path:
+ *   x = z;  if cnt > 0:  x = (z > 0 ? z / repetition : z * repetition)
+ *                            - frequency * cnt - presence
+ *   x = x + (sum of v's biases);  out = v allowed ? x : -inf
+ * in fp32, rounded once to the logits' type.  A token that is neither counted
+ * nor biased keeps its bits (NaN and infinities too); one that is not allowed
+ * gives -inf whatever its logit holds, and a row may lose all of its tokens.
+ *  logits, out  device [B][R] rows of V elements, row_stride / out_stride >= V
+ *               elements apart (at most 2^30); type dtype, element aligned.
+ *               out may be logits itself (in place, the same stride); other
+ *               overlaps are not supported.  The padding behind V is neither
+ *               read nor written.
+ *  B, R >= 0, B <= 65535; V 1..2^24-1
+ *  what         host pointer; its device pointers as described above
+ * Nothing is launched when B or R is 0.  Returns DART_OK or an error code. */
+int dart_logits_adjust(const void* logits, int B, int R, int V, int64_t row_stride, int dtype,
+                       const dart_adjust_t* what, void* out, int64_t out_stride, void* stream);
+
+/* A paged cache of keys and values, each device [pages][page][heads][dim] of
+ * one 16-bit type: element strides as given (multiples of 8, `dim` contiguous),
+ * base 16-byte aligned.  Sequence b's position p is row p % page of page
+ * table[b][p / page]. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_page_stride, k_row_stride, k_head_stride;
+  int64_t v_page_stride, v_row_stride, v_head_stride;
+  const int32_t* table;      /* device [B][table_width], rows table_stride apart */
+  int64_t table_stride;
+  int32_t table_width;       /* pages a sequence can have: positions 0 .. table_width * page - 1 (below 2^31) */
+  int32_t pages;             /* pages in the cache */
+  int32_t page;              /* positions per page, a multiple of 8 */
+  int32_t heads;             /* key / value heads */
+  int32_t dim;               /* elements per head, a multiple of 8, 8..128 */
+  int32_t dtype;             /* DART_F16 or DART_BF16 */
+} dart_cache_t;
+
+/* Rotary positions: at position p, pair j of a head turns by p * freqs[j]
+ * radians and is scaled by `magnitude`.  turns[j] is freqs[j] as a fraction of
+ * a full turn in units of 2^-64 (dart_rotary_pack_host), so that p * turns[j]
+ * in 64-bit arithmetic keeps exactly the part that matters at any position. */
+typedef struct {
+  const uint64_t* turns;     /* device [rot / 2] */
+  float magnitude;           /* finite */
+  int32_t rot;               /* elements of each head that turn: a multiple of 16, 16..dim; the rest stay */
+  int32_t interleaved;       /* 0: pair j is elements (j, j + rot/2); 1: elements (2j, 2j + 1) */
+  int32_t reserved;          /* must be 0 */
+} dart_rotary_t;
+
+/* turns[j] from freqs[j] (host, radians per position, magnitude below 2^31; count values). */
+int dart_rotary_pack_host(const double* freqs, int count, uint64_t* turns);
+
+/* Appends a chunk's keys and values to a paged cache, with the norms of the
+ * queries' and keys' heads and the rotary positions applied on the way.  Token
+ * i of sequence b goes to position lengths[b] + i of the cache and turns by
+ * position lengths[b] + i, or lengths[b] + offsets[row] when offsets are given
+ * (a tree's nodes: the root's offset + dart_tree_build's out_pos).
+ *   x^ = x / sqrt(mean(x^2) + eps) * weight   (heads of q / k with a weight)
+ * then the turn, in fp32, rounded once to the cache's type.
+ *  q, out   device [T][q_heads][dim] (token and head strides in elements,
+ *           multiples of 8; bases 16-byte aligned); out receives the finished
+ *           queries and may be q itself.  q_heads = 0: no queries.
+ *  k, v     device [T][cache->heads][dim], strides as for q
+ *  lengths  device [B], tokens in the cache before the chunk, >= 0
+ *  starts   device [B+1], increasing, starts[b] <= T
+ *  offsets  device [T] or NULL
+ *  rotary   host pointer or NULL (no turn)
+ *  q_weight, k_weight   device [dim] of the cache's type, or NULL (no norm); eps >= 0
+ * A token whose position or page id is out of range writes nothing to the
+ * cache and sets DART_DEVERR_CACHE in *device_err (device uint32 or NULL); its
+ * query is still finished.  Returns DART_OK or an error code. */
+int dart_kv_append(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                   const void* k, int64_t k_token_stride, int64_t k_head_stride,
+                   const void* v, int64_t v_token_stride, int64_t v_head_stride,
+                   int T, int B, const int32_t* lengths, const int32_t* starts, const int32_t* offsets,
+                   const dart_rotary_t* rotary, const void* q_weight, const void* k_weight, float eps,
+                   const dart_cache_t* cache, void* out, int64_t out_token_stride, int64_t out_head_stride,
+                   uint32_t* device_err, void* stream);
+
+/* Device workspace bytes that dart_tree_attention needs for these sizes (the
+ * result does not depend on the device); 0 when the arguments are invalid. */
+size_t dart_attention_workspace_bytes(int T, int B, int q_heads, int heads, int dim);
+
+/* Attention of a chunk over the paged cache that holds its sequence, the
+ * chunk's own keys and values included (dart_kv_append writes them).  With S =
+ * lengths[b] + (the chunk's tokens) and lead as above:
+ *   token i < lead sees positions 0 .. lengths[b] + i
+ *   node j sees positions 0 .. lengths[b] + lead - 1, and position lengths[b]
+ *   + lead + m for every bit m of row j of its mask (bits behind the chunk are
+ *   ignored)
+ *   out = softmax(scale * q.k) v over those positions, 0 if there are none;
+ *   out_lse = log sum exp(scale * q.k), -inf if there are none
+ * Query head g reads key head g / (q_heads / heads).  Statistics and sums are
+ * fp32; the probabilities are rounded to the cache's type for the product with
+ * v.  Cache rows from position S on may hold anything; the v rows below S are
+ * finite.
+ *  q, out   as for dart_kv_append; out must not overlap q or the cache
+ *  q_heads  a multiple of cache->heads
+ *  mask     device uint32 [B][N][ceil(N/32)], or NULL with N = 0 (causal);
+ *           N <= 1024
+ *  scale    finite
+ *  out_lse  device float [T][q_heads] or NULL
+ *  workspace  device, >= dart_attention_workspace_bytes(...), 256-byte
+ *           aligned; its first 256 bytes zero-filled before the first use
+ *           (dart_device_error reads and clears the error word there).  Calls
+ *           that may overlap need workspaces of their own.
+ * A length or page id out of range sets DART_DEVERR_CACHE: the positions
+ * concerned are left out, or read as zeros.  Returns DART_OK or an error code. */
+int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                        int T, int B, const int32_t* lengths, const int32_t* starts,
+                        const uint32_t* mask, int N, float scale, const dart_cache_t* cache,
+                        void* out, int64_t out_token_stride, int64_t out_head_stride, float* out_lse,
+                        void* workspace, size_t workspace_bytes, void* stream);
 
 /* Smallest power of two >= max(2 * M, 8) (load factor at most 1/2); 0 on
  * overflow. */

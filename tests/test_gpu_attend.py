@@ -1,0 +1,192 @@
+"""tree_attention against its 64-bit form (needs a GB300)."""
+import math
+
+import numpy as np
+import pytest
+
+from tests import steps_refs as refs
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16}
+
+
+@pytest.fixture(scope="module")
+def D():
+    import draft_tree_construction_gb300 as D
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    D.build()
+    return D
+
+
+def _case(dtype, lengths, counts, Hq, Hkv, dim, page, N=0, heads_first=False, extra=0, seed=0, peaky=1.0):
+    """CPU tensors.  Rows of the pages behind each sequence's end hold NaN, unused pages infinities."""
+    g = torch.Generator().manual_seed(seed)
+    rng = np.random.default_rng(seed)
+    B, T = len(lengths), sum(counts) + extra
+    q = (torch.randn(T, Hq, dim, generator=g) * peaky).to(DT[dtype])
+    need = [(a + n + page - 1) // page for a, n in zip(lengths, counts)]
+    total, width = sum(need) + 2, max(need) + 2
+    order = rng.permutation(total)
+    pages, at = np.full((B, width), total - 1, np.int32), 0
+    shape = (total, page, Hkv, dim)
+    k, v = (torch.randn(shape, generator=g).to(DT[dtype]) for _ in range(2))
+    used = torch.zeros(total, page, dtype=torch.bool)
+    for b, m in enumerate(need):
+        pages[b, :m] = order[at:at + m]
+        S = lengths[b] + counts[b]
+        for j in range(m):
+            used[pages[b, j], :max(0, min(page, S - j * page))] = True
+        at += m
+    whole = used.any(-1)
+    for c in (k, v):
+        c[~used] = math.nan
+        c[~whole] = math.inf
+    mask = None
+    if N:
+        mask = np.stack([refs.random_tree(N, max(1, N // 5), rng)[2] for _ in range(B)])
+    s = dict(q=q, k_cache=k, v_cache=v, pages=pages, lengths=np.array(lengths, np.int32),
+             starts=np.cumsum([0] + list(counts)).astype(np.int32), mask=mask, heads_first=heads_first)
+    return s
+
+
+def _cuda(s):
+    d = {n: (torch.from_numpy(x).cuda() if isinstance(x, np.ndarray) else x) for n, x in s.items()}
+    d["q"] = s["q"].cuda()
+    for c in ("k_cache", "v_cache"):
+        d[c] = s[c].transpose(1, 2).contiguous().cuda().transpose(1, 2) if s["heads_first"] else s[c].cuda()
+    return d
+
+
+def _args(d):
+    return d["q"], d["k_cache"], d["v_cache"], d["pages"], d["lengths"], d["starts"]
+
+
+def _check(D, s, scale=None, **kw):
+    d = _cuda(s)
+    T, Hq, dim = s["q"].shape
+    out = torch.full((T, Hq, dim), 5.0, dtype=s["q"].dtype, device="cuda")
+    got = D.tree_attention(*_args(d), mask=d["mask"], scale=scale, out=out, lse=True, **kw)
+    assert D.device_error(got["workspace"]) == 0
+    want, lse, bound, lse_bound = refs.attend(s["q"], s["k_cache"], s["v_cache"], s["pages"], s["lengths"],
+                                              s["starts"], s["mask"], scale if scale is not None else dim ** -0.5)
+    inside = ~torch.isnan(want[:, 0, 0])
+    refs.close(got["out"][inside.cuda()], want[inside], bound[inside], s["q"].dtype)
+    refs.close(got["lse"][inside.cuda()], lse[inside], lse_bound[inside], torch.float32)
+    assert bool((got["out"][~inside.cuda()] == 5.0).all())                # rows of no sequence stay
+    return d, got
+
+
+CASES = [
+    # dtype, lengths, counts, Hq, Hkv, dim, page, N, heads first, rows behind
+    ("bf16", [700], [1], 8, 2, 128, 64, 0, False, 0),
+    ("bf16", [0], [1], 1, 1, 128, 16, 0, False, 0),                       # one token, no context
+    ("f16", [5, 128, 127, 129, 0], [1, 1, 1, 1, 1], 8, 8, 64, 16, 0, False, 3),
+    ("bf16", [300, 0, 60], [33, 40, 0], 8, 2, 128, 32, 32, False, 2),      # trees behind their roots; an empty one
+    ("f16", [250, 77], [78, 78], 4, 1, 128, 16, 78, True, 0),              # nodes alone
+    ("bf16", [100, 3], [50, 20], 6, 2, 96, 24, 40, False, 0),              # a chunk shorter than its tree
+    ("bf16", [130], [257], 2, 1, 128, 128, 0, True, 0),                    # a prompt's piece, causal
+    ("f16", [0, 0], [140, 300], 7, 1, 72, 8, 0, False, 1),
+    ("bf16", [1000], [97], 32, 1, 64, 256, 96, False, 0),                  # 32 query heads on one key head
+    ("f16", [64, 64], [2, 3], 5, 5, 8, 8, 0, False, 0),
+    ("bf16", [2, 5], [200, 129], 3, 1, 128, 40, 129, False, 0),
+    ("bf16", [3000] * 3 + [17], [1] * 4, 16, 4, 128, 64, 0, False, 0),
+    ("f16", [31] * 40, [5] * 40, 4, 2, 128, 16, 4, False, 0),              # more sequences than lanes
+]
+
+
+@pytest.mark.parametrize("dtype,lengths,counts,Hq,Hkv,dim,page,N,heads_first,extra", CASES)
+def test_attention_matches_the_definition(D, dtype, lengths, counts, Hq, Hkv, dim, page, N, heads_first, extra):
+    s = _case(dtype, lengths, counts, Hq, Hkv, dim, page, N, heads_first, extra, seed=Hq + page)
+    _check(D, s)
+
+
+@pytest.mark.parametrize("scale,peaky", [(0.0, 1.0), (-0.3, 1.0), (1.0, 4.0)])
+def test_scales_and_peaks(D, scale, peaky):
+    """Uniform weights, a negative scale, and scores hundreds apart."""
+    _check(D, _case("bf16", [333], [40], 4, 2, 128, 16, 30, seed=3, peaky=peaky), scale=scale)
+
+
+def test_rows_whose_mask_leaves_nothing(D):
+    s = _case("bf16", [0, 40], [20, 20], 4, 2, 64, 16, 20, seed=4)
+    s["mask"][0, 3] = 0
+    s["mask"][0, 11] = 0
+    s["mask"][1, 5] = 0                                                   # still sees its context
+    d, got = _check(D, s)
+    assert bool((got["out"][3] == 0).all()) and bool((got["lse"][11] == -math.inf).all())
+
+
+def test_mask_bits_behind_the_chunk_are_ignored(D):
+    s = _case("f16", [10], [25], 2, 1, 64, 8, 25, seed=5)
+    d, got = _check(D, s)
+    s["mask"][..., 0] |= np.int32(-2 ** 31 + 2 ** 30 + 2 ** 25)           # bits 25, 30, 31
+    _, again = _check(D, s)
+    assert torch.equal(got["out"], again["out"])
+
+
+def test_strided_queries_and_a_reused_workspace(D):
+    s = _case("bf16", [90, 300], [17, 33], 4, 2, 128, 16, seed=6)
+    d = _cuda(s)
+    ref = D.tree_attention(*_args(d))["out"]
+    wide = torch.zeros(50, 12, 128, dtype=torch.bfloat16, device="cuda")
+    wide[:, 3:7] = d["q"]
+    room = torch.zeros(50, 8, 136, dtype=torch.bfloat16, device="cuda")
+    ws = torch.zeros(D.attention_workspace_bytes(50, 2, 4, 2, 128), dtype=torch.uint8, device="cuda")
+    for _ in range(3):
+        D.tree_attention(wide[:, 3:7], *_args(d)[1:], out=room[:, ::2, :128], workspace=ws)
+        assert torch.equal(room[:, ::2, :128], ref)
+    assert int(room[:, 1::2].abs().max()) == 0 and int(room[:, :, 128:].abs().max()) == 0
+    assert D.device_error(ws) == 0
+
+
+def test_ids_and_lengths_out_of_range_are_reported(D):
+    s = _case("bf16", [100, 100], [4, 4], 2, 1, 64, 16, seed=7)
+    d = _cuda(s)
+    good = D.tree_attention(*_args(d))["out"]
+    d["pages"][1, 2] = 10 ** 6
+    got = D.tree_attention(*_args(d))
+    assert D.device_error(got["workspace"]) == 32
+    assert torch.equal(got["out"][:4], good[:4])
+    d["pages"][1, 2] = -7
+    got = D.tree_attention(*_args(d))
+    assert D.device_error(got["workspace"]) == 32 and torch.equal(got["out"][:4], good[:4])
+    d = _cuda(s)
+    d["lengths"][1] = 10 ** 9                         # far more than its pages hold
+    got = D.tree_attention(*_args(d))
+    assert D.device_error(got["workspace"]) == 32 and torch.equal(got["out"][:4], good[:4])
+
+
+def test_same_bits_every_time_on_any_stream_and_in_graphs(D):
+    s = _case("bf16", [2000, 37, 515], [65, 65, 65], 8, 2, 128, 32, 64, seed=8)
+    d = _cuda(s)
+    first = D.tree_attention(*_args(d), mask=d["mask"])["out"]
+    for _ in range(3):
+        assert torch.equal(D.tree_attention(*_args(d), mask=d["mask"])["out"], first)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    got = D.tree_attention(*_args(d), mask=d["mask"], stream=side)["out"]
+    torch.cuda.synchronize()
+    assert torch.equal(got, first)
+    T, Hq, dim = s["q"].shape
+    outs = [torch.empty_like(first) for _ in range(2)]
+    ws = torch.zeros(D.attention_workspace_bytes(T, 3, Hq, 2, dim), dtype=torch.uint8, device="cuda")
+    graphs = [torch.cuda.CUDAGraph() for _ in range(2)]
+    for graph, out in zip(graphs, outs):              # two graphs share the workspace, replayed in order
+        with torch.cuda.graph(graph):
+            D.tree_attention(*_args(d), mask=d["mask"], out=out, workspace=ws)
+    d["lengths"].sub_(20)
+    want = D.tree_attention(*_args(d), mask=d["mask"])["out"]
+    for _ in range(2):
+        for graph, out in zip(graphs, outs):
+            graph.replay()
+            assert torch.equal(out, want)
+    assert D.device_error(ws) == 0
+
+
+def test_empty_calls(D):
+    s = _case("f16", [5], [0], 2, 1, 64, 8, seed=9)
+    d = _cuda(s)
+    assert D.tree_attention(*_args(d))["out"].shape == (0, 2, 64)

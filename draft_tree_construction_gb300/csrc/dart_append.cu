@@ -227,7 +227,7 @@ int check_cache(const dart_cache_t* c, int B) {
   if (c->heads < 1 || c->heads > 65535 || c->dim < 8 || c->dim > 128 || c->dim % 8 != 0) return DART_ERR_INVALID_ARG;
   if (c->page < 8 || c->page % 8 != 0 || c->page > (1 << 20) || c->pages < 0 || c->table_width < 0)
     return DART_ERR_INVALID_ARG;
-  if ((long long)c->table_width * c->page >= (1ll << 31)) return DART_ERR_INVALID_ARG;
+  if ((long long)c->table_width * c->page > (1ll << 30)) return DART_ERR_INVALID_ARG;
   if (c->table_stride < 0 || (B > 1 && c->table_stride < c->table_width)) return DART_ERR_INVALID_ARG;
   const long long st[6] = {c->k_page_stride, c->k_row_stride, c->k_head_stride,
                            c->v_page_stride, c->v_row_stride, c->v_head_stride};

@@ -1,9 +1,29 @@
 // dart_attend.cu -- K7: attention of a chunk of new tokens over a paged cache,
 // the chunk's tail being a tree with packed ancestor-or-self masks.
 //
-// One CTA per token and query head: 128 positions at a time, a thread each for
-// the scores, a running maximum and sum, then a thread per output element.
+// Mathematics.  For the rows of one key head (a row = a token and one of the
+// head group's queries) and tiles of 128 cache positions,
+//   S = Q K^T,  m' = max(m, rowmax S),  P = 2^(c S - m'),  l' = l 2^(m - m') + rowsum P,
+//   O' = O 2^(m - m') + P V,            out = O / l,       c = scale * log2 e,
+// one pass over the cache, fp32 statistics, P rounded to the cache's type for
+// the second product.  m only moves when the maximum has grown by more than
+// 2^8 (the factor 2^(m - m') then touches O); p stays below 2^8 and l above 2^-0
+// until then, which neither fp16 nor fp32 minds.
+//
+// One persistent CTA per SM.  The work is the list of (sequence, key head,
+// block of 256 rows, tile of 128 positions), cut into equal contiguous spans,
+// so a block's tiles may be spread over several CTAs: each leaves (m, l, O) of
+// its part in the workspace and the join kernel merges them in a fixed order.
+// Within a CTA:
+//   warp 8      copies K and V tiles by TMA, one box per page and 64 columns,
+//               into a ring of swizzled shared-memory stages
+//   warp 9      issues the tcgen05 products: S into TMEM, P V into TMEM, P being
+//               read from TMEM where it replaced S
+//   warps 0-3, 4-7   softmax of one 128-row half each, a thread per row; while
+//               one half's softmax runs, the tensor unit works on the other's
 #include <cmath>
+
+#include <cuda.h>
 
 #include "dart_launch.h"
 
@@ -11,125 +31,844 @@ namespace dart {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kThreads = 128;
+constexpr int kThreads = 320;
+constexpr int kCtas = 152;              // nominal: the workspace does not depend on the device
+constexpr int kHalfRows = 128;
+constexpr int kBlockRows = 2 * kHalfRows;
+constexpr int kTile = 128;              // cache positions per tile
+constexpr int kColBytes = 128;          // one swizzle span: 64 elements
+constexpr int kHalfTileBytes = kTile * kColBytes;    // 128 rows of 64 elements
+constexpr int kRingBytes = 10 * kHalfTileBytes;      // 160 KiB of K / V stages
+constexpr float kRescale = 8.f;         // growth of the maximum (in log2) that moves m
+constexpr uint32_t kTmemCols = 512;     // S0 | S1 | O0 | O1
+constexpr long long kDrainLimit = 1ll << 31;
 
 struct AttendParams {
   const void* q;
   void* out;
   float* lse;
   long long q_ts, q_hs, o_ts, o_hs;
-  int Hq, Hkv, G, D, T, B, N;
+  int Hq, Hkv, G, D, T, B, N, MW;
   const int32_t* lengths;
   const int32_t* starts;
   const uint32_t* mask;
-  float scale;
-  dart_cache_t c;
+  float c;                    // |scale| log2 e (1 for scale 0, the queries being zeroed then)
+  uint32_t q_and, q_xor;      // query bits: sign flipped for a negative scale, all cleared for scale 0
+  const int32_t* table;
+  long long table_stride;
+  long long cap;              // positions a sequence's pages can hold
+  int page, pages, box;       // positions per page, pages, positions per TMA box
+  int k_slot[3], v_slot[3];   // which of (head, row, page) is coordinate 1, 2, 3
   uint32_t* err;
+  struct Joint* joints;       // [kCtas]
+  float* parts;               // [kCtas][2][slot_rows][cols + 2]
+  int slot_rows;
+  long long wait_limit;
 };
 
-template <typename T> __device__ __forceinline__ float to_float(T x);
-template <> __device__ __forceinline__ float to_float(__half x) { return __half2float(x); }
-template <> __device__ __forceinline__ float to_float(__nv_bfloat16 x) { return __bfloat162float(x); }
-template <typename T> __device__ __forceinline__ T from_float(float x);
-template <> __device__ __forceinline__ __half from_float(float x) { return __float2half_rn(x); }
-template <> __device__ __forceinline__ __nv_bfloat16 from_float(float x) { return __float2bfloat16_rn(x); }
+// A block of rows whose tiles ended in a later CTA than they began in.
+struct Joint {
+  int parts;                  // CTAs that share it, this one the first; 0 = none
+  int rows, row0;             // rows of the block, its first row within (sequence, head)
+  int head, token0;           // key head, the sequence's first token
+  int pad[3];
+};
 
-template <typename T>
-__global__ void __launch_bounds__(kThreads)
-attend_kernel(const AttendParams P) {
-  __shared__ float sq[128];
-  __shared__ float sp[kThreads];
-  __shared__ int spage[kThreads];
-  __shared__ float red[4];
-  const int t = blockIdx.x, h = blockIdx.y, tid = threadIdx.x, lane = tid & 31;
-  const dart_cache_t& C = P.c;
-  int b = 0;
-  while (b < P.B && P.starts[b + 1] <= t) ++b;
-  if (b >= P.B || P.starts[b] > t) return;
-  const int i = t - P.starts[b], n = min(P.starts[b + 1], P.T) - P.starts[b];
-  const int len = max(P.lengths[b], 0);
-  const long long cap = (long long)C.table_width * C.page;
-  long long S = (long long)len + n;
-  if (S > cap || P.lengths[b] < 0) {
-    if (tid == 0) set_dev_error(P.err, DART_DEVERR_CACHE);
-    if (S > cap) S = cap;
-  }
-  const int lead = max(n - P.N, 0);
-  const long long plain = (long long)len + (i < lead ? i + 1 : lead);   // positions below are visible
-  const long long end = i < lead ? min(plain, S) : S;
-  const int MW = (P.N + 31) / 32;
-  const uint32_t* bits = i >= lead ? P.mask + ((long long)b * P.N + (i - lead)) * MW : nullptr;
-
-  const int hk = h / P.G;
-  const T* q = static_cast<const T*>(P.q) + (long long)t * P.q_ts + (long long)h * P.q_hs;
-  if (tid < P.D) sq[tid] = to_float(q[tid]) * P.scale;
-  float m = -INFINITY, l = 0.f, acc = 0.f;
-  for (long long p0 = 0; p0 < end; p0 += kThreads) {
-    const long long p = p0 + tid;
-    float s = -INFINITY;
-    int page = -1;
-    __syncthreads();
-    if (p < end) {
-      bool see = p < plain;
-      if (!see && bits) {
-        const int j = int(p - plain);
-        see = j < P.N && ((bits[j >> 5] >> (j & 31)) & 1u);
-      }
-      if (see) {
-        page = C.table[(long long)b * C.table_stride + p / C.page];
-        if (page < 0 || page >= C.pages) {
-          set_dev_error(P.err, DART_DEVERR_CACHE);
-          page = -1;
-        }
-        s = 0.f;
-        if (page >= 0) {
-          const T* k = static_cast<const T*>(C.k) + page * C.k_page_stride + (p % C.page) * C.k_row_stride +
-                       (long long)hk * C.k_head_stride;
-          for (int d = 0; d < P.D; ++d) s += sq[d] * to_float(k[d]);
-        }
-      }
-    }
-    float mx = s;
-    for (int o = 16; o; o >>= 1) mx = fmaxf(mx, __shfl_xor_sync(kFull, mx, o));
-    if (lane == 0) red[tid >> 5] = mx;
-    __syncthreads();
-    const float mn = fmaxf(m, fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])));
-    if (mn == -INFINITY) continue;
-    const float keep = expf(m - mn);
-    const float e = expf(s - mn);
-    m = mn;
-    float sum = e;
-    for (int o = 16; o; o >>= 1) sum += __shfl_xor_sync(kFull, sum, o);
-    sp[tid] = e;
-    spage[tid] = page;
-    __syncthreads();
-    if (lane == 0) red[tid >> 5] = sum;
-    __syncthreads();
-    l = l * keep + (red[0] + red[1] + red[2] + red[3]);
-    acc *= keep;
-    if (tid < P.D)
-      for (int j = 0; j < kThreads; ++j)
-        if (spage[j] >= 0)
-          acc += sp[j] * to_float(static_cast<const T*>(C.v)[spage[j] * C.v_page_stride +
-                                                             ((p0 + j) % C.page) * C.v_row_stride +
-                                                             (long long)hk * C.v_head_stride + tid]);
-  }
-  if (tid < P.D)
-    (static_cast<T*>(P.out) + (long long)t * P.o_ts + (long long)h * P.o_hs)[tid] =
-        from_float<T>(l > 0.f ? acc / l : 0.f);
-  if (P.lse && tid == 0) P.lse[(long long)t * P.Hq + h] = l > 0.f ? m + logf(l) : -INFINITY;
+// ----------------------------------------------------------------- PTX glue
+__device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
+                                        uint64_t* bar) {
+  asm volatile(
+      "cp.async.bulk.tensor.4d.shared::cluster.global.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4, %5}], [%6];"
+      :: "r"(smem_u32(dst)), "l"(map), "r"(c0), "r"(c1), "r"(c2), "r"(c3), "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void fence_async() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_ld() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
+               :: "r"(smem_u32(bar)) : "memory");
+}
+__device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
+               :: "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+}
+__device__ __forceinline__ void mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool add) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
+               "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+               :: "r"(d), "r"(a), "l"(b), "r"(idesc), "r"(uint32_t(add)) : "memory");
+}
+__device__ __forceinline__ void tmem_ld32(uint32_t addr, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,"
+      "%30,%31}, [%32];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* x) {
+  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
+      "%31,%32};"
+      :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
+         "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
+         "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};"
+      :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
+         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
 }
 
+// Shared-memory matrix descriptor, 128-byte swizzle: rows of 128 bytes in
+// groups of 8 (1024 bytes apart: the stride offset); `lead` is the distance
+// between blocks of 64 columns where the 64-element span runs along the
+// operand's outer dimension (V), and unused where it runs along K (Q, K).
+__device__ __forceinline__ uint64_t smem_desc(uint32_t addr, uint32_t lead) {
+  return uint64_t((addr & 0x3FFFFu) >> 4) | (uint64_t(lead >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (1ull << 46) | (2ull << 61);
+}
+
+template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
+  const __half2 h = __floats2half2_rn(a, b);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+  uint32_t w;
+  memcpy(&w, &h, 4);
+  return w;
+}
+
+// Operand type in the instruction descriptor.
+template <typename T> constexpr uint32_t kTypeCode = 0;
+template <> constexpr uint32_t kTypeCode<__nv_bfloat16> = 1;
+
+// TMEM loads fill registers asynchronously: after this wait the N values of x
+// are there, and the compiler may not have used them before.
+template <int N>
+__device__ __forceinline__ void loaded(float* x) {
+  tc_wait_ld();
+#pragma unroll
+  for (int k = 0; k < N; ++k) asm volatile("" : "+f"(x[k]));
+}
+
+// ----------------------------------------------------------------- the work
+// One sequence's chunk.
+struct Chunk {
+  int start, n, len, lead, S, blocks;
+};
+__device__ __forceinline__ Chunk load_chunk(const AttendParams& P, int b) {
+  Chunk c;
+  const int s0 = P.starts[b], s1 = min(P.starts[b + 1], P.T);
+  c.start = s0;
+  c.n = s0 >= 0 && s1 > s0 ? s1 - s0 : 0;
+  c.len = int(min((long long)max(P.lengths[b], 0), P.cap));
+  c.S = int(min((long long)c.len + c.n, P.cap));
+  c.lead = max(c.n - P.N, 0);
+  c.blocks = int(((long long)c.n * P.G + kBlockRows - 1) / kBlockRows);
+  return c;
+}
+// Positions that some row of block `blk` sees end here.
+__device__ __forceinline__ int block_end(const AttendParams& P, const Chunk& c, int blk) {
+  const long long r1 = min((long long)(blk + 1ll) * kBlockRows, (long long)c.n * P.G);
+  const int last = int((r1 - 1) / P.G);
+  return last >= c.lead ? c.S : min(c.len + last + 1, c.S);
+}
+__device__ __forceinline__ int block_tiles(const AttendParams& P, const Chunk& c, int blk) {
+  return max(1, (block_end(P, c, blk) + kTile - 1) / kTile);
+}
+// Tiles of all blocks of one head.
+__device__ __forceinline__ long long head_tiles(const AttendParams& P, const Chunk& c) {
+  if (c.blocks == 0) return 0;
+  long long t = 0;
+  // blocks of nodes and the last one see everything; causal ones less
+  for (int k = 0; k < c.blocks; ++k) {
+    const int n = block_tiles(P, c, k);
+    if (((long long)k * kBlockRows) / P.G >= c.lead) return t + (long long)n * (c.blocks - k);
+    t += n;
+  }
+  return t;
+}
+
+// A CTA's walk over its span of the tile list.
+struct Walk {
+  long long u, u1;            // the span's next tile and its end
+  int b, h, blk;              // the block that tile belongs to
+  long long blk_u;            // the block's first tile
+  Chunk c;
+  int tiles;                  // the block's tiles
+  // the part of the block that lies in the span
+  int t0, t1, end, rows;
+  bool whole;
+
+  __device__ __forceinline__ bool open(const AttendParams& P) {
+    if (u >= u1) return false;
+    tiles = block_tiles(P, c, blk);
+    end = block_end(P, c, blk);
+    t0 = int(u - blk_u);
+    t1 = int(min((long long)tiles, u1 - blk_u));
+    rows = int(min((long long)kBlockRows, (long long)c.n * P.G - (long long)blk * kBlockRows));
+    whole = t0 == 0 && t1 == tiles;
+    return true;
+  }
+  __device__ __forceinline__ bool next(const AttendParams& P) {
+    u = blk_u + t1;
+    if (u >= u1) return false;
+    blk_u = u;
+    if (++blk >= c.blocks) {
+      blk = 0;
+      if (++h >= P.Hkv) {
+        h = 0;
+        do {
+          if (++b >= P.B) return false;
+          c = load_chunk(P, b);
+        } while (c.blocks == 0);
+      }
+    }
+    return open(P);
+  }
+};
+
+// What the CTA's span is, and where it begins.
+struct Span {
+  long long total, u0, u1, base;   // base: the first tile of sequence b
+  int b, ctas;
+};
+
+struct Shared {
+  uint64_t kv_full[10], kv_empty[10];
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  Span span;
+  long long scan[kThreads / 32];
+  uint32_t tmem;
+  int dead;                        // a wait ran out: everyone leaves
+};
+
+// Bounded wait of a whole warp; false (for all lanes) once any wait of the CTA ran out.
+__device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, Shared* sh, long long limit) {
+  if (mbar_try_wait(bar, parity)) return true;
+  const long long t0 = clock64();
+  while (!mbar_try_wait(bar, parity)) {
+    if (*reinterpret_cast<volatile int*>(&sh->dead)) return false;
+    if (clock64() - t0 > limit) {
+      *reinterpret_cast<volatile int*>(&sh->dead) = 1;
+      return false;
+    }
+  }
+  return true;
+}
+__device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared* sh, long long limit) {
+  return __all_sync(kFull, wait_lane(bar, parity, sh, limit));
+}
+
+// All threads: the tile count of all sequences, this CTA's span and the sequence it begins in.
+__device__ void find_span(const AttendParams& P, Shared* sh) {
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  constexpr int kWarps = kThreads / 32;
+  long long total = 0;
+  bool bad = false;
+  for (int pass = 0; pass < 2; ++pass) {
+    long long before = 0;
+    const long long u0 = sh->span.u0;
+    for (int b0 = 0; b0 < P.B; b0 += kThreads) {
+      const int b = b0 + tid;
+      long long cost = 0;
+      if (b < P.B) {
+        const Chunk c = load_chunk(P, b);
+        cost = head_tiles(P, c) * P.Hkv;
+        bad |= P.lengths[b] < 0 || (c.n > 0 && (long long)P.lengths[b] + c.n > P.cap);
+      }
+      long long incl = cost;
+      for (int o = 1; o < 32; o <<= 1) {
+        const long long x = __shfl_up_sync(kFull, incl, o);
+        if (lane >= o) incl += x;
+      }
+      __syncthreads();
+      if (lane == 31) sh->scan[warp] = incl;
+      __syncthreads();
+      long long lower = before;
+      for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) lower += sh->scan[w];
+        before += sh->scan[w];
+      }
+      incl += lower;
+      if (pass == 1 && cost > 0 && u0 >= incl - cost && u0 < incl) {
+        sh->span.b = b;
+        sh->span.base = incl - cost;
+      }
+    }
+    if (pass == 0) {
+      total = before;
+      if (tid == 0) {
+        const long long ctas = min((long long)gridDim.x, total);
+        const long long c = blockIdx.x;
+        sh->span.total = total;
+        sh->span.ctas = int(ctas);
+        sh->span.u0 = c < ctas ? total * c / ctas : total;
+        sh->span.u1 = c < ctas ? total * (c + 1) / ctas : total;
+      }
+      __syncthreads();
+    }
+  }
+  if (bad && blockIdx.x == 0) set_dev_error(P.err, DART_DEVERR_CACHE);
+  __syncthreads();
+}
+
+__device__ __forceinline__ bool begin_walk(const AttendParams& P, const Shared* sh, Walk& w) {
+  w.u = sh->span.u0;
+  w.u1 = sh->span.u1;
+  if (w.u >= w.u1) return false;
+  w.b = sh->span.b;
+  w.c = load_chunk(P, w.b);
+  const long long per_head = head_tiles(P, w.c);
+  long long off = w.u - sh->span.base;
+  w.h = int(off / per_head);
+  off -= w.h * per_head;
+  w.blk = 0;
+  long long first = 0;
+  for (;;) {
+    const int n = block_tiles(P, w.c, w.blk);
+    if (first + n > off || w.blk + 1 >= w.c.blocks) break;
+    first += n;
+    ++w.blk;
+  }
+  w.blk_u = w.u - (off - first);
+  return w.open(P);
+}
+
+// Loads of a part of n tiles enter the ring as K0, then K(j+1) and V(j) in turn.
+__device__ __forceinline__ int k_load(int j) { return j == 0 ? 0 : 2 * j - 1; }
+__device__ __forceinline__ int v_load(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
+
+template <typename T, int DH>       // DH: blocks of 64 columns per head
+__global__ void __launch_bounds__(kThreads, 1)
+attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
+  constexpr int kStageBytes = DH * kHalfTileBytes;
+  constexpr int kStages = kRingBytes / kStageBytes;
+  constexpr int kCols = 64 * DH;
+  extern __shared__ __align__(1024) unsigned char smem[];
+  unsigned char* sq = smem;                               // 2 halves of Q
+  unsigned char* ring = smem + 2 * kStageBytes;
+  Shared* sh = reinterpret_cast<Shared*>(ring + kRingBytes);
+
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  if (tid == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh->kv_full[i], 1);
+      mbar_init(&sh->kv_empty[i], 1);
+    }
+    for (int t = 0; t < 2; ++t) {
+      mbar_init(&sh->q_full[t], 4);
+      mbar_init(&sh->s_full[t], 1);
+      mbar_init(&sh->p_full[t], 4);
+      mbar_init(&sh->o_full[t], 1);
+    }
+    mbar_init(&sh->drain, 1);
+    fence_mbar_init();
+    sh->dead = 0;
+    sh->span.u0 = 0;
+    P.joints[blockIdx.x].parts = 0;        // this thread names the CTA's joint later, if there is one
+  }
+  if (warp == 9) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
+                 :: "r"(smem_u32(&sh->tmem)), "r"(kTmemCols) : "memory");
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  __syncthreads();
+  find_span(P, sh);
+  tc_before();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = sh->tmem;
+
+  Walk w;
+  bool more = begin_walk(P, sh, w);
+
+  if (warp == 8) {
+    // ------------------------------------------------------------ producer
+    uint32_t idx = 0;
+    bool ok = true;
+    while (more && ok) {
+      const int n = w.t1 - w.t0;
+      const int32_t* table = P.table + (long long)w.b * P.table_stride;
+      for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
+        const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
+        const int j = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : (i - 2) / 2);
+        const int p0 = (w.t0 + j) * kTile;
+        const int boxes = (min(w.end - p0, kTile) + P.box - 1) / P.box;      // 0 for a block that sees nothing
+        const int at = p0 + (lane / DH) * P.box;
+        const bool mine = lane / DH < boxes;
+        int page = 0;
+        if (mine) {
+          page = table[at / P.page];
+          if (page < 0 || page >= P.pages) {
+            set_dev_error(P.err, DART_DEVERR_CACHE);
+            page = P.pages;               // out of the map's range: the box arrives as zeros
+          }
+        }
+        const uint32_t stage = idx % kStages;
+        ok = wait_warp(&sh->kv_empty[stage], ((idx / kStages) & 1u) ^ 1u, sh, P.wait_limit);
+        if (!ok) break;
+        if (lane == 0) mbar_expect_tx(&sh->kv_full[stage], uint32_t(boxes * DH * P.box * kColBytes));
+        __syncwarp();
+        if (mine) {
+          const int half = lane % DH, row = at % P.page;
+          const int* slot = is_k ? P.k_slot : P.v_slot;
+          auto pick = [&](int i) { return slot[i] == 0 ? w.h : slot[i] == 1 ? row : page; };
+          tma_box(ring + stage * kStageBytes + half * kHalfTileBytes + (lane / DH) * P.box * kColBytes,
+                  is_k ? &kmap : &vmap, 64 * half, pick(0), pick(1), pick(2),
+                  &sh->kv_full[stage]);
+        }
+      }
+      if (ok) more = w.next(P);
+    }
+    // no copy may land after the CTA has left: each stage's last load is waited for
+    for (uint32_t i = 0; i < uint32_t(kStages); ++i) {
+      const uint32_t loads = idx > i ? (idx - i + kStages - 1) / kStages : 0;
+      if (loads > 0) mbar_wait_bounded(&sh->kv_full[i], (loads - 1) & 1u, kDrainLimit);
+    }
+    __syncwarp();
+  } else if (warp == 9) {
+    // ---------------------------------------------------------- tensor unit
+    if (lane == 0) {
+      constexpr uint32_t type = kTypeCode<T>;
+      const uint32_t id_s = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 3) << 17) |
+                            (uint32_t(kHalfRows >> 4) << 24);
+      const uint32_t id_o = (1u << 4) | (type << 7) | (type << 10) | (1u << 16) | (uint32_t(kCols >> 3) << 17) |
+                            (uint32_t(kHalfRows >> 4) << 24);
+      const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
+      const int k_steps = (P.D + 15) / 16;
+      uint32_t idx = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+      bool ok = true;
+      auto product_s = [&](int t, uint32_t stage) {
+        for (int k = 0; k < k_steps; ++k) {
+          const uint32_t off = uint32_t(k >> 2) * kHalfTileBytes + uint32_t(k & 3) * 32u;
+          mma_ss(tmem + uint32_t(t) * kTile, smem_desc(q_addr + uint32_t(t) * kStageBytes + off, 16),
+                 smem_desc(ring_addr + stage * kStageBytes + off, 16), id_s, k > 0);
+        }
+      };
+      while (more && ok) {
+        const int n = w.t1 - w.t0, halves = w.rows > kHalfRows ? 2 : 1;
+        for (int j = -1; j < n && ok; ++j) {
+          uint32_t ks = 0, vs = 0;
+          if (j + 1 < n) {
+            const uint32_t i = idx + k_load(j + 1);
+            ks = i % kStages;
+            if (!(ok = wait_lane(&sh->kv_full[ks], (i / kStages) & 1u, sh, P.wait_limit))) break;
+          }
+          if (j >= 0) {
+            const uint32_t i = idx + v_load(j, n);
+            vs = i % kStages;
+            if (!(ok = wait_lane(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
+          }
+          for (int t = 0; t < halves && ok; ++t) {
+            if (j < 0) {
+              if (!(ok = wait_lane(&sh->q_full[t], q_seen[t]++ & 1u, sh, P.wait_limit))) break;
+              tc_after();
+            } else {
+              if (!(ok = wait_lane(&sh->p_full[t], p_seen[t]++ & 1u, sh, P.wait_limit))) break;
+              tc_after();
+              // steps of 16 positions; those wholly behind the block's end are left out
+              const int valid = max(0, min(w.end - (w.t0 + j) * kTile, kTile));
+              const int steps = max(1, (valid + 15) / 16);
+              for (int k = 0; k < steps; ++k)
+                mma_ts(tmem + 2 * kTile + uint32_t(t) * kCols, tmem + uint32_t(t) * kTile + uint32_t(k) * 8u,
+                       smem_desc(ring_addr + vs * kStageBytes + uint32_t(k) * 16u * kColBytes, kHalfTileBytes), id_o,
+                       j > 0 || k > 0);
+            }
+            if (j + 1 < n) product_s(t, ks);
+            tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
+          }
+          if (!ok) break;
+          if (j >= 0) tc_commit(&sh->kv_empty[vs]);
+          if (j + 1 < n) tc_commit(&sh->kv_empty[ks]);
+        }
+        idx += 2 * n;
+        if (ok) more = w.next(P);
+      }
+      tc_commit(&sh->drain);
+      mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
+    }
+    __syncwarp();
+  } else {
+    // --------------------------------------------------------------- softmax
+    const int t = warp >> 2;
+    const int row = (warp & 3) * 32 + lane;                       // within the half
+    const uint32_t lane_base = uint32_t(warp & 3) << 21;          // TMEM lanes 32 (warp & 3) ..
+    const uint32_t ts = tmem + lane_base + uint32_t(t) * kTile;
+    const uint32_t to = tmem + lane_base + 2 * kTile + uint32_t(t) * kCols;
+    unsigned char* q_half = sq + t * kStageBytes;
+    uint32_t idx = 0, s_seen = 0, o_seen = 0;
+
+    auto active = [&]() { return w.rows > t * kHalfRows; };
+    auto skip_inactive = [&]() {
+      while (more && !active()) {
+        idx += 2 * (w.t1 - w.t0);
+        more = w.next(P);
+      }
+    };
+    // this warp's 32 rows of the block's queries, swizzled
+    auto load_q = [&]() {
+      constexpr int kChunks = 8 * DH, kPer = 32 / kChunks;        // 16-byte chunks per row, rows per step
+      const int chunk = lane % kChunks;
+#pragma unroll 4
+      for (int i = 0; i < 32; i += kPer) {
+        const int r = (warp & 3) * 32 + i + lane / kChunks;
+        const int rr = t * kHalfRows + r;
+        if (rr < w.rows) {
+          const long long g = (long long)w.blk * kBlockRows + rr;
+          const int token = int(g / P.G), head = w.h * P.G + int(g % P.G);
+          uint4 x = make_uint4(0, 0, 0, 0);
+          if (8 * chunk < P.D) {
+            x = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + (long long)(w.c.start + token) * P.q_ts +
+                                                (long long)head * P.q_hs + 8 * chunk);
+            x.x = (x.x & P.q_and) ^ P.q_xor;
+            x.y = (x.y & P.q_and) ^ P.q_xor;
+            x.z = (x.z & P.q_and) ^ P.q_xor;
+            x.w = (x.w & P.q_and) ^ P.q_xor;
+          }
+          *reinterpret_cast<uint4*>(q_half + (chunk >> 3) * kHalfTileBytes + r * kColBytes +
+                                    (((chunk & 7) ^ (r & 7)) << 4)) = x;
+        }
+      }
+      fence_async();
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->q_full[t]);
+    };
+
+    skip_inactive();
+    if (more) load_q();
+    bool ok = true;
+    while (more && ok) {
+      const int n = w.t1 - w.t0;
+      const int my_row = t * kHalfRows + row;
+      const bool warp_on = t * kHalfRows + (warp & 3) * 32 < w.rows;
+      const bool row_on = my_row < w.rows;
+      const long long g = (long long)w.blk * kBlockRows + min(my_row, w.rows - 1);
+      const int token = int(g / P.G);
+      // the row sees positions below `plain` and the set bits from `tree` on
+      const int plain = min(w.c.len + min(token + 1, w.c.lead), w.c.S);
+      const int tree = w.c.len + w.c.lead;
+      const int nodes = token >= w.c.lead ? min(min(P.N, w.c.n - w.c.lead), w.c.S - tree) : 0;   // may be < 0
+      const uint32_t* bits = P.mask + ((long long)w.b * P.N + (token - w.c.lead)) * P.MW;    // read if nodes > 0
+      // tiles below the block's least `plain` need no mask
+      const int first_token = int(((long long)w.blk * kBlockRows) / P.G);
+      const int open_end = min(w.c.len + min(first_token + 1, w.c.lead), w.c.S);
+
+      float m = -INFINITY, l = 0.f;
+      for (int j = 0; j < n && ok; ++j) {
+        const int p0 = (w.t0 + j) * kTile;
+        ok = wait_warp(&sh->s_full[t], s_seen++ & 1u, sh, P.wait_limit);
+        if (!ok) break;
+        tc_after();
+        if (warp_on) {
+          float s[kTile];
+#pragma unroll
+          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+          loaded<kTile>(s);
+          if (p0 + kTile > open_end) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              const int q0 = p0 + 32 * i;
+              const int below = max(0, min(plain - q0, 32));
+              uint32_t see = below >= 32 ? kFull : (1u << below) - 1u;
+              const int at = q0 - tree;
+              if (nodes > 0 && at > -32 && at < nodes) {
+                uint32_t x;
+                if (at < 0) {
+                  x = bits[0] << (-at);
+                } else {
+                  const int wd = at >> 5;
+                  const uint32_t hi = wd + 1 < P.MW ? bits[wd + 1] : 0u;
+                  x = __funnelshift_r(bits[wd], hi, at & 31);
+                }
+                if (nodes - at < 32) x &= (1u << (nodes - at)) - 1u;
+                see |= x;
+              }
+#pragma unroll
+              for (int k = 0; k < 32; ++k)
+                if (!((see >> k) & 1u)) s[32 * i + k] = -INFINITY;
+            }
+          }
+          float mx = s[0];
+#pragma unroll
+          for (int k = 1; k < kTile; ++k) mx = fmaxf(mx, s[k]);
+          mx *= P.c;
+          if (j == 0) {
+            m = mx;
+          } else {
+            const bool grow = mx > m + kRescale;
+            if (__any_sync(kFull, grow)) {
+              const float keep = grow ? ex2_approx(m - mx) : 1.f;
+              if (grow) {
+                m = mx;
+                l *= keep;
+              }
+#pragma unroll
+              for (int i = 0; i < kCols / 32; ++i) {
+                float o[32];
+                tmem_ld32(to + 32 * i, o);
+                loaded<32>(o);
+#pragma unroll
+                for (int k = 0; k < 32; ++k) o[k] *= keep;
+                tmem_st32(to + 32 * i, o);
+              }
+            }
+          }
+          const float off = m == -INFINITY ? 0.f : m;
+          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            uint32_t pk[16];
+#pragma unroll
+            for (int k = 0; k < 16; ++k) {
+              const float a = ex2_approx(fmaf(s[32 * i + 2 * k], P.c, -off));
+              const float b = ex2_approx(fmaf(s[32 * i + 2 * k + 1], P.c, -off));
+              sum[k & 3] += a + b;
+              pk[k] = pack2<T>(a, b);
+            }
+            tmem_st16(ts + 16 * i, pk);
+          }
+          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          tc_wait_st();
+        }
+        // V rows behind the end may hold anything, and 0 * NaN is NaN: those that
+        // share a step of 16 with valid rows are cleared
+        if (t == 0 && j == n - 1 && w.t1 == w.tiles) {
+          const int valid = max(0, min(w.end - p0, kTile));
+          const int upto = max(16, (valid + 15) / 16 * 16);
+          if (valid < upto) {
+            const uint32_t i = idx + v_load(j, n);
+            ok = wait_warp(&sh->kv_full[i % kStages], (i / kStages) & 1u, sh, P.wait_limit);
+            if (!ok) break;
+            const int r = valid + (tid >> 3);
+            if (r < upto)
+#pragma unroll
+              for (int hf = 0; hf < DH; ++hf)
+                *reinterpret_cast<uint4*>(ring + (i % kStages) * kStageBytes + hf * kHalfTileBytes + r * kColBytes +
+                                          (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+            fence_async();
+          }
+        }
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->p_full[t]);
+      }
+      if (!ok) break;
+      idx += 2 * n;
+
+      // the finished part, while the next one's queries are already on their way
+      Walk done = w;
+      more = w.next(P);
+      skip_inactive();
+      if (more) load_q();
+      ok = wait_warp(&sh->o_full[t], o_seen++ & 1u, sh, P.wait_limit);
+      if (!ok) break;
+      tc_after();
+      if (done.whole) {
+        const float inv = l > 0.f ? 1.f / l : 0.f;
+        const long long tok = done.c.start + token;
+        const int head = done.h * P.G + int(g % P.G);
+        T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
+        if (warp_on) {
+#pragma unroll
+          for (int i = 0; i < kCols / 32; ++i) {
+            float o[32];
+            tmem_ld32(to + 32 * i, o);
+            loaded<32>(o);
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+              const float* x = o + 8 * k;
+              const uint4 y = make_uint4(pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv),
+                                         pack2<T>(x[4] * inv, x[5] * inv), pack2<T>(x[6] * inv, x[7] * inv));
+              if (row_on && 32 * i + 8 * k < P.D) *reinterpret_cast<uint4*>(dst + 32 * i + 8 * k) = y;
+            }
+          }
+          if (row_on && P.lse) P.lse[tok * P.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+        }
+      } else if (warp_on) {
+        const int slot = done.t0 > 0 ? 0 : 1;
+        float* dst = P.parts + (((long long)blockIdx.x * 2 + slot) * P.slot_rows + my_row) * (kCols + 4);
+#pragma unroll
+        for (int i = 0; i < kCols / 32; ++i) {
+          float o[32];
+          tmem_ld32(to + 32 * i, o);
+          loaded<32>(o);
+#pragma unroll
+          for (int k = 0; k < 8; ++k)
+            if (row_on)
+              *reinterpret_cast<float4*>(dst + 32 * i + 4 * k) =
+                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+        }
+        if (row_on) *reinterpret_cast<float2*>(dst + kCols) = make_float2(m, l);
+      }
+      if (t == 0 && warp == 0 && lane == 0 && done.t0 == 0 && done.t1 < done.tiles) {
+        // the block goes on in later CTAs: this one's joint names it
+        const Span& sp = sh->span;
+        const long long last = done.blk_u + done.tiles - 1;
+        Joint jt;
+        jt.parts = int(((last + 1) * sp.ctas - 1) / sp.total) - int(blockIdx.x) + 1;
+        jt.rows = done.rows;
+        jt.row0 = done.blk * kBlockRows;
+        jt.head = done.h;
+        jt.token0 = done.c.start;
+        P.joints[blockIdx.x] = jt;
+      }
+    }
+  }
+
+  tc_before();
+  __syncthreads();
+  tc_after();
+  if (warp == 9) {
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
+    if (lane == 0 && sh->dead) set_dev_error(P.err, DART_DEVERR_WAIT_TIMEOUT);
+  }
+}
+
+// One warp per row of a block whose tiles several CTAs shared:
+//   m = max m_i,  l = sum l_i 2^(m_i - m),  out = (sum O_i 2^(m_i - m)) / l
+template <typename T, int DH>
+__global__ void __launch_bounds__(256)
+join_kernel(const AttendParams P) {
+  constexpr int kCols = 64 * DH, kPer = kCols / 32;
+  const Joint jt = P.joints[blockIdx.x];
+  if (jt.parts <= 0) return;
+  const int lane = threadIdx.x & 31;
+  const long long cta_stride = 2ll * P.slot_rows * (kCols + 4);
+  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < jt.rows; r += gridDim.y * 8) {
+    // the first part lies in its CTA's slot 1, the others in slot 0
+    const float* first = P.parts + ((long long)blockIdx.x * 2 + 1) * P.slot_rows * (kCols + 4) + (long long)r * (kCols + 4);
+    const float* rest = P.parts + ((long long)blockIdx.x * 2) * P.slot_rows * (kCols + 4) + (long long)r * (kCols + 4);
+    float m = -INFINITY;
+    for (int i = lane; i < jt.parts; i += 32) m = fmaxf(m, (i == 0 ? first : rest + i * cta_stride)[kCols]);
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+    const float off = m == -INFINITY ? 0.f : m;
+    float l = 0.f, acc[kPer];
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
+#pragma unroll 4
+    for (int i = 0; i < jt.parts; ++i) {
+      const float* src = i == 0 ? first : rest + i * cta_stride;
+      const float2 ml = *reinterpret_cast<const float2*>(src + kCols);
+      const float f = ex2_approx(ml.x - off);
+      l = fmaf(ml.y, f, l);
+#pragma unroll
+      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(src[kPer * lane + k], f, acc[k]);
+    }
+    const float inv = l > 0.f ? 1.f / l : 0.f;
+    const int g = jt.row0 + r;
+    const long long tok = jt.token0 + g / P.G;
+    const int head = jt.head * P.G + g % P.G;
+    T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
+    if (kPer * lane < P.D) {
+#pragma unroll
+      for (int k = 0; k < kPer; k += 2)
+        *reinterpret_cast<uint32_t*>(dst + kPer * lane + k) = pack2<T>(acc[k] * inv, acc[k + 1] * inv);
+    }
+    if (P.lse && lane == 0) P.lse[tok * P.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  }
+}
+
+int gcd(int a, int b) { return b ? gcd(b, a % b) : a; }
 bool mult8(long long a, long long b) { return ((a | b) & 7) == 0; }
 bool aligned16(const void* p) { return p && (reinterpret_cast<uintptr_t>(p) & 15) == 0; }
+
+using EncodeFn = CUresult (*)(CUtensorMap*, CUtensorMapDataType, cuuint32_t, void*, const cuuint64_t*,
+                              const cuuint64_t*, const cuuint32_t*, const cuuint32_t*, CUtensorMapInterleave,
+                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
+EncodeFn tensor_map_encoder() {
+  static const EncodeFn fn = [] {
+    void* f = nullptr;
+    cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
+    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
+        q != cudaDriverEntryPointSuccess)
+      f = nullptr;
+    return reinterpret_cast<EncodeFn>(f);
+  }();
+  return fn;
+}
+
+// The cache as a 4-dimensional map (columns, then head, row and page in the
+// order of their strides) with a box of `box` rows by 64 columns; slot[i]
+// names what coordinate i + 1 is: 0 head, 1 row, 2 page.
+bool cache_map(const dart_cache_t& c, const void* base, long long page_stride, long long row_stride,
+               long long head_stride, int box, CUtensorMap* map, int* slot) {
+  const EncodeFn encode = tensor_map_encoder();
+  if (!encode) return false;
+  const long long size[3] = {c.heads, c.page, c.pages};
+  const long long stride[3] = {head_stride, row_stride, page_stride};
+  for (int i = 0; i < 3; ++i) slot[i] = i;
+  auto key = [&](int i) { return size[i] > 1 ? stride[i] : -1ll; };     // dimensions of one come first
+  for (int i = 0; i < 2; ++i)
+    for (int j = 0; j < 2 - i; ++j)
+      if (key(slot[j]) > key(slot[j + 1])) {
+        const int x = slot[j];
+        slot[j] = slot[j + 1];
+        slot[j + 1] = x;
+      }
+  cuuint64_t dims[4] = {cuuint64_t(c.dim), 0, 0, 0}, strides[3];
+  cuuint32_t boxes[4] = {64, 1, 1, 1}, steps[4] = {1, 1, 1, 1};
+  for (int i = 0; i < 3; ++i) {
+    dims[i + 1] = cuuint64_t(size[slot[i]]);
+    // a dimension of one is never stepped along: any valid stride serves
+    strides[i] = size[slot[i]] > 1 ? cuuint64_t(stride[slot[i]]) * 2 : cuuint64_t(c.dim) * 2;
+    if (strides[i] == 0) return false;
+    if (slot[i] == 1) boxes[i + 1] = cuuint32_t(box);
+  }
+  return encode(map, c.dtype == DART_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                const_cast<void*>(base), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+// Workspace: error word (256 bytes), joints, then the parts.
+constexpr size_t kJointBytes = (sizeof(Joint) * kCtas + 255) / 256 * 256;
+int slot_rows(long long T, long long group) {
+  const long long r = T * group;
+  return int(r < kBlockRows ? (r < 1 ? 1 : r) : kBlockRows);
+}
+
+template <typename T, int DH>
+cudaError_t launch(const AttendParams& P, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
+  const int smem = 2 * DH * kHalfTileBytes + kRingBytes + int(sizeof(Shared));
+  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  if (e != cudaSuccess) return e;
+  attend_kernel<T, DH><<<kCtas, kThreads, smem, s>>>(P, km, vm);
+  e = cudaGetLastError();
+  if (e != cudaSuccess) return e;
+  const int chunks = (P.slot_rows + 31) / 32;
+  join_kernel<T, DH><<<dim3(kCtas, chunks), 256, 0, s>>>(P);
+  return cudaGetLastError();
+}
 
 }  // namespace
 }  // namespace dart
 
 extern "C" size_t dart_attention_workspace_bytes(int T, int B, int q_heads, int heads, int dim) {
+  using namespace dart;
   if (T < 0 || B < 0 || q_heads < 1 || heads < 1 || q_heads % heads != 0 || dim < 8 || dim > 128 || dim % 8 != 0)
     return 0;
-  return dart::kCtrlBytes;
+  const size_t cols = dim <= 64 ? 64 : 128;
+  return kCtrlBytes + kJointBytes + size_t(kCtas) * 2 * slot_rows(T, q_heads / heads) * (cols + 4) * 4;
 }
 
 extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
@@ -140,28 +879,47 @@ extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_
   using namespace dart;
   if (T < 0 || T > (1 << 26) || B < 0 || q_heads < 1 || q_heads > 65535 || N < 0 || N > kMaxN)
     return DART_ERR_INVALID_ARG;
+  if ((long long)T * q_heads >= (1ll << 31)) return DART_ERR_INVALID_ARG;
   const int rc = check_cache(cache, B);
   if (rc) return rc;
   if (q_heads % cache->heads != 0 || !std::isfinite(scale)) return DART_ERR_INVALID_ARG;
   if (T == 0 || B == 0) return DART_OK;
+  if (cache->pages < 1 || cache->table_width < 1) return DART_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !mult8(q_token_stride, q_head_stride) ||
       !mult8(out_token_stride, out_head_stride) || !lengths || !starts || (N > 0 && !mask))
     return DART_ERR_INVALID_ARG;
   if (!workspace || (reinterpret_cast<uintptr_t>(workspace) & 255) != 0 ||
       workspace_bytes < dart_attention_workspace_bytes(T, B, q_heads, cache->heads, cache->dim))
     return DART_ERR_WORKSPACE;
+  const dart_cache_t& c = *cache;
   AttendParams P;
   P.q = q; P.out = out; P.lse = out_lse;
   P.q_ts = q_token_stride; P.q_hs = q_head_stride;
   P.o_ts = out_token_stride; P.o_hs = out_head_stride;
-  P.Hq = q_heads; P.Hkv = cache->heads; P.G = q_heads / cache->heads; P.D = cache->dim;
-  P.T = T; P.B = B; P.N = N;
-  P.lengths = lengths; P.starts = starts; P.mask = mask; P.scale = scale;
-  P.c = *cache;
-  P.err = static_cast<uint32_t*>(workspace);
-  const dim3 grid(T, q_heads);
+  P.Hq = q_heads; P.Hkv = c.heads; P.G = q_heads / c.heads; P.D = c.dim;
+  P.T = T; P.B = B; P.N = N; P.MW = (N + 31) / 32;
+  P.lengths = lengths; P.starts = starts; P.mask = mask;
+  P.c = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504088896341f;
+  P.q_and = scale == 0.f ? 0u : kFull;
+  P.q_xor = scale < 0.f ? 0x80008000u : 0u;
+  P.table = c.table; P.table_stride = c.table_stride;
+  P.cap = (long long)c.table_width * c.page;
+  P.page = c.page; P.pages = c.pages; P.box = gcd(c.page, kTile);
+  uint8_t* ws = static_cast<uint8_t*>(workspace);
+  P.err = reinterpret_cast<uint32_t*>(ws);
+  P.joints = reinterpret_cast<Joint*>(ws + kCtrlBytes);
+  P.parts = reinterpret_cast<float*>(ws + kCtrlBytes + kJointBytes);
+  P.slot_rows = slot_rows(T, P.G);
+  P.wait_limit = rows_wait_limit();
+  CUtensorMap km, vm;
+  if (!cache_map(c, c.k, c.k_page_stride, c.k_row_stride, c.k_head_stride, P.box, &km, P.k_slot) ||
+      !cache_map(c, c.v, c.v_page_stride, c.v_row_stride, c.v_head_stride, P.box, &vm, P.v_slot))
+    return DART_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cache->dtype == DART_F16) attend_kernel<__half><<<grid, kThreads, 0, s>>>(P);
-  else attend_kernel<__nv_bfloat16><<<grid, kThreads, 0, s>>>(P);
-  return cudaGetLastError() == cudaSuccess ? DART_OK : DART_ERR_CUDA;
+  cudaError_t e;
+  if (c.dtype == DART_F16)
+    e = c.dim <= 64 ? launch<__half, 1>(P, km, vm, s) : launch<__half, 2>(P, km, vm, s);
+  else
+    e = c.dim <= 64 ? launch<__nv_bfloat16, 1>(P, km, vm, s) : launch<__nv_bfloat16, 2>(P, km, vm, s);
+  return e == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

@@ -425,7 +425,7 @@ typedef struct {
   int64_t v_page_stride, v_row_stride, v_head_stride;
   const int32_t* table;      /* device [B][table_width], rows table_stride apart */
   int64_t table_stride;
-  int32_t table_width;       /* pages a sequence can have: positions 0 .. table_width * page - 1 (below 2^31) */
+  int32_t table_width;       /* pages a sequence can have: positions 0 .. table_width * page - 1 (at most 2^30) */
   int32_t pages;             /* pages in the cache */
   int32_t page;              /* positions per page, a multiple of 8 */
   int32_t heads;             /* key / value heads */
@@ -493,7 +493,7 @@ size_t dart_attention_workspace_bytes(int T, int B, int q_heads, int heads, int 
  * v.  Cache rows from position S on may hold anything; the v rows below S are
  * finite.
  *  q, out   as for dart_kv_append; out must not overlap q or the cache
- *  q_heads  a multiple of cache->heads
+ *  q_heads  a multiple of cache->heads; T * q_heads < 2^31
  *  mask     device uint32 [B][N][ceil(N/32)], or NULL with N = 0 (causal);
  *           N <= 1024
  *  scale    finite

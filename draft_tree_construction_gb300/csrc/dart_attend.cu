@@ -31,7 +31,12 @@ namespace dart {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kThreads = 320;
+constexpr int kThreads = 384;
+// registers per thread: the launch gives every thread 168; the warpgroup of
+// warps 8-11 gives up most of its own and the softmax warpgroups share them
+// (256 * 208 + 128 * 88 = 384 * 168)
+constexpr int kSoftmaxRegs = 208;
+constexpr int kIssueRegs = 88;
 constexpr int kCtas = 152;              // nominal: the workspace does not depend on the device
 constexpr int kHalfRows = 128;
 constexpr int kBlockRows = 2 * kHalfRows;
@@ -43,12 +48,26 @@ constexpr float kRescale = 8.f;         // growth of the maximum (in log2) that 
 constexpr uint32_t kTmemCols = 512;     // S0 | S1 | O0 | O1
 constexpr long long kDrainLimit = 1ll << 31;
 
+// x / d and x % d for 0 <= x < 2^31 by one multiplication: with L = ceil(log2 d)
+// and mul = ceil(2^(31 + L) / d), the error x * (mul - 2^(31 + L) / d) stays below 2^(31 + L) / d.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int div(int x) const { return int((uint64_t(uint32_t(x)) * mul) >> shift); }
+};
+FastDiv fast_div(uint32_t d) {
+  uint32_t L = 0;
+  while ((1ull << L) < d) ++L;
+  const uint64_t one = 1ull << (31 + L);
+  return FastDiv{d, uint32_t((one + d - 1) / d), 31 + L};
+}
+
 struct AttendParams {
   const void* q;
   void* out;
   float* lse;
   long long q_ts, q_hs, o_ts, o_hs;
   int Hq, Hkv, G, D, T, B, N, MW;
+  FastDiv by_group, by_page;
   const int32_t* lengths;
   const int32_t* starts;
   const uint32_t* mask;
@@ -156,6 +175,23 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
   return w;
 }
 
+// Two fp32 values in one register pair, for the packed arithmetic.
+__device__ __forceinline__ uint64_t pair(float a, float b) {
+  return uint64_t(__float_as_uint(a)) | (uint64_t(__float_as_uint(b)) << 32);
+}
+__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float(uint32_t(x)); }
+__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float(uint32_t(x >> 32)); }
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+  uint64_t d;
+  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+  return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+  uint64_t d;
+  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+  return d;
+}
+
 // Operand type in the instruction descriptor.
 template <typename T> constexpr uint32_t kTypeCode = 0;
 template <> constexpr uint32_t kTypeCode<__nv_bfloat16> = 1;
@@ -172,7 +208,7 @@ __device__ __forceinline__ void loaded(float* x) {
 // ----------------------------------------------------------------- the work
 // One sequence's chunk.
 struct Chunk {
-  int start, n, len, lead, S, blocks;
+  int start, n, len, lead, S, rows, blocks;       // rows = n * G < 2^31
 };
 __device__ __forceinline__ Chunk load_chunk(const AttendParams& P, int b) {
   Chunk c;
@@ -182,13 +218,14 @@ __device__ __forceinline__ Chunk load_chunk(const AttendParams& P, int b) {
   c.len = int(min((long long)max(P.lengths[b], 0), P.cap));
   c.S = int(min((long long)c.len + c.n, P.cap));
   c.lead = max(c.n - P.N, 0);
-  c.blocks = int(((long long)c.n * P.G + kBlockRows - 1) / kBlockRows);
+  c.rows = c.n * P.G;
+  c.blocks = int((unsigned(c.rows) + kBlockRows - 1) / kBlockRows);
   return c;
 }
 // Positions that some row of block `blk` sees end here.
 __device__ __forceinline__ int block_end(const AttendParams& P, const Chunk& c, int blk) {
-  const long long r1 = min((long long)(blk + 1ll) * kBlockRows, (long long)c.n * P.G);
-  const int last = int((r1 - 1) / P.G);
+  const int r1 = c.rows - blk * kBlockRows < kBlockRows ? c.rows : (blk + 1) * kBlockRows;
+  const int last = P.by_group.div(r1 - 1);
   return last >= c.lead ? c.S : min(c.len + last + 1, c.S);
 }
 __device__ __forceinline__ int block_tiles(const AttendParams& P, const Chunk& c, int blk) {
@@ -201,7 +238,7 @@ __device__ __forceinline__ long long head_tiles(const AttendParams& P, const Chu
   // blocks of nodes and the last one see everything; causal ones less
   for (int k = 0; k < c.blocks; ++k) {
     const int n = block_tiles(P, c, k);
-    if (((long long)k * kBlockRows) / P.G >= c.lead) return t + (long long)n * (c.blocks - k);
+    if (P.by_group.div(k * kBlockRows) >= c.lead) return t + (long long)n * (c.blocks - k);
     t += n;
   }
   return t;
@@ -224,7 +261,7 @@ struct Walk {
     end = block_end(P, c, blk);
     t0 = int(u - blk_u);
     t1 = int(min((long long)tiles, u1 - blk_u));
-    rows = int(min((long long)kBlockRows, (long long)c.n * P.G - (long long)blk * kBlockRows));
+    rows = min(kBlockRows, c.rows - blk * kBlockRows);
     whole = t0 == 0 && t1 == tiles;
     return true;
   }
@@ -278,57 +315,72 @@ __device__ __forceinline__ bool wait_warp(uint64_t* bar, uint32_t parity, Shared
   return __all_sync(kFull, wait_lane(bar, parity, sh, limit));
 }
 
-// All threads: the tile count of all sequences, this CTA's span and the sequence it begins in.
+// x * c / n for c <= n <= kCtas.
+__device__ __forceinline__ long long share(long long x, int c, int n) {
+  if (x < (1ll << 24)) return (unsigned(x) * unsigned(c)) / unsigned(n);
+  return x * c / n;
+}
+
+// All threads: the tile count of all sequences, this CTA's span and the
+// sequence it begins in.  Sequences are taken kThreads at a time; when they fit
+// in one such group its scan is kept, else a second pass looks for the span.
 __device__ void find_span(const AttendParams& P, Shared* sh) {
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   constexpr int kWarps = kThreads / 32;
-  long long total = 0;
+  const bool one_group = P.B <= kThreads;
+  long long before = 0, cost = 0, incl = 0;
   bool bad = false;
-  for (int pass = 0; pass < 2; ++pass) {
-    long long before = 0;
-    const long long u0 = sh->span.u0;
-    for (int b0 = 0; b0 < P.B; b0 += kThreads) {
-      const int b = b0 + tid;
-      long long cost = 0;
-      if (b < P.B) {
-        const Chunk c = load_chunk(P, b);
-        cost = head_tiles(P, c) * P.Hkv;
-        bad |= P.lengths[b] < 0 || (c.n > 0 && (long long)P.lengths[b] + c.n > P.cap);
-      }
-      long long incl = cost;
-      for (int o = 1; o < 32; o <<= 1) {
-        const long long x = __shfl_up_sync(kFull, incl, o);
-        if (lane >= o) incl += x;
-      }
-      __syncthreads();
-      if (lane == 31) sh->scan[warp] = incl;
-      __syncthreads();
-      long long lower = before;
-      for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) lower += sh->scan[w];
-        before += sh->scan[w];
-      }
-      incl += lower;
-      if (pass == 1 && cost > 0 && u0 >= incl - cost && u0 < incl) {
-        sh->span.b = b;
-        sh->span.base = incl - cost;
-      }
+  auto scan = [&](int b) {           // cost of sequence b, the inclusive sum in incl, the group's total added to before
+    cost = 0;
+    if (b < P.B) {
+      const Chunk c = load_chunk(P, b);
+      cost = head_tiles(P, c) * P.Hkv;
+      bad |= P.lengths[b] < 0 || (c.n > 0 && (long long)P.lengths[b] + c.n > P.cap);
     }
-    if (pass == 0) {
-      total = before;
-      if (tid == 0) {
-        const long long ctas = min((long long)gridDim.x, total);
-        const long long c = blockIdx.x;
-        sh->span.total = total;
-        sh->span.ctas = int(ctas);
-        sh->span.u0 = c < ctas ? total * c / ctas : total;
-        sh->span.u1 = c < ctas ? total * (c + 1) / ctas : total;
-      }
-      __syncthreads();
+    incl = cost;
+    for (int o = 1; o < 32; o <<= 1) {
+      const long long x = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += x;
+    }
+    __syncthreads();
+    if (lane == 31) sh->scan[warp] = incl;
+    __syncthreads();
+    long long lower = before;
+#pragma unroll
+    for (int w = 0; w < kWarps; ++w) {
+      const long long x = sh->scan[w];
+      if (w < warp) lower += x;
+      before += x;
+    }
+    incl += lower;
+  };
+  auto locate = [&](int b, long long u0) {
+    if (cost > 0 && u0 >= incl - cost && u0 < incl) {
+      sh->span.b = b;
+      sh->span.base = incl - cost;
+    }
+  };
+  for (int b0 = 0; b0 < P.B; b0 += kThreads) scan(b0 + tid);
+  const long long total = before;
+  const int ctas = int(min((long long)gridDim.x, total)), c = blockIdx.x;
+  const long long u0 = c < ctas ? share(total, c, ctas) : total;
+  const long long u1 = c < ctas ? share(total, c + 1, ctas) : total;
+  if (tid == 0) {
+    sh->span.total = total;
+    sh->span.ctas = ctas;
+    sh->span.u0 = u0;
+    sh->span.u1 = u1;
+  }
+  if (one_group) {
+    locate(tid, u0);
+  } else {
+    before = 0;
+    for (int b0 = 0; b0 < P.B; b0 += kThreads) {
+      scan(b0 + tid);
+      locate(b0 + tid, u0);
     }
   }
   if (bad && blockIdx.x == 0) set_dev_error(P.err, DART_DEVERR_CACHE);
-  __syncthreads();
 }
 
 __device__ __forceinline__ bool begin_walk(const AttendParams& P, const Shared* sh, Walk& w) {
@@ -339,7 +391,8 @@ __device__ __forceinline__ bool begin_walk(const AttendParams& P, const Shared* 
   w.c = load_chunk(P, w.b);
   const long long per_head = head_tiles(P, w.c);
   long long off = w.u - sh->span.base;
-  w.h = int(off / per_head);
+  if (off < (1ll << 31) && per_head < (1ll << 31)) w.h = int(unsigned(off) / unsigned(per_head));
+  else w.h = int(off / per_head);
   off -= w.h * per_head;
   w.blk = 0;
   long long first = 0;
@@ -383,7 +436,6 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
     mbar_init(&sh->drain, 1);
     fence_mbar_init();
     sh->dead = 0;
-    sh->span.u0 = 0;
     P.joints[blockIdx.x].parts = 0;        // this thread names the CTA's joint later, if there is one
   }
   if (warp == 9) {
@@ -398,117 +450,124 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
   tc_after();
   const uint32_t tmem = sh->tmem;
 
-  Walk w;
-  bool more = begin_walk(P, sh, w);
-
-  if (warp == 8) {
-    // ------------------------------------------------------------ producer
-    uint32_t idx = 0;
-    bool ok = true;
-    while (more && ok) {
-      const int n = w.t1 - w.t0;
-      const int32_t* table = P.table + (long long)w.b * P.table_stride;
-      for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
-        const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
-        const int j = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : (i - 2) / 2);
-        const int p0 = (w.t0 + j) * kTile;
-        const int boxes = (min(w.end - p0, kTile) + P.box - 1) / P.box;      // 0 for a block that sees nothing
-        const int at = p0 + (lane / DH) * P.box;
-        const bool mine = lane / DH < boxes;
-        int page = 0;
-        if (mine) {
-          page = table[at / P.page];
-          if (page < 0 || page >= P.pages) {
-            set_dev_error(P.err, DART_DEVERR_CACHE);
-            page = P.pages;               // out of the map's range: the box arrives as zeros
-          }
-        }
-        const uint32_t stage = idx % kStages;
-        ok = wait_warp(&sh->kv_empty[stage], ((idx / kStages) & 1u) ^ 1u, sh, P.wait_limit);
-        if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&sh->kv_full[stage], uint32_t(boxes * DH * P.box * kColBytes));
-        __syncwarp();
-        if (mine) {
-          const int half = lane % DH, row = at % P.page;
-          const int* slot = is_k ? P.k_slot : P.v_slot;
-          auto pick = [&](int i) { return slot[i] == 0 ? w.h : slot[i] == 1 ? row : page; };
-          tma_box(ring + stage * kStageBytes + half * kHalfTileBytes + (lane / DH) * P.box * kColBytes,
-                  is_k ? &kmap : &vmap, 64 * half, pick(0), pick(1), pick(2),
-                  &sh->kv_full[stage]);
-        }
-      }
-      if (ok) more = w.next(P);
-    }
-    // no copy may land after the CTA has left: each stage's last load is waited for
-    for (uint32_t i = 0; i < uint32_t(kStages); ++i) {
-      const uint32_t loads = idx > i ? (idx - i + kStages - 1) / kStages : 0;
-      if (loads > 0) mbar_wait_bounded(&sh->kv_full[i], (loads - 1) & 1u, kDrainLimit);
-    }
-    __syncwarp();
-  } else if (warp == 9) {
-    // ---------------------------------------------------------- tensor unit
-    if (lane == 0) {
-      constexpr uint32_t type = kTypeCode<T>;
-      const uint32_t id_s = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 3) << 17) |
-                            (uint32_t(kHalfRows >> 4) << 24);
-      const uint32_t id_o = (1u << 4) | (type << 7) | (type << 10) | (1u << 16) | (uint32_t(kCols >> 3) << 17) |
-                            (uint32_t(kHalfRows >> 4) << 24);
-      const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
-      const int k_steps = (P.D + 15) / 16;
-      uint32_t idx = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+  if (warp >= 8) {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
+    if (warp == 8) {
+      // ------------------------------------------------------------ producer
+      Walk w;
+      bool more = begin_walk(P, sh, w);
+      uint32_t idx = 0;
       bool ok = true;
-      auto product_s = [&](int t, uint32_t stage) {
-        for (int k = 0; k < k_steps; ++k) {
-          const uint32_t off = uint32_t(k >> 2) * kHalfTileBytes + uint32_t(k & 3) * 32u;
-          mma_ss(tmem + uint32_t(t) * kTile, smem_desc(q_addr + uint32_t(t) * kStageBytes + off, 16),
-                 smem_desc(ring_addr + stage * kStageBytes + off, 16), id_s, k > 0);
-        }
-      };
       while (more && ok) {
-        const int n = w.t1 - w.t0, halves = w.rows > kHalfRows ? 2 : 1;
-        for (int j = -1; j < n && ok; ++j) {
-          uint32_t ks = 0, vs = 0;
-          if (j + 1 < n) {
-            const uint32_t i = idx + k_load(j + 1);
-            ks = i % kStages;
-            if (!(ok = wait_lane(&sh->kv_full[ks], (i / kStages) & 1u, sh, P.wait_limit))) break;
-          }
-          if (j >= 0) {
-            const uint32_t i = idx + v_load(j, n);
-            vs = i % kStages;
-            if (!(ok = wait_lane(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
-          }
-          for (int t = 0; t < halves && ok; ++t) {
-            if (j < 0) {
-              if (!(ok = wait_lane(&sh->q_full[t], q_seen[t]++ & 1u, sh, P.wait_limit))) break;
-              tc_after();
-            } else {
-              if (!(ok = wait_lane(&sh->p_full[t], p_seen[t]++ & 1u, sh, P.wait_limit))) break;
-              tc_after();
-              // steps of 16 positions; those wholly behind the block's end are left out
-              const int valid = max(0, min(w.end - (w.t0 + j) * kTile, kTile));
-              const int steps = max(1, (valid + 15) / 16);
-              for (int k = 0; k < steps; ++k)
-                mma_ts(tmem + 2 * kTile + uint32_t(t) * kCols, tmem + uint32_t(t) * kTile + uint32_t(k) * 8u,
-                       smem_desc(ring_addr + vs * kStageBytes + uint32_t(k) * 16u * kColBytes, kHalfTileBytes), id_o,
-                       j > 0 || k > 0);
+        const int n = w.t1 - w.t0;
+        const int32_t* table = P.table + (long long)w.b * P.table_stride;
+        for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
+          const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
+          const int j = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : (i - 2) / 2);
+          const int p0 = (w.t0 + j) * kTile;
+          const int boxes = (min(w.end - p0, kTile) + P.box - 1) / P.box;      // 0 for a block that sees nothing
+          const int at = p0 + (lane / DH) * P.box;
+          const bool mine = lane / DH < boxes;
+          int page = 0;
+          if (mine) {
+            page = table[P.by_page.div(at)];
+            if (page < 0 || page >= P.pages) {
+              set_dev_error(P.err, DART_DEVERR_CACHE);
+              page = P.pages;               // out of the map's range: the box arrives as zeros
             }
-            if (j + 1 < n) product_s(t, ks);
-            tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
           }
+          const uint32_t stage = idx % kStages;
+          ok = wait_warp(&sh->kv_empty[stage], ((idx / kStages) & 1u) ^ 1u, sh, P.wait_limit);
           if (!ok) break;
-          if (j >= 0) tc_commit(&sh->kv_empty[vs]);
-          if (j + 1 < n) tc_commit(&sh->kv_empty[ks]);
+          if (lane == 0) mbar_expect_tx(&sh->kv_full[stage], uint32_t(boxes * DH * P.box * kColBytes));
+          __syncwarp();
+          if (mine) {
+            const int half = lane % DH, row = at - P.by_page.div(at) * P.page;
+            const int* slot = is_k ? P.k_slot : P.v_slot;
+            auto pick = [&](int i) { return slot[i] == 0 ? w.h : slot[i] == 1 ? row : page; };
+            tma_box(ring + stage * kStageBytes + half * kHalfTileBytes + (lane / DH) * P.box * kColBytes,
+                    is_k ? &kmap : &vmap, 64 * half, pick(0), pick(1), pick(2),
+                    &sh->kv_full[stage]);
+          }
         }
-        idx += 2 * n;
         if (ok) more = w.next(P);
       }
-      tc_commit(&sh->drain);
-      mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
+      // no copy may land after the CTA has left: each stage's last load is waited for
+      for (uint32_t i = 0; i < uint32_t(kStages); ++i) {
+        const uint32_t loads = idx > i ? (idx - i + kStages - 1) / kStages : 0;
+        if (loads > 0) mbar_wait_bounded(&sh->kv_full[i], (loads - 1) & 1u, kDrainLimit);
+      }
+      __syncwarp();
+    } else if (warp == 9) {
+      // ---------------------------------------------------------- tensor unit
+      Walk w;
+      bool more = begin_walk(P, sh, w);
+      if (lane == 0) {
+        constexpr uint32_t type = kTypeCode<T>;
+        const uint32_t id_s = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 3) << 17) |
+                              (uint32_t(kHalfRows >> 4) << 24);
+        const uint32_t id_o = (1u << 4) | (type << 7) | (type << 10) | (1u << 16) | (uint32_t(kCols >> 3) << 17) |
+                              (uint32_t(kHalfRows >> 4) << 24);
+        const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
+        const int k_steps = (P.D + 15) / 16;
+        uint32_t idx = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+        bool ok = true;
+        auto product_s = [&](int t, uint32_t stage) {
+          for (int k = 0; k < k_steps; ++k) {
+            const uint32_t off = uint32_t(k >> 2) * kHalfTileBytes + uint32_t(k & 3) * 32u;
+            mma_ss(tmem + uint32_t(t) * kTile, smem_desc(q_addr + uint32_t(t) * kStageBytes + off, 16),
+                   smem_desc(ring_addr + stage * kStageBytes + off, 16), id_s, k > 0);
+          }
+        };
+        while (more && ok) {
+          const int n = w.t1 - w.t0, halves = w.rows > kHalfRows ? 2 : 1;
+          for (int j = -1; j < n && ok; ++j) {
+            uint32_t ks = 0, vs = 0;
+            if (j + 1 < n) {
+              const uint32_t i = idx + k_load(j + 1);
+              ks = i % kStages;
+              if (!(ok = wait_lane(&sh->kv_full[ks], (i / kStages) & 1u, sh, P.wait_limit))) break;
+            }
+            if (j >= 0) {
+              const uint32_t i = idx + v_load(j, n);
+              vs = i % kStages;
+              if (!(ok = wait_lane(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
+            }
+            for (int t = 0; t < halves && ok; ++t) {
+              if (j < 0) {
+                if (!(ok = wait_lane(&sh->q_full[t], q_seen[t]++ & 1u, sh, P.wait_limit))) break;
+                tc_after();
+              } else {
+                if (!(ok = wait_lane(&sh->p_full[t], p_seen[t]++ & 1u, sh, P.wait_limit))) break;
+                tc_after();
+                // steps of 16 positions; those wholly behind the block's end are left out
+                const int valid = max(0, min(w.end - (w.t0 + j) * kTile, kTile));
+                const int steps = max(1, (valid + 15) / 16);
+                for (int k = 0; k < steps; ++k)
+                  mma_ts(tmem + 2 * kTile + uint32_t(t) * kCols, tmem + uint32_t(t) * kTile + uint32_t(k) * 8u,
+                         smem_desc(ring_addr + vs * kStageBytes + uint32_t(k) * 16u * kColBytes, kHalfTileBytes), id_o,
+                         j > 0 || k > 0);
+              }
+              if (j + 1 < n) product_s(t, ks);
+              tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
+            }
+            if (!ok) break;
+            if (j >= 0) tc_commit(&sh->kv_empty[vs]);
+            if (j + 1 < n) tc_commit(&sh->kv_empty[ks]);
+          }
+          idx += 2 * n;
+          if (ok) more = w.next(P);
+        }
+        tc_commit(&sh->drain);
+        mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
+      }
+      __syncwarp();
     }
-    __syncwarp();
   } else {
     // --------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
+    Walk w;
+    bool more = begin_walk(P, sh, w);
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;                       // within the half
     const uint32_t lane_base = uint32_t(warp & 3) << 21;          // TMEM lanes 32 (warp & 3) ..
@@ -528,24 +587,30 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
     auto load_q = [&]() {
       constexpr int kChunks = 8 * DH, kPer = 32 / kChunks;        // 16-byte chunks per row, rows per step
       const int chunk = lane % kChunks;
-#pragma unroll 4
-      for (int i = 0; i < 32; i += kPer) {
-        const int r = (warp & 3) * 32 + i + lane / kChunks;
-        const int rr = t * kHalfRows + r;
-        if (rr < w.rows) {
-          const long long g = (long long)w.blk * kBlockRows + rr;
-          const int token = int(g / P.G), head = w.h * P.G + int(g % P.G);
-          uint4 x = make_uint4(0, 0, 0, 0);
-          if (8 * chunk < P.D) {
-            x = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) + (long long)(w.c.start + token) * P.q_ts +
-                                                (long long)head * P.q_hs + 8 * chunk);
-            x.x = (x.x & P.q_and) ^ P.q_xor;
-            x.y = (x.y & P.q_and) ^ P.q_xor;
-            x.z = (x.z & P.q_and) ^ P.q_xor;
-            x.w = (x.w & P.q_and) ^ P.q_xor;
+      const int first = t * kHalfRows + (warp & 3) * 32 + lane / kChunks;
+      for (int i0 = 0; i0 < 32 && first - lane / kChunks + i0 < w.rows; i0 += 8 * kPer) {
+        uint4 x[8];
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int rr = first + i0 + u * kPer;
+          x[u] = make_uint4(0, 0, 0, 0);
+          if (rr < w.rows && 8 * chunk < P.D) {
+            const int g = w.blk * kBlockRows + rr;
+            const int token = P.by_group.div(g), head = w.h * P.G + g - token * P.G;
+            x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) +
+                                                   (long long)(w.c.start + token) * P.q_ts +
+                                                   (long long)head * P.q_hs + 8 * chunk);
           }
+        }
+#pragma unroll
+        for (int u = 0; u < 8; ++u) {
+          const int r = (first + i0 + u * kPer) & (kHalfRows - 1);
+          x[u].x = (x[u].x & P.q_and) ^ P.q_xor;
+          x[u].y = (x[u].y & P.q_and) ^ P.q_xor;
+          x[u].z = (x[u].z & P.q_and) ^ P.q_xor;
+          x[u].w = (x[u].w & P.q_and) ^ P.q_xor;
           *reinterpret_cast<uint4*>(q_half + (chunk >> 3) * kHalfTileBytes + r * kColBytes +
-                                    (((chunk & 7) ^ (r & 7)) << 4)) = x;
+                                    (((chunk & 7) ^ (r & 7)) << 4)) = x[u];
         }
       }
       fence_async();
@@ -561,15 +626,15 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       const int my_row = t * kHalfRows + row;
       const bool warp_on = t * kHalfRows + (warp & 3) * 32 < w.rows;
       const bool row_on = my_row < w.rows;
-      const long long g = (long long)w.blk * kBlockRows + min(my_row, w.rows - 1);
-      const int token = int(g / P.G);
+      const int g = w.blk * kBlockRows + min(my_row, w.rows - 1);
+      const int token = P.by_group.div(g);
       // the row sees positions below `plain` and the set bits from `tree` on
       const int plain = min(w.c.len + min(token + 1, w.c.lead), w.c.S);
       const int tree = w.c.len + w.c.lead;
       const int nodes = token >= w.c.lead ? min(min(P.N, w.c.n - w.c.lead), w.c.S - tree) : 0;   // may be < 0
       const uint32_t* bits = P.mask + ((long long)w.b * P.N + (token - w.c.lead)) * P.MW;    // read if nodes > 0
       // tiles below the block's least `plain` need no mask
-      const int first_token = int(((long long)w.blk * kBlockRows) / P.G);
+      const int first_token = P.by_group.div(w.blk * kBlockRows);
       const int open_end = min(w.c.len + min(first_token + 1, w.c.lead), w.c.S);
 
       float m = -INFINITY, l = 0.f;
@@ -607,9 +672,14 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
                 if (!((see >> k) & 1u)) s[32 * i + k] = -INFINITY;
             }
           }
-          float mx = s[0];
+          float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll
-          for (int k = 1; k < kTile; ++k) mx = fmaxf(mx, s[k]);
+          for (int k = 4; k < kTile; k += 8) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+              top[i] = k + 4 + i < kTile ? fmaxf(top[i], fmaxf(s[k + i], s[k + 4 + i])) : fmaxf(top[i], s[k + i]);
+          }
+          float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           mx *= P.c;
           if (j == 0) {
             m = mx;
@@ -633,20 +703,22 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
             }
           }
           const float off = m == -INFINITY ? 0.f : m;
-          float sum[4] = {0.f, 0.f, 0.f, 0.f};
+          const uint64_t c2 = pair(P.c, P.c), off2 = pair(-off, -off);
+          uint64_t sum[2] = {0ull, 0ull};
 #pragma unroll
           for (int i = 0; i < 4; ++i) {
             uint32_t pk[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) {
-              const float a = ex2_approx(fmaf(s[32 * i + 2 * k], P.c, -off));
-              const float b = ex2_approx(fmaf(s[32 * i + 2 * k + 1], P.c, -off));
-              sum[k & 3] += a + b;
+              const uint64_t x = fma2(pair(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), c2, off2);
+              const float a = ex2_approx(low(x)), b = ex2_approx(high(x));
+              sum[k & 1] = add2(sum[k & 1], pair(a, b));
               pk[k] = pack2<T>(a, b);
             }
             tmem_st16(ts + 16 * i, pk);
           }
-          l += (sum[0] + sum[1]) + (sum[2] + sum[3]);
+          sum[0] = add2(sum[0], sum[1]);
+          l += low(sum[0]) + high(sum[0]);
           tc_wait_st();
         }
         // V rows behind the end may hold anything, and 0 * NaN is NaN: those that
@@ -685,7 +757,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       if (done.whole) {
         const float inv = l > 0.f ? 1.f / l : 0.f;
         const long long tok = done.c.start + token;
-        const int head = done.h * P.G + int(g % P.G);
+        const int head = done.h * P.G + g - token * P.G;
         T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
         if (warp_on) {
 #pragma unroll
@@ -775,9 +847,9 @@ join_kernel(const AttendParams P) {
       for (int k = 0; k < kPer; ++k) acc[k] = fmaf(src[kPer * lane + k], f, acc[k]);
     }
     const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int g = jt.row0 + r;
-    const long long tok = jt.token0 + g / P.G;
-    const int head = jt.head * P.G + g % P.G;
+    const int g = jt.row0 + r, token = P.by_group.div(g);
+    const long long tok = jt.token0 + token;
+    const int head = jt.head * P.G + g - token * P.G;
     T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
     if (kPer * lane < P.D) {
 #pragma unroll
@@ -904,6 +976,8 @@ extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_
   P.q_xor = scale < 0.f ? 0x80008000u : 0u;
   P.table = c.table; P.table_stride = c.table_stride;
   P.cap = (long long)c.table_width * c.page;
+  P.by_group = fast_div(uint32_t(P.G));
+  P.by_page = fast_div(uint32_t(c.page));
   P.page = c.page; P.pages = c.pages; P.box = gcd(c.page, kTile);
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   P.err = reinterpret_cast<uint32_t*>(ws);

@@ -640,6 +640,22 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       float m = -INFINITY, l = 0.f;
       for (int j = 0; j < n && ok; ++j) {
         const int p0 = (w.t0 + j) * kTile;
+        // what this row sees of the tile, looked up while the product is under way
+        const bool masked = p0 + kTile > open_end;
+        uint32_t see[4] = {kFull, kFull, kFull, kFull};
+        if (masked) {
+          uint32_t word[5];
+          const int at0 = p0 - tree, wd0 = at0 >> 5;           // floor: the word that holds bit at0
+#pragma unroll
+          for (int i = 0; i < 5; ++i)
+            word[i] = wd0 + i >= 0 && 32 * (wd0 + i) < nodes ? bits[wd0 + i] : 0u;
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const int below = max(0, min(plain - p0 - 32 * i, 32)), left = max(0, min(nodes - at0 - 32 * i, 32));
+            const uint32_t x = __funnelshift_r(word[i], word[i + 1], at0 & 31);
+            see[i] = (below >= 32 ? kFull : (1u << below) - 1u) | (x & (left >= 32 ? kFull : (1u << left) - 1u));
+          }
+        }
         ok = wait_warp(&sh->s_full[t], s_seen++ & 1u, sh, P.wait_limit);
         if (!ok) break;
         tc_after();
@@ -648,29 +664,10 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
 #pragma unroll
           for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
           loaded<kTile>(s);
-          if (p0 + kTile > open_end) {
+          if (masked) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-              const int q0 = p0 + 32 * i;
-              const int below = max(0, min(plain - q0, 32));
-              uint32_t see = below >= 32 ? kFull : (1u << below) - 1u;
-              const int at = q0 - tree;
-              if (nodes > 0 && at > -32 && at < nodes) {
-                uint32_t x;
-                if (at < 0) {
-                  x = bits[0] << (-at);
-                } else {
-                  const int wd = at >> 5;
-                  const uint32_t hi = wd + 1 < P.MW ? bits[wd + 1] : 0u;
-                  x = __funnelshift_r(bits[wd], hi, at & 31);
-                }
-                if (nodes - at < 32) x &= (1u << (nodes - at)) - 1u;
-                see |= x;
-              }
-#pragma unroll
-              for (int k = 0; k < 32; ++k)
-                if (!((see >> k) & 1u)) s[32 * i + k] = -INFINITY;
-            }
+            for (int k = 0; k < kTile; ++k)
+              if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = -INFINITY;
           }
           float top[4] = {s[0], s[1], s[2], s[3]};
 #pragma unroll

@@ -109,6 +109,13 @@ __device__ __forceinline__ void tc_commit(uint64_t* bar) {
   asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];"
                :: "r"(smem_u32(bar)) : "memory");
 }
+// One thread of the warp issues; the warp runs converged so that descriptors
+// and addresses stay in uniform registers.
+__device__ __forceinline__ uint32_t elect() {
+  uint32_t e;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xFFFFFFFF;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+  return e;
+}
 __device__ __forceinline__ void mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, bool add) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %4, 0;\n\t"
                "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}"
@@ -502,65 +509,73 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       // ---------------------------------------------------------- tensor unit
       Walk w;
       bool more = begin_walk(P, sh, w);
-      if (lane == 0) {
-        constexpr uint32_t type = kTypeCode<T>;
-        const uint32_t id_s = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 3) << 17) |
-                              (uint32_t(kHalfRows >> 4) << 24);
-        const uint32_t id_o = (1u << 4) | (type << 7) | (type << 10) | (1u << 16) | (uint32_t(kCols >> 3) << 17) |
-                              (uint32_t(kHalfRows >> 4) << 24);
-        const uint32_t q_addr = smem_u32(sq), ring_addr = smem_u32(ring);
-        const int k_steps = (P.D + 15) / 16;
-        uint32_t idx = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
-        bool ok = true;
-        auto product_s = [&](int t, uint32_t stage) {
-          for (int k = 0; k < k_steps; ++k) {
-            const uint32_t off = uint32_t(k >> 2) * kHalfTileBytes + uint32_t(k & 3) * 32u;
-            mma_ss(tmem + uint32_t(t) * kTile, smem_desc(q_addr + uint32_t(t) * kStageBytes + off, 16),
-                   smem_desc(ring_addr + stage * kStageBytes + off, 16), id_s, k > 0);
+      constexpr uint32_t type = kTypeCode<T>;
+      constexpr uint32_t id_s = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 3) << 17) |
+                                (uint32_t(kHalfRows >> 4) << 24);
+      constexpr uint32_t id_o = (1u << 4) | (type << 7) | (type << 10) | (1u << 16) | (uint32_t(kCols >> 3) << 17) |
+                                (uint32_t(kHalfRows >> 4) << 24);
+      const uint64_t q_desc = smem_desc(smem_u32(sq), 16), k_desc = smem_desc(smem_u32(ring), 16),
+                     v_desc = smem_desc(smem_u32(ring), kHalfTileBytes);
+      const int k_steps = (P.D + 15) / 16;
+      uint32_t idx = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+      bool ok = true;
+      while (more && ok) {
+        const int n = w.t1 - w.t0, halves = w.rows > kHalfRows ? 2 : 1;
+        for (int j = -1; j < n && ok; ++j) {
+          uint32_t ks = 0, vs = 0;
+          if (j + 1 < n) {
+            const uint32_t i = idx + k_load(j + 1);
+            ks = i % kStages;
+            if (!(ok = wait_warp(&sh->kv_full[ks], (i / kStages) & 1u, sh, P.wait_limit))) break;
           }
-        };
-        while (more && ok) {
-          const int n = w.t1 - w.t0, halves = w.rows > kHalfRows ? 2 : 1;
-          for (int j = -1; j < n && ok; ++j) {
-            uint32_t ks = 0, vs = 0;
-            if (j + 1 < n) {
-              const uint32_t i = idx + k_load(j + 1);
-              ks = i % kStages;
-              if (!(ok = wait_lane(&sh->kv_full[ks], (i / kStages) & 1u, sh, P.wait_limit))) break;
-            }
-            if (j >= 0) {
-              const uint32_t i = idx + v_load(j, n);
-              vs = i % kStages;
-              if (!(ok = wait_lane(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
-            }
-            for (int t = 0; t < halves && ok; ++t) {
-              if (j < 0) {
-                if (!(ok = wait_lane(&sh->q_full[t], q_seen[t]++ & 1u, sh, P.wait_limit))) break;
-                tc_after();
-              } else {
-                if (!(ok = wait_lane(&sh->p_full[t], p_seen[t]++ & 1u, sh, P.wait_limit))) break;
-                tc_after();
-                // steps of 16 positions; those wholly behind the block's end are left out
-                const int valid = max(0, min(w.end - (w.t0 + j) * kTile, kTile));
-                const int steps = max(1, (valid + 15) / 16);
-                for (int k = 0; k < steps; ++k)
-                  mma_ts(tmem + 2 * kTile + uint32_t(t) * kCols, tmem + uint32_t(t) * kTile + uint32_t(k) * 8u,
-                         smem_desc(ring_addr + vs * kStageBytes + uint32_t(k) * 16u * kColBytes, kHalfTileBytes), id_o,
-                         j > 0 || k > 0);
+          if (j >= 0) {
+            const uint32_t i = idx + v_load(j, n);
+            vs = i % kStages;
+            if (!(ok = wait_warp(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
+          }
+          // steps of 16 positions; those wholly behind the block's end are left out
+          const int steps = max(1, (min(w.end - (w.t0 + j) * kTile, kTile) + 15) / 16);
+#pragma unroll
+          for (int t = 0; t < 2; ++t) {
+            if (t >= halves || !ok) continue;
+            uint64_t* bar = j < 0 ? &sh->q_full[t] : &sh->p_full[t];
+            const uint32_t seen = j < 0 ? q_seen[t]++ : p_seen[t]++;
+            if (!(ok = wait_warp(bar, seen & 1u, sh, P.wait_limit))) continue;
+            tc_after();
+            if (elect()) {
+              if (j >= 0) {
+                const uint64_t vd = v_desc + uint64_t(vs * (kStageBytes >> 4));
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                  if (k < steps)
+                    mma_ts(tmem + 2 * kTile + t * kCols, tmem + t * kTile + k * 8, vd + k * (16 * kColBytes >> 4), id_o,
+                           j > 0 || k > 0);
               }
-              if (j + 1 < n) product_s(t, ks);
+              if (j + 1 < n) {
+                const uint64_t kd = k_desc + uint64_t(ks * (kStageBytes >> 4)), qd = q_desc + t * (kStageBytes >> 4);
+#pragma unroll
+                for (int k = 0; k < 4 * DH; ++k) {
+                  const int off = ((k >> 2) * kHalfTileBytes + (k & 3) * 32) >> 4;
+                  if (k < k_steps) mma_ss(tmem + t * kTile, qd + off, kd + off, id_s, k > 0);
+                }
+              }
               tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
             }
-            if (!ok) break;
+            __syncwarp();
+          }
+          if (!ok) break;
+          if (elect()) {
             if (j >= 0) tc_commit(&sh->kv_empty[vs]);
             if (j + 1 < n) tc_commit(&sh->kv_empty[ks]);
           }
-          idx += 2 * n;
-          if (ok) more = w.next(P);
+          __syncwarp();
         }
-        tc_commit(&sh->drain);
-        mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
+        idx += 2 * n;
+        if (ok) more = w.next(P);
       }
+      // every product has ended before the tensor memory is given back
+      if (elect()) tc_commit(&sh->drain);
+      mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
       __syncwarp();
     }
   } else {

@@ -15,8 +15,9 @@
 // so a block's tiles may be spread over several CTAs: each leaves (m, l, O) of
 // its part in the workspace and the join kernel merges them in a fixed order.
 // Within a CTA:
-//   warp 8      copies K and V tiles by TMA, one box per page and 64 columns,
-//               into a ring of swizzled shared-memory stages
+//   warps 8, 10, 11  copy K and V tiles by TMA, one box per page and 64 columns,
+//               into a ring of swizzled shared-memory stages; they take the
+//               loads in turn, because a box costs its warp about 100 cycles
 //   warp 9      issues the tcgen05 products: S into TMEM, P V into TMEM, P being
 //               read from TMEM where it replaced S
 //   warps 0-3, 4-7   softmax of one 128-row half each, a thread per row; while
@@ -46,6 +47,7 @@ constexpr int kHalfTileBytes = kTile * kColBytes;    // 128 rows of 64 elements
 constexpr int kRingBytes = 10 * kHalfTileBytes;      // 160 KiB of K / V stages
 constexpr float kRescale = 8.f;         // growth of the maximum (in log2) that moves m
 constexpr uint32_t kTmemCols = 512;     // S0 | S1 | O0 | O1
+constexpr uint32_t kProducers = 3;      // warps 8, 10 and 11, which take the loads in turn
 constexpr long long kDrainLimit = 1ll << 31;
 
 // x / d and x % d for 0 <= x < 2^31 by one multiplication: with L = ceil(log2 d)
@@ -459,16 +461,22 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
-    if (warp == 8) {
-      // ------------------------------------------------------------ producer
+    if (warp != 9) {
+      // ------------------------------------------------------------ producers
+      const uint32_t pid = warp == 8 ? 0u : uint32_t(warp - 9);
       Walk w;
       bool more = begin_walk(P, sh, w);
-      uint32_t idx = 0;
+      uint32_t idx = 0, turn = 0;            // loads so far, and whose turn the next one is
       bool ok = true;
       while (more && ok) {
         const int n = w.t1 - w.t0;
         const int32_t* table = P.table + (long long)w.b * P.table_stride;
         for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
+          if (turn != pid) {
+            turn = turn + 1 < kProducers ? turn + 1 : 0;
+            continue;
+          }
+          turn = turn + 1 < kProducers ? turn + 1 : 0;
           const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
           const int j = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : (i - 2) / 2);
           const int p0 = (w.t0 + j) * kTile;
@@ -499,13 +507,11 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
         }
         if (ok) more = w.next(P);
       }
-      // no copy may land after the CTA has left: each stage's last load is waited for
-      for (uint32_t i = 0; i < uint32_t(kStages); ++i) {
-        const uint32_t loads = idx > i ? (idx - i + kStages - 1) / kStages : 0;
-        if (loads > 0) mbar_wait_bounded(&sh->kv_full[i], (loads - 1) & 1u, kDrainLimit);
-      }
+      // no copy may land after the CTA has left: the last load of each stage is waited for
+      for (uint32_t i = idx > uint32_t(kStages) ? idx - kStages : 0; i < idx; ++i)
+        if (i % kProducers == pid) mbar_wait_bounded(&sh->kv_full[i % kStages], (i / kStages) & 1u, kDrainLimit);
       __syncwarp();
-    } else if (warp == 9) {
+    } else {
       // ---------------------------------------------------------- tensor unit
       Walk w;
       bool more = begin_walk(P, sh, w);

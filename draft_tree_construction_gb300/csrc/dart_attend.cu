@@ -82,7 +82,7 @@ struct AttendParams {
   int k_slot[3], v_slot[3];   // which of (head, row, page) is coordinate 1, 2, 3
   uint32_t* err;
   struct Joint* joints;       // [kCtas]
-  float* parts;               // [kCtas][2][slot_rows][cols + 2]
+  float4* parts;              // [kCtas][2] slots: [cols / 4][slot_rows] float4, then [slot_rows] (m, l)
   int slot_rows;
   long long wait_limit;
 };
@@ -94,6 +94,13 @@ struct Joint {
   int head, token0;           // key head, the sequence's first token
   int pad[3];
 };
+
+// A CTA's slot 1 takes the block that begins in it and goes on in the next one,
+// slot 0 a block that began before it.
+template <int COLS>
+__device__ __forceinline__ float4* part_slot(const AttendParams& P, int cta, int slot) {
+  return P.parts + (long long)(2 * cta + slot) * ((COLS / 4) * P.slot_rows + (P.slot_rows + 1) / 2);
+}
 
 // ----------------------------------------------------------------- PTX glue
 __device__ __forceinline__ void tma_box(void* dst, const CUtensorMap* map, int c0, int c1, int c2, int c3,
@@ -140,17 +147,14 @@ __device__ __forceinline__ void tmem_ld32(uint32_t addr, float* x) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(addr));
 }
-__device__ __forceinline__ void tmem_st32(uint32_t addr, const float* x) {
-  const uint32_t* r = reinterpret_cast<const uint32_t*>(x);
+__device__ __forceinline__ void tmem_ld16(uint32_t addr, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
   asm volatile(
-      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
-      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,"
-      "%31,%32};"
-      :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]),
-         "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]),
-         "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]),
-         "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
-      : "memory");
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(addr));
 }
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
@@ -253,31 +257,24 @@ __device__ __forceinline__ long long head_tiles(const AttendParams& P, const Chu
   return t;
 }
 
-// A CTA's walk over its span of the tile list.
+// A CTA's walk over its span of the tile list, a block's part at a time.
 struct Walk {
-  long long u, u1;            // the span's next tile and its end
-  int b, h, blk;              // the block that tile belongs to
-  long long blk_u;            // the block's first tile
+  int left;                   // tiles of the span from this part on
+  int b, h, blk;              // the block
   Chunk c;
-  int tiles;                  // the block's tiles
-  // the part of the block that lies in the span
-  int t0, t1, end, rows;
-  bool whole;
+  int tiles, end, rows;       // of the block: its tiles, where the last one ends, its rows
+  int t0, t1;                 // the part: tiles t0 .. t1
 
-  __device__ __forceinline__ bool open(const AttendParams& P) {
-    if (u >= u1) return false;
+  __device__ __forceinline__ void open(const AttendParams& P, int from) {
     tiles = block_tiles(P, c, blk);
     end = block_end(P, c, blk);
-    t0 = int(u - blk_u);
-    t1 = int(min((long long)tiles, u1 - blk_u));
     rows = min(kBlockRows, c.rows - blk * kBlockRows);
-    whole = t0 == 0 && t1 == tiles;
-    return true;
+    t0 = from;
+    t1 = min(tiles, from + left);
   }
   __device__ __forceinline__ bool next(const AttendParams& P) {
-    u = blk_u + t1;
-    if (u >= u1) return false;
-    blk_u = u;
+    left -= t1 - t0;
+    if (left <= 0) return false;
     if (++blk >= c.blocks) {
       blk = 0;
       if (++h >= P.Hkv) {
@@ -288,7 +285,8 @@ struct Walk {
         } while (c.blocks == 0);
       }
     }
-    return open(P);
+    open(P, 0);
+    return true;
   }
 };
 
@@ -393,26 +391,24 @@ __device__ void find_span(const AttendParams& P, Shared* sh) {
 }
 
 __device__ __forceinline__ bool begin_walk(const AttendParams& P, const Shared* sh, Walk& w) {
-  w.u = sh->span.u0;
-  w.u1 = sh->span.u1;
-  if (w.u >= w.u1) return false;
+  w.left = int(sh->span.u1 - sh->span.u0);
+  if (w.left <= 0) return false;
   w.b = sh->span.b;
   w.c = load_chunk(P, w.b);
   const long long per_head = head_tiles(P, w.c);
-  long long off = w.u - sh->span.base;
+  long long off = sh->span.u0 - sh->span.base;
   if (off < (1ll << 31) && per_head < (1ll << 31)) w.h = int(unsigned(off) / unsigned(per_head));
   else w.h = int(off / per_head);
   off -= w.h * per_head;
   w.blk = 0;
-  long long first = 0;
   for (;;) {
     const int n = block_tiles(P, w.c, w.blk);
-    if (first + n > off || w.blk + 1 >= w.c.blocks) break;
-    first += n;
+    if (n > off || w.blk + 1 >= w.c.blocks) break;
+    off -= n;
     ++w.blk;
   }
-  w.blk_u = w.u - (off - first);
-  return w.open(P);
+  w.open(P, int(off));
+  return true;
 }
 
 // Loads of a part of n tiles enter the ring as K0, then K(j+1) and V(j) in turn.
@@ -605,38 +601,44 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       }
     };
     // this warp's 32 rows of the block's queries, swizzled
+    constexpr int kChunks = 8 * DH, kPer = 32 / kChunks, kSteps = 32 / kPer;   // 16-byte chunks a row, rows a step
+    const int chunk = lane % kChunks, sub = lane / kChunks, warp_row = (warp & 3) * 32;
+    auto place = [&](int r) {
+      return q_half + (chunk >> 3) * kHalfTileBytes + r * kColBytes + (((chunk & 7) ^ (r & 7)) << 4);
+    };
+    auto query = [&](int rr) {           // row rr of the block
+      const int g = w.blk * kBlockRows + rr, token = P.by_group.div(g);
+      return static_cast<const T*>(P.q) + (long long)(w.c.start + token) * P.q_ts +
+             (long long)(w.h * P.G + g - token * P.G) * P.q_hs;
+    };
     auto load_q = [&]() {
-      constexpr int kChunks = 8 * DH, kPer = 32 / kChunks;        // 16-byte chunks per row, rows per step
-      const int chunk = lane % kChunks;
-      const int first = t * kHalfRows + (warp & 3) * 32 + lane / kChunks;
-      for (int i0 = 0; i0 < 32 && first - lane / kChunks + i0 < w.rows; i0 += 8 * kPer) {
-        uint4 x[8];
+      uint4 x[kSteps];
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int rr = first + i0 + u * kPer;
-          x[u] = make_uint4(0, 0, 0, 0);
-          if (rr < w.rows && 8 * chunk < P.D) {
-            const int g = w.blk * kBlockRows + rr;
-            const int token = P.by_group.div(g), head = w.h * P.G + g - token * P.G;
-            x[u] = *reinterpret_cast<const uint4*>(static_cast<const T*>(P.q) +
-                                                   (long long)(w.c.start + token) * P.q_ts +
-                                                   (long long)head * P.q_hs + 8 * chunk);
-          }
-        }
+      for (int u = 0; u < kSteps; ++u) {
+        const int rr = t * kHalfRows + warp_row + u * kPer + sub;
+        x[u] = make_uint4(0, 0, 0, 0);
+        if (rr < w.rows && 8 * chunk < P.D) x[u] = *reinterpret_cast<const uint4*>(query(rr) + 8 * chunk);
+      }
 #pragma unroll
-        for (int u = 0; u < 8; ++u) {
-          const int r = (first + i0 + u * kPer) & (kHalfRows - 1);
-          x[u].x = (x[u].x & P.q_and) ^ P.q_xor;
-          x[u].y = (x[u].y & P.q_and) ^ P.q_xor;
-          x[u].z = (x[u].z & P.q_and) ^ P.q_xor;
-          x[u].w = (x[u].w & P.q_and) ^ P.q_xor;
-          *reinterpret_cast<uint4*>(q_half + (chunk >> 3) * kHalfTileBytes + r * kColBytes +
-                                    (((chunk & 7) ^ (r & 7)) << 4)) = x[u];
-        }
+      for (int u = 0; u < kSteps; ++u) {
+        x[u].x = (x[u].x & P.q_and) ^ P.q_xor;
+        x[u].y = (x[u].y & P.q_and) ^ P.q_xor;
+        x[u].z = (x[u].z & P.q_and) ^ P.q_xor;
+        x[u].w = (x[u].w & P.q_and) ^ P.q_xor;
+        *reinterpret_cast<uint4*>(place(warp_row + u * kPer + sub)) = x[u];
       }
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_full[t]);
+    };
+    // a row per lane: the next block's queries come to L2 while this one is finished
+    auto prefetch_q = [&]() {
+      const int rr = t * kHalfRows + warp_row + lane;
+      if (rr < w.rows) {
+        const T* src = query(rr);
+        asm volatile("prefetch.global.L2 [%0];" :: "l"(src));
+        if (P.D > 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + 64));
+      }
     };
 
     skip_inactive();
@@ -710,13 +712,13 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
                 l *= keep;
               }
 #pragma unroll
-              for (int i = 0; i < kCols / 32; ++i) {
-                float o[32];
-                tmem_ld32(to + 32 * i, o);
-                loaded<32>(o);
+              for (int i = 0; i < kCols / 16; ++i) {
+                float o[16];
+                tmem_ld16(to + 16 * i, o);
+                loaded<16>(o);
 #pragma unroll
-                for (int k = 0; k < 32; ++k) o[k] *= keep;
-                tmem_st32(to + 32 * i, o);
+                for (int k = 0; k < 16; ++k) o[k] *= keep;
+                tmem_st16(to + 16 * i, reinterpret_cast<const uint32_t*>(o));
               }
             }
           }
@@ -765,18 +767,17 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       idx += 2 * n;
 
       // the finished part, while the next one's queries are already on their way
-      Walk done = w;
+      const int d_start = w.c.start, d_h = w.h, d_row0 = w.blk * kBlockRows, d_rows = w.rows, d_t0 = w.t0;
+      const int d_after = w.tiles - w.t1;                // the block's tiles in later CTAs
       more = w.next(P);
       skip_inactive();
-      if (more) load_q();
+      if (more) prefetch_q();
       ok = wait_warp(&sh->o_full[t], o_seen++ & 1u, sh, P.wait_limit);
       if (!ok) break;
       tc_after();
-      if (done.whole) {
+      if (d_t0 == 0 && d_after == 0) {
+        // through the query buffer (its products have ended), so that rows leave in whole lines
         const float inv = l > 0.f ? 1.f / l : 0.f;
-        const long long tok = done.c.start + token;
-        const int head = done.h * P.G + g - token * P.G;
-        T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
         if (warp_on) {
 #pragma unroll
           for (int i = 0; i < kCols / 32; ++i) {
@@ -786,16 +787,32 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
               const float* x = o + 8 * k;
-              const uint4 y = make_uint4(pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv),
-                                         pack2<T>(x[4] * inv, x[5] * inv), pack2<T>(x[6] * inv, x[7] * inv));
-              if (row_on && 32 * i + 8 * k < P.D) *reinterpret_cast<uint4*>(dst + 32 * i + 8 * k) = y;
+              *reinterpret_cast<uint4*>(q_half + (i >> 1) * kHalfTileBytes + row * kColBytes +
+                                        (((((i & 1) << 2) + k) ^ (row & 7)) << 4)) =
+                  make_uint4(pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv),
+                             pack2<T>(x[4] * inv, x[5] * inv), pack2<T>(x[6] * inv, x[7] * inv));
             }
           }
-          if (row_on && P.lse) P.lse[tok * P.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          if (row_on && P.lse)
+            P.lse[(long long)(d_start + token) * P.Hq + d_h * P.G + g - token * P.G] =
+                l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          __syncwarp();
+#pragma unroll
+          for (int u = 0; u < kSteps; ++u) {
+            const int r = warp_row + u * kPer + sub, rr = t * kHalfRows + r;
+            if (rr < d_rows && 8 * chunk < P.D) {
+              const int gg = d_row0 + rr;
+              const int tok = P.by_group.div(gg), head = d_h * P.G + gg - tok * P.G;
+              *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + (long long)(d_start + tok) * P.o_ts +
+                                        (long long)head * P.o_hs + 8 * chunk) =
+                  *reinterpret_cast<const uint4*>(place(r));
+            }
+          }
+          __syncwarp();
         }
       } else if (warp_on) {
-        const int slot = done.t0 > 0 ? 0 : 1;
-        float* dst = P.parts + (((long long)blockIdx.x * 2 + slot) * P.slot_rows + my_row) * (kCols + 4);
+        // [4 columns][row] so that a warp writes whole lines, then (m, l) of each row
+        float4* dst = part_slot<kCols>(P, blockIdx.x, d_t0 > 0 ? 0 : 1);
 #pragma unroll
         for (int i = 0; i < kCols / 32; ++i) {
           float o[32];
@@ -804,21 +821,20 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (row_on)
-              *reinterpret_cast<float4*>(dst + 32 * i + 4 * k) =
-                  make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+              dst[(8 * i + k) * P.slot_rows + my_row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
         }
-        if (row_on) *reinterpret_cast<float2*>(dst + kCols) = make_float2(m, l);
+        if (row_on) reinterpret_cast<float2*>(dst + kCols / 4 * P.slot_rows)[my_row] = make_float2(m, l);
       }
-      if (t == 0 && warp == 0 && lane == 0 && done.t0 == 0 && done.t1 < done.tiles) {
-        // the block goes on in later CTAs: this one's joint names it
+      if (more) load_q();
+      if (t == 0 && warp == 0 && lane == 0 && d_t0 == 0 && d_after > 0) {
+        // the span ends within the block: the joint names it and the CTAs that share it
         const Span& sp = sh->span;
-        const long long last = done.blk_u + done.tiles - 1;
         Joint jt;
-        jt.parts = int(((last + 1) * sp.ctas - 1) / sp.total) - int(blockIdx.x) + 1;
-        jt.rows = done.rows;
-        jt.row0 = done.blk * kBlockRows;
-        jt.head = done.h;
-        jt.token0 = done.c.start;
+        jt.parts = int(((sp.u1 + d_after) * sp.ctas - 1) / sp.total) - int(blockIdx.x) + 1;
+        jt.rows = d_rows;
+        jt.row0 = d_row0;
+        jt.head = d_h;
+        jt.token0 = d_start;
         P.joints[blockIdx.x] = jt;
       }
     }
@@ -833,48 +849,69 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
   }
 }
 
-// One warp per row of a block whose tiles several CTAs shared:
+// 32 rows of a block whose tiles several CTAs shared:
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  out = (sum O_i 2^(m_i - m)) / l
+// A thread takes four columns of a row; a warp takes up to 8 rows by 4 such
+// groups, so that both the parts (16 bytes of 8 rows) and the output (8 bytes
+// of 4 groups) move in whole sectors.
+constexpr int kJoinRows = 32;
 template <typename T, int DH>
 __global__ void __launch_bounds__(256)
 join_kernel(const AttendParams P) {
-  constexpr int kCols = 64 * DH, kPer = kCols / 32;
+  constexpr int kCols = 64 * DH, kC4 = kCols / 4;
+  __shared__ float2 ml[kCtas][kJoinRows];        // (m, l) of each part, then the part's weight
+  __shared__ float row_m[kJoinRows], row_inv[kJoinRows];
+  asm volatile("griddepcontrol.wait;" ::: "memory");
   const Joint jt = P.joints[blockIdx.x];
-  if (jt.parts <= 0) return;
-  const int lane = threadIdx.x & 31;
-  const long long cta_stride = 2ll * P.slot_rows * (kCols + 4);
-  for (int r = blockIdx.y * 8 + (threadIdx.x >> 5); r < jt.rows; r += gridDim.y * 8) {
-    // the first part lies in its CTA's slot 1, the others in slot 0
-    const float* first = P.parts + ((long long)blockIdx.x * 2 + 1) * P.slot_rows * (kCols + 4) + (long long)r * (kCols + 4);
-    const float* rest = P.parts + ((long long)blockIdx.x * 2) * P.slot_rows * (kCols + 4) + (long long)r * (kCols + 4);
-    float m = -INFINITY;
-    for (int i = lane; i < jt.parts; i += 32) m = fmaxf(m, (i == 0 ? first : rest + i * cta_stride)[kCols]);
-#pragma unroll
-    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(kFull, m, o));
+  const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, jt.rows - r0);
+  if (jt.parts <= 0 || rows <= 0) return;
+  const int tid = threadIdx.x;
+  auto slot = [&](int i) { return part_slot<kCols>(P, blockIdx.x + i, i == 0 ? 1 : 0); };
+  for (int e = tid; e < jt.parts * kJoinRows; e += 256) {
+    const int i = e / kJoinRows, r = e % kJoinRows;
+    if (r < rows) ml[i][r] = reinterpret_cast<const float2*>(slot(i) + kC4 * P.slot_rows)[r0 + r];
+  }
+  __syncthreads();
+  if (tid < rows) {
+    float m = -INFINITY, l = 0.f;
+    for (int i = 0; i < jt.parts; ++i) m = fmaxf(m, ml[i][tid].x);
     const float off = m == -INFINITY ? 0.f : m;
-    float l = 0.f, acc[kPer];
-#pragma unroll
-    for (int k = 0; k < kPer; ++k) acc[k] = 0.f;
-#pragma unroll 4
+    for (int i = 0; i < jt.parts; ++i) l = fmaf(ml[i][tid].y, ex2_approx(ml[i][tid].x - off), l);
+    row_m[tid] = off;
+    row_inv[tid] = l > 0.f ? 1.f / l : 0.f;
+    if (P.lse) {
+      const int g = jt.row0 + r0 + tid, token = P.by_group.div(g);
+      P.lse[(long long)(jt.token0 + token) * P.Hq + jt.head * P.G + g - token * P.G] =
+          l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    }
+  }
+  __syncthreads();
+  for (int e = tid; e < jt.parts * kJoinRows; e += 256) {
+    const int i = e / kJoinRows, r = e % kJoinRows;
+    if (r < rows) ml[i][r].x = ex2_approx(ml[i][r].x - row_m[r]);
+  }
+  __syncthreads();
+  const int lg = rows >= 8 ? 3 : rows >= 4 ? 2 : rows >= 2 ? 1 : 0;      // rows taken together: 2^lg
+  const int groups = (rows + (1 << lg) - 1) >> lg;
+  for (int e = tid; e < (groups * kC4) << lg; e += 256) {
+    const int c4 = (e >> lg) % kC4, r = ((e >> lg) / kC4 << lg) + (e & ((1 << lg) - 1));
+    if (r >= rows) continue;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
     for (int i = 0; i < jt.parts; ++i) {
-      const float* src = i == 0 ? first : rest + i * cta_stride;
-      const float2 ml = *reinterpret_cast<const float2*>(src + kCols);
-      const float f = ex2_approx(ml.x - off);
-      l = fmaf(ml.y, f, l);
-#pragma unroll
-      for (int k = 0; k < kPer; ++k) acc[k] = fmaf(src[kPer * lane + k], f, acc[k]);
+      const float4 x = slot(i)[c4 * P.slot_rows + r0 + r];
+      const float f = ml[i][r].x;
+      acc.x = fmaf(x.x, f, acc.x);
+      acc.y = fmaf(x.y, f, acc.y);
+      acc.z = fmaf(x.z, f, acc.z);
+      acc.w = fmaf(x.w, f, acc.w);
     }
-    const float inv = l > 0.f ? 1.f / l : 0.f;
-    const int g = jt.row0 + r, token = P.by_group.div(g);
-    const long long tok = jt.token0 + token;
-    const int head = jt.head * P.G + g - token * P.G;
-    T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
-    if (kPer * lane < P.D) {
-#pragma unroll
-      for (int k = 0; k < kPer; k += 2)
-        *reinterpret_cast<uint32_t*>(dst + kPer * lane + k) = pack2<T>(acc[k] * inv, acc[k + 1] * inv);
-    }
-    if (P.lse && lane == 0) P.lse[tok * P.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+    const float inv = row_inv[r];
+    const int g = jt.row0 + r0 + r, token = P.by_group.div(g);
+    if (4 * c4 < P.D)
+      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + (long long)(jt.token0 + token) * P.o_ts +
+                                (long long)(jt.head * P.G + g - token * P.G) * P.o_hs + 4 * c4) =
+          make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
   }
 }
 
@@ -945,9 +982,17 @@ cudaError_t launch(const AttendParams& P, const CUtensorMap& km, const CUtensorM
   attend_kernel<T, DH><<<kCtas, kThreads, smem, s>>>(P, km, vm);
   e = cudaGetLastError();
   if (e != cudaSuccess) return e;
-  const int chunks = (P.slot_rows + 31) / 32;
-  join_kernel<T, DH><<<dim3(kCtas, chunks), 256, 0, s>>>(P);
-  return cudaGetLastError();
+  // the join's CTAs take their places while the last attention CTAs finish, and wait there
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(kCtas, (P.slot_rows + kJoinRows - 1) / kJoinRows);
+  cfg.blockDim = dim3(256);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return cudaLaunchKernelEx(&cfg, join_kernel<T, DH>, P);
 }
 
 }  // namespace
@@ -958,7 +1003,8 @@ extern "C" size_t dart_attention_workspace_bytes(int T, int B, int q_heads, int 
   if (T < 0 || B < 0 || q_heads < 1 || heads < 1 || q_heads % heads != 0 || dim < 8 || dim > 128 || dim % 8 != 0)
     return 0;
   const size_t cols = dim <= 64 ? 64 : 128;
-  return kCtrlBytes + kJointBytes + size_t(kCtas) * 2 * slot_rows(T, q_heads / heads) * (cols + 4) * 4;
+  const size_t rows = slot_rows(T, q_heads / heads);
+  return kCtrlBytes + kJointBytes + size_t(kCtas) * 2 * (cols / 4 * rows + (rows + 1) / 2) * sizeof(float4);
 }
 
 extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
@@ -1000,7 +1046,7 @@ extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_
   uint8_t* ws = static_cast<uint8_t*>(workspace);
   P.err = reinterpret_cast<uint32_t*>(ws);
   P.joints = reinterpret_cast<Joint*>(ws + kCtrlBytes);
-  P.parts = reinterpret_cast<float*>(ws + kCtrlBytes + kJointBytes);
+  P.parts = reinterpret_cast<float4*>(ws + kCtrlBytes + kJointBytes);
   P.slot_rows = slot_rows(T, P.G);
   P.wait_limit = rows_wait_limit();
   CUtensorMap km, vm;

@@ -849,69 +849,74 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
   }
 }
 
-// 32 rows of a block whose tiles several CTAs shared:
+// Rows of a block whose tiles several CTAs shared, in one pass over the parts:
 //   m = max m_i,  l = sum l_i 2^(m_i - m),  out = (sum O_i 2^(m_i - m)) / l
-// A thread takes four columns of a row; a warp takes up to 8 rows by 4 such
-// groups, so that both the parts (16 bytes of 8 rows) and the output (8 bytes
-// of 4 groups) move in whole sectors.
-constexpr int kJoinRows = 32;
+// Latency bounds it, so nothing waits for another thread: a thread takes four
+// columns of two rows and four parts at a time, and finds its rows' weights
+// itself.  A warp covers 8 rows by 4 column groups, so that the parts (16 bytes
+// of 8 rows) and the output (8 bytes of 4 groups) move in whole sectors.
+constexpr int kJoinRows = 16, kJoinBatch = 4;
 template <typename T, int DH>
-__global__ void __launch_bounds__(256)
+__global__ void __launch_bounds__(128 * DH)
 join_kernel(const AttendParams P) {
   constexpr int kCols = 64 * DH, kC4 = kCols / 4;
-  __shared__ float2 ml[kCtas][kJoinRows];        // (m, l) of each part, then the part's weight
-  __shared__ float row_m[kJoinRows], row_inv[kJoinRows];
   asm volatile("griddepcontrol.wait;" ::: "memory");
   const Joint jt = P.joints[blockIdx.x];
-  const int r0 = blockIdx.y * kJoinRows, rows = min(kJoinRows, jt.rows - r0);
-  if (jt.parts <= 0 || rows <= 0) return;
-  const int tid = threadIdx.x;
-  auto slot = [&](int i) { return part_slot<kCols>(P, blockIdx.x + i, i == 0 ? 1 : 0); };
-  for (int e = tid; e < jt.parts * kJoinRows; e += 256) {
-    const int i = e / kJoinRows, r = e % kJoinRows;
-    if (r < rows) ml[i][r] = reinterpret_cast<const float2*>(slot(i) + kC4 * P.slot_rows)[r0 + r];
-  }
-  __syncthreads();
-  if (tid < rows) {
-    float m = -INFINITY, l = 0.f;
-    for (int i = 0; i < jt.parts; ++i) m = fmaxf(m, ml[i][tid].x);
-    const float off = m == -INFINITY ? 0.f : m;
-    for (int i = 0; i < jt.parts; ++i) l = fmaf(ml[i][tid].y, ex2_approx(ml[i][tid].x - off), l);
-    row_m[tid] = off;
-    row_inv[tid] = l > 0.f ? 1.f / l : 0.f;
-    if (P.lse) {
-      const int g = jt.row0 + r0 + tid, token = P.by_group.div(g);
-      P.lse[(long long)(jt.token0 + token) * P.Hq + jt.head * P.G + g - token * P.G] =
-          l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+  const int r0 = blockIdx.y * kJoinRows + (threadIdx.x & 7), c4 = threadIdx.x >> 3;
+  if (jt.parts <= 0 || r0 >= jt.rows) return;
+  const bool two = r0 + 8 < jt.rows;
+  float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.f, 0.f};
+  float4 acc[2] = {make_float4(0.f, 0.f, 0.f, 0.f), make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int i0 = 0; i0 < jt.parts; i0 += kJoinBatch) {
+    float4 x[kJoinBatch][2];
+    float2 ml[kJoinBatch][2];
+#pragma unroll
+    for (int i = 0; i < kJoinBatch; ++i)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        ml[i][e] = make_float2(-INFINITY, 0.f);
+        x[i][e] = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (i0 + i < jt.parts && (e == 0 || two)) {
+          const float4* slot = part_slot<kCols>(P, blockIdx.x + i0 + i, i0 + i == 0 ? 1 : 0);
+          ml[i][e] = reinterpret_cast<const float2*>(slot + kC4 * P.slot_rows)[r0 + 8 * e];
+          x[i][e] = slot[c4 * P.slot_rows + r0 + 8 * e];
+        }
+      }
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float top = m[e];
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) top = fmaxf(top, ml[i][e].x);
+      const float off = top == -INFINITY ? 0.f : top;
+      const float keep = ex2_approx(m[e] - off);
+      m[e] = top;
+      l[e] *= keep;
+      acc[e].x *= keep;
+      acc[e].y *= keep;
+      acc[e].z *= keep;
+      acc[e].w *= keep;
+#pragma unroll
+      for (int i = 0; i < kJoinBatch; ++i) {
+        const float f = ex2_approx(ml[i][e].x - off);
+        l[e] = fmaf(ml[i][e].y, f, l[e]);
+        acc[e].x = fmaf(x[i][e].x, f, acc[e].x);
+        acc[e].y = fmaf(x[i][e].y, f, acc[e].y);
+        acc[e].z = fmaf(x[i][e].z, f, acc[e].z);
+        acc[e].w = fmaf(x[i][e].w, f, acc[e].w);
+      }
     }
   }
-  __syncthreads();
-  for (int e = tid; e < jt.parts * kJoinRows; e += 256) {
-    const int i = e / kJoinRows, r = e % kJoinRows;
-    if (r < rows) ml[i][r].x = ex2_approx(ml[i][r].x - row_m[r]);
-  }
-  __syncthreads();
-  const int lg = rows >= 8 ? 3 : rows >= 4 ? 2 : rows >= 2 ? 1 : 0;      // rows taken together: 2^lg
-  const int groups = (rows + (1 << lg) - 1) >> lg;
-  for (int e = tid; e < (groups * kC4) << lg; e += 256) {
-    const int c4 = (e >> lg) % kC4, r = ((e >> lg) / kC4 << lg) + (e & ((1 << lg) - 1));
-    if (r >= rows) continue;
-    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = 0; i < jt.parts; ++i) {
-      const float4 x = slot(i)[c4 * P.slot_rows + r0 + r];
-      const float f = ml[i][r].x;
-      acc.x = fmaf(x.x, f, acc.x);
-      acc.y = fmaf(x.y, f, acc.y);
-      acc.z = fmaf(x.z, f, acc.z);
-      acc.w = fmaf(x.w, f, acc.w);
-    }
-    const float inv = row_inv[r];
-    const int g = jt.row0 + r0 + r, token = P.by_group.div(g);
+#pragma unroll
+  for (int e = 0; e < 2; ++e) {
+    if (e == 1 && !two) break;
+    const float inv = l[e] > 0.f ? 1.f / l[e] : 0.f;
+    const int g = jt.row0 + r0 + 8 * e, token = P.by_group.div(g);
+    const long long tok = jt.token0 + token;
+    const int head = jt.head * P.G + g - token * P.G;
     if (4 * c4 < P.D)
-      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + (long long)(jt.token0 + token) * P.o_ts +
-                                (long long)(jt.head * P.G + g - token * P.G) * P.o_hs + 4 * c4) =
-          make_uint2(pack2<T>(acc.x * inv, acc.y * inv), pack2<T>(acc.z * inv, acc.w * inv));
+      *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs + 4 * c4) =
+          make_uint2(pack2<T>(acc[e].x * inv, acc[e].y * inv), pack2<T>(acc[e].z * inv, acc[e].w * inv));
+    if (P.lse && c4 == 0) P.lse[tok * P.Hq + head] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.69314718055994531f : -INFINITY;
   }
 }
 
@@ -988,7 +993,7 @@ cudaError_t launch(const AttendParams& P, const CUtensorMap& km, const CUtensorM
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
   cfg.gridDim = dim3(kCtas, (P.slot_rows + kJoinRows - 1) / kJoinRows);
-  cfg.blockDim = dim3(256);
+  cfg.blockDim = dim3(128 * DH);
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;

@@ -7,12 +7,16 @@ from __future__ import annotations
 
 import contextlib
 import ctypes as C
+import functools
 import math
 
 import numpy as np
 
 from . import (DTYPE_CODES, DartError, _check, _check_error_word, _check_tensor, _check_workspace, _device_of,
-               _mask_dtypes, _on_device, _ptr, _row_stride, _stream_ptr, _torch, lib)
+               _mask_dtypes, _on_device, _row_stride, _stream_ptr, _torch, lib)
+
+
+_codes = functools.cache(DTYPE_CODES)
 
 
 class _Adjust(C.Structure):
@@ -52,19 +56,48 @@ def declare(L):
     L.dart_tree_attention.restype = i32
 
 
-def _strides(t):
-    """Element strides, 0 for a dimension that is never stepped along."""
-    return [st if size > 1 else 0 for size, st in zip(t.shape, t.stride())]
+# A call's host work is a good part of a small call's time, so the checks here
+# decide on plain integers and only a failing one looks for its words.
+
+_HERE = contextlib.nullcontext()
 
 
 @contextlib.contextmanager
-def _launching(dev, stream):
-    """The tensors' device, and the stream that the call launches on: what the
-    call allocates and clears itself is ordered with its kernels there."""
+def _elsewhere(dev, stream):
     with _on_device(dev):
         _stream_ptr(stream, dev)
-        with _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext():
+        with _torch().cuda.stream(stream) if stream is not None else _HERE:
             yield
+
+
+def _launching(dev, stream):
+    """Context of a call: the tensors' device, and the stream that it launches on,
+    so that what it allocates and clears itself is ordered with its kernels."""
+    if stream is None and dev.index == _torch().cuda.current_device():
+        return _HERE
+    return _elsewhere(dev, stream)
+
+
+def _stream(stream, dev):
+    """The stream's handle as an integer (the current one's without a stream)."""
+    if stream is None:
+        return _torch()._C._cuda_getCurrentRawStream(dev.index)
+    return stream.cuda_stream
+
+
+def _at(t):
+    return None if t is None else t.data_ptr()
+
+
+def _one_device(names, tensors):
+    """The one CUDA device of the tensors that are given."""
+    dev = tensors[0].device
+    for t in tensors:
+        if t is not None and (t.device != dev or not t.is_cuda):
+            break
+    else:
+        return dev
+    return _device_of(*zip(names, tensors))
 
 
 def _check_inner(t, name):
@@ -90,48 +123,55 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
     itself, or a new [B, R, V] tensor with evenly spaced rows."""
     torch = _torch()
     ids, vals = bias if bias is not None else (None, None)
-    dev = _device_of(("logits", logits), ("history", history), ("lengths", lengths), ("repetition", repetition),
-                     ("presence", presence), ("frequency", frequency), ("bias ids", ids), ("bias values", vals),
-                     ("allowed", allowed), ("tokens", tokens), ("mask", mask), ("out", out))
-    codes = DTYPE_CODES()
-    if logits.dtype not in codes or logits.dim() != 3:
+    dev = _one_device(("logits", "history", "lengths", "repetition", "presence", "frequency", "bias ids",
+                       "bias values", "allowed", "tokens", "mask", "out"),
+                      (logits, history, lengths, repetition, presence, frequency, ids, vals, allowed, tokens, mask,
+                       out))
+    code = _codes().get(logits.dtype)
+    if code is None or logits.dim() != 3:
         raise DartError("logits must be [B, R, V] float32, float16 or bfloat16")
     B, R, V = logits.shape
     if V < 1:
         raise DartError("logits must have at least one token")
-    stride = _row_stride(logits)
+    stride = V if logits.is_contiguous() else _row_stride(logits)
     a = _Adjust()
     if history is not None:
         if history.dim() != 2 or history.shape[0] != B:
             raise DartError(f"history must be [{B}, H]")
         _check_tensor(history, "history", torch.int32, contiguous=False)
         _check_inner(history, "history")
-        a.history, a.history_width = _ptr(history), history.shape[1]
+        a.history, a.history_width = history.data_ptr(), history.shape[1]
         a.history_stride = history.stride(0) if B > 1 else history.shape[1]
         if B > 1 and a.history_stride < history.shape[1]:
             raise DartError("history rows overlap")
     elif lengths is not None:
         raise DartError("lengths are given without a history")
-    _check_tensor(lengths, "lengths", torch.int32, (B,))
-    for t, name in ((repetition, "repetition"), (presence, "presence"), (frequency, "frequency")):
-        _check_tensor(t, name, torch.float32, (B,))
-    a.history_len = _ptr(lengths)
-    a.repetition, a.presence, a.frequency = _ptr(repetition), _ptr(presence), _ptr(frequency)
+    if lengths is not None:
+        _check_tensor(lengths, "lengths", torch.int32, (B,))
+        a.history_len = lengths.data_ptr()
+    if repetition is not None:
+        _check_tensor(repetition, "repetition", torch.float32, (B,))
+        a.repetition = repetition.data_ptr()
+    if presence is not None:
+        _check_tensor(presence, "presence", torch.float32, (B,))
+        a.presence = presence.data_ptr()
+    if frequency is not None:
+        _check_tensor(frequency, "frequency", torch.float32, (B,))
+        a.frequency = frequency.data_ptr()
     if ids is not None:
         if vals is None or ids.dim() != 2 or ids.shape[0] != B:
             raise DartError(f"bias must be (ids [{B}, K], values [{B}, K])")
         _check_tensor(ids, "bias ids", torch.int32)
         _check_tensor(vals, "bias values", torch.float32, tuple(ids.shape))
-        a.bias_ids, a.bias_vals, a.bias_count = _ptr(ids), _ptr(vals), ids.shape[1]
+        a.bias_ids, a.bias_vals, a.bias_count = ids.data_ptr(), vals.data_ptr(), ids.shape[1]
     if allowed is not None:
         words = (V + 31) // 32
         if tuple(allowed.shape) not in ((B, words), (B, R, words)):
             raise DartError(f"allowed must be [{B}, {words}] or [{B}, {R}, {words}], got {tuple(allowed.shape)}")
         _check_tensor(allowed, "allowed", _mask_dtypes(), contiguous=False)
         _check_inner(allowed, "allowed")
-        st = _strides(allowed)
-        a.allowed, a.allowed_seq_stride = _ptr(allowed), st[0]
-        a.allowed_row_stride = st[1] if allowed.dim() == 3 else 0
+        a.allowed, a.allowed_seq_stride = allowed.data_ptr(), allowed.stride(0) if B > 1 else 0
+        a.allowed_row_stride = allowed.stride(1) if allowed.dim() == 3 and R > 1 else 0
     if (tokens is None) != (mask is None):
         raise DartError("a tree needs both its tokens and its mask")
     if tokens is not None:
@@ -142,7 +182,7 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
         _check_tensor(mask, "mask", _mask_dtypes(), (B, N, (N + 31) // 32))
         if R not in (N, N + 1):
             raise DartError(f"a tree of {N} nodes needs {N} or {N + 1} rows of logits, got {R}")
-        a.tokens, a.mask, a.N = _ptr(tokens), _ptr(mask), N
+        a.tokens, a.mask, a.N = tokens.data_ptr(), mask.data_ptr(), N
     if out is not None:
         _check_tensor(out, "out", logits.dtype, (B, R, V), contiguous=False)
         out_stride = _row_stride(out)
@@ -152,10 +192,13 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
         if out is None:
             # rows that keep the input's alignment take whole vectors from end to end
             out_stride = V + (stride - V) % (16 // logits.element_size())
-            out = torch.empty((B, R, out_stride), dtype=logits.dtype, device=dev)[..., :V]
-        rc = lib().dart_logits_adjust(_ptr(logits), B, R, V, stride, codes[logits.dtype], C.byref(a), _ptr(out),
-                                      out_stride, _stream_ptr(stream, dev))
-    _check(rc, "dart_logits_adjust")
+            out = torch.empty((B, R, out_stride), dtype=logits.dtype, device=dev)
+            if out_stride != V:
+                out = out[..., :V]
+        rc = lib().dart_logits_adjust(logits.data_ptr(), B, R, V, stride, code, C.byref(a), out.data_ptr(),
+                                      out_stride, _stream(stream, dev))
+    if rc:
+        _check(rc, "dart_logits_adjust")
     return out
 
 
@@ -164,49 +207,61 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
 def _cache(k_cache, v_cache, pages, B):
     """The descriptor of caches [P, page, heads, dim] with a page table [B, width]."""
     torch = _torch()
-    if k_cache.dim() != 4 or v_cache.dim() != 4 or tuple(k_cache.shape) != tuple(v_cache.shape):
+    shape, dt = k_cache.shape, k_cache.dtype
+    if len(shape) != 4 or v_cache.shape != shape:
         raise DartError("k_cache and v_cache must both be [pages, page, heads, dim]")
-    if k_cache.dtype not in (torch.float16, torch.bfloat16) or v_cache.dtype != k_cache.dtype:
+    if dt not in (torch.float16, torch.bfloat16) or v_cache.dtype != dt:
         raise DartError("k_cache and v_cache must both be float16 or bfloat16")
     if pages.dim() != 2 or pages.shape[0] != B:
         raise DartError(f"pages must be [{B}, width]")
     _check_tensor(pages, "pages", torch.int32, contiguous=False)
-    _check_inner(pages, "pages")
-    c = _Cache()
+    count, page, heads, dim = shape
+    if page < 8 or page % 8:
+        raise DartError(f"pages must hold a multiple of 8 positions, got {page}")
+    if not 8 <= dim <= 128 or dim % 8:
+        raise DartError(f"heads must have a multiple of 8 elements, 8 to 128, got {dim}")
+    strides = []
     for t, x in ((k_cache, "k"), (v_cache, "v")):
-        _check_inner(t, f"{x}_cache")
-        setattr(c, x, t.data_ptr())
-        for name, st in zip(("page", "row", "head"), _strides(t)):
-            if st % 8:
-                raise DartError(f"{x}_cache strides must be multiples of 8 elements")
-            setattr(c, f"{x}_{name}_stride", st)
-    c.pages, c.page, c.heads, c.dim = k_cache.shape
-    if c.page < 8 or c.page % 8:
-        raise DartError(f"pages must hold a multiple of 8 positions, got {c.page}")
-    if not 8 <= c.dim <= 128 or c.dim % 8:
-        raise DartError(f"heads must have a multiple of 8 elements, 8 to 128, got {c.dim}")
-    c.dtype = DTYPE_CODES()[k_cache.dtype]
-    c.table, c.table_width = _ptr(pages), pages.shape[1]
-    c.table_stride = pages.stride(0) if B > 1 else pages.shape[1]
-    if B > 1 and c.table_stride < pages.shape[1]:
+        # a dimension of one is never stepped along
+        st = t.stride()
+        a, b, c = st[0] if count > 1 else 0, st[1], st[2] if heads > 1 else 0
+        if st[3] != 1:
+            raise DartError(f"{x}_cache must have unit stride in its last dimension")
+        if (a | b | c) & 7 or t.data_ptr() & 15:
+            raise DartError(f"{x}_cache must be 16-byte aligned, with strides of multiples of 8 elements")
+        # memory shared between elements (an expanded tensor) cannot be written
+        if b == 0 or (a == 0 and count > 1) or (c == 0 and heads > 1):
+            raise DartError(f"{x}_cache must not be an expanded tensor")
+        strides += (a, b, c)
+    width, step = pages.shape[1], pages.stride(0)
+    if width > 1 and pages.stride(1) != 1:
+        raise DartError("pages must have unit stride in its last dimension")
+    if B <= 1:
+        step = width
+    elif step < width:
         raise DartError("the rows of pages overlap")
-    return c
+    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages.data_ptr(), step, width, count, page, heads,
+                  dim, _codes()[dt])
 
 
 def _heads(t, name, T, heads, dim, dtype):
     """A [T, heads, dim] tensor of vectors: its (token, head) strides."""
+    st = t.stride()
+    if t.dtype == dtype and t.shape == (T, heads, dim) and st[2] == 1:
+        a, b = st[0] if T > 1 else 0, st[1] if heads > 1 else 0
+        if not ((a | b) & 7 or t.data_ptr() & 15):
+            return a, b
     _check_tensor(t, name, dtype, (T, heads, dim), contiguous=False)
     _check_inner(t, name)
-    st = _strides(t)
-    if st[0] % 8 or st[1] % 8 or t.data_ptr() % 16:
-        raise DartError(f"{name} must be 16-byte aligned, with strides of multiples of 8 elements")
-    return st[0], st[1]
+    raise DartError(f"{name} must be 16-byte aligned, with strides of multiples of 8 elements")
 
 
-def _no_overlap(t, name):
-    """Outputs whose elements share memory (an expanded tensor) are refused."""
-    if t.numel() > 1 and any(size > 1 and st == 0 for size, st in zip(t.shape, t.stride())):
+def _output(t, name, T, heads, dim, dtype):
+    """_heads of a tensor that is written: its elements share no memory."""
+    a, b = _heads(t, name, T, heads, dim, dtype)
+    if (a == 0 and T > 1) or (b == 0 and heads > 1):
         raise DartError(f"{name} must not be an expanded tensor")
+    return a, b
 
 
 def _sequences(lengths, starts):
@@ -214,8 +269,10 @@ def _sequences(lengths, starts):
     if lengths.dim() != 1:
         raise DartError("lengths must be [B]")
     B = lengths.shape[0]
-    _check_tensor(lengths, "lengths", torch.int32)
-    _check_tensor(starts, "starts", torch.int32, (B + 1,))
+    if lengths.dtype != torch.int32 or not lengths.is_contiguous():
+        _check_tensor(lengths, "lengths", torch.int32)
+    if starts.dtype != torch.int32 or starts.shape != (B + 1,) or not starts.is_contiguous():
+        _check_tensor(starts, "starts", torch.int32, (B + 1,))
     return B
 
 
@@ -280,47 +337,45 @@ def kv_append(q, k, v, k_cache, v_cache, pages, lengths, starts, *, rotary: Rota
     whose rows outside every sequence are unset (None without q).  device_err (int32 [>= 1], zeroed by the caller) collects
     the error bits of tokens that do not fit in their pages."""
     torch = _torch()
-    dev = _device_of(("k", k), ("v", v), ("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("pages", pages),
-                     ("lengths", lengths), ("starts", starts), ("rotary", rotary.turns if rotary is not None else None),
-                     ("offsets", offsets), ("q_weight", q_weight), ("k_weight", k_weight), ("out", out),
-                     ("device_err", device_err))
+    dev = _one_device(("k", "v", "q", "k_cache", "v_cache", "pages", "lengths", "starts", "rotary", "offsets",
+                       "q_weight", "k_weight", "out", "device_err"),
+                      (k, v, q, k_cache, v_cache, pages, lengths, starts,
+                       rotary.turns if rotary is not None else None, offsets, q_weight, k_weight, out, device_err))
     B = _sequences(lengths, starts)
     c = _cache(k_cache, v_cache, pages, B)
-    _no_overlap(k_cache, "k_cache")
-    _no_overlap(v_cache, "v_cache")
     if k.dim() != 3:
         raise DartError("k must be [T, heads, dim]")
-    T, dt = k.shape[0], k_cache.dtype
-    ks, vs = _heads(k, "k", T, c.heads, c.dim, dt), _heads(v, "v", T, c.heads, c.dim, dt)
-    qs = os = (0, 0)
-    Hq = 0
+    T, dt, dim = k.shape[0], k_cache.dtype, c.dim
+    k0, k1 = _heads(k, "k", T, c.heads, dim, dt)
+    v0, v1 = _heads(v, "v", T, c.heads, dim, dt)
+    Hq = q0 = q1 = o0 = o1 = 0
     if q is not None:
         if q.dim() != 3:
             raise DartError("q must be [T, q_heads, dim]")
         Hq = q.shape[1]
-        qs = _heads(q, "q", T, Hq, c.dim, dt)
+        q0, q1 = _heads(q, "q", T, Hq, dim, dt)
         if out is not None:
-            os = _heads(out, "out", T, Hq, c.dim, dt)
-            _no_overlap(out, "out")
-            if out.data_ptr() == q.data_ptr() and os != qs:
+            o0, o1 = _output(out, "out", T, Hq, dim, dt)
+            if out.data_ptr() == q.data_ptr() and (o0, o1) != (q0, q1):
                 raise DartError("out shares its first element with q, but not its strides")
     elif out is not None or q_weight is not None:
         raise DartError("out or q_weight is given without q")
     _check_tensor(offsets, "offsets", torch.int32, (T,))
-    _check_tensor(q_weight, "q_weight", dt, (c.dim,))
-    _check_tensor(k_weight, "k_weight", dt, (c.dim,))
-    if rotary is not None and rotary.rot > c.dim:
-        raise DartError(f"rotary turns {rotary.rot} elements of heads of {c.dim}")
+    _check_tensor(q_weight, "q_weight", dt, (dim,))
+    _check_tensor(k_weight, "k_weight", dt, (dim,))
+    if rotary is not None and rotary.rot > dim:
+        raise DartError(f"rotary turns {rotary.rot} elements of heads of {dim}")
     _check_error_word(device_err)
     with _launching(dev, stream):
         if q is not None and out is None:
-            out = torch.empty((T, Hq, c.dim), dtype=dt, device=dev)
-            os = _heads(out, "out", T, Hq, c.dim, dt)
-        rc = lib().dart_kv_append(_ptr(q), *qs, Hq, _ptr(k), *ks, _ptr(v), *vs, T, B, _ptr(lengths), _ptr(starts),
-                                  _ptr(offsets), C.byref(rotary.desc) if rotary is not None else None,
-                                  _ptr(q_weight), _ptr(k_weight), float(eps), C.byref(c), _ptr(out), *os,
-                                  _ptr(device_err), _stream_ptr(stream, dev))
-    _check(rc, "dart_kv_append")
+            out = torch.empty((T, Hq, dim), dtype=dt, device=dev)
+            o0, o1 = Hq * dim, dim
+        rc = lib().dart_kv_append(_at(q), q0, q1, Hq, k.data_ptr(), k0, k1, v.data_ptr(), v0, v1, T, B,
+                                  lengths.data_ptr(), starts.data_ptr(), _at(offsets),
+                                  C.byref(rotary.desc) if rotary is not None else None, _at(q_weight), _at(k_weight),
+                                  eps, C.byref(c), _at(out), o0, o1, _at(device_err), _stream(stream, dev))
+    if rc:
+        _check(rc, "dart_kv_append")
     return out
 
 
@@ -346,16 +401,17 @@ def tree_attention(q, k_cache, v_cache, pages, lengths, starts, *, mask=None, sc
     reads.  A workspace is reused by calls in order on one stream; calls that
     may overlap need one each."""
     torch = _torch()
-    dev = _device_of(("q", q), ("k_cache", k_cache), ("v_cache", v_cache), ("pages", pages), ("lengths", lengths),
-                     ("starts", starts), ("mask", mask), ("out", out), ("workspace", workspace))
+    dev = _one_device(("q", "k_cache", "v_cache", "pages", "lengths", "starts", "mask", "out", "workspace"),
+                      (q, k_cache, v_cache, pages, lengths, starts, mask, out, workspace))
     B = _sequences(lengths, starts)
     c = _cache(k_cache, v_cache, pages, B)
     if q.dim() != 3:
         raise DartError("q must be [T, q_heads, dim]")
-    T, Hq = q.shape[:2]
-    qs = _heads(q, "q", T, Hq, c.dim, k_cache.dtype)
-    if Hq < 1 or Hq % c.heads:
-        raise DartError(f"{Hq} query heads do not share {c.heads} key heads evenly")
+    T, Hq, dim = q.shape
+    dt, heads = k_cache.dtype, c.heads
+    q0, q1 = _heads(q, "q", T, Hq, c.dim, dt)
+    if Hq < 1 or Hq % heads:
+        raise DartError(f"{Hq} query heads do not share {heads} key heads evenly")
     N = 0
     if mask is not None:
         if mask.dim() != 3 or mask.shape[0] != B or mask.shape[2] != (mask.shape[1] + 31) // 32:
@@ -363,25 +419,25 @@ def tree_attention(q, k_cache, v_cache, pages, lengths, starts, *, mask=None, sc
         N = mask.shape[1]
         _check_tensor(mask, "mask", _mask_dtypes())
     if out is not None:
-        os = _heads(out, "out", T, Hq, c.dim, q.dtype)
-        _no_overlap(out, "out")
+        o0, o1 = _output(out, "out", T, Hq, dim, dt)
         if out.numel() and out.data_ptr() == q.data_ptr():
             raise DartError("out must not be q")
-    need = attention_workspace_bytes(T, B, Hq, c.heads, c.dim)
+    L = lib()
+    need = L.dart_attention_workspace_bytes(T, B, Hq, heads, dim)
     if workspace is not None:
         _check_workspace(workspace, need)
     with _launching(dev, stream):
         if out is None:
-            out = torch.empty((T, Hq, c.dim), dtype=q.dtype, device=dev)
-            os = _heads(out, "out", T, Hq, c.dim, q.dtype)
-        ws = workspace
-        if ws is None:
-            ws = torch.empty(need, dtype=torch.uint8, device=dev)
-            ws[:256].zero_()
+            out = torch.empty((T, Hq, dim), dtype=dt, device=dev)
+            o0, o1 = Hq * dim, dim
+        if workspace is None:
+            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace[:256].zero_()
         sums = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse else None
-        rc = lib().dart_tree_attention(_ptr(q), *qs, Hq, T, B, _ptr(lengths), _ptr(starts), _ptr(mask), N,
-                                       1.0 / math.sqrt(c.dim) if scale is None else float(scale), C.byref(c),
-                                       _ptr(out), *os, _ptr(sums), _ptr(ws), ws.numel() * ws.element_size(),
-                                       _stream_ptr(stream, dev))
-    _check(rc, "dart_tree_attention")
-    return dict(out=out, lse=sums, workspace=ws)
+        rc = L.dart_tree_attention(q.data_ptr(), q0, q1, Hq, T, B, lengths.data_ptr(), starts.data_ptr(), _at(mask), N,
+                                   dim ** -0.5 if scale is None else scale, C.byref(c), out.data_ptr(), o0, o1,
+                                   _at(sums), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
+                                   _stream(stream, dev))
+    if rc:
+        _check(rc, "dart_tree_attention")
+    return {"out": out, "lse": sums, "workspace": workspace}

@@ -150,7 +150,7 @@ def test_turns_are_exact_fractions(L):
 @pytest.fixture
 def on_cpu(monkeypatch):
     """CPU tensors pass the device check; reaching the library is a failure."""
-    monkeypatch.setattr(_steps, "_device_of", lambda *named: torch.device("cuda", 0))
+    monkeypatch.setattr(_steps, "_one_device", lambda names, tensors: torch.device("cuda", 0))
 
     def reached(*a, **k):
         raise AssertionError("the checks let this call through")

@@ -8,6 +8,7 @@
 // that slice of its rows.  A bitmap of the tokens that are counted or biased
 // lets every other element pass unexamined, and a vector of elements that the
 // grammar bans is written without being read.
+#include <atomic>
 #include <cmath>
 
 #include "dart_launch.h"
@@ -17,11 +18,15 @@ namespace {
 
 constexpr int kAdjThreads = 256;
 constexpr int kAdjWarps = kAdjThreads / 32;
-constexpr int kAdjWarpTokens = 1024;                       // tokens of the slice that one warp owns
-constexpr int kAdjSlice = kAdjWarps * kAdjWarpTokens;      // tokens per CTA
-constexpr int kAdjWords = kAdjSlice / 32;
+constexpr int kAdjVecs = 4;                                // 16-byte vectors a lane takes of a row
 constexpr int kMaxBias = 1024;                             // biases per sequence
 constexpr unsigned kFull = 0xFFFFFFFFu;
+
+// A vector per lane makes a block of tokens (256 of 16 bits, 128 of 32).  The
+// blocks of a CTA's slice go to its warps in turn, because the tokens that are
+// counted crowd together at low ids.
+template <typename T> constexpr int kBlock = 32 * (16 / int(sizeof(T)));
+template <typename T> constexpr int kSlice = kAdjWarps * kAdjVecs * kBlock<T>;
 
 struct AdjustParams {
   const void* in;
@@ -55,7 +60,19 @@ union Vec {
   T e[16 / sizeof(T)];
 };
 
-// `count` (<= 32) bits from bit `at` on of a word array of `words` words.
+// Logits pass through once: keep them out of the way of what is used again.
+__device__ __forceinline__ uint4 ldg_stream(const void* p) {
+  uint4 v;
+  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
+               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
+  return v;
+}
+__device__ __forceinline__ void stg_stream(void* p, uint4 v) {
+  asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
+               :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// 32 bits from bit `at` on of an array of `words` words (those behind it are 0).
 __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int at, int words) {
   const int i = at >> 5;
   const uint32_t lo = w[i];
@@ -64,36 +81,69 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int at, int words
   return __funnelshift_r(lo, hi, at & 31);
 }
 
+// The vector with -inf in the places whose bit of `keep` is clear.
 template <typename T>
-__global__ void __launch_bounds__(kAdjThreads)
+__device__ __forceinline__ uint4 ban(uint4 u, uint32_t keep) {
+  uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    uint32_t m;
+    if (sizeof(T) == 2) {
+      const uint32_t t = keep >> (2 * j);
+      const uint32_t u2 = (t | (t << 15)) & 0x00010001u;      // the two bits, one in each half
+      m = (u2 << 16) - u2;                                    // 0xFFFF in each kept half
+    } else {
+      m = 0u - ((keep >> j) & 1u);
+    }
+    w[j] = (w[j] & m) | (Elem<T>::kNegInf & ~m);
+  }
+  return make_uint4(w[0], w[1], w[2], w[3]);
+}
+
+// ALIGNED: every row begins on a 16-byte boundary, in and out.
+template <typename T, bool ALIGNED>
+__global__ void __launch_bounds__(kAdjThreads, 3)
 adjust_kernel(const AdjustParams P) {
   constexpr int E = 16 / int(sizeof(T));
+  constexpr int kBlk = kBlock<T>, kCta = kSlice<T>, kWords = kCta / 32;
+  constexpr uint32_t kAll = (1u << E) - 1u;
   extern __shared__ __align__(16) unsigned char smem[];
-  uint32_t* counts = reinterpret_cast<uint32_t*>(smem);                         // [kAdjSlice]
-  float* bias = reinterpret_cast<float*>(smem) + (P.count ? kAdjSlice : 0);     // [kAdjSlice]
-  __shared__ uint32_t cnt_bits[kAdjWords + 1];     // token is counted
-  __shared__ uint32_t bias_bits[kAdjWords + 1];    // token has a bias
-  __shared__ int32_t list_id[kMaxBias];            // the slice's biases, in their order
+  uint32_t* counts = reinterpret_cast<uint32_t*>(smem);                    // [kCta], with penalties
+  float* bias = reinterpret_cast<float*>(smem) + (P.count ? kCta : 0);     // [kCta], with biases
+  __shared__ __align__(16) uint32_t touched[kWords + 1];         // token is counted or biased
+  __shared__ uint32_t bias_bits[kWords + 1];       // token is biased
+  __shared__ int32_t list_id[kMaxBias];            // the slice's biases, in their order; then the tree's tokens
+  __shared__ float list_val[kMaxBias];
   __shared__ int32_t warp_n[kAdjWarps];
+  static_assert(kMaxN <= kMaxBias, "the tree's tokens take the place of the bias list");
 
   const int b = blockIdx.z;
-  const int v0 = blockIdx.x * kAdjSlice;
-  const int vn = min(P.V - v0, kAdjSlice);
+  const int v0 = blockIdx.x * kCta;
+  const int vn = min(P.V - v0, kCta);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const dart_adjust_t& a = P.a;
 
-  for (int i = tid; i <= kAdjWords; i += kAdjThreads) cnt_bits[i] = bias_bits[i] = 0u;
-  if (P.count)
-    for (int i = tid; i < kAdjSlice; i += kAdjThreads) counts[i] = 0u;
+  for (int i = tid; i <= kWords; i += kAdjThreads) touched[i] = bias_bits[i] = 0u;
+  {
+    uint4* z = reinterpret_cast<uint4*>(smem);
+    const int n = ((P.count ? 1 : 0) + (a.bias_count > 0 ? 1 : 0)) * (kCta / 4);
+    for (int i = tid; i < n; i += kAdjThreads) z[i] = make_uint4(0, 0, 0, 0);
+  }
   __syncthreads();
   if (P.count && a.history) {
     const int32_t* h = a.history + (long long)b * a.history_stride;
     const int len = a.history_len ? max(0, min(a.history_len[b], a.history_width)) : a.history_width;
-    for (int i = tid; i < len; i += kAdjThreads) {
-      const uint32_t t = uint32_t(h[i]) - uint32_t(v0);
-      if (t < uint32_t(vn)) {
-        atomicAdd(&counts[t], 1u);
-        atomicOr(&cnt_bits[t >> 5], 1u << (t & 31));
+    for (int i0 = tid; i0 < len; i0 += 8 * kAdjThreads) {
+      int32_t id[8];
+#pragma unroll
+      for (int k = 0; k < 8; ++k) id[k] = i0 + k * kAdjThreads < len ? h[i0 + k * kAdjThreads] : -1;
+#pragma unroll
+      for (int k = 0; k < 8; ++k) {
+        const uint32_t t = uint32_t(id[k]) - uint32_t(v0);
+        if (id[k] >= 0 && t < uint32_t(vn)) {
+          atomicAdd(&counts[t], 1u);
+          atomicOr(&touched[t >> 5], 1u << (t & 31));
+        }
       }
     }
   }
@@ -101,17 +151,18 @@ adjust_kernel(const AdjustParams P) {
     // The slice's biases, compacted in their order; then the first entry of
     // each id sums that id's values in order, so that repeated ids always give
     // the same sum.
-    __shared__ float list_val[kMaxBias];
     int n = 0;
     for (int base = 0; base < a.bias_count; base += kAdjThreads) {
       const int i = base + tid;
-      uint32_t t = kFull;
-      if (i < a.bias_count) t = uint32_t(a.bias_ids[(long long)b * a.bias_count + i]) - uint32_t(v0);
-      const bool in = t < uint32_t(vn);
+      int32_t id = -1;
+      if (i < a.bias_count) id = a.bias_ids[(long long)b * a.bias_count + i];
+      const uint32_t t = uint32_t(id) - uint32_t(v0);
+      const bool in = id >= 0 && t < uint32_t(vn);
       const unsigned m = __ballot_sync(kFull, in);
       if (lane == 0) warp_n[warp] = __popc(m);
       __syncthreads();
       int at = n + __popc(m & ((1u << lane) - 1u));
+#pragma unroll
       for (int w = 0; w < kAdjWarps; ++w) {
         if (w < warp) at += warp_n[w];
         n += warp_n[w];
@@ -133,125 +184,239 @@ adjust_kernel(const AdjustParams P) {
       bias[t] = s;
       atomicOr(&bias_bits[t >> 5], 1u << (t & 31));
     }
+    __syncthreads();
+    for (int i = tid; i < kWords; i += kAdjThreads) atomicOr(&touched[i], bias_bits[i]);
+  }
+  const int r_begin = blockIdx.y * P.row_group, r_end = min(P.R, r_begin + P.row_group);
+  const bool paths = P.count && a.N > 0;
+  int32_t* toks = list_id;
+  if (paths) {
+    __syncthreads();
+    for (int i = tid; i < a.N; i += kAdjThreads) toks[i] = a.tokens[(long long)b * a.N + i];
   }
   __syncthreads();
 
-  // from here on a warp touches its own tokens only
-  const int w0 = warp * kAdjWarpTokens;
-  const int wn = min(vn - w0, kAdjWarpTokens);
-  if (wn <= 0) return;
-  const float rep = a.repetition ? a.repetition[b] : 1.f;
+  // from here on a warp touches its own blocks only: block i begins at token
+  // (8 i + warp) * kBlk of the slice
+  if (warp * kBlk >= vn) return;
+  auto begin = [&](int i) { return (kAdjWarps * i + warp) * kBlk; };
+  auto size = [&](int i) { return min(vn - begin(i), kBlk); };          // <= 0 behind the vocabulary
+  const float rep = a.repetition ? a.repetition[b] : 1.f, inv_rep = 1.f / rep;
   const float pres = a.presence ? a.presence[b] : 0.f;
   const float freq = a.frequency ? a.frequency[b] : 0.f;
   const int words = (P.V + 31) >> 5;
   const int MW = (a.N + 31) >> 5;
-  const int r_end = min(P.R, int(blockIdx.y + 1) * P.row_group);
+  const bool biased = a.bias_count > 0;
 
-  // the counted / biased element t (index within the slice)
-  auto adjusted = [&](T raw, int t) -> T {
-    float x = Elem<T>::get(raw);
-    if ((cnt_bits[t >> 5] >> (t & 31)) & 1u) {
-      const uint32_t c = counts[t];
-      x = x > 0.f ? x / rep : x * rep;
-      x = x - freq * float(c) - pres;
+  // the nodes whose tokens this warp owns, 32 nodes a lane
+  uint32_t own_nodes = 0u;
+  auto owns = [&](int node) {
+    const uint32_t t = uint32_t(toks[node]) - uint32_t(v0);
+    return t < uint32_t(vn) && int(t / kBlk) % kAdjWarps == warp;
+  };
+  if (paths)
+    for (int k = 0; k < 32 && 32 * lane + k < a.N; ++k) own_nodes |= uint32_t(owns(32 * lane + k)) << k;
+  auto node_bits = [&](int r) {       // this lane's word of the row's path
+    const int node = r - (P.R - a.N);
+    return paths && r < r_end && node >= 0 && lane < MW ? a.mask[((long long)b * a.N + node) * MW + lane] : 0u;
+  };
+  // the tokens of the row's path join the counts, and leave them again
+  auto path_in = [&](uint32_t m) {
+    for (; m; m &= m - 1) {
+      const int t = toks[32 * lane + __ffs(m) - 1] - v0;
+      atomicAdd(&counts[t], 1u);
+      atomicOr(&touched[t >> 5], 1u << (t & 31));
     }
-    if ((bias_bits[t >> 5] >> (t & 31)) & 1u) x += bias[t];
-    return Elem<T>::put(x);
+    __syncwarp();
+  };
+  auto path_out = [&](uint32_t m) {
+    __syncwarp();
+    for (; m; m &= m - 1) {
+      const int t = toks[32 * lane + __ffs(m) - 1] - v0;
+      if (atomicSub(&counts[t], 1u) == 1u && !((bias_bits[t >> 5] >> (t & 31)) & 1u))
+        atomicAnd(&touched[t >> 5], ~(1u << (t & 31)));
+    }
+    __syncwarp();
   };
 
-  for (int r = blockIdx.y * P.row_group; r < r_end; ++r) {
-    const long long row = (long long)b * P.R + r;
-    const T* in = static_cast<const T*>(P.in) + row * P.in_stride + v0;
-    T* out = static_cast<T*>(P.out) + row * P.out_stride + v0;
-    const uint32_t* allow =
-        a.allowed ? a.allowed + (long long)b * a.allowed_seq_stride + (long long)r * a.allowed_row_stride : nullptr;
-
-    // the tokens on this row's path that the warp owns join the counts
-    const int node = r - (P.R - a.N);
-    const bool path = P.count && a.N > 0 && node >= 0;
-    uint32_t on_path = 0;
-    const int32_t* toks = nullptr;
-    if (path) {
-      toks = a.tokens + (long long)b * a.N + 32 * lane;
-      if (lane < MW) {
-        on_path = a.mask[((long long)b * a.N + node) * MW + lane];
-        if (32 * lane + 32 > a.N) on_path &= (1u << (a.N & 31)) - 1u;
-      }
-      for (uint32_t m = on_path; m; m &= m - 1) {
-        const uint32_t t = uint32_t(toks[__ffs(m) - 1]) - uint32_t(v0 + w0);
-        if (t < uint32_t(wn)) {
-          atomicAdd(&counts[w0 + t], 1u);
-          atomicOr(&cnt_bits[(w0 + t) >> 5], 1u << (t & 31));
-        }
-      }
-      __syncwarp();
-    }
-
-    auto scalar = [&](int t) {
-      const uint32_t word = allow ? allow[(v0 + t) >> 5] : kFull;
-      T x;
-      if ((word >> ((v0 + t) & 31)) & 1u) {
-        x = in[t];
-        if (((cnt_bits[t >> 5] | bias_bits[t >> 5]) >> (t & 31)) & 1u) x = adjusted(x, t);
-      } else {
-        x = Elem<T>::put(-INFINITY);
-      }
-      out[t] = x;
-    };
-    // elements before the first 16-byte boundary of the warp's part
-    const int phase = int((reinterpret_cast<uintptr_t>(in + w0) / sizeof(T)) % E);
-    const int head = min((E - phase) % E, wn);
-    if (((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0) {
-      const int nv = (wn - head) / E;
-      for (int i = lane; i < nv; i += 32) {
-        const int t = w0 + head + i * E;
-        constexpr uint32_t all = (1u << E) - 1u;
-        const uint32_t ok = (allow ? bits_at(allow, v0 + t, words) : kFull) & all;
-        Vec<T> x;
-        if (ok == 0u) {
-          x.u = make_uint4(Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf, Elem<T>::kNegInf);
-        } else {
-          x.u = *reinterpret_cast<const uint4*>(in + t);
-          const uint32_t hit = (bits_at(cnt_bits, t, kAdjWords + 1) | bits_at(bias_bits, t, kAdjWords + 1)) & all;
-          if (hit & ok) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              if ((hit >> e) & 1u) x.e[e] = adjusted(x.e[e], t + e);
-          }
-          if (ok != all) {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-              if (!((ok >> e) & 1u)) x.e[e] = Elem<T>::put(-INFINITY);
-          }
-        }
-        *reinterpret_cast<uint4*>(out + t) = x.u;
-      }
-      if (lane < head) scalar(w0 + lane);
-      const int tail = head + nv * E;
-      if (lane < wn - tail) scalar(w0 + tail + lane);
+  // element x with count c and bias y (0: not biased, as far as the value goes)
+  auto apply = [&](float x, uint32_t c, float y) {
+    const float z = fmaf(-freq, float(c), x > 0.f ? x * inv_rep : x * rep) - pres;
+    return (c ? z : x) + y;
+  };
+  auto scalar = [&](const T* in, T* out, const uint32_t* allow, int t) {
+    const uint32_t word = allow ? allow[(v0 + t) >> 5] : kFull;
+    T x;
+    if ((word >> ((v0 + t) & 31)) & 1u) {
+      x = in[t];
+      if ((touched[t >> 5] >> (t & 31)) & 1u)
+        x = Elem<T>::put(apply(Elem<T>::get(x), P.count ? counts[t] : 0u, biased ? bias[t] : 0.f));
     } else {
-      for (int i = lane; i < wn; i += 32) scalar(w0 + i);
+      x = Elem<T>::put(-INFINITY);
     }
+    out[t] = x;
+  };
+  // the elements of `hit` of the vector at token t (a multiple of 4 if ALIGNED)
+  auto adjust_vec = [&](Vec<T>& x, uint32_t hit, int t) {
+    uint32_t c[E];
+    float y[E];
+#pragma unroll
+    for (int e = 0; e < E; ++e) c[e] = 0u, y[e] = 0.f;
+    if constexpr (ALIGNED) {
+#pragma unroll
+      for (int e = 0; e < E; e += 4) {
+        if (P.count) *reinterpret_cast<uint4*>(c + e) = *reinterpret_cast<const uint4*>(counts + t + e);
+        if (biased) *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(bias + t + e);
+      }
+    } else {
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        if (P.count) c[e] = counts[t + e];
+        if (biased) y[e] = bias[t + e];
+      }
+    }
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if ((hit >> e) & 1u) x.e[e] = Elem<T>::put(apply(Elem<T>::get(x.e[e]), c[e], y[e]));
+  };
 
-    if (path) {        // and leave them again
-      __syncwarp();
-      for (uint32_t m = on_path; m; m &= m - 1) {
-        const uint32_t t = uint32_t(toks[__ffs(m) - 1]) - uint32_t(v0 + w0);
-        if (t < uint32_t(wn)) {
-          if (atomicSub(&counts[w0 + t], 1u) == 1u) atomicAnd(&cnt_bits[(w0 + t) >> 5], ~(1u << (t & 31)));
+  const T* in = static_cast<const T*>(P.in) + ((long long)b * P.R + r_begin) * P.in_stride + v0;
+  T* out = static_cast<T*>(P.out) + ((long long)b * P.R + r_begin) * P.out_stride + v0;
+  const uint32_t* allow =
+      a.allowed ? a.allowed + (long long)b * a.allowed_seq_stride + (long long)r_begin * a.allowed_row_stride : nullptr;
+  uint32_t path = node_bits(r_begin);
+
+  if constexpr (ALIGNED) {
+    // The lane's vectors lie kStep tokens apart, from t0 on; the first `nv` of
+    // them are whole.  The next row's grammar bits come while this one is worked on.
+    constexpr int kStep = kAdjWarps * kBlk;
+    const int t0 = begin(0) + lane * E;
+    int nv = 0;
+#pragma unroll
+    for (int i = 0; i < kAdjVecs; ++i) nv += t0 + i * kStep + E <= vn ? 1 : 0;
+    // tokens behind the last whole vector of the vocabulary, the warp that owns them taking them singly
+    const int rest = vn % E, rest0 = vn - rest;
+    const bool mine = lane < rest && rest0 / kBlk % kAdjWarps == warp;
+    const uint8_t* bytes = reinterpret_cast<const uint8_t*>(touched) + (t0 >> 3);
+    const int shift = t0 & 7;                     // a vector of four shares its byte with its neighbour
+    auto grammar = [&](const uint32_t* al) {      // eight bits per vector
+      uint32_t ok = 0u;
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(al) + ((v0 + t0) >> 3);
+#pragma unroll
+      for (int i = 0; i < kAdjVecs; ++i)
+        if (i < nv) ok |= ((uint32_t(src[i * (kStep / 8)]) >> shift) & kAll) << (8 * i);
+      return ok;
+    };
+    uint32_t ok = allow ? grammar(allow) : kFull;
+    in += t0;
+    out += t0;
+    for (int r = r_begin; r < r_end; ++r) {
+      Vec<T> x[kAdjVecs];
+#pragma unroll
+      for (int i = 0; i < kAdjVecs; ++i)
+        if (i < nv && ((ok >> (8 * i)) & kAll)) x[i].u = ldg_stream(in + i * kStep);
+      const uint32_t next_path = node_bits(r + 1);
+      uint32_t next_ok = kFull;
+      if (allow && r + 1 < r_end) next_ok = grammar(allow + a.allowed_row_stride);
+      const uint32_t m = path & own_nodes;
+      const bool walked = paths && __any_sync(kFull, m != 0u);
+      if (walked) path_in(m);
+#pragma unroll
+      for (int i = 0; i < kAdjVecs; ++i) {
+        if (i < nv) {
+          const uint32_t keep = (ok >> (8 * i)) & kAll;
+          const uint32_t hit = (uint32_t(bytes[i * (kStep / 8)]) >> shift) & keep;
+          if (hit) adjust_vec(x[i], hit, t0 + i * kStep);
+          if (allow) x[i].u = ban<T>(x[i].u, keep);
+          stg_stream(out + i * kStep, x[i].u);
         }
       }
-      __syncwarp();
+      if (mine) scalar(in - t0, out - t0, allow, rest0 + lane);
+      if (walked) path_out(m);
+      in += P.in_stride;
+      out += P.out_stride;
+      if (allow) allow += a.allowed_row_stride;
+      ok = next_ok;
+      path = next_path;
+    }
+  } else {
+    for (int r = r_begin; r < r_end; ++r) {
+      const uint32_t m = path & own_nodes;
+      path = node_bits(r + 1);
+      const bool walked = paths && __any_sync(kFull, m != 0u);
+      if (walked) path_in(m);
+      // elements before the first 16-byte boundary of every block of this row (a block is a multiple of 16 bytes)
+      const int head = int((16u - unsigned(reinterpret_cast<uintptr_t>(in) & 15u)) & 15u) / int(sizeof(T));
+      const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+      if (same) {
+        uint32_t ok[kAdjVecs];
+        Vec<T> x[kAdjVecs];
+#pragma unroll
+        for (int i = 0; i < kAdjVecs; ++i) {
+          const int t = begin(i) + head + lane * E;
+          ok[i] = head + (lane + 1) * E <= size(i) ? (allow ? bits_at(allow, v0 + t, words) & kAll : kAll) : 0u;
+        }
+#pragma unroll
+        for (int i = 0; i < kAdjVecs; ++i)
+          if (ok[i]) x[i].u = ldg_stream(in + begin(i) + head + lane * E);
+#pragma unroll
+        for (int i = 0; i < kAdjVecs; ++i) {
+          const int n = size(i), t = begin(i) + head + lane * E;
+          if (head + (lane + 1) * E <= n) {
+            const uint32_t hit = bits_at(touched, t, kWords + 1) & ok[i];
+            if (hit) adjust_vec(x[i], hit, t);
+            if (allow) x[i].u = ban<T>(x[i].u, ok[i]);
+            stg_stream(out + t, x[i].u);
+          }
+          if (lane < min(head, n)) scalar(in, out, allow, begin(i) + lane);
+          const int tail = head < n ? head + (n - head) / E * E : max(n, 0);
+          if (lane < n - tail) scalar(in, out, allow, begin(i) + tail + lane);
+        }
+      } else {
+        for (int i = 0; i < kAdjVecs; ++i)
+          for (int k = lane; k < size(i); k += 32) scalar(in, out, allow, begin(i) + k);
+      }
+      if (walked) path_out(m);
+      in += P.in_stride;
+      out += P.out_stride;
+      if (allow) allow += a.allowed_row_stride;
     }
   }
 }
 
-template <typename T>
-cudaError_t launch_adjust(const AdjustParams& P, dim3 grid, size_t smem, cudaStream_t stream) {
-  const cudaError_t e =
-      cudaFuncSetAttribute(adjust_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kAdjSlice);
+template <typename T, bool ALIGNED>
+cudaError_t raise_limit() {
+  static std::atomic<uint64_t> ready{0};       // devices whose shared-memory limit is raised
+  int dev = 0;
+  cudaError_t e = cudaGetDevice(&dev);
   if (e != cudaSuccess) return e;
-  adjust_kernel<T><<<grid, kAdjThreads, smem, stream>>>(P);
+  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
+  if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
+    e = cudaFuncSetAttribute(adjust_kernel<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kSlice<T>);
+    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
+  }
+  return e;
+}
+
+template <typename T>
+cudaError_t launch_adjust(AdjustParams P, int B, cudaStream_t stream) {
+  const uintptr_t low = reinterpret_cast<uintptr_t>(P.in) | reinterpret_cast<uintptr_t>(P.out) |
+                        uintptr_t((P.in_stride | P.out_stride) * int(sizeof(T)));
+  const bool aligned = (low & 15) == 0;
+  const cudaError_t e = aligned ? raise_limit<T, true>() : raise_limit<T, false>();
+  if (e != cudaSuccess) return e;
+  const int slices = (P.V + kSlice<T> - 1) / kSlice<T>;
+  // rows per CTA: enough CTAs to fill the device a few times, then as many rows
+  // as possible share one count
+  const long long want = 152ll * 3 * 4, per = (long long)slices * B;
+  long long groups = (want + per - 1) / per;
+  groups = groups > P.R ? P.R : groups;
+  if (groups > 65535) groups = 65535;
+  P.row_group = int((P.R + groups - 1) / groups);
+  const dim3 grid(slices, (P.R + P.row_group - 1) / P.row_group, B);
+  const size_t smem = size_t(4 * kSlice<T>) * ((P.count ? 1 : 0) + (P.a.bias_count > 0 ? 1 : 0));
+  if (aligned) adjust_kernel<T, true><<<grid, kAdjThreads, smem, stream>>>(P);
+  else adjust_kernel<T, false><<<grid, kAdjThreads, smem, stream>>>(P);
   return cudaGetLastError();
 }
 
@@ -287,21 +452,10 @@ extern "C" int dart_logits_adjust(const void* logits, int B, int R, int V, int64
   P.out_stride = out_stride;
   P.a = a;
   P.count = a.repetition || a.presence || a.frequency;
-  const int slices = (V + kAdjSlice - 1) / kAdjSlice;
-  // rows per CTA: enough CTAs to fill the device a few times, then as many rows
-  // as possible share one count
-  const long long want = 152ll * 3 * 4;
-  const long long per = (long long)slices * B;
-  long long groups = (want + per - 1) / per;
-  groups = groups < 1 ? 1 : groups > R ? R : groups;
-  if (groups > 65535) groups = 65535;
-  P.row_group = int((R + groups - 1) / groups);
-  const dim3 grid(slices, (R + P.row_group - 1) / P.row_group, B);
-  const size_t smem = size_t(4 * kAdjSlice) * ((P.count ? 1 : 0) + (a.bias_count > 0 ? 1 : 0));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
-  if (dtype == DART_F32) e = launch_adjust<float>(P, grid, smem, s);
-  else if (dtype == DART_F16) e = launch_adjust<__half>(P, grid, smem, s);
-  else e = launch_adjust<__nv_bfloat16>(P, grid, smem, s);
+  if (dtype == DART_F32) e = launch_adjust<float>(P, B, s);
+  else if (dtype == DART_F16) e = launch_adjust<__half>(P, B, s);
+  else e = launch_adjust<__nv_bfloat16>(P, B, s);
   return e == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

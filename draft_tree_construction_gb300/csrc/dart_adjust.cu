@@ -23,8 +23,9 @@ constexpr int kMaxBias = 1024;                             // biases per sequenc
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // A vector per lane makes a block of tokens (256 of 16 bits, 128 of 32).  The
-// blocks of a CTA's slice go to its warps in turn, because the tokens that are
-// counted crowd together at low ids.
+// blocks of the vocabulary are dealt to the CTAs in turn and a CTA's blocks to
+// its warps in turn, because the tokens that are counted crowd together at low
+// ids and a block that holds any takes several times as long.
 template <typename T> constexpr int kBlock = 32 * (16 / int(sizeof(T)));
 template <typename T> constexpr int kSlice = kAdjWarps * kAdjVecs * kBlock<T>;
 
@@ -35,6 +36,7 @@ struct AdjustParams {
   long long in_stride, out_stride;
   dart_adjust_t a;
   bool count;                          // some penalty is given
+  FastDiv by_slices;                   // slices of the vocabulary: block k belongs to slice k % slices
 };
 
 template <typename T> struct Elem;
@@ -114,14 +116,36 @@ adjust_kernel(const AdjustParams P) {
   __shared__ uint32_t bias_bits[kWords + 1];       // token is biased
   __shared__ int32_t list_id[kMaxBias];            // the slice's biases, in their order; then the tree's tokens
   __shared__ float list_val[kMaxBias];
-  __shared__ int32_t warp_n[kAdjWarps];
+  __shared__ int32_t warp_n[kMaxBias / kAdjThreads][kAdjWarps];
   static_assert(kMaxN <= kMaxBias, "the tree's tokens take the place of the bias list");
 
-  const int b = blockIdx.z;
-  const int v0 = blockIdx.x * kCta;
-  const int vn = min(P.V - v0, kCta);
+  const int b = blockIdx.z, slice = blockIdx.x, slices = int(P.by_slices.d);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   const dart_adjust_t& a = P.a;
+  // token -> its place in the slice, -1 if it belongs to another or to none
+  auto local = [&](int32_t token) {
+    const int blk = token / kBlk, k = P.by_slices.div(blk);
+    return uint32_t(token) < uint32_t(P.V) && blk - k * slices == slice ? k * kBlk + token % kBlk : -1;
+  };
+
+  // Everything that the slice needs from memory is asked for before anything waits.
+  constexpr int kAhead = 8, kBiasAhead = kMaxBias / kAdjThreads;
+  const int32_t* hist = P.count && a.history ? a.history + (long long)b * a.history_stride : nullptr;
+  const int width = hist ? a.history_width : 0;
+  int32_t id[kAhead], bias_id[kBiasAhead];
+  float bias_val[kBiasAhead];
+#pragma unroll
+  for (int k = 0; k < kAhead; ++k) id[k] = tid + k * kAdjThreads < width ? hist[tid + k * kAdjThreads] : -1;
+#pragma unroll
+  for (int k = 0; k < kBiasAhead; ++k) {
+    const int i = tid + k * kAdjThreads;
+    bias_id[k] = i < a.bias_count ? a.bias_ids[(long long)b * a.bias_count + i] : -1;
+    bias_val[k] = i < a.bias_count ? a.bias_vals[(long long)b * a.bias_count + i] : 0.f;
+  }
+  const int len = hist ? (a.history_len ? max(0, min(a.history_len[b], width)) : width) : 0;
+  const float rep = a.repetition ? a.repetition[b] : 1.f, inv_rep = 1.f / rep;
+  const float pres = a.presence ? a.presence[b] : 0.f;
+  const float freq = a.frequency ? a.frequency[b] : 0.f;
 
   for (int i = tid; i <= kWords; i += kAdjThreads) touched[i] = bias_bits[i] = 0u;
   {
@@ -130,20 +154,17 @@ adjust_kernel(const AdjustParams P) {
     for (int i = tid; i < n; i += kAdjThreads) z[i] = make_uint4(0, 0, 0, 0);
   }
   __syncthreads();
-  if (P.count && a.history) {
-    const int32_t* h = a.history + (long long)b * a.history_stride;
-    const int len = a.history_len ? max(0, min(a.history_len[b], a.history_width)) : a.history_width;
-    for (int i0 = tid; i0 < len; i0 += 8 * kAdjThreads) {
-      int32_t id[8];
+  for (int i0 = tid; i0 < len; i0 += kAhead * kAdjThreads) {
+    if (i0 != tid) {
 #pragma unroll
-      for (int k = 0; k < 8; ++k) id[k] = i0 + k * kAdjThreads < len ? h[i0 + k * kAdjThreads] : -1;
+      for (int k = 0; k < kAhead; ++k) id[k] = i0 + k * kAdjThreads < len ? hist[i0 + k * kAdjThreads] : -1;
+    }
 #pragma unroll
-      for (int k = 0; k < 8; ++k) {
-        const uint32_t t = uint32_t(id[k]) - uint32_t(v0);
-        if (id[k] >= 0 && t < uint32_t(vn)) {
-          atomicAdd(&counts[t], 1u);
-          atomicOr(&touched[t >> 5], 1u << (t & 31));
-        }
+    for (int k = 0; k < kAhead; ++k) {
+      const int t = i0 + k * kAdjThreads < len ? local(id[k]) : -1;
+      if (t >= 0) {
+        atomicAdd(&counts[t], 1u);
+        atomicOr(&touched[t >> 5], 1u << (t & 31));
       }
     }
   }
@@ -152,27 +173,25 @@ adjust_kernel(const AdjustParams P) {
     // each id sums that id's values in order, so that repeated ids always give
     // the same sum.
     int n = 0;
-    for (int base = 0; base < a.bias_count; base += kAdjThreads) {
-      const int i = base + tid;
-      int32_t id = -1;
-      if (i < a.bias_count) id = a.bias_ids[(long long)b * a.bias_count + i];
-      const uint32_t t = uint32_t(id) - uint32_t(v0);
-      const bool in = id >= 0 && t < uint32_t(vn);
-      const unsigned m = __ballot_sync(kFull, in);
-      if (lane == 0) warp_n[warp] = __popc(m);
+#pragma unroll
+    for (int k = 0; k < kBiasAhead; ++k) {
+      if (k * kAdjThreads >= a.bias_count) break;
+      const int t = local(bias_id[k]);
+      const unsigned m = __ballot_sync(kFull, t >= 0);
+      if (lane == 0) warp_n[k][warp] = __popc(m);
       __syncthreads();
       int at = n + __popc(m & ((1u << lane) - 1u));
 #pragma unroll
       for (int w = 0; w < kAdjWarps; ++w) {
-        if (w < warp) at += warp_n[w];
-        n += warp_n[w];
+        if (w < warp) at += warp_n[k][w];
+        n += warp_n[k][w];
       }
-      if (in) {
-        list_id[at] = int32_t(t);
-        list_val[at] = a.bias_vals[(long long)b * a.bias_count + i];
+      if (t >= 0) {
+        list_id[at] = t;
+        list_val[at] = bias_val[k];
       }
-      __syncthreads();
     }
+    __syncthreads();
     for (int i = tid; i < n; i += kAdjThreads) {
       const int32_t t = list_id[i];
       bool first = true;
@@ -183,37 +202,31 @@ adjust_kernel(const AdjustParams P) {
         if (list_id[j] == t) s += list_val[j];
       bias[t] = s;
       atomicOr(&bias_bits[t >> 5], 1u << (t & 31));
+      atomicOr(&touched[t >> 5], 1u << (t & 31));
     }
-    __syncthreads();
-    for (int i = tid; i < kWords; i += kAdjThreads) atomicOr(&touched[i], bias_bits[i]);
   }
   const int r_begin = blockIdx.y * P.row_group, r_end = min(P.R, r_begin + P.row_group);
   const bool paths = P.count && a.N > 0;
-  int32_t* toks = list_id;
+  int32_t* toks = list_id;                       // from here on: the places of the tree's tokens in the slice
   if (paths) {
     __syncthreads();
-    for (int i = tid; i < a.N; i += kAdjThreads) toks[i] = a.tokens[(long long)b * a.N + i];
+    for (int i = tid; i < a.N; i += kAdjThreads) toks[i] = local(a.tokens[(long long)b * a.N + i]);
   }
   __syncthreads();
 
-  // from here on a warp touches its own blocks only: block i begins at token
-  // (8 i + warp) * kBlk of the slice
-  if (warp * kBlk >= vn) return;
-  auto begin = [&](int i) { return (kAdjWarps * i + warp) * kBlk; };
-  auto size = [&](int i) { return min(vn - begin(i), kBlk); };          // <= 0 behind the vocabulary
-  const float rep = a.repetition ? a.repetition[b] : 1.f, inv_rep = 1.f / rep;
-  const float pres = a.presence ? a.presence[b] : 0.f;
-  const float freq = a.frequency ? a.frequency[b] : 0.f;
+  // From here on a warp touches its own blocks only: block i lies at place
+  // (8 i + warp) * kBlk of the slice and holds the tokens from token(i) on.
+  auto place = [&](int i) { return (kAdjWarps * i + warp) * kBlk; };
+  auto token = [&](int i) { return ((kAdjWarps * i + warp) * slices + slice) * kBlk; };
+  auto size = [&](int i) { return min(P.V - token(i), kBlk); };          // <= 0 behind the vocabulary
+  if (token(0) >= P.V) return;
   const int words = (P.V + 31) >> 5;
   const int MW = (a.N + 31) >> 5;
   const bool biased = a.bias_count > 0;
 
   // the nodes whose tokens this warp owns, 32 nodes a lane
   uint32_t own_nodes = 0u;
-  auto owns = [&](int node) {
-    const uint32_t t = uint32_t(toks[node]) - uint32_t(v0);
-    return t < uint32_t(vn) && int(t / kBlk) % kAdjWarps == warp;
-  };
+  auto owns = [&](int node) { return toks[node] >= 0 && toks[node] / kBlk % kAdjWarps == warp; };
   if (paths)
     for (int k = 0; k < 32 && 32 * lane + k < a.N; ++k) own_nodes |= uint32_t(owns(32 * lane + k)) << k;
   auto node_bits = [&](int r) {       // this lane's word of the row's path
@@ -223,7 +236,7 @@ adjust_kernel(const AdjustParams P) {
   // the tokens of the row's path join the counts, and leave them again
   auto path_in = [&](uint32_t m) {
     for (; m; m &= m - 1) {
-      const int t = toks[32 * lane + __ffs(m) - 1] - v0;
+      const int t = toks[32 * lane + __ffs(m) - 1];
       atomicAdd(&counts[t], 1u);
       atomicOr(&touched[t >> 5], 1u << (t & 31));
     }
@@ -232,7 +245,7 @@ adjust_kernel(const AdjustParams P) {
   auto path_out = [&](uint32_t m) {
     __syncwarp();
     for (; m; m &= m - 1) {
-      const int t = toks[32 * lane + __ffs(m) - 1] - v0;
+      const int t = toks[32 * lane + __ffs(m) - 1];
       if (atomicSub(&counts[t], 1u) == 1u && !((bias_bits[t >> 5] >> (t & 31)) & 1u))
         atomicAnd(&touched[t >> 5], ~(1u << (t & 31)));
     }
@@ -244,19 +257,20 @@ adjust_kernel(const AdjustParams P) {
     const float z = fmaf(-freq, float(c), x > 0.f ? x * inv_rep : x * rep) - pres;
     return (c ? z : x) + y;
   };
-  auto scalar = [&](const T* in, T* out, const uint32_t* allow, int t) {
-    const uint32_t word = allow ? allow[(v0 + t) >> 5] : kFull;
+  // one element: token v, at place t of the slice
+  auto scalar = [&](const T* in, T* out, const uint32_t* allow, int v, int t) {
+    const uint32_t word = allow ? allow[v >> 5] : kFull;
     T x;
-    if ((word >> ((v0 + t) & 31)) & 1u) {
-      x = in[t];
+    if ((word >> (v & 31)) & 1u) {
+      x = in[v];
       if ((touched[t >> 5] >> (t & 31)) & 1u)
         x = Elem<T>::put(apply(Elem<T>::get(x), P.count ? counts[t] : 0u, biased ? bias[t] : 0.f));
     } else {
       x = Elem<T>::put(-INFINITY);
     }
-    out[t] = x;
+    out[v] = x;
   };
-  // the elements of `hit` of the vector at token t (a multiple of 4 if ALIGNED)
+  // the elements `hit` of the vector at place t (a multiple of 4 if ALIGNED)
   auto adjust_vec = [&](Vec<T>& x, uint32_t hit, int t) {
     uint32_t c[E];
     float y[E];
@@ -280,41 +294,40 @@ adjust_kernel(const AdjustParams P) {
       if ((hit >> e) & 1u) x.e[e] = Elem<T>::put(apply(Elem<T>::get(x.e[e]), c[e], y[e]));
   };
 
-  const T* in = static_cast<const T*>(P.in) + ((long long)b * P.R + r_begin) * P.in_stride + v0;
-  T* out = static_cast<T*>(P.out) + ((long long)b * P.R + r_begin) * P.out_stride + v0;
+  const T* in = static_cast<const T*>(P.in) + ((long long)b * P.R + r_begin) * P.in_stride;
+  T* out = static_cast<T*>(P.out) + ((long long)b * P.R + r_begin) * P.out_stride;
   const uint32_t* allow =
       a.allowed ? a.allowed + (long long)b * a.allowed_seq_stride + (long long)r_begin * a.allowed_row_stride : nullptr;
   uint32_t path = node_bits(r_begin);
 
   if constexpr (ALIGNED) {
-    // The lane's vectors lie kStep tokens apart, from t0 on; the first `nv` of
+    // The lane's vectors lie `step` tokens apart, from v0 on; the first `nv` of
     // them are whole.  The next row's grammar bits come while this one is worked on.
-    constexpr int kStep = kAdjWarps * kBlk;
-    const int t0 = begin(0) + lane * E;
+    const int step = kAdjWarps * slices * kBlk, v0 = token(0) + lane * E, t0 = place(0) + lane * E;
     int nv = 0;
 #pragma unroll
-    for (int i = 0; i < kAdjVecs; ++i) nv += t0 + i * kStep + E <= vn ? 1 : 0;
+    for (int i = 0; i < kAdjVecs; ++i) nv += v0 + i * step + E <= P.V ? 1 : 0;
     // tokens behind the last whole vector of the vocabulary, the warp that owns them taking them singly
-    const int rest = vn % E, rest0 = vn - rest;
-    const bool mine = lane < rest && rest0 / kBlk % kAdjWarps == warp;
+    const int rest = P.V % E, rest0 = P.V - rest, rest_at = local(rest0);
+    const bool mine = rest > 0 && lane < rest && rest_at >= 0 && rest_at / kBlk % kAdjWarps == warp;
     const uint8_t* bytes = reinterpret_cast<const uint8_t*>(touched) + (t0 >> 3);
     const int shift = t0 & 7;                     // a vector of four shares its byte with its neighbour
     auto grammar = [&](const uint32_t* al) {      // eight bits per vector
       uint32_t ok = 0u;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(al) + ((v0 + t0) >> 3);
+      const uint8_t* src = reinterpret_cast<const uint8_t*>(al) + (v0 >> 3);
 #pragma unroll
       for (int i = 0; i < kAdjVecs; ++i)
-        if (i < nv) ok |= ((uint32_t(src[i * (kStep / 8)]) >> shift) & kAll) << (8 * i);
+        if (i < nv) ok |= ((uint32_t(src[i * (step / 8)]) >> shift) & kAll) << (8 * i);
       return ok;
     };
     uint32_t ok = allow ? grammar(allow) : kFull;
-    in += t0;
-    out += t0;
+    in += v0;
+    out += v0;
     for (int r = r_begin; r < r_end; ++r) {
       Vec<T> x[kAdjVecs];
 #pragma unroll
       for (int i = 0; i < kAdjVecs; ++i)
-        if (i < nv && ((ok >> (8 * i)) & kAll)) x[i].u = ldg_stream(in + i * kStep);
+        if (i < nv && ((ok >> (8 * i)) & kAll)) x[i].u = ldg_stream(in + i * step);
       const uint32_t next_path = node_bits(r + 1);
       uint32_t next_ok = kFull;
       if (allow && r + 1 < r_end) next_ok = grammar(allow + a.allowed_row_stride);
@@ -325,13 +338,13 @@ adjust_kernel(const AdjustParams P) {
       for (int i = 0; i < kAdjVecs; ++i) {
         if (i < nv) {
           const uint32_t keep = (ok >> (8 * i)) & kAll;
-          const uint32_t hit = (uint32_t(bytes[i * (kStep / 8)]) >> shift) & keep;
-          if (hit) adjust_vec(x[i], hit, t0 + i * kStep);
+          const uint32_t hit = (uint32_t(bytes[i * (kAdjWarps * kBlk / 8)]) >> shift) & keep;
+          if (hit) adjust_vec(x[i], hit, t0 + i * (kAdjWarps * kBlk));
           if (allow) x[i].u = ban<T>(x[i].u, keep);
-          stg_stream(out + i * kStep, x[i].u);
+          stg_stream(out + i * step, x[i].u);
         }
       }
-      if (mine) scalar(in - t0, out - t0, allow, rest0 + lane);
+      if (mine) scalar(in - v0, out - v0, allow, rest0 + lane, rest_at + lane);
       if (walked) path_out(m);
       in += P.in_stride;
       out += P.out_stride;
@@ -353,28 +366,28 @@ adjust_kernel(const AdjustParams P) {
         Vec<T> x[kAdjVecs];
 #pragma unroll
         for (int i = 0; i < kAdjVecs; ++i) {
-          const int t = begin(i) + head + lane * E;
-          ok[i] = head + (lane + 1) * E <= size(i) ? (allow ? bits_at(allow, v0 + t, words) & kAll : kAll) : 0u;
+          const int v = token(i) + head + lane * E;
+          ok[i] = head + (lane + 1) * E <= size(i) ? (allow ? bits_at(allow, v, words) & kAll : kAll) : 0u;
         }
 #pragma unroll
         for (int i = 0; i < kAdjVecs; ++i)
-          if (ok[i]) x[i].u = ldg_stream(in + begin(i) + head + lane * E);
+          if (ok[i]) x[i].u = ldg_stream(in + token(i) + head + lane * E);
 #pragma unroll
         for (int i = 0; i < kAdjVecs; ++i) {
-          const int n = size(i), t = begin(i) + head + lane * E;
+          const int n = size(i), t = place(i) + head + lane * E;
           if (head + (lane + 1) * E <= n) {
             const uint32_t hit = bits_at(touched, t, kWords + 1) & ok[i];
             if (hit) adjust_vec(x[i], hit, t);
             if (allow) x[i].u = ban<T>(x[i].u, ok[i]);
-            stg_stream(out + t, x[i].u);
+            stg_stream(out + token(i) + head + lane * E, x[i].u);
           }
-          if (lane < min(head, n)) scalar(in, out, allow, begin(i) + lane);
+          if (lane < min(head, n)) scalar(in, out, allow, token(i) + lane, place(i) + lane);
           const int tail = head < n ? head + (n - head) / E * E : max(n, 0);
-          if (lane < n - tail) scalar(in, out, allow, begin(i) + tail + lane);
+          if (lane < n - tail) scalar(in, out, allow, token(i) + tail + lane, place(i) + tail + lane);
         }
       } else {
         for (int i = 0; i < kAdjVecs; ++i)
-          for (int k = lane; k < size(i); k += 32) scalar(in, out, allow, begin(i) + k);
+          for (int k = lane; k < size(i); k += 32) scalar(in, out, allow, token(i) + k, place(i) + k);
       }
       if (walked) path_out(m);
       in += P.in_stride;
@@ -406,9 +419,10 @@ cudaError_t launch_adjust(AdjustParams P, int B, cudaStream_t stream) {
   const cudaError_t e = aligned ? raise_limit<T, true>() : raise_limit<T, false>();
   if (e != cudaSuccess) return e;
   const int slices = (P.V + kSlice<T> - 1) / kSlice<T>;
+  P.by_slices = fast_div(uint32_t(slices));
   // rows per CTA: enough CTAs to fill the device a few times, then as many rows
   // as possible share one count
-  const long long want = 152ll * 3 * 4, per = (long long)slices * B;
+  const long long want = 152ll * 3 * 2, per = (long long)slices * B;
   long long groups = (want + per - 1) / per;
   groups = groups > P.R ? P.R : groups;
   if (groups > 65535) groups = 65535;

@@ -50,19 +50,6 @@ constexpr uint32_t kTmemCols = 512;     // S0 | S1 | O0 | O1
 constexpr uint32_t kProducers = 3;      // warps 8, 10 and 11, which take the loads in turn
 constexpr long long kDrainLimit = 1ll << 31;
 
-// x / d and x % d for 0 <= x < 2^31 by one multiplication: with L = ceil(log2 d)
-// and mul = ceil(2^(31 + L) / d), the error x * (mul - 2^(31 + L) / d) stays below 2^(31 + L) / d.
-struct FastDiv {
-  uint32_t d, mul, shift;
-  __device__ __forceinline__ int div(int x) const { return int((uint64_t(uint32_t(x)) * mul) >> shift); }
-};
-FastDiv fast_div(uint32_t d) {
-  uint32_t L = 0;
-  while ((1ull << L) < d) ++L;
-  const uint64_t one = 1ull << (31 + L);
-  return FastDiv{d, uint32_t((one + d - 1) / d), 31 + L};
-}
-
 struct AttendParams {
   const void* q;
   void* out;

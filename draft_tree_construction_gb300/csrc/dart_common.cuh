@@ -168,6 +168,19 @@ inline bool ws_layout(long long R, int V, int es, int k, WsLayout* L) {
   return true;
 }
 
+// x / d for 0 <= x < 2^31 by one multiplication: with L = ceil(log2 d)
+// and mul = ceil(2^(31 + L) / d), the error x * (mul - 2^(31 + L) / d) stays below 2^(31 + L) / d.
+struct FastDiv {
+  uint32_t d, mul, shift;
+  __device__ __forceinline__ int div(int x) const { return int((uint64_t(uint32_t(x)) * mul) >> shift); }
+};
+inline FastDiv fast_div(uint32_t d) {
+  uint32_t L = 0;
+  while ((1ull << L) < d) ++L;
+  const uint64_t one = 1ull << (31 + L);
+  return FastDiv{d, uint32_t((one + d - 1) / d), 31 + L};
+}
+
 // --------------------------------------------------------------- PTX glue
 __device__ __forceinline__ float ex2_approx(float x) {
   float y;

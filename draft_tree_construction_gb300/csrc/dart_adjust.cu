@@ -4,10 +4,11 @@
 // What a row needs beyond its own elements is small and shared: how often each
 // token occurs in the sequence's history, and the summed bias of each token.
 // So a CTA owns a slice of the vocabulary of one sequence, counts the history
-// and sums the biases of that slice in shared memory once, and then streams
-// that slice of its rows.  A bitmap of the tokens that are counted or biased
-// lets every other element pass unexamined, and a vector of elements that the
-// grammar bans is written without being read.
+// and sums the biases of that slice in shared memory once, and then copies that
+// slice of its rows, whole vectors at a time; a vector that the grammar bans is
+// written without being read.  The few elements that are counted or biased are
+// set afterwards, each by a lane that keeps its change in registers from row to
+// row: examining every vector for them cost more than the copy itself.
 #include <atomic>
 #include <cmath>
 
@@ -19,7 +20,14 @@ namespace {
 constexpr int kAdjThreads = 256;
 constexpr int kAdjWarps = kAdjThreads / 32;
 constexpr int kAdjVecs = 4;                                // 16-byte vectors a lane takes of a row
+constexpr int kSparse = 24;                                // touched tokens of a block that are set one by one
+constexpr int kFix = kSparse * kAdjVecs / 32;              // ... and those of a warp's blocks, per lane
+constexpr int kDepth = 3;                                  // rows under way per warp
+constexpr int kRingBytes = kDepth * kAdjWarps * kAdjVecs * 512;
 constexpr int kMaxBias = 1024;                             // biases per sequence
+constexpr int kCountBits = 21;                             // a token's count: history and path
+constexpr int kMaxHistory = 1 << 20;
+static_assert(kMaxHistory + kMaxN < (1 << kCountBits) && kMaxBias + 1 <= (1 << (32 - kCountBits)), "a place's word");
 constexpr unsigned kFull = 0xFFFFFFFFu;
 
 // A vector per lane makes a block of tokens (256 of 16 bits, 128 of 32).  The
@@ -63,11 +71,45 @@ union Vec {
 };
 
 // Logits pass through once: keep them out of the way of what is used again.
-__device__ __forceinline__ uint4 ldg_stream(const void* p) {
-  uint4 v;
-  asm volatile("ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];"
-               : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "l"(p) : "memory");
-  return v;
+// The load is predicated and leaves v alone otherwise, so that no register is
+// copied (and nothing waits) between the load and the use.
+__device__ __forceinline__ void ldg_stream(uint4& v, const void* p, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
+               "@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
+               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"(uint32_t(on)) : "memory");
+}
+__device__ __forceinline__ void ldg_word(uint32_t& v, const void* p, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}"
+               : "+r"(v) : "l"(p), "r"(uint32_t(on)) : "memory");
+}
+__device__ __forceinline__ void ldg_byte(uint32_t& v, const void* p, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.u8 %0, [%1];\n\t}"
+               : "+r"(v) : "l"(p), "r"(uint32_t(on)) : "memory");
+}
+// One element's bits.
+template <typename T>
+__device__ __forceinline__ void ldg_elem(uint32_t& v, const T* p, bool on) {
+  if (sizeof(T) == 4) {
+    ldg_word(v, p, on);
+  } else {
+    asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.u16 %0, [%1];\n\t}"
+                 : "+r"(v) : "l"(p), "r"(uint32_t(on)) : "memory");
+  }
+}
+// 16 bytes from memory to shared memory, without a register.
+__device__ __forceinline__ void cp_async(void* dst, const void* src, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+               "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(uint32_t(on)) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+template <typename T>
+__device__ __forceinline__ T elem_of(uint32_t v) {
+  T x;
+  memcpy(&x, &v, sizeof(T));
+  return x;
 }
 __device__ __forceinline__ void stg_stream(void* p, uint4 v) {
   asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
@@ -83,41 +125,34 @@ __device__ __forceinline__ uint32_t bits_at(const uint32_t* w, int at, int words
   return __funnelshift_r(lo, hi, at & 31);
 }
 
-// The vector with -inf in the places whose bit of `keep` is clear.
+// The vector with -inf where the mask is 0.
 template <typename T>
-__device__ __forceinline__ uint4 ban(uint4 u, uint32_t keep) {
-  uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    uint32_t m;
-    if (sizeof(T) == 2) {
-      const uint32_t t = keep >> (2 * j);
-      const uint32_t u2 = (t | (t << 15)) & 0x00010001u;      // the two bits, one in each half
-      m = (u2 << 16) - u2;                                    // 0xFFFF in each kept half
-    } else {
-      m = 0u - ((keep >> j) & 1u);
-    }
-    w[j] = (w[j] & m) | (Elem<T>::kNegInf & ~m);
-  }
-  return make_uint4(w[0], w[1], w[2], w[3]);
+__device__ __forceinline__ uint4 ban(uint4 u, uint4 m) {
+  constexpr uint32_t kInf = Elem<T>::kNegInf;
+  return make_uint4((u.x & m.x) | (kInf & ~m.x), (u.y & m.y) | (kInf & ~m.y), (u.z & m.z) | (kInf & ~m.z),
+                    (u.w & m.w) | (kInf & ~m.w));
 }
 
 // ALIGNED: every row begins on a 16-byte boundary, in and out.
 template <typename T, bool ALIGNED>
-__global__ void __launch_bounds__(kAdjThreads, 3)
+__global__ void __launch_bounds__(kAdjThreads, 2)
 adjust_kernel(const AdjustParams P) {
   constexpr int E = 16 / int(sizeof(T));
   constexpr int kBlk = kBlock<T>, kCta = kSlice<T>, kWords = kCta / 32;
   constexpr uint32_t kAll = (1u << E) - 1u;
+  // the ring: kDepth rows of each warp's vectors, on their way from memory or worked on
   extern __shared__ __align__(16) unsigned char smem[];
-  uint32_t* counts = reinterpret_cast<uint32_t*>(smem);                    // [kCta], with penalties
-  float* bias = reinterpret_cast<float*>(smem) + (P.count ? kCta : 0);     // [kCta], with biases
-  __shared__ __align__(16) uint32_t touched[kWords + 1];         // token is counted or biased
-  __shared__ uint32_t bias_bits[kWords + 1];       // token is biased
-  __shared__ int32_t list_id[kMaxBias];            // the slice's biases, in their order; then the tree's tokens
-  __shared__ float list_val[kMaxBias];
+  // a place's word: 1 + its index in the bias list (0: not biased), and how often its token is counted
+  uint32_t* counts = reinterpret_cast<uint32_t*>(smem + (ALIGNED ? kRingBytes : 0));    // [kCta], with penalties or biases
+  __shared__ uint32_t touched[kWords];             // place is counted or biased
+  __shared__ uint32_t on_path[kWords];             // place's token is on the present row's path
+  __shared__ int32_t list_id[kMaxBias];            // the slice's biases, in their order
+  __shared__ float list_val[kMaxBias];             // ... the first entry of an id holding the id's sum
+  __shared__ uint16_t list_own[kAdjWarps][32 * kFix];      // each warp's touched places in blocks that have few
+  __shared__ uint32_t row_ok[ALIGNED ? kDepth : 1][kAdjThreads];      // grammar bits of the rows in the ring
+  __shared__ uint4 spread[1 << E];                 // the mask of a vector whose elements are the bits of the index
+  __shared__ int16_t toks[kMaxN];                  // the places of the tree's tokens, -1 outside the slice
   __shared__ int32_t warp_n[kMaxBias / kAdjThreads][kAdjWarps];
-  static_assert(kMaxN <= kMaxBias, "the tree's tokens take the place of the bias list");
 
   const int b = blockIdx.z, slice = blockIdx.x, slices = int(P.by_slices.d);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -146,13 +181,21 @@ adjust_kernel(const AdjustParams P) {
   const float rep = a.repetition ? a.repetition[b] : 1.f, inv_rep = 1.f / rep;
   const float pres = a.presence ? a.presence[b] : 0.f;
   const float freq = a.frequency ? a.frequency[b] : 0.f;
+  const bool touching = P.count || a.bias_count > 0, paths = P.count && a.N > 0;
 
-  for (int i = tid; i <= kWords; i += kAdjThreads) touched[i] = bias_bits[i] = 0u;
-  {
-    uint4* z = reinterpret_cast<uint4*>(smem);
-    const int n = ((P.count ? 1 : 0) + (a.bias_count > 0 ? 1 : 0)) * (kCta / 4);
-    for (int i = tid; i < n; i += kAdjThreads) z[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < kWords; i += kAdjThreads) touched[i] = on_path[i] = 0u;
+  if (touching)
+    for (int i = tid; i < kCta / 4; i += kAdjThreads) reinterpret_cast<uint4*>(counts)[i] = make_uint4(0, 0, 0, 0);
+  for (int i = tid; i < (1 << E); i += kAdjThreads) {
+    uint32_t w[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      w[j] = E == 4 ? 0u - ((uint32_t(i) >> j) & 1u)
+                    : ((i >> (2 * j)) & 1 ? 0xFFFFu : 0u) | ((i >> (2 * j)) & 2 ? 0xFFFF0000u : 0u);
+    spread[i] = make_uint4(w[0], w[1], w[2], w[3]);
   }
+  if (paths)
+    for (int i = tid; i < a.N; i += kAdjThreads) toks[i] = int16_t(local(a.tokens[(long long)b * a.N + i]));
   __syncthreads();
   for (int i0 = tid; i0 < len; i0 += kAhead * kAdjThreads) {
     if (i0 != tid) {
@@ -200,17 +243,10 @@ adjust_kernel(const AdjustParams P) {
       float s = list_val[i];
       for (int j = i + 1; j < n; ++j)
         if (list_id[j] == t) s += list_val[j];
-      bias[t] = s;
-      atomicOr(&bias_bits[t >> 5], 1u << (t & 31));
+      list_val[i] = s;                           // no other entry reads it: only the first of an id reads values
+      atomicAdd(&counts[t], uint32_t(i + 1) << kCountBits);
       atomicOr(&touched[t >> 5], 1u << (t & 31));
     }
-  }
-  const int r_begin = blockIdx.y * P.row_group, r_end = min(P.R, r_begin + P.row_group);
-  const bool paths = P.count && a.N > 0;
-  int32_t* toks = list_id;                       // from here on: the places of the tree's tokens in the slice
-  if (paths) {
-    __syncthreads();
-    for (int i = tid; i < a.N; i += kAdjThreads) toks[i] = local(a.tokens[(long long)b * a.N + i]);
   }
   __syncthreads();
 
@@ -220,176 +256,320 @@ adjust_kernel(const AdjustParams P) {
   auto token = [&](int i) { return ((kAdjWarps * i + warp) * slices + slice) * kBlk; };
   auto size = [&](int i) { return min(P.V - token(i), kBlk); };          // <= 0 behind the vocabulary
   if (token(0) >= P.V) return;
-  const int words = (P.V + 31) >> 5;
   const int MW = (a.N + 31) >> 5;
-  const bool biased = a.bias_count > 0;
+  const int r_begin = blockIdx.y * P.row_group, r_end = min(P.R, r_begin + P.row_group);
+
+  // The touched places of blocks that have few of them go to a list, a lane
+  // taking every 32nd; the other blocks (bits of `dense`) look for theirs vector by vector.
+  int own = 0;
+  uint32_t dense = 0u;
+  {
+    constexpr int kPer = kBlk / 32;              // words per block
+    uint32_t m = lane < kAdjVecs * kPer ? touched[place(lane / kPer) / 32 + lane % kPer] : 0u;
+    int n = __popc(m), in_block = n;
+#pragma unroll
+    for (int o = 1; o < kPer; o <<= 1) in_block += __shfl_xor_sync(kFull, in_block, o);
+    const bool many = in_block > kSparse;
+#pragma unroll
+    for (int i = 0; i < kAdjVecs; ++i) dense |= uint32_t(__shfl_sync(kFull, int(many), i * kPer)) << i;
+    if (many) m = 0u, n = 0;
+    int incl = n;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const int x = __shfl_up_sync(kFull, incl, o);
+      if (lane >= o) incl += x;
+    }
+    own = __shfl_sync(kFull, incl, 31);
+    for (int at = incl - n; m; m &= m - 1, ++at)
+      list_own[warp][at] = uint16_t(place(lane / kPer) + 32 * (lane % kPer) + __ffs(m) - 1);
+    __syncwarp();
+  }
+  // a touched element: scaled if counted, then what it gains, rounded once in fp32
+  struct Change { int v; bool counted; float gain; };
+  auto change = [&](int t) {
+    const uint32_t word = counts[t], c = word & ((1u << kCountBits) - 1u), i = word >> kCountBits;
+    const float bias = i ? list_val[i - 1] : 0.f;
+    Change h;
+    h.v = ((t / kBlk) * slices + slice) * kBlk + t % kBlk;
+    h.counted = c != 0u;
+    h.gain = c ? bias - fmaf(freq, float(c), pres) : bias;
+    return h;
+  };
+  auto apply = [&](T raw, const Change& h) {
+    const float x = Elem<T>::get(raw);
+    return Elem<T>::put(fmaf(x, h.counted ? (x > 0.f ? inv_rep : rep) : 1.f, h.gain));
+  };
+  auto keeps = [](const uint32_t* allow, int v) { return !allow || ((allow[v >> 5] >> (v & 31)) & 1u); };
+  auto marked = [&](int t) { return (on_path[t >> 5] >> (t & 31)) & 1u; };
+  // this lane's touched elements stay in registers
+  Change fix[kFix];
+  int fix_at[kFix];
+#pragma unroll
+  for (int k = 0; k < kFix; ++k) {
+    fix_at[k] = lane + 32 * k < own ? list_own[warp][lane + 32 * k] : -1;
+    fix[k].v = 0;
+    if (fix_at[k] >= 0) fix[k] = change(fix_at[k]);
+  }
 
   // the nodes whose tokens this warp owns, 32 nodes a lane
   uint32_t own_nodes = 0u;
-  auto owns = [&](int node) { return toks[node] >= 0 && toks[node] / kBlk % kAdjWarps == warp; };
   if (paths)
-    for (int k = 0; k < 32 && 32 * lane + k < a.N; ++k) own_nodes |= uint32_t(owns(32 * lane + k)) << k;
-  auto node_bits = [&](int r) {       // this lane's word of the row's path
+    for (int k = 0; k < 32 && 32 * lane + k < a.N; ++k) {
+      const int t = toks[32 * lane + k];
+      own_nodes |= uint32_t(t >= 0 && t / kBlk % kAdjWarps == warp) << k;
+    }
+  auto node_bits = [&](int r) {       // this lane's word of row r's path, the warp's own nodes
     const int node = r - (P.R - a.N);
-    return paths && r < r_end && node >= 0 && lane < MW ? a.mask[((long long)b * a.N + node) * MW + lane] : 0u;
+    return paths && r < r_end && node >= 0 && lane < MW ? a.mask[((long long)b * a.N + node) * MW + lane] & own_nodes
+                                                         : 0u;
   };
-  // the tokens of the row's path join the counts, and leave them again
-  auto path_in = [&](uint32_t m) {
-    for (; m; m &= m - 1) {
-      const int t = toks[32 * lane + __ffs(m) - 1];
+  // The tokens of a row's path join the counts and are marked: nothing sets a
+  // marked element until the row is copied; then each is set once, from `in`,
+  // which still holds it when the row is changed in place.
+  auto each = [&](uint32_t path, auto&& f) {
+    for (uint32_t m = path; m; m &= m - 1) f(int(toks[32 * lane + __ffs(m) - 1]));
+    __syncwarp();
+  };
+  auto path_in = [&](uint32_t path) {
+    each(path, [&](int t) {
       atomicAdd(&counts[t], 1u);
-      atomicOr(&touched[t >> 5], 1u << (t & 31));
+      atomicOr(&on_path[t >> 5], 1u << (t & 31));
+    });
+  };
+  // a lane's first token of the path, read with the row's vectors (most lanes have none, few have two)
+  struct First { uint32_t raw, word; };
+  auto path_read = [&](First& f, uint32_t path, const T* in, const uint32_t* allow) {
+    int v = 0;
+    if (path) {
+      const int t = toks[32 * lane + __ffs(path) - 1];
+      v = ((t / kBlk) * slices + slice) * kBlk + t % kBlk;
     }
+    ldg_elem(f.raw, in + v, path != 0u);
+    ldg_word(f.word, allow + (v >> 5), path != 0u && allow != nullptr);
+  };
+  auto path_out = [&](uint32_t path, const First& first, const T* in, T* out, const uint32_t* allow) {
     __syncwarp();
+    bool begun = false;
+    each(path, [&](int t) {               // the lane that clears the mark sets the element
+      const uint32_t bit = 1u << (t & 31);
+      if (atomicAnd(&on_path[t >> 5], ~bit) & bit) {
+        const Change h = change(t);
+        if (begun ? keeps(allow, h.v) : (first.word >> (h.v & 31)) & 1u) out[h.v] = apply(begun ? in[h.v] : elem_of<T>(first.raw), h);
+      }
+      begun = true;
+    });
+    each(path, [&](int t) { atomicSub(&counts[t], 1u); });
   };
-  auto path_out = [&](uint32_t m) {
-    __syncwarp();
-    for (; m; m &= m - 1) {
-      const int t = toks[32 * lane + __ffs(m) - 1];
-      if (atomicSub(&counts[t], 1u) == 1u && !((bias_bits[t >> 5] >> (t & 31)) & 1u))
-        atomicAnd(&touched[t >> 5], ~(1u << (t & 31)));
-    }
-    __syncwarp();
-  };
-
-  // element x with count c and bias y (0: not biased, as far as the value goes)
-  auto apply = [&](float x, uint32_t c, float y) {
-    const float z = fmaf(-freq, float(c), x > 0.f ? x * inv_rep : x * rep) - pres;
-    return (c ? z : x) + y;
-  };
-  // one element: token v, at place t of the slice
-  auto scalar = [&](const T* in, T* out, const uint32_t* allow, int v, int t) {
-    const uint32_t word = allow ? allow[v >> 5] : kFull;
-    T x;
-    if ((word >> (v & 31)) & 1u) {
-      x = in[v];
-      if ((touched[t >> 5] >> (t & 31)) & 1u)
-        x = Elem<T>::put(apply(Elem<T>::get(x), P.count ? counts[t] : 0u, biased ? bias[t] : 0.f));
-    } else {
-      x = Elem<T>::put(-INFINITY);
-    }
-    out[v] = x;
-  };
-  // the elements `hit` of the vector at place t (a multiple of 4 if ALIGNED)
-  auto adjust_vec = [&](Vec<T>& x, uint32_t hit, int t) {
-    uint32_t c[E];
-    float y[E];
+  // (the words are looked into when they are used, so that nothing waits here)
+  auto fix_read = [&](const T* in, const uint32_t* allow, uint32_t* raw, uint32_t* word) {
 #pragma unroll
-    for (int e = 0; e < E; ++e) c[e] = 0u, y[e] = 0.f;
+    for (int k = 0; k < kFix; ++k)
+      if (32 * k < own) {
+        ldg_elem(raw[k], in + fix[k].v, fix_at[k] >= 0);
+        ldg_word(word[k], allow + (fix[k].v >> 5), fix_at[k] >= 0 && allow != nullptr);
+      }
+  };
+  auto fix_set = [&](T* out, bool walked, const uint32_t* raw, const uint32_t* word) {
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < kFix; ++k)
+      if (32 * k < own && fix_at[k] >= 0 && ((word[k] >> (fix[k].v & 31)) & 1u) && !(walked && marked(fix_at[k])))
+        out[fix[k].v] = apply(elem_of<T>(raw[k]), fix[k]);
+  };
+  // the touched elements of a dense block's vector, at place t (a multiple of 4 if ALIGNED)
+  auto dense_set = [&](Vec<T>& x, uint32_t hit, int t) {
+    uint32_t c[E];
     if constexpr (ALIGNED) {
 #pragma unroll
-      for (int e = 0; e < E; e += 4) {
-        if (P.count) *reinterpret_cast<uint4*>(c + e) = *reinterpret_cast<const uint4*>(counts + t + e);
-        if (biased) *reinterpret_cast<float4*>(y + e) = *reinterpret_cast<const float4*>(bias + t + e);
-      }
+      for (int e = 0; e < E; e += 4) *reinterpret_cast<uint4*>(c + e) = *reinterpret_cast<const uint4*>(counts + t + e);
     } else {
 #pragma unroll
-      for (int e = 0; e < E; ++e) {
-        if (P.count) c[e] = counts[t + e];
-        if (biased) y[e] = bias[t + e];
-      }
+      for (int e = 0; e < E; ++e) c[e] = counts[t + e];
     }
 #pragma unroll
-    for (int e = 0; e < E; ++e)
-      if ((hit >> e) & 1u) x.e[e] = Elem<T>::put(apply(Elem<T>::get(x.e[e]), c[e], y[e]));
+    for (int e = 0; e < E; ++e) {
+      const uint32_t n = c[e] & ((1u << kCountBits) - 1u), i = c[e] >> kCountBits;
+      float gain = i ? list_val[i - 1] : 0.f;
+      if (n) gain -= fmaf(freq, float(n), pres);
+      const float y = Elem<T>::get(x.e[e]);
+      const T z = Elem<T>::put(fmaf(y, n ? (y > 0.f ? inv_rep : rep) : 1.f, gain));
+      if ((hit >> e) & 1u) x.e[e] = z;
+    }
   };
 
   const T* in = static_cast<const T*>(P.in) + ((long long)b * P.R + r_begin) * P.in_stride;
   T* out = static_cast<T*>(P.out) + ((long long)b * P.R + r_begin) * P.out_stride;
   const uint32_t* allow =
       a.allowed ? a.allowed + (long long)b * a.allowed_seq_stride + (long long)r_begin * a.allowed_row_stride : nullptr;
-  uint32_t path = node_bits(r_begin);
 
   if constexpr (ALIGNED) {
     // The lane's vectors lie `step` tokens apart, from v0 on; the first `nv` of
-    // them are whole.  The next row's grammar bits come while this one is worked on.
-    const int step = kAdjWarps * slices * kBlk, v0 = token(0) + lane * E, t0 = place(0) + lane * E;
+    // them are whole.  Rows pass through the ring: copied there kDepth - 1 rows
+    // ahead (but for vectors that the grammar bans), changed there, written
+    // from there with the banned elements replaced.
+    const int step = kAdjWarps * slices * kBlk, v0 = token(0) + lane * E;
+    constexpr int kPlaceStep = kAdjWarps * kBlk;
     int nv = 0;
 #pragma unroll
     for (int i = 0; i < kAdjVecs; ++i) nv += v0 + i * step + E <= P.V ? 1 : 0;
     // tokens behind the last whole vector of the vocabulary, the warp that owns them taking them singly
     const int rest = P.V % E, rest0 = P.V - rest, rest_at = local(rest0);
-    const bool mine = rest > 0 && lane < rest && rest_at >= 0 && rest_at / kBlk % kAdjWarps == warp;
-    const uint8_t* bytes = reinterpret_cast<const uint8_t*>(touched) + (t0 >> 3);
-    const int shift = t0 & 7;                     // a vector of four shares its byte with its neighbour
-    auto grammar = [&](const uint32_t* al) {      // eight bits per vector
-      uint32_t ok = 0u;
-      const uint8_t* src = reinterpret_cast<const uint8_t*>(al) + (v0 >> 3);
-#pragma unroll
-      for (int i = 0; i < kAdjVecs; ++i)
-        if (i < nv) ok |= ((uint32_t(src[i * (step / 8)]) >> shift) & kAll) << (8 * i);
-      return ok;
+    const bool tail = rest > 0 && lane < rest && rest_at >= 0 && rest_at / kBlk % kAdjWarps == warp;
+    const int shift = v0 & 7;                     // a vector of four shares its byte with its neighbour
+    unsigned char* ring = smem + warp * (kAdjVecs * 512);            // + depth * kAdjWarps * kAdjVecs * 512
+    constexpr int kRowBytes = kAdjWarps * kAdjVecs * 512;
+    // where the element at place t lies in the warp's part of a row
+    auto element = [&](int slot, int t) {
+      return reinterpret_cast<T*>(ring + slot * kRowBytes + t / kPlaceStep * 512) + t % kBlk;
     };
-    uint32_t ok = allow ? grammar(allow) : kFull;
-    in += v0;
-    out += v0;
-    for (int r = r_begin; r < r_end; ++r) {
-      Vec<T> x[kAdjVecs];
+    // grammar bits: asked for a row before the row's copy begins (eight bits per vector)
+    uint32_t bits[kAdjVecs];
 #pragma unroll
-      for (int i = 0; i < kAdjVecs; ++i)
-        if (i < nv && ((ok >> (8 * i)) & kAll)) x[i].u = ldg_stream(in + i * step);
-      const uint32_t next_path = node_bits(r + 1);
-      uint32_t next_ok = kFull;
-      if (allow && r + 1 < r_end) next_ok = grammar(allow + a.allowed_row_stride);
-      const uint32_t m = path & own_nodes;
-      const bool walked = paths && __any_sync(kFull, m != 0u);
-      if (walked) path_in(m);
+    for (int i = 0; i < kAdjVecs; ++i) bits[i] = kFull;
+    auto ask = [&](int r) {
+      const uint8_t* src =
+          reinterpret_cast<const uint8_t*>(allow + (long long)(r - r_begin) * a.allowed_row_stride) + (v0 >> 3);
+#pragma unroll
+      for (int i = 0; i < kAdjVecs; ++i) ldg_byte(bits[i], src + i * (step / 8), i < nv && r < r_end);
+    };
+    auto copy = [&](int r, int slot) {
+      uint32_t ok = 0u;
+      const T* src = in + (long long)(r - r_begin) * P.in_stride + v0;
 #pragma unroll
       for (int i = 0; i < kAdjVecs; ++i) {
-        if (i < nv) {
-          const uint32_t keep = (ok >> (8 * i)) & kAll;
-          const uint32_t hit = (uint32_t(bytes[i * (kAdjWarps * kBlk / 8)]) >> shift) & keep;
-          if (hit) adjust_vec(x[i], hit, t0 + i * (kAdjWarps * kBlk));
-          if (allow) x[i].u = ban<T>(x[i].u, keep);
-          stg_stream(out + i * step, x[i].u);
-        }
+        const uint32_t k = (bits[i] >> shift) & kAll;
+        ok |= k << (8 * i);
+        cp_async(ring + slot * kRowBytes + i * 512 + lane * 16, src + i * step, r < r_end && i < nv && k != 0u);
       }
-      if (mine) scalar(in - v0, out - v0, allow, rest0 + lane, rest_at + lane);
-      if (walked) path_out(m);
-      in += P.in_stride;
-      out += P.out_stride;
-      if (allow) allow += a.allowed_row_stride;
-      ok = next_ok;
-      path = next_path;
-    }
-  } else {
+      cp_commit();
+      row_ok[slot][tid] = ok;
+      if (allow) ask(r + 1);
+    };
+    if (allow) ask(r_begin);
+    for (int k = 0; k < kDepth - 1; ++k) copy(r_begin + k, k);
+    uint32_t path = node_bits(r_begin);
+    int slot = 0;
     for (int r = r_begin; r < r_end; ++r) {
-      const uint32_t m = path & own_nodes;
-      path = node_bits(r + 1);
-      const bool walked = paths && __any_sync(kFull, m != 0u);
-      if (walked) path_in(m);
+      copy(r + kDepth - 1, slot == 0 ? kDepth - 1 : slot - 1);
+      const uint32_t next_path = node_bits(r + 1);
+      cp_wait<kDepth - 1>();
+      __syncwarp();
+      const bool walked = paths && __any_sync(kFull, path != 0u);
+      if (walked) path_in(path);
+      if (own > 0) {
+#pragma unroll
+        for (int k = 0; k < kFix; ++k)
+          if (32 * k < own && fix_at[k] >= 0 && !(walked && marked(fix_at[k]))) {
+            T* e = element(slot, fix_at[k]);
+            *e = apply(*e, fix[k]);
+          }
+      }
+      if (walked) {
+        __syncwarp();
+        each(path, [&](int t) {               // the lane that clears the mark sets the element
+          const uint32_t bit = 1u << (t & 31);
+          if ((on_path[t >> 5] & bit) && !((dense >> (t / kPlaceStep)) & 1u) &&
+              (atomicAnd(&on_path[t >> 5], ~bit) & bit)) {
+            T* e = element(slot, t);
+            *e = apply(*e, change(t));
+          }
+        });
+      }
+      __syncwarp();
+      const uint32_t ok = row_ok[slot][tid];
+      T* dst = out + v0;
+#pragma unroll
+      for (int i = 0; i < kAdjVecs; ++i) {
+        Vec<T> x;
+        x.u = *reinterpret_cast<const uint4*>(ring + slot * kRowBytes + i * 512 + lane * 16);
+        const uint32_t k = (ok >> (8 * i)) & kAll;
+        if ((dense >> i) & 1u) {
+          const int t = place(i) + lane * E;
+          uint32_t hit = ((touched[t >> 5] >> (t & 31)) | (walked ? on_path[t >> 5] >> (t & 31) : 0u)) & k;
+          if (i < nv && hit) dense_set(x, hit, t);
+        }
+        if (allow) x.u = ban<T>(x.u, spread[k]);
+        if (i < nv) stg_stream(dst + i * step, x.u);
+      }
+      if (tail) {
+        const int v = rest0 + lane, t = rest_at + lane;
+        T y = Elem<T>::put(-INFINITY);
+        if (keeps(allow ? allow + (long long)(r - r_begin) * a.allowed_row_stride : nullptr, v)) {
+          y = in[(long long)(r - r_begin) * P.in_stride + v];
+          if (touching && counts[t]) y = apply(y, change(t));
+        }
+        out[v] = y;
+      }
+      if (walked) {
+        __syncwarp();
+        each(path, [&](int t) {
+          atomicAnd(&on_path[t >> 5], ~(1u << (t & 31)));
+          atomicSub(&counts[t], 1u);
+        });
+      }
+      out += P.out_stride;
+      path = next_path;
+      slot = slot + 1 < kDepth ? slot + 1 : 0;
+    }
+    cp_wait<0>();
+  } else {
+    const int words = (P.V + 31) >> 5;
+    for (int r = r_begin; r < r_end; ++r) {
       // elements before the first 16-byte boundary of every block of this row (a block is a multiple of 16 bytes)
       const int head = int((16u - unsigned(reinterpret_cast<uintptr_t>(in) & 15u)) & 15u) / int(sizeof(T));
       const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
+      uint32_t raw[kFix], word[kFix];
+#pragma unroll
+      for (int k = 0; k < kFix; ++k) raw[k] = 0u, word[k] = kFull;
+      if (own > 0) fix_read(in, allow, raw, word);
+      const uint32_t path = node_bits(r);
+      const bool walked = paths && __any_sync(kFull, path != 0u);
+      First first{0u, kFull};
+      if (paths) path_read(first, path, in, allow);
+      if (walked) path_in(path);
+      // one element: token token(i) + k
+      auto scalar = [&](int i, int k) {
+        const int v = token(i) + k, t = place(i) + k;
+        T y = Elem<T>::put(-INFINITY);
+        if (keeps(allow, v)) {
+          y = in[v];
+          if (((dense >> i) & 1u) && ((touched[t >> 5] >> (t & 31)) & 1u) && !(walked && marked(t)))
+            y = apply(y, change(t));
+        }
+        out[v] = y;
+      };
       if (same) {
         uint32_t ok[kAdjVecs];
         Vec<T> x[kAdjVecs];
 #pragma unroll
-        for (int i = 0; i < kAdjVecs; ++i) {
-          const int v = token(i) + head + lane * E;
-          ok[i] = head + (lane + 1) * E <= size(i) ? (allow ? bits_at(allow, v, words) & kAll : kAll) : 0u;
-        }
+        for (int i = 0; i < kAdjVecs; ++i)
+          ok[i] = head + (lane + 1) * E <= size(i)
+                      ? (allow ? bits_at(allow, token(i) + head + lane * E, words) & kAll : kAll)
+                      : 0u;
 #pragma unroll
         for (int i = 0; i < kAdjVecs; ++i)
-          if (ok[i]) x[i].u = ldg_stream(in + token(i) + head + lane * E);
+          ldg_stream(x[i].u, in + token(i) + head + lane * E, ok[i] != 0u);
 #pragma unroll
         for (int i = 0; i < kAdjVecs; ++i) {
           const int n = size(i), t = place(i) + head + lane * E;
           if (head + (lane + 1) * E <= n) {
-            const uint32_t hit = bits_at(touched, t, kWords + 1) & ok[i];
-            if (hit) adjust_vec(x[i], hit, t);
-            if (allow) x[i].u = ban<T>(x[i].u, ok[i]);
-            stg_stream(out + token(i) + head + lane * E, x[i].u);
+            if ((dense >> i) & 1u) {
+              uint32_t hit = bits_at(touched, t, kWords) & ok[i];
+              if (walked) hit &= ~bits_at(on_path, t, kWords);
+              if (hit) dense_set(x[i], hit, t);
+            }
+            stg_stream(out + token(i) + head + lane * E, allow ? ban<T>(x[i].u, spread[ok[i]]) : x[i].u);
           }
-          if (lane < min(head, n)) scalar(in, out, allow, token(i) + lane, place(i) + lane);
+          if (lane < min(head, n)) scalar(i, lane);
           const int tail = head < n ? head + (n - head) / E * E : max(n, 0);
-          if (lane < n - tail) scalar(in, out, allow, token(i) + tail + lane, place(i) + tail + lane);
+          if (lane < n - tail) scalar(i, tail + lane);
         }
       } else {
         for (int i = 0; i < kAdjVecs; ++i)
-          for (int k = lane; k < size(i); k += 32) scalar(in, out, allow, token(i) + k, place(i) + k);
+          for (int k = lane; k < size(i); k += 32) scalar(i, k);
       }
-      if (walked) path_out(m);
+      if (own > 0) fix_set(out, walked, raw, word);
+      if (walked) path_out(path, first, in, out, allow);
       in += P.in_stride;
       out += P.out_stride;
       if (allow) allow += a.allowed_row_stride;
@@ -405,7 +585,8 @@ cudaError_t raise_limit() {
   if (e != cudaSuccess) return e;
   const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
   if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(adjust_kernel<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize, 8 * kSlice<T>);
+    e = cudaFuncSetAttribute(adjust_kernel<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             4 * kSlice<T> + (ALIGNED ? kRingBytes : 0));
     if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
   }
   return e;
@@ -428,7 +609,7 @@ cudaError_t launch_adjust(AdjustParams P, int B, cudaStream_t stream) {
   if (groups > 65535) groups = 65535;
   P.row_group = int((P.R + groups - 1) / groups);
   const dim3 grid(slices, (P.R + P.row_group - 1) / P.row_group, B);
-  const size_t smem = size_t(4 * kSlice<T>) * ((P.count ? 1 : 0) + (P.a.bias_count > 0 ? 1 : 0));
+  const size_t smem = (aligned ? kRingBytes : 0) + (P.count || P.a.bias_count > 0 ? 4 * kSlice<T> : 0);
   if (aligned) adjust_kernel<T, true><<<grid, kAdjThreads, smem, stream>>>(P);
   else adjust_kernel<T, false><<<grid, kAdjThreads, smem, stream>>>(P);
   return cudaGetLastError();
@@ -445,7 +626,7 @@ extern "C" int dart_logits_adjust(const void* logits, int B, int R, int V, int64
   if (row_stride < V || row_stride > kMaxRowStride || out_stride < V || out_stride > kMaxRowStride)
     return DART_ERR_INVALID_ARG;
   const dart_adjust_t& a = *what;
-  if (a.history_width < 0 || a.bias_count < 0 || a.bias_count > kMaxBias || a.N < 0 || a.N > kMaxN)
+  if (a.history_width < 0 || a.history_width > kMaxHistory || a.bias_count < 0 || a.bias_count > kMaxBias || a.N < 0 || a.N > kMaxN)
     return DART_ERR_INVALID_ARG;
   if (a.history && a.history_stride < a.history_width && B > 1) return DART_ERR_INVALID_ARG;
   if (a.N > 0 && R != a.N && R != a.N + 1) return DART_ERR_INVALID_ARG;

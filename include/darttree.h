@@ -375,7 +375,7 @@ typedef struct {
   const int32_t* history;        /* device [B][history_width], rows history_stride apart: tokens so far; ids outside
                                     [0, V) (padding) are not counted */
   int64_t history_stride;
-  int32_t history_width;
+  int32_t history_width;         /* 0..2^20 */
   int32_t bias_count;            /* entries per sequence, 0..1024 */
   const int32_t* history_len;    /* device [B]: entries in use (limited to 0..history_width), or NULL for all */
   const float* repetition;       /* device [B], > 0: a counted token's z becomes z / r if z > 0, else z * r */

@@ -163,7 +163,54 @@ adjust_kernel(const AdjustParams P) {
     return uint32_t(token) < uint32_t(P.V) && blk - k * slices == slice ? k * kBlk + token % kBlk : -1;
   };
 
+  // From here to the end a warp copies and changes its own blocks only: block i
+  // lies at place (8 i + warp) * kBlk of the slice and holds the tokens from token(i) on.
+  auto place = [&](int i) { return (kAdjWarps * i + warp) * kBlk; };
+  auto token = [&](int i) { return ((kAdjWarps * i + warp) * slices + slice) * kBlk; };
+  auto size = [&](int i) { return min(P.V - token(i), kBlk); };          // <= 0 behind the vocabulary
+  const int r_begin = blockIdx.y * P.row_group, r_end = min(P.R, r_begin + P.row_group);
+  const T* in = static_cast<const T*>(P.in) + ((long long)b * P.R + r_begin) * P.in_stride;
+  T* out = static_cast<T*>(P.out) + ((long long)b * P.R + r_begin) * P.out_stride;
+  const uint32_t* allow =
+      a.allowed ? a.allowed + (long long)b * a.allowed_seq_stride + (long long)r_begin * a.allowed_row_stride : nullptr;
+
+  // Aligned rows: a lane's vectors lie `step` tokens apart, from v0 on; the
+  // first `nv` of them are whole.  Rows pass through the ring: copied there
+  // kDepth - 1 rows ahead (but for vectors that the grammar bans), changed
+  // there, written from there with the banned elements replaced.
+  const int step = kAdjWarps * slices * kBlk, v0 = token(0) + lane * E;
+  constexpr int kPlaceStep = kAdjWarps * kBlk, kRowBytes = kAdjWarps * kAdjVecs * 512;
+  const int shift = v0 & 7;                       // a vector of four shares its byte with its neighbour
+  unsigned char* ring = smem + warp * (kAdjVecs * 512);            // + slot * kRowBytes
+  int nv = 0;
+#pragma unroll
+  for (int i = 0; i < kAdjVecs; ++i) nv += v0 + i * step + E <= P.V ? 1 : 0;
+  // grammar bits: asked for a row before the row's copy begins (eight bits per vector)
+  uint32_t bits[kAdjVecs];
+#pragma unroll
+  for (int i = 0; i < kAdjVecs; ++i) bits[i] = kFull;
+  auto ask = [&](int r) {
+    const uint8_t* src =
+        reinterpret_cast<const uint8_t*>(allow + (long long)(r - r_begin) * a.allowed_row_stride) + (v0 >> 3);
+#pragma unroll
+    for (int i = 0; i < kAdjVecs; ++i) ldg_byte(bits[i], src + i * (step / 8), i < nv && r < r_end);
+  };
+  auto copy = [&](int r, int slot) {
+    uint32_t ok = 0u;
+    const T* src = in + (long long)(r - r_begin) * P.in_stride + v0;
+#pragma unroll
+    for (int i = 0; i < kAdjVecs; ++i) {
+      const uint32_t k = (bits[i] >> shift) & kAll;
+      ok |= k << (8 * i);
+      cp_async(ring + slot * kRowBytes + i * 512 + lane * 16, src + i * step, r < r_end && i < nv && k != 0u);
+    }
+    cp_commit();
+    row_ok[slot][tid] = ok;
+    if (allow) ask(r + 1);
+  };
+
   // Everything that the slice needs from memory is asked for before anything waits.
+  if (ALIGNED && allow) ask(r_begin);
   constexpr int kAhead = 8, kBiasAhead = kMaxBias / kAdjThreads;
   const int32_t* hist = P.count && a.history ? a.history + (long long)b * a.history_stride : nullptr;
   const int width = hist ? a.history_width : 0;
@@ -182,6 +229,11 @@ adjust_kernel(const AdjustParams P) {
   const float pres = a.presence ? a.presence[b] : 0.f;
   const float freq = a.frequency ? a.frequency[b] : 0.f;
   const bool touching = P.count || a.bias_count > 0, paths = P.count && a.N > 0;
+
+  if constexpr (ALIGNED) {
+#pragma unroll
+    for (int k = 0; k < kDepth - 1; ++k) copy(r_begin + k, k);
+  }
 
   for (int i = tid; i < kWords; i += kAdjThreads) touched[i] = on_path[i] = 0u;
   if (touching)
@@ -250,14 +302,8 @@ adjust_kernel(const AdjustParams P) {
   }
   __syncthreads();
 
-  // From here on a warp touches its own blocks only: block i lies at place
-  // (8 i + warp) * kBlk of the slice and holds the tokens from token(i) on.
-  auto place = [&](int i) { return (kAdjWarps * i + warp) * kBlk; };
-  auto token = [&](int i) { return ((kAdjWarps * i + warp) * slices + slice) * kBlk; };
-  auto size = [&](int i) { return min(P.V - token(i), kBlk); };          // <= 0 behind the vocabulary
   if (token(0) >= P.V) return;
   const int MW = (a.N + 31) >> 5;
-  const int r_begin = blockIdx.y * P.row_group, r_end = min(P.R, r_begin + P.row_group);
 
   // The touched places of blocks that have few of them go to a list, a lane
   // taking every 32nd; the other blocks (bits of `dense`) look for theirs vector by vector.
@@ -397,56 +443,14 @@ adjust_kernel(const AdjustParams P) {
     }
   };
 
-  const T* in = static_cast<const T*>(P.in) + ((long long)b * P.R + r_begin) * P.in_stride;
-  T* out = static_cast<T*>(P.out) + ((long long)b * P.R + r_begin) * P.out_stride;
-  const uint32_t* allow =
-      a.allowed ? a.allowed + (long long)b * a.allowed_seq_stride + (long long)r_begin * a.allowed_row_stride : nullptr;
-
   if constexpr (ALIGNED) {
-    // The lane's vectors lie `step` tokens apart, from v0 on; the first `nv` of
-    // them are whole.  Rows pass through the ring: copied there kDepth - 1 rows
-    // ahead (but for vectors that the grammar bans), changed there, written
-    // from there with the banned elements replaced.
-    const int step = kAdjWarps * slices * kBlk, v0 = token(0) + lane * E;
-    constexpr int kPlaceStep = kAdjWarps * kBlk;
-    int nv = 0;
-#pragma unroll
-    for (int i = 0; i < kAdjVecs; ++i) nv += v0 + i * step + E <= P.V ? 1 : 0;
     // tokens behind the last whole vector of the vocabulary, the warp that owns them taking them singly
     const int rest = P.V % E, rest0 = P.V - rest, rest_at = local(rest0);
     const bool tail = rest > 0 && lane < rest && rest_at >= 0 && rest_at / kBlk % kAdjWarps == warp;
-    const int shift = v0 & 7;                     // a vector of four shares its byte with its neighbour
-    unsigned char* ring = smem + warp * (kAdjVecs * 512);            // + depth * kAdjWarps * kAdjVecs * 512
-    constexpr int kRowBytes = kAdjWarps * kAdjVecs * 512;
     // where the element at place t lies in the warp's part of a row
     auto element = [&](int slot, int t) {
       return reinterpret_cast<T*>(ring + slot * kRowBytes + t / kPlaceStep * 512) + t % kBlk;
     };
-    // grammar bits: asked for a row before the row's copy begins (eight bits per vector)
-    uint32_t bits[kAdjVecs];
-#pragma unroll
-    for (int i = 0; i < kAdjVecs; ++i) bits[i] = kFull;
-    auto ask = [&](int r) {
-      const uint8_t* src =
-          reinterpret_cast<const uint8_t*>(allow + (long long)(r - r_begin) * a.allowed_row_stride) + (v0 >> 3);
-#pragma unroll
-      for (int i = 0; i < kAdjVecs; ++i) ldg_byte(bits[i], src + i * (step / 8), i < nv && r < r_end);
-    };
-    auto copy = [&](int r, int slot) {
-      uint32_t ok = 0u;
-      const T* src = in + (long long)(r - r_begin) * P.in_stride + v0;
-#pragma unroll
-      for (int i = 0; i < kAdjVecs; ++i) {
-        const uint32_t k = (bits[i] >> shift) & kAll;
-        ok |= k << (8 * i);
-        cp_async(ring + slot * kRowBytes + i * 512 + lane * 16, src + i * step, r < r_end && i < nv && k != 0u);
-      }
-      cp_commit();
-      row_ok[slot][tid] = ok;
-      if (allow) ask(r + 1);
-    };
-    if (allow) ask(r_begin);
-    for (int k = 0; k < kDepth - 1; ++k) copy(r_begin + k, k);
     uint32_t path = node_bits(r_begin);
     int slot = 0;
     for (int r = r_begin; r < r_end; ++r) {

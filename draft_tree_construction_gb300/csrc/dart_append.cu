@@ -16,6 +16,7 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kAppThreads = 128;
+constexpr int kBatch = 3;             // quads of heads that a warp has under way
 
 struct AppendParams {
   const void* q;
@@ -35,43 +36,45 @@ struct AppendParams {
   float eps;
   dart_cache_t c;
   int quads, parts;           // groups of four heads; warps per token
+  FastDiv by_parts, by_page;
+  float inv_dim;
   uint32_t* err;
 };
 
-template <typename T> __device__ __forceinline__ float2 unpack2(uint32_t w);
-template <> __device__ __forceinline__ float2 unpack2<__half>(uint32_t w) {
+// A 32-bit word of two elements as two fp32 values, and back.
+template <typename T> __device__ __forceinline__ uint64_t unpack2(uint32_t w);
+template <> __device__ __forceinline__ uint64_t unpack2<__half>(uint32_t w) {
   __half2 h;
   memcpy(&h, &w, 4);
-  return __half22float2(h);
+  const float2 f = __half22float2(h);
+  return pair(f.x, f.y);
 }
-template <> __device__ __forceinline__ float2 unpack2<__nv_bfloat16>(uint32_t w) {
-  return make_float2(__uint_as_float(w << 16), __uint_as_float(w & 0xFFFF0000u));
+template <> __device__ __forceinline__ uint64_t unpack2<__nv_bfloat16>(uint32_t w) {
+  return uint64_t(w << 16) | (uint64_t(w & 0xFFFF0000u) << 32);
 }
-template <typename T> __device__ __forceinline__ uint32_t pack2(float a, float b);
-template <> __device__ __forceinline__ uint32_t pack2<__half>(float a, float b) {
-  const __half2 h = __floats2half2_rn(a, b);
+template <typename T> __device__ __forceinline__ uint32_t pack2(uint64_t x);
+template <> __device__ __forceinline__ uint32_t pack2<__half>(uint64_t x) {
+  const __half2 h = __floats2half2_rn(low(x), high(x));
   uint32_t w;
   memcpy(&w, &h, 4);
   return w;
 }
-template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, float b) {
-  const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
+template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(uint64_t x) {
+  const __nv_bfloat162 h = __floats2bfloat162_rn(low(x), high(x));
   uint32_t w;
   memcpy(&w, &h, 4);
   return w;
 }
-template <typename T> __device__ __forceinline__ void unpack8(uint4 u, float* x) {
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const float2 f = unpack2<T>(w[i]);
-    x[2 * i] = f.x;
-    x[2 * i + 1] = f.y;
-  }
+template <typename T> __device__ __forceinline__ void unpack8(uint4 u, uint64_t* x) {
+  x[0] = unpack2<T>(u.x);
+  x[1] = unpack2<T>(u.y);
+  x[2] = unpack2<T>(u.z);
+  x[3] = unpack2<T>(u.w);
 }
-template <typename T> __device__ __forceinline__ uint4 pack8(const float* x) {
-  return make_uint4(pack2<T>(x[0], x[1]), pack2<T>(x[2], x[3]), pack2<T>(x[4], x[5]), pack2<T>(x[6], x[7]));
+template <typename T> __device__ __forceinline__ uint4 pack8(const uint64_t* x) {
+  return make_uint4(pack2<T>(x[0]), pack2<T>(x[1]), pack2<T>(x[2]), pack2<T>(x[3]));
 }
+__device__ __forceinline__ uint64_t swap2(uint64_t x) { return (x << 32) | (x >> 32); }
 
 // The sequence of token t: the number of entries of starts[1..B] that are <= t
 // (B when t lies behind them all).  The 32 lanes probe together.
@@ -93,25 +96,9 @@ template <typename T>
 __global__ void __launch_bounds__(kAppThreads)
 append_kernel(const AppendParams P) {
   const int lane = threadIdx.x & 31;
-  const long long unit = (long long)blockIdx.x * (kAppThreads / 32) + (threadIdx.x >> 5);
-  const int t = int(unit / P.parts), part = int(unit % P.parts);
+  const int unit = blockIdx.x * (kAppThreads / 32) + (threadIdx.x >> 5);
+  const int t = P.by_parts.div(unit), part = unit - t * P.parts;
   if (t >= P.T) return;
-  const int b = find_sequence(P.starts, P.B, t, lane);
-  if (b >= P.B) return;
-  const int index = t - P.starts[b];
-  if (index < 0) return;
-
-  const int len = P.lengths[b];
-  const long long slot = (long long)len + index;
-  const dart_cache_t& C = P.c;
-  bool fits = len >= 0 && slot < (long long)C.table_width * C.page;
-  int page = 0, in_page = 0;
-  if (fits) {
-    page = C.table[(long long)b * C.table_stride + slot / C.page];
-    in_page = int(slot % C.page);
-    fits = page >= 0 && page < C.pages;
-  }
-  if (!fits && part == 0 && lane == 0) set_dev_error(P.err, DART_DEVERR_CACHE);
 
   // this lane's two vectors of a head
   const int sub = lane & 7;
@@ -128,92 +115,135 @@ append_kernel(const AppendParams P) {
   }
   const bool has_a = va < nv, has_b = vb < nv;
 
-  float cs[8], sn[8];
+  // The heads' vectors are asked for first, kBatch quads at a time: everything
+  // that follows up to their use (the token's sequence, its page, its angles)
+  // waits for memory as well.
+  uint4 ua[kBatch], ub[kBatch];
+  auto fetch = [&](int first) {
+#pragma unroll
+    for (int i = 0; i < kBatch; ++i) {
+      const int quad = first + i * P.parts, h = 4 * quad + (lane >> 3);
+      const T* src = nullptr;
+      if (h < P.Hq) src = static_cast<const T*>(P.q) + (long long)t * P.q_ts + (long long)h * P.q_hs;
+      else if (h < P.Hq + P.Hkv)
+        src = static_cast<const T*>(P.k) + (long long)t * P.k_ts + (long long)(h - P.Hq) * P.k_hs;
+      else if (h < P.Hq + 2 * P.Hkv)
+        src = static_cast<const T*>(P.v) + (long long)t * P.v_ts + (long long)(h - P.Hq - P.Hkv) * P.v_hs;
+      ua[i] = ub[i] = make_uint4(0, 0, 0, 0);
+      if (src && has_a) ua[i] = *reinterpret_cast<const uint4*>(src + 8 * va);
+      if (src && has_b) ub[i] = *reinterpret_cast<const uint4*>(src + 8 * vb);
+    }
+  };
+  fetch(part);
+  uint64_t phase[8];
+#pragma unroll
+  for (int j = 0; j < 8; ++j) phase[j] = turns ? P.turns[8 * sub + j] : 0ull;
+
+  const int b = find_sequence(P.starts, P.B, t, lane);
+  if (b >= P.B) return;
+  const int index = t - P.starts[b];
+  if (index < 0) return;
+  const int len = P.lengths[b];
+  const long long slot = (long long)len + index;
+  const dart_cache_t& C = P.c;
+  bool fits = len >= 0 && slot < (long long)C.table_width * C.page;
+  int page = 0, in_page = 0;
+  if (fits) {
+    const int at = P.by_page.div(int(slot));
+    page = C.table[(long long)b * C.table_stride + at];
+    in_page = int(slot) - at * C.page;
+  }
+
+  uint64_t cs[4], sn[4];                     // of this lane's pairs 2j, 2j + 1
   if (turns) {
     const long long pos = P.offsets ? (long long)len + P.offsets[t] : slot;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      // the position's phase as a fraction of a turn, exact modulo 2^64; its upper half in half turns
-      const uint64_t phase = uint64_t(pos) * P.turns[8 * sub + j];
-      const float x = float(int32_t(uint32_t(phase >> 32))) * 0x1p-31f;
-      sincospif(x, &sn[j], &cs[j]);
-      sn[j] *= P.magnitude;
-      cs[j] *= P.magnitude;
+    for (int j = 0; j < 4; ++j) {
+      float s[2], c[2];
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        // the position's phase as a fraction of a turn, exact modulo 2^64; its upper half in half turns
+        const uint64_t turned = uint64_t(pos) * phase[2 * j + e];
+        sincospif(float(int32_t(uint32_t(turned >> 32))) * 0x1p-31f, &s[e], &c[e]);
+      }
+      sn[j] = pair(s[0] * P.magnitude, s[1] * P.magnitude);
+      cs[j] = pair(c[0] * P.magnitude, c[1] * P.magnitude);
     }
   }
+  if (fits) fits = page >= 0 && page < C.pages;
+  if (!fits && part == 0 && lane == 0) set_dev_error(P.err, DART_DEVERR_CACHE);
 
-  for (int quad = part; quad < P.quads; quad += P.parts) {
-    const int h = 4 * quad + (lane >> 3);
-    const bool is_q = h < P.Hq, is_k = !is_q && h < P.Hq + P.Hkv, is_v = !is_q && !is_k && h < P.Hq + 2 * P.Hkv;
-    const T* src = nullptr;
-    T* dst = nullptr;
-    const T* weight = nullptr;
-    if (is_q) {
-      src = static_cast<const T*>(P.q) + (long long)t * P.q_ts + (long long)h * P.q_hs;
-      dst = static_cast<T*>(P.out) + (long long)t * P.o_ts + (long long)h * P.o_hs;
-      weight = static_cast<const T*>(P.q_weight);
-    } else if (is_k && fits) {
-      src = static_cast<const T*>(P.k) + (long long)t * P.k_ts + (long long)(h - P.Hq) * P.k_hs;
-      dst = static_cast<T*>(C.k) + (long long)page * C.k_page_stride + (long long)in_page * C.k_row_stride +
-            (long long)(h - P.Hq) * C.k_head_stride;
-      weight = static_cast<const T*>(P.k_weight);
-    } else if (is_v && fits) {
-      const int hv = h - P.Hq - P.Hkv;
-      src = static_cast<const T*>(P.v) + (long long)t * P.v_ts + (long long)hv * P.v_hs;
-      dst = static_cast<T*>(C.v) + (long long)page * C.v_page_stride + (long long)in_page * C.v_row_stride +
-            (long long)hv * C.v_head_stride;
-    }
-    uint4 ua = make_uint4(0, 0, 0, 0), ub = ua;
-    if (src && has_a) ua = *reinterpret_cast<const uint4*>(src + 8 * va);
-    if (src && has_b) ub = *reinterpret_cast<const uint4*>(src + 8 * vb);
-    if (!is_v) {
-      float xa[8], xb[8];
-      unpack8<T>(ua, xa);
-      unpack8<T>(ub, xb);
-      float ss = 0.f;
+  for (int first = part; first < P.quads; first += kBatch * P.parts) {
+    if (first != part) fetch(first);
 #pragma unroll
-      for (int j = 0; j < 8; ++j) ss += xa[j] * xa[j] + xb[j] * xb[j];
-#pragma unroll
-      for (int s = 1; s < 8; s <<= 1) ss += __shfl_xor_sync(0xFFu << (lane & 24), ss, s);
-      if (weight) {
-        const float inv = rsqrtf(ss / float(P.D) + P.eps);
-        float wa[8], wb[8];
-        unpack8<T>(has_a ? *reinterpret_cast<const uint4*>(weight + 8 * va) : make_uint4(0, 0, 0, 0), wa);
-        unpack8<T>(has_b ? *reinterpret_cast<const uint4*>(weight + 8 * vb) : make_uint4(0, 0, 0, 0), wb);
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          xa[j] *= inv * wa[j];
-          xb[j] *= inv * wb[j];
-        }
+    for (int i = 0; i < kBatch; ++i) {
+      const int quad = first + i * P.parts, h = 4 * quad + (lane >> 3);
+      if (quad >= P.quads) break;
+      const bool is_q = h < P.Hq, is_k = !is_q && h < P.Hq + P.Hkv, is_v = !is_q && !is_k && h < P.Hq + 2 * P.Hkv;
+      T* dst = nullptr;
+      const T* weight = nullptr;
+      if (is_q) {
+        dst = static_cast<T*>(P.out) + (long long)t * P.o_ts + (long long)h * P.o_hs;
+        weight = static_cast<const T*>(P.q_weight);
+      } else if (is_k) {
+        if (fits)
+          dst = static_cast<T*>(C.k) + (long long)page * C.k_page_stride + (long long)in_page * C.k_row_stride +
+                (long long)(h - P.Hq) * C.k_head_stride;
+        weight = static_cast<const T*>(P.k_weight);
+      } else if (is_v && fits) {
+        dst = static_cast<T*>(C.v) + (long long)page * C.v_page_stride + (long long)in_page * C.v_row_stride +
+              (long long)(h - P.Hq - P.Hkv) * C.v_head_stride;
       }
-      if (turns) {
-        if (P.interleaved) {
-          // vectors 2 sub, 2 sub + 1: pairs 8 sub .. 8 sub + 7 in place
+      if ((is_q || is_k) && (weight || P.rot > 0)) {
+        uint64_t xa[4], xb[4];
+        unpack8<T>(ua[i], xa);
+        unpack8<T>(ub[i], xb);
+        if (weight) {
+          uint64_t ss = mul2(xa[0], xa[0]);
+#pragma unroll
+          for (int j = 1; j < 4; ++j) ss = fma2(xa[j], xa[j], ss);
+#pragma unroll
+          for (int j = 0; j < 4; ++j) ss = fma2(xb[j], xb[j], ss);
+          float sum = low(ss) + high(ss);
+#pragma unroll
+          for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xFFu << (lane & 24), sum, s);
+          const float inv = rsqrtf(fmaf(sum, P.inv_dim, P.eps));
+          const uint64_t inv2 = pair(inv, inv);
+          uint64_t wa[4], wb[4];
+          unpack8<T>(has_a ? *reinterpret_cast<const uint4*>(weight + 8 * va) : make_uint4(0, 0, 0, 0), wa);
+          unpack8<T>(has_b ? *reinterpret_cast<const uint4*>(weight + 8 * vb) : make_uint4(0, 0, 0, 0), wb);
 #pragma unroll
           for (int j = 0; j < 4; ++j) {
-            const float a0 = xa[2 * j], a1 = xa[2 * j + 1];
-            xa[2 * j] = a0 * cs[j] - a1 * sn[j];
-            xa[2 * j + 1] = a1 * cs[j] + a0 * sn[j];
-            const float b0 = xb[2 * j], b1 = xb[2 * j + 1];
-            xb[2 * j] = b0 * cs[4 + j] - b1 * sn[4 + j];
-            xb[2 * j + 1] = b1 * cs[4 + j] + b0 * sn[4 + j];
-          }
-        } else {
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            const float a = xa[j], c = xb[j];
-            xa[j] = a * cs[j] - c * sn[j];
-            xb[j] = c * cs[j] + a * sn[j];
+            xa[j] = mul2(xa[j], mul2(inv2, wa[j]));
+            xb[j] = mul2(xb[j], mul2(inv2, wb[j]));
           }
         }
+        if (turns) {
+          if (P.interleaved) {
+            // vectors 2 sub, 2 sub + 1 hold pairs 8 sub .. 8 sub + 7: (x, y) -> (x c - y s, y c + x s)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t ca = cs[j >> 1], sa = sn[j >> 1], cb = cs[2 + (j >> 1)], sb = sn[2 + (j >> 1)];
+              const float c0 = j & 1 ? high(ca) : low(ca), s0 = j & 1 ? high(sa) : low(sa);
+              const float c1 = j & 1 ? high(cb) : low(cb), s1 = j & 1 ? high(sb) : low(sb);
+              xa[j] = fma2(swap2(xa[j]), pair(-s0, s0), mul2(xa[j], pair(c0, c0)));
+              xb[j] = fma2(swap2(xb[j]), pair(-s1, s1), mul2(xb[j], pair(c1, c1)));
+            }
+          } else {
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+              const uint64_t x = xa[j], y = xb[j], minus = sn[j] ^ 0x8000000080000000ull;
+              xa[j] = fma2(y, minus, mul2(x, cs[j]));
+              xb[j] = fma2(x, sn[j], mul2(y, cs[j]));
+            }
+          }
+        }
+        ua[i] = pack8<T>(xa);
+        ub[i] = pack8<T>(xb);
       }
-      if (weight || turns) {
-        ua = pack8<T>(xa);
-        ub = pack8<T>(xb);
-      }
+      if (dst && has_a) *reinterpret_cast<uint4*>(dst + 8 * va) = ua[i];
+      if (dst && has_b) *reinterpret_cast<uint4*>(dst + 8 * vb) = ub[i];
     }
-    if (dst && has_a) *reinterpret_cast<uint4*>(dst + 8 * va) = ua;
-    if (dst && has_b) *reinterpret_cast<uint4*>(dst + 8 * vb) = ub;
   }
 }
 
@@ -317,11 +347,14 @@ extern "C" int dart_kv_append(const void* q, int64_t q_token_stride, int64_t q_h
   P.c = *cache;
   P.err = device_err;
   P.quads = (q_heads + 2 * cache->heads + 3) / 4;
-  // one warp per token when there are tokens enough to fill the device, else a
-  // token's heads are spread over several
+  // A warp takes one batch of quads when tokens are few, then several, so that
+  // the angles are computed once for as many heads as the number of warps allows.
   const long long want = 152ll * 32;
   long long parts = (want + T - 1) / T;
   P.parts = int(parts < 1 ? 1 : parts > P.quads ? P.quads : parts);
+  P.by_parts = fast_div(uint32_t(P.parts));
+  P.by_page = fast_div(uint32_t(cache->page));
+  P.inv_dim = 1.f / float(cache->dim);
   const long long warps = (long long)T * P.parts;
   const unsigned grid = unsigned((warps + kAppThreads / 32 - 1) / (kAppThreads / 32));
   cudaStream_t s = static_cast<cudaStream_t>(stream);

@@ -175,23 +175,6 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
   return w;
 }
 
-// Two fp32 values in one register pair, for the packed arithmetic.
-__device__ __forceinline__ uint64_t pair(float a, float b) {
-  return uint64_t(__float_as_uint(a)) | (uint64_t(__float_as_uint(b)) << 32);
-}
-__device__ __forceinline__ float low(uint64_t x) { return __uint_as_float(uint32_t(x)); }
-__device__ __forceinline__ float high(uint64_t x) { return __uint_as_float(uint32_t(x >> 32)); }
-__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
-  uint64_t d;
-  asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
-  return d;
-}
-__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
-  uint64_t d;
-  asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
-  return d;
-}
-
 // Operand type in the instruction descriptor.
 template <typename T> constexpr uint32_t kTypeCode = 0;
 template <> constexpr uint32_t kTypeCode<__nv_bfloat16> = 1;

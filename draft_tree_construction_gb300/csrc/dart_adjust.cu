@@ -96,15 +96,6 @@ __device__ __forceinline__ void ldg_elem(uint32_t& v, const T* p, bool on) {
                  : "+r"(v) : "l"(p), "r"(uint32_t(on)) : "memory");
   }
 }
-// 16 bytes from memory to shared memory, without a register.
-__device__ __forceinline__ void cp_async(void* dst, const void* src, bool on) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
-               "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}"
-               :: "r"(smem_u32(dst)), "l"(src), "r"(uint32_t(on)) : "memory");
-}
-__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-__device__ __forceinline__ void cp_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
 template <typename T>
 __device__ __forceinline__ T elem_of(uint32_t v) {
   T x;
@@ -202,9 +193,9 @@ adjust_kernel(const AdjustParams P) {
     for (int i = 0; i < kAdjVecs; ++i) {
       const uint32_t k = (bits[i] >> shift) & kAll;
       ok |= k << (8 * i);
-      cp_async(ring + slot * kRowBytes + i * 512 + lane * 16, src + i * step, r < r_end && i < nv && k != 0u);
+      cp_async16(ring + slot * kRowBytes + i * 512 + lane * 16, src + i * step, r < r_end && i < nv && k != 0u);
     }
-    cp_commit();
+    cp_async_commit();
     row_ok[slot][tid] = ok;
     if (allow) ask(r + 1);
   };
@@ -456,7 +447,7 @@ adjust_kernel(const AdjustParams P) {
     for (int r = r_begin; r < r_end; ++r) {
       copy(r + kDepth - 1, slot == 0 ? kDepth - 1 : slot - 1);
       const uint32_t next_path = node_bits(r + 1);
-      cp_wait<kDepth - 1>();
+      cp_async_wait<kDepth - 1>();
       __syncwarp();
       const bool walked = paths && __any_sync(kFull, path != 0u);
       if (walked) path_in(path);
@@ -515,7 +506,7 @@ adjust_kernel(const AdjustParams P) {
       path = next_path;
       slot = slot + 1 < kDepth ? slot + 1 : 0;
     }
-    cp_wait<0>();
+    cp_async_wait<0>();
   } else {
     const int words = (P.V + 31) >> 5;
     for (int r = r_begin; r < r_end; ++r) {

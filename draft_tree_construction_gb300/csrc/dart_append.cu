@@ -2,11 +2,10 @@
 // norms of query and key heads and the rotary positions in the same pass.
 //
 // One warp takes four heads of one token at a time, eight lanes a head, two
-// 16-byte vectors a lane: the two vectors hold the two elements of each pair
-// (half layout), or neighbouring pairs (interleaved), so the turn needs no
-// exchange, a norm is one reduction over eight lanes, and the sines and
-// cosines, which depend on the token and the lane alone, are computed once and
-// serve every head that the warp takes.
+// 16-byte vectors a lane: a lane holds both elements of each of its pairs, so
+// the turn needs no exchange, a norm is one reduction over eight lanes, and the
+// sines and cosines, which depend on the token alone, are computed once (two
+// pairs a lane, then exchanged) and serve every head that the warp takes.
 #include <cmath>
 
 #include "dart_launch.h"
@@ -16,7 +15,9 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kAppThreads = 128;
-constexpr int kBatch = 3;             // quads of heads that a warp has under way
+constexpr int kAhead = 6;             // quads of heads that a warp has under way
+constexpr int kQuadBytes = 1024;      // two vectors a lane
+constexpr int kRingBytes = kAppThreads / 32 * kAhead * kQuadBytes;
 
 struct AppendParams {
   const void* q;
@@ -35,8 +36,8 @@ struct AppendParams {
   const void* k_weight;
   float eps;
   dart_cache_t c;
-  int quads, parts;           // groups of four heads; warps per token
-  FastDiv by_parts, by_page;
+  int q_quads, k_quads, quads, parts;   // groups of four heads: of q, of k (and v), all; warps per token
+  FastDiv by_parts, by_page, by_share;  // by_share: T / B, if B sequences of one length would fill T (else d = 0)
   float inv_dim;
   uint32_t* err;
 };
@@ -100,50 +101,75 @@ append_kernel(const AppendParams P) {
   const int t = P.by_parts.div(unit), part = unit - t * P.parts;
   if (t >= P.T) return;
 
-  // this lane's two vectors of a head
+  // This lane's two vectors of a head; eight lanes' vectors lie side by side.
+  // Half layout: the rv lanes that turn hold the two vectors of a pair each, the
+  // others what stays.  Interleaved: a pair lies within a vector, so any two do.
   const int sub = lane & 7;
-  const int rv = P.rot >> 4;                 // lanes that turn; each holds one vector of either half
-  const int nv = P.D >> 3;
-  const bool turns = sub < rv;
-  int va, vb;
-  if (turns) {
-    va = P.interleaved ? 2 * sub : sub;
-    vb = P.interleaved ? 2 * sub + 1 : sub + rv;
+  const int rv = P.rot >> 4, nv = P.D >> 3;
+  int va = sub, vb = sub + 8;
+  bool turn_a, turn_b;
+  if (P.interleaved) {
+    turn_a = va < 2 * rv;
+    turn_b = vb < 2 * rv;
   } else {
-    va = 2 * rv + 2 * (sub - rv);
-    vb = va + 1;
+    turn_a = turn_b = sub < rv;
+    if (turn_a) vb = sub + rv;
+    else va = sub + rv, vb = va + 8 - rv;
   }
   const bool has_a = va < nv, has_b = vb < nv;
 
-  // The heads' vectors are asked for first, kBatch quads at a time: everything
-  // that follows up to their use (the token's sequence, its page, its angles)
-  // waits for memory as well.
-  uint4 ua[kBatch], ub[kBatch];
-  auto fetch = [&](int first) {
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int quad = first + i * P.parts, h = 4 * quad + (lane >> 3);
-      const T* src = nullptr;
-      if (h < P.Hq) src = static_cast<const T*>(P.q) + (long long)t * P.q_ts + (long long)h * P.q_hs;
-      else if (h < P.Hq + P.Hkv)
-        src = static_cast<const T*>(P.k) + (long long)t * P.k_ts + (long long)(h - P.Hq) * P.k_hs;
-      else if (h < P.Hq + 2 * P.Hkv)
-        src = static_cast<const T*>(P.v) + (long long)t * P.v_ts + (long long)(h - P.Hq - P.Hkv) * P.v_hs;
-      ua[i] = ub[i] = make_uint4(0, 0, 0, 0);
-      if (src && has_a) ua[i] = *reinterpret_cast<const uint4*>(src + 8 * va);
-      if (src && has_b) ub[i] = *reinterpret_cast<const uint4*>(src + 8 * vb);
+  // The quads of the queries, then of the keys, then of the values; this warp's are part, part + parts, ...
+  struct Segment { const T* src; long long hs; int first, end, heads; };
+  auto segment = [&](int kind) {
+    Segment g;
+    if (kind == 0) {
+      g = Segment{static_cast<const T*>(P.q) + (long long)t * P.q_ts, P.q_hs, 0, P.q_quads, P.Hq};
+    } else if (kind == 1) {
+      g = Segment{static_cast<const T*>(P.k) + (long long)t * P.k_ts, P.k_hs, P.q_quads, P.q_quads + P.k_quads, P.Hkv};
+    } else {
+      g = Segment{static_cast<const T*>(P.v) + (long long)t * P.v_ts, P.v_hs, P.q_quads + P.k_quads, P.quads, P.Hkv};
     }
+    return g;
   };
-  fetch(part);
-  uint64_t phase[8];
-#pragma unroll
-  for (int j = 0; j < 8; ++j) phase[j] = turns ? P.turns[8 * sub + j] : 0ull;
+  // The heads' vectors are asked for first, kAhead quads of them: everything
+  // that follows up to their use (the token's sequence, its page, its angles)
+  // waits for memory as well.  They arrive in shared memory, each lane reading
+  // back what it asked for.
+  extern __shared__ __align__(16) unsigned char smem[];
+  unsigned char* ring = smem + (threadIdx.x >> 5) * (kAhead * kQuadBytes) + 16 * lane;
+  int asked = part, into = 0;                // the next quad to ask for, and its place
+  auto ask = [&]() {
+    if (asked < P.quads) {
+      const int kind = asked < P.q_quads ? 0 : asked < P.q_quads + P.k_quads ? 1 : 2;
+      const Segment g = segment(kind);
+      const int h = 4 * (asked - g.first) + (lane >> 3);
+      const T* src = g.src + (long long)h * g.hs;
+      cp_async16(ring + into * kQuadBytes, src + 8 * va, has_a && h < g.heads);
+      cp_async16(ring + into * kQuadBytes + 512, src + 8 * vb, has_b && h < g.heads);
+      asked += P.parts;
+    }
+    cp_async_commit();
+    into = into + 1 < kAhead ? into + 1 : 0;
+  };
+#pragma unroll 1
+  for (int i = 0; i < kAhead - 1; ++i) ask();
+  int quad = part, place = 0;
+  const int kind0 = quad < P.q_quads ? 0 : quad < P.q_quads + P.k_quads ? 1 : 2;
+  const bool my_pair = 4 * lane < P.rot;     // pairs 2 lane and 2 lane + 1 are this lane's to compute
+  const uint64_t turn0 = my_pair ? P.turns[2 * lane] : 0ull, turn1 = my_pair ? P.turns[2 * lane + 1] : 0ull;
 
-  const int b = find_sequence(P.starts, P.B, t, lane);
-  if (b >= P.B) return;
-  const int index = t - P.starts[b];
+  const int off = P.offsets ? P.offsets[t] : 0;
+  // chunks of one size (a tree per sequence, a token per sequence) are found without a search
+  int b = P.by_share.d ? P.by_share.div(t) : 0;
+  int start = P.starts[b], end = P.starts[b + 1], len = P.lengths[b];
+  if (t < start || t >= end) {
+    b = find_sequence(P.starts, P.B, t, lane);
+    if (b >= P.B) return;
+    start = P.starts[b];
+    len = P.lengths[b];
+  }
+  const int index = t - start;
   if (index < 0) return;
-  const int len = P.lengths[b];
   const long long slot = (long long)len + index;
   const dart_cache_t& C = P.c;
   bool fits = len >= 0 && slot < (long long)C.table_width * C.page;
@@ -154,50 +180,100 @@ append_kernel(const AppendParams P) {
     in_page = int(slot) - at * C.page;
   }
 
-  uint64_t cs[4], sn[4];                     // of this lane's pairs 2j, 2j + 1
-  if (turns) {
-    const long long pos = P.offsets ? (long long)len + P.offsets[t] : slot;
+  uint64_t cs[4], sn[4];                     // of this lane's pairs, two at a time (see `from`)
+  if (P.rot > 0) {
+    const long long pos = P.offsets ? (long long)len + off : slot;
+    float s[2], c[2];
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      // the position's phase as a fraction of a turn, exact modulo 2^64; its upper half in half turns
+      const uint64_t turned = uint64_t(pos) * (e ? turn1 : turn0);
+      sincospif(float(int32_t(uint32_t(turned >> 32))) * 0x1p-31f, &s[e], &c[e]);
+      s[e] *= P.magnitude;
+      c[e] *= P.magnitude;
+    }
+    const uint64_t cc = pair(c[0], c[1]), ss = pair(s[0], s[1]);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float s[2], c[2];
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        // the position's phase as a fraction of a turn, exact modulo 2^64; its upper half in half turns
-        const uint64_t turned = uint64_t(pos) * phase[2 * j + e];
-        sincospif(float(int32_t(uint32_t(turned >> 32))) * 0x1p-31f, &s[e], &c[e]);
-      }
-      sn[j] = pair(s[0] * P.magnitude, s[1] * P.magnitude);
-      cs[j] = pair(c[0] * P.magnitude, c[1] * P.magnitude);
+      // half layout: pairs 8 sub + 2 j and the next; interleaved: pairs 4 va + 2 j for j < 2, then 4 vb + 2 (j - 2)
+      const int from = P.interleaved ? (j < 2 ? 2 * va + j : 2 * vb + j - 2) & 31 : (4 * sub + j) & 31;
+      cs[j] = __shfl_sync(kFull, cc, from);
+      sn[j] = __shfl_sync(kFull, ss, from);
     }
   }
   if (fits) fits = page >= 0 && page < C.pages;
   if (!fits && part == 0 && lane == 0) set_dev_error(P.err, DART_DEVERR_CACHE);
 
-  for (int first = part; first < P.quads; first += kBatch * P.parts) {
-    if (first != part) fetch(first);
-#pragma unroll
-    for (int i = 0; i < kBatch; ++i) {
-      const int quad = first + i * P.parts, h = 4 * quad + (lane >> 3);
-      if (quad >= P.quads) break;
-      const bool is_q = h < P.Hq, is_k = !is_q && h < P.Hq + P.Hkv, is_v = !is_q && !is_k && h < P.Hq + 2 * P.Hkv;
-      T* dst = nullptr;
-      const T* weight = nullptr;
-      if (is_q) {
-        dst = static_cast<T*>(P.out) + (long long)t * P.o_ts + (long long)h * P.o_hs;
-        weight = static_cast<const T*>(P.q_weight);
-      } else if (is_k) {
-        if (fits)
-          dst = static_cast<T*>(C.k) + (long long)page * C.k_page_stride + (long long)in_page * C.k_row_stride +
-                (long long)(h - P.Hq) * C.k_head_stride;
-        weight = static_cast<const T*>(P.k_weight);
-      } else if (is_v && fits) {
-        dst = static_cast<T*>(C.v) + (long long)page * C.v_page_stride + (long long)in_page * C.v_row_stride +
-              (long long)(h - P.Hq - P.Hkv) * C.v_head_stride;
+  for (int kind = kind0; kind < 3; ++kind) {
+    const Segment g = segment(kind);
+    if (quad >= g.end) continue;
+    T* dst = nullptr;
+    long long dst_hs = 0;
+    const T* weight = nullptr;
+    if (kind == 0) {
+      dst = static_cast<T*>(P.out) + (long long)t * P.o_ts;
+      dst_hs = P.o_hs;
+      weight = static_cast<const T*>(P.q_weight);
+    } else if (kind == 1) {
+      dst = static_cast<T*>(C.k) + (long long)page * C.k_page_stride + (long long)in_page * C.k_row_stride;
+      dst_hs = C.k_head_stride;
+      weight = static_cast<const T*>(P.k_weight);
+    } else {
+      dst = static_cast<T*>(C.v) + (long long)page * C.v_page_stride + (long long)in_page * C.v_row_stride;
+      dst_hs = C.v_head_stride;
+    }
+    const bool writes = kind == 0 || fits;
+    const bool works = kind < 2 && (weight || P.rot > 0);
+    // The norm's weight and the turn in one pair of factors: an element is
+    //   inv * (x * w cos -+ y * w' sin),  y and w' being its partner and its partner's weight
+    uint64_t ka[4], la[4], kb[4], lb[4];
+    if (works) {
+      const uint64_t one = pair(1.f, 1.f);
+      uint64_t wa[4] = {one, one, one, one}, wb[4] = {one, one, one, one};
+      if (weight) {
+        if (has_a) unpack8<T>(*reinterpret_cast<const uint4*>(weight + 8 * va), wa);
+        if (has_b) unpack8<T>(*reinterpret_cast<const uint4*>(weight + 8 * vb), wb);
       }
-      if ((is_q || is_k) && (weight || P.rot > 0)) {
-        uint64_t xa[4], xb[4];
-        unpack8<T>(ua[i], xa);
-        unpack8<T>(ub[i], xb);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        ka[j] = wa[j];
+        kb[j] = wb[j];
+        la[j] = lb[j] = 0ull;
+        if (P.interleaved) {
+          // word j of a vector holds one pair: the vector's pairs 4 v + j
+          if (turn_a) {
+            const float c = j & 1 ? high(cs[j >> 1]) : low(cs[j >> 1]), s = j & 1 ? high(sn[j >> 1]) : low(sn[j >> 1]);
+            ka[j] = mul2(wa[j], pair(c, c));
+            la[j] = mul2(swap2(wa[j]), pair(-s, s));
+          }
+          if (turn_b) {
+            const float c = j & 1 ? high(cs[2 + (j >> 1)]) : low(cs[2 + (j >> 1)]);
+            const float s = j & 1 ? high(sn[2 + (j >> 1)]) : low(sn[2 + (j >> 1)]);
+            kb[j] = mul2(wb[j], pair(c, c));
+            lb[j] = mul2(swap2(wb[j]), pair(-s, s));
+          }
+        } else if (turn_a) {
+          ka[j] = mul2(wa[j], cs[j]);
+          kb[j] = mul2(wb[j], cs[j]);
+          la[j] = mul2(wb[j], sn[j] ^ 0x8000000080000000ull);
+          lb[j] = mul2(wa[j], sn[j]);
+        }
+      }
+    }
+    for (; quad < g.end; quad += P.parts) {
+      ask();
+      cp_async_wait<kAhead - 1>();
+      uint4 ua = *reinterpret_cast<const uint4*>(ring + place * kQuadBytes);
+      uint4 ub = *reinterpret_cast<const uint4*>(ring + place * kQuadBytes + 512);
+      place = place + 1 < kAhead ? place + 1 : 0;
+      const int h = 4 * (quad - g.first) + (lane >> 3);
+      if (works) {
+        uint64_t xa[4], xb[4], ya[4], yb[4];
+        if (!has_b) ub = make_uint4(0, 0, 0, 0);          // never asked for
+        if (!has_a) ua = make_uint4(0, 0, 0, 0);
+        unpack8<T>(ua, xa);
+        unpack8<T>(ub, xb);
+        uint64_t inv2 = 0ull;
         if (weight) {
           uint64_t ss = mul2(xa[0], xa[0]);
 #pragma unroll
@@ -206,43 +282,29 @@ append_kernel(const AppendParams P) {
           for (int j = 0; j < 4; ++j) ss = fma2(xb[j], xb[j], ss);
           float sum = low(ss) + high(ss);
 #pragma unroll
-          for (int s = 1; s < 8; s <<= 1) sum += __shfl_xor_sync(0xFFu << (lane & 24), sum, s);
+          for (int o = 1; o < 8; o <<= 1) sum += __shfl_xor_sync(kFull, sum, o);
           const float inv = rsqrtf(fmaf(sum, P.inv_dim, P.eps));
-          const uint64_t inv2 = pair(inv, inv);
-          uint64_t wa[4], wb[4];
-          unpack8<T>(has_a ? *reinterpret_cast<const uint4*>(weight + 8 * va) : make_uint4(0, 0, 0, 0), wa);
-          unpack8<T>(has_b ? *reinterpret_cast<const uint4*>(weight + 8 * vb) : make_uint4(0, 0, 0, 0), wb);
+          inv2 = pair(inv, inv);
+        }
 #pragma unroll
-          for (int j = 0; j < 4; ++j) {
-            xa[j] = mul2(xa[j], mul2(inv2, wa[j]));
-            xb[j] = mul2(xb[j], mul2(inv2, wb[j]));
+        for (int j = 0; j < 4; ++j) {
+          ya[j] = mul2(xa[j], ka[j]);
+          yb[j] = mul2(xb[j], kb[j]);
+          if (turn_a) ya[j] = fma2(P.interleaved ? swap2(xa[j]) : xb[j], la[j], ya[j]);
+          if (turn_b) yb[j] = fma2(P.interleaved ? swap2(xb[j]) : xa[j], lb[j], yb[j]);
+          if (weight) {
+            ya[j] = mul2(ya[j], inv2);
+            yb[j] = mul2(yb[j], inv2);
           }
         }
-        if (turns) {
-          if (P.interleaved) {
-            // vectors 2 sub, 2 sub + 1 hold pairs 8 sub .. 8 sub + 7: (x, y) -> (x c - y s, y c + x s)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint64_t ca = cs[j >> 1], sa = sn[j >> 1], cb = cs[2 + (j >> 1)], sb = sn[2 + (j >> 1)];
-              const float c0 = j & 1 ? high(ca) : low(ca), s0 = j & 1 ? high(sa) : low(sa);
-              const float c1 = j & 1 ? high(cb) : low(cb), s1 = j & 1 ? high(sb) : low(sb);
-              xa[j] = fma2(swap2(xa[j]), pair(-s0, s0), mul2(xa[j], pair(c0, c0)));
-              xb[j] = fma2(swap2(xb[j]), pair(-s1, s1), mul2(xb[j], pair(c1, c1)));
-            }
-          } else {
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const uint64_t x = xa[j], y = xb[j], minus = sn[j] ^ 0x8000000080000000ull;
-              xa[j] = fma2(y, minus, mul2(x, cs[j]));
-              xb[j] = fma2(x, sn[j], mul2(y, cs[j]));
-            }
-          }
-        }
-        ua[i] = pack8<T>(xa);
-        ub[i] = pack8<T>(xb);
+        ua = pack8<T>(ya);
+        ub = pack8<T>(yb);
       }
-      if (dst && has_a) *reinterpret_cast<uint4*>(dst + 8 * va) = ua[i];
-      if (dst && has_b) *reinterpret_cast<uint4*>(dst + 8 * vb) = ub[i];
+      if (writes && h < g.heads) {
+        T* to = dst + (long long)h * dst_hs;
+        if (has_a) *reinterpret_cast<uint4*>(to + 8 * va) = ua;
+        if (has_b) *reinterpret_cast<uint4*>(to + 8 * vb) = ub;
+      }
     }
   }
 }
@@ -346,7 +408,9 @@ extern "C" int dart_kv_append(const void* q, int64_t q_token_stride, int64_t q_h
   P.q_weight = q_weight; P.k_weight = k_weight; P.eps = eps;
   P.c = *cache;
   P.err = device_err;
-  P.quads = (q_heads + 2 * cache->heads + 3) / 4;
+  P.q_quads = (q_heads + 3) / 4;
+  P.k_quads = (cache->heads + 3) / 4;
+  P.quads = P.q_quads + 2 * P.k_quads;
   // A warp takes one batch of quads when tokens are few, then several, so that
   // the angles are computed once for as many heads as the number of warps allows.
   const long long want = 152ll * 32;
@@ -354,11 +418,12 @@ extern "C" int dart_kv_append(const void* q, int64_t q_token_stride, int64_t q_h
   P.parts = int(parts < 1 ? 1 : parts > P.quads ? P.quads : parts);
   P.by_parts = fast_div(uint32_t(P.parts));
   P.by_page = fast_div(uint32_t(cache->page));
+  P.by_share = T % B == 0 ? fast_div(uint32_t(T / B)) : FastDiv{0, 0, 0};
   P.inv_dim = 1.f / float(cache->dim);
   const long long warps = (long long)T * P.parts;
   const unsigned grid = unsigned((warps + kAppThreads / 32 - 1) / (kAppThreads / 32));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cache->dtype == DART_F16) append_kernel<__half><<<grid, kAppThreads, 0, s>>>(P);
-  else append_kernel<__nv_bfloat16><<<grid, kAppThreads, 0, s>>>(P);
+  if (cache->dtype == DART_F16) append_kernel<__half><<<grid, kAppThreads, kRingBytes, s>>>(P);
+  else append_kernel<__nv_bfloat16><<<grid, kAppThreads, kRingBytes, s>>>(P);
   return cudaGetLastError() == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

@@ -278,6 +278,16 @@ __device__ __forceinline__ void bulk_g2s(void* dst, const void* src, uint32_t by
       :: "r"(smem_u32(dst)), "l"(src), "r"(bytes), "r"(smem_u32(bar)), "l"(pol) : "memory");
 }
 
+// 16 bytes from memory to shared memory, without a register.
+__device__ __forceinline__ void cp_async16(void* dst, const void* src, bool on) {
+  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t"
+               "@p cp.async.cg.shared.global [%0], [%1], 16;\n\t}"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(uint32_t(on)) : "memory");
+}
+__device__ __forceinline__ void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_async_wait() { asm volatile("cp.async.wait_group %0;" :: "n"(N) : "memory"); }
+
 // 32 bytes (32-byte aligned) in one load: two 16-byte vectors.
 __device__ __forceinline__ void ldg_nc_v8(const void* p, uint4& a, uint4& b) {
   asm volatile("ld.global.nc.v8.u32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"

@@ -93,8 +93,8 @@ __device__ __forceinline__ int find_sequence(const int32_t* starts, int B, int t
   return lo;
 }
 
-template <typename T>
-__global__ void __launch_bounds__(kAppThreads)
+template <typename T, bool INTERLEAVED>
+__global__ void __launch_bounds__(kAppThreads, 5)
 append_kernel(const AppendParams P) {
   const int lane = threadIdx.x & 31;
   const int unit = blockIdx.x * (kAppThreads / 32) + (threadIdx.x >> 5);
@@ -108,7 +108,7 @@ append_kernel(const AppendParams P) {
   const int rv = P.rot >> 4, nv = P.D >> 3;
   int va = sub, vb = sub + 8;
   bool turn_a, turn_b;
-  if (P.interleaved) {
+  if (INTERLEAVED) {
     turn_a = va < 2 * rv;
     turn_b = vb < 2 * rv;
   } else {
@@ -137,19 +137,27 @@ append_kernel(const AppendParams P) {
   // back what it asked for.
   extern __shared__ __align__(16) unsigned char smem[];
   unsigned char* ring = smem + (threadIdx.x >> 5) * (kAhead * kQuadBytes) + 16 * lane;
-  int asked = part, into = 0;                // the next quad to ask for, and its place
+  int asked = part, ask_end = 0, ask_heads = 0, ask_h = 0, into = 0;    // the next quad to ask for, its place
+  const T* ask_at = nullptr;
+  long long ask_step = 0;
   auto ask = [&]() {
     if (asked < P.quads) {
-      const int kind = asked < P.q_quads ? 0 : asked < P.q_quads + P.k_quads ? 1 : 2;
-      const Segment g = segment(kind);
-      const int h = 4 * (asked - g.first) + (lane >> 3);
-      const T* src = g.src + (long long)h * g.hs;
-      cp_async16(ring + into * kQuadBytes, src + 8 * va, has_a && h < g.heads);
-      cp_async16(ring + into * kQuadBytes + 512, src + 8 * vb, has_b && h < g.heads);
+      if (asked >= ask_end) {                // a new segment
+        const Segment g = segment(asked < P.q_quads ? 0 : asked < P.q_quads + P.k_quads ? 1 : 2);
+        ask_end = g.end;
+        ask_heads = g.heads;
+        ask_h = 4 * (asked - g.first) + (lane >> 3);
+        ask_at = g.src + (long long)ask_h * g.hs;
+        ask_step = 4ll * P.parts * g.hs;
+      }
+      cp_async16(ring + into, ask_at + 8 * va, has_a && ask_h < ask_heads);
+      cp_async16(ring + into + 512, ask_at + 8 * vb, has_b && ask_h < ask_heads);
       asked += P.parts;
+      ask_h += 4 * P.parts;
+      ask_at += ask_step;
     }
     cp_async_commit();
-    into = into + 1 < kAhead ? into + 1 : 0;
+    into = into + kQuadBytes < kAhead * kQuadBytes ? into + kQuadBytes : 0;
   };
 #pragma unroll 1
   for (int i = 0; i < kAhead - 1; ++i) ask();
@@ -196,7 +204,7 @@ append_kernel(const AppendParams P) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       // half layout: pairs 8 sub + 2 j and the next; interleaved: pairs 4 va + 2 j for j < 2, then 4 vb + 2 (j - 2)
-      const int from = P.interleaved ? (j < 2 ? 2 * va + j : 2 * vb + j - 2) & 31 : (4 * sub + j) & 31;
+      const int from = INTERLEAVED ? (j < 2 ? 2 * va + j : 2 * vb + j - 2) & 31 : (4 * sub + j) & 31;
       cs[j] = __shfl_sync(kFull, cc, from);
       sn[j] = __shfl_sync(kFull, ss, from);
     }
@@ -239,7 +247,7 @@ append_kernel(const AppendParams P) {
         ka[j] = wa[j];
         kb[j] = wb[j];
         la[j] = lb[j] = 0ull;
-        if (P.interleaved) {
+        if (INTERLEAVED) {
           // word j of a vector holds one pair: the vector's pairs 4 v + j
           if (turn_a) {
             const float c = j & 1 ? high(cs[j >> 1]) : low(cs[j >> 1]), s = j & 1 ? high(sn[j >> 1]) : low(sn[j >> 1]);
@@ -260,17 +268,21 @@ append_kernel(const AppendParams P) {
         }
       }
     }
-    for (; quad < g.end; quad += P.parts) {
+    int h = 4 * (quad - g.first) + (lane >> 3);
+    T* to = dst + (long long)h * dst_hs;
+    const long long to_step = 4ll * P.parts * dst_hs;
+    for (; quad < g.end; quad += P.parts, h += 4 * P.parts, to += to_step) {
       ask();
       cp_async_wait<kAhead - 1>();
-      uint4 ua = *reinterpret_cast<const uint4*>(ring + place * kQuadBytes);
-      uint4 ub = *reinterpret_cast<const uint4*>(ring + place * kQuadBytes + 512);
-      place = place + 1 < kAhead ? place + 1 : 0;
-      const int h = 4 * (quad - g.first) + (lane >> 3);
+      uint4 ua = *reinterpret_cast<const uint4*>(ring + place);
+      uint4 ub = *reinterpret_cast<const uint4*>(ring + place + 512);
+      place = place + kQuadBytes < kAhead * kQuadBytes ? place + kQuadBytes : 0;
       if (works) {
         uint64_t xa[4], xb[4], ya[4], yb[4];
-        if (!has_b) ub = make_uint4(0, 0, 0, 0);          // never asked for
-        if (!has_a) ua = make_uint4(0, 0, 0, 0);
+        if (nv < 16) {                                    // what was never asked for
+          if (!has_b) ub = make_uint4(0, 0, 0, 0);
+          if (!has_a) ua = make_uint4(0, 0, 0, 0);
+        }
         unpack8<T>(ua, xa);
         unpack8<T>(ub, xb);
         uint64_t inv2 = 0ull;
@@ -290,8 +302,8 @@ append_kernel(const AppendParams P) {
         for (int j = 0; j < 4; ++j) {
           ya[j] = mul2(xa[j], ka[j]);
           yb[j] = mul2(xb[j], kb[j]);
-          if (turn_a) ya[j] = fma2(P.interleaved ? swap2(xa[j]) : xb[j], la[j], ya[j]);
-          if (turn_b) yb[j] = fma2(P.interleaved ? swap2(xb[j]) : xa[j], lb[j], yb[j]);
+          if (turn_a) ya[j] = fma2(INTERLEAVED ? swap2(xa[j]) : xb[j], la[j], ya[j]);
+          if (turn_b) yb[j] = fma2(INTERLEAVED ? swap2(xb[j]) : xa[j], lb[j], yb[j]);
           if (weight) {
             ya[j] = mul2(ya[j], inv2);
             yb[j] = mul2(yb[j], inv2);
@@ -301,7 +313,6 @@ append_kernel(const AppendParams P) {
         ub = pack8<T>(yb);
       }
       if (writes && h < g.heads) {
-        T* to = dst + (long long)h * dst_hs;
         if (has_a) *reinterpret_cast<uint4*>(to + 8 * va) = ua;
         if (has_b) *reinterpret_cast<uint4*>(to + 8 * vb) = ub;
       }
@@ -423,7 +434,13 @@ extern "C" int dart_kv_append(const void* q, int64_t q_token_stride, int64_t q_h
   const long long warps = (long long)T * P.parts;
   const unsigned grid = unsigned((warps + kAppThreads / 32 - 1) / (kAppThreads / 32));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cache->dtype == DART_F16) append_kernel<__half><<<grid, kAppThreads, kRingBytes, s>>>(P);
-  else append_kernel<__nv_bfloat16><<<grid, kAppThreads, kRingBytes, s>>>(P);
+  const bool inter = P.interleaved != 0;
+  if (cache->dtype == DART_F16) {
+    if (inter) append_kernel<__half, true><<<grid, kAppThreads, kRingBytes, s>>>(P);
+    else append_kernel<__half, false><<<grid, kAppThreads, kRingBytes, s>>>(P);
+  } else {
+    if (inter) append_kernel<__nv_bfloat16, true><<<grid, kAppThreads, kRingBytes, s>>>(P);
+    else append_kernel<__nv_bfloat16, false><<<grid, kAppThreads, kRingBytes, s>>>(P);
+  }
   return cudaGetLastError() == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

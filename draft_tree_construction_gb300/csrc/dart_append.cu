@@ -15,7 +15,7 @@ namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
 constexpr int kAppThreads = 128;
-constexpr int kAhead = 6;             // quads of heads that a warp has under way
+constexpr int kAhead = 5;             // quads of heads that a warp has under way
 constexpr int kQuadBytes = 1024;      // two vectors a lane
 constexpr int kRingBytes = kAppThreads / 32 * kAhead * kQuadBytes;
 

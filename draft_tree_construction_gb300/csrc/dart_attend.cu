@@ -15,13 +15,15 @@
 // so a block's tiles may be spread over several CTAs: each leaves (m, l, O) of
 // its part in the workspace and the join kernel merges them in a fixed order.
 // Within a CTA:
-//   warps 8, 10, 11  copy K and V tiles by TMA, one box per page and 64 columns,
+//   warps 8, 11 copy K and V tiles by TMA, one box per page and 64 columns,
 //               into a ring of swizzled shared-memory stages; they take the
 //               loads in turn, because a box costs its warp about 100 cycles
-//   warp 9      issues the tcgen05 products: S into TMEM, P V into TMEM, P being
-//               read from TMEM where it replaced S
-//   warps 0-3, 4-7   softmax of one 128-row half each, a thread per row; while
-//               one half's softmax runs, the tensor unit works on the other's
+//   warps 9, 10 issue the tcgen05 products of one 128-row half each: S into
+//               TMEM, P V into TMEM, P being read from TMEM where it replaced S.
+//               One warp for both left the tensor unit idle for the 900 cycles
+//               a tile that its waits and commits take (61% busy).
+//   warps 0-3, 4-7   softmax of one half each, a thread per row; while one
+//               half's softmax runs, the tensor unit works on the other's
 #include <cmath>
 
 #include <cuda.h>
@@ -47,7 +49,7 @@ constexpr int kHalfTileBytes = kTile * kColBytes;    // 128 rows of 64 elements
 constexpr int kRingBytes = 10 * kHalfTileBytes;      // 160 KiB of K / V stages
 constexpr float kRescale = 8.f;         // growth of the maximum (in log2) that moves m
 constexpr uint32_t kTmemCols = 512;     // S0 | S1 | O0 | O1
-constexpr uint32_t kProducers = 3;      // warps 8, 10 and 11, which take the loads in turn
+constexpr uint32_t kProducers = 2;      // warps 8 and 11, which take the loads in turn
 constexpr long long kDrainLimit = 1ll << 31;
 
 struct AttendParams {
@@ -268,7 +270,7 @@ struct Span {
 
 struct Shared {
   uint64_t kv_full[10], kv_empty[10];
-  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain;
+  uint64_t q_full[2], s_full[2], p_full[2], o_full[2], drain[2];
   Span span;
   long long scan[kThreads / 32];
   uint32_t tmem;
@@ -400,7 +402,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
   if (tid == 0) {
     for (int i = 0; i < kStages; ++i) {
       mbar_init(&sh->kv_full[i], 1);
-      mbar_init(&sh->kv_empty[i], 1);
+      mbar_init(&sh->kv_empty[i], 2);        // one from either half
     }
     for (int t = 0; t < 2; ++t) {
       mbar_init(&sh->q_full[t], 4);
@@ -408,7 +410,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       mbar_init(&sh->p_full[t], 4);
       mbar_init(&sh->o_full[t], 1);
     }
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain[0], 1);
+    mbar_init(&sh->drain[1], 1);
     fence_mbar_init();
     sh->dead = 0;
     P.joints[blockIdx.x].parts = 0;        // this thread names the CTA's joint later, if there is one
@@ -427,9 +430,9 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
 
   if (warp >= 8) {
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kIssueRegs));
-    if (warp != 9) {
+    if (warp == 8 || warp == 11) {
       // ------------------------------------------------------------ producers
-      const uint32_t pid = warp == 8 ? 0u : uint32_t(warp - 9);
+      const uint32_t pid = warp == 8 ? 0u : 1u;
       Walk w;
       bool more = begin_walk(P, sh, w);
       uint32_t idx = 0, turn = 0;            // loads so far, and whose turn the next one is
@@ -489,11 +492,25 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       const uint64_t q_desc = smem_desc(smem_u32(sq), 16), k_desc = smem_desc(smem_u32(ring), 16),
                      v_desc = smem_desc(smem_u32(ring), kHalfTileBytes);
       const int k_steps = (P.D + 15) / 16;
-      uint32_t idx = 0, q_seen[2] = {0, 0}, p_seen[2] = {0, 0};
+      const int t = warp - 9;                 // the half whose products this warp issues
+      const uint32_t s_at = tmem + t * kTile, o_at = tmem + 2 * kTile + t * kCols;
+      const uint64_t qd = q_desc + t * (kStageBytes >> 4);
+      uint32_t idx = 0, q_seen = 0, p_seen = 0;
       bool ok = true;
       while (more && ok) {
-        const int n = w.t1 - w.t0, halves = w.rows > kHalfRows ? 2 : 1;
-        for (int j = -1; j < n && ok; ++j) {
+        const int n = w.t1 - w.t0;
+        if (w.rows <= t * kHalfRows) {
+          // The block has no second half.  This warp still sees every load arrive
+          // and gives its stage up: a stage's phases are told apart by their
+          // parity alone, so nobody may fall two of them behind or run ahead.
+          for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
+            ok = wait_warp(&sh->kv_full[idx % kStages], (idx / kStages) & 1u, sh, P.wait_limit);
+            if (ok && lane == 0) mbar_arrive(&sh->kv_empty[idx % kStages]);
+          }
+          if (ok) more = w.next(P);
+          continue;
+        }
+        for (int j = -1; j < n; ++j) {
           uint32_t ks = 0, vs = 0;
           if (j + 1 < n) {
             const uint32_t i = idx + k_load(j + 1);
@@ -507,36 +524,26 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
           }
           // steps of 16 positions; those wholly behind the block's end are left out
           const int steps = max(1, (min(w.end - (w.t0 + j) * kTile, kTile) + 15) / 16);
-#pragma unroll
-          for (int t = 0; t < 2; ++t) {
-            if (t >= halves || !ok) continue;
-            uint64_t* bar = j < 0 ? &sh->q_full[t] : &sh->p_full[t];
-            const uint32_t seen = j < 0 ? q_seen[t]++ : p_seen[t]++;
-            if (!(ok = wait_warp(bar, seen & 1u, sh, P.wait_limit))) continue;
-            tc_after();
-            if (elect()) {
-              if (j >= 0) {
-                const uint64_t vd = v_desc + uint64_t(vs * (kStageBytes >> 4));
-#pragma unroll
-                for (int k = 0; k < kTile / 16; ++k)
-                  if (k < steps)
-                    mma_ts(tmem + 2 * kTile + t * kCols, tmem + t * kTile + k * 8, vd + k * (16 * kColBytes >> 4), id_o,
-                           j > 0 || k > 0);
-              }
-              if (j + 1 < n) {
-                const uint64_t kd = k_desc + uint64_t(ks * (kStageBytes >> 4)), qd = q_desc + t * (kStageBytes >> 4);
-#pragma unroll
-                for (int k = 0; k < 4 * DH; ++k) {
-                  const int off = ((k >> 2) * kHalfTileBytes + (k & 3) * 32) >> 4;
-                  if (k < k_steps) mma_ss(tmem + t * kTile, qd + off, kd + off, id_s, k > 0);
-                }
-              }
-              tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
-            }
-            __syncwarp();
-          }
+          ok = j < 0 ? wait_warp(&sh->q_full[t], q_seen++ & 1u, sh, P.wait_limit)
+                     : wait_warp(&sh->p_full[t], p_seen++ & 1u, sh, P.wait_limit);
           if (!ok) break;
+          tc_after();
           if (elect()) {
+            if (j >= 0) {
+              const uint64_t vd = v_desc + uint64_t(vs * (kStageBytes >> 4));
+#pragma unroll
+              for (int k = 0; k < kTile / 16; ++k)
+                if (k < steps) mma_ts(o_at, s_at + k * 8, vd + k * (16 * kColBytes >> 4), id_o, j > 0 || k > 0);
+            }
+            if (j + 1 < n) {
+              const uint64_t kd = k_desc + uint64_t(ks * (kStageBytes >> 4));
+#pragma unroll
+              for (int k = 0; k < 4 * DH; ++k) {
+                const int off = ((k >> 2) * kHalfTileBytes + (k & 3) * 32) >> 4;
+                if (k < k_steps) mma_ss(s_at, qd + off, kd + off, id_s, k > 0);
+              }
+            }
+            tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
             if (j >= 0) tc_commit(&sh->kv_empty[vs]);
             if (j + 1 < n) tc_commit(&sh->kv_empty[ks]);
           }
@@ -546,8 +553,8 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
         if (ok) more = w.next(P);
       }
       // every product has ended before the tensor memory is given back
-      if (elect()) tc_commit(&sh->drain);
-      mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
+      if (elect()) tc_commit(&sh->drain[t]);
+      mbar_wait_bounded(&sh->drain[t], 0, kDrainLimit);
       __syncwarp();
     }
   } else {
@@ -712,15 +719,15 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
           tc_wait_st();
         }
         // V rows behind the end may hold anything, and 0 * NaN is NaN: those that
-        // share a step of 16 with valid rows are cleared
-        if (t == 0 && j == n - 1 && w.t1 == w.tiles) {
+        // share a step of 16 with valid rows are cleared (by either half, which write the same)
+        if (j == n - 1 && w.t1 == w.tiles) {
           const int valid = max(0, min(w.end - p0, kTile));
           const int upto = max(16, (valid + 15) / 16 * 16);
           if (valid < upto) {
             const uint32_t i = idx + v_load(j, n);
             ok = wait_warp(&sh->kv_full[i % kStages], (i / kStages) & 1u, sh, P.wait_limit);
             if (!ok) break;
-            const int r = valid + (tid >> 3);
+            const int r = valid + ((tid & 127) >> 3);
             if (r < upto)
 #pragma unroll
               for (int hf = 0; hf < DH; ++hf)

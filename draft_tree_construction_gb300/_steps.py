@@ -59,23 +59,28 @@ def declare(L):
 # A call's host work is a good part of a small call's time, so the checks here
 # decide on plain integers and only a failing one looks for its words.
 
-_HERE = contextlib.nullcontext()
-
-
 @contextlib.contextmanager
 def _elsewhere(dev, stream):
     with _on_device(dev):
         _stream_ptr(stream, dev)
-        with _torch().cuda.stream(stream) if stream is not None else _HERE:
+        with _torch().cuda.stream(stream) if stream is not None else contextlib.nullcontext():
             yield
 
 
-def _launching(dev, stream):
-    """Context of a call: the tensors' device, and the stream that it launches on,
-    so that what it allocates and clears itself is ordered with its kernels."""
+def _enter(dev, stream):
+    """Makes the tensors' device current, and the stream that the call launches
+    on, so that what the call allocates and clears itself is ordered with its
+    kernels.  Returns what _leave takes; None where nothing has to change."""
     if stream is None and dev.index == _torch().cuda.current_device():
-        return _HERE
-    return _elsewhere(dev, stream)
+        return None
+    scope = _elsewhere(dev, stream)
+    scope.__enter__()
+    return scope
+
+
+def _leave(scope):
+    if scope is not None:
+        scope.__exit__(None, None, None)
 
 
 def _stream(stream, dev):
@@ -183,12 +188,14 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
         if R not in (N, N + 1):
             raise DartError(f"a tree of {N} nodes needs {N} or {N + 1} rows of logits, got {R}")
         a.tokens, a.mask, a.N = tokens.data_ptr(), mask.data_ptr(), N
+    out_stride = 0
     if out is not None:
         _check_tensor(out, "out", logits.dtype, (B, R, V), contiguous=False)
         out_stride = _row_stride(out)
         if out.data_ptr() == logits.data_ptr() and out_stride != stride and B * R > 1:
             raise DartError("out shares its first element with logits, but not its rows")
-    with _launching(dev, stream):
+    scope = _enter(dev, stream)
+    try:
         if out is None:
             # rows that keep the input's alignment take whole vectors from end to end
             out_stride = V + (stride - V) % (16 // logits.element_size())
@@ -197,6 +204,8 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
                 out = out[..., :V]
         rc = lib().dart_logits_adjust(logits.data_ptr(), B, R, V, stride, code, C.byref(a), out.data_ptr(),
                                       out_stride, _stream(stream, dev))
+    finally:
+        _leave(scope)
     if rc:
         _check(rc, "dart_logits_adjust")
     return out
@@ -214,7 +223,8 @@ def _cache(k_cache, v_cache, pages, B):
         raise DartError("k_cache and v_cache must both be float16 or bfloat16")
     if pages.dim() != 2 or pages.shape[0] != B:
         raise DartError(f"pages must be [{B}, width]")
-    _check_tensor(pages, "pages", torch.int32, contiguous=False)
+    if pages.dtype != torch.int32:
+        _check_tensor(pages, "pages", torch.int32, contiguous=False)
     count, page, heads, dim = shape
     if page < 8 or page % 8:
         raise DartError(f"pages must hold a multiple of 8 positions, got {page}")
@@ -360,13 +370,17 @@ def kv_append(q, k, v, k_cache, v_cache, pages, lengths, starts, *, rotary: Rota
                 raise DartError("out shares its first element with q, but not its strides")
     elif out is not None or q_weight is not None:
         raise DartError("out or q_weight is given without q")
-    _check_tensor(offsets, "offsets", torch.int32, (T,))
-    _check_tensor(q_weight, "q_weight", dt, (dim,))
-    _check_tensor(k_weight, "k_weight", dt, (dim,))
+    if offsets is not None:
+        _check_tensor(offsets, "offsets", torch.int32, (T,))
+    for t, name in ((q_weight, "q_weight"), (k_weight, "k_weight")):
+        if t is not None and (t.dtype != dt or t.shape != (dim,) or t.stride(0) != 1):
+            _check_tensor(t, name, dt, (dim,))
     if rotary is not None and rotary.rot > dim:
         raise DartError(f"rotary turns {rotary.rot} elements of heads of {dim}")
-    _check_error_word(device_err)
-    with _launching(dev, stream):
+    if device_err is not None:
+        _check_error_word(device_err)
+    scope = _enter(dev, stream)
+    try:
         if q is not None and out is None:
             out = torch.empty((T, Hq, dim), dtype=dt, device=dev)
             o0, o1 = Hq * dim, dim
@@ -374,6 +388,8 @@ def kv_append(q, k, v, k_cache, v_cache, pages, lengths, starts, *, rotary: Rota
                                   lengths.data_ptr(), starts.data_ptr(), _at(offsets),
                                   C.byref(rotary.desc) if rotary is not None else None, _at(q_weight), _at(k_weight),
                                   eps, C.byref(c), _at(out), o0, o1, _at(device_err), _stream(stream, dev))
+    finally:
+        _leave(scope)
     if rc:
         _check(rc, "dart_kv_append")
     return out
@@ -418,26 +434,34 @@ def tree_attention(q, k_cache, v_cache, pages, lengths, starts, *, mask=None, sc
             raise DartError(f"mask must be [{B}, N, ceil(N / 32)]")
         N = mask.shape[1]
         _check_tensor(mask, "mask", _mask_dtypes())
+    o0 = o1 = 0
     if out is not None:
         o0, o1 = _output(out, "out", T, Hq, dim, dt)
         if out.numel() and out.data_ptr() == q.data_ptr():
             raise DartError("out must not be q")
     L = lib()
     need = L.dart_attention_workspace_bytes(T, B, Hq, heads, dim)
+    room = 0
     if workspace is not None:
-        _check_workspace(workspace, need)
-    with _launching(dev, stream):
+        room = workspace.numel() * workspace.element_size()
+        if room < need or not workspace.is_contiguous():
+            _check_workspace(workspace, need)
+    sums = None
+    scope = _enter(dev, stream)
+    try:
         if out is None:
             out = torch.empty((T, Hq, dim), dtype=dt, device=dev)
             o0, o1 = Hq * dim, dim
         if workspace is None:
-            workspace = torch.empty(need, dtype=torch.uint8, device=dev)
+            workspace, room = torch.empty(need, dtype=torch.uint8, device=dev), need
             workspace[:256].zero_()
-        sums = torch.empty((T, Hq), dtype=torch.float32, device=dev) if lse else None
+        if lse:
+            sums = torch.empty((T, Hq), dtype=torch.float32, device=dev)
         rc = L.dart_tree_attention(q.data_ptr(), q0, q1, Hq, T, B, lengths.data_ptr(), starts.data_ptr(), _at(mask), N,
                                    dim ** -0.5 if scale is None else scale, C.byref(c), out.data_ptr(), o0, o1,
-                                   _at(sums), workspace.data_ptr(), workspace.numel() * workspace.element_size(),
-                                   _stream(stream, dev))
+                                   _at(sums), workspace.data_ptr(), room, _stream(stream, dev))
+    finally:
+        _leave(scope)
     if rc:
         _check(rc, "dart_tree_attention")
     return {"out": out, "lse": sums, "workspace": workspace}

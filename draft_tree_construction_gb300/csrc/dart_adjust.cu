@@ -9,7 +9,6 @@
 // written without being read.  The few elements that are counted or biased are
 // set afterwards, each by a lane that keeps its change in registers from row to
 // row: examining every vector for them cost more than the copy itself.
-#include <atomic>
 #include <cmath>
 
 #include "dart_launch.h"
@@ -574,17 +573,8 @@ adjust_kernel(const AdjustParams P) {
 
 template <typename T, bool ALIGNED>
 cudaError_t raise_limit() {
-  static std::atomic<uint64_t> ready{0};       // devices whose shared-memory limit is raised
-  int dev = 0;
-  cudaError_t e = cudaGetDevice(&dev);
-  if (e != cudaSuccess) return e;
-  const uint64_t bit = dev < 64 ? 1ull << dev : 0ull;
-  if (!bit || !(ready.load(std::memory_order_relaxed) & bit)) {
-    e = cudaFuncSetAttribute(adjust_kernel<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             4 * kSlice<T> + (ALIGNED ? kRingBytes : 0));
-    if (e == cudaSuccess) ready.fetch_or(bit, std::memory_order_relaxed);
-  }
-  return e;
+  return cudaFuncSetAttribute(adjust_kernel<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                              4 * kSlice<T> + (ALIGNED ? kRingBytes : 0));
 }
 
 template <typename T>

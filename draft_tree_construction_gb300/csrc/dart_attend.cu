@@ -51,6 +51,7 @@ constexpr float kRescale = 8.f;         // growth of the maximum (in log2) that 
 constexpr uint32_t kTmemCols = 512;     // S0 | S1 | O0 | O1
 constexpr uint32_t kProducers = 2;      // warps 8 and 11, which take the loads in turn
 constexpr long long kDrainLimit = 1ll << 31;
+constexpr long long kProbeCycles = 1ll << 20;
 
 struct AttendParams {
   const void* q;
@@ -277,11 +278,13 @@ struct Shared {
   int dead;                        // a wait ran out: everyone leaves
 };
 
-// Bounded wait of a whole warp; false (for all lanes) once any wait of the CTA ran out.
+// Bounded wait of a whole warp; false (for all lanes) once any wait of the CTA ran
+// out.  A probe may suspend the thread for some microseconds, so a limit below
+// that (a test of this path) is kept by probes that do not.
 __device__ __forceinline__ bool wait_lane(uint64_t* bar, uint32_t parity, Shared* sh, long long limit) {
-  if (mbar_try_wait(bar, parity)) return true;
+  if (mbar_test_wait(bar, parity)) return true;
   const long long t0 = clock64();
-  while (!mbar_try_wait(bar, parity)) {
+  while (!(limit < kProbeCycles ? mbar_test_wait(bar, parity) : mbar_try_wait(bar, parity))) {
     if (*reinterpret_cast<volatile int*>(&sh->dead)) return false;
     if (clock64() - t0 > limit) {
       *reinterpret_cast<volatile int*>(&sh->dead) = 1;

@@ -93,7 +93,7 @@ def close(got, want, bound, dtype, extra=0.0):
     Below the smallest normal number (finfo.tiny) the type's steps stop
     shrinking: they are all tiny * eps wide (fp16: 2^-14 * 2^-10 = 2^-24), so
     half a step there is tiny * eps / 2 however small the value."""
-    g, w = got.double().cpu(), want
+    g, w, bound = got.double().cpu(), want.cpu(), bound.cpu()
     finite = torch.isfinite(w)
     assert torch.equal(torch.isnan(g), torch.isnan(w))
     assert torch.equal(g[~finite & ~torch.isnan(w)], w[~finite & ~torch.isnan(w)])
@@ -151,7 +151,7 @@ def visible(len_, n, N, i, mask_row):
     return see
 
 
-def attend(q, k_cache, v_cache, pages, lengths, starts, mask, scale):
+def attend(q, k_cache, v_cache, pages, lengths, starts, mask, scale, device="cpu"):
     """(out, lse, bound on out, bound on lse), float64, for the rows inside sequences; NaN elsewhere.
 
     A score is a sum of D products accumulated in fp32 with at most 2 u each
@@ -164,42 +164,46 @@ def attend(q, k_cache, v_cache, pages, lengths, starts, mask, scale):
     _, page, Hkv, _ = k_cache.shape
     G = Hq // Hkv
     dt = q.dtype
-    out = torch.full((T, Hq, D), math.nan, dtype=torch.float64)
-    bound = torch.zeros((T, Hq, D), dtype=torch.float64)
-    lse = torch.full((T, Hq), math.nan, dtype=torch.float64)
-    lse_bound = torch.zeros((T, Hq), dtype=torch.float64)
+    new = lambda *shape, fill=0.0: torch.full(shape, fill, dtype=torch.float64, device=device)
+    out, bound = new(T, Hq, D, fill=math.nan), new(T, Hq, D)
+    lse, lse_bound = new(T, Hq, fill=math.nan), new(T, Hq)
+    q, k_cache, v_cache = q.to(device), k_cache.to(device), v_cache.to(device)
     N = mask.shape[1] if mask is not None else 0
     for b in range(len(lengths)):
-        len_, n = int(lengths[b]), int(starts[b + 1] - starts[b])
+        len_, n, at = int(lengths[b]), int(starts[b + 1] - starts[b]), int(starts[b])
         S = len_ + n
         if n == 0:
             continue
         pos = torch.arange(S)
         rows = torch.as_tensor(pages[b]).long()[pos // page]
-        k, v = k_cache[rows, pos % page].double(), v_cache[rows, pos % page].double()      # [S, Hkv, D]
-        for i in range(n):
-            t = int(starts[b]) + i
-            lead = max(n - N, 0)
-            see = torch.from_numpy(visible(len_, n, N, i, mask[b, i - lead] if i >= lead else None))
-            if not see.any():
-                out[t], lse[t] = 0.0, -math.inf
-                continue
-            qq = q[t].double().view(Hkv, G, D)
-            kk, vv = k[see], v[see]
-            s = torch.einsum("hgd,shd->hgs", qq, kk) * scale
-            size = torch.einsum("hgd,shd->hgs", qq.abs(), kk.abs()).amax(-1) * abs(scale)
-            top = s.amax(-1, keepdim=True)
-            w = torch.exp(s - top)
-            l = w.sum(-1, keepdim=True)
-            p = w / l
-            out[t] = torch.einsum("hgs,shd->hgd", p, vv).reshape(Hq, D)
-            lse[t] = (top + torch.log(l)).reshape(Hq)
-            reach = torch.einsum("hgs,shd->hgd", p, vv.abs())
-            delta = 2 * D * U * size + 2.0 ** -20 + 8 * U * (top - s.amin(-1, keepdim=True)).amax(-1)
-            terms = 2 * int(see.sum()) * U
-            eb = (half_step(dt) + 2 * delta + 2 * terms)[..., None] * reach
-            if dt == torch.float16:
-                eb = eb + int(see.sum()) * 2.0 ** -25 * vv.abs().amax()
-            bound[t] = eb.reshape(Hq, D)
-            lse_bound[t] = (delta + terms + 2.0 ** -20 + 4 * U * lse[t].view(Hkv, G).abs()).reshape(Hq)
+        where = (rows.to(device), (pos % page).to(device))
+        k = k_cache[where].double().transpose(0, 1)                    # [Hkv, S, D]
+        v = v_cache[where].double().transpose(0, 1)
+        lead = max(n - N, 0)
+        see = np.stack([visible(len_, n, N, i, mask[b, i - lead] if i >= lead else None) for i in range(n)])
+        see = torch.from_numpy(see).to(device)                         # [n, S]
+        qq = q[at:at + n].double().view(n, Hkv, G, D).permute(1, 0, 2, 3).reshape(Hkv, n * G, D)
+        wide = see[None, :, None, :].expand(Hkv, n, G, S).reshape(Hkv, n * G, S)
+        s = (qq @ k.transpose(1, 2) * scale).masked_fill(~wide, -math.inf)
+        size = (qq.abs() @ k.abs().transpose(1, 2) * abs(scale)).masked_fill(~wide, 0.0).amax(-1, keepdim=True)
+        low = s.masked_fill(~wide, math.inf).amin(-1, keepdim=True)
+        top = s.amax(-1, keepdim=True)
+        some = wide.any(-1, keepdim=True)
+        top, low = top.masked_fill(~some, 0.0), low.masked_fill(~some, 0.0)
+        w = torch.exp(s - top)
+        l = w.sum(-1, keepdim=True)
+        p = w / l.clamp_min(1e-300)
+        count = see.sum(-1).double()[None, :, None, None].expand(Hkv, n, G, 1).reshape(Hkv, n * G, 1)
+        delta = 2 * D * U * size + 2.0 ** -20 + 8 * U * (top - low)
+        terms = 2 * U * count
+        reach = p @ v.abs()
+        eb = (half_step(dt) + 2 * delta + 2 * terms) * reach
+        if dt == torch.float16:
+            eb = eb + count * 2.0 ** -25 * v.abs().amax()
+        back = lambda x: x.view(Hkv, n, G, -1).permute(1, 0, 2, 3).reshape(n, Hq, -1)
+        out[at:at + n], bound[at:at + n] = back(p @ v), back(eb)
+        sums = (top + torch.log(l)).masked_fill(~some, -math.inf)
+        lse[at:at + n] = back(sums)[..., 0]
+        lb = delta + terms + 2.0 ** -20 + 4 * U * torch.nan_to_num(sums, neginf=0.0).abs()
+        lse_bound[at:at + n] = back(lb)[..., 0]
     return out, lse, bound, lse_bound

@@ -186,6 +186,50 @@ def test_same_bits_every_time_on_any_stream_and_in_graphs(D):
     assert D.device_error(ws) == 0
 
 
+@pytest.mark.parametrize("dtype,B,ctx,n,Hq,Hkv,dim,page,N", [
+    ("bf16", 24, 1500, 79, 32, 8, 128, 16, 78),       # blocks of 256 rows and blocks of 60 in turn, many per CTA
+    ("f16", 40, 900, 33, 28, 4, 64, 32, 32),          # 231 rows a head; ten stages
+    ("bf16", 3, 2500, 700, 16, 2, 96, 64, 0),         # causal blocks of growing length
+    ("f16", 450, 60, 1, 16, 2, 128, 16, 0),           # more sequences than threads
+    ("bf16", 450, 300, 5, 8, 8, 64, 24, 4),
+    ("bf16", 1, 60000, 1, 8, 1, 128, 128, 0),         # one block over every CTA
+])
+def test_many_blocks_per_cta(D, dtype, B, ctx, n, Hq, Hkv, dim, page, N):
+    """Enough work that each CTA walks through several blocks, of one half and of two, and joins at both ends."""
+    rng = np.random.default_rng(B)
+    lengths = [int(x) for x in rng.integers(ctx // 2, ctx + 1, B)]
+    s = _case(dtype, lengths, [n] * B, Hq, Hkv, dim, page, N, seed=B)
+    d = _cuda(s)
+    got = D.tree_attention(*_args(d), mask=d["mask"], lse=True)
+    assert D.device_error(got["workspace"]) == 0
+    want, lse, bound, lse_bound = refs.attend(s["q"], s["k_cache"], s["v_cache"], s["pages"], s["lengths"],
+                                              s["starts"], s["mask"], dim ** -0.5, device="cuda")
+    refs.close(got["out"], want, bound, s["q"].dtype)
+    refs.close(got["lse"], lse, lse_bound, torch.float32)
+    for _ in range(3):
+        again = D.tree_attention(*_args(d), mask=d["mask"], workspace=got["workspace"])
+        assert torch.equal(again["out"], got["out"])
+
+
+def test_a_wait_that_runs_out_is_reported(D):
+    """A limit of 64 cycles ends every wait on memory: the call returns, says so, and the next one is right."""
+    s = _case("bf16", [3000, 700], [40, 1], 8, 2, 128, 64, seed=11)
+    d = _cuda(s)
+    ws = torch.zeros(D.attention_workspace_bytes(41, 2, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    want = D.tree_attention(*_args(d), workspace=ws)["out"]
+    flush = torch.ones(64 << 20, dtype=torch.float32, device="cuda")
+    D.set_wait_limit(64)
+    try:
+        flush.mul_(1.0)
+        D.tree_attention(*_args(d), workspace=ws)
+        flags = D.device_error(ws)
+    finally:
+        D.set_wait_limit(0)
+    assert flags & 1, flags
+    assert torch.equal(D.tree_attention(*_args(d), workspace=ws)["out"], want)
+    assert D.device_error(ws) == 0
+
+
 def test_empty_calls(D):
     s = _case("f16", [5], [0], 2, 1, 64, 8, seed=9)
     d = _cuda(s)

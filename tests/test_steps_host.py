@@ -152,9 +152,9 @@ def on_cpu(monkeypatch):
     """CPU tensors pass the device check; reaching the library is a failure."""
     monkeypatch.setattr(_steps, "_one_device", lambda names, tensors: torch.device("cuda", 0))
 
-    def reached(*a, **k):
+    def reached(dev, stream):
         raise AssertionError("the checks let this call through")
-    monkeypatch.setattr(_steps, "_launching", reached)
+    monkeypatch.setattr(_steps, "_enter", reached)
 
 
 def test_host_tensors_are_refused():

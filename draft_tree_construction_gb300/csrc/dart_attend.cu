@@ -63,8 +63,9 @@ struct AttendParams {
   const int32_t* lengths;
   const int32_t* starts;
   const uint32_t* mask;
-  float c;                    // |scale| log2 e (1 for scale 0, the queries being zeroed then)
-  uint32_t q_and, q_xor;      // query bits: sign flipped for a negative scale, all cleared for scale 0
+  float c;                    // |scale| log2 e (next to nothing for scale 0, so that -inf stays -inf)
+  uint32_t negate;            // the products of Q and K change their sign: the scale is negative
+  bool wide_out;              // 32-byte stores
   const int32_t* table;
   long long table_stride;
   long long cap;              // positions a sequence's pages can hold
@@ -176,6 +177,18 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
   uint32_t w;
   memcpy(&w, &h, 4);
   return w;
+}
+
+// 32 bytes (32-byte aligned) in one store.
+__device__ __forceinline__ void stg_v8(void* p, const uint32_t* r) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "l"(p), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
+// 16 bytes from memory (or zeros) to shared memory, without a register.
+__device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool copy) {
+  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
+               :: "r"(smem_u32(dst)), "l"(src), "r"(copy ? 16u : 0u) : "memory");
 }
 
 // Operand type in the instruction descriptor.
@@ -543,7 +556,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
 #pragma unroll
               for (int k = 0; k < 4 * DH; ++k) {
                 const int off = ((k >> 2) * kHalfTileBytes + (k & 3) * 32) >> 4;
-                if (k < k_steps) mma_ss(s_at, qd + off, kd + off, id_s, k > 0);
+                if (k < k_steps) mma_ss(s_at, qd + off, kd + off, id_s | P.negate, k > 0);
               }
             }
             tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
@@ -580,49 +593,36 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
         more = w.next(P);
       }
     };
-    // this warp's 32 rows of the block's queries, swizzled
+    // This warp's 32 rows of the block's queries, swizzled, copied without
+    // registers as soon as the buffer is free; give_q hands them to the products.
     constexpr int kChunks = 8 * DH, kPer = 32 / kChunks, kSteps = 32 / kPer;   // 16-byte chunks a row, rows a step
     const int chunk = lane % kChunks, sub = lane / kChunks, warp_row = (warp & 3) * 32;
-    auto place = [&](int r) {
-      return q_half + (chunk >> 3) * kHalfTileBytes + r * kColBytes + (((chunk & 7) ^ (r & 7)) << 4);
-    };
-    auto query = [&](int rr) {           // row rr of the block
-      const int g = w.blk * kBlockRows + rr, token = P.by_group.div(g);
-      return static_cast<const T*>(P.q) + (long long)(w.c.start + token) * P.q_ts +
-             (long long)(w.h * P.G + g - token * P.G) * P.q_hs;
-    };
-    auto load_q = [&]() {
-      uint4 x[kSteps];
-#pragma unroll
+    auto ask_q = [&]() {
+#pragma unroll 4
       for (int u = 0; u < kSteps; ++u) {
-        const int rr = t * kHalfRows + warp_row + u * kPer + sub;
-        x[u] = make_uint4(0, 0, 0, 0);
-        if (rr < w.rows && 8 * chunk < P.D) x[u] = *reinterpret_cast<const uint4*>(query(rr) + 8 * chunk);
+        const int r = warp_row + u * kPer + sub, rr = t * kHalfRows + r;
+        if (rr < w.rows) {
+          const int g = w.blk * kBlockRows + rr, token = P.by_group.div(g);
+          const T* src = static_cast<const T*>(P.q) + (long long)(w.c.start + token) * P.q_ts +
+                         (long long)(w.h * P.G + g - token * P.G) * P.q_hs;
+          cp_async16_or_zero(q_half + (chunk >> 3) * kHalfTileBytes + r * kColBytes + (((chunk & 7) ^ (r & 7)) << 4),
+                             src + (8 * chunk < P.D ? 8 * chunk : 0), 8 * chunk < P.D);
+        }
       }
-#pragma unroll
-      for (int u = 0; u < kSteps; ++u) {
-        x[u].x = (x[u].x & P.q_and) ^ P.q_xor;
-        x[u].y = (x[u].y & P.q_and) ^ P.q_xor;
-        x[u].z = (x[u].z & P.q_and) ^ P.q_xor;
-        x[u].w = (x[u].w & P.q_and) ^ P.q_xor;
-        *reinterpret_cast<uint4*>(place(warp_row + u * kPer + sub)) = x[u];
-      }
+      cp_async_commit();
+    };
+    auto give_q = [&]() {
+      cp_async_wait<0>();
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_full[t]);
     };
-    // a row per lane: the next block's queries come to L2 while this one is finished
-    auto prefetch_q = [&]() {
-      const int rr = t * kHalfRows + warp_row + lane;
-      if (rr < w.rows) {
-        const T* src = query(rr);
-        asm volatile("prefetch.global.L2 [%0];" :: "l"(src));
-        if (P.D > 64) asm volatile("prefetch.global.L2 [%0];" :: "l"(src + 64));
-      }
-    };
 
     skip_inactive();
-    if (more) load_q();
+    if (more) {
+      ask_q();
+      give_q();
+    }
     bool ok = true;
     while (more && ok) {
       const int n = w.t1 - w.t0;
@@ -751,44 +751,43 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       const int d_after = w.tiles - w.t1;                // the block's tiles in later CTAs
       more = w.next(P);
       skip_inactive();
-      if (more) prefetch_q();
+      if (more) ask_q();
       ok = wait_warp(&sh->o_full[t], o_seen++ & 1u, sh, P.wait_limit);
       if (!ok) break;
       tc_after();
       if (d_t0 == 0 && d_after == 0) {
-        // through the query buffer (its products have ended), so that rows leave in whole lines
+        // A thread's row leaves 32 (or 16) bytes at a time: whole sectors, and
+        // nothing to wait for.  (Through shared memory the rows would leave in
+        // whole lines, but the next queries would have to wait for the buffer.)
         const float inv = l > 0.f ? 1.f / l : 0.f;
         if (warp_on) {
+          const long long tok = d_start + token;
+          const int head = d_h * P.G + g - token * P.G;
+          T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
 #pragma unroll
           for (int i = 0; i < kCols / 32; ++i) {
             float o[32];
             tmem_ld32(to + 32 * i, o);
             loaded<32>(o);
+            uint32_t y[16];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-              const float* x = o + 8 * k;
-              *reinterpret_cast<uint4*>(q_half + (i >> 1) * kHalfTileBytes + row * kColBytes +
-                                        (((((i & 1) << 2) + k) ^ (row & 7)) << 4)) =
-                  make_uint4(pack2<T>(x[0] * inv, x[1] * inv), pack2<T>(x[2] * inv, x[3] * inv),
-                             pack2<T>(x[4] * inv, x[5] * inv), pack2<T>(x[6] * inv, x[7] * inv));
-            }
-          }
-          if (row_on && P.lse)
-            P.lse[(long long)(d_start + token) * P.Hq + d_h * P.G + g - token * P.G] =
-                l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-          __syncwarp();
+            for (int k = 0; k < 16; ++k) y[k] = pack2<T>(o[2 * k] * inv, o[2 * k + 1] * inv);
 #pragma unroll
-          for (int u = 0; u < kSteps; ++u) {
-            const int r = warp_row + u * kPer + sub, rr = t * kHalfRows + r;
-            if (rr < d_rows && 8 * chunk < P.D) {
-              const int gg = d_row0 + rr;
-              const int tok = P.by_group.div(gg), head = d_h * P.G + gg - tok * P.G;
-              *reinterpret_cast<uint4*>(static_cast<T*>(P.out) + (long long)(d_start + tok) * P.o_ts +
-                                        (long long)head * P.o_hs + 8 * chunk) =
-                  *reinterpret_cast<const uint4*>(place(r));
+            for (int k = 0; k < 2; ++k) {
+              T* to_row = dst + 32 * i + 16 * k;
+              if (P.wide_out) {
+                if (row_on && 32 * i + 16 * k < P.D) stg_v8(to_row, y + 8 * k);
+              } else {
+                if (row_on && 32 * i + 16 * k < P.D)
+                  *reinterpret_cast<uint4*>(to_row) = make_uint4(y[8 * k], y[8 * k + 1], y[8 * k + 2], y[8 * k + 3]);
+                if (row_on && 32 * i + 16 * k + 8 < P.D)
+                  *reinterpret_cast<uint4*>(to_row + 8) =
+                      make_uint4(y[8 * k + 4], y[8 * k + 5], y[8 * k + 6], y[8 * k + 7]);
+              }
             }
+            if (i == 0 && more) give_q();
           }
-          __syncwarp();
+          if (row_on && P.lse) P.lse[tok * P.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
         }
       } else if (warp_on) {
         // [4 columns][row] so that a warp writes whole lines, then (m, l) of each row
@@ -802,10 +801,11 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
           for (int k = 0; k < 8; ++k)
             if (row_on)
               dst[(8 * i + k) * P.slot_rows + my_row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
+          if (i == 0 && more) give_q();
         }
         if (row_on) reinterpret_cast<float2*>(dst + kCols / 4 * P.slot_rows)[my_row] = make_float2(m, l);
       }
-      if (more) load_q();
+      if (!warp_on && more) give_q();
       if (t == 0 && warp == 0 && lane == 0 && d_t0 == 0 && d_after > 0) {
         // the span ends within the block: the joint names it and the CTAs that share it
         const Span& sp = sh->span;
@@ -1020,9 +1020,10 @@ extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_
   P.Hq = q_heads; P.Hkv = c.heads; P.G = q_heads / c.heads; P.D = c.dim;
   P.T = T; P.B = B; P.N = N; P.MW = (N + 31) / 32;
   P.lengths = lengths; P.starts = starts; P.mask = mask;
-  P.c = scale == 0.f ? 1.f : std::fabs(scale) * 1.44269504088896341f;
-  P.q_and = scale == 0.f ? 0u : kFull;
-  P.q_xor = scale < 0.f ? 0x80008000u : 0u;
+  P.c = scale == 0.f ? 1e-30f : std::fabs(scale) * 1.44269504088896341f;
+  P.negate = scale < 0.f ? 1u << 13 : 0u;
+  P.wide_out = c.dim % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0 &&
+               ((out_token_stride | out_head_stride) & 15) == 0;
   P.table = c.table; P.table_stride = c.table_stride;
   P.cap = (long long)c.table_width * c.page;
   P.by_group = fast_div(uint32_t(P.G));

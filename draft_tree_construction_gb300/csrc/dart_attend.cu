@@ -179,6 +179,11 @@ template <> __device__ __forceinline__ uint32_t pack2<__nv_bfloat16>(float a, fl
   return w;
 }
 
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
 // 32 bytes (32-byte aligned) in one store.
 __device__ __forceinline__ void stg_v8(void* p, const uint32_t* r) {
   asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
@@ -677,7 +682,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
           for (int k = 4; k < kTile; k += 8) {
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-              top[i] = k + 4 + i < kTile ? fmaxf(top[i], fmaxf(s[k + i], s[k + 4 + i])) : fmaxf(top[i], s[k + i]);
+              top[i] = k + 4 + i < kTile ? max3(top[i], s[k + i], s[k + 4 + i]) : fmaxf(top[i], s[k + i]);
           }
           float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
           mx *= P.c;

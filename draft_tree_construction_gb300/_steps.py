@@ -96,12 +96,13 @@ def _at(t):
 
 def _one_device(names, tensors):
     """The one CUDA device of the tensors that are given."""
-    dev = tensors[0].device
-    for t in tensors:
-        if t is not None and (t.device != dev or not t.is_cuda):
-            break
-    else:
-        return dev
+    index = tensors[0].get_device()
+    if index >= 0:
+        for t in tensors:
+            if t is not None and t.get_device() != index:
+                break
+        else:
+            return tensors[0].device
     return _device_of(*zip(names, tensors))
 
 
@@ -221,37 +222,38 @@ def _cache(k_cache, v_cache, pages, B):
         raise DartError("k_cache and v_cache must both be [pages, page, heads, dim]")
     if dt not in (torch.float16, torch.bfloat16) or v_cache.dtype != dt:
         raise DartError("k_cache and v_cache must both be float16 or bfloat16")
-    if pages.dim() != 2 or pages.shape[0] != B:
+    table, (width, step) = pages.shape, (pages.shape[-1], pages.stride(0) if pages.dim() == 2 else 0)
+    if len(table) != 2 or table[0] != B:
         raise DartError(f"pages must be [{B}, width]")
     if pages.dtype != torch.int32:
         _check_tensor(pages, "pages", torch.int32, contiguous=False)
-    count, page, heads, dim = shape
-    if page < 8 or page % 8:
-        raise DartError(f"pages must hold a multiple of 8 positions, got {page}")
-    if not 8 <= dim <= 128 or dim % 8:
-        raise DartError(f"heads must have a multiple of 8 elements, 8 to 128, got {dim}")
-    strides = []
-    for t, x in ((k_cache, "k"), (v_cache, "v")):
-        # a dimension of one is never stepped along
-        st = t.stride()
-        a, b, c = st[0] if count > 1 else 0, st[1], st[2] if heads > 1 else 0
-        if st[3] != 1:
-            raise DartError(f"{x}_cache must have unit stride in its last dimension")
-        if (a | b | c) & 7 or t.data_ptr() & 15:
-            raise DartError(f"{x}_cache must be 16-byte aligned, with strides of multiples of 8 elements")
-        # memory shared between elements (an expanded tensor) cannot be written
-        if b == 0 or (a == 0 and count > 1) or (c == 0 and heads > 1):
-            raise DartError(f"{x}_cache must not be an expanded tensor")
-        strides += (a, b, c)
-    width, step = pages.shape[1], pages.stride(0)
     if width > 1 and pages.stride(1) != 1:
         raise DartError("pages must have unit stride in its last dimension")
     if B <= 1:
         step = width
     elif step < width:
         raise DartError("the rows of pages overlap")
-    return _Cache(k_cache.data_ptr(), v_cache.data_ptr(), *strides, pages.data_ptr(), step, width, count, page, heads,
-                  dim, _codes()[dt])
+    count, page, heads, dim = shape
+    if page < 8 or page & 7:
+        raise DartError(f"pages must hold a multiple of 8 positions, got {page}")
+    if not 8 <= dim <= 128 or dim & 7:
+        raise DartError(f"heads must have a multiple of 8 elements, 8 to 128, got {dim}")
+    k0, k1, k2, k3 = k_cache.stride()
+    v0, v1, v2, v3 = v_cache.stride()
+    if k3 != 1 or v3 != 1:
+        raise DartError("k_cache and v_cache must have unit stride in their last dimension")
+    if count <= 1:                  # a dimension of one is never stepped along
+        k0 = v0 = 8
+    if heads == 1:
+        k2 = v2 = 8
+    at, vat = k_cache.data_ptr(), v_cache.data_ptr()
+    if (k0 | k1 | k2 | v0 | v1 | v2) & 7 or (at | vat) & 15:
+        raise DartError("k_cache and v_cache must be 16-byte aligned, with strides of multiples of 8 elements")
+    if not (k0 and k1 and k2 and v0 and v1 and v2):
+        # memory shared between elements (an expanded tensor) cannot be written
+        raise DartError("k_cache and v_cache must not be expanded tensors")
+    return _Cache(at, vat, k0, k1, k2, v0, v1, v2, pages.data_ptr(), step, width, count, page, heads, dim,
+                  _codes()[dt])
 
 
 def _heads(t, name, T, heads, dim, dtype):

@@ -643,8 +643,8 @@ def tree_select(tokens, parents, pos, scores, M: int, *, device_err=None, stream
 
 
 def set_wait_limit(cycles: int) -> None:
-    """SM clock cycles any one wait of the row pass may take before it gives up
-    (<= 0 restores the default of about two seconds).  For tests of the timeout
+    """SM clock cycles any one wait of the row pass or of tree_attention may take
+    before it gives up (<= 0 restores the default of about two seconds).  For tests of the timeout
     path."""
     lib().dart_set_wait_limit(int(cycles))
 

@@ -1,14 +1,29 @@
 // dart_adjust.cu -- K5: penalties for repeated tokens, biases and grammar
 // masks on logits, in one pass from the input rows to the output rows.
 //
-// What a row needs beyond its own elements is small and shared: how often each
-// token occurs in the sequence's history, and the summed bias of each token.
-// So a CTA owns a slice of the vocabulary of one sequence, counts the history
-// and sums the biases of that slice in shared memory once, and then copies that
-// slice of its rows, whole vectors at a time; a vector that the grammar bans is
+// Mathematics: x = z;  if counted: x = z (1 / r or r) - f cnt - p;  x += bias;
+// -inf where the grammar bans the token; fp32, rounded once.
+//
+// What bounds it: memory, one read of the logits that are kept and one write of
+// all.  What a row needs beyond its own elements is small and shared: how often
+// each token occurs in the sequence's history, and the summed bias of each
+// token.  So a CTA owns a slice of the vocabulary of one sequence, counts the
+// history and sums the biases of that slice in shared memory once, and then
+// copies that slice of its rows, whole vectors at a time, through a ring of
+// shared-memory rows that cp.async fills ahead; a vector that the grammar bans is
 // written without being read.  The few elements that are counted or biased are
-// set afterwards, each by a lane that keeps its change in registers from row to
-// row: examining every vector for them cost more than the copy itself.
+// changed in the ring, each by a lane that keeps its change in registers from
+// row to row.
+//
+// Measured (GB300, bf16, kernel alone):
+//   64 x 8 rows of 151936, 2048 tokens of history, 300 biases   58 us, 5.4 TB/s
+//   4 trees of 497 rows of 151936, 4096 tokens, one mask each  212 us, 5.4 TB/s
+//   256 x 8 rows of 32000 (fp16), masks that keep 2% of a row   56 us: 2.5 TB/s
+//     of what has to move, 3.5 TB/s of what does, since a kept logit brings its
+//     128-byte line
+//   8 rows of 151936 of one sequence                            4.4 us
+// Looking into every vector for touched elements instead took 99 and 359 us for
+// the first two, registers in place of the ring 73 and 245 us.
 #include <cmath>
 
 #include "dart_launch.h"
@@ -19,9 +34,10 @@ namespace {
 constexpr int kAdjThreads = 256;
 constexpr int kAdjWarps = kAdjThreads / 32;
 constexpr int kAdjVecs = 4;                                // 16-byte vectors a lane takes of a row
-constexpr int kSparse = 24;                                // touched tokens of a block that are set one by one
+constexpr int kSparse = 24;                                // touched tokens of a block that are set one by one (8: 82
+                                                           // for 77 us with 16384 tokens of history, 209 for 212 with 4096)
 constexpr int kFix = kSparse * kAdjVecs / 32;              // ... and those of a warp's blocks, per lane
-constexpr int kDepth = 3;                                  // rows under way per warp
+constexpr int kDepth = 3;                                  // rows under way per warp (2: 62 us for 58; 4 leave one CTA an SM: 80)
 constexpr int kRingBytes = kDepth * kAdjWarps * kAdjVecs * 512;
 constexpr int kMaxBias = 1024;                             // biases per sequence
 constexpr int kCountBits = 21;                             // a token's count: history and path
@@ -69,14 +85,8 @@ union Vec {
   T e[16 / sizeof(T)];
 };
 
-// Logits pass through once: keep them out of the way of what is used again.
-// The load is predicated and leaves v alone otherwise, so that no register is
-// copied (and nothing waits) between the load and the use.
-__device__ __forceinline__ void ldg_stream(uint4& v, const void* p, bool on) {
-  asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %5, 0;\n\t"
-               "@p ld.global.L1::no_allocate.v4.u32 {%0,%1,%2,%3}, [%4];\n\t}"
-               : "+r"(v.x), "+r"(v.y), "+r"(v.z), "+r"(v.w) : "l"(p), "r"(uint32_t(on)) : "memory");
-}
+// Predicated loads that leave v alone otherwise, so that no register is copied
+// (and nothing waits) between the load and the use.
 __device__ __forceinline__ void ldg_word(uint32_t& v, const void* p, bool on) {
   asm volatile("{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %2, 0;\n\t@p ld.global.u32 %0, [%1];\n\t}"
                : "+r"(v) : "l"(p), "r"(uint32_t(on)) : "memory");
@@ -101,6 +111,7 @@ __device__ __forceinline__ T elem_of(uint32_t v) {
   memcpy(&x, &v, sizeof(T));
   return x;
 }
+// Logits pass through once: keep them out of the way of what is used again.
 __device__ __forceinline__ void stg_stream(void* p, uint4 v) {
   asm volatile("st.global.L1::no_allocate.v4.u32 [%0], {%1,%2,%3,%4};"
                :: "l"(p), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
@@ -123,23 +134,28 @@ __device__ __forceinline__ uint4 ban(uint4 u, uint4 m) {
                     (u.w & m.w) | (kInf & ~m.w));
 }
 
-// ALIGNED: every row begins on a 16-byte boundary, in and out.
-template <typename T, bool ALIGNED>
+// How the rows lie: every one begins on a 16-byte boundary, in and out; every
+// one is as far from such a boundary in as it is out; or neither, and elements
+// are taken one by one.  64 x 8 rows of 151936 with biases: 58 us aligned, 71 us
+// shifted (an odd row length), 320 us one by one.
+enum Rows { kAligned, kShifted, kSingle };
+template <typename T, int ROWS>
 __global__ void __launch_bounds__(kAdjThreads, 2)
 adjust_kernel(const AdjustParams P) {
   constexpr int E = 16 / int(sizeof(T));
   constexpr int kBlk = kBlock<T>, kCta = kSlice<T>, kWords = kCta / 32;
   constexpr uint32_t kAll = (1u << E) - 1u;
+  constexpr bool kRing = ROWS != kSingle;
   // the ring: kDepth rows of each warp's vectors, on their way from memory or worked on
   extern __shared__ __align__(16) unsigned char smem[];
   // a place's word: 1 + its index in the bias list (0: not biased), and how often its token is counted
-  uint32_t* counts = reinterpret_cast<uint32_t*>(smem + (ALIGNED ? kRingBytes : 0));    // [kCta], with penalties or biases
+  uint32_t* counts = reinterpret_cast<uint32_t*>(smem + (kRing ? kRingBytes : 0));    // [kCta], with penalties or biases
   __shared__ uint32_t touched[kWords];             // place is counted or biased
   __shared__ uint32_t on_path[kWords];             // place's token is on the present row's path
   __shared__ int32_t list_id[kMaxBias];            // the slice's biases, in their order
   __shared__ float list_val[kMaxBias];             // ... the first entry of an id holding the id's sum
   __shared__ uint16_t list_own[kAdjWarps][32 * kFix];      // each warp's touched places in blocks that have few
-  __shared__ uint32_t row_ok[ALIGNED ? kDepth : 1][kAdjThreads];      // grammar bits of the rows in the ring
+  __shared__ uint32_t row_ok[kRing ? kDepth : 1][kAdjThreads];      // grammar bits of the rows in the ring
   __shared__ uint4 spread[1 << E];                 // the mask of a vector whose elements are the bits of the index
   __shared__ int16_t toks[kMaxN];                  // the places of the tree's tokens, -1 outside the slice
   __shared__ int32_t warp_n[kMaxBias / kAdjThreads][kAdjWarps];
@@ -164,35 +180,48 @@ adjust_kernel(const AdjustParams P) {
   const uint32_t* allow =
       a.allowed ? a.allowed + (long long)b * a.allowed_seq_stride + (long long)r_begin * a.allowed_row_stride : nullptr;
 
-  // Aligned rows: a lane's vectors lie `step` tokens apart, from v0 on; the
-  // first `nv` of them are whole.  Rows pass through the ring: copied there
-  // kDepth - 1 rows ahead (but for vectors that the grammar bans), changed
-  // there, written from there with the banned elements replaced.
+  // The ring: a lane's vectors lie `step` tokens apart, from v0 + head on, where
+  // `head` elements come before the first 16-byte boundary of each block of the
+  // row (0 for aligned rows; blocks are multiples of 16 bytes).  Rows are copied
+  // there kDepth - 1 rows ahead (but for vectors that the grammar bans), changed
+  // there, and written from there with the banned elements replaced.
   const int step = kAdjWarps * slices * kBlk, v0 = token(0) + lane * E;
   constexpr int kPlaceStep = kAdjWarps * kBlk, kRowBytes = kAdjWarps * kAdjVecs * 512;
-  const int shift = v0 & 7;                       // a vector of four shares its byte with its neighbour
   unsigned char* ring = smem + warp * (kAdjVecs * 512);            // + slot * kRowBytes
-  int nv = 0;
+  auto row_of = [&](int r) { return in + (long long)(r - r_begin) * P.in_stride; };
+  auto head_of = [&](int r) {
+    return ROWS == kAligned
+               ? 0
+               : int((16u - unsigned(reinterpret_cast<uintptr_t>(row_of(r)) & 15u)) & 15u) / int(sizeof(T));
+  };
+  auto whole = [&](int i, int head) { return head + (lane + 1) * E <= size(i); };
+  // grammar bits: asked for a row before the row's copy begins (a vector's bits
+  // lie in one byte, or in two if the rows are shifted)
+  uint32_t bits[kAdjVecs], more_bits[kAdjVecs];
 #pragma unroll
-  for (int i = 0; i < kAdjVecs; ++i) nv += v0 + i * step + E <= P.V ? 1 : 0;
-  // grammar bits: asked for a row before the row's copy begins (eight bits per vector)
-  uint32_t bits[kAdjVecs];
-#pragma unroll
-  for (int i = 0; i < kAdjVecs; ++i) bits[i] = kFull;
+  for (int i = 0; i < kAdjVecs; ++i) bits[i] = more_bits[i] = kFull;
+  const int mask_bytes = ((P.V + 31) >> 5) * 4;
   auto ask = [&](int r) {
-    const uint8_t* src =
-        reinterpret_cast<const uint8_t*>(allow + (long long)(r - r_begin) * a.allowed_row_stride) + (v0 >> 3);
+    const uint8_t* src = reinterpret_cast<const uint8_t*>(allow + (long long)(r - r_begin) * a.allowed_row_stride);
+    const int head = head_of(r), at = (v0 + head) >> 3;
 #pragma unroll
-    for (int i = 0; i < kAdjVecs; ++i) ldg_byte(bits[i], src + i * (step / 8), i < nv && r < r_end);
+    for (int i = 0; i < kAdjVecs; ++i) {
+      const bool on = r < r_end && whole(i, head);
+      ldg_byte(bits[i], src + at + i * (step / 8), on);
+      if (ROWS == kShifted)
+        ldg_byte(more_bits[i], src + at + i * (step / 8) + 1, on && at + i * (step / 8) + 1 < mask_bytes);
+    }
   };
   auto copy = [&](int r, int slot) {
     uint32_t ok = 0u;
-    const T* src = in + (long long)(r - r_begin) * P.in_stride + v0;
+    const int head = head_of(r);
+    const T* src = row_of(r) + v0 + head;
 #pragma unroll
     for (int i = 0; i < kAdjVecs; ++i) {
-      const uint32_t k = (bits[i] >> shift) & kAll;
+      const uint32_t two = ROWS == kShifted ? (bits[i] & 0xFFu) | (more_bits[i] << 8) : bits[i];
+      const uint32_t k = (two >> ((v0 + head) & 7)) & kAll;
       ok |= k << (8 * i);
-      cp_async16(ring + slot * kRowBytes + i * 512 + lane * 16, src + i * step, r < r_end && i < nv && k != 0u);
+      cp_async16(ring + slot * kRowBytes + i * 512 + lane * 16, src + i * step, r < r_end && whole(i, head) && k != 0u);
     }
     cp_async_commit();
     row_ok[slot][tid] = ok;
@@ -200,7 +229,7 @@ adjust_kernel(const AdjustParams P) {
   };
 
   // Everything that the slice needs from memory is asked for before anything waits.
-  if (ALIGNED && allow) ask(r_begin);
+  if (kRing && allow) ask(r_begin);
   constexpr int kAhead = 8, kBiasAhead = kMaxBias / kAdjThreads;
   const int32_t* hist = P.count && a.history ? a.history + (long long)b * a.history_stride : nullptr;
   const int width = hist ? a.history_width : 0;
@@ -220,7 +249,7 @@ adjust_kernel(const AdjustParams P) {
   const float freq = a.frequency ? a.frequency[b] : 0.f;
   const bool touching = P.count || a.bias_count > 0, paths = P.count && a.N > 0;
 
-  if constexpr (ALIGNED) {
+  if constexpr (kRing) {
 #pragma unroll
     for (int k = 0; k < kDepth - 1; ++k) copy(r_begin + k, k);
   }
@@ -359,93 +388,84 @@ adjust_kernel(const AdjustParams P) {
     return paths && r < r_end && node >= 0 && lane < MW ? a.mask[((long long)b * a.N + node) * MW + lane] & own_nodes
                                                          : 0u;
   };
-  // The tokens of a row's path join the counts and are marked: nothing sets a
-  // marked element until the row is copied; then each is set once, from `in`,
-  // which still holds it when the row is changed in place.
   auto each = [&](uint32_t path, auto&& f) {
     for (uint32_t m = path; m; m &= m - 1) f(int(toks[32 * lane + __ffs(m) - 1]));
     __syncwarp();
   };
+  // The tokens of a row's path join the counts and are marked, for the time of the row.
   auto path_in = [&](uint32_t path) {
     each(path, [&](int t) {
       atomicAdd(&counts[t], 1u);
       atomicOr(&on_path[t >> 5], 1u << (t & 31));
     });
   };
-  // a lane's first token of the path, read with the row's vectors (most lanes have none, few have two)
-  struct First { uint32_t raw, word; };
-  auto path_read = [&](First& f, uint32_t path, const T* in, const uint32_t* allow) {
-    int v = 0;
-    if (path) {
-      const int t = toks[32 * lane + __ffs(path) - 1];
-      v = ((t / kBlk) * slices + slice) * kBlk + t % kBlk;
-    }
-    ldg_elem(f.raw, in + v, path != 0u);
-    ldg_word(f.word, allow + (v >> 5), path != 0u && allow != nullptr);
-  };
-  auto path_out = [&](uint32_t path, const First& first, const T* in, T* out, const uint32_t* allow) {
+  auto path_out = [&](uint32_t path) {
     __syncwarp();
-    bool begun = false;
-    each(path, [&](int t) {               // the lane that clears the mark sets the element
-      const uint32_t bit = 1u << (t & 31);
-      if (atomicAnd(&on_path[t >> 5], ~bit) & bit) {
-        const Change h = change(t);
-        if (begun ? keeps(allow, h.v) : (first.word >> (h.v & 31)) & 1u) out[h.v] = apply(begun ? in[h.v] : elem_of<T>(first.raw), h);
-      }
-      begun = true;
+    each(path, [&](int t) {
+      atomicAnd(&on_path[t >> 5], ~(1u << (t & 31)));
+      atomicSub(&counts[t], 1u);
     });
-    each(path, [&](int t) { atomicSub(&counts[t], 1u); });
   };
-  // (the words are looked into when they are used, so that nothing waits here)
-  auto fix_read = [&](const T* in, const uint32_t* allow, uint32_t* raw, uint32_t* word) {
-#pragma unroll
-    for (int k = 0; k < kFix; ++k)
-      if (32 * k < own) {
-        ldg_elem(raw[k], in + fix[k].v, fix_at[k] >= 0);
-        ldg_word(word[k], allow + (fix[k].v >> 5), fix_at[k] >= 0 && allow != nullptr);
-      }
-  };
-  auto fix_set = [&](T* out, bool walked, const uint32_t* raw, const uint32_t* word) {
-    __syncwarp();
-#pragma unroll
-    for (int k = 0; k < kFix; ++k)
-      if (32 * k < own && fix_at[k] >= 0 && ((word[k] >> (fix[k].v & 31)) & 1u) && !(walked && marked(fix_at[k])))
-        out[fix[k].v] = apply(elem_of<T>(raw[k]), fix[k]);
-  };
-  // the touched elements of a dense block's vector, at place t (a multiple of 4 if ALIGNED)
-  auto dense_set = [&](Vec<T>& x, uint32_t hit, int t) {
-    uint32_t c[E];
-    if constexpr (ALIGNED) {
-#pragma unroll
-      for (int e = 0; e < E; e += 4) *reinterpret_cast<uint4*>(c + e) = *reinterpret_cast<const uint4*>(counts + t + e);
-    } else {
-#pragma unroll
-      for (int e = 0; e < E; ++e) c[e] = counts[t + e];
-    }
-#pragma unroll
-    for (int e = 0; e < E; ++e) {
-      const uint32_t n = c[e] & ((1u << kCountBits) - 1u), i = c[e] >> kCountBits;
-      float gain = i ? list_val[i - 1] : 0.f;
-      if (n) gain -= fmaf(freq, float(n), pres);
-      const float y = Elem<T>::get(x.e[e]);
-      const T z = Elem<T>::put(fmaf(y, n ? (y > 0.f ? inv_rep : rep) : 1.f, gain));
-      if ((hit >> e) & 1u) x.e[e] = z;
-    }
+  // one element by itself: token v, at place t
+  auto single = [&](T raw, bool keep, int t) {
+    T y = Elem<T>::put(-INFINITY);
+    if (keep) y = touching && counts[t] ? apply(raw, change(t)) : raw;
+    return y;
   };
 
-  if constexpr (ALIGNED) {
-    // tokens behind the last whole vector of the vocabulary, the warp that owns them taking them singly
-    const int rest = P.V % E, rest0 = P.V - rest, rest_at = local(rest0);
-    const bool tail = rest > 0 && lane < rest && rest_at >= 0 && rest_at / kBlk % kAdjWarps == warp;
-    // where the element at place t lies in the warp's part of a row
-    auto element = [&](int slot, int t) {
-      return reinterpret_cast<T*>(ring + slot * kRowBytes + t / kPlaceStep * 512) + t % kBlk;
+  if constexpr (kRing) {
+    // the touched elements of a dense block's vector, at place t
+    auto dense_set = [&](Vec<T>& x, uint32_t hit, int t) {
+      uint32_t c[E];
+      if constexpr (ROWS == kAligned) {
+#pragma unroll
+        for (int e = 0; e < E; e += 4)
+          *reinterpret_cast<uint4*>(c + e) = *reinterpret_cast<const uint4*>(counts + t + e);
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) c[e] = counts[t + e];
+      }
+#pragma unroll
+      for (int e = 0; e < E; ++e) {
+        const uint32_t n = c[e] & ((1u << kCountBits) - 1u), i = c[e] >> kCountBits;
+        float gain = i ? list_val[i - 1] : 0.f;
+        if (n) gain -= fmaf(freq, float(n), pres);
+        const float y = Elem<T>::get(x.e[e]);
+        const T z = Elem<T>::put(fmaf(y, n ? (y > 0.f ? inv_rep : rep) : 1.f, gain));
+        if ((hit >> e) & 1u) x.e[e] = z;
+      }
     };
+    // A block's elements before its first and behind its last whole vector are
+    // set singly: lane E i + s takes the s-th of block i (and the s + E-th, which
+    // only the vocabulary's last block can have).
+    const int tail_blk = lane / E, tail_s = lane % E;
+    const int tail_n = tail_blk < kAdjVecs ? max(size(tail_blk), 0) : 0;
+    auto tail_at = [&](int head, int s) {       // its offset in the block, -1 if there is none
+      const int vecs = max(tail_n - head, 0) / E * E;
+      return s < tail_n - vecs ? (s < head ? s : vecs + s) : -1;
+    };
+    const bool tails = __any_sync(kFull, ROWS == kShifted || tail_at(0, tail_s) >= 0);
+    uint32_t tail_raw = 0u, tail_word = kFull;
+    auto tail_read = [&](int r) {
+      const int k = tails && r < r_end ? tail_at(head_of(r), tail_s) : -1;
+      const int v = token(tail_blk) + k;
+      ldg_elem(tail_raw, row_of(r) + v, k >= 0);
+      ldg_word(tail_word, allow + (long long)(r - r_begin) * a.allowed_row_stride + (v >> 5), k >= 0 && allow);
+    };
+    tail_read(r_begin);
+
     uint32_t path = node_bits(r_begin);
     int slot = 0;
     for (int r = r_begin; r < r_end; ++r) {
       copy(r + kDepth - 1, slot == 0 ? kDepth - 1 : slot - 1);
       const uint32_t next_path = node_bits(r + 1);
+      const int head = head_of(r);
+      // where the element at place t lies in the warp's part of the row, nullptr if it is set singly
+      auto element = [&](int t) -> T* {
+        const int i = t / kPlaceStep, k = t % kBlk - head;
+        if (ROWS == kShifted && unsigned(k) >= unsigned(max(size(i) - head, 0) / E * E)) return nullptr;
+        return reinterpret_cast<T*>(ring + slot * kRowBytes + i * 512) + k;
+      };
       cp_async_wait<kDepth - 1>();
       __syncwarp();
       const bool walked = paths && __any_sync(kFull, path != 0u);
@@ -454,116 +474,78 @@ adjust_kernel(const AdjustParams P) {
 #pragma unroll
         for (int k = 0; k < kFix; ++k)
           if (32 * k < own && fix_at[k] >= 0 && !(walked && marked(fix_at[k]))) {
-            T* e = element(slot, fix_at[k]);
-            *e = apply(*e, fix[k]);
+            T* e = element(fix_at[k]);
+            if (e) *e = apply(*e, fix[k]);
           }
       }
+      const T tail_was = elem_of<T>(tail_raw);
+      const uint32_t tail_kept = tail_word;
       if (walked) {
         __syncwarp();
         each(path, [&](int t) {               // the lane that clears the mark sets the element
           const uint32_t bit = 1u << (t & 31);
           if ((on_path[t >> 5] & bit) && !((dense >> (t / kPlaceStep)) & 1u) &&
               (atomicAnd(&on_path[t >> 5], ~bit) & bit)) {
-            T* e = element(slot, t);
-            *e = apply(*e, change(t));
+            T* e = element(t);
+            if (e) *e = apply(*e, change(t));
           }
         });
       }
       __syncwarp();
       const uint32_t ok = row_ok[slot][tid];
-      T* dst = out + v0;
+      T* dst = out + v0 + head;
 #pragma unroll
       for (int i = 0; i < kAdjVecs; ++i) {
         Vec<T> x;
         x.u = *reinterpret_cast<const uint4*>(ring + slot * kRowBytes + i * 512 + lane * 16);
         const uint32_t k = (ok >> (8 * i)) & kAll;
+        const bool on = whole(i, head);
         if ((dense >> i) & 1u) {
-          const int t = place(i) + lane * E;
-          uint32_t hit = ((touched[t >> 5] >> (t & 31)) | (walked ? on_path[t >> 5] >> (t & 31) : 0u)) & k;
-          if (i < nv && hit) dense_set(x, hit, t);
+          const int t = place(i) + head + lane * E;
+          uint32_t hit = 0u;
+          if (on) {
+            hit = bits_at(touched, t, kWords);
+            if (walked) hit |= bits_at(on_path, t, kWords);
+            hit &= k;
+          }
+          if (hit) dense_set(x, hit, t);
         }
         if (allow) x.u = ban<T>(x.u, spread[k]);
-        if (i < nv) stg_stream(dst + i * step, x.u);
+        if (on) stg_stream(dst + i * step, x.u);
       }
-      if (tail) {
-        const int v = rest0 + lane, t = rest_at + lane;
-        T y = Elem<T>::put(-INFINITY);
-        if (keeps(allow ? allow + (long long)(r - r_begin) * a.allowed_row_stride : nullptr, v)) {
-          y = in[(long long)(r - r_begin) * P.in_stride + v];
-          if (touching && counts[t]) y = apply(y, change(t));
+      if (tails) {
+        const int k = tail_at(head, tail_s);
+        if (k >= 0) {
+          const int v = token(tail_blk) + k;
+          out[v] = single(tail_was, (tail_kept >> (v & 31)) & 1u, place(tail_blk) + k);
         }
-        out[v] = y;
+        const int far = tail_at(head, tail_s + E);
+        if (far >= 0 && tail_blk < kAdjVecs) {
+          const int v = token(tail_blk) + far;
+          out[v] = single(row_of(r)[v], keeps(allow ? allow + (long long)(r - r_begin) * a.allowed_row_stride : nullptr, v),
+                          place(tail_blk) + far);
+        }
+        tail_read(r + 1);
       }
-      if (walked) {
-        __syncwarp();
-        each(path, [&](int t) {
-          atomicAnd(&on_path[t >> 5], ~(1u << (t & 31)));
-          atomicSub(&counts[t], 1u);
-        });
-      }
+      if (walked) path_out(path);
       out += P.out_stride;
       path = next_path;
       slot = slot + 1 < kDepth ? slot + 1 : 0;
     }
     cp_async_wait<0>();
   } else {
-    const int words = (P.V + 31) >> 5;
     for (int r = r_begin; r < r_end; ++r) {
-      // elements before the first 16-byte boundary of every block of this row (a block is a multiple of 16 bytes)
-      const int head = int((16u - unsigned(reinterpret_cast<uintptr_t>(in) & 15u)) & 15u) / int(sizeof(T));
-      const bool same = ((reinterpret_cast<uintptr_t>(in) ^ reinterpret_cast<uintptr_t>(out)) & 15u) == 0;
-      uint32_t raw[kFix], word[kFix];
-#pragma unroll
-      for (int k = 0; k < kFix; ++k) raw[k] = 0u, word[k] = kFull;
-      if (own > 0) fix_read(in, allow, raw, word);
       const uint32_t path = node_bits(r);
       const bool walked = paths && __any_sync(kFull, path != 0u);
-      First first{0u, kFull};
-      if (paths) path_read(first, path, in, allow);
       if (walked) path_in(path);
-      // one element: token token(i) + k
-      auto scalar = [&](int i, int k) {
-        const int v = token(i) + k, t = place(i) + k;
-        T y = Elem<T>::put(-INFINITY);
-        if (keeps(allow, v)) {
-          y = in[v];
-          if (((dense >> i) & 1u) && ((touched[t >> 5] >> (t & 31)) & 1u) && !(walked && marked(t)))
-            y = apply(y, change(t));
+#pragma unroll 1
+      for (int i = 0; i < kAdjVecs; ++i)
+#pragma unroll 4
+        for (int k = lane; k < size(i); k += 32) {
+          const int v = token(i) + k;
+          out[v] = single(in[v], keeps(allow, v), place(i) + k);
         }
-        out[v] = y;
-      };
-      if (same) {
-        uint32_t ok[kAdjVecs];
-        Vec<T> x[kAdjVecs];
-#pragma unroll
-        for (int i = 0; i < kAdjVecs; ++i)
-          ok[i] = head + (lane + 1) * E <= size(i)
-                      ? (allow ? bits_at(allow, token(i) + head + lane * E, words) & kAll : kAll)
-                      : 0u;
-#pragma unroll
-        for (int i = 0; i < kAdjVecs; ++i)
-          ldg_stream(x[i].u, in + token(i) + head + lane * E, ok[i] != 0u);
-#pragma unroll
-        for (int i = 0; i < kAdjVecs; ++i) {
-          const int n = size(i), t = place(i) + head + lane * E;
-          if (head + (lane + 1) * E <= n) {
-            if ((dense >> i) & 1u) {
-              uint32_t hit = bits_at(touched, t, kWords) & ok[i];
-              if (walked) hit &= ~bits_at(on_path, t, kWords);
-              if (hit) dense_set(x[i], hit, t);
-            }
-            stg_stream(out + token(i) + head + lane * E, allow ? ban<T>(x[i].u, spread[ok[i]]) : x[i].u);
-          }
-          if (lane < min(head, n)) scalar(i, lane);
-          const int tail = head < n ? head + (n - head) / E * E : max(n, 0);
-          if (lane < n - tail) scalar(i, tail + lane);
-        }
-      } else {
-        for (int i = 0; i < kAdjVecs; ++i)
-          for (int k = lane; k < size(i); k += 32) scalar(i, k);
-      }
-      if (own > 0) fix_set(out, walked, raw, word);
-      if (walked) path_out(path, first, in, out, allow);
+      if (walked) path_out(path);
       in += P.in_stride;
       out += P.out_stride;
       if (allow) allow += a.allowed_row_stride;
@@ -571,33 +553,36 @@ adjust_kernel(const AdjustParams P) {
   }
 }
 
-template <typename T, bool ALIGNED>
-cudaError_t raise_limit() {
-  return cudaFuncSetAttribute(adjust_kernel<T, ALIGNED>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                              4 * kSlice<T> + (ALIGNED ? kRingBytes : 0));
+template <typename T, int ROWS>
+cudaError_t launch_rows_as(const AdjustParams& P, dim3 grid, cudaStream_t stream) {
+  constexpr int kMost = 4 * kSlice<T> + (ROWS != kSingle ? kRingBytes : 0);
+  const cudaError_t e =
+      cudaFuncSetAttribute(adjust_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+  if (e != cudaSuccess) return e;
+  const bool touching = P.count || P.a.bias_count > 0;
+  adjust_kernel<T, ROWS><<<grid, kAdjThreads, kMost - (touching ? 0 : 4 * kSlice<T>), stream>>>(P);
+  return cudaGetLastError();
 }
 
 template <typename T>
 cudaError_t launch_adjust(AdjustParams P, int B, cudaStream_t stream) {
-  const uintptr_t low = reinterpret_cast<uintptr_t>(P.in) | reinterpret_cast<uintptr_t>(P.out) |
-                        uintptr_t((P.in_stride | P.out_stride) * int(sizeof(T)));
-  const bool aligned = (low & 15) == 0;
-  const cudaError_t e = aligned ? raise_limit<T, true>() : raise_limit<T, false>();
-  if (e != cudaSuccess) return e;
   const int slices = (P.V + kSlice<T> - 1) / kSlice<T>;
   P.by_slices = fast_div(uint32_t(slices));
-  // rows per CTA: enough CTAs to fill the device a few times, then as many rows
-  // as possible share one count
+  // Rows per CTA: enough CTAs to fill the device three times (two an SM are
+  // resident), then as many rows as possible share one count.  Half as many CTAs
+  // left four trees of 497 rows at 227 us, twice as many 64 x 8 rows at 66 us,
+  // against 210 and 58.
   const long long want = 152ll * 3 * 2, per = (long long)slices * B;
   long long groups = (want + per - 1) / per;
   groups = groups > P.R ? P.R : groups;
   if (groups > 65535) groups = 65535;
   P.row_group = int((P.R + groups - 1) / groups);
   const dim3 grid(slices, (P.R + P.row_group - 1) / P.row_group, B);
-  const size_t smem = (aligned ? kRingBytes : 0) + (P.count || P.a.bias_count > 0 ? 4 * kSlice<T> : 0);
-  if (aligned) adjust_kernel<T, true><<<grid, kAdjThreads, smem, stream>>>(P);
-  else adjust_kernel<T, false><<<grid, kAdjThreads, smem, stream>>>(P);
-  return cudaGetLastError();
+  const uintptr_t in = reinterpret_cast<uintptr_t>(P.in), out = reinterpret_cast<uintptr_t>(P.out);
+  const uintptr_t in_step = uintptr_t(P.in_stride) * sizeof(T), out_step = uintptr_t(P.out_stride) * sizeof(T);
+  if (((in | out | in_step | out_step) & 15) == 0) return launch_rows_as<T, kAligned>(P, grid, stream);
+  if ((((in ^ out) | (in_step ^ out_step)) & 15) == 0) return launch_rows_as<T, kShifted>(P, grid, stream);
+  return launch_rows_as<T, kSingle>(P, grid, stream);
 }
 
 }  // namespace

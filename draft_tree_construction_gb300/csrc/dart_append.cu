@@ -1,11 +1,24 @@
 // dart_append.cu -- K6: a chunk's keys and values into a paged cache, with the
 // norms of query and key heads and the rotary positions in the same pass.
 //
+// Mathematics: x^ = w x / sqrt(mean(x^2) + eps);  a pair (x, y) at position p turns
+// to (x c - y s, y c + x s), c + i s = m e^(i p f);  fp32, rounded once.
+//
+// What bounds it: memory, q, k and v read once and written once; then the
+// instructions (60% of the issue slots), the lookups of a token's sequence, page
+// and position (four loads, one after the other) being hidden behind the heads'.
 // One warp takes four heads of one token at a time, eight lanes a head, two
 // 16-byte vectors a lane: a lane holds both elements of each of its pairs, so
 // the turn needs no exchange, a norm is one reduction over eight lanes, and the
 // sines and cosines, which depend on the token alone, are computed once (two
-// pairs a lane, then exchanged) and serve every head that the warp takes.
+// pairs a lane, then exchanged) and serve every head that the warp takes.  The
+// angle is kept in 2^-64 turns, in integers: exact at any position.
+//
+// Measured (GB300, kernel alone, 32 + 8 + 8 heads of 128):
+//   64 trees of 79 rows, norms and half layout, 16-token pages   25 us, 5.0 TB/s
+//   8191 tokens, 64 of 128 elements turned, interleaved         34.4 us, 5.9 TB/s
+//   one token                                                    3.5 us
+// Sines per head and registers in place of the ring took 50, 50 and 4.1 us.
 #include <cmath>
 
 #include "dart_launch.h"
@@ -422,8 +435,10 @@ extern "C" int dart_kv_append(const void* q, int64_t q_token_stride, int64_t q_h
   P.q_quads = (q_heads + 3) / 4;
   P.k_quads = (cache->heads + 3) / 4;
   P.quads = P.q_quads + 2 * P.k_quads;
-  // A warp takes one batch of quads when tokens are few, then several, so that
-  // the angles are computed once for as many heads as the number of warps allows.
+  // One warp per token when tokens fill the device, so that the angles are
+  // computed once for all heads (two warps: 33 us for 25 with 5056 tokens); the
+  // quads of a token spread over several warps when they do not (one token: 3.5
+  // us for 8.2).
   const long long want = 152ll * 32;
   long long parts = (want + T - 1) / T;
   P.parts = int(parts < 1 ? 1 : parts > P.quads ? P.quads : parts);

@@ -547,7 +547,8 @@ int dart_device_error(const void* workspace, uint32_t* out_flags, void* stream);
 int dart_noalloc_device_error(uint32_t* out_flags, void* stream);
 
 /* Sets the number of SM clock cycles any one wait of the row pass (a bulk
- * copy landing, a slot freeing, a barrier of the CTA) may take before the pass
+ * copy landing, a slot freeing, a barrier of the CTA) or of dart_tree_attention
+ * (a tile landing, a product or its operands) may take before the kernel
  * gives up: the CTA then ends every other wait, lets its copies in flight
  * land, sets DART_DEVERR_WAIT_TIMEOUT and returns, and its outputs are
  * invalid.  cycles <= 0 restores the default (4e9, about two seconds).  For

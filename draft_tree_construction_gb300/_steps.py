@@ -344,10 +344,11 @@ def kv_append(q, k, v, k_cache, v_cache, pages, lengths, starts, *, rotary: Rota
     rows starts[b] .. starts[b + 1] (rows outside are left alone).  q_weight,
     k_weight ([dim]) apply the norm of each head, rotary the turn by position
     lengths[b] + index in the chunk, or lengths[b] + offsets[row] (int32 [T]; a
-    tree's nodes: 1 + their lead's last offset, counted by tree_build's pos).
-    Returns the finished queries: out, which may be q itself, or a new tensor
-    whose rows outside every sequence are unset (None without q).  device_err (int32 [>= 1], zeroed by the caller) collects
-    the error bits of tokens that do not fit in their pages."""
+    tree's nodes: the root's offset + tree_build's pos).  Returns the finished
+    queries: out, which may be q itself, or a new tensor whose rows outside
+    every sequence are unset (None without q).  device_err (int32 [>= 1], zeroed
+    by the caller) collects the error bits of tokens that do not fit in their
+    pages."""
     torch = _torch()
     dev = _one_device(("k", "v", "q", "k_cache", "v_cache", "pages", "lengths", "starts", "rotary", "offsets",
                        "q_weight", "k_weight", "out", "device_err"),

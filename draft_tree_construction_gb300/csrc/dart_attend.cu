@@ -26,19 +26,20 @@
 //               half's softmax runs, the tensor unit works on the other's
 //
 // Measured (GB300, bf16, 32 + 8 heads of 128, both kernels):
-//   64 x 1 token over 4100..8200 positions    244 us, 6.5 TB/s: the cache, once
+//   64 x 1 token over 4100..8200 positions    247 us, 6.4 TB/s: the cache, once
 //   2 x 2048 tokens over 32768 positions     1370 us, 1.40 PFLOP/s (fp16; 1.22 when
 //     the card holds its power limit for seconds): a tile takes 3000 cycles, 2048
 //     of them in the tensor unit; the chain S -> softmax (1500) -> P V -> next S
 //     of a half is what is longer.  Handing P over in two halves: 1480 us.
-//   32 trees of 497 rows over ~3100 positions  718 us, 1.12 PFLOP/s of what is seen
-//   64 trees of 79 rows over ~1600 positions   183 us: 316 rows are a block of
+//   32 trees of 497 rows over ~3100 positions  727 us, 1.11 PFLOP/s of what is seen
+//   64 trees of 79 rows over ~1600 positions   185 us: 316 rows are a block of
 //     256 and one of 60, so the cache passes through the CTAs twice (5 TB/s from
 //     L2 and memory), and six block changes a CTA take a tenth.  Dealing the
 //     tiles of a short block to both halves and merging them: 199 us.
-//   1 token over 4098 positions               13.8 us, 8 of them before the first
+//   1 token over 4098 positions                 15 us, 8 of them before the first
 //     product and in the join
 #include <cmath>
+#include <type_traits>
 
 #include <cuda.h>
 
@@ -85,6 +86,8 @@ struct AttendParams {
   long long cap;              // positions a sequence's pages can hold
   int page, pages, box;       // positions per page, pages, positions per TMA box
   int k_slot[3], v_slot[3];   // which of (head, row, page) is coordinate 1, 2, 3
+  const void* v;              // the values again, for what a product cannot take (see take_out)
+  long long v_ps, v_rs, v_hs;
   uint32_t* err;
   struct Joint* joints;       // [kCtas]
   float4* parts;              // [kCtas][2] slots: [cols / 4][slot_rows] float4, then [slot_rows] (m, l)
@@ -161,6 +164,17 @@ __device__ __forceinline__ void tmem_ld16(uint32_t addr, float* x) {
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
       : "r"(addr));
 }
+__device__ __forceinline__ void tmem_ld8(uint32_t addr, float* x) {
+  uint32_t* r = reinterpret_cast<uint32_t*>(x);
+  asm volatile("tcgen05.ld.sync.aligned.32x32b.x8.b32 {%0,%1,%2,%3,%4,%5,%6,%7}, [%8];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7])
+               : "r"(addr));
+}
+__device__ __forceinline__ void tmem_st8(uint32_t addr, const uint32_t* r) {
+  asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};"
+               :: "r"(addr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+               : "memory");
+}
 __device__ __forceinline__ void tmem_st16(uint32_t addr, const uint32_t* r) {
   asm volatile(
       "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
@@ -208,6 +222,11 @@ __device__ __forceinline__ void stg_v8(void* p, const uint32_t* r) {
 __device__ __forceinline__ void cp_async16_or_zero(void* dst, const void* src, bool copy) {
   asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;"
                :: "r"(smem_u32(dst)), "l"(src), "r"(copy ? 16u : 0u) : "memory");
+}
+
+// The log-sum-exp of a row with maximum m (of c S) and sum l: -inf where it sees nothing, NaN stays NaN.
+__device__ __forceinline__ float log_sum(float m, float l) {
+  return l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718055994531f;
 }
 
 // Operand type in the instruction descriptor.
@@ -308,6 +327,7 @@ struct Shared {
   long long scan[kThreads / 32];
   uint32_t tmem;
   int dead;                        // a wait ran out: everyone leaves
+  int odd;                         // a row whose block's rows see different positions is not finite
 };
 
 // Bounded wait of a whole warp; false (for all lanes) once any wait of the CTA ran
@@ -422,6 +442,40 @@ __device__ __forceinline__ bool begin_walk(const AttendParams& P, const Shared* 
 __device__ __forceinline__ int k_load(int j) { return j == 0 ? 0 : 2 * j - 1; }
 __device__ __forceinline__ int v_load(int j, int n) { return j < n - 1 ? 2 * j + 2 : 2 * n - 1; }
 
+// A row's P is 0 where it does not see, but 0 * NaN is NaN in the product: where a
+// block's rows see different positions, an infinity or NaN in V reaches rows that
+// it must not reach.  A row finds that in its sums at the block's end; the CTA then
+// goes over its span once more, carefully: what is not finite is taken out of those
+// tiles before the product and given back to the rows that see it.  (Looking at the
+// tiles themselves, every time, cost a tenth: the products need the shared memory.)
+// take_out: the threads of a half go over the tile's `valid` rows; both halves write
+// the same.
+template <typename T> constexpr uint32_t kExpBits = 0x7F807F80u;
+template <> constexpr uint32_t kExpBits<__half> = 0x7C007C00u;
+template <typename T, int DH>
+__device__ __forceinline__ void take_out(unsigned char* v, int valid) {
+  constexpr uint32_t e = kExpBits<T>, one = e & (0u - e) & 0xFFFFu;
+  unsigned char* mine = v + (threadIdx.x & 127) * 16;           // eight threads a row
+  const int r0 = (threadIdx.x & 127) >> 3;
+#pragma unroll 1
+  for (int i = 0; i < 8 * DH; ++i)
+    if (16 * (i & 7) + r0 < valid) {
+      uint32_t* x = reinterpret_cast<uint32_t*>(mine + i * 2048);
+      for (int k = 0; k < 4; ++k) {
+        // the top bit of each element whose exponent is all ones
+        const uint32_t odd = ((x[k] & e) + (one | one << 16)) & 0x80008000u;
+        if (odd) x[k] &= ~((odd >> 15) * 0xFFFFu);
+      }
+    }
+  fence_async();
+}
+// Between the passes: true if there is a second one.  Once per thread of the CTA.
+__device__ __forceinline__ bool go_over_again(const Shared* sh) {
+  asm volatile("bar.sync 1, %0;" :: "n"(kThreads) : "memory");
+  return __all_sync(kFull, *reinterpret_cast<const volatile int*>(&sh->odd) != 0 &&
+                               *reinterpret_cast<const volatile int*>(&sh->dead) == 0);
+}
+
 template <typename T, int DH>       // DH: blocks of 64 columns per head
 __global__ void __launch_bounds__(kThreads, 1)
 attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap vmap) {
@@ -449,6 +503,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
     mbar_init(&sh->drain[1], 1);
     fence_mbar_init();
     sh->dead = 0;
+    sh->odd = 0;
     P.joints[blockIdx.x].parts = 0;        // this thread names the CTA's joint later, if there is one
   }
   if (warp == 9) {
@@ -468,57 +523,59 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
     if (warp == 8 || warp == 11) {
       // ------------------------------------------------------------ producers
       const uint32_t pid = warp == 8 ? 0u : 1u;
-      Walk w;
-      bool more = begin_walk(P, sh, w);
       uint32_t idx = 0, turn = 0;            // loads so far, and whose turn the next one is
       bool ok = true;
-      while (more && ok) {
-        const int n = w.t1 - w.t0;
-        const int32_t* table = P.table + (long long)w.b * P.table_stride;
-        for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
-          if (turn != pid) {
+      auto span_of = [&]() {
+        Walk w;
+        bool more = begin_walk(P, sh, w);
+        while (more && ok) {
+          const int n = w.t1 - w.t0;
+          const int32_t* table = P.table + (long long)w.b * P.table_stride;
+          for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
+            if (turn != pid) {
+              turn = turn + 1 < kProducers ? turn + 1 : 0;
+              continue;
+            }
             turn = turn + 1 < kProducers ? turn + 1 : 0;
-            continue;
-          }
-          turn = turn + 1 < kProducers ? turn + 1 : 0;
-          const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
-          const int j = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : (i - 2) / 2);
-          const int p0 = (w.t0 + j) * kTile;
-          const int boxes = (min(w.end - p0, kTile) + P.box - 1) / P.box;      // 0 for a block that sees nothing
-          const int at = p0 + (lane / DH) * P.box;
-          const bool mine = lane / DH < boxes;
-          int page = 0;
-          if (mine) {
-            page = table[P.by_page.div(at)];
-            if (page < 0 || page >= P.pages) {
-              set_dev_error(P.err, DART_DEVERR_CACHE);
-              page = P.pages;               // out of the map's range: the box arrives as zeros
+            const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
+            const int j = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : (i - 2) / 2);
+            const int p0 = (w.t0 + j) * kTile;
+            const int boxes = (min(w.end - p0, kTile) + P.box - 1) / P.box;      // 0 for a block that sees nothing
+            const int at = p0 + (lane / DH) * P.box;
+            const bool mine = lane / DH < boxes;
+            int page = 0;
+            if (mine) {
+              page = table[P.by_page.div(at)];
+              if (page < 0 || page >= P.pages) {
+                set_dev_error(P.err, DART_DEVERR_CACHE);
+                page = P.pages;               // out of the map's range: the box arrives as zeros
+              }
+            }
+            const uint32_t stage = idx % kStages;
+            ok = wait_warp(&sh->kv_empty[stage], ((idx / kStages) & 1u) ^ 1u, sh, P.wait_limit);
+            if (!ok) break;
+            if (lane == 0) mbar_expect_tx(&sh->kv_full[stage], uint32_t(boxes * DH * P.box * kColBytes));
+            __syncwarp();
+            if (mine) {
+              const int half = lane % DH, row = at - P.by_page.div(at) * P.page;
+              const int* slot = is_k ? P.k_slot : P.v_slot;
+              auto pick = [&](int i) { return slot[i] == 0 ? w.h : slot[i] == 1 ? row : page; };
+              tma_box(ring + stage * kStageBytes + half * kHalfTileBytes + (lane / DH) * P.box * kColBytes,
+                      is_k ? &kmap : &vmap, 64 * half, pick(0), pick(1), pick(2),
+                      &sh->kv_full[stage]);
             }
           }
-          const uint32_t stage = idx % kStages;
-          ok = wait_warp(&sh->kv_empty[stage], ((idx / kStages) & 1u) ^ 1u, sh, P.wait_limit);
-          if (!ok) break;
-          if (lane == 0) mbar_expect_tx(&sh->kv_full[stage], uint32_t(boxes * DH * P.box * kColBytes));
-          __syncwarp();
-          if (mine) {
-            const int half = lane % DH, row = at - P.by_page.div(at) * P.page;
-            const int* slot = is_k ? P.k_slot : P.v_slot;
-            auto pick = [&](int i) { return slot[i] == 0 ? w.h : slot[i] == 1 ? row : page; };
-            tma_box(ring + stage * kStageBytes + half * kHalfTileBytes + (lane / DH) * P.box * kColBytes,
-                    is_k ? &kmap : &vmap, 64 * half, pick(0), pick(1), pick(2),
-                    &sh->kv_full[stage]);
-          }
+          if (ok) more = w.next(P);
         }
-        if (ok) more = w.next(P);
-      }
+      };
+      span_of();
+      if (go_over_again(sh)) span_of();
       // no copy may land after the CTA has left: the last load of each stage is waited for
       for (uint32_t i = idx > uint32_t(kStages) ? idx - kStages : 0; i < idx; ++i)
         if (i % kProducers == pid) mbar_wait_bounded(&sh->kv_full[i % kStages], (i / kStages) & 1u, kDrainLimit);
       __syncwarp();
     } else {
       // ---------------------------------------------------------- tensor unit
-      Walk w;
-      bool more = begin_walk(P, sh, w);
       constexpr uint32_t type = kTypeCode<T>;
       constexpr uint32_t id_s = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 3) << 17) |
                                 (uint32_t(kHalfRows >> 4) << 24);
@@ -532,61 +589,67 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       const uint64_t qd = q_desc + t * (kStageBytes >> 4);
       uint32_t idx = 0, q_seen = 0, p_seen = 0;
       bool ok = true;
-      while (more && ok) {
-        const int n = w.t1 - w.t0;
-        if (w.rows <= t * kHalfRows) {
-          // The block has no second half.  This warp still sees every load arrive
-          // and gives its stage up: a stage's phases are told apart by their
-          // parity alone, so nobody may fall two of them behind or run ahead.
-          for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
-            ok = wait_warp(&sh->kv_full[idx % kStages], (idx / kStages) & 1u, sh, P.wait_limit);
-            if (ok && lane == 0) mbar_arrive(&sh->kv_empty[idx % kStages]);
-          }
-          if (ok) more = w.next(P);
-          continue;
-        }
-        for (int j = -1; j < n; ++j) {
-          uint32_t ks = 0, vs = 0;
-          if (j + 1 < n) {
-            const uint32_t i = idx + k_load(j + 1);
-            ks = i % kStages;
-            if (!(ok = wait_warp(&sh->kv_full[ks], (i / kStages) & 1u, sh, P.wait_limit))) break;
-          }
-          if (j >= 0) {
-            const uint32_t i = idx + v_load(j, n);
-            vs = i % kStages;
-            if (!(ok = wait_warp(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
-          }
-          // steps of 16 positions; those wholly behind the block's end are left out
-          const int steps = max(1, (min(w.end - (w.t0 + j) * kTile, kTile) + 15) / 16);
-          ok = j < 0 ? wait_warp(&sh->q_full[t], q_seen++ & 1u, sh, P.wait_limit)
-                     : wait_warp(&sh->p_full[t], p_seen++ & 1u, sh, P.wait_limit);
-          if (!ok) break;
-          tc_after();
-          if (elect()) {
-            if (j >= 0) {
-              const uint64_t vd = v_desc + uint64_t(vs * (kStageBytes >> 4));
-#pragma unroll
-              for (int k = 0; k < kTile / 16; ++k)
-                if (k < steps) mma_ts(o_at, s_at + k * 8, vd + k * (16 * kColBytes >> 4), id_o, j > 0 || k > 0);
+      auto span_of = [&]() {
+        Walk w;
+        bool more = begin_walk(P, sh, w);
+        while (more && ok) {
+          const int n = w.t1 - w.t0;
+          if (w.rows <= t * kHalfRows) {
+            // The block has no second half.  This warp still sees every load arrive
+            // and gives its stage up: a stage's phases are told apart by their
+            // parity alone, so nobody may fall two of them behind or run ahead.
+            for (int i = 0; i < 2 * n && ok; ++i, ++idx) {
+              ok = wait_warp(&sh->kv_full[idx % kStages], (idx / kStages) & 1u, sh, P.wait_limit);
+              if (ok && lane == 0) mbar_arrive(&sh->kv_empty[idx % kStages]);
             }
+            if (ok) more = w.next(P);
+            continue;
+          }
+          for (int j = -1; j < n; ++j) {
+            uint32_t ks = 0, vs = 0;
             if (j + 1 < n) {
-              const uint64_t kd = k_desc + uint64_t(ks * (kStageBytes >> 4));
-#pragma unroll
-              for (int k = 0; k < 4 * DH; ++k) {
-                const int off = ((k >> 2) * kHalfTileBytes + (k & 3) * 32) >> 4;
-                if (k < k_steps) mma_ss(s_at, qd + off, kd + off, id_s | P.negate, k > 0);
-              }
+              const uint32_t i = idx + k_load(j + 1);
+              ks = i % kStages;
+              if (!(ok = wait_warp(&sh->kv_full[ks], (i / kStages) & 1u, sh, P.wait_limit))) break;
             }
-            tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
-            if (j >= 0) tc_commit(&sh->kv_empty[vs]);
-            if (j + 1 < n) tc_commit(&sh->kv_empty[ks]);
+            if (j >= 0) {
+              const uint32_t i = idx + v_load(j, n);
+              vs = i % kStages;
+              if (!(ok = wait_warp(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
+            }
+            // steps of 16 positions; those wholly behind the block's end are left out
+            const int steps = max(1, (min(w.end - (w.t0 + j) * kTile, kTile) + 15) / 16);
+            ok = j < 0 ? wait_warp(&sh->q_full[t], q_seen++ & 1u, sh, P.wait_limit)
+                       : wait_warp(&sh->p_full[t], p_seen++ & 1u, sh, P.wait_limit);
+            if (!ok) break;
+            tc_after();
+            if (elect()) {
+              if (j >= 0) {
+                const uint64_t vd = v_desc + uint64_t(vs * (kStageBytes >> 4));
+#pragma unroll
+                for (int k = 0; k < kTile / 16; ++k)
+                  if (k < steps) mma_ts(o_at, s_at + k * 8, vd + k * (16 * kColBytes >> 4), id_o, j > 0 || k > 0);
+              }
+              if (j + 1 < n) {
+                const uint64_t kd = k_desc + uint64_t(ks * (kStageBytes >> 4));
+#pragma unroll
+                for (int k = 0; k < 4 * DH; ++k) {
+                  const int off = ((k >> 2) * kHalfTileBytes + (k & 3) * 32) >> 4;
+                  if (k < k_steps) mma_ss(s_at, qd + off, kd + off, id_s | P.negate, k > 0);
+                }
+              }
+              tc_commit(j + 1 < n ? &sh->s_full[t] : &sh->o_full[t]);
+              if (j >= 0) tc_commit(&sh->kv_empty[vs]);
+              if (j + 1 < n) tc_commit(&sh->kv_empty[ks]);
+            }
+            __syncwarp();
           }
-          __syncwarp();
+          idx += 2 * n;
+          if (ok) more = w.next(P);
         }
-        idx += 2 * n;
-        if (ok) more = w.next(P);
-      }
+      };
+      span_of();
+      if (go_over_again(sh)) span_of();
       // every product has ended before the tensor memory is given back
       if (elect()) tc_commit(&sh->drain[t]);
       mbar_wait_bounded(&sh->drain[t], 0, kDrainLimit);
@@ -595,8 +658,6 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
   } else {
     // --------------------------------------------------------------- softmax
     asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kSoftmaxRegs));
-    Walk w;
-    bool more = begin_walk(P, sh, w);
     const int t = warp >> 2;
     const int row = (warp & 3) * 32 + lane;                       // within the half
     const uint32_t lane_base = uint32_t(warp & 3) << 21;          // TMEM lanes 32 (warp & 3) ..
@@ -604,13 +665,18 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
     const uint32_t to = tmem + lane_base + 2 * kTile + uint32_t(t) * kCols;
     unsigned char* q_half = sq + t * kStageBytes;
     uint32_t idx = 0, s_seen = 0, o_seen = 0;
+    bool ok = true;
 
-    auto active = [&]() { return w.rows > t * kHalfRows; };
-    auto skip_inactive = [&]() {
-      while (more && !active()) {
-        idx += 2 * (w.t1 - w.t0);
-        more = w.next(P);
-      }
+    auto span_of = [&](auto careful) {
+      constexpr bool kCareful = decltype(careful)::value;
+      Walk w;
+      bool more = begin_walk(P, sh, w);
+      auto active = [&]() { return w.rows > t * kHalfRows; };
+      auto skip_inactive = [&]() {
+        while (more && !active()) {
+          idx += 2 * (w.t1 - w.t0);
+          more = w.next(P);
+        }
     };
     // This warp's 32 rows of the block's queries, swizzled, copied without
     // registers as soon as the buffer is free; give_q hands them to the products.
@@ -642,7 +708,6 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       ask_q();
       give_q();
     }
-    bool ok = true;
     while (more && ok) {
       const int n = w.t1 - w.t0;
       const int my_row = t * kHalfRows + row;
@@ -680,6 +745,12 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
         }
         ok = wait_warp(&sh->s_full[t], s_seen++ & 1u, sh, P.wait_limit);
         if (!ok) break;
+        if (kCareful && masked && open_end < w.end) {
+          const uint32_t i = idx + v_load(j, n);
+          ok = wait_warp(&sh->kv_full[i % kStages], (i / kStages) & 1u, sh, P.wait_limit);
+          if (!ok) break;
+          take_out<T, DH>(ring + (i % kStages) * kStageBytes, min(w.end - p0, kTile));
+        }
         tc_after();
         if (warp_on) {
           float s[kTile];
@@ -768,12 +839,44 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
       // the finished part, while the next one's queries are already on their way
       const int d_start = w.c.start, d_h = w.h, d_row0 = w.blk * kBlockRows, d_rows = w.rows, d_t0 = w.t0;
       const int d_after = w.tiles - w.t1;                // the block's tiles in later CTAs
+      const int d_b = w.b, d_odd0 = open_end < w.end ? max(open_end / kTile, w.t0) * kTile : w.end;
+      const int d_odd1 = min(w.t1 * kTile, w.end);       // rows differ in what they see of d_odd0 .. d_odd1
       more = w.next(P);
       skip_inactive();
       if (more) ask_q();
       ok = wait_warp(&sh->o_full[t], o_seen++ & 1u, sh, P.wait_limit);
       if (!ok) break;
       tc_after();
+      const bool differ = d_odd0 < d_odd1;
+      uint64_t odd = 0ull;                               // 0 while all is finite, else NaN
+      auto look = [&](const float* o) {
+#pragma unroll
+        for (int k = 0; k < 32; k += 2) odd = fma2(pair(o[k], o[k + 1]), 0ull, odd);
+      };
+      if (kCareful && differ && warp_on) {         // what take_out took is given to the rows that see it
+        const int32_t* table = P.table + (long long)d_b * P.table_stride;
+#pragma unroll 1
+        for (int col = 0; col < P.D; col += 8) {
+          float o[8];
+          tmem_ld8(to + col, o);
+          loaded<8>(o);
+#pragma unroll 1
+          for (int p = d_odd0; p < d_odd1; ++p) {
+            const int x = p - tree, pg = P.by_page.div(p), page = table[pg];
+            const bool sees = p < plain || (x >= 0 && x < nodes && (bits[x >> 5] >> (x & 31) & 1u));
+            if (!sees || page < 0 || page >= P.pages) continue;
+            const T* src = static_cast<const T*>(P.v) + page * P.v_ps + (p - pg * P.page) * P.v_rs + d_h * P.v_hs;
+#pragma unroll
+            for (int k = 0; k < 8; ++k) {
+              const float y = float(src[col + k]);
+              if (!(fabsf(y) < INFINITY)) o[k] += y;
+            }
+          }
+          __syncwarp();
+          tmem_st8(to + col, reinterpret_cast<const uint32_t*>(o));
+        }
+        tc_wait_st();
+      }
       if (d_t0 == 0 && d_after == 0) {
         // A thread's row leaves 32 (or 16) bytes at a time: whole sectors, and
         // nothing to wait for.  (Through shared memory the rows would leave in
@@ -788,6 +891,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
             float o[32];
             tmem_ld32(to + 32 * i, o);
             loaded<32>(o);
+            if (!kCareful) look(o);
             uint32_t y[16];
 #pragma unroll
             for (int k = 0; k < 16; ++k) y[k] = pack2<T>(o[2 * k] * inv, o[2 * k + 1] * inv);
@@ -807,7 +911,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
             }
             if (i == 0 && more) give_q();
           }
-          if (row_on && P.lse) P.lse[tok * P.Hq + head] = l > 0.f ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
+          if (row_on && P.lse) P.lse[tok * P.Hq + head] = log_sum(m, l);
         }
       } else if (warp_on) {
         // [4 columns][row] so that a warp writes whole lines, then (m, l) of each row
@@ -817,6 +921,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
           float o[32];
           tmem_ld32(to + 32 * i, o);
           loaded<32>(o);
+          if (!kCareful) look(o);
 #pragma unroll
           for (int k = 0; k < 8; ++k)
             if (row_on)
@@ -825,6 +930,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
         }
         if (row_on) reinterpret_cast<float2*>(dst + kCols / 4 * P.slot_rows)[my_row] = make_float2(m, l);
       }
+      if (!kCareful && odd != 0ull && differ && row_on) *reinterpret_cast<volatile int*>(&sh->odd) = 1;
       if (!warp_on && more) give_q();
       if (t == 0 && warp == 0 && lane == 0 && d_t0 == 0 && d_after > 0) {
         // the span ends within the block: the joint names it and the CTAs that share it
@@ -838,6 +944,9 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
         P.joints[blockIdx.x] = jt;
       }
     }
+    };
+    span_of(std::false_type{});
+    if (go_over_again(sh)) span_of(std::true_type{});
   }
 
   tc_before();
@@ -916,7 +1025,7 @@ join_kernel(const AttendParams P) {
     if (4 * c4 < P.D)
       *reinterpret_cast<uint2*>(static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs + 4 * c4) =
           make_uint2(pack2<T>(acc[e].x * inv, acc[e].y * inv), pack2<T>(acc[e].z * inv, acc[e].w * inv));
-    if (P.lse && c4 == 0) P.lse[tok * P.Hq + head] = l[e] > 0.f ? (m[e] + log2f(l[e])) * 0.69314718055994531f : -INFINITY;
+    if (P.lse && c4 == 0) P.lse[tok * P.Hq + head] = log_sum(m[e], l[e]);
   }
 }
 
@@ -1054,6 +1163,7 @@ extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_
   P.joints = reinterpret_cast<Joint*>(ws + kCtrlBytes);
   P.parts = reinterpret_cast<float4*>(ws + kCtrlBytes + kJointBytes);
   P.slot_rows = slot_rows(T, P.G);
+  P.v = c.v; P.v_ps = c.v_page_stride; P.v_rs = c.v_row_stride; P.v_hs = c.v_head_stride;
   P.wait_limit = rows_wait_limit();
   CUtensorMap km, vm;
   if (!cache_map(c, c.k, c.k_page_stride, c.k_row_stride, c.k_head_stride, P.box, &km, P.k_slot) ||

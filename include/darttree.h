@@ -490,8 +490,8 @@ size_t dart_attention_workspace_bytes(int T, int B, int q_heads, int heads, int 
  *   out_lse = log sum exp(scale * q.k), -inf if there are none
  * Query head g reads key head g / (q_heads / heads).  Statistics and sums are
  * fp32; the probabilities are rounded to the cache's type for the product with
- * v.  Cache rows from position S on may hold anything; the v rows below S are
- * finite.
+ * v.  What a row does not see does not reach it, infinities and NaN included;
+ * cache rows from position S on may hold anything.
  *  q, out   as for dart_kv_append; out must not overlap q or the cache
  *  q_heads  a multiple of cache->heads; T * q_heads < 2^31
  *  mask     device uint32 [B][N][ceil(N/32)], or NULL with N = 0 (causal);

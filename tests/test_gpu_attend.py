@@ -119,6 +119,54 @@ def test_rows_whose_mask_leaves_nothing(D):
     assert bool((got["out"][3] == 0).all()) and bool((got["lse"][11] == -math.inf).all())
 
 
+@pytest.mark.parametrize("dtype,lengths,counts,Hq,Hkv,dim,page,N,heads_first", [
+    ("bf16", [200, 0, 90], [65, 65, 40], 8, 2, 128, 16, 64, False),       # trees; a chunk of leads and nodes
+    ("f16", [70, 5], [150, 129], 4, 1, 64, 32, 0, True),                  # causal: later tokens of the chunk
+    ("bf16", [128] * 30, [79] * 30, 32, 8, 72, 24, 78, False),            # blocks of one and of two halves
+    ("f16", [5000], [100], 16, 1, 128, 64, 99, False),                    # joined blocks
+])
+def test_what_a_row_does_not_see_does_not_reach_it(D, dtype, lengths, counts, Hq, Hkv, dim, page, N, heads_first):
+    """NaN and infinities in keys and values of positions that some rows see and others do not: the others keep
+    the bits they have without them, and the rows that see one of the values' have it in its column."""
+    s = _case(dtype, lengths, counts, Hq, Hkv, dim, page, N, heads_first, seed=12)
+    rng = np.random.default_rng(12)
+    odd = {}                                          # row of q -> {(kv head, column): value}
+    keys = torch.zeros(sum(counts), Hkv, dtype=torch.bool)      # rows that see a NaN key
+    plain, given = [c.clone() for c in (s["k_cache"], s["v_cache"])], [s["k_cache"], s["v_cache"]]
+    for b, (at, n) in enumerate(zip(lengths, counts)):
+        lead = max(n - N, 0)
+        see = np.stack([refs.visible(at, n, N, i, s["mask"][b, i - lead] if i >= lead else None) for i in range(n)])
+        for j, p in enumerate(rng.choice(np.arange(at + 1, at + n), 3, replace=False)):
+            h, col = int(rng.integers(Hkv)), int(rng.integers(dim))
+            where = (int(s["pages"][b, p // page]), int(p % page), h)
+            rows = [int(s["starts"][b]) + i for i in range(n) if see[i, p]]
+            if j == 0:                                # a key
+                given[0][where + (col,)] = math.nan
+                keys[rows, h] = True
+            else:
+                x = (math.nan, math.inf, -math.inf)[(b + j) % 3]
+                given[1][where + (col,)] = x
+                plain[1][where + (col,)] = 0.0
+                for r in rows:
+                    old = odd.setdefault(r, {}).get((h, col), 0.0)
+                    odd[r][h, col] = old + x          # inf - inf is NaN
+    d = _cuda(s)
+    got = D.tree_attention(*_args(d), mask=d["mask"], lse=True)
+    assert D.device_error(got["workspace"]) == 0
+    d2 = _cuda(dict(s, k_cache=plain[0], v_cache=plain[1]))
+    ref = D.tree_attention(*_args(d2), mask=d2["mask"], lse=True)
+    want, G = ref["out"].cpu().clone(), Hq // Hkv
+    for r, cells in odd.items():
+        for (h, col), x in cells.items():
+            want[r, h * G:(h + 1) * G, col] = x
+    spoilt = keys.repeat_interleave(G, 1)
+    out, lse = got["out"].cpu(), got["lse"].cpu()
+    assert bool(out[spoilt].isnan().all()) and bool(lse[spoilt].isnan().all())
+    assert torch.equal(lse[~spoilt], ref["lse"].cpu()[~spoilt])
+    assert torch.equal(out[~spoilt].isnan(), want[~spoilt].isnan())
+    assert torch.equal(out[~spoilt].nan_to_num(nan=7.0), want[~spoilt].nan_to_num(nan=7.0))
+
+
 def test_mask_bits_behind_the_chunk_are_ignored(D):
     s = _case("f16", [10], [25], 2, 1, 64, 8, 25, seed=5)
     d, got = _check(D, s)

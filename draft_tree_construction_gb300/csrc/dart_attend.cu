@@ -29,16 +29,22 @@
 //   64 x 1 token over 4100..8200 positions    247 us, 6.4 TB/s: the cache, once
 //   2 x 2048 tokens over 32768 positions     1370 us, 1.40 PFLOP/s (fp16; 1.22 when
 //     the card holds its power limit for seconds): a tile takes 3000 cycles, 2048
-//     of them in the tensor unit; the chain S -> softmax (1500) -> P V -> next S
-//     of a half is what is longer.  Handing P over in two halves: 1480 us.
+//     of them in the tensor unit; the chain S -> softmax (1400) -> P V -> next S
+//     of a half is what is longer.  Handing P over in two halves: 1480 us.  Two
+//     threads a row, 64 positions each: 1460 us (the exponentials, 512 cycles a
+//     half's tile, and the row's exchange leave the softmax at 1500).
 //   32 trees of 497 rows over ~3100 positions  727 us, 1.11 PFLOP/s of what is seen
-//   64 trees of 79 rows over ~1600 positions   185 us: 316 rows are a block of
+//   64 trees of 79 rows over ~1600 positions   182 us: 316 rows are a block of
 //     256 and one of 60, so the cache passes through the CTAs twice (5 TB/s from
 //     L2 and memory), and six block changes a CTA take a tenth.  Dealing the
-//     tiles of a short block to both halves and merging them: 199 us.
+//     tiles of a short block to both halves and merging them: 199 us.  Moving a
+//     span's end to a block's end that is near, so that fewer blocks are joined:
+//     192 us here, 10 us less in 128 trees over ~450 positions, 10 us more in 16
+//     over ~6000.
 //   1 token over 4098 positions                 15 us, 8 of them before the first
 //     product and in the join
 #include <cmath>
+#include <limits>
 #include <type_traits>
 
 #include <cuda.h>
@@ -78,7 +84,7 @@ struct AttendParams {
   const int32_t* lengths;
   const int32_t* starts;
   const uint32_t* mask;
-  float c;                    // |scale| log2 e (next to nothing for scale 0, so that -inf stays -inf)
+  float c;                    // |scale| log2 e
   uint32_t negate;            // the products of Q and K change their sign: the scale is negative
   bool wide_out;              // 32-byte stores
   const int32_t* table;
@@ -677,273 +683,277 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
           idx += 2 * (w.t1 - w.t0);
           more = w.next(P);
         }
-    };
-    // This warp's 32 rows of the block's queries, swizzled, copied without
-    // registers as soon as the buffer is free; give_q hands them to the products.
-    constexpr int kChunks = 8 * DH, kPer = 32 / kChunks, kSteps = 32 / kPer;   // 16-byte chunks a row, rows a step
-    const int chunk = lane % kChunks, sub = lane / kChunks, warp_row = (warp & 3) * 32;
-    auto ask_q = [&]() {
+      };
+      // This warp's 32 rows of the block's queries, swizzled, copied without registers
+      // as soon as the buffer is free; give_q hands them to the products.  Lane r finds
+      // where row r lies (when each lane found its vector's row, step by step, a block
+      // took 2600 cycles to ask).
+      constexpr int kChunks = 8 * DH, kPer = 32 / kChunks;        // 16-byte chunks a row, rows a step
+      auto ask_q = [&]() {
+        const int chunk = lane % kChunks, sub = lane / kChunks, first = (warp & 3) * 32;
+        const int rows = w.rows - t * kHalfRows - first;
+        const int g = w.blk * kBlockRows + t * kHalfRows + first + max(0, min(lane, rows - 1));
+        const int token = P.by_group.div(g);
+        const long long at = (long long)(w.c.start + token) * P.q_ts + (long long)(w.h * P.G + g - token * P.G) * P.q_hs;
+        const bool inside = 8 * chunk < P.D;
+        const T* src = static_cast<const T*>(P.q) + (inside ? 8 * chunk : 0);
+        unsigned char* dst = q_half + (chunk >> 3) * kHalfTileBytes + first * kColBytes;
 #pragma unroll 4
-      for (int u = 0; u < kSteps; ++u) {
-        const int r = warp_row + u * kPer + sub, rr = t * kHalfRows + r;
-        if (rr < w.rows) {
-          const int g = w.blk * kBlockRows + rr, token = P.by_group.div(g);
-          const T* src = static_cast<const T*>(P.q) + (long long)(w.c.start + token) * P.q_ts +
-                         (long long)(w.h * P.G + g - token * P.G) * P.q_hs;
-          cp_async16_or_zero(q_half + (chunk >> 3) * kHalfTileBytes + r * kColBytes + (((chunk & 7) ^ (r & 7)) << 4),
-                             src + (8 * chunk < P.D ? 8 * chunk : 0), 8 * chunk < P.D);
+        for (int u = 0; u < 32 / kPer; ++u) {
+          const int r = u * kPer + sub;
+          const long long from = __shfl_sync(kFull, at, r);
+          if (r < rows) cp_async16_or_zero(dst + r * kColBytes + (((chunk & 7) ^ (r & 7)) << 4), src + from, inside);
         }
+        cp_async_commit();
+      };
+      auto give_q = [&]() {
+        cp_async_wait<0>();
+        fence_async();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh->q_full[t]);
+      };
+
+      skip_inactive();
+      if (more) {
+        ask_q();
+        give_q();
       }
-      cp_async_commit();
-    };
-    auto give_q = [&]() {
-      cp_async_wait<0>();
-      fence_async();
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->q_full[t]);
-    };
+      while (more && ok) {
+        const int n = w.t1 - w.t0;
+        const int my_row = t * kHalfRows + row;
+        const bool warp_on = t * kHalfRows + (warp & 3) * 32 < w.rows;
+        const bool row_on = my_row < w.rows;
+        const int g = w.blk * kBlockRows + min(my_row, w.rows - 1);
+        const int token = P.by_group.div(g);
+        // the row sees positions below `plain` and the set bits from `tree` on
+        const int plain = min(w.c.len + min(token + 1, w.c.lead), w.c.S);
+        const int tree = w.c.len + w.c.lead;
+        const int nodes = token >= w.c.lead ? min(min(P.N, w.c.n - w.c.lead), w.c.S - tree) : 0;   // may be < 0
+        const uint32_t* bits = P.mask + ((long long)w.b * P.N + (token - w.c.lead)) * P.MW;    // read if nodes > 0
+        // tiles below the block's least `plain` need no mask
+        const int first_token = P.by_group.div(w.blk * kBlockRows);
+        const int open_end = min(w.c.len + min(first_token + 1, w.c.lead), w.c.S);
 
-    skip_inactive();
-    if (more) {
-      ask_q();
-      give_q();
-    }
-    while (more && ok) {
-      const int n = w.t1 - w.t0;
-      const int my_row = t * kHalfRows + row;
-      const bool warp_on = t * kHalfRows + (warp & 3) * 32 < w.rows;
-      const bool row_on = my_row < w.rows;
-      const int g = w.blk * kBlockRows + min(my_row, w.rows - 1);
-      const int token = P.by_group.div(g);
-      // the row sees positions below `plain` and the set bits from `tree` on
-      const int plain = min(w.c.len + min(token + 1, w.c.lead), w.c.S);
-      const int tree = w.c.len + w.c.lead;
-      const int nodes = token >= w.c.lead ? min(min(P.N, w.c.n - w.c.lead), w.c.S - tree) : 0;   // may be < 0
-      const uint32_t* bits = P.mask + ((long long)w.b * P.N + (token - w.c.lead)) * P.MW;    // read if nodes > 0
-      // tiles below the block's least `plain` need no mask
-      const int first_token = P.by_group.div(w.blk * kBlockRows);
-      const int open_end = min(w.c.len + min(first_token + 1, w.c.lead), w.c.S);
-
-      float m = -INFINITY, l = 0.f;
-      for (int j = 0; j < n && ok; ++j) {
-        const int p0 = (w.t0 + j) * kTile;
-        // what this row sees of the tile, looked up while the product is under way
-        const bool masked = p0 + kTile > open_end;
-        uint32_t see[4] = {kFull, kFull, kFull, kFull};
-        if (masked) {
-          uint32_t word[5];
-          const int at0 = p0 - tree, wd0 = at0 >> 5;           // floor: the word that holds bit at0
-#pragma unroll
-          for (int i = 0; i < 5; ++i)
-            word[i] = wd0 + i >= 0 && 32 * (wd0 + i) < nodes ? bits[wd0 + i] : 0u;
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            const int below = max(0, min(plain - p0 - 32 * i, 32)), left = max(0, min(nodes - at0 - 32 * i, 32));
-            const uint32_t x = __funnelshift_r(word[i], word[i + 1], at0 & 31);
-            see[i] = (below >= 32 ? kFull : (1u << below) - 1u) | (x & (left >= 32 ? kFull : (1u << left) - 1u));
-          }
-        }
-        ok = wait_warp(&sh->s_full[t], s_seen++ & 1u, sh, P.wait_limit);
-        if (!ok) break;
-        if (kCareful && masked && open_end < w.end) {
-          const uint32_t i = idx + v_load(j, n);
-          ok = wait_warp(&sh->kv_full[i % kStages], (i / kStages) & 1u, sh, P.wait_limit);
-          if (!ok) break;
-          take_out<T, DH>(ring + (i % kStages) * kStageBytes, min(w.end - p0, kTile));
-        }
-        tc_after();
-        if (warp_on) {
-          float s[kTile];
-#pragma unroll
-          for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
-          loaded<kTile>(s);
+        float m = -INFINITY, l = 0.f;
+        for (int j = 0; j < n && ok; ++j) {
+          const int p0 = (w.t0 + j) * kTile;
+          // what this row sees of the tile, looked up while the product is under way
+          const bool masked = p0 + kTile > open_end;
+          uint32_t see[4] = {kFull, kFull, kFull, kFull};
           if (masked) {
+            uint32_t word[5];
+            const int at0 = p0 - tree, wd0 = at0 >> 5;           // floor: the word that holds bit at0
 #pragma unroll
-            for (int k = 0; k < kTile; ++k)
-              if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = -INFINITY;
-          }
-          float top[4] = {s[0], s[1], s[2], s[3]};
+            for (int i = 0; i < 5; ++i)
+              word[i] = wd0 + i >= 0 && 32 * (wd0 + i) < nodes ? bits[wd0 + i] : 0u;
 #pragma unroll
-          for (int k = 4; k < kTile; k += 8) {
-#pragma unroll
-            for (int i = 0; i < 4; ++i)
-              top[i] = k + 4 + i < kTile ? max3(top[i], s[k + i], s[k + 4 + i]) : fmaxf(top[i], s[k + i]);
-          }
-          float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
-          mx *= P.c;
-          if (j == 0) {
-            m = mx;
-          } else {
-            const bool grow = mx > m + kRescale;
-            if (__any_sync(kFull, grow)) {
-              const float keep = grow ? ex2_approx(m - mx) : 1.f;
-              if (grow) {
-                m = mx;
-                l *= keep;
-              }
-#pragma unroll
-              for (int i = 0; i < kCols / 16; ++i) {
-                float o[16];
-                tmem_ld16(to + 16 * i, o);
-                loaded<16>(o);
-#pragma unroll
-                for (int k = 0; k < 16; ++k) o[k] *= keep;
-                tmem_st16(to + 16 * i, reinterpret_cast<const uint32_t*>(o));
-              }
+            for (int i = 0; i < 4; ++i) {
+              const int below = max(0, min(plain - p0 - 32 * i, 32)), left = max(0, min(nodes - at0 - 32 * i, 32));
+              const uint32_t x = __funnelshift_r(word[i], word[i + 1], at0 & 31);
+              see[i] = (below >= 32 ? kFull : (1u << below) - 1u) | (x & (left >= 32 ? kFull : (1u << left) - 1u));
             }
           }
-          const float off = m == -INFINITY ? 0.f : m;
-          const uint64_t c2 = pair(P.c, P.c), off2 = pair(-off, -off);
-          uint64_t sum[2] = {0ull, 0ull};
-#pragma unroll
-          for (int i = 0; i < 4; ++i) {
-            uint32_t pk[16];
-#pragma unroll
-            for (int k = 0; k < 16; ++k) {
-              const uint64_t x = fma2(pair(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), c2, off2);
-              const float a = ex2_approx(low(x)), b = ex2_approx(high(x));
-              sum[k & 1] = add2(sum[k & 1], pair(a, b));
-              pk[k] = pack2<T>(a, b);
-            }
-            tmem_st16(ts + 16 * i, pk);
-          }
-          sum[0] = add2(sum[0], sum[1]);
-          l += low(sum[0]) + high(sum[0]);
-          tc_wait_st();
-        }
-        // V rows behind the end may hold anything, and 0 * NaN is NaN: those that
-        // share a step of 16 with valid rows are cleared (by either half, which write the same)
-        if (j == n - 1 && w.t1 == w.tiles) {
-          const int valid = max(0, min(w.end - p0, kTile));
-          const int upto = max(16, (valid + 15) / 16 * 16);
-          if (valid < upto) {
+          ok = wait_warp(&sh->s_full[t], s_seen++ & 1u, sh, P.wait_limit);
+          if (!ok) break;
+          if (kCareful && masked && open_end < w.end) {
             const uint32_t i = idx + v_load(j, n);
             ok = wait_warp(&sh->kv_full[i % kStages], (i / kStages) & 1u, sh, P.wait_limit);
             if (!ok) break;
-            const int r = valid + ((tid & 127) >> 3);
-            if (r < upto)
-#pragma unroll
-              for (int hf = 0; hf < DH; ++hf)
-                *reinterpret_cast<uint4*>(ring + (i % kStages) * kStageBytes + hf * kHalfTileBytes + r * kColBytes +
-                                          (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
-            fence_async();
+            take_out<T, DH>(ring + (i % kStages) * kStageBytes, min(w.end - p0, kTile));
           }
-        }
-        tc_before();
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh->p_full[t]);
-      }
-      if (!ok) break;
-      idx += 2 * n;
-
-      // the finished part, while the next one's queries are already on their way
-      const int d_start = w.c.start, d_h = w.h, d_row0 = w.blk * kBlockRows, d_rows = w.rows, d_t0 = w.t0;
-      const int d_after = w.tiles - w.t1;                // the block's tiles in later CTAs
-      const int d_b = w.b, d_odd0 = open_end < w.end ? max(open_end / kTile, w.t0) * kTile : w.end;
-      const int d_odd1 = min(w.t1 * kTile, w.end);       // rows differ in what they see of d_odd0 .. d_odd1
-      more = w.next(P);
-      skip_inactive();
-      if (more) ask_q();
-      ok = wait_warp(&sh->o_full[t], o_seen++ & 1u, sh, P.wait_limit);
-      if (!ok) break;
-      tc_after();
-      const bool differ = d_odd0 < d_odd1;
-      uint64_t odd = 0ull;                               // 0 while all is finite, else NaN
-      auto look = [&](const float* o) {
+          tc_after();
+          if (warp_on) {
+            float s[kTile];
 #pragma unroll
-        for (int k = 0; k < 32; k += 2) odd = fma2(pair(o[k], o[k + 1]), 0ull, odd);
-      };
-      if (kCareful && differ && warp_on) {         // what take_out took is given to the rows that see it
-        const int32_t* table = P.table + (long long)d_b * P.table_stride;
-#pragma unroll 1
-        for (int col = 0; col < P.D; col += 8) {
-          float o[8];
-          tmem_ld8(to + col, o);
-          loaded<8>(o);
-#pragma unroll 1
-          for (int p = d_odd0; p < d_odd1; ++p) {
-            const int x = p - tree, pg = P.by_page.div(p), page = table[pg];
-            const bool sees = p < plain || (x >= 0 && x < nodes && (bits[x >> 5] >> (x & 31) & 1u));
-            if (!sees || page < 0 || page >= P.pages) continue;
-            const T* src = static_cast<const T*>(P.v) + page * P.v_ps + (p - pg * P.page) * P.v_rs + d_h * P.v_hs;
+            for (int i = 0; i < 4; ++i) tmem_ld32(ts + 32 * i, s + 32 * i);
+            loaded<kTile>(s);
+            if (masked) {
 #pragma unroll
-            for (int k = 0; k < 8; ++k) {
-              const float y = float(src[col + k]);
-              if (!(fabsf(y) < INFINITY)) o[k] += y;
+              for (int k = 0; k < kTile; ++k)
+                if (!((see[k >> 5] >> (k & 31)) & 1u)) s[k] = -INFINITY;
+            }
+            float top[4] = {s[0], s[1], s[2], s[3]};
+#pragma unroll
+            for (int k = 4; k < kTile; k += 8) {
+#pragma unroll
+              for (int i = 0; i < 4; ++i)
+                top[i] = k + 4 + i < kTile ? max3(top[i], s[k + i], s[k + 4 + i]) : fmaxf(top[i], s[k + i]);
+            }
+            float mx = fmaxf(fmaxf(top[0], top[1]), fmaxf(top[2], top[3]));
+            mx *= P.c;
+            if (j == 0) {
+              m = mx;
+            } else {
+              const bool grow = mx > m + kRescale;
+              if (__any_sync(kFull, grow)) {
+                const float keep = grow ? ex2_approx(m - mx) : 1.f;
+                if (grow) {
+                  m = mx;
+                  l *= keep;
+                }
+#pragma unroll
+                for (int i = 0; i < kCols / 16; ++i) {
+                  float o[16];
+                  tmem_ld16(to + 16 * i, o);
+                  loaded<16>(o);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k) o[k] *= keep;
+                  tmem_st16(to + 16 * i, reinterpret_cast<const uint32_t*>(o));
+                }
+              }
+            }
+            const float off = m == -INFINITY ? 0.f : m;
+            const uint64_t c2 = pair(P.c, P.c), off2 = pair(-off, -off);
+            uint64_t sum[2] = {0ull, 0ull};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+              uint32_t pk[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) {
+                const uint64_t x = fma2(pair(s[32 * i + 2 * k], s[32 * i + 2 * k + 1]), c2, off2);
+                const float a = ex2_approx(low(x)), b = ex2_approx(high(x));
+                sum[k & 1] = add2(sum[k & 1], pair(a, b));
+                pk[k] = pack2<T>(a, b);
+              }
+              tmem_st16(ts + 16 * i, pk);
+            }
+            sum[0] = add2(sum[0], sum[1]);
+            l += low(sum[0]) + high(sum[0]);
+            tc_wait_st();
+          }
+          // V rows behind the end may hold anything, and 0 * NaN is NaN: those that
+          // share a step of 16 with valid rows are cleared (by either half, which write the same)
+          if (j == n - 1 && w.t1 == w.tiles) {
+            const int valid = max(0, min(w.end - p0, kTile));
+            const int upto = max(16, (valid + 15) / 16 * 16);
+            if (valid < upto) {
+              const uint32_t i = idx + v_load(j, n);
+              ok = wait_warp(&sh->kv_full[i % kStages], (i / kStages) & 1u, sh, P.wait_limit);
+              if (!ok) break;
+              const int r = valid + ((tid & 127) >> 3);
+              if (r < upto)
+#pragma unroll
+                for (int hf = 0; hf < DH; ++hf)
+                  *reinterpret_cast<uint4*>(ring + (i % kStages) * kStageBytes + hf * kHalfTileBytes + r * kColBytes +
+                                            (tid & 7) * 16) = make_uint4(0, 0, 0, 0);
+              fence_async();
             }
           }
+          tc_before();
           __syncwarp();
-          tmem_st8(to + col, reinterpret_cast<const uint32_t*>(o));
+          if (lane == 0) mbar_arrive(&sh->p_full[t]);
         }
-        tc_wait_st();
-      }
-      if (d_t0 == 0 && d_after == 0) {
-        // A thread's row leaves 32 (or 16) bytes at a time: whole sectors, and
-        // nothing to wait for.  (Through shared memory the rows would leave in
-        // whole lines, but the next queries would have to wait for the buffer.)
-        const float inv = l > 0.f ? 1.f / l : 0.f;
-        if (warp_on) {
-          const long long tok = d_start + token;
-          const int head = d_h * P.G + g - token * P.G;
-          T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
+        if (!ok) break;
+        idx += 2 * n;
+
+        // the finished part, while the next one's queries are already on their way
+        const int d_start = w.c.start, d_h = w.h, d_row0 = w.blk * kBlockRows, d_rows = w.rows, d_t0 = w.t0;
+        const int d_after = w.tiles - w.t1;                // the block's tiles in later CTAs
+        const int d_b = w.b, d_odd0 = open_end < w.end ? max(open_end / kTile, w.t0) * kTile : w.end;
+        const int d_odd1 = min(w.t1 * kTile, w.end);       // rows differ in what they see of d_odd0 .. d_odd1
+        more = w.next(P);
+        skip_inactive();
+        if (more) ask_q();
+        ok = wait_warp(&sh->o_full[t], o_seen++ & 1u, sh, P.wait_limit);
+        if (!ok) break;
+        tc_after();
+        const bool differ = d_odd0 < d_odd1;
+        uint64_t odd = 0ull;                               // 0 while all is finite, else NaN
+        auto look = [&](const float* o) {
+#pragma unroll
+          for (int k = 0; k < 32; k += 2) odd = fma2(pair(o[k], o[k + 1]), 0ull, odd);
+        };
+        if (kCareful && differ && warp_on) {         // what take_out took is given to the rows that see it
+          const int32_t* table = P.table + (long long)d_b * P.table_stride;
+#pragma unroll 1
+          for (int col = 0; col < P.D; col += 8) {
+            float o[8];
+            tmem_ld8(to + col, o);
+            loaded<8>(o);
+#pragma unroll 1
+            for (int p = d_odd0; p < d_odd1; ++p) {
+              const int x = p - tree, pg = P.by_page.div(p), page = table[pg];
+              const bool sees = p < plain || (x >= 0 && x < nodes && (bits[x >> 5] >> (x & 31) & 1u));
+              if (!sees || page < 0 || page >= P.pages) continue;
+              const T* src = static_cast<const T*>(P.v) + page * P.v_ps + (p - pg * P.page) * P.v_rs + d_h * P.v_hs;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) {
+                const float y = float(src[col + k]);
+                if (!(fabsf(y) < INFINITY)) o[k] += y;
+              }
+            }
+            __syncwarp();
+            tmem_st8(to + col, reinterpret_cast<const uint32_t*>(o));
+          }
+          tc_wait_st();
+        }
+        if (d_t0 == 0 && d_after == 0) {
+          // A thread's row leaves 32 (or 16) bytes at a time: whole sectors, and
+          // nothing to wait for.  (Through shared memory the rows would leave in
+          // whole lines, but the next queries would have to wait for the buffer.)
+          const float inv = l > 0.f ? 1.f / l : 0.f;
+          if (warp_on) {
+            const long long tok = d_start + token;
+            const int head = d_h * P.G + g - token * P.G;
+            T* dst = static_cast<T*>(P.out) + tok * P.o_ts + (long long)head * P.o_hs;
+#pragma unroll
+            for (int i = 0; i < kCols / 32; ++i) {
+              float o[32];
+              tmem_ld32(to + 32 * i, o);
+              loaded<32>(o);
+              if (!kCareful) look(o);
+              uint32_t y[16];
+#pragma unroll
+              for (int k = 0; k < 16; ++k) y[k] = pack2<T>(o[2 * k] * inv, o[2 * k + 1] * inv);
+#pragma unroll
+              for (int k = 0; k < 2; ++k) {
+                T* to_row = dst + 32 * i + 16 * k;
+                // (305 us for 314 with 16 bytes, 2 x 1024 tokens over 16384 positions)
+                if (P.wide_out) {
+                  if (row_on && 32 * i + 16 * k < P.D) stg_v8(to_row, y + 8 * k);
+                } else {
+                  if (row_on && 32 * i + 16 * k < P.D)
+                    *reinterpret_cast<uint4*>(to_row) = make_uint4(y[8 * k], y[8 * k + 1], y[8 * k + 2], y[8 * k + 3]);
+                  if (row_on && 32 * i + 16 * k + 8 < P.D)
+                    *reinterpret_cast<uint4*>(to_row + 8) =
+                        make_uint4(y[8 * k + 4], y[8 * k + 5], y[8 * k + 6], y[8 * k + 7]);
+                }
+              }
+              if (i == 0 && more) give_q();
+            }
+            if (row_on && P.lse) P.lse[tok * P.Hq + head] = log_sum(m, l);
+          }
+        } else if (warp_on) {
+          // [4 columns][row] so that a warp writes whole lines, then (m, l) of each row
+          float4* dst = part_slot<kCols>(P, blockIdx.x, d_t0 > 0 ? 0 : 1);
 #pragma unroll
           for (int i = 0; i < kCols / 32; ++i) {
             float o[32];
             tmem_ld32(to + 32 * i, o);
             loaded<32>(o);
             if (!kCareful) look(o);
-            uint32_t y[16];
 #pragma unroll
-            for (int k = 0; k < 16; ++k) y[k] = pack2<T>(o[2 * k] * inv, o[2 * k + 1] * inv);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-              T* to_row = dst + 32 * i + 16 * k;
-              // (305 us for 314 with 16 bytes, 2 x 1024 tokens over 16384 positions)
-              if (P.wide_out) {
-                if (row_on && 32 * i + 16 * k < P.D) stg_v8(to_row, y + 8 * k);
-              } else {
-                if (row_on && 32 * i + 16 * k < P.D)
-                  *reinterpret_cast<uint4*>(to_row) = make_uint4(y[8 * k], y[8 * k + 1], y[8 * k + 2], y[8 * k + 3]);
-                if (row_on && 32 * i + 16 * k + 8 < P.D)
-                  *reinterpret_cast<uint4*>(to_row + 8) =
-                      make_uint4(y[8 * k + 4], y[8 * k + 5], y[8 * k + 6], y[8 * k + 7]);
-              }
-            }
+            for (int k = 0; k < 8; ++k)
+              if (row_on)
+                dst[(8 * i + k) * P.slot_rows + my_row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
             if (i == 0 && more) give_q();
           }
-          if (row_on && P.lse) P.lse[tok * P.Hq + head] = log_sum(m, l);
+          if (row_on) reinterpret_cast<float2*>(dst + kCols / 4 * P.slot_rows)[my_row] = make_float2(m, l);
         }
-      } else if (warp_on) {
-        // [4 columns][row] so that a warp writes whole lines, then (m, l) of each row
-        float4* dst = part_slot<kCols>(P, blockIdx.x, d_t0 > 0 ? 0 : 1);
-#pragma unroll
-        for (int i = 0; i < kCols / 32; ++i) {
-          float o[32];
-          tmem_ld32(to + 32 * i, o);
-          loaded<32>(o);
-          if (!kCareful) look(o);
-#pragma unroll
-          for (int k = 0; k < 8; ++k)
-            if (row_on)
-              dst[(8 * i + k) * P.slot_rows + my_row] = make_float4(o[4 * k], o[4 * k + 1], o[4 * k + 2], o[4 * k + 3]);
-          if (i == 0 && more) give_q();
+        if (!kCareful && odd != 0ull && differ && row_on) *reinterpret_cast<volatile int*>(&sh->odd) = 1;
+        if (!warp_on && more) give_q();
+        if (t == 0 && warp == 0 && lane == 0 && d_t0 == 0 && d_after > 0) {
+          // the span ends within the block: the joint names it and the CTAs that share it
+          const Span& sp = sh->span;
+          Joint jt;
+          jt.parts = int(((sp.u1 + d_after) * sp.ctas - 1) / sp.total) - int(blockIdx.x) + 1;
+          jt.rows = d_rows;
+          jt.row0 = d_row0;
+          jt.head = d_h;
+          jt.token0 = d_start;
+          P.joints[blockIdx.x] = jt;
         }
-        if (row_on) reinterpret_cast<float2*>(dst + kCols / 4 * P.slot_rows)[my_row] = make_float2(m, l);
       }
-      if (!kCareful && odd != 0ull && differ && row_on) *reinterpret_cast<volatile int*>(&sh->odd) = 1;
-      if (!warp_on && more) give_q();
-      if (t == 0 && warp == 0 && lane == 0 && d_t0 == 0 && d_after > 0) {
-        // the span ends within the block: the joint names it and the CTAs that share it
-        const Span& sp = sh->span;
-        Joint jt;
-        jt.parts = int(((sp.u1 + d_after) * sp.ctas - 1) / sp.total) - int(blockIdx.x) + 1;
-        jt.rows = d_rows;
-        jt.row0 = d_row0;
-        jt.head = d_h;
-        jt.token0 = d_start;
-        P.joints[blockIdx.x] = jt;
-      }
-    }
     };
     span_of(std::false_type{});
     if (go_over_again(sh)) span_of(std::true_type{});
@@ -1132,7 +1142,7 @@ extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_
   if ((long long)T * q_heads >= (1ll << 31)) return DART_ERR_INVALID_ARG;
   const int rc = check_cache(cache, B);
   if (rc) return rc;
-  if (q_heads % cache->heads != 0 || !std::isfinite(scale)) return DART_ERR_INVALID_ARG;
+  if (q_heads % cache->heads != 0 || !std::isfinite(scale * 1.44269504f)) return DART_ERR_INVALID_ARG;
   if (T == 0 || B == 0) return DART_OK;
   if (cache->pages < 1 || cache->table_width < 1) return DART_ERR_INVALID_ARG;
   if (!aligned16(q) || !aligned16(out) || !mult8(q_token_stride, q_head_stride) ||
@@ -1149,7 +1159,8 @@ extern "C" int dart_tree_attention(const void* q, int64_t q_token_stride, int64_
   P.Hq = q_heads; P.Hkv = c.heads; P.G = q_heads / c.heads; P.D = c.dim;
   P.T = T; P.B = B; P.N = N; P.MW = (N + 31) / 32;
   P.lengths = lengths; P.starts = starts; P.mask = mask;
-  P.c = scale == 0.f ? 1e-30f : std::fabs(scale) * 1.44269504088896341f;
+  // the least positive number for scale 0: any finite score becomes next to nothing, -inf stays -inf
+  P.c = scale == 0.f ? std::numeric_limits<float>::denorm_min() : std::fabs(scale) * 1.44269504088896341f;
   P.negate = scale < 0.f ? 1u << 13 : 0u;
   P.wide_out = c.dim % 16 == 0 && (reinterpret_cast<uintptr_t>(out) & 31) == 0 &&
                ((out_token_stride | out_head_stride) & 15) == 0;

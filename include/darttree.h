@@ -458,7 +458,8 @@ int dart_rotary_pack_host(const double* freqs, int count, uint64_t* turns);
  *  q, out   device [T][q_heads][dim] (token and head strides in elements,
  *           multiples of 8; bases 16-byte aligned); out receives the finished
  *           queries and may be q itself.  q_heads = 0: no queries.
- *  k, v     device [T][cache->heads][dim], strides as for q
+ *  k, v     device [T][cache->heads][dim], strides as for q; none of q, k, v
+ *           and out overlaps the cache
  *  lengths  device [B], tokens in the cache before the chunk, >= 0
  *  starts   device [B+1], increasing, starts[b] <= T
  *  offsets  device [T] or NULL
@@ -496,7 +497,7 @@ size_t dart_attention_workspace_bytes(int T, int B, int q_heads, int heads, int 
  *  q_heads  a multiple of cache->heads; T * q_heads < 2^31
  *  mask     device uint32 [B][N][ceil(N/32)], or NULL with N = 0 (causal);
  *           N <= 1024
- *  scale    finite
+ *  scale    finite, also times log2 e
  *  out_lse  device float [T][q_heads] or NULL
  *  workspace  device, >= dart_attention_workspace_bytes(...), 256-byte
  *           aligned; its first 256 bytes zero-filled before the first use

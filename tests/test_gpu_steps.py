@@ -134,3 +134,37 @@ def test_a_verification_step(D):
     torch.cuda.synchronize()
     assert torch.equal(again[0]["tokens"], tree["tokens"]) and torch.equal(again[2]["out"], att["out"])
     assert torch.equal(again[4].view(torch.int16), final.view(torch.int16))
+
+
+@pytest.mark.parametrize("heads_first", [False, True])
+def test_pages_whose_offsets_pass_32_bits(D, heads_first):
+    """A cache of 2^32 elements and more: the pages at its end serve like those of a small cache, and the tokens
+    before the first sequence and behind the last one stay as they were."""
+    gen = torch.Generator(device="cuda").manual_seed(21)
+    hq, hkv, dim, page, B, width = 8, 4, 128, 64, 3, 5
+    count = 2 ** 32 // (page * hkv * dim) + B * width + 1
+    shape = (count, hkv, page, dim) if heads_first else (count, page, hkv, dim)
+    far = [torch.empty(shape, dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    near = [torch.zeros((B * width,) + shape[1:], dtype=torch.bfloat16, device="cuda") for _ in range(2)]
+    low = torch.arange(B * width, dtype=torch.int32, device="cuda").view(B, width)
+    high = low + (count - B * width)
+    for f, n in zip(far, near):
+        n.normal_(generator=gen)
+        f[-B * width:] = n
+    lengths = torch.tensor([100, 0, 250], dtype=torch.int32, device="cuda")
+    starts = torch.tensor([2, 42, 43, 103], dtype=torch.int32, device="cuda")
+    qkv = torch.randn(106, hq + 2 * hkv, dim, device="cuda", generator=gen).bfloat16()
+    results = []
+    for caches, pages in ((near, low), (far, high)):
+        view = [c.transpose(1, 2) if heads_first else c for c in caches]
+        q = torch.full((106, hq, dim), 3.0, dtype=torch.bfloat16, device="cuda")
+        err = torch.zeros(1, dtype=torch.int32, device="cuda")
+        D.kv_append(qkv[:, :hq], qkv[:, hq:hq + hkv], qkv[:, hq + hkv:], *view, pages, lengths, starts,
+                    rotary=D.Rotary(*D.rotary_frequencies(dim)), out=q, device_err=err)
+        att = D.tree_attention(q, *view, pages, lengths, starts, out=torch.full_like(q, 4.0))
+        assert int(err) == 0 and D.device_error(att["workspace"]) == 0
+        assert bool((q[[0, 1, 103, 104, 105]] == 3).all()) and bool((att["out"][[0, 1, 103, 104, 105]] == 4).all())
+        results.append((q, att["out"], caches[0][-B * width:].clone(), caches[1][-B * width:].clone()))
+    for a, b in zip(*results):
+        assert torch.equal(a, b)
+    assert not torch.equal(results[0][2], torch.zeros_like(results[0][2]))

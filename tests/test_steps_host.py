@@ -116,7 +116,7 @@ def _attend(L, cache=None, **kw):
 def test_attention_argument_checks(L):
     assert _attend(L, None) == INVALID
     for kw in (dict(Hq=3), dict(Hq=0), dict(T=-1), dict(B=-1), dict(N=-1), dict(N=1025), dict(scale=math.nan),
-               dict(scale=math.inf), dict(T=3, q=0), dict(T=3, out=FAKE + 8), dict(T=3, ts=260), dict(T=3, lengths=0),
+               dict(scale=math.inf), dict(scale=2.9e38), dict(T=3, q=0), dict(T=3, out=FAKE + 8), dict(T=3, ts=260), dict(T=3, lengths=0),
                dict(T=3, starts=0), dict(T=3, N=5)):
         assert _attend(L, _cache(), **kw) == INVALID, kw
     for kw in (dict(ws=0), dict(ws=FAKE + 64), dict(wsb=100)):

@@ -2,12 +2,16 @@
 
 Each translation unit compiles in parallel, then one nvcc call links the
 shared library next to this file.  Objects go to ``_build/`` (git-ignored).
+The Python module _steps_native (host C++ against PyTorch's headers, no device
+code) is compiled beside them, with the host compiler.
 """
 from __future__ import annotations
 
 import os
+import shutil
 import subprocess
 import sys
+import sysconfig
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -15,26 +19,41 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdarttree.so")
+NATIVE = os.path.join(HERE, "_steps_native.so")
+NATIVE_SOURCE = os.path.join(CSRC, "dart_steps_py.cpp")
 SOURCES = ["dart_api.cu", "dart_rows.cu", "dart_tree.cu", "dart_select.cu", "dart_probe.cu",
            "dart_adjust.cu", "dart_append.cu", "dart_attend.cu"]
 
 NVCC = os.environ.get("NVCC", "nvcc")
+CXX = os.environ.get("CXX", "g++")
 ARCH = ["-gencode", "arch=compute_103a,code=sm_103a"]
 FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE, "-I", CSRC]
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES]
+    files = [os.path.join(CSRC, s) for s in SOURCES] + [NATIVE_SOURCE]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "darttree.h"))
     return files
 
 
 def needs_build() -> bool:
-    if not os.path.exists(LIB):
+    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
         return True
-    t = os.path.getmtime(LIB)
+    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
     return any(os.path.getmtime(f) > t for f in _inputs())
+
+
+def _native_command(target: str) -> list[str]:
+    import torch
+    home = os.path.dirname(torch.__file__)
+    cuda = os.path.dirname(os.path.dirname(os.path.realpath(shutil.which(NVCC) or "/usr/local/cuda/bin/nvcc")))
+    return [CXX, "-O2", "-std=c++17", "-shared", "-fPIC", f"-D_GLIBCXX_USE_CXX11_ABI={int(torch.compiled_with_cxx11_abi())}",
+            "-I", INCLUDE, "-isystem", os.path.join(home, "include"),
+            "-isystem", os.path.join(home, "include", "torch", "csrc", "api", "include"),
+            "-isystem", os.path.join(cuda, "include"), "-isystem", sysconfig.get_paths()["include"], NATIVE_SOURCE,
+            "-o", target, "-L", os.path.join(home, "lib"), "-ltorch_python", "-ltorch_cpu", "-lc10", "-lc10_cuda",
+            f"-Wl,-rpath,{os.path.join(home, 'lib')}"]
 
 
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
@@ -51,6 +70,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
+    native = NATIVE + ".tmp"
+    procs.append((os.path.basename(NATIVE_SOURCE), subprocess.Popen(_native_command(native), stdout=subprocess.PIPE,
+                                                                    stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -60,10 +82,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"nvcc failed:\n{msg}")
+        raise RuntimeError(f"compilation failed:\n{msg}")
     tmp = LIB + ".tmp"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
+    os.replace(native, NATIVE)
     os.replace(tmp, LIB)
     return LIB
 

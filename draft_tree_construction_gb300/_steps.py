@@ -8,7 +8,9 @@ from __future__ import annotations
 import contextlib
 import ctypes as C
 import functools
+import importlib.util
 import math
+import os
 
 import numpy as np
 
@@ -56,8 +58,30 @@ def declare(L):
     L.dart_tree_attention.restype = i32
 
 
-# A call's host work is a good part of a small call's time, so the checks here
-# decide on plain integers and only a failing one looks for its words.
+# A call's host work is a good part of a small call's time: _steps_native makes
+# the usual calls, and returns None for those that it leaves to the code here (a
+# stream is given, the tensors are not on the current device, something is empty
+# or wrong).  The checks here decide on plain integers and only a failing one
+# looks for its words.
+
+_native = None
+
+
+def _load_native():
+    global _native
+    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_steps_native.so")
+    L = lib()
+    if not os.path.exists(path):
+        raise DartError(f"{path} is missing: run draft_tree_construction_gb300.build()")
+    _torch()                                   # its libraries first
+    spec = importlib.util.spec_from_file_location("_steps_native", path)
+    module = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(module)
+    module.bind(*(C.cast(f, C.c_void_p).value for f in (L.dart_logits_adjust, L.dart_kv_append, L.dart_tree_attention,
+                                                        L.dart_attention_workspace_bytes)))
+    _native = module
+    return module
+
 
 @contextlib.contextmanager
 def _elsewhere(dev, stream):
@@ -127,8 +151,13 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
     returns them, let row R - N + i count the tokens on node i's path too; R
     is N or N + 1.  Returns the adjusted logits: out, which may be logits
     itself, or a new [B, R, V] tensor with evenly spaced rows."""
-    torch = _torch()
     ids, vals = bias if bias is not None else (None, None)
+    if stream is None and logits.is_cuda:
+        made = (_native or _load_native()).adjust(logits, history, lengths, repetition, presence, frequency, ids, vals,
+                                                  allowed, tokens, mask, out)
+        if made is not None:
+            return made
+    torch = _torch()
     dev = _one_device(("logits", "history", "lengths", "repetition", "presence", "frequency", "bias ids",
                        "bias values", "allowed", "tokens", "mask", "out"),
                       (logits, history, lengths, repetition, presence, frequency, ids, vals, allowed, tokens, mask,
@@ -309,6 +338,7 @@ class Rotary:
         self.rot = 2 * freqs.size
         self.turns = _torch().from_numpy(turns.view(np.int64)).to(device)
         self.desc = _Rotary(self.turns.data_ptr(), self.magnitude, self.rot, int(self.interleaved), 0)
+        self.address = C.addressof(self.desc)
 
 
 def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, original: int | None = None,
@@ -349,6 +379,12 @@ def kv_append(q, k, v, k_cache, v_cache, pages, lengths, starts, *, rotary: Rota
     every sequence are unset (None without q).  device_err (int32 [>= 1], zeroed
     by the caller) collects the error bits of tokens that do not fit in their
     pages."""
+    if stream is None and k.is_cuda:
+        turns, address = (rotary.turns, rotary.address) if rotary is not None else (None, 0)
+        made = (_native or _load_native()).append(q, k, v, k_cache, v_cache, pages, lengths, starts, turns, address,
+                                                  offsets, q_weight, k_weight, eps, out, device_err)
+        if made is not None:
+            return made
     torch = _torch()
     dev = _one_device(("k", "v", "q", "k_cache", "v_cache", "pages", "lengths", "starts", "rotary", "offsets",
                        "q_weight", "k_weight", "out", "device_err"),
@@ -419,6 +455,11 @@ def tree_attention(q, k_cache, v_cache, pages, lengths, starts, *, mask=None, sc
     with lse=True, else None) and the workspace, whose error bits device_error
     reads.  A workspace is reused by calls in order on one stream; calls that
     may overlap need one each."""
+    if stream is None and q.is_cuda:
+        made = (_native or _load_native()).attend(q, k_cache, v_cache, pages, lengths, starts, mask, scale, out, lse,
+                                                  workspace)
+        if made is not None:
+            return {"out": made[0], "lse": made[1], "workspace": made[2]}
     torch = _torch()
     dev = _one_device(("q", "k_cache", "v_cache", "pages", "lengths", "starts", "mask", "out", "workspace"),
                       (q, k_cache, v_cache, pages, lengths, starts, mask, out, workspace))

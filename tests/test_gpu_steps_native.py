@@ -1,0 +1,184 @@
+"""The calls that _steps_native makes against the same calls by the Python binding (needs a GB300).
+
+Both end in the same entry point, so the results are the same bits; what the
+native module does not take must come out as the binding's error.
+"""
+import sys
+import types
+
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+
+@pytest.fixture(scope="module")
+def D():
+    import draft_tree_construction_gb300 as D
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    D.build()
+    return D
+
+
+@pytest.fixture
+def both(D, monkeypatch):
+    """Runs a call natively (it must be taken) and by the binding alone."""
+    from draft_tree_construction_gb300 import _steps
+    native = _steps._load_native()
+
+    def run(name, call):
+        taken = []
+
+        def watch(f):
+            def g(*args):
+                r = f(*args)
+                taken.append(r is not None)
+                return r
+            return g
+        monkeypatch.setattr(_steps, "_native", types.SimpleNamespace(**{name: watch(getattr(native, name))}))
+        a = call()
+        monkeypatch.setattr(_steps, "_native", types.SimpleNamespace(**{name: lambda *args: None}))
+        b = call()
+        monkeypatch.setattr(_steps, "_native", native)
+        assert taken == [True]
+        return a, b
+    return run
+
+
+def _i32(*s, high=50):
+    return torch.randint(0, high, s, dtype=torch.int32, device="cuda")
+
+
+@pytest.mark.parametrize("dtype,pad", [(torch.float32, 0), (torch.bfloat16, 5), (torch.float16, 8)])
+def test_adjust(both, D, dtype, pad):
+    B, R, V, N = 3, 6, 1001, 5
+    z = torch.randn(B, R, V + pad, device="cuda").to(dtype)[..., :V]
+    f = lambda: torch.rand(B, device="cuda") + 0.5
+    kw = dict(history=_i32(B, 20)[:, :17], lengths=_i32(B, high=18), repetition=f(), presence=f(), frequency=f(),
+              bias=(_i32(B, 9), torch.randn(B, 9, device="cuda")), tokens=_i32(B, N), mask=_i32(B, N, 1, high=31))
+    for allowed in (None, _i32(B, 32, high=2 ** 31 - 1), _i32(B, R, 40, high=2 ** 31 - 1)[..., :32]):
+        a, b = both("adjust", lambda: D.adjust_logits(z, allowed=allowed, **kw))
+        assert a.shape == z.shape and a.dtype == dtype and a.stride() == b.stride()
+        assert torch.equal(a.nan_to_num(), b.nan_to_num())
+        out = torch.empty(B, R, V + 3, device="cuda", dtype=dtype)[..., :V]
+        a, b = both("adjust", lambda: D.adjust_logits(z, allowed=allowed, out=out, **kw))
+        assert a is out and b is out
+    a, b = both("adjust", lambda: D.adjust_logits(z[:1, :1], allowed=_i32(1, 32)[:1] | -1))
+    assert torch.equal(a, z[:1, :1]) and torch.equal(b, a)
+
+
+def _cached(B=3, T=70, Hq=8, Hkv=2, dim=128, page=16, width=12):
+    qkv = torch.randn(T, Hq + 2 * Hkv, dim, device="cuda").bfloat16()
+    caches = [torch.randn(B * width, page, Hkv, dim, device="cuda").bfloat16() for _ in range(2)]
+    pages = torch.randperm(B * width, device="cuda").int().view(B, width)
+    return dict(q=qkv[:, :Hq], k=qkv[:, Hq:Hq + Hkv], v=qkv[:, Hq + Hkv:], k_cache=caches[0], v_cache=caches[1],
+                pages=pages, lengths=torch.tensor([3, 0, 77], dtype=torch.int32, device="cuda"),
+                starts=torch.tensor([0, 20, 60, 70], dtype=torch.int32, device="cuda"))
+
+
+def test_append(both, D):
+    a = _cached()
+    rotary, err = D.Rotary(*D.rotary_frequencies(64), interleaved=True), torch.zeros(1, dtype=torch.int32, device="cuda")
+    w = torch.rand(128, device="cuda").bfloat16()
+    for kw in (dict(), dict(rotary=rotary, offsets=_i32(70), q_weight=w, k_weight=w, device_err=err),
+               dict(rotary=rotary, out=torch.empty(70, 8, 136, dtype=torch.bfloat16, device="cuda")[..., :128])):
+        caches = []
+
+        def call():
+            caches.append((a["k_cache"].clone(), a["v_cache"].clone()))
+            return D.kv_append(**dict(a, k_cache=caches[-1][0], v_cache=caches[-1][1]), **kw).clone()
+        x, y = both("append", call)
+        assert torch.equal(x, y)
+        for c, d, before in zip(*caches, (a["k_cache"], a["v_cache"])):
+            assert torch.equal(c, d) and not torch.equal(c, before)
+    assert int(err) == 0
+
+
+def test_attend(both, D):
+    a = _cached()
+    del a["k"], a["v"]
+    a["q"] = a["q"].contiguous()
+    ws = torch.zeros(D.attention_workspace_bytes(70, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    for kw in (dict(), dict(mask=_i32(3, 9, 1, high=2 ** 9), lse=True), dict(scale=0.3, workspace=ws),
+               dict(out=torch.empty(70, 8, 136, dtype=torch.bfloat16, device="cuda")[..., :128], workspace=ws)):
+        results = []
+
+        def call():
+            r = D.tree_attention(**a, **kw)
+            results.append(r["out"].clone())
+            return r
+        x, y = both("attend", call)
+        assert torch.equal(*results)
+        assert (x["lse"] is None) == (y["lse"] is None) == ("lse" not in kw)
+        if x["lse"] is not None:
+            assert torch.equal(x["lse"], y["lse"])
+        if "out" in kw:
+            assert x["out"] is kw["out"]
+        if "workspace" in kw:
+            assert x["workspace"] is ws
+        assert D.device_error(x["workspace"]) == 0
+
+
+def test_the_current_stream_and_graphs(D):
+    z, f = torch.randn(2, 3, 5000, device="cuda"), torch.full((2,), 2.0, device="cuda")
+    hist = _i32(2, 30)
+    want = D.adjust_logits(z, history=hist, repetition=f)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        got = D.adjust_logits(z, history=hist, repetition=f)
+    torch.cuda.current_stream().wait_stream(side)
+    assert torch.equal(got, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        got = D.adjust_logits(z, history=hist, repetition=f)
+    z.add_(1.0)
+    graph.replay()
+    assert torch.equal(got, D.adjust_logits(z, history=hist, repetition=f))
+
+
+def test_references_are_kept_in_balance(D):
+    a = _cached()
+    q = a["q"].contiguous()
+    ws = torch.zeros(D.attention_workspace_bytes(70, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+    out = torch.empty_like(q)
+    args = (q, a["k_cache"], a["v_cache"], a["pages"], a["lengths"], a["starts"])
+    z = torch.randn(1, 1, 64, device="cuda")
+    watched = (*args, ws, out, z, None)
+    before = [sys.getrefcount(x) for x in watched[:-1]]
+    for _ in range(50):
+        D.tree_attention(*args, out=out, workspace=ws)
+        D.adjust_logits(z, out=z)
+        D.kv_append(q, a["k"], a["v"], *args[1:], out=out)
+    assert [sys.getrefcount(x) for x in watched[:-1]] == before
+
+
+def test_what_is_wrong_raises_as_ever(D):
+    from draft_tree_construction_gb300 import DartError
+    z, i32, f32 = torch.randn(2, 6, 100, device="cuda"), _i32, lambda *s: torch.zeros(s, device="cuda")
+    for kw in (dict(history=i32(3, 9)), dict(history=i32(2, 9).long()), dict(history=i32(9, 2).t()),
+               dict(lengths=i32(2)), dict(history=i32(2, 9), lengths=i32(3)), dict(repetition=f32(3)),
+               dict(repetition=f32(2).cpu()), dict(presence=f32(2).double()), dict(bias=(i32(2, 3), None)),
+               dict(bias=(i32(2, 3), f32(2, 4))), dict(bias=(i32(2, 2000), f32(2, 2000))), dict(allowed=i32(2, 3)),
+               dict(allowed=f32(2, 4)), dict(tokens=i32(2, 5)), dict(tokens=i32(2, 4), mask=i32(2, 4, 1)),
+               dict(out=z.half()), dict(out=f32(2, 6, 101)), dict(out=f32(1, 6, 100).expand(2, 6, 100))):
+        with pytest.raises(DartError):
+            D.adjust_logits(z, **kw)
+    a = _cached()
+    h = lambda *s: torch.zeros(s, dtype=torch.bfloat16, device="cuda")
+    for kw in (dict(q=h(70, 8, 64)), dict(k=h(70, 3, 128)), dict(v=h(70, 2, 132)[..., :128][..., 4:]),
+               dict(k_cache=a["k_cache"].half()), dict(pages=i32(2, 3)), dict(lengths=i32(3).long()),
+               dict(starts=i32(3)), dict(offsets=i32(6)), dict(q_weight=h(64)), dict(out=h(1, 8, 128).expand(70, 8, 128)),
+               dict(q=None, out=h(70, 8, 128)), dict(device_err=h(1)), dict(eps=-1.0),
+               dict(k_cache=h(1, 16, 2, 128).expand(36, 16, 2, 128))):
+        with pytest.raises(DartError):
+            D.kv_append(**dict(a, **kw))
+    del a["k"], a["v"]
+    a["q"] = a["q"].contiguous()
+    for kw in (dict(q=h(70, 3, 128)), dict(q=a["q"].float()), dict(mask=i32(3, 40, 1)), dict(mask=i32(2, 40, 2)),
+               dict(out=a["q"]), dict(out=h(70, 8, 64)), dict(scale=float("nan")), dict(lengths=i32(3).cpu()),
+               dict(workspace=torch.zeros(100, dtype=torch.uint8, device="cuda"))):
+        with pytest.raises(DartError):
+            D.tree_attention(**dict(a, **kw))

@@ -248,3 +248,11 @@ def test_attention_binding_checks(on_cpu):
     for kw in bad:
         with pytest.raises(DartError):
             D.tree_attention(**dict(a, **kw))
+
+
+def test_the_native_module_leaves_what_is_not_on_the_device():
+    D.build()
+    native = _steps._load_native()
+    assert native.adjust(1, 2) is None and native.append() is None and native.attend(None) is None
+    with pytest.raises(TypeError):
+        native.bind(1, 2)

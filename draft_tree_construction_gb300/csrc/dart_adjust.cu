@@ -228,9 +228,10 @@ adjust_kernel(const AdjustParams P) {
     if (allow) ask(r + 1);
   };
 
-  // Everything that the slice needs from memory is asked for before anything waits.
+  // Everything that the slice needs from memory is asked for before anything waits
+  // (of a long history the first kAhead entries a thread, then kMore at a time).
   if (kRing && allow) ask(r_begin);
-  constexpr int kAhead = 8, kBiasAhead = kMaxBias / kAdjThreads;
+  constexpr int kAhead = 8, kMore = 16, kBiasAhead = kMaxBias / kAdjThreads;
   const int32_t* hist = P.count && a.history ? a.history + (long long)b * a.history_stride : nullptr;
   const int width = hist ? a.history_width : 0;
   int32_t id[kAhead], bias_id[kBiasAhead];
@@ -268,19 +269,21 @@ adjust_kernel(const AdjustParams P) {
   if (paths)
     for (int i = tid; i < a.N; i += kAdjThreads) toks[i] = int16_t(local(a.tokens[(long long)b * a.N + i]));
   __syncthreads();
-  for (int i0 = tid; i0 < len; i0 += kAhead * kAdjThreads) {
-    if (i0 != tid) {
-#pragma unroll
-      for (int k = 0; k < kAhead; ++k) id[k] = i0 + k * kAdjThreads < len ? hist[i0 + k * kAdjThreads] : -1;
+  auto tally = [&](int i, int32_t token) {
+    const int t = i < len ? local(token) : -1;
+    if (t >= 0) {
+      atomicAdd(&counts[t], 1u);
+      atomicOr(&touched[t >> 5], 1u << (t & 31));
     }
+  };
 #pragma unroll
-    for (int k = 0; k < kAhead; ++k) {
-      const int t = i0 + k * kAdjThreads < len ? local(id[k]) : -1;
-      if (t >= 0) {
-        atomicAdd(&counts[t], 1u);
-        atomicOr(&touched[t >> 5], 1u << (t & 31));
-      }
-    }
+  for (int k = 0; k < kAhead; ++k) tally(tid + k * kAdjThreads, id[k]);
+  for (int i0 = tid + kAhead * kAdjThreads; i0 < len; i0 += kMore * kAdjThreads) {
+    int32_t more[kMore];
+#pragma unroll
+    for (int k = 0; k < kMore; ++k) more[k] = i0 + k * kAdjThreads < len ? hist[i0 + k * kAdjThreads] : -1;
+#pragma unroll
+    for (int k = 0; k < kMore; ++k) tally(i0 + k * kAdjThreads, more[k]);
   }
   if (a.bias_count > 0) {
     // The slice's biases, compacted in their order; then the first entry of
@@ -574,6 +577,12 @@ cudaError_t launch_adjust(AdjustParams P, int B, cudaStream_t stream) {
   // against 210 and 58.
   const long long want = 152ll * 3 * 2, per = (long long)slices * B;
   long long groups = (want + per - 1) / per;
+  // Each CTA counts the whole history, which takes it about as long as one row per
+  // 2048 entries, so beyond one round of CTAs a long one wants more rows each: 24 x 5
+  // fp32 rows of 32000 with 14312 tokens 42 -> 20 us, 83 x 4 of 9640 with 12285 26 -> 18.
+  const long long rows = 1 + (P.count ? P.a.history_width / 2048 : 0), round = 152ll * 2 / per, most = P.R / rows;
+  if (groups > round && groups > most) groups = round > most ? round : most;
+  groups = groups < 1 ? 1 : groups;
   groups = groups > P.R ? P.R : groups;
   if (groups > 65535) groups = 65535;
   P.row_group = int((P.R + groups - 1) / groups);

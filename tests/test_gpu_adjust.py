@@ -187,3 +187,13 @@ def test_side_stream_and_graph_replay(D):
     kw["lengths"].fill_(3)
     graph.replay()
     assert torch.equal(out.view(torch.int16), D.adjust_logits(z, **kw).view(torch.int16))
+
+
+@pytest.mark.parametrize("dtype,B,R,V", [("f32", 16, 5, 32000), ("bf16", 7, 3, 1003)])
+def test_long_histories(D, dtype, B, R, V):
+    """Lengths about the ends of the batches in which a CTA reads them; many rows a CTA and few."""
+    s = _inputs(dtype, B, R, V, 15000, 5, 0, None, seed=B)
+    s["lengths"][:7] = [0, 1, 2047, 2048, 2049, 6145, 14999]
+    got = _call(D, s, s["z"].cuda())
+    want, bound = _want(s)
+    refs.close(got, want, bound, DT[dtype])

@@ -16,14 +16,15 @@
 // row to row.
 //
 // Measured (GB300, bf16, kernel alone):
-//   64 x 8 rows of 151936, 2048 tokens of history, 300 biases   58 us, 5.4 TB/s
-//   4 trees of 497 rows of 151936, 4096 tokens, one mask each  212 us, 5.4 TB/s
-//   256 x 8 rows of 32000 (fp16), masks that keep 2% of a row   56 us: 2.5 TB/s
+//   64 x 8 rows of 151936, 2048 tokens of history, 300 biases   59 us, 5.3 TB/s
+//   4 trees of 497 rows of 151936, 4096 tokens, one mask each  215 us, 5.3 TB/s
+//   256 x 8 rows of 32000 (fp16), masks that keep 2% of a row   55 us: 2.6 TB/s
 //     of what has to move, 3.5 TB/s of what does, since a kept logit brings its
 //     128-byte line
 //   8 rows of 151936 of one sequence                            4.4 us
 // Looking into every vector for touched elements instead took 99 and 359 us for
 // the first two, registers in place of the ring 73 and 245 us.
+#include <algorithm>
 #include <cmath>
 
 #include "dart_launch.h"
@@ -571,19 +572,27 @@ template <typename T>
 cudaError_t launch_adjust(AdjustParams P, int B, cudaStream_t stream) {
   const int slices = (P.V + kSlice<T> - 1) / kSlice<T>;
   P.by_slices = fast_div(uint32_t(slices));
-  // Rows per CTA: enough CTAs to fill the device three times (two an SM are
-  // resident), then as many rows as possible share one count.  Half as many CTAs
-  // left four trees of 497 rows at 227 us, twice as many 64 x 8 rows at 66 us,
-  // against 210 and 58.
-  const long long want = 152ll * 3 * 2, per = (long long)slices * B;
-  long long groups = (want + per - 1) / per;
-  // Each CTA counts the whole history, which takes it about as long as one row per
-  // 2048 entries, so beyond one round of CTAs a long one wants more rows each: 24 x 5
-  // fp32 rows of 32000 with 14312 tokens 42 -> 20 us, 83 x 4 of 9640 with 12285 26 -> 18.
-  const long long rows = 1 + (P.count ? P.a.history_width / 2048 : 0), round = 152ll * 2 / per, most = P.R / rows;
-  if (groups > round && groups > most) groups = round > most ? round : most;
-  groups = groups < 1 ? 1 : groups;
-  groups = groups > P.R ? P.R : groups;
+  // Rows per CTA.  304 CTAs run together; each begins and counts, for as long as `count`
+  // rows take, before its first row, and one that began late or holds the crowded ids
+  // ends up to 0.4 of its rows after the others.  So w rounds of CTAs, each with a share
+  // of the rows, take about w (count + rows) + 0.4 rows, and the least of that is taken:
+  //   4 trees of 497 rows of 151936, 4096 tokens: 232, 218, 216, 220, 224 us with w = 1..5
+  //   6 trees of 285 rows of 13938, 511 tokens: 42, 35, 38, 42 us with w = 1..4
+  //   64 x 8 rows of 151936, 2048 tokens: 59 and 68 us with w = 4 and 8
+  //   24 x 5 fp32 rows of 32000, 14312 tokens: 20 and 42 us with w = 1 and 4
+  //   178 trees of 286 rows of 9353, 583 tokens: 912, 863, 805 us with w = 4, 5 and 6
+  const long long per = (long long)slices * B, together = 152 * 2;
+  const float count = 2.f + (P.count ? float(P.a.history_width) / 1600.f : 0.f);
+  long long groups = 1;
+  float least = 3e38f;
+  for (int w = 1; w <= 16; ++w) {
+    long long g = std::max(1ll, std::min(w * together / per, (long long)P.R));
+    const long long rows = (P.R + g - 1) / g;
+    g = (P.R + rows - 1) / rows;
+    const float cost = float((per * g + together - 1) / together) * (count + float(rows)) + 0.4f * float(rows);
+    if (cost < least) least = cost, groups = g;
+    if (g == P.R) break;
+  }
   if (groups > 65535) groups = 65535;
   P.row_group = int((P.R + groups - 1) / groups);
   const dim3 grid(slices, (P.R + P.row_group - 1) / P.row_group, B);

@@ -27,20 +27,21 @@
 //
 // Measured (GB300, bf16, 32 + 8 heads of 128, both kernels):
 //   64 x 1 token over 4100..8200 positions    247 us, 6.4 TB/s: the cache, once
-//   2 x 2048 tokens over 32768 positions     1370 us, 1.40 PFLOP/s (fp16; 1.22 when
+//   2 x 2048 tokens over 32768 positions     1340 us, 1.43 PFLOP/s (fp16; 1.21 when
 //     the card holds its power limit for seconds): a tile takes 3000 cycles, 2048
 //     of them in the tensor unit; the chain S -> softmax (1400) -> P V -> next S
 //     of a half is what is longer.  Handing P over in two halves: 1480 us.  Two
 //     threads a row, 64 positions each: 1460 us (the exponentials, 512 cycles a
 //     half's tile, and the row's exchange leave the softmax at 1500).
-//   32 trees of 497 rows over ~3100 positions  727 us, 1.11 PFLOP/s of what is seen
-//   64 trees of 79 rows over ~1600 positions   182 us: 316 rows are a block of
+//   32 trees of 497 rows over ~3100 positions  721 us, 1.11 PFLOP/s of what is seen
+//   64 trees of 79 rows over ~1600 positions   181 us: 316 rows are a block of
 //     256 and one of 60, so the cache passes through the CTAs twice (5 TB/s from
 //     L2 and memory), and six block changes a CTA take a tenth.  Dealing the
 //     tiles of a short block to both halves and merging them: 199 us.  Moving a
 //     span's end to a block's end that is near, so that fewer blocks are joined:
 //     192 us here, 10 us less in 128 trees over ~450 positions, 10 us more in 16
-//     over ~6000.
+//     over ~6000.  A block joined by the CTA that comes last instead of by a second
+//     kernel: 197 us, and 32 x 1 token over ~750 positions 39 us for 30.
 //   1 token over 4098 positions                 15 us, 8 of them before the first
 //     product and in the join
 #include <cmath>
@@ -293,8 +294,12 @@ struct Walk {
   int b, h, blk;              // the block
   Chunk c;
   int tiles, end, rows;       // of the block: its tiles, where the last one ends, its rows
-  int t0, t1;                 // the part: tiles t0 .. t1
+  int t0, t1;                 // the part: tiles t0 .. t1 in the order in which they are taken
 
+  // Every other block takes its tiles from the last to the first: the ones that the
+  // block before it, over the same cache, has just read are still in L2 (2 x 2048
+  // tokens over 32768 positions 1363 -> 1337 us, 64 trees of 79 rows 187 -> 185.5).
+  __device__ __forceinline__ int tile(int t) const { return blk & 1 ? tiles - 1 - t : t; }
   __device__ __forceinline__ void open(const AttendParams& P, int from) {
     tiles = block_tiles(P, c, blk);
     end = block_end(P, c, blk);
@@ -545,7 +550,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
             turn = turn + 1 < kProducers ? turn + 1 : 0;
             const bool is_k = i == 0 || (i < 2 * n - 1 && (i & 1));
             const int j = is_k ? (i + 1) / 2 : (i == 2 * n - 1 ? n - 1 : (i - 2) / 2);
-            const int p0 = (w.t0 + j) * kTile;
+            const int p0 = w.tile(w.t0 + j) * kTile;
             const int boxes = (min(w.end - p0, kTile) + P.box - 1) / P.box;      // 0 for a block that sees nothing
             const int at = p0 + (lane / DH) * P.box;
             const bool mine = lane / DH < boxes;
@@ -624,7 +629,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
               if (!(ok = wait_warp(&sh->kv_full[vs], (i / kStages) & 1u, sh, P.wait_limit))) break;
             }
             // steps of 16 positions; those wholly behind the block's end are left out
-            const int steps = max(1, (min(w.end - (w.t0 + j) * kTile, kTile) + 15) / 16);
+            const int steps = max(1, (min(w.end - w.tile(w.t0 + j) * kTile, kTile) + 15) / 16);
             ok = j < 0 ? wait_warp(&sh->q_full[t], q_seen++ & 1u, sh, P.wait_limit)
                        : wait_warp(&sh->p_full[t], p_seen++ & 1u, sh, P.wait_limit);
             if (!ok) break;
@@ -736,7 +741,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
 
         float m = -INFINITY, l = 0.f;
         for (int j = 0; j < n && ok; ++j) {
-          const int p0 = (w.t0 + j) * kTile;
+          const int tile = w.tile(w.t0 + j), p0 = tile * kTile;
           // what this row sees of the tile, looked up while the product is under way
           const bool masked = p0 + kTile > open_end;
           uint32_t see[4] = {kFull, kFull, kFull, kFull};
@@ -823,7 +828,7 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
           }
           // V rows behind the end may hold anything, and 0 * NaN is NaN: those that
           // share a step of 16 with valid rows are cleared (by either half, which write the same)
-          if (j == n - 1 && w.t1 == w.tiles) {
+          if (tile == w.tiles - 1) {
             const int valid = max(0, min(w.end - p0, kTile));
             const int upto = max(16, (valid + 15) / 16 * 16);
             if (valid < upto) {
@@ -849,8 +854,9 @@ attend_kernel(const AttendParams P, const __grid_constant__ CUtensorMap kmap, co
         // the finished part, while the next one's queries are already on their way
         const int d_start = w.c.start, d_h = w.h, d_row0 = w.blk * kBlockRows, d_rows = w.rows, d_t0 = w.t0;
         const int d_after = w.tiles - w.t1;                // the block's tiles in later CTAs
-        const int d_b = w.b, d_odd0 = open_end < w.end ? max(open_end / kTile, w.t0) * kTile : w.end;
-        const int d_odd1 = min(w.t1 * kTile, w.end);       // rows differ in what they see of d_odd0 .. d_odd1
+        const int tile0 = min(w.tile(w.t0), w.tile(w.t1 - 1)), d_b = w.b;
+        const int d_odd0 = open_end < w.end ? max(open_end / kTile, tile0) * kTile : w.end;
+        const int d_odd1 = min((tile0 + n) * kTile, w.end);      // rows differ in what they see of d_odd0 .. d_odd1
         more = w.next(P);
         skip_inactive();
         if (more) ask_q();

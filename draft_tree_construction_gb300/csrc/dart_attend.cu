@@ -41,7 +41,7 @@
 //     span's end to a block's end that is near, so that fewer blocks are joined:
 //     192 us here, 10 us less in 128 trees over ~450 positions, 10 us more in 16
 //     over ~6000.  A block joined by the CTA that comes last instead of by a second
-//     kernel: 197 us, and 32 x 1 token over ~750 positions 39 us for 30.
+//     kernel: 197 us, and 8 x 1 token over ~750 positions 17.3 us for 15.0.
 //   1 token over 4098 positions                 15 us, 8 of them before the first
 //     product and in the join
 #include <cmath>

@@ -182,3 +182,39 @@ def test_what_is_wrong_raises_as_ever(D):
                dict(workspace=torch.zeros(100, dtype=torch.uint8, device="cuda"))):
         with pytest.raises(DartError):
             D.tree_attention(**dict(a, **kw))
+
+
+def test_two_threads_on_two_streams(D):
+    """Calls that overlap, each thread with its own stream, caches and workspace: the bits of calls by themselves."""
+    import threading
+    cases = [_cached(), _cached()]
+    rotary = D.Rotary(*D.rotary_frequencies(128))
+    hist, f = _i32(2, 3000), torch.full((2,), 1.5, device="cuda")
+    z = torch.randn(2, 4, 60000, device="cuda")
+    tables = [torch.zeros(D.attention_workspace_bytes(70, 3, 8, 2, 128), dtype=torch.uint8, device="cuda")
+              for _ in range(2)]
+
+    def step(a, ws):
+        q = D.kv_append(**a, rotary=rotary)
+        att = D.tree_attention(q, a["k_cache"], a["v_cache"], a["pages"], a["lengths"], a["starts"], workspace=ws)
+        return att["out"], D.adjust_logits(z, history=hist, repetition=f)
+    want = [step(a, ws) for a, ws in zip(cases, tables)]
+    torch.cuda.synchronize()
+    got, errors = [None, None], []
+
+    def work(i):
+        try:
+            with torch.cuda.stream(torch.cuda.Stream()):
+                for _ in range(30):
+                    got[i] = step(cases[i], tables[i])
+                torch.cuda.current_stream().synchronize()
+        except Exception as e:                        # into the main thread
+            errors.append(e)
+    threads = [threading.Thread(target=work, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not errors
+    for a, b, ws in zip(got, want, tables):
+        assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and D.device_error(ws) == 0

@@ -186,12 +186,17 @@ append_kernel(const AppendParams P) {
   int start = P.starts[b], end = P.starts[b + 1], len = P.lengths[b];
   if (t < start || t >= end) {
     b = find_sequence(P.starts, P.B, t, lane);
-    if (b >= P.B) return;
-    start = P.starts[b];
-    len = P.lengths[b];
+    if (b < P.B) {
+      start = P.starts[b];
+      len = P.lengths[b];
+    }
   }
   const int index = t - start;
-  if (index < 0) return;
+  if (b >= P.B || index < 0) {      // a row of no sequence
+    // the copies asked for must have landed before the CTA gives its shared memory up
+    cp_async_wait<0>();
+    return;
+  }
   const long long slot = (long long)len + index;
   const dart_cache_t& C = P.c;
   bool fits = len >= 0 && slot < (long long)C.table_width * C.page;

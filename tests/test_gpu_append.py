@@ -202,3 +202,25 @@ def test_frequencies_are_stretched_between_the_bounds():
     mid = (turns > 1) & (turns < 32)
     assert (f[mid] < plain[mid]).all() and (f[mid] > plain[mid] / 8).all()
     assert np.allclose(D.rotary_frequencies(64, 10000.0, 8.0)[0], plain / 8)
+
+
+@pytest.mark.parametrize("before,behind", [(3000, 0), (0, 20000), (2500, 9000)])
+def test_many_rows_of_no_sequence(D, before, behind):
+    """CTAs whose warps have nothing to do next to CTAs that work: the rows outside stay, the sequences' tokens come
+    out as they do by themselves, and no copy of the one lands in the shared memory of the other."""
+    s = _case("bf16", [37, 5, 90], [60, 1, 83], 32, 8, 128, 16, seed=17)
+    d, rotary = _cuda(s), D.Rotary(D.rotary_frequencies(128)[0])
+    w = torch.full((128,), 1.25, dtype=torch.bfloat16, device="cuda")
+    want = D.kv_append(d["q"], d["k"], d["v"], d["k_cache"], d["v_cache"], d["pages"], d["lengths"], d["starts"],
+                       rotary=rotary, q_weight=w, k_weight=w)
+    n, T = s["qkv"].shape[0], before + s["qkv"].shape[0] + behind
+    for _ in range(3):
+        d2 = _cuda(s)
+        wide = torch.full((T, 48, 128), math.nan, dtype=torch.bfloat16, device="cuda")
+        wide[before:before + n] = d2["qkv"]
+        out = torch.full((T, 32, 128), 3.0, dtype=torch.bfloat16, device="cuda")
+        D.kv_append(wide[:, :32], wide[:, 32:40], wide[:, 40:], d2["k_cache"], d2["v_cache"], d2["pages"],
+                    d2["lengths"], d2["starts"] + before, rotary=rotary, q_weight=w, k_weight=w, out=out)
+        assert torch.equal(out[before:before + n], want)
+        assert bool((out[:before] == 3.0).all()) and bool((out[before + n:] == 3.0).all())
+        assert torch.equal(d2["k_cache"], d["k_cache"]) and torch.equal(d2["v_cache"], d["v_cache"])

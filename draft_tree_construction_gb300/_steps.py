@@ -61,8 +61,8 @@ def declare(L):
 # A call's host work is a good part of a small call's time: _steps_native makes
 # the usual calls, and returns None for those that it leaves to the code here (a
 # stream is given, the tensors are not on the current device, something is empty
-# or wrong).  The checks here decide on plain integers and only a failing one
-# looks for its words.
+# or wrong), before it has called the library.  The checks here decide on plain
+# integers and only a failing one looks for its words.
 
 _native = None
 
@@ -78,7 +78,7 @@ def _load_native():
     module = importlib.util.module_from_spec(spec)
     spec.loader.exec_module(module)
     module.bind(*(C.cast(f, C.c_void_p).value for f in (L.dart_logits_adjust, L.dart_kv_append, L.dart_tree_attention,
-                                                        L.dart_attention_workspace_bytes)))
+                                                        L.dart_attention_workspace_bytes)), _check)
     _native = module
     return module
 

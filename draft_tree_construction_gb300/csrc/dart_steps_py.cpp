@@ -7,6 +7,8 @@
 // as the Python binding would accept it, on the current device and stream;
 // otherwise it returns None, nothing has happened, and the caller goes the
 // binding's way, which handles the rest and finds the words for what is wrong.
+// Once the entry point has been called, its answer is the call's: an error is
+// raised here, because part of the work may have been launched.
 #include <Python.h>
 
 #include <climits>
@@ -30,6 +32,14 @@ decltype(&dart_logits_adjust) logits_adjust = nullptr;
 decltype(&dart_kv_append) kv_append = nullptr;
 decltype(&dart_tree_attention) tree_attention = nullptr;
 decltype(&dart_attention_workspace_bytes) workspace_bytes = nullptr;
+PyObject* check = nullptr;          // check(code, name) raises the package's error; also from bind()
+
+PyObject* failed(int rc, const char* name) {
+  PyObject* const r = PyObject_CallFunction(check, "is", rc, name);
+  if (r) PyErr_Format(PyExc_RuntimeError, "%s failed (%d)", name, rc);
+  Py_XDECREF(r);
+  return nullptr;
+}
 
 // Takes tensors that lie on the current device; ok turns false at the first argument that does not.
 struct Taker {
@@ -148,7 +158,7 @@ PyObject* adjust(PyObject*, PyObject* const* args, Py_ssize_t count) {
   Py_BEGIN_ALLOW_THREADS
   rc = logits_adjust(from, int(B), int(R), int(V), stride, code, &a, to, out_stride, stream);
   Py_END_ALLOW_THREADS
-  if (rc != DART_OK) Py_RETURN_NONE;
+  if (rc != DART_OK) return failed(rc, "dart_logits_adjust");
   return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(args[11]);
   END_HANDLE_TH_ERRORS
 }
@@ -248,7 +258,7 @@ PyObject* append(PyObject*, PyObject* const* args, Py_ssize_t count) {
                  at_of<int32_t>(offsets), rotary, at_of<void>(q_weight), at_of<void>(k_weight), float(eps), &c,
                  out->data_ptr(), ho.token, ho.head, at_of<uint32_t>(err), stream);
   Py_END_ALLOW_THREADS
-  if (rc != DART_OK) Py_RETURN_NONE;
+  if (rc != DART_OK) return failed(rc, "dart_kv_append");
   return made.defined() ? THPVariable_Wrap(made) : Py_NewRef(args[14]);
   END_HANDLE_TH_ERRORS
 }
@@ -310,7 +320,7 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t count) {
                       ho.token, ho.head, wants_lse ? static_cast<float*>(made_lse.data_ptr()) : nullptr,
                       workspace->data_ptr(), workspace->nbytes(), stream);
   Py_END_ALLOW_THREADS
-  if (rc != DART_OK) Py_RETURN_NONE;
+  if (rc != DART_OK) return failed(rc, "dart_tree_attention");
   PyObject* result = PyTuple_New(3);
   if (!result) return nullptr;
   PyTuple_SET_ITEM(result, 0, made.defined() ? THPVariable_Wrap(made) : Py_NewRef(args[8]));
@@ -320,11 +330,12 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// (dart_logits_adjust, dart_kv_append, dart_tree_attention, dart_attention_workspace_bytes): their addresses
+// (the addresses of dart_logits_adjust, dart_kv_append, dart_tree_attention and
+// dart_attention_workspace_bytes, then what raises the package's error)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t count) {
   void* at[4];
-  if (count != 4) {
-    PyErr_SetString(PyExc_TypeError, "bind takes four addresses");
+  if (count != 5 || !PyCallable_Check(args[4])) {
+    PyErr_SetString(PyExc_TypeError, "bind takes four addresses and a function");
     return nullptr;
   }
   for (int i = 0; i < 4; ++i) {
@@ -335,6 +346,9 @@ PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t count) {
   kv_append = reinterpret_cast<decltype(kv_append)>(at[1]);
   tree_attention = reinterpret_cast<decltype(tree_attention)>(at[2]);
   workspace_bytes = reinterpret_cast<decltype(workspace_bytes)>(at[3]);
+  PyObject* const old = check;
+  check = Py_NewRef(args[4]);
+  Py_XDECREF(old);
   Py_RETURN_NONE;
 }
 

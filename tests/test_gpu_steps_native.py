@@ -218,3 +218,43 @@ def test_two_threads_on_two_streams(D):
     assert not errors
     for a, b, ws in zip(got, want, tables):
         assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1]) and D.device_error(ws) == 0
+
+
+@pytest.mark.parametrize("code", [1, 3, 4])
+def test_a_call_that_fails_is_made_once(D, monkeypatch, code):
+    """What an entry point answers is the call's answer: a call that it refuses, or whose launch it reports as failed
+    (part of it may have been launched), is not made again by the binding.  In place, a second one would scale, norm
+    and turn twice."""
+    import ctypes as C
+
+    from draft_tree_construction_gb300 import DartError, _steps
+    L, calls, kept = D.lib(), [], []
+
+    def answering(name):
+        f = C.CFUNCTYPE(C.c_int, *getattr(L, name).argtypes)(lambda *args: calls.append(name) or code)
+        kept.append(f)
+        return f
+    names = ("dart_logits_adjust", "dart_kv_append", "dart_tree_attention")
+    stubs = types.SimpleNamespace(dart_attention_workspace_bytes=L.dart_attention_workspace_bytes,
+                                  **{name: answering(name) for name in names})
+    a = _cached()
+    q = a["q"].contiguous()
+    z = torch.randn(2, 3, 500, device="cuda")
+    before = [t.clone() for t in (z, q, a["k_cache"], a["v_cache"])]
+    monkeypatch.setattr(_steps, "lib", lambda: stubs)
+    _steps._load_native()
+    monkeypatch.setattr(_steps, "lib", D.lib)
+    try:
+        for call in (lambda: D.adjust_logits(z, history=_i32(2, 30), repetition=torch.full((2,), 2.0, device="cuda"),
+                                             out=z),
+                     lambda: D.kv_append(q, a["k"], a["v"], a["k_cache"], a["v_cache"], a["pages"], a["lengths"],
+                                         a["starts"], rotary=D.Rotary(*D.rotary_frequencies(128)), out=q),
+                     lambda: D.tree_attention(q, a["k_cache"], a["v_cache"], a["pages"], a["lengths"], a["starts"])):
+            with pytest.raises(DartError, match=f"\\({code}\\)"):
+                call()
+    finally:
+        _steps._load_native()
+    assert calls == list(names)
+    for t, was in zip((z, q, a["k_cache"], a["v_cache"]), before):
+        assert torch.equal(t, was)
+    D.tree_attention(q, a["k_cache"], a["v_cache"], a["pages"], a["lengths"], a["starts"])       # the library again

@@ -561,11 +561,10 @@ template <typename T, int ROWS>
 cudaError_t launch_rows_as(const AdjustParams& P, dim3 grid, cudaStream_t stream) {
   constexpr int kMost = 4 * kSlice<T> + (ROWS != kSingle ? kRingBytes : 0);
   const cudaError_t e =
-      cudaFuncSetAttribute(adjust_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost);
+      settled(cudaFuncSetAttribute(adjust_kernel<T, ROWS>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
   if (e != cudaSuccess) return e;
   const bool touching = P.count || P.a.bias_count > 0;
-  adjust_kernel<T, ROWS><<<grid, kAdjThreads, kMost - (touching ? 0 : 4 * kSlice<T>), stream>>>(P);
-  return cudaGetLastError();
+  return launch_kernel(adjust_kernel<T, ROWS>, grid, kAdjThreads, kMost - (touching ? 0 : 4 * kSlice<T>), stream, P);
 }
 
 template <typename T>

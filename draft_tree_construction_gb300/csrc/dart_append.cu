@@ -456,12 +456,8 @@ extern "C" int dart_kv_append(const void* q, int64_t q_token_stride, int64_t q_h
   const unsigned grid = unsigned((warps + kAppThreads / 32 - 1) / (kAppThreads / 32));
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   const bool inter = P.interleaved != 0;
-  if (cache->dtype == DART_F16) {
-    if (inter) append_kernel<__half, true><<<grid, kAppThreads, kRingBytes, s>>>(P);
-    else append_kernel<__half, false><<<grid, kAppThreads, kRingBytes, s>>>(P);
-  } else {
-    if (inter) append_kernel<__nv_bfloat16, true><<<grid, kAppThreads, kRingBytes, s>>>(P);
-    else append_kernel<__nv_bfloat16, false><<<grid, kAppThreads, kRingBytes, s>>>(P);
-  }
-  return cudaGetLastError() == cudaSuccess ? DART_OK : DART_ERR_CUDA;
+  const auto kernel = cache->dtype == DART_F16
+                          ? (inter ? append_kernel<__half, true> : append_kernel<__half, false>)
+                          : (inter ? append_kernel<__nv_bfloat16, true> : append_kernel<__nv_bfloat16, false>);
+  return launch_kernel(kernel, grid, kAppThreads, kRingBytes, s, P) == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

@@ -1056,8 +1056,8 @@ EncodeFn tensor_map_encoder() {
   static const EncodeFn fn = [] {
     void* f = nullptr;
     cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-    if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q) != cudaSuccess ||
-        q != cudaDriverEntryPointSuccess)
+    if (settled(cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &q)) !=
+            cudaSuccess || q != cudaDriverEntryPointSuccess)
       f = nullptr;
     return reinterpret_cast<EncodeFn>(f);
   }();
@@ -1107,10 +1107,10 @@ int slot_rows(long long T, long long group) {
 template <typename T, int DH>
 cudaError_t launch(const AttendParams& P, const CUtensorMap& km, const CUtensorMap& vm, cudaStream_t s) {
   const int smem = 2 * DH * kHalfTileBytes + kRingBytes + int(sizeof(Shared));
-  cudaError_t e = cudaFuncSetAttribute(attend_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+  cudaError_t e =
+      settled(cudaFuncSetAttribute(attend_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if (e != cudaSuccess) return e;
-  attend_kernel<T, DH><<<kCtas, kThreads, smem, s>>>(P, km, vm);
-  e = cudaGetLastError();
+  e = launch_kernel(attend_kernel<T, DH>, kCtas, kThreads, smem, s, P, km, vm);
   if (e != cudaSuccess) return e;
   // the join's CTAs take their places while the last attention CTAs finish, and wait there
   cudaLaunchAttribute at[1];
@@ -1122,7 +1122,7 @@ cudaError_t launch(const AttendParams& P, const CUtensorMap& km, const CUtensorM
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  return cudaLaunchKernelEx(&cfg, join_kernel<T, DH>, P);
+  return settled(cudaLaunchKernelEx(&cfg, join_kernel<T, DH>, P));
 }
 
 }  // namespace

@@ -6,6 +6,25 @@
 
 namespace dart {
 
+// What a runtime call answered; a failure is not left behind for a later call to find.
+inline cudaError_t settled(cudaError_t e) {
+  if (e != cudaSuccess) cudaGetLastError();
+  return e;
+}
+
+// Launches a kernel and returns this launch's own result: cudaGetLastError() would
+// also return an error that an earlier call left behind, for a launch that went well.
+template <typename... Params, typename... Args>
+cudaError_t launch_kernel(void (*kernel)(Params...), dim3 grid, dim3 block, size_t smem, cudaStream_t stream,
+                          Args&&... args) {
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = block;
+  cfg.dynamicSmemBytes = smem;
+  cfg.stream = stream;
+  return settled(cudaLaunchKernelEx(&cfg, kernel, static_cast<Args&&>(args)...));
+}
+
 long long rows_wait_limit();
 // Multiprocessors of the current device (cached per device; 0 if unknown).
 int device_sms();

@@ -258,3 +258,43 @@ def test_a_call_that_fails_is_made_once(D, monkeypatch, code):
     for t, was in zip((z, q, a["k_cache"], a["v_cache"]), before):
         assert torch.equal(t, was)
     D.tree_attention(q, a["k_cache"], a["v_cache"], a["pages"], a["lengths"], a["starts"])       # the library again
+
+
+def _leave_an_error_behind(D):
+    """device_error on a capturing stream: refused by the runtime, which remembers the refusal."""
+    import ctypes as C
+
+    from draft_tree_construction_gb300 import DartError
+    with open("/proc/self/maps") as maps:
+        path = next(line.split()[-1] for line in maps if "libcudart.so" in line)
+    rt, graph = C.CDLL(path), C.c_void_p()
+    side, ws = torch.cuda.Stream(), torch.zeros(256, dtype=torch.uint8, device="cuda")
+    torch.cuda.synchronize()
+    assert rt.cudaStreamBeginCapture(C.c_void_p(side.cuda_stream), C.c_int(2)) == 0           # relaxed
+    try:
+        with pytest.raises(DartError):
+            D.device_error(ws, stream=side)
+    finally:
+        assert rt.cudaStreamEndCapture(C.c_void_p(side.cuda_stream), C.byref(graph)) != 0     # the capture is void
+        rt.cudaGetLastError()                    # of the runtime that PyTorch uses; the library has one of its own
+    assert not graph.value
+
+
+def test_an_older_error_is_not_taken_for_a_failed_launch(D):
+    """What another call left behind does not make a call raise that has launched, in place least of all."""
+    z, hist = torch.randn(2, 3, 5000, device="cuda"), _i32(2, 30)
+    rep = torch.full((2,), 2.0, device="cuda")
+    a = _cached()
+    a["q"], rotary = a["q"].contiguous(), D.Rotary(*D.rotary_frequencies(128))
+
+    def steps(z, a):
+        yield D.adjust_logits(z, history=hist, repetition=rep, out=z)
+        yield D.kv_append(**a, rotary=rotary, out=a["q"])
+        yield D.tree_attention(*(a[k] for k in ("q", "k_cache", "v_cache", "pages", "lengths", "starts")))["out"]
+    copies = lambda: (z.clone(), {k: t.clone() for k, t in a.items()})
+    want = list(steps(*copies()))
+    z2, a2 = copies()
+    made = steps(z2, a2)
+    for w in want:
+        _leave_an_error_behind(D)
+        assert torch.equal(next(made), w)

@@ -163,7 +163,7 @@ CtxGetIdFn g_ctx_get_id = nullptr;
 
 bool driver_entry(const char* name, void** fn) {
   cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-  return cudaGetDriverEntryPointByVersion(name, fn, 12000, cudaEnableDefault, &q) == cudaSuccess &&
+  return settled(cudaGetDriverEntryPointByVersion(name, fn, 12000, cudaEnableDefault, &q)) == cudaSuccess &&
          q == cudaDriverEntryPointSuccess && *fn;
 }
 
@@ -184,7 +184,7 @@ int static_scratch(void** out) {
   if (g_ctx_get_current(&ctx) != 0) return DART_ERR_CUDA;
   if (!ctx) {
     // no context current on this thread yet: the lookup binds the device's primary context
-    if (cudaGetSymbolAddress(&addr, g_static_scratch) != cudaSuccess || !addr) return DART_ERR_CUDA;
+    if (settled(cudaGetSymbolAddress(&addr, g_static_scratch)) != cudaSuccess || !addr) return DART_ERR_CUDA;
     if (g_ctx_get_current(&ctx) != 0 || !ctx) return DART_ERR_CUDA;
   }
   unsigned long long id = 0;
@@ -194,7 +194,7 @@ int static_scratch(void** out) {
       *out = g_scratch_cache[i].addr;
       return DART_OK;
     }
-  if (!addr && (cudaGetSymbolAddress(&addr, g_static_scratch) != cudaSuccess || !addr)) return DART_ERR_CUDA;
+  if (!addr && (settled(cudaGetSymbolAddress(&addr, g_static_scratch)) != cudaSuccess || !addr)) return DART_ERR_CUDA;
   // a full cache forgets its oldest entry (contexts that old are usually gone)
   if (g_scratch_used == kMaxScratchContexts) {
     for (int i = 1; i < kMaxScratchContexts; ++i) g_scratch_cache[i - 1] = g_scratch_cache[i];
@@ -209,9 +209,9 @@ int static_scratch(void** out) {
 // block when the word is nonzero.  The caller has synchronised the stream.
 int read_error_word(void* ctrl, uint32_t* out_flags) {
   uint32_t word = 0;
-  if (cudaMemcpy(&word, ctrl, sizeof(word), cudaMemcpyDeviceToHost) != cudaSuccess) return DART_ERR_CUDA;
+  if (settled(cudaMemcpy(&word, ctrl, sizeof(word), cudaMemcpyDeviceToHost)) != cudaSuccess) return DART_ERR_CUDA;
   *out_flags = word;
-  if (word != 0u && cudaMemset(ctrl, 0, kCtrlBytes) != cudaSuccess) return DART_ERR_CUDA;
+  if (word != 0u && settled(cudaMemset(ctrl, 0, kCtrlBytes)) != cudaSuccess) return DART_ERR_CUDA;
   return DART_OK;
 }
 
@@ -312,12 +312,12 @@ int dart_tree_plan_create(dart_tree_plan_t* out_plan, const void* logits, int B,
                          out_tokens, out_parents, out_pos, out_mask, workspace, workspace_bytes, &L);
   if (rc) return rc;
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DART_ERR_CUDA;
+  if (settled(cudaGetDevice(&dev)) != cudaSuccess) return DART_ERR_CUDA;
   cudaStream_t s = nullptr;
-  if (cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking) != cudaSuccess) return DART_ERR_CUDA;
+  if (settled(cudaStreamCreateWithFlags(&s, cudaStreamNonBlocking)) != cudaSuccess) return DART_ERR_CUDA;
   // the launches are recorded on a stream of the plan's own, none of them runs
   cudaGraph_t graph = nullptr;
-  if (cudaStreamBeginCapture(s, cudaStreamCaptureModeThreadLocal) != cudaSuccess) {
+  if (settled(cudaStreamBeginCapture(s, cudaStreamCaptureModeThreadLocal)) != cudaSuccess) {
     cudaStreamDestroy(s);
     return DART_ERR_CUDA;
   }
@@ -373,11 +373,11 @@ int dart_tree_plan_create(dart_tree_plan_t* out_plan, const void* logits, int B,
 int dart_tree_plan_launch(dart_tree_plan_t plan, void* stream) {
   if (!plan) return DART_ERR_INVALID_ARG;
   int dev = -1;
-  if (cudaGetDevice(&dev) != cudaSuccess) return DART_ERR_CUDA;
+  if (settled(cudaGetDevice(&dev)) != cudaSuccess) return DART_ERR_CUDA;
   if (dev != plan->device) return DART_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaStreamCaptureStatus cs = cudaStreamCaptureStatusNone;
-  if (cudaStreamIsCapturing(s, &cs) != cudaSuccess) return DART_ERR_CUDA;
+  if (settled(cudaStreamIsCapturing(s, &cs)) != cudaSuccess) return DART_ERR_CUDA;
   if (cs != cudaStreamCaptureStatusNone) {
     // a caller capturing its own graph: record the kernels themselves
     if (plan->B == 0) return DART_OK;
@@ -385,12 +385,13 @@ int dart_tree_plan_launch(dart_tree_plan_t plan, void* stream) {
                        plan->W, plan->lambda, plan->beta, plan->has_table ? &plan->table : nullptr, plan->ctx,
                        plan->tokens, plan->parents, plan->pos, plan->mask, plan->scores, plan->ws, plan->L, s);
   }
-  return cudaGraphLaunch(plan->exec, s) == cudaSuccess ? DART_OK : DART_ERR_CUDA;
+  return settled(cudaGraphLaunch(plan->exec, s)) == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }
 
 int dart_tree_plan_destroy(dart_tree_plan_t plan) {
   if (!plan) return DART_OK;
-  const bool ok = cudaGraphExecDestroy(plan->exec) == cudaSuccess && cudaGraphDestroy(plan->graph) == cudaSuccess;
+  const bool ok = settled(cudaGraphExecDestroy(plan->exec)) == cudaSuccess &&
+                  settled(cudaGraphDestroy(plan->graph)) == cudaSuccess;
   delete plan;
   return ok ? DART_OK : DART_ERR_CUDA;
 }
@@ -681,7 +682,7 @@ void dart_set_wait_limit(int64_t cycles) { set_rows_wait_limit((long long)cycles
 int dart_device_error(const void* workspace, uint32_t* out_flags, void* stream) {
   if (!workspace || !out_flags) return DART_ERR_INVALID_ARG;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  if (cudaStreamSynchronize(s) != cudaSuccess) return DART_ERR_CUDA;
+  if (settled(cudaStreamSynchronize(s)) != cudaSuccess) return DART_ERR_CUDA;
   return read_error_word(const_cast<void*>(workspace), out_flags);
 }
 
@@ -690,7 +691,7 @@ int dart_noalloc_device_error(uint32_t* out_flags, void* stream) {
   void* scratch = nullptr;
   int rc = static_scratch(&scratch);
   if (rc) return rc;
-  if (cudaStreamSynchronize(static_cast<cudaStream_t>(stream)) != cudaSuccess) return DART_ERR_CUDA;
+  if (settled(cudaStreamSynchronize(static_cast<cudaStream_t>(stream))) != cudaSuccess) return DART_ERR_CUDA;
   return read_error_word(scratch, out_flags);
 }
 

@@ -20,7 +20,7 @@
 // reach on this GPU.  The bulk ring can also interleave its warps: the CTA
 // reads one contiguous span, warp w taking its 4 KiB steps w, w + warps,
 // w + 2 warps, ... (fewer, longer sequential streams for the memory system).
-#include "dart_common.cuh"
+#include "dart_launch.h"
 
 #include <cfloat>
 
@@ -251,7 +251,7 @@ extern "C" int dart_probe_stream(const void* src, uint64_t bytes, int mode, int 
   const int threads = warps_per_cta * 32;
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    e = settled(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     if (e == cudaSuccess) kernel<<<ctas, threads, smem, s>>>(P);
   };
   if (bulk) {

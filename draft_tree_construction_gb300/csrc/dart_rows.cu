@@ -1310,7 +1310,7 @@ cudaError_t launch_row_pass(const void* logits, long long R, int V, long long st
   const size_t smem = rows_smem_bytes();
   cudaError_t e = cudaSuccess;
   auto go = [&](auto kernel) {
-    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    e = settled(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     if (e == cudaSuccess) kernel<<<unsigned(grid), kRowThreads, smem, stream>>>(P);
   };
   if (dtype == DART_F32) go(row_stream_kernel<DART_F32>);

@@ -144,13 +144,13 @@ inline int tree_threads(int W, int k, int B, int sms) {
 int device_sms() {
   static std::atomic<int> cache[64];
   int dev = 0;
-  if (cudaGetDevice(&dev) != cudaSuccess || dev < 0) return 0;
+  if (settled(cudaGetDevice(&dev)) != cudaSuccess || dev < 0) return 0;
   if (dev < 64) {
     const int c = cache[dev].load(std::memory_order_relaxed);
     if (c > 0) return c;
   }
   int sms = 0;
-  if (cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess) return 0;
+  if (settled(cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev)) != cudaSuccess) return 0;
   if (dev < 64) cache[dev].store(sms, std::memory_order_relaxed);
   return sms;
 }
@@ -629,11 +629,11 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   const int threads = tree_threads(a.W, a.k, a.B, device_sms());
   cudaError_t e;
   if (a.W <= 32) {
-    e = cudaFuncSetAttribute(tree_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    e = settled(cudaFuncSetAttribute(tree_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     if (e != cudaSuccess) return e;
     tree_kernel<1><<<a.B, threads, smem, stream>>>(a);
   } else {
-    e = cudaFuncSetAttribute(tree_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem));
+    e = settled(cudaFuncSetAttribute(tree_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
     if (e != cudaSuccess) return e;
     tree_kernel<2><<<a.B, threads, smem, stream>>>(a);
   }

@@ -298,3 +298,15 @@ def test_an_older_error_is_not_taken_for_a_failed_launch(D):
     for w in want:
         _leave_an_error_behind(D)
         assert torch.equal(next(made), w)
+
+
+def test_a_refused_call_leaves_no_error_behind(D):
+    """The library's other calls, which launch after device_error was refused, launch and say so."""
+    parents = torch.tensor([[-1, 0, 0, 1]], dtype=torch.int32, device="cuda")
+    want = D.mask_pack(parents)
+    z = torch.randn(4, 3000, device="cuda")
+    ids = D.row_topk(z, 1.0, 4)[0]
+    _leave_an_error_behind(D)
+    assert torch.equal(D.mask_pack(parents), want)
+    _leave_an_error_behind(D)
+    assert torch.equal(D.row_topk(z, 1.0, 4)[0], ids)

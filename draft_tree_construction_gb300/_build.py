@@ -3,7 +3,8 @@
 Each translation unit compiles in parallel, then one nvcc call links the
 shared library next to this file.  Objects go to ``_build/`` (git-ignored).
 The Python module _steps_native (host C++ against PyTorch's headers, no device
-code) is compiled beside them, with the host compiler.
+code) is compiled beside them, with the host compiler; the library is linked
+whether or not that succeeds.
 """
 from __future__ import annotations
 
@@ -12,6 +13,7 @@ import shutil
 import subprocess
 import sys
 import sysconfig
+import warnings
 
 HERE = os.path.dirname(os.path.abspath(__file__))
 ROOT = os.path.dirname(HERE)
@@ -31,17 +33,22 @@ FLAGS = ["-O3", "-lineinfo", "-std=c++17", "-Xcompiler", "-fPIC", "-I", INCLUDE,
 
 
 def _inputs():
-    files = [os.path.join(CSRC, s) for s in SOURCES] + [NATIVE_SOURCE]
+    files = [os.path.join(CSRC, s) for s in SOURCES]
     files += [os.path.join(CSRC, f) for f in os.listdir(CSRC) if f.endswith((".cuh", ".h"))]
     files.append(os.path.join(INCLUDE, "darttree.h"))
     return files
 
 
+def _native_inputs():
+    return [NATIVE_SOURCE, os.path.join(INCLUDE, "darttree.h")]
+
+
+def _stale(target: str, inputs: list[str]) -> bool:
+    return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in inputs)
+
+
 def needs_build() -> bool:
-    if not os.path.exists(LIB) or not os.path.exists(NATIVE):
-        return True
-    t = min(os.path.getmtime(LIB), os.path.getmtime(NATIVE))
-    return any(os.path.getmtime(f) > t for f in _inputs())
+    return _stale(LIB, _inputs()) or (_stale(NATIVE, _native_inputs()) and not _native_failed)
 
 
 def _native_command(target: str) -> list[str]:
@@ -56,11 +63,49 @@ def _native_command(target: str) -> list[str]:
             f"-Wl,-rpath,{os.path.join(home, 'lib')}"]
 
 
+# The library needs nvcc alone; the Python module also PyTorch's headers, and the
+# steps work without it.  So a module that cannot be built is said so once a
+# process and does not keep the library from being linked.
+_native_failed = False
+
+
+def _start_native(target: str):
+    """(the module's running compilation, "") or (None, why there is none)."""
+    try:
+        return subprocess.Popen(_native_command(target), stdout=subprocess.PIPE, stderr=subprocess.STDOUT), ""
+    except Exception as e:                 # no PyTorch, no host compiler
+        return None, f"{type(e).__name__}: {e}"
+
+
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
-    if not force and not needs_build():
-        return LIB
+    global _native_failed
+    want_lib = force or _stale(LIB, _inputs())
+    want_native = (force or _stale(NATIVE, _native_inputs())) and (force or not _native_failed)
+    native, why = NATIVE + f".{os.getpid()}.tmp", ""
+    compiling = None
+    if want_native:
+        compiling, why = _start_native(native)
+    try:
+        if want_lib:
+            _build_library(verbose, list(extra_flags or []))
+    finally:
+        if compiling is not None:
+            out, _ = compiling.communicate()
+            why = out.decode(errors="replace") if compiling.returncode else ""
+    if want_native:
+        _native_failed = bool(why)
+        if why:
+            if os.path.exists(NATIVE):         # of other sources: its structures may lie differently
+                os.remove(NATIVE)
+            warnings.warn(f"_steps_native was not built, calls of the steps around a tree take some microseconds "
+                          f"longer:\n{why}", RuntimeWarning, stacklevel=2)
+        else:
+            os.replace(native, NATIVE)
+    return LIB
+
+
+def _build_library(verbose: bool, extra: list[str]) -> None:
     os.makedirs(BUILD, exist_ok=True)
-    extra = list(extra_flags or [])
     procs = []
     objs = []
     for src in SOURCES:
@@ -70,9 +115,6 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
         if verbose:
             print(" ".join(cmd), file=sys.stderr)
         procs.append((src, subprocess.Popen(cmd, stdout=subprocess.PIPE, stderr=subprocess.STDOUT)))
-    native = NATIVE + ".tmp"
-    procs.append((os.path.basename(NATIVE_SOURCE), subprocess.Popen(_native_command(native), stdout=subprocess.PIPE,
-                                                                    stderr=subprocess.STDOUT)))
     failed = []
     for src, p in procs:
         out, _ = p.communicate()
@@ -82,13 +124,11 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             print(out.decode(errors="replace"), file=sys.stderr)
     if failed:
         msg = "\n".join(f"--- {s}\n{o}" for s, o in failed)
-        raise RuntimeError(f"compilation failed:\n{msg}")
+        raise RuntimeError(f"nvcc failed:\n{msg}")
     tmp = LIB + ".tmp"
     cmd = [NVCC, *ARCH, "-shared", "-o", tmp, *objs]
     subprocess.run(cmd, check=True)
-    os.replace(native, NATIVE)
     os.replace(tmp, LIB)
-    return LIB
 
 
 if __name__ == "__main__":

@@ -21,7 +21,6 @@ CSRC = os.path.join(HERE, "csrc")
 INCLUDE = os.path.join(ROOT, "include")
 BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdarttree.so")
-NATIVE = os.path.join(HERE, "_steps_native.so")
 NATIVE_SOURCE = os.path.join(CSRC, "dart_steps_py.cpp")
 SOURCES = ["dart_api.cu", "dart_rows.cu", "dart_tree.cu", "dart_select.cu", "dart_probe.cu",
            "dart_adjust.cu", "dart_append.cu", "dart_attend.cu"]
@@ -43,12 +42,28 @@ def _native_inputs():
     return [NATIVE_SOURCE, os.path.join(INCLUDE, "darttree.h")]
 
 
+def native_path() -> str | None:
+    """The module's file for this interpreter and this PyTorch, whose binary interfaces it is bound to (None without
+    PyTorch)."""
+    try:
+        import torch
+    except ImportError:
+        return None
+    tag = f"torch-{torch.__version__}-{(torch.version.git_version or '')[:8]}"
+    return os.path.join(HERE, f"_steps_native.{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
 def _stale(target: str, inputs: list[str]) -> bool:
     return not os.path.exists(target) or any(os.path.getmtime(f) > os.path.getmtime(target) for f in inputs)
 
 
+def _native_stale() -> bool:
+    path = native_path()
+    return path is not None and _stale(path, _native_inputs())
+
+
 def needs_build() -> bool:
-    return _stale(LIB, _inputs()) or (_stale(NATIVE, _native_inputs()) and not _native_failed)
+    return _stale(LIB, _inputs()) or (_native_stale() and not _native_failed)
 
 
 def _native_command(target: str) -> list[str]:
@@ -80,8 +95,9 @@ def _start_native(target: str):
 def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | None = None) -> str:
     global _native_failed
     want_lib = force or _stale(LIB, _inputs())
-    want_native = (force or _stale(NATIVE, _native_inputs())) and (force or not _native_failed)
-    native, why = NATIVE + f".{os.getpid()}.tmp", ""
+    path, why = native_path(), ""
+    want_native = path is not None and (force or (_native_stale() and not _native_failed))
+    native = f"{path}.{os.getpid()}.tmp"
     compiling = None
     if want_native:
         compiling, why = _start_native(native)
@@ -95,12 +111,12 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     if want_native:
         _native_failed = bool(why)
         if why:
-            if os.path.exists(NATIVE):         # of other sources: its structures may lie differently
-                os.remove(NATIVE)
+            if os.path.exists(path):           # of other sources: its structures may lie differently
+                os.remove(path)
             warnings.warn(f"_steps_native was not built, calls of the steps around a tree take some microseconds "
                           f"longer:\n{why}", RuntimeWarning, stacklevel=2)
         else:
-            os.replace(native, NATIVE)
+            os.replace(native, path)
     return LIB
 
 

@@ -16,6 +16,7 @@ import numpy as np
 
 from . import (DTYPE_CODES, DartError, _check, _check_error_word, _check_tensor, _check_workspace, _device_of,
                _mask_dtypes, _on_device, _row_stride, _stream_ptr, _torch, lib)
+from ._build import native_path
 
 
 _codes = functools.cache(DTYPE_CODES)
@@ -69,9 +70,9 @@ _native = None
 
 def _load_native():
     global _native
-    path = os.path.join(os.path.dirname(os.path.abspath(__file__)), "_steps_native.so")
+    path = native_path()
     L = lib()
-    if not os.path.exists(path):
+    if path is None or not os.path.exists(path):
         raise DartError(f"{path} is missing: run draft_tree_construction_gb300.build()")
     _torch()                                   # its libraries first
     spec = importlib.util.spec_from_file_location("_steps_native", path)

@@ -27,8 +27,9 @@ def tree(tmp_path, monkeypatch):
         path.write_text(text.format(python=sys.executable, log=str(log)))
         path.chmod(path.stat().st_mode | stat.S_IXUSR)
         monkeypatch.setattr(_build, tool, str(path))
-    for name, target in (("LIB", "lib.so"), ("NATIVE", "native.so"), ("BUILD", "objects")):
+    for name, target in (("LIB", "lib.so"), ("BUILD", "objects")):
         monkeypatch.setattr(_build, name, str(tmp_path / target))
+    monkeypatch.setattr(_build, "native_path", lambda: str(tmp_path / "native.so"))
     monkeypatch.setattr(_build, "_native_failed", False, raising=False)
     setup("NVCC", WORKS)
     setup("CXX", WORKS)
@@ -84,3 +85,17 @@ def test_a_module_of_other_sources_does_not_stay(tree):
     with pytest.warns(RuntimeWarning):
         _build.build(force=True)
     assert tree.files() == {"lib.so"}
+
+
+def test_the_module_is_one_for_each_pytorch_and_interpreter(tree, tmp_path, monkeypatch):
+    """After an upgrade the module of the versions before is neither taken for fresh nor loaded."""
+    import sysconfig
+
+    torch = pytest.importorskip("torch")
+    monkeypatch.undo()
+    own = _build.native_path()
+    assert torch.__version__ in own and own.endswith(sysconfig.get_config_var("EXT_SUFFIX"))
+    monkeypatch.setattr(torch, "__version__", "1.2.3")
+    other = _build.native_path()
+    assert other != own and os.path.dirname(other) == _build.HERE and not os.path.exists(other)
+    assert _build.needs_build() and _build._native_stale()

@@ -11,6 +11,7 @@ import functools
 import importlib.util
 import math
 import os
+import warnings
 
 import numpy as np
 
@@ -63,21 +64,38 @@ def declare(L):
 # the usual calls, and returns None for those that it leaves to the code here (a
 # stream is given, the tensors are not on the current device, something is empty
 # or wrong), before it has called the library.  The checks here decide on plain
-# integers and only a failing one looks for its words.
+# integers and only a failing one looks for its words.  Without the module every
+# call is made by the code here.
 
 _native = None
 
 
+class _LeaveAll:
+    """In the module's place where there is none: every call goes the binding's way."""
+
+    @staticmethod
+    def adjust(*args):
+        return None
+
+    append = attend = adjust
+
+
 def _load_native():
     global _native
-    path = native_path()
     L = lib()
-    if path is None or not os.path.exists(path):
-        raise DartError(f"{path} is missing: run draft_tree_construction_gb300.build()")
     _torch()                                   # its libraries first
-    spec = importlib.util.spec_from_file_location("_steps_native", path)
-    module = importlib.util.module_from_spec(spec)
-    spec.loader.exec_module(module)
+    path = native_path()
+    try:
+        if path is None or not os.path.exists(path):
+            raise ImportError(f"{path} is missing: run draft_tree_construction_gb300.build()")
+        spec = importlib.util.spec_from_file_location("_steps_native", path)
+        module = importlib.util.module_from_spec(spec)
+        spec.loader.exec_module(module)
+    except ImportError as e:
+        _native = _LeaveAll
+        warnings.warn(f"calls of the steps around a tree take some microseconds longer: {e}", RuntimeWarning,
+                      stacklevel=3)
+        return _native
     module.bind(*(C.cast(f, C.c_void_p).value for f in (L.dart_logits_adjust, L.dart_kv_append, L.dart_tree_attention,
                                                         L.dart_attention_workspace_bytes)), _check)
     _native = module

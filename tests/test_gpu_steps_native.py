@@ -310,3 +310,27 @@ def test_a_refused_call_leaves_no_error_behind(D):
     assert torch.equal(D.mask_pack(parents), want)
     _leave_an_error_behind(D)
     assert torch.equal(D.row_topk(z, 1.0, 4)[0], ids)
+
+
+def test_without_the_module(D, monkeypatch):
+    """The same bits by the binding alone, and one warning."""
+    import warnings
+
+    from draft_tree_construction_gb300 import _steps
+    a, z, hist = _cached(), torch.randn(2, 3, 5000, device="cuda"), _i32(2, 30)
+    rep = torch.full((2,), 1.5, device="cuda")
+
+    def steps():
+        caches = [a["k_cache"].clone(), a["v_cache"].clone()]
+        q = D.kv_append(**dict(a, k_cache=caches[0], v_cache=caches[1]))
+        att = D.tree_attention(q, *caches, a["pages"], a["lengths"], a["starts"])
+        return q, *caches, att["out"], D.adjust_logits(z, history=hist, repetition=rep)
+    want = steps()
+    monkeypatch.setattr(_steps, "native_path", lambda: None)
+    monkeypatch.setattr(_steps, "_native", None)
+    with warnings.catch_warnings(record=True) as said:
+        warnings.simplefilter("always")
+        got = steps()
+    assert [w.category for w in said] == [RuntimeWarning] and _steps._native is _steps._LeaveAll
+    for x, y in zip(got, want):
+        assert torch.equal(x, y)

@@ -256,3 +256,18 @@ def test_the_native_module_leaves_what_is_not_on_the_device():
     assert native.adjust(1, 2) is None and native.append() is None and native.attend(None) is None
     with pytest.raises(TypeError):
         native.bind(1, 2)
+
+
+@pytest.mark.parametrize("content", [None, b"not a shared object"])
+def test_without_the_native_module_the_binding_takes_every_call(monkeypatch, tmp_path, content):
+    """A module that is missing or cannot be imported is said once; the calls go on."""
+    D.build()
+    path = tmp_path / "native.so"
+    if content is not None:
+        path.write_bytes(content)
+    monkeypatch.setattr(_steps, "native_path", lambda: str(path))
+    monkeypatch.setattr(_steps, "_native", None)
+    with pytest.warns(RuntimeWarning, match="longer"):
+        native = _steps._load_native()
+    assert _steps._native is native
+    assert native.adjust(*range(12)) is None and native.append(*range(16)) is None and native.attend(*range(11)) is None

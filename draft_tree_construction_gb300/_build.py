@@ -8,6 +8,7 @@ whether or not that succeeds.
 """
 from __future__ import annotations
 
+import glob
 import os
 import shutil
 import subprocess
@@ -51,6 +52,12 @@ def native_path() -> str | None:
         return None
     tag = f"torch-{torch.__version__}-{(torch.version.git_version or '')[:8]}"
     return os.path.join(HERE, f"_steps_native.{tag}{sysconfig.get_config_var('EXT_SUFFIX')}")
+
+
+def _modules() -> list[str]:
+    """The modules of every PyTorch that the tree was built with: those of an older library go with it, whose
+    structures may lie differently."""
+    return glob.glob(os.path.join(glob.escape(os.path.dirname(LIB)), "_steps_native.*.so"))
 
 
 def _stale(target: str, inputs: list[str]) -> bool:
@@ -104,6 +111,9 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
     try:
         if want_lib:
             _build_library(verbose, list(extra_flags or []))
+            for old in _modules():
+                if old != path:
+                    os.remove(old)
     finally:
         if compiling is not None:
             out, _ = compiling.communicate()

@@ -99,3 +99,13 @@ def test_the_module_is_one_for_each_pytorch_and_interpreter(tree, tmp_path, monk
     other = _build.native_path()
     assert other != own and os.path.dirname(other) == _build.HERE and not os.path.exists(other)
     assert _build.needs_build() and _build._native_stale()
+
+
+def test_modules_of_an_older_library_go_with_it(tree, tmp_path, monkeypatch):
+    monkeypatch.setattr(_build, "native_path", lambda: str(tmp_path / "_steps_native.two.so"))
+    (tmp_path / "_steps_native.one.so").write_text("of another PyTorch")
+    _build.build()
+    assert tree.files() == {"lib.so", "_steps_native.two.so"}
+    (tmp_path / "_steps_native.one.so").write_text("of another PyTorch")
+    _build.build()                                   # the library stays, and so does what was built for it
+    assert tree.files() == {"lib.so", "_steps_native.one.so", "_steps_native.two.so"}

@@ -163,7 +163,9 @@ def adjust_logits(logits, *, history=None, lengths=None, repetition=None, presen
     logits: CUDA [B, R, V] float32/float16/bfloat16, rows evenly spaced (a view
     of a padded vocabulary serves): draft rows, or the verified rows of a tree.
     history: int32 [B, H], of which lengths (int32 [B]) entries count; ids
-    outside [0, V) do not.  repetition, presence, frequency: float32 [B].
+    outside [0, V) do not.  repetition, presence, frequency: float32 [B], all
+    over that one history: repetition over a prompt and what was generated, the
+    others over what was generated alone, take two calls (the second in place).
     bias: (ids int32 [B, K], values float32 [B, K]).  allowed: packed bits,
     int32 (or uint32) [B, ceil(V/32)] or [B, R, ceil(V/32)].  tokens (int32
     [B, N]) and mask (int32 [B, N, ceil(N/32)]) of a tree, as tree_build

@@ -403,6 +403,11 @@ typedef struct {
  * in fp32, rounded once to the logits' type.  A token that is neither counted
  * nor biased keeps its bits (NaN and infinities too); one that is not allowed
  * gives -inf whatever its logit holds, and a row may lose all of its tokens.
+ * One history serves all three penalties.  Where repetition is to count the
+ * prompt as well and the other two the generated tokens alone, make two calls,
+ * the second in place: repetition over both, then presence and frequency (with
+ * the biases and masks) over what was generated; the logits pass through twice
+ * and are rounded twice.
  *  logits, out  device [B][R] rows of V elements, row_stride / out_stride >= V
  *               elements apart (at most 2^30); type dtype, element aligned.
  *               out may be logits itself (in place, the same stride); other

@@ -371,7 +371,11 @@ def rotary_frequencies(rot: int, base: float = 10000.0, factor: float = 1.0, ori
     it (the length that the model was trained on), a pair that turns more than
     `fast` times within `original` positions keeps its frequency, one that turns
     less than `slow` times is divided by factor, those between are blended
-    linearly in their number of turns, and the magnitude is 0.1 ln(factor) + 1."""
+    linearly in their number of turns, and the magnitude is 0.1 ln(factor) + 1.
+    Many models are run with another ramp instead: linear in the pair's index
+    j between the pairs that turn `fast` and `slow` times, those two rounded to
+    whole pairs.  Its frequencies differ between the two ends; for such a model
+    give Rotary the frequencies of its own ramp."""
     if rot < 2 or rot % 2 or not base > 0 or not factor >= 1:
         raise DartError("rot must be even, base > 0 and factor >= 1")
     f = float(base) ** (-np.arange(rot // 2, dtype=np.float64) / (rot // 2))

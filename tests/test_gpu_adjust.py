@@ -197,3 +197,63 @@ def test_long_histories(D, dtype, B, R, V):
     got = _call(D, s, s["z"].cuda())
     want, bound = _want(s)
     refs.close(got, want, bound, DT[dtype])
+
+
+@pytest.mark.parametrize("dtype,V,N,grammar", [("bf16", 9001, 33, None), ("f32", 8192, 5, "row"), ("f16", 1003, 70, None),
+                                               ("bf16", 40000, 1000, "sequence")])
+def test_what_lies_outside_is_not_counted(D, dtype, V, N, grammar):
+    """Tree tokens outside [0, V), mask bits from N up, bias ids outside [0, V): as if they were not there."""
+    s = _inputs(dtype, 2, N + 1, V, 50, 12, N, grammar, seed=N)
+    far = np.array([-1, -2 ** 31, V, V + 1, 2 ** 31 - 1, V + 65536, -V], np.int64).astype(np.int32)
+    rng = np.random.default_rng(N)
+    s["tokens"][:, ::3] = rng.choice(far, s["tokens"][:, ::3].shape)
+    s["bias"][0][:, 1::2] = rng.choice(far, s["bias"][0][:, 1::2].shape)
+    clean = s["mask"].copy()
+    if N % 32:
+        s["mask"].view(np.uint32)[..., -1] |= np.uint32(0xFFFFFFFF << (N % 32) & 0xFFFFFFFF)
+    assert np.array_equal(refs.unpack(s["mask"], N), refs.unpack(clean, N))
+    want, bound = _want(s)
+    got = _call(D, s, s["z"].cuda())
+    refs.close(got, want, bound, DT[dtype])
+    # the same bits as a call that names none of it
+    inside = dict(s, tokens=s["tokens"].copy(), mask=clean, bias=tuple(x.copy() for x in s["bias"]))
+    inside["bias"][0][:, 1::2] = -1
+    inside["tokens"][(s["tokens"] < 0) | (s["tokens"] >= V)] = -1
+    assert torch.equal(_call(D, inside, s["z"].cuda()).view(torch.int8), got.view(torch.int8))
+
+
+def test_histories_of_their_own_take_two_calls(D):
+    """Repetition over prompt and output, presence and frequency over the output alone: two calls, the second in place."""
+    s = _inputs("f32", 2, 4, 5000, 90, 7, 0, "row", seed=31)
+    s["history"] = np.abs(s["history"]) % 4000
+    prompt, made = s["history"], s["history"][:, 60:]
+    g = lambda x: torch.from_numpy(np.ascontiguousarray(x)).cuda()
+    z = D.adjust_logits(s["z"].cuda(), history=g(prompt), repetition=g(s["rep"]))
+    got = D.adjust_logits(z, history=g(made), presence=g(s["pres"]), frequency=g(s["freq"]),
+                          bias=tuple(g(x) for x in s["bias"]), allowed=g(s["allowed"]), out=z)
+    first, bound1 = refs.adjust(s["z"], prompt, None, s["rep"])
+    want, bound2 = refs.adjust(first, made, None, None, s["pres"], s["freq"], s["bias"], s["allowed"])
+    # the first call's rounding to fp32 enters the second as it stands
+    refs.close(got, want, bound2 + bound1 + first.abs() * 2.0 ** -24, torch.float32)
+
+
+@pytest.mark.parametrize("dtype,B,R,V", [("bf16", 60, 240, 151936), ("f16", 60, 240, 151933), ("f32", 46, 3, 16000003)])
+def test_more_elements_than_32_bits_count(D, dtype, B, R, V):
+    """Offsets past 2^31 elements (past 2^32 bytes): every sequence as it comes out by itself."""
+    assert B * R * V > 2 ** 31
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    z = torch.empty(B, R, V, dtype=DT[dtype], device="cuda")
+    for b in range(B):
+        z[b].normal_(generator=gen)
+    draw = lambda high, *s: torch.randint(0, high, s, dtype=torch.int32, device="cuda", generator=gen)
+    kw = dict(history=draw(V, B, 40), repetition=torch.rand(B, device="cuda", generator=gen) + 0.6,
+              frequency=torch.rand(B, device="cuda", generator=gen), allowed=draw(2 ** 31 - 1, B, (V + 31) // 32))
+    ids, vals = draw(V, B, 20), torch.randn(B, 20, device="cuda", generator=gen)
+    got = D.adjust_logits(z, bias=(ids, vals), **kw)
+    for b in range(B):
+        alone = D.adjust_logits(z[b:b + 1].clone(), bias=(ids[b:b + 1], vals[b:b + 1]),
+                                **{k: x[b:b + 1].contiguous() for k, x in kw.items()})
+        assert torch.equal(got[b].view(torch.int8), alone[0].view(torch.int8)), b
+    D.adjust_logits(z, bias=(ids, vals), out=z, **kw)
+    for b in range(B):
+        assert torch.equal(z[b].view(torch.int8), got[b].view(torch.int8)), b

@@ -282,3 +282,82 @@ def test_empty_calls(D):
     s = _case("f16", [5], [0], 2, 1, 64, 8, seed=9)
     d = _cuda(s)
     assert D.tree_attention(*_args(d))["out"].shape == (0, 2, 64)
+
+
+def _tile_columns(S, dim, shift):
+    """[S, dim] of 0 and 1: position p of tile t = p // 128 has a 1 in columns t mod a and a + t mod b (a + b <= dim
+    without a common factor, so that the pair names the tile), all moved by `shift`."""
+    a, b = {64: (31, 33), 96: (47, 49), 128: (61, 67)}[dim]
+    t = torch.arange(S) // 128
+    assert S <= 128 * a * b
+    x = torch.zeros(S, dim, dtype=torch.float64)
+    x[torch.arange(S), t % a] = 1.0
+    x[torch.arange(S), a + t % b] = 1.0
+    return x.roll(shift, 1)
+
+
+def _uniform(s, D_of_head, skip=None):
+    """(out, lse) of equal weights over what each row sees; without tile `skip` = (sequence, tile): a planted mistake."""
+    T, Hq, dim = s["q"].shape
+    Hkv = s["k_cache"].shape[2]
+    N = s["mask"].shape[1] if s["mask"] is not None else 0
+    out = torch.full((T, Hq, dim), math.nan, dtype=torch.float64)
+    lse = torch.full((T, Hq), math.nan, dtype=torch.float64)
+    tiles = torch.ones(T, Hq, 1, dtype=torch.float64)
+    for b, len_ in enumerate(s["lengths"]):
+        at, n = int(s["starts"][b]), int(s["starts"][b + 1] - s["starts"][b])
+        S, lead = int(len_) + n, max(n - N, 0)
+        if n == 0:
+            continue
+        see = torch.from_numpy(np.stack([refs.visible(int(len_), n, N, i, s["mask"][b, i - lead] if i >= lead else None)
+                                         for i in range(n)])).double()
+        if skip is not None and skip[0] == b:
+            see[:, 128 * skip[1]:128 * skip[1] + 128] = 0.0
+        count = see.sum(-1, keepdim=True)
+        for h in range(Hkv):
+            rows = (see @ _tile_columns(S, dim, D_of_head * h)) / count
+            for g in range(h * Hq // Hkv, (h + 1) * Hq // Hkv):
+                out[at:at + n, g], lse[at:at + n, g] = rows, torch.log(count)[:, 0]
+        tiles[at:at + n] = (S + 127) // 128
+    return out, lse, tiles
+
+
+@pytest.mark.parametrize("dtype,lengths,counts,Hq,Hkv,dim,page,N", [
+    ("bf16", [60000], [1], 8, 1, 128, 128, 0),           # one block over every CTA
+    ("f16", [130000], [1], 4, 1, 64, 64, 0),
+    ("bf16", [30000, 77, 12001, 0, 9000], [33, 5, 33, 1, 33], 8, 2, 128, 16, 32),
+    ("bf16", [5000], [700], 16, 2, 96, 64, 0),           # causal blocks of growing length
+    ("f16", [2900 - 71 * i for i in range(36)], [79] * 36, 8, 2, 128, 16, 78),       # blocks of 256 rows and of 60
+])
+@pytest.mark.parametrize("scale", [0.0, None])
+def test_every_tile_counts_once(D, dtype, lengths, counts, Hq, Hkv, dim, page, N, scale):
+    """Equal weights (scale 0, or keys of zeros) over values that name their tile: a tile that is lost or taken twice
+    where a span ends, parts are joined or the order turns around changes its columns by a thirtieth or more.
+
+    A weight is 2^x with |x| below 2^-140: 1 within 2^-22, exactly 1 once rounded to 16 bits, so the products' sums are
+    whole numbers, exact in fp32.  The sum of weights: 32 additions in a lane's chain, one a tile, one a part, each off
+    by at most u; a part's factor 2^-22 and a product, in sum and output alike; 1 / l, its product and a spare u."""
+    shift = 7
+    s = _case(dtype, lengths, counts, Hq, Hkv, dim, page, N, seed=len(lengths) + dim)
+    for b, len_ in enumerate(lengths):
+        p = torch.arange(len_ + counts[b])
+        where = (torch.from_numpy(s["pages"][b]).long()[p // page], p % page)
+        if scale is None:
+            s["k_cache"][where] = 0.0
+        for h in range(Hkv):
+            s["v_cache"][where + (torch.full_like(p, h),)] = _tile_columns(len(p), dim, shift * h).to(DT[dtype])
+    d = _cuda(s)
+    got = D.tree_attention(*_args(d), mask=d["mask"], scale=scale, lse=True)
+    assert D.device_error(got["workspace"]) == 0
+    want, lse, tiles = _uniform(s, shift)
+    off = 3 * 2.0 ** -22 + (32 + tiles + 2 * 152 + 3) * refs.U
+    refs.close(got["out"], want, off * want, DT[dtype])
+    near = off[..., 0] + 2.0 ** -22 + 8 * refs.U * lse
+    refs.close(got["lse"], lse, near, torch.float32)
+    b = int(np.argmax(lengths))
+    for tile in (0, lengths[b] // 256, lengths[b] // 128 - 1):            # the check sees a lost tile
+        lost, lost_lse, _ = _uniform(s, shift, (b, tile))
+        with pytest.raises(AssertionError):
+            refs.close(got["out"], lost, off * lost, DT[dtype])
+        with pytest.raises(AssertionError):
+            refs.close(got["lse"], lost_lse, near, torch.float32)

@@ -10,7 +10,7 @@
 // 2^8 (the factor 2^(m - m') then touches O); p stays below 2^8 and l above 2^-0
 // until then, which neither fp16 nor fp32 minds.
 //
-// One persistent CTA per SM.  The work is the list of (sequence, key head,
+// One persistent CTA per SM (at most 152).  The work is the list of (sequence, key head,
 // block of 256 rows, tile of 128 positions), cut into equal contiguous spans,
 // so a block's tiles may be spread over several CTAs: each leaves (m, l, O) of
 // its part in the workspace and the join kernel merges them in a fixed order.
@@ -62,7 +62,7 @@ constexpr int kThreads = 384;
 // (256 * 208 + 128 * 88 = 384 * 168)
 constexpr int kSoftmaxRegs = 208;
 constexpr int kIssueRegs = 88;
-constexpr int kCtas = 152;              // nominal: the workspace does not depend on the device
+constexpr int kCtas = 152;              // at most: the workspace does not depend on the device
 constexpr int kHalfRows = 128;
 constexpr int kBlockRows = 2 * kHalfRows;
 constexpr int kTile = 128;              // cache positions per tile
@@ -1110,14 +1110,16 @@ cudaError_t launch(const AttendParams& P, const CUtensorMap& km, const CUtensorM
   cudaError_t e =
       settled(cudaFuncSetAttribute(attend_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if (e != cudaSuccess) return e;
-  e = launch_kernel(attend_kernel<T, DH>, kCtas, kThreads, smem, s, P, km, vm);
+  // no more CTAs than run together: the spans are equal, so a CTA of a second round would double the time
+  const int sms = device_sms(), ctas = sms > 0 && sms < kCtas ? sms : kCtas;
+  e = launch_kernel(attend_kernel<T, DH>, ctas, kThreads, smem, s, P, km, vm);
   if (e != cudaSuccess) return e;
   // the join's CTAs take their places while the last attention CTAs finish, and wait there
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
   at[0].val.programmaticStreamSerializationAllowed = 1;
   cudaLaunchConfig_t cfg = {};
-  cfg.gridDim = dim3(kCtas, (P.slot_rows + kJoinRows - 1) / kJoinRows);
+  cfg.gridDim = dim3(ctas, (P.slot_rows + kJoinRows - 1) / kJoinRows);
   cfg.blockDim = dim3(128 * DH);
   cfg.stream = s;
   cfg.attrs = at;

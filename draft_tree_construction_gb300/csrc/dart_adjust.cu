@@ -19,11 +19,14 @@
 //   64 x 8 rows of 151936, 2048 tokens of history, 300 biases   59 us, 5.3 TB/s
 //   4 trees of 497 rows of 151936, 4096 tokens, one mask each  215 us, 5.3 TB/s
 //   256 x 8 rows of 32000 (fp16), masks that keep 2% of a row   55 us: 2.6 TB/s
-//     of what has to move, 3.5 TB/s of what does, since a kept logit brings its
-//     128-byte line
+//     of what has to move, 4.3 TB/s of the 235 MB that do (131 written; 104 read,
+//     since a kept logit brings its 128-byte line).  As long as with masks that
+//     keep everything (56 us, 270 MB); 39 us with masks that keep nothing.  Its
+//     1024 CTAs are 3.4 rounds: 228 sequences, three rounds, take 46 us
 //   8 rows of 151936 of one sequence                            4.4 us
 // Looking into every vector for touched elements instead took 99 and 359 us for
-// the first two, registers in place of the ring 73 and 245 us.
+// the first two, registers in place of the ring 73 and 245 us, but 49 us for the
+// masked rows.
 #include <algorithm>
 #include <cmath>
 
@@ -137,8 +140,10 @@ __device__ __forceinline__ uint4 ban(uint4 u, uint4 m) {
 
 // How the rows lie: every one begins on a 16-byte boundary, in and out; every
 // one is as far from such a boundary in as it is out; or neither, and elements
-// are taken one by one.  64 x 8 rows of 151936 with biases: 58 us aligned, 71 us
-// shifted (an odd row length), 320 us one by one.
+// are taken one by one.  64 x 8 rows of 151936 with biases: 59 us aligned, 70 us
+// shifted (an odd row length: a block of an unaligned row leaves a vector's worth
+// of elements at its ends to be read and written singly), 330 us one by one (2
+// bytes a lane and instruction).
 enum Rows { kAligned, kShifted, kSingle };
 template <typename T, int ROWS>
 __global__ void __launch_bounds__(kAdjThreads, 2)

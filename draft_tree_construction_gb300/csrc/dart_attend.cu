@@ -34,6 +34,7 @@
 //     threads a row, 64 positions each: 1460 us (the exponentials, 512 cycles a
 //     half's tile, and the row's exchange leave the softmax at 1500).
 //   32 trees of 497 rows over ~3100 positions  721 us, 1.11 PFLOP/s of what is seen
+//     (830 us when the card holds its power limit for seconds)
 //   64 trees of 79 rows over ~1600 positions   181 us: 316 rows are a block of
 //     256 and one of 60, so the cache passes through the CTAs twice (5 TB/s from
 //     L2 and memory), and six block changes a CTA take a tenth.  Dealing the

@@ -8,6 +8,7 @@ whether or not that succeeds.
 """
 from __future__ import annotations
 
+import contextlib
 import glob
 import os
 import shutil
@@ -114,20 +115,36 @@ def build(force: bool = False, verbose: bool = False, extra_flags: list[str] | N
             for old in _modules():
                 if old != path:
                     os.remove(old)
-    finally:
-        if compiling is not None:
-            out, _ = compiling.communicate()
-            why = out.decode(errors="replace") if compiling.returncode else ""
+    except BaseException:
+        _finish_native(compiling)
+        _remove(native)
+        raise
     if want_native:
+        why = why or _finish_native(compiling)
         _native_failed = bool(why)
         if why:
-            if os.path.exists(path):           # of other sources: its structures may lie differently
-                os.remove(path)
+            _remove(native)
+            _remove(path)                      # of other sources: its structures may lie differently
             warnings.warn(f"_steps_native was not built, calls of the steps around a tree take some microseconds "
                           f"longer:\n{why}", RuntimeWarning, stacklevel=2)
         else:
             os.replace(native, path)
     return LIB
+
+
+def _finish_native(compiling) -> str:
+    """What went wrong with the compilation, "" if nothing did."""
+    if compiling is None:
+        return ""
+    out, _ = compiling.communicate()
+    if compiling.returncode == 0:
+        return ""
+    return out.decode(errors="replace") or f"the host compiler returned {compiling.returncode}"
+
+
+def _remove(path: str) -> None:
+    with contextlib.suppress(FileNotFoundError):
+        os.remove(path)
 
 
 def _build_library(verbose: bool, extra: list[str]) -> None:

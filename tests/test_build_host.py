@@ -78,6 +78,20 @@ def test_a_library_that_fails_to_compile_raises(tree):
     assert "lib.so" not in tree.files() and _build.needs_build()
 
 
+def test_a_compiler_that_dies_without_a_word_has_failed(tree, tmp_path):
+    tree.set("CXX", "#!{python}\nimport sys\n# {log}\nopen(sys.argv[sys.argv.index('-o') + 1], 'w')\nsys.exit(9)\n")
+    with pytest.warns(RuntimeWarning, match="returned 9"):
+        _build.build()
+    assert tree.files() == {"lib.so"}
+
+
+def test_a_failed_build_leaves_no_parts(tree):
+    tree.set("NVCC", FAILS)
+    with pytest.raises(RuntimeError):
+        _build.build()
+    assert tree.files() == set()
+
+
 def test_a_module_of_other_sources_does_not_stay(tree):
     """Its structures may lie differently than the new library's."""
     _build.build()

@@ -29,6 +29,7 @@ __all__ = [
     "tree_build", "tree_build_noalloc", "tree_from_topk", "tree_from_rows", "row_topk", "mask_pack", "tree_select", "set_wait_limit", "device_error", "noalloc_device_error",
     "TreeBuilder",
     "adjust_logits", "kv_append", "tree_attention", "attention_workspace_bytes", "Rotary", "rotary_frequencies",
+    "sample_logits", "tree_accept", "kv_keep", "attention_weights", "kv_evict",
     "DTYPE_CODES",
 ]
 
@@ -121,6 +122,7 @@ def _declare(L):
     L.dart_status_string.argtypes = [i32]
     L.dart_status_string.restype = C.c_char_p
     _steps.declare(L)
+    _verified.declare(L)
     return L
 
 
@@ -746,3 +748,5 @@ class TreeBuilder:
 from . import _steps  # noqa: E402  (it builds on the helpers above)
 from ._steps import (Rotary, adjust_logits, attention_workspace_bytes, kv_append, rotary_frequencies,  # noqa: E402
                      tree_attention)
+from . import _verified  # noqa: E402
+from ._verified import attention_weights, kv_evict, kv_keep, sample_logits, tree_accept  # noqa: E402

@@ -25,7 +25,8 @@ BUILD = os.path.join(HERE, "_build")
 LIB = os.path.join(HERE, "libdarttree.so")
 NATIVE_SOURCE = os.path.join(CSRC, "dart_steps_py.cpp")
 SOURCES = ["dart_api.cu", "dart_rows.cu", "dart_tree.cu", "dart_select.cu", "dart_probe.cu",
-           "dart_adjust.cu", "dart_append.cu", "dart_attend.cu"]
+           "dart_adjust.cu", "dart_append.cu", "dart_attend.cu",
+           "dart_sample.cu", "dart_keep.cu", "dart_weights.cu"]
 
 NVCC = os.environ.get("NVCC", "nvcc")
 CXX = os.environ.get("CXX", "g++")

@@ -516,6 +516,129 @@ int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
                         void* out, int64_t out_token_stride, int64_t out_head_stride, float* out_lse,
                         void* workspace, size_t workspace_bytes, void* stream);
 
+/* ------------------------------------------------------------ behind a verified tree
+ * What a serving loop does once the target's rows of a tree are known: a token
+ * is drawn at every row (dart_logits_sample), the tree is walked along the
+ * drawn tokens (dart_tree_accept), the path's keys and values move up behind
+ * the root (dart_kv_keep); and, where a cache has to stay within a budget, the
+ * attention that each position gets is added up (dart_attention_weights) and
+ * the positions that got most stay (dart_kv_evict). */
+
+/* Draws a token from each row of logits.  With the row's tokens in descending
+ * order of their logits, the lower id first where they are equal, and
+ *   w_i = exp((z_i - max) / temperature)
+ * the first n of that order are kept: n = max(1, min(top_k, n_p, n_m)), n_p the
+ * first place where the running sum of w reaches top_p times the sum of the
+ * first top_k, n_m the number of w_i >= min_p.  The token drawn is the first
+ * whose running sum exceeds u times the sum of the n kept; its probability is
+ * w / that sum.  Weights are integers of 2^(62 - ceil(log2(V + 1))) parts of
+ * the largest, exact to a few of them, and sums are exact, so a draw does not
+ * depend on the order of summation.
+ * NaN and -inf are never drawn; a row without any other logit gives token -1
+ * and probability 0.  +inf is drawn before anything finite.
+ *  logits      device [B][R] rows of V elements, row_stride >= V apart (at most
+ *              2^30), element aligned; the padding is not read.  V < 2^24,
+ *              B * R < 2^31
+ *  uniforms    device float [B][R], in [0, 1) (smaller counts as 0, larger draws
+ *              the last kept token)
+ *  temperature device float [B] or NULL (1); <= 0 or NaN: the first token of the
+ *              order, probability 1
+ *  top_k       device int32 [B] or NULL; <= 0: no limit
+ *  top_p       device float [B] or NULL; >= 1 or NaN: no limit, <= 0: one token
+ *  min_p       device float [B] or NULL; <= 0 or NaN: no limit
+ *  out_tokens  device int32 [B][R], out_probs device float [B][R]
+ * Nothing is launched when B or R is 0.  Returns DART_OK or an error code. */
+int dart_logits_sample(const void* logits, int B, int R, int V, int64_t row_stride, int dtype,
+                       const float* uniforms, const float* temperature, const int32_t* top_k,
+                       const float* top_p, const float* min_p, int32_t* out_tokens, float* out_probs,
+                       void* stream);
+
+/* Walks each tree along the tokens picked at its nodes (DART, Figure 3 caption:
+ * the target verifies the tree): from the root, to the child whose token is the
+ * pick of the node reached (the lowest child where several carry it), until
+ * none is or `depth` nodes are accepted.
+ *  picks       device int32 [B][N + 1]: the root's pick, then each node's (as
+ *              dart_logits_sample draws them from a tree's N + 1 rows)
+ *  tokens, parents  device int32 [B][N], as dart_tree_build writes them.  A
+ *              negative token is never accepted, nor is a node whose parent is
+ *              not below it.  N <= 1024
+ *  depth       0..N, the most nodes accepted
+ *  out_path    device int32 [B][depth + 1]: 0 (the root's row), then the row
+ *              (node + 1) of each accepted node, increasing; -1 behind
+ *  out_counts  device int32 [B]: entries of the path, the accepted nodes + 1
+ *  out_tokens  device int32 [B][depth + 1]: the pick at each entry of the path,
+ *              so the accepted tokens and the one that follows them; -1 behind
+ * Returns DART_OK or an error code. */
+int dart_tree_accept(const int32_t* picks, const int32_t* tokens, const int32_t* parents, int B, int N,
+                     int depth, int32_t* out_path, int32_t* out_counts, int32_t* out_tokens, void* stream);
+
+/* Moves the rows of a path up behind one another: position lengths[b] +
+ * path[b][i] of K and V, all heads, goes to lengths[b] + i for i < counts[b].
+ * In place; nothing else of the cache is written.  The pages of the positions
+ * written belong to one sequence only.
+ *  lengths     device [B], tokens in the cache before the chunk, >= 0
+ *  path        device int32 [B] rows of `width` >= 1, path_stride apart,
+ *              increasing, path[i] >= i
+ *  counts      device int32 [B], 0..width
+ *  out_lengths device int32 [B] or NULL: lengths[b] + counts[b].  Not lengths
+ *              itself: every layer's call reads that.
+ * A length or count out of range leaves the sequence and its length as they
+ * are; an entry out of order, a position or a page id out of range is left out;
+ * each sets DART_DEVERR_CACHE in *device_err (device uint32 or NULL).  Returns
+ * DART_OK or an error code. */
+int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, const int32_t* path, int64_t path_stride,
+                 const int32_t* counts, int B, int width, int32_t* out_lengths, uint32_t* device_err,
+                 void* stream);
+
+/* Adds to each cached position the attention weights that a chunk's rows give
+ * it: for position p and key head h,
+ *   scores[b][h][p] += sum exp(scale * q.k_p - lse)
+ * over the chunk's tokens that see p (dart_tree_attention says which) and the
+ * q_heads / heads queries of h, lse being what dart_tree_attention returned for
+ * the same call.  fp32, summed in a fixed order; scores of other positions are
+ * not touched.  A row whose lse is not finite adds nothing (a caller sets +inf to
+ * leave a row out, say of a node that was not accepted), and what a row does not
+ * see does not reach a score.  Only the cache's k is read.
+ *  q, lengths, starts, mask, N, scale   as for dart_tree_attention
+ *  lse         device float [T][q_heads]
+ *  scores      device float [B][heads] rows of scores_width elements with the
+ *              given strides; positions from scores_width on are left out and
+ *              set DART_DEVERR_CACHE, as lengths and page ids out of range do
+ *              (the latter read as zeros)
+ *  device_err  device uint32 or NULL; a wait that runs out sets
+ *              DART_DEVERR_WAIT_TIMEOUT there
+ * Returns DART_OK or an error code. */
+int dart_attention_weights(const void* q, int64_t q_token_stride, int64_t q_head_stride, int q_heads,
+                           int T, int B, const int32_t* lengths, const int32_t* starts,
+                           const uint32_t* mask, int N, float scale, const dart_cache_t* cache,
+                           const float* lse, float* scores, int64_t scores_seq_stride,
+                           int64_t scores_head_stride, int scores_width, uint32_t* device_err,
+                           void* stream);
+
+/* Brings each sequence of more than `keep` tokens back to `keep`: per key head
+ * the first `first` positions, the last `last`, and of those between the ones of
+ * largest score (the lower position first where scores are equal; NaN is the
+ * least) stay, in their order.  Their keys, values and scores move up to
+ * positions 0 .. keep - 1, in place; the scores behind them, up to the old
+ * length, become 0.  The heads of a position part ways: slot i of two heads may
+ * hold different tokens, which attention does not mind.  Keys keep the rotary
+ * positions they were written with, so later calls of dart_kv_append give
+ * offsets from the shortened length.  A sequence's pages belong to it alone.
+ *  lengths     device [B], tokens in the cache
+ *  scores      device float, as for dart_attention_weights
+ *  keep        >= 1; first, last >= 0, first + last <= keep
+ *  out_index   device int32 [B][heads][keep]: the old position of each slot; -1
+ *              from the length on
+ *  out_lengths device int32 [B] or NULL: min(length, keep).  Not lengths itself.
+ * A length beyond the table's pages or scores_width leaves the sequence and its
+ * length as they are, a page id out of range the rows in it; either sets
+ * DART_DEVERR_CACHE in *device_err (device uint32 or NULL).  Returns DART_OK or
+ * an error code. */
+int dart_kv_evict(const dart_cache_t* cache, const int32_t* lengths, int B, float* scores,
+                  int64_t scores_seq_stride, int64_t scores_head_stride, int scores_width, int keep,
+                  int first, int last, int32_t* out_index, int32_t* out_lengths, uint32_t* device_err,
+                  void* stream);
+
 /* Smallest power of two >= max(2 * M, 8) (load factor at most 1/2); 0 on
  * overflow. */
 uint64_t dart_ngram_capacity_for(uint64_t M);
@@ -553,7 +676,8 @@ int dart_device_error(const void* workspace, uint32_t* out_flags, void* stream);
 int dart_noalloc_device_error(uint32_t* out_flags, void* stream);
 
 /* Sets the number of SM clock cycles any one wait of the row pass (a bulk
- * copy landing, a slot freeing, a barrier of the CTA) or of dart_tree_attention
+ * copy landing, a slot freeing, a barrier of the CTA), of dart_tree_attention or
+ * of dart_attention_weights
  * (a tile landing, a product or its operands) may take before the kernel
  * gives up: the CTA then ends every other wait, lets its copies in flight
  * land, sets DART_DEVERR_WAIT_TIMEOUT and returns, and its outputs are

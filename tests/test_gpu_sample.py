@@ -1,0 +1,185 @@
+"""sample_logits against its 64-bit form (needs a GB300)."""
+import math
+
+import numpy as np
+import pytest
+
+from tests import verified_refs as refs
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
+
+
+def _near(V):
+    """How near to an edge, as a share of the sum, u may lie for another token to be drawn.
+
+    A weight is within one part of 2^-(62 - bits) of the largest, bits = the length of V, and within 2^-45 of itself; a
+    sum of up to V of them, at least the largest, within V parts and 2^-45.  The running sum and its total are both off
+    by that, the reference's own sums in 64 bits by less: four times it covers them."""
+    return 4.0 * (V * 2.0 ** -(62 - V.bit_length()) + 2.0 ** -45)
+
+
+@pytest.fixture(scope="module")
+def D():
+    import draft_tree_construction_gb300 as D
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    D.build()
+    return D
+
+
+def _check(D, z, u, heat=None, k=None, p=None, m=None):
+    """z [B, R, V] and u [B, R] on the CPU, the settings as lists over B; a share of 2^-8 of the rows at most lies too
+    near an edge to say."""
+    B, R, V = z.shape
+    f = lambda x: None if x is None else torch.tensor(x, dtype=torch.float32, device="cuda")
+    zc = z.cuda() if z.is_contiguous() else torch.empty_strided(z.shape, z.stride(), dtype=z.dtype, device="cuda").copy_(z)
+    out = D.sample_logits(zc, u.cuda(), temperature=f(heat), top_p=f(p), min_p=f(m),
+                          top_k=None if k is None else torch.tensor(k, dtype=torch.int32, device="cuda"))
+    tokens, probs = out["tokens"].cpu(), out["probs"].cpu()
+    assert tokens.dtype == torch.int32 and probs.dtype == torch.float32
+    unsaid = 0
+    for b in range(B):
+        rows = z[b].double().numpy()
+        one = lambda x, default: default if x is None else float(np.float32(x[b]))
+        for r in range(R):
+            t, pr, near = refs.sample(rows[r], float(u[b, r]), one(heat, 1.0), int(one(k, 0)), one(p, 1.0), one(m, 0.0))
+            if near < _near(V):
+                unsaid += 1
+                continue
+            assert int(tokens[b, r]) == t, (b, r, near)
+            # a quotient of exact integers, rounded once
+            assert abs(float(probs[b, r]) - pr) <= 2.0 ** -23 * pr + 1e-30, (b, r)
+    assert unsaid <= max(1, B * R // 256)
+    return tokens
+
+
+def _logits(B, R, V, dtype, seed, scale=2.0, pad=0, spikes=8):
+    g = torch.Generator().manual_seed(seed)
+    z = torch.randn((B, R, V + pad), generator=g) * scale
+    ids = torch.randint(0, V, (B, R, spikes), generator=g)
+    z.scatter_add_(2, ids, torch.rand((B, R, spikes), generator=g) * 10)
+    z[..., V:] = 1e4
+    return z.to(DT[dtype])[..., :V], torch.rand((B, R), generator=g)
+
+
+SETTINGS = {
+    "all": {}, "heat": dict(heat=[0.3, 0.8, 1.7]), "greedy": dict(heat=[0.0, -1.0, math.nan]),
+    "top_k": dict(k=[1, 5, 40]), "many_k": dict(k=[0, 900, 100000]), "top_p": dict(p=[0.1, 0.9, 0.999]),
+    "no_p": dict(p=[1.0, 0.0, 2.0]), "min_p": dict(m=[0.05, 0.5, 1.0]), "no_m": dict(m=[0.0, 1.5, -1.0]),
+    "each": dict(heat=[0.7, 1.0, 1.3], k=[50, 0, 300], p=[0.8, 0.95, 1.0], m=[0.01, 0.0, 0.1]),
+    "k_then_p": dict(heat=[0.9, 2.0, 5.0], k=[20, 200, 2000], p=[0.5, 0.9, 0.99]),
+}
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("name", list(SETTINGS))
+def test_settings(D, dtype, name):
+    z, u = _logits(3, 11, 5003, dtype, seed=len(name), pad=5)
+    _check(D, z, u, **SETTINGS[name])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [1, 2, 3, 7, 8, 31, 64, 257, 1000, 32000, 151936])
+def test_sizes(D, dtype, V):
+    R = 3 if V > 10000 else 9
+    z, u = _logits(2, R, V, dtype, seed=V, spikes=min(8, V))
+    _check(D, z, u, heat=[0.8, 1.1], k=[0, 20], p=[0.95, 0.9])
+    _check(D, z, u, m=[0.02, 0.0])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("pad", [1, 3, 8, 13])
+def test_rows_at_any_alignment(D, dtype, pad):
+    z, u = _logits(2, 6, 777, dtype, seed=pad, pad=pad)
+    _check(D, z, u, heat=[1.0, 0.6], p=[0.97, 1.0])
+
+
+# values that share a bin: all tiny, all large, one step apart in 32 bits, few distinct ones
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("kind", ["tiny", "large", "huge", "close", "quantised", "constant", "negative", "signed zeros"])
+def test_unusual_values(D, dtype, kind):
+    g = torch.Generator().manual_seed(5)
+    n = torch.randn((2, 8, 3001), generator=g)
+    z = {"tiny": n * 1e-4, "large": n * 300, "huge": n * 3e4, "close": 10 + n * 1e-4, "quantised": (n * 2).round(),
+         "constant": torch.full_like(n, 3.25), "negative": -5 - n.abs() * 3,
+         "signed zeros": torch.where(n > 0, 0.0, -0.0)}[kind].to(DT[dtype])
+    u = torch.rand((2, 8), generator=g)
+    _check(D, z, u)
+    _check(D, z, u, heat=[0.01, 50.0], p=[0.9, 0.5])
+    _check(D, z, u, k=[7, 1500], p=[0.9, 1.0], m=[0.0, 0.2])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_rows_with_nothing_and_with_infinities(D, dtype):
+    z, u = _logits(1, 8, 501, dtype, seed=2)
+    z = z.clone()
+    z[0, 0] = -math.inf                       # a grammar's mask that leaves nothing
+    z[0, 1] = math.nan
+    z[0, 2, ::2] = -math.inf
+    z[0, 3, ::3] = math.nan
+    z[0, 4, 7] = math.inf
+    z[0, 5, [3, 400]] = math.inf
+    z[0, 6, :500] = -math.inf                 # one token left
+    z[0, 7, 1:] = torch.finfo(DT[dtype]).min  # a mask of the type's lowest value
+    for kw in ({}, dict(p=[0.9]), dict(k=[3], m=[0.1]), dict(heat=[0.0]), dict(heat=[1e-30])):
+        tokens = _check(D, z, u, **kw)
+        assert tokens[0, 0] == -1 and tokens[0, 1] == -1 and tokens[0, 4] == 7 and tokens[0, 6] == 500
+
+
+def test_ends_of_the_uniforms(D):
+    z, _ = _logits(1, 6, 4000, "bf16", seed=3)
+    u = torch.tensor([[0.0, 1.0 - 2.0 ** -24, 1.0, -1.0, 2.0, math.nan]])
+    out = D.sample_logits(z.cuda(), u.cuda(), top_p=torch.tensor([0.9], device="cuda"))
+    got = out["tokens"].cpu()[0].tolist()
+    rows = z[0].double().numpy()
+    clamp = [0.0, 1.0 - 2.0 ** -24, 1.0 - 2.0 ** -24, 0.0, 1.0 - 2.0 ** -24, 0.0]
+    assert got == [refs.sample(rows[i], clamp[i], p=float(np.float32(0.9)))[0] for i in range(6)]
+
+
+def test_draws_follow_the_distribution(D):
+    """65536 evenly spaced numbers over one row: each token is drawn as often as its weight says, within one."""
+    z, _ = _logits(1, 1, 300, "f32", seed=9, scale=1.0, spikes=1)
+    n = 1 << 16
+    rows = z.expand(1, n, 300).contiguous().cuda()
+    u = ((torch.arange(n) + 0.5) / n)[None].cuda()
+    tokens = D.sample_logits(rows, u)["tokens"].cpu()[0].numpy()
+    p = torch.softmax(z[0, 0].double(), -1).numpy()
+    assert np.all(np.abs(np.bincount(tokens, minlength=300) - p * n) <= 1.0 + 1e-6 * n)
+
+
+def test_empty_and_refusals(D):
+    z, u = _logits(2, 3, 50, "bf16", seed=1)
+    z, u = z.cuda(), u.cuda()
+    assert D.sample_logits(z[:0], u[:0])["tokens"].shape == (0, 3)
+    for bad in (dict(uniforms=u.double()), dict(uniforms=u[:, :2]), dict(logits=z.double()), dict(logits=z[0]),
+                dict(top_k=torch.ones(2, device="cuda")), dict(temperature=torch.ones(3, device="cuda")),
+                dict(min_p=torch.ones(2))):
+        kw = dict(logits=z, uniforms=u)
+        kw.update(bad)
+        with pytest.raises(D.DartError):
+            D.sample_logits(kw.pop("logits"), kw.pop("uniforms"), **kw)
+
+
+def test_stream_and_graph(D):
+    z, u = _logits(4, 5, 9000, "f16", seed=4)
+    z, u = z.cuda(), u.cuda()
+    p = torch.full((4,), 0.9, device="cuda")
+    want = D.sample_logits(z, u, top_p=p)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    other = D.sample_logits(z, u, top_p=p, stream=s)
+    torch.cuda.synchronize()
+    assert torch.equal(other["tokens"], want["tokens"])
+    g = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(g):
+        out = D.sample_logits(z, u, top_p=p)
+    u.copy_(u.flip(0))
+    z.copy_(z.flip(0))
+    g.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(out["tokens"], want["tokens"].flip(0))
+    assert torch.equal(out["probs"], want["probs"].flip(0))

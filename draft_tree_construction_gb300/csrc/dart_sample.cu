@@ -7,21 +7,23 @@
 // p times the sum of the first k, n_m the number of w_i >= min_p.  The token is the
 // first whose running sum exceeds u times the sum of the n kept ones.
 //
-// Nothing is sorted.  The order is by value, so a histogram of the values answers every
-// question of place: a 16-bit logit is its own bin (where its magnitude is usual; the
-// rest share three bins), and a bin's weight is its count times the weight of its one
-// value.  So a row is read once with an integer add in shared memory for each logit, the
-// exponentials are those of a few thousand values, and a second reading (from L2) finds
-// the wanted occurrence of the value that was drawn.  Bins of several values (all of
-// them where logits have 32 bits) have their weights summed element by element, and the
-// one that a place falls into is divided again, 2048 parts at a time, until its parts
-// hold one value each.
+// Rows are not sorted.  What matters of a row is a few hundred tokens near its largest
+// logit, so one reading finds the largest, a second one (from L2) lists the tokens within
+// 2^-12 of its weight and sums the others' weights, and the list alone is sorted and
+// summed.  Where a limit or the random number reaches further down, a histogram of the
+// distances from the largest (1/64 of a binary order each) says how far, and the second
+// reading is repeated: to that depth, or, where more than 2048 tokens lie before it, for
+// the tokens around that place alone, those before it only summed.  What is left (many
+// equal values, several limits far down) goes by general(), a histogram of the values.
 //
 // Which token a random number falls on is a matter of the last bits of sums over the
-// whole vocabulary, so weights are 64-bit integers: 2^-y to 2^-45 or better, summed
-// exactly in any order.  Results are the same bits every time.
+// whole vocabulary, so weights are 64-bit integers, good to 2^-45, and their sums exact in
+// any order.  Only sums of what is not listed are taken with less (the bounds are at Tail
+// and Mid); where a place lies so near to an edge that this could matter, the next form
+// decides, general() at last.  Results are the same bits every time.
 //
-// Latency and shared-memory adds bound it, not memory: see the figures at the launch.
+// Rows that are fewer than the SMs are shared by up to eight CTAs of a cluster, which hand
+// their largest logit, list and sum to the first one through distributed shared memory.
 #include <cmath>
 
 #include "dart_launch.h"
@@ -30,7 +32,8 @@ namespace dart {
 namespace {
 
 constexpr unsigned kFull = 0xFFFFFFFFu;
-constexpr int kThreads = 512, kWarps = kThreads / 32;
+constexpr int kThreads = 512;                // of general(), and of a row that is shared
+constexpr int kManyThreads = 256, kManyCtas = 4;   // of one row of many
 constexpr int kParts = 2048;                 // of a bin that is divided again
 
 struct SampleParams {
@@ -41,6 +44,8 @@ struct SampleParams {
   int32_t* tokens;
   float* probs;
   int R, V, shift;                           // a weight of 1 is 2^shift
+  int ranks;                                 // CTAs that share a row
+  long long rows;
 };
 
 // Which 16-bit magnitudes have bins of their own: kLow .. kHigh - 1.  bf16: 2^-8 .. 2^9;
@@ -126,7 +131,9 @@ struct Weigh {
     const uint64_t x2 = (uint64_t(a) * a) >> 17;                       // x^2 / 2
     const uint64_t x3 = (uint64_t(uint32_t(x2 >> 16)) * a) >> 24;      // x^3 / 2
     const uint64_t x4 = (uint64_t(uint32_t(x3 >> 8)) * a) >> 32;       // x^4 / 2
-    const uint64_t s = x - x2 + x3 / 3 - x4 / 12;
+    // a third and a twelfth by 32-bit products, to 2^-47
+    const uint64_t s = x - x2 + (uint64_t(__umulhi(uint32_t(x3 >> 16), 0x55555556u)) << 16) -
+                       (uint64_t(__umulhi(uint32_t(x4 >> 8), 0x15555556u)) << 8);
     const uint64_t t = table[j], w = t - __umul64hi(t, s);
     const int down = 63 - shift + whole;
     return down < 64 ? (w + (1ull << (down - 1))) >> down : 0ull;
@@ -134,47 +141,72 @@ struct Weigh {
 };
 
 // ---------------------------------------------------------------- the row
-// All threads; f(z) of every logit that counts (not NaN, not -inf), in any order.
-template <typename T, typename F>
-__device__ __forceinline__ void each_logit(const T* row, int V, F&& f) {
-  constexpr int kPer = 16 / int(sizeof(T)), kUnroll = 4;
-  const int head = min(V, int((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / int(sizeof(T)));
-  const int vecs = (V - head) / kPer, tail = head + vecs * kPer;
-  const uint4* body = reinterpret_cast<const uint4*>(row + head);
-  auto one = [&](uint32_t bits, float z) {
-    if (z > -INFINITY) f(bits, z);
-  };
-  auto scalar = [&](int i) {
-    if constexpr (sizeof(T) == 2) {
-      const uint32_t b = reinterpret_cast<const uint16_t*>(row)[i];
-      one(b, to_float<T>(b));
-    } else {
-      const float z = reinterpret_cast<const float*>(row)[i];
-      one(__float_as_uint(z) >> 16, z);
-    }
-  };
-  if (int(threadIdx.x) < head) scalar(threadIdx.x);
-  if (tail + int(threadIdx.x) < V) scalar(tail + threadIdx.x);
-  for (int v0 = threadIdx.x; v0 < vecs; v0 += kThreads * kUnroll) {
-    uint4 x[kUnroll];
+// The part of a row that a CTA reads: vectors v0 .. v1 of the aligned middle, and the
+// elements before it (by the first CTA) and behind it (by the last).
+template <typename T>
+struct Slice {
+  static constexpr int kPer = 16 / int(sizeof(T));
+  const T* row;
+  const uint4* body;
+  int head, tail, V, v0, v1;
+  bool first, last;
+  __device__ __forceinline__ Slice(const T* r, int n, int rank, int ranks) : row(r), V(n) {
+    head = min(n, int((16 - (reinterpret_cast<uintptr_t>(r) & 15)) & 15) / int(sizeof(T)));
+    const int vecs = (n - head) / kPer, per = (vecs + ranks - 1) / ranks;
+    tail = head + vecs * kPer;
+    body = reinterpret_cast<const uint4*>(r + head);
+    v0 = min(rank * per, vecs);
+    v1 = min(v0 + per, vecs);
+    first = rank == 0;
+    last = rank == ranks - 1;
+  }
+  // All threads; one(i) of the single elements, vec(x, i) of the vectors, i the place of the (first) element.
+  template <int NT, typename F, typename G>
+  __device__ __forceinline__ void each(F&& one, G&& vec) const {
+    constexpr int kUnroll = 4;
+    const int t = threadIdx.x;
+    if (first && t < head) one(t);
+    if (last && tail + t < V) one(tail + t);
+    for (int v = v0 + t; v < v1; v += NT * kUnroll) {
+      uint4 x[kUnroll];
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u)
-      if (v0 + u * kThreads < vecs) x[u] = __ldg(body + v0 + u * kThreads);
+      for (int u = 0; u < kUnroll; ++u)
+        if (v + u * NT < v1) x[u] = __ldg(body + v + u * NT);
 #pragma unroll
-    for (int u = 0; u < kUnroll; ++u) {
-      if (v0 + u * kThreads >= vecs) break;
-      const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if constexpr (sizeof(T) == 2) {
-          one(w[k] & 0xFFFFu, to_float<T>(w[k] & 0xFFFFu));
-          one(w[k] >> 16, to_float<T>(w[k] >> 16));
-        } else {
-          one(w[k] >> 16, __uint_as_float(w[k]));
-        }
-      }
+      for (int u = 0; u < kUnroll; ++u)
+        if (v + u * NT < v1) vec(x[u], head + (v + u * NT) * kPer);
     }
   }
+};
+// The upper 16 bits and the value of element k of a vector, or of a single one.
+template <typename T>
+__device__ __forceinline__ uint32_t bits_of(const uint4& x, int k) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (sizeof(T) == 2) return k & 1 ? w[k >> 1] >> 16 : w[k >> 1] & 0xFFFFu;
+  else return w[k] >> 16;
+}
+template <typename T>
+__device__ __forceinline__ float value_of(const uint4& x, int k) {
+  const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+  if constexpr (sizeof(T) == 2) return to_float<T>(bits_of<T>(x, k));
+  else return __uint_as_float(w[k]);
+}
+template <typename T> __device__ __forceinline__ float value_at(const T* row, int i) { return float(row[i]); }
+template <typename T> __device__ __forceinline__ uint32_t bits_at(const T* row, int i) {
+  if constexpr (sizeof(T) == 2) return reinterpret_cast<const uint16_t*>(row)[i];
+  else return reinterpret_cast<const uint32_t*>(row)[i] >> 16;
+}
+// f(upper bits, value, place) of every logit of the slice that counts (not NaN, not -inf), in any order.
+template <int NT, typename T, typename F>
+__device__ __forceinline__ void each_logit(const Slice<T>& s, F&& f) {
+  auto one = [&](uint32_t bits, float z, int i) {
+    if (z > -INFINITY) f(bits, z, i);
+  };
+  s.template each<NT>([&](int i) { one(bits_at(s.row, i), value_at(s.row, i), i); },
+         [&](const uint4& x, int i) {
+#pragma unroll
+           for (int k = 0; k < Slice<T>::kPer; ++k) one(bits_of<T>(x, k), value_of<T>(x, k), i + k);
+         });
 }
 
 struct Place {                               // of a token in the order
@@ -184,17 +216,35 @@ struct Place {                               // of a token in the order
   uint64_t weight;                           // their weight
 };
 
+constexpr int kList = 2048;                  // tokens that are listed
+constexpr int kMaxRanks = 8;
+enum Verdict : uint32_t { kDone, kPlan, kRefine, kRead, kGeneral };
+
 struct Shared {
   uint64_t table[256];
-  uint64_t warp_weight[kWarps];
-  uint32_t warp_count[kWarps];
+  uint64_t warp_weight[32];
+  uint64_t tails[kMaxRanks], heads[kMaxRanks];   // by rank, with the first CTA: the sums of what is not listed
   uint64_t at_weight;                        // what a search found
-  uint32_t at_count, at_bin, at_key, at_r;
-  uint32_t part_count[kParts];
-  uint64_t part_weight[kParts];
+  uint32_t warp_count[32];
+  uint64_t tops[kMaxRanks];                  // by rank, with every CTA: the largest logit, and what at least top_k reach
+  uint32_t at_count, at_bin, end_count, at_end;
+  uint32_t mine, others;                     // tokens listed by this CTA, and handed over to it
+  uint32_t first;                            // greedy: the first place of the largest logit
+  uint32_t verdict;
+  float cut, cut_above;                      // tokens from cut up to below cut_above are listed
+  float from, scale;                         // a plan's first distance, and its steps a binary order
+  float least;                               // the smallest logit that min-p keeps
+  float want;                                // how far a plan has to reach
+};
+// With the list: two arrays of kList words (tokens; running sums, or what the others hand over, or the plan's counts).
+// In general(): the parts of a bin, then the bins.
+struct Parts {
+  uint64_t weight[kParts];
+  uint32_t count[kParts];
 };
 
 // Exclusive sums over the CTA's threads, and the totals.
+template <int NT>
 __device__ __forceinline__ void scan(Shared* sh, uint32_t& c, uint64_t& w, uint32_t& total_c, uint64_t& total_w) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   uint32_t ci = c;
@@ -219,7 +269,7 @@ __device__ __forceinline__ void scan(Shared* sh, uint32_t& c, uint64_t& w, uint3
   total_c = 0;
   total_w = 0;
 #pragma unroll
-  for (int i = 0; i < kWarps; ++i) {
+  for (int i = 0; i < NT / 32; ++i) {
     if (i == warp) {
       cb = total_c;
       wb = total_w;
@@ -231,282 +281,310 @@ __device__ __forceinline__ void scan(Shared* sh, uint32_t& c, uint64_t& w, uint3
   w = wb + wi - w;
 }
 
+// sum times f, rounded down or up: f's 24 bits times 64; nothing for f <= 0 and NaN, sum from 1 on.
+__device__ __forceinline__ uint64_t share_of(uint64_t sum, float f, bool up) {
+  if (!(f > 0.f)) return 0ull;
+  if (f >= 1.f) return sum;
+  const uint32_t bits = __float_as_uint(f), m = (bits & 0x7FFFFFu) | 0x800000u, down = 150 - (bits >> 23);
+  if ((bits >> 23) == 0 || down >= 128) return up ? 1ull : 0ull;
+  const uint64_t lo = sum * m, hi = __umul64hi(sum, m);
+  const uint64_t x = down < 64 ? (hi << (64 - down)) | (lo >> down) : hi >> (down - 64);
+  const uint64_t rest = down < 64 ? lo & ((1ull << down) - 1) : lo | (hi & ((1ull << (down - 64)) - 1));
+  return x + (up && rest ? 1ull : 0ull);
+}
+
+struct Settings {
+  float heat, top_p, min_p, u;
+  int top_k;
+  bool by_k, by_p, by_m;                     // limits that are set; by_k: below the vocabulary
+  bool tail;                                 // the weight of what is not listed counts
+  float least;                               // by_m: the smallest logit that it keeps
+};
+
+// A row's draw by the histogram of its values.  The order is by value, so counts and
+// weights of values answer every question of place.  A 16-bit logit is its own bin where
+// its magnitude is usual (the rest share three bins), and a bin's weight is its count
+// times the weight of its one value.  Bins of several values (all of them where logits
+// have 32 bits) have their weights summed element by element, and the one that a place
+// falls into is divided again, 2048 parts at a time, until its parts hold one value each.
+// Integer adds in shared memory bound it, one for each logit.
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams P) {
+__device__ __noinline__ void general(const SampleParams& P, const T* logits, long long at, const Weigh& weigh,
+                                     const Settings& S, Shared* sh, unsigned char* scratch) {
   using B = Bins<T>;
   constexpr int kPer = (B::kCount + kThreads - 1) / kThreads;       // bins of a thread
   static_assert(kPer <= 64, "a warp looks at a thread's bins in two steps");
-  extern __shared__ __align__(16) unsigned char smem[];
-  Shared* sh = reinterpret_cast<Shared*>(smem);
-  uint64_t* bin_weight = reinterpret_cast<uint64_t*>(sh + 1);       // of bins of several values: all, or three
+  Parts* parts = reinterpret_cast<Parts*>(scratch);
+  uint64_t* bin_weight = reinterpret_cast<uint64_t*>(parts + 1);    // of bins of several values: all, or three
   uint32_t* bin_count = reinterpret_cast<uint32_t*>(bin_weight + (B::kSingle ? 4 : B::kCount + 1));
   auto slot = [](int bin) { return B::kSingle ? (bin == 0 ? 0 : bin == B::kMiddle ? 1 : 2) : bin; };
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, V = P.V;
+  const Slice<T> row(logits, V, 0, 1);
 
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  const int b = blockIdx.x / P.R, V = P.V;
-  const T* row = static_cast<const T*>(P.logits) + (long long)blockIdx.x * P.stride;
-  const float heat = P.temperature ? P.temperature[b] : 1.f;
-  const int top_k = P.top_k ? P.top_k[b] : 0;
-  const float top_p = P.top_p ? P.top_p[b] : 1.f, min_p = P.min_p ? P.min_p[b] : 0.f;
-  const bool greedy = !(heat > 0.f) || top_k == 1 || top_p <= 0.f || min_p > 1.f;
-
-  // ---- counts of all bins, and the largest logit
-  if (!greedy) {
-    for (int i = tid; i < B::kCount; i += kThreads) bin_count[i] = 0;
-    for (int i = tid; i < (B::kSingle ? 4 : B::kCount); i += kThreads) bin_weight[i] = 0;
-    if (tid < 256) sh->table[tid] = __umul64hi(kSixteenths[tid >> 4], kParts256[tid & 15]) >> 1;
-    __syncthreads();
-  }
-  float top = -INFINITY;
-  if (greedy)
-    each_logit(row, V, [&](uint32_t, float z) { top = fmaxf(top, z); });
-  else
-    each_logit(row, V, [&](uint32_t bits, float z) {
-      top = fmaxf(top, z);
-      atomicAdd(&bin_count[B::of(bits)], 1u);
-    });
-  {
-    const uint32_t key = __reduce_max_sync(kFull, ord_f32(top));
-    if (lane == 0) sh->warp_count[warp] = key;
-    __syncthreads();
-    uint32_t best = sh->warp_count[lane % kWarps];
-    best = __reduce_max_sync(kFull, best);
-    top = unord_f32(best);
-    __syncthreads();
-  }
-  if (top == -INFINITY) {                    // nothing is left to draw from
-    if (tid == 0) {
-      P.tokens[blockIdx.x] = -1;
-      P.probs[blockIdx.x] = 0.f;
-    }
-    return;
-  }
-
-  Place drawn{ord_f32(top), 0u, 0u, 0ull};
-  float prob = 1.f;
-  if (!greedy) {
-    Weigh weigh;
-    weigh.top = top;
-    weigh.shift = P.shift;
-    weigh.table = sh->table;
-    // beyond 2^100 every logit but the largest weighs nothing anyway
-    const double c = fmin(1.4426950408889634 / double(heat), 1.2676506002282294e30);
-    weigh.c_hi = float(c);
-    weigh.c_lo = float(c - double(weigh.c_hi));
-
-    // ---- places by count
-    const int bin0 = min(tid * kPer, B::kCount), bin1 = min(bin0 + kPer, B::kCount);
-    uint32_t count0 = 0, total;
-    uint64_t weight0 = 0, all;
-    for (int i = bin0; i < bin1; ++i) count0 += bin_count[i];
-    const uint32_t mine = count0;
-    scan(sh, count0, weight0, total, all);
-    uint32_t enough = total;                 // n_m
-    if (min_p > 0.f) {
-      // w >= min_p where z >= max + T ln(min_p)
-      const float least = __double2float_ru(double(top) + double(heat) * log(double(min_p)));
-      const uint32_t key = ord_f32(least);
-      uint32_t n = 0;
-      bool cut = false;
-      for (int i = bin0; i < bin1; ++i) {
-        if (bin_count[i] == 0) continue;
-        if (B::low_key(i) >= key) n += bin_count[i];
-        else if (B::high_key(i) >= key) cut = true;
-      }
-      uint32_t zero = 0;
-      uint64_t none = 0;
-      scan(sh, n, none, enough, all);
-      if (__syncthreads_or(cut)) {
-        // the bin that the limit falls into, element by element
-        each_logit(row, V, [&](uint32_t bits, float z) {
-          if (z >= least && B::low_key(B::of(bits)) < key) ++zero;
-        });
-        uint32_t more;
-        none = 0;
-        scan(sh, zero, none, more, all);
-        enough += more;
-      }
-      enough = max(enough, 1u);
-    }
-    const uint32_t most = top_k > 0 ? min(uint32_t(top_k), total) : total;
-    const bool by_p = top_p < 1.f;
-    const uint32_t last = by_p ? most : min(most, enough);          // weights are wanted up to this place
-    if (count0 < last && last <= count0 + mine) {
-      uint32_t n = count0;
-      int i = bin0;
-      while (n + bin_count[i] < last) n += bin_count[i++];
-      sh->at_bin = uint32_t(i);
-    }
-    __syncthreads();
-    const int last_bin = int(sh->at_bin);
-
-    // ---- weights of the bins up to there
-    bool several = false;
-    for (int i = bin0; i < min(bin1, last_bin + 1); ++i) several |= !B::single(i) && bin_count[i] > 0;
-    if (__syncthreads_or(several))
-      each_logit(row, V, [&](uint32_t bits, float z) {
-        const int i = B::of(bits);
-        if (i <= last_bin && !B::single(i))
-          atomicAdd(reinterpret_cast<unsigned long long*>(&bin_weight[slot(i)]), (unsigned long long)weigh(z));
-      });
-    __syncthreads();
-    auto weight_of = [&](int i) -> uint64_t {
-      const uint32_t n = bin_count[i];
-      if (n == 0) return 0ull;
-      return B::single(i) ? n * weigh(B::value(i)) : bin_weight[slot(i)];
-    };
-    weight0 = 0;
-    for (int i = bin0; i < min(bin1, last_bin + 1); ++i) weight0 += weight_of(i);
-    uint64_t own = weight0;
-    {
-      uint32_t c = 0, cc;
-      scan(sh, c, weight0, cc, all);
-    }
-
-    // The place of the token before which there are x tokens (by_count), or the first
-    // whose running sum exceeds x.  All threads.
-    auto find = [&](bool by_count, uint64_t x) -> Place {
-      const bool here = by_count ? count0 <= x && x < uint64_t(count0) + mine : weight0 <= x && x < weight0 + own;
-      __syncthreads();
-      if (here) {
-        sh->at_bin = uint32_t(bin0);
-        sh->at_count = count0;
-        sh->at_weight = weight0;
-      }
-      __syncthreads();
-      Place at;
-      int bin = int(sh->at_bin);
-      at.count = sh->at_count;
-      at.weight = sh->at_weight;
-      // every warp looks at that thread's bins
-      const int end = min(bin + kPer, B::kCount);
-      for (int i0 = bin; i0 < end; i0 += 32) {
-        const int i = i0 + lane;
-        uint32_t c = i < end ? bin_count[i] : 0u;
-        uint64_t w = i < end && i <= last_bin ? weight_of(i) : 0ull;
-        const uint32_t c1 = c;
-        const uint64_t w1 = w;
+  // ---- counts of all bins
+  __syncthreads();
+  for (int i = tid; i < B::kCount; i += kThreads) bin_count[i] = 0;
+  for (int i = tid; i < (B::kSingle ? 4 : B::kCount); i += kThreads) bin_weight[i] = 0;
+  __syncthreads();
+  // 16-bit logits of the three shared bins are set aside, where there are few of them
+  uint16_t* aside = reinterpret_cast<uint16_t*>(parts->weight);
+  constexpr uint32_t kAside = sizeof(parts->weight) / 2;
+  if (tid == 0) sh->mine = 0;
+  __syncthreads();
+  auto count = [&](uint32_t bits, float z) {
+    if (z > -INFINITY) atomicAdd(&bin_count[B::of(bits)], 1u);
+  };
+  auto shared_bin = [&](uint32_t bits, float z) { return B::kSingle && z > -INFINITY && !B::single(B::of(bits)); };
+  row.template each<kThreads>(
+      [&](int i) {
+        const uint32_t bits = bits_at(logits, i);
+        count(bits, value_at(logits, i));
+        if (shared_bin(bits, value_at(logits, i))) {
+          const uint32_t k = atomicAdd(&sh->mine, 1u);
+          if (k < kAside) aside[k] = uint16_t(bits);
+        }
+      },
+      [&](const uint4& x, int) {
+        uint32_t few = 0;
 #pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-          const uint32_t cx = __shfl_up_sync(kFull, c, o);
-          const uint64_t wx = __shfl_up_sync(kFull, w, o);
-          if (lane >= o) {
-            c += cx;
-            w += wx;
-          }
+        for (int k = 0; k < Slice<T>::kPer; ++k) {
+          count(bits_of<T>(x, k), value_of<T>(x, k));
+          few |= (shared_bin(bits_of<T>(x, k), value_of<T>(x, k)) ? 1u : 0u) << k;
         }
-        const uint32_t hit = __ballot_sync(kFull, by_count ? x < uint64_t(at.count) + c : x < at.weight + w);
-        const int l = hit ? __ffs(hit) - 1 : 31;
-        bin = i0 + l;
-        const uint32_t add_c = __shfl_sync(kFull, hit ? c - c1 : c, l);
-        const uint64_t add_w = __shfl_sync(kFull, hit ? w - w1 : w, l);
-        at.count += add_c;
-        at.weight += add_w;
-        if (hit) break;
-      }
-      at.key = B::high_key(bin);
-      if (!B::single(bin)) {
-        // divided again until a part is one value
-        uint32_t lo = B::low_key(bin), hi = at.key;
-        for (;;) {
-          const uint32_t span = hi - lo;
-          const int bits = span ? 32 - __clz(span) : 0, down = bits > 11 ? bits - 11 : 0;
-          __syncthreads();
-          for (int i = tid; i < kParts; i += kThreads) {
-            sh->part_count[i] = 0;
-            sh->part_weight[i] = 0;
-          }
-          __syncthreads();
-          each_logit(row, V, [&](uint32_t, float z) {
-            const uint32_t key = ord_f32(z);
-            if (key >= lo && key <= hi) {
-              const uint32_t i = (hi - key) >> down;
-              atomicAdd(&sh->part_count[i], 1u);
-              atomicAdd(reinterpret_cast<unsigned long long*>(&sh->part_weight[i]), (unsigned long long)weigh(z));
+        if (few) {
+          uint32_t k = atomicAdd(&sh->mine, uint32_t(__popc(few)));
+#pragma unroll
+          for (int e = 0; e < Slice<T>::kPer; ++e)
+            if ((few >> e) & 1u) {
+              if (k < kAside) aside[k] = uint16_t(bits_of<T>(x, e));
+              ++k;
             }
-          });
-          __syncthreads();
-          constexpr int kEach = kParts / kThreads;
-          uint32_t c = 0, cc;
-          uint64_t w = 0, ww;
-          for (int k = 0; k < kEach; ++k) {
-            c += sh->part_count[tid * kEach + k];
-            w += sh->part_weight[tid * kEach + k];
-          }
-          scan(sh, c, w, cc, ww);
-          c += at.count;
-          w += at.weight;
-          for (int k = 0; k < kEach; ++k) {
-            const uint32_t n = sh->part_count[tid * kEach + k];
-            const uint64_t m = sh->part_weight[tid * kEach + k];
-            if (by_count ? c <= x && x < uint64_t(c) + n : w <= x && x < w + m) {
-              sh->at_bin = uint32_t(tid * kEach + k);
-              sh->at_count = c;
-              sh->at_weight = w;
-            }
-            c += n;
-            w += m;
-          }
-          __syncthreads();
-          hi -= sh->at_bin << down;
-          lo = max(lo, hi - ((1u << down) - 1u));
-          at.count = sh->at_count;
-          at.weight = sh->at_weight;
-          if (down == 0) break;
         }
-        at.key = hi;
-      }
-      at.r = by_count ? uint32_t(x - at.count) : uint32_t((x - at.weight) / weigh(unord_f32(at.key)));
-      return at;
-    };
-    // the weight up to and with the token at a place
-    auto upto = [&](const Place& at) { return at.weight + (uint64_t(at.r) + 1) * weigh(unord_f32(at.key)); };
+      });
+  __syncthreads();
 
-    uint64_t sum = all;                      // of the first `most`
-    if (most < total && (by_p || most <= enough)) sum = upto(find(true, most - 1));
-    uint32_t n = most;
-    if (by_p) {
-      // the first place where the running sum is at least p times the sum
-      uint64_t reach = uint64_t(ceil(double(top_p) * double(sum)));
-      reach = reach < 1 ? 1 : reach > sum ? sum : reach;
-      const Place at = find(false, reach - 1);
-      n = at.count + at.r + 1;
-      sum = upto(at);
+  // ---- places by count
+  const int bin0 = min(tid * kPer, B::kCount), bin1 = min(bin0 + kPer, B::kCount);
+  uint32_t count0 = 0, total;
+  uint64_t weight0 = 0, all;
+  for (int i = bin0; i < bin1; ++i) count0 += bin_count[i];
+  const uint32_t mine = count0;
+  scan<kThreads>(sh, count0, weight0, total, all);
+  uint32_t enough = total;                 // n_m
+  if (S.by_m) {
+    const float least = S.least;
+    const uint32_t key = ord_f32(least);
+    uint32_t n = 0;
+    bool cut = false;
+    for (int i = bin0; i < bin1; ++i) {
+      if (bin_count[i] == 0) continue;
+      if (B::low_key(i) >= key) n += bin_count[i];
+      else if (B::high_key(i) >= key) cut = true;
     }
-    if (enough < n) {
-      n = enough;
-      sum = upto(find(true, n - 1));
+    uint32_t zero = 0;
+    uint64_t none = 0;
+    scan<kThreads>(sh, n, none, enough, all);
+    if (__syncthreads_or(cut)) {
+      // the bin that the limit falls into, element by element
+      each_logit<kThreads>(row, [&](uint32_t bits, float z, int) {
+        if (z >= least && B::low_key(B::of(bits)) < key) ++zero;
+      });
+      uint32_t more;
+      none = 0;
+      scan<kThreads>(sh, zero, none, more, all);
+      enough += more;
     }
-    const float u = P.uniforms[blockIdx.x];
-    uint64_t x = u > 0.f ? uint64_t(double(u) * double(sum)) : 0ull;
-    if (x >= sum) x = sum - 1;
-    drawn = find(false, x);
-    prob = float(double(weigh(unord_f32(drawn.key))) / double(sum));
+    enough = max(enough, 1u);
   }
+  const uint32_t most = S.top_k > 0 ? min(uint32_t(S.top_k), total) : total;
+  const bool by_p = S.by_p;
+  const uint32_t last = by_p ? most : min(most, enough);          // weights are wanted up to this place
+  if (count0 < last && last <= count0 + mine) {
+    uint32_t n = count0;
+    int i = bin0;
+    while (n + bin_count[i] < last) n += bin_count[i++];
+    sh->at_bin = uint32_t(i);
+  }
+  __syncthreads();
+  const int last_bin = int(sh->at_bin);
+
+  // ---- weights of the bins up to there
+  bool several = false;
+  for (int i = bin0; i < min(bin1, last_bin + 1); ++i) several |= !B::single(i) && bin_count[i] > 0;
+  if (__syncthreads_or(several)) {
+    if constexpr (B::kSingle) {
+      // three sums: in registers, then one after the other over the CTA
+      uint64_t w[3] = {0ull, 0ull, 0ull};
+      auto add = [&](uint32_t bits, float z, int) {
+        const int i = B::of(bits);
+        if (i <= last_bin && !B::single(i)) {
+          const uint64_t x = weigh(z);
+          if (i == 0) w[0] += x;
+          else if (i == B::kMiddle) w[1] += x;
+          else w[2] += x;
+        }
+      };
+      if (sh->mine <= kAside)
+        for (int k = tid; k < int(sh->mine); k += kThreads) add(aside[k], to_float<T>(aside[k]), 0);
+      else
+        each_logit<kThreads>(row, add);
+      for (int k = 0; k < 3; ++k) {
+        uint32_t c = 0, cc;
+        uint64_t sum;
+        scan<kThreads>(sh, c, w[k], cc, sum);
+        if (tid == 0) bin_weight[k] = sum;
+      }
+    } else {
+      each_logit<kThreads>(row, [&](uint32_t bits, float z, int) {
+        const int i = B::of(bits);
+        if (i <= last_bin) atomicAdd(reinterpret_cast<unsigned long long*>(&bin_weight[i]), (unsigned long long)weigh(z));
+      });
+    }
+  }
+  __syncthreads();
+  auto weight_of = [&](int i) -> uint64_t {
+    const uint32_t n = bin_count[i];
+    if (n == 0) return 0ull;
+    return B::single(i) ? n * weigh(B::value(i)) : bin_weight[slot(i)];
+  };
+  weight0 = 0;
+  for (int i = bin0; i < min(bin1, last_bin + 1); ++i) weight0 += weight_of(i);
+  uint64_t own = weight0;
+  {
+    uint32_t c = 0, cc;
+    scan<kThreads>(sh, c, weight0, cc, all);
+  }
+
+  // The place of the token before which there are x tokens (by_count), or the first
+  // whose running sum exceeds x.  All threads.
+  auto find = [&](bool by_count, uint64_t x) -> Place {
+    const bool here = by_count ? count0 <= x && x < uint64_t(count0) + mine : weight0 <= x && x < weight0 + own;
+    __syncthreads();
+    if (here) {
+      sh->at_bin = uint32_t(bin0);
+      sh->at_count = count0;
+      sh->at_weight = weight0;
+    }
+    __syncthreads();
+    Place at;
+    int bin = int(sh->at_bin);
+    at.count = sh->at_count;
+    at.weight = sh->at_weight;
+    // every warp looks at that thread's bins
+    const int end = min(bin + kPer, B::kCount);
+    for (int i0 = bin; i0 < end; i0 += 32) {
+      const int i = i0 + lane;
+      uint32_t c = i < end ? bin_count[i] : 0u;
+      uint64_t w = i < end && i <= last_bin ? weight_of(i) : 0ull;
+      const uint32_t c1 = c;
+      const uint64_t w1 = w;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const uint32_t cx = __shfl_up_sync(kFull, c, o);
+        const uint64_t wx = __shfl_up_sync(kFull, w, o);
+        if (lane >= o) {
+          c += cx;
+          w += wx;
+        }
+      }
+      const uint32_t hit = __ballot_sync(kFull, by_count ? x < uint64_t(at.count) + c : x < at.weight + w);
+      const int l = hit ? __ffs(hit) - 1 : 31;
+      bin = i0 + l;
+      const uint32_t add_c = __shfl_sync(kFull, hit ? c - c1 : c, l);
+      const uint64_t add_w = __shfl_sync(kFull, hit ? w - w1 : w, l);
+      at.count += add_c;
+      at.weight += add_w;
+      if (hit) break;
+    }
+    at.key = B::high_key(bin);
+    if (!B::single(bin)) {
+      // divided again until a part is one value
+      uint32_t lo = B::low_key(bin), hi = at.key;
+      for (;;) {
+        const uint32_t span = hi - lo;
+        const int bits = span ? 32 - __clz(span) : 0, down = bits > 11 ? bits - 11 : 0;
+        __syncthreads();
+        for (int i = tid; i < kParts; i += kThreads) {
+          parts->count[i] = 0;
+          parts->weight[i] = 0;
+        }
+        __syncthreads();
+        each_logit<kThreads>(row, [&](uint32_t, float z, int) {
+          const uint32_t key = ord_f32(z);
+          if (key >= lo && key <= hi) {
+            const uint32_t i = (hi - key) >> down;
+            atomicAdd(&parts->count[i], 1u);
+            atomicAdd(reinterpret_cast<unsigned long long*>(&parts->weight[i]), (unsigned long long)weigh(z));
+          }
+        });
+        __syncthreads();
+        constexpr int kEach = kParts / kThreads;
+        uint32_t c = 0, cc;
+        uint64_t w = 0, ww;
+        for (int k = 0; k < kEach; ++k) {
+          c += parts->count[tid * kEach + k];
+          w += parts->weight[tid * kEach + k];
+        }
+        scan<kThreads>(sh, c, w, cc, ww);
+        c += at.count;
+        w += at.weight;
+        for (int k = 0; k < kEach; ++k) {
+          const uint32_t n = parts->count[tid * kEach + k];
+          const uint64_t m = parts->weight[tid * kEach + k];
+          if (by_count ? c <= x && x < uint64_t(c) + n : w <= x && x < w + m) {
+            sh->at_bin = uint32_t(tid * kEach + k);
+            sh->at_count = c;
+            sh->at_weight = w;
+          }
+          c += n;
+          w += m;
+        }
+        __syncthreads();
+        hi -= sh->at_bin << down;
+        lo = max(lo, hi - ((1u << down) - 1u));
+        at.count = sh->at_count;
+        at.weight = sh->at_weight;
+        if (down == 0) break;
+      }
+      at.key = hi;
+    }
+    at.r = by_count ? uint32_t(x - at.count) : uint32_t((x - at.weight) / weigh(unord_f32(at.key)));
+    return at;
+  };
+  // the weight up to and with the token at a place
+  auto upto = [&](const Place& at) { return at.weight + (uint64_t(at.r) + 1) * weigh(unord_f32(at.key)); };
+
+  uint64_t sum = all;                      // of the first `most`
+  if (most < total && (by_p || most <= enough)) sum = upto(find(true, most - 1));
+  uint32_t n = most;
+  if (by_p) {
+    // the first place where the running sum is at least p times the sum
+    const uint64_t reach = share_of(sum, S.top_p, true);             // at least 1: p > 0
+    const Place end = find(false, reach - 1);
+    n = end.count + end.r + 1;
+    sum = upto(end);
+  }
+  if (enough < n) {
+    n = enough;
+    sum = upto(find(true, n - 1));
+  }
+  const uint64_t x = min(share_of(sum, S.u, false), sum - 1);
+  const Place drawn = find(false, x);
 
   // ---- the drawn.r-th token (from 0) of that logit in the order of ids
   const float z = unord_f32(drawn.key);
-  constexpr int kVec = 16 / int(sizeof(T));
-  const int head = min(V, int((16 - (reinterpret_cast<uintptr_t>(row) & 15)) & 15) / int(sizeof(T)));
-  const int vecs = (V - head) / kVec, tail = head + vecs * kVec;
-  const uint4* body = reinterpret_cast<const uint4*>(row + head);
+  constexpr int kVec = Slice<T>::kPer;
+  const int head = row.head, tail = row.tail, vecs = row.v1;
+  const uint4* body = row.body;
   auto matches = [&](const uint4& x) -> uint32_t {           // a bit for each element of a vector
-    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
     uint32_t m = 0;
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      if constexpr (sizeof(T) == 2) {
-        m |= (to_float<T>(w[k] & 0xFFFFu) == z ? 1u : 0u) << (2 * k);
-        m |= (to_float<T>(w[k] >> 16) == z ? 1u : 0u) << (2 * k + 1);
-      } else {
-        m |= (__uint_as_float(w[k]) == z ? 1u : 0u) << k;
-      }
-    }
+    for (int k = 0; k < kVec; ++k) m |= (value_of<T>(x, k) == z ? 1u : 0u) << k;
     return m;
   };
   // warp w has the vectors from w share to (w + 1) share; the head is before them, the tail behind
-  const int share = (vecs + kWarps - 1) / kWarps, v0 = min(warp * share, vecs), v1 = min(v0 + share, vecs);
-  uint32_t n = 0;
+  const int share = (vecs + (kThreads / 32) - 1) / (kThreads / 32), v0 = min(warp * share, vecs), v1 = min(v0 + share, vecs);
+  uint32_t hits = 0;
   for (int v = v0 + lane; v < v1; v += 32 * 4) {
     uint4 x[4];
 #pragma unroll
@@ -514,18 +592,18 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
       if (v + 32 * k < v1) x[k] = __ldg(body + v + 32 * k);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
-      if (v + 32 * k < v1) n += __popc(matches(x[k]));
+      if (v + 32 * k < v1) hits += __popc(matches(x[k]));
   }
-  n = __reduce_add_sync(kFull, n);
+  hits = __reduce_add_sync(kFull, hits);
   __syncthreads();
-  if (lane == 0) sh->warp_count[warp] = n;
+  if (lane == 0) sh->warp_count[warp] = hits;
   __syncthreads();
   if (warp != 0) return;
   uint32_t left = drawn.r;
   int token = -1;
   auto singly = [&](int i0, int i1) {
     for (int i = i0; i < i1 && token < 0; ++i)
-      if (float(row[i]) == z) {
+      if (float(logits[i]) == z) {
         if (left == 0) token = i;
         else --left;
       }
@@ -533,8 +611,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
   singly(0, head);
   if (token < 0) {
     int w = 0;
-    while (w < kWarps && left >= sh->warp_count[w]) left -= sh->warp_count[w++];
-    if (w < kWarps) {
+    while (w < (kThreads / 32) && left >= sh->warp_count[w]) left -= sh->warp_count[w++];
+    if (w < (kThreads / 32)) {
       const int first = min(w * share, vecs), end = min(first + share, vecs);
       for (int v = first; v < end; v += 32) {
         const uint32_t m = v + lane < end ? matches(__ldg(body + v + lane)) : 0u;
@@ -563,18 +641,740 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleParams 
     }
   }
   if (lane == 0) {
-    P.tokens[blockIdx.x] = token;
-    P.probs[blockIdx.x] = prob;
+    P.tokens[at] = token;
+    P.probs[at] = float(double(weigh(unord_f32(drawn.key))) / double(sum));
+  }
+}
+
+// ------------------------------------------------------------------ clusters
+__device__ __forceinline__ uint32_t cluster_rank() {
+  uint32_t r;
+  asm volatile("mov.u32 %0, %%cluster_ctarank;" : "=r"(r));
+  return r;
+}
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
+// The address of a variable of this CTA in another one of the cluster.
+__device__ __forceinline__ uint32_t there(const void* p, uint32_t rank) {
+  uint32_t a;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+  return a;
+}
+__device__ __forceinline__ void put32(uint32_t at, uint32_t x) {
+  asm volatile("st.shared::cluster.u32 [%0], %1;" :: "r"(at), "r"(x) : "memory");
+}
+__device__ __forceinline__ void put64(uint32_t at, uint64_t x) {
+  asm volatile("st.shared::cluster.u64 [%0], %1;" :: "r"(at), "l"(x) : "memory");
+}
+__device__ __forceinline__ uint32_t get32(uint32_t at) {
+  uint32_t x;
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+__device__ __forceinline__ uint32_t add32(uint32_t at, uint32_t x) {
+  uint32_t old;
+  asm volatile("atom.relaxed.cluster.shared::cluster.add.u32 %0, [%1], %2;" : "=r"(old) : "r"(at), "r"(x) : "memory");
+  return old;
+}
+
+// ------------------------------------------------------------------- the list
+// Descending, by all threads; n <= kList, entries behind it are cleared up to a power of two.
+template <int NT>
+__device__ __forceinline__ void sort_list(uint64_t* list, int n) {
+  const int tid = threadIdx.x;
+  int N = 32;
+  while (N < n) N <<= 1;
+  for (int i = n + tid; i < N; i += NT) list[i] = 0;
+  __syncthreads();
+  if (N <= NT) {                       // an entry a thread; within a warp by shuffles
+    uint64_t x = tid < N ? list[tid] : 0ull;
+    for (int size = 2; size <= N; size <<= 1) {
+      for (int stride = size >> 1; stride > 0; stride >>= 1) {
+        uint64_t y;
+        if (stride < 32) {
+          if (tid >= N) continue;
+          y = __shfl_xor_sync(kFull, x, stride);
+        } else {
+          __syncthreads();
+          if (tid < N) list[tid] = x;
+          __syncthreads();
+          if (tid >= N) continue;
+          y = list[tid ^ stride];
+        }
+        const bool keep_max = ((tid & stride) == 0) == ((tid & size) == 0);
+        if ((x < y) == keep_max) x = y;
+      }
+    }
+    __syncthreads();
+    if (tid < N) list[tid] = x;
+  } else {
+    for (int size = 2; size <= N; size <<= 1) {
+      for (int stride = size >> 1; stride > 0; stride >>= 1) {
+        for (int i = tid; i < N / 2; i += NT) {
+          const int a = 2 * i - (i & (stride - 1)), b = a + stride;
+          const uint64_t x = list[a], y = list[b];
+          if ((x < y) == ((a & size) == 0)) {
+            list[a] = y;
+            list[b] = x;
+          }
+        }
+        __syncthreads();
+      }
+    }
+  }
+  __syncthreads();
+}
+
+// Sum over the CTA's threads, to all of them.
+template <int NT>
+__device__ __forceinline__ uint32_t block_sum(Shared* sh, uint32_t x) {
+  x = __reduce_add_sync(kFull, x);
+  __syncthreads();
+  if ((threadIdx.x & 31) == 0) sh->warp_count[threadIdx.x >> 5] = x;
+  __syncthreads();
+  return __reduce_add_sync(kFull, (threadIdx.x & 31) < NT / 32 ? sh->warp_count[threadIdx.x & 31] : 0u);
+}
+
+// What the list of n tokens decides: the row's draw (kDone), how far the list has to reach
+// (kPlan, with sh->want), or nothing (kGeneral).
+// above, below: the weights of the tokens before the list and behind it, together off by at
+// most `slack`; complete: there are none.  known: the sum of what is kept, once it is known
+// (then x is drawn from it); it receives that sum.
+template <int NT>
+__device__ __forceinline__ Verdict decide(const Settings& S, const Weigh& weigh, Shared* sh, const uint64_t* list,
+                                          uint64_t* cum, int n, uint64_t above, uint64_t below, uint64_t slack,
+                                          bool complete, uint64_t& known, int32_t* token, float* prob) {
+  constexpr int kEach = kList / NT;
+  const int tid = threadIdx.x, each = (n + NT - 1) / NT, i0 = tid * each;
+  uint64_t run[kEach], w = 0, head;
+  uint32_t c = 0, cc, kept = 0;
+  for (int e = 0; e < kEach; ++e) {
+    run[e] = 0;
+    if (e < each && i0 + e < n) {
+      const float z = unord_f32(uint32_t(list[i0 + e] >> 32));
+      w += weigh(z);
+      kept += z >= S.least;
+    }
+    run[e] = w;
+  }
+  scan<NT>(sh, c, w, cc, head);
+  head += above;
+  for (int e = 0; e < kEach; ++e) {
+    run[e] += w + above;
+    if (e < each && i0 + e < n) cum[i0 + e] = run[e];
+  }
+  // tokens of the list whose running sum is at most x
+  auto upto = [&](uint64_t x) {
+    if (each <= 1) return int(__syncthreads_count(tid < n && run[0] <= x));
+    uint32_t k = 0;
+    for (int e = 0; e < kEach; ++e) k += e < each && i0 + e < n && run[e] <= x;
+    return int(block_sum<NT>(sh, k));
+  };
+  // Whether the first running sum above x lies in the list whatever the sums that are off;
+  // if not, how far it is.
+  const float units = __uint_as_float(uint32_t(127 - weigh.shift) << 23);
+  auto place = [&](uint64_t x, int& i) {
+    i = upto(x);
+    bool sure = i < n && (above == 0 || x >= above);
+    if (slack > 0)
+      sure = sure && x + slack < head && (above == 0 || x >= above + slack) && upto(x > slack ? x - slack : 0ull) == i &&
+             upto(x + slack) == i;
+    if (!sure && tid == 0) sh->want = float(x) * units;
+    return sure;
+  };
+  int keep = n, i;
+  uint64_t sum = known ? known : head + below;
+  if (known == 0) {
+    if (S.by_k) {
+      if (n < S.top_k && !complete && !(S.by_m && !S.by_p)) {
+        if (tid == 0) sh->want = float(S.top_k);
+        return kPlan;
+      }
+      keep = min(n, S.top_k);
+      __syncthreads();
+      sum = cum[keep - 1];
+    }
+    if (S.by_p) {
+      if (!place(share_of(sum, S.top_p, true) - 1, i)) return kPlan;   // at least 1: p > 0
+      keep = min(keep, i + 1);
+    }
+    if (S.by_m) keep = max(1, min(keep, each <= 1 ? int(__syncthreads_count(kept)) : int(block_sum<NT>(sh, kept))));
+    if (S.by_p || S.by_m) {
+      __syncthreads();
+      sum = cum[keep - 1];
+      if (above == 0) slack = 0;
+    }
+  }
+  if (!place(min(share_of(sum, S.u, false), sum - 1), i)) {
+    if (S.by_p && known == 0) known = sum;
+    return kPlan;
+  }
+  if (tid == 0) {
+    i = min(i, keep - 1);
+    *token = int32_t(~uint32_t(list[i]));
+    *prob = float(double(cum[i] - (i > 0 ? cum[i - 1] : above)) / double(sum));
+  }
+  return kDone;
+}
+
+// Largest of a vector's elements, NaN left out (two of them where they have 16 bits).
+template <typename T> __device__ __forceinline__ uint32_t max2(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t max2<__nv_bfloat16>(uint32_t a, uint32_t b) {
+  __nv_bfloat162 x, y;
+  memcpy(&x, &a, 4);
+  memcpy(&y, &b, 4);
+  x = __hmax2(x, y);
+  memcpy(&a, &x, 4);
+  return a;
+}
+template <> __device__ __forceinline__ uint32_t max2<__half>(uint32_t a, uint32_t b) {
+  __half2 x, y;
+  memcpy(&x, &a, 4);
+  memcpy(&y, &b, 4);
+  x = __hmax2(x, y);
+  memcpy(&a, &x, 4);
+  return a;
+}
+template <typename T> constexpr uint32_t kLowest2 = 0xFF7FFF7Fu;        // the lowest finite value, twice
+template <> constexpr uint32_t kLowest2<__half> = 0xFBFFFBFFu;
+template <typename T>
+__device__ __forceinline__ float max_of(const uint4& x) {
+  if constexpr (sizeof(T) == 2) {
+    const uint32_t m = max2<T>(max2<T>(x.x, x.y), max2<T>(x.z, x.w));
+    return fmaxf(to_float<T>(m & 0xFFFFu), to_float<T>(m >> 16));
+  } else {
+    return fmaxf(fmaxf(__uint_as_float(x.x), __uint_as_float(x.y)), fmaxf(__uint_as_float(x.z), __uint_as_float(x.w)));
+  }
+}
+
+// Weights of tokens that are not listed, 2^-12 at most, in fp32.  The exponent y < 64 (what
+// lies beyond adds less than a part) is off by (2^-25 + 2^-25) y, the factor c and the
+// product, so the weight by 2^-24 64 ln 2 < 2^-18 of itself; ex2 and the sum of a vector's
+// eight add 2^-21; a vector's sum is rounded to a whole part.
+template <typename T>
+struct Tail {
+  float top, c, one;                         // one: 2^shift
+  __device__ __forceinline__ uint64_t operator()(const uint4& x) const {
+    const uint64_t low2 = pair(-top, -top), c2 = pair(c, c);
+    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+    uint64_t sum = 0;
+    if constexpr (sizeof(T) == 2) {
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        const uint32_t v = max2<T>(w[k], kLowest2<T>);                 // -inf and NaN weigh nothing
+        const uint64_t y = mul2(add2(pair(to_float<T>(v & 0xFFFFu), to_float<T>(v >> 16)), low2), c2);
+        sum = add2(sum, pair(ex2_approx(low(y)), ex2_approx(high(y))));
+      }
+    } else {
+#pragma unroll
+      for (int k = 0; k < 4; k += 2) {
+        const float a = fmaxf(__uint_as_float(w[k]), -3.4028235e38f), b = fmaxf(__uint_as_float(w[k + 1]), -3.4028235e38f);
+        const uint64_t y = mul2(add2(pair(a, b), low2), c2);
+        sum = add2(sum, pair(ex2_approx(low(y)), ex2_approx(high(y))));
+      }
+    }
+    return __float2ull_rn((low(sum) + high(sum)) * one);
+  }
+  __device__ __forceinline__ uint64_t operator()(float z) const { return __float2ull_rn(ex2_approx((z - top) * c) * one); }
+};
+
+// A weight to 2^-29 of itself, for sums of tokens whose order does not matter.  2^-y with y in
+// two parts, y = whole + j / 256 + r, |r| <= 2^-9: 2^-r - 1 in fp32 (2^-33 of 1), 2^-j/256 and
+// their product in parts of 2^-31.
+struct Mid {
+  float top, c_hi, c_lo;
+  int shift;
+  const uint64_t* table;
+  __device__ __forceinline__ uint64_t operator()(float z) const {
+    const float d = top - z, v = d - top, e = (top - (d - v)) - (z + v), y = d * c_hi;
+    if (!(y < 62.f)) return 0ull;
+    constexpr float kRound = 12582912.f;     // 1.5 2^23: a sum with it is a whole number
+    const float n = fmaf(y, 256.f, kRound);
+    const int steps = __float_as_int(n) - __float_as_int(kRound);
+    const float r = fmaf(n - kRound, -0.00390625f, y) + (fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi));
+    const float s = r * fmaf(r, fmaf(r, -0.05550410866f, 0.2402265070f), -0.6931471806f);     // 2^-r - 1
+    const int q = __float_as_int(fmaf(s, 2147483648.f, kRound)) - __float_as_int(kRound);
+    const int a = int(uint32_t(table[steps & 255] >> 32));
+    const uint32_t w = uint32_t(a) + uint32_t(int((long long)a * q >> 31));
+    return (uint64_t(w) << (shift - 31)) >> (steps >> 8);
+  }
+};
+
+constexpr int kSteps = 64;                   // of a plan, in a binary order of weight
+constexpr float kNear = 12.f;                // binary orders that are listed at first
+constexpr int32_t kUndecided = -2;           // a row's token until general() has drawn it
+
+// The settings of a row's sequence, and the weights' factor: log2(e) / heat in two parts,
+// each step's remainder carried on.
+struct Asked {
+  Settings S;
+  bool greedy;
+  float c_hi, c_lo;
+};
+__device__ __forceinline__ Asked settings_of(const SampleParams& P, long long at, int V) {
+  const int b = int(at / P.R);
+  Asked a;
+  Settings& S = a.S;
+  S.heat = P.temperature ? P.temperature[b] : 1.f;
+  S.top_k = P.top_k ? P.top_k[b] : 0;
+  S.top_p = P.top_p ? P.top_p[b] : 1.f;
+  S.min_p = P.min_p ? P.min_p[b] : 0.f;
+  S.u = P.uniforms[at];
+  S.by_k = S.top_k > 0 && S.top_k < V;
+  S.by_p = S.top_p < 1.f;
+  S.by_m = S.min_p > 0.f;
+  S.tail = !S.by_k && (S.by_p || !S.by_m);
+  S.least = -INFINITY;
+  a.greedy = !(S.heat > 0.f) || S.top_k == 1 || S.top_p <= 0.f || S.min_p > 1.f;
+  constexpr float kHi = 1.44269502162933349609375f, kLo = 1.92596299112661746887e-8f;   // log2(e)
+  a.c_hi = kHi / S.heat;
+  a.c_lo = (fmaf(-a.c_hi, S.heat, kHi) + kLo) / S.heat;
+  if (!(a.c_hi < 1e30f)) {                   // every logit but the largest weighs nothing anyway
+    a.c_hi = 1e30f;
+    a.c_lo = 0.f;
+  }
+  if (!(S.heat < INFINITY)) a.c_hi = a.c_lo = 0.f;
+  return a;
+}
+__device__ __forceinline__ void fill_table(Shared* sh) {
+  if (threadIdx.x < 256)
+    sh->table[threadIdx.x] = __umul64hi(kSixteenths[threadIdx.x >> 4], kParts256[threadIdx.x & 15]) >> 1;
+}
+// w >= min_p where z >= max + T ln(min_p); by one thread, in 64 bits.
+__device__ __forceinline__ float least_of(const Settings& S, float top) {
+  const float x = __double2float_ru(double(top) + double(S.heat) * log(double(S.min_p)));
+  return x <= top ? x : -INFINITY;           // an infinite temperature times nothing
+}
+
+// NT threads; kAll: a row that the list does not decide goes by general() here, else its token
+// becomes kUndecided and rest_kernel draws it.
+template <typename T, int NT, int kCtas, bool kAll>
+__global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared* sh = reinterpret_cast<Shared*>(smem);
+  uint64_t* list = reinterpret_cast<uint64_t*>(sh + 1);
+  uint64_t* cum = list + kList;
+  uint32_t* plan = reinterpret_cast<uint32_t*>(cum);                   // kList counts
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const uint32_t ranks = kAll ? uint32_t(P.ranks) : 1u, rank = kAll && ranks > 1 ? cluster_rank() : 0u;
+  const long long at = blockIdx.x / ranks;                             // the row
+  const int V = P.V;
+  const T* logits = static_cast<const T*>(P.logits) + at * P.stride;
+  const Slice<T> row(logits, V, int(rank), int(ranks));
+  auto sync = [&]() {
+    if (kAll && ranks > 1) {
+      cluster_arrive();
+      cluster_wait();
+    } else {
+      __syncthreads();
+    }
+  };
+  if (tid == 0) {
+    sh->mine = 0;
+    sh->others = 0;
+    sh->first = 0xFFFFFFFFu;
+  }
+  if (kAll && ranks > 1) cluster_arrive();   // every CTA runs before another one writes to it
+  const Asked asked = settings_of(P, at, V);
+  Settings S = asked.S;
+  const bool greedy = asked.greedy;
+  const float lowest = -3.4028235e38f;
+  // a binary order of weight in logits
+  const float binary = fminf(0.69314718055994531f * S.heat, 3.4028235e38f);
+
+  // ---- the largest logit
+  float top = -INFINITY, part = -INFINITY;   // of the thread's odd vectors, of its even ones
+  {
+    bool odd = false;
+    row.template each<NT>([&](int i) { top = fmaxf(top, value_at(logits, i)); },
+                          [&](const uint4& x, int) {
+                            const float m = max_of<T>(x);
+                            if (odd) top = fmaxf(top, m);
+                            else part = fmaxf(part, m);
+                            odd = !odd;
+                          });
+  }
+  const float mine = fmaxf(top, part), rest = fminf(top, part);
+  uint32_t best = __reduce_max_sync(kFull, ord_f32(mine));
+  if (lane == 0) sh->warp_count[warp] = best;
+  if (!greedy) fill_table(sh);
+  __syncthreads();
+  best = __reduce_max_sync(kFull, sh->warp_count[lane % (NT / 32)]);
+  // Each thread has the maxima of two disjoint parts of the row, so what top_k of those
+  // maxima reach is reached by top_k tokens: the list need not go further down.
+  uint32_t reach = 0;
+  if (!greedy && S.by_k && S.top_k <= 2 * NT) {
+    float lo = unord_f32(best) - 32.f * binary, hi = unord_f32(best);
+    const bool two = S.top_k > NT / 2;       // for few the larger one of each thread serves
+    auto enough = [&](float x) {
+      return __syncthreads_count(mine >= x) + (two ? __syncthreads_count(rest >= x) : 0) >= S.top_k;
+    };
+    if (enough(fmaxf(lo, lowest))) {
+      lo = fmaxf(lo, lowest);
+      for (int i = 0; i < 10; ++i) {
+        const float mid = 0.5f * (lo + hi);
+        if (enough(mid)) lo = mid;
+        else hi = mid;
+      }
+      reach = ord_f32(lo);
+    }
+  }
+  if (kAll && ranks > 1) {
+    cluster_wait();
+    if (tid < int(ranks)) put64(there(&sh->tops[rank], tid), uint64_t(best) << 32 | reach);
+    sync();
+    const uint64_t x = sh->tops[lane % ranks];
+    best = __reduce_max_sync(kFull, uint32_t(x >> 32));
+    reach = __reduce_max_sync(kFull, uint32_t(x));
+  }
+  top = unord_f32(best);
+  if (top == -INFINITY) {                    // nothing is left to draw from
+    if (rank == 0 && tid == 0) {
+      P.tokens[at] = -1;
+      P.probs[at] = 0.f;
+    }
+    return;
+  }
+
+  if (greedy) {
+    uint32_t first = 0xFFFFFFFFu;
+    if (mine == top)
+      row.template each<NT>([&](int i) { if (value_at(logits, i) == top) first = min(first, uint32_t(i)); },
+                            [&](const uint4& x, int i) {
+                              if (max_of<T>(x) != top) return;
+#pragma unroll
+                              for (int k = Slice<T>::kPer - 1; k >= 0; --k)
+                                if (value_of<T>(x, k) == top) first = min(first, uint32_t(i + k));
+                            });
+    if (first != 0xFFFFFFFFu) atomicMin(&sh->first, first);
+    __syncthreads();
+    first = sh->first;
+    if (kAll && ranks > 1) {
+      if (tid == 0) put64(there(&sh->tails[rank], 0), first);
+      sync();
+      if (rank != 0) return;
+      first = __reduce_min_sync(kFull, uint32_t(sh->tails[lane % ranks]));
+    }
+    if (tid == 0) {
+      P.tokens[at] = int32_t(first);
+      P.probs[at] = 1.f;
+    }
+    return;
+  }
+
+  Weigh weigh;
+  weigh.top = top;
+  weigh.shift = P.shift;
+  weigh.table = sh->table;
+  weigh.c_hi = asked.c_hi;
+  weigh.c_lo = asked.c_lo;
+  if (S.by_m) {
+    if (tid == 0) sh->least = least_of(S, top);
+    __syncthreads();
+    S.least = sh->least;
+  }
+  S.tail = S.tail && top < INFINITY;
+  const Tail<T> light{top, weigh.c_hi, __uint_as_float(uint32_t(127 + P.shift) << 23)};
+  // short rows are listed whole; min-p alone says itself what is kept
+  float cut = fmaxf(top - kNear * binary, lowest);
+  if (V <= NT || binary > 1e30f) cut = lowest;       // so the lowest value weighs nothing where it stands for none
+  else if (top == INFINITY) cut = top;
+  else if (reach != 0) cut = unord_f32(reach);
+  if (V > NT && S.by_m && !S.by_p) cut = fmaxf(S.by_k && reach != 0 ? fmaxf(cut, S.least) : S.least, lowest);
+  const Mid mid{top, weigh.c_hi, weigh.c_lo, P.shift, sh->table};
+  uint64_t known = 0;
+
+  // ---- the tokens near the largest, and the weight of the others
+  uint64_t before = 0, behind = 0;
+  const bool rest_counts = S.tail && cut > lowest;
+  auto put = [&](float z, int i, uint32_t k) {
+    if (k < uint32_t(kList)) list[k] = elem_key(z, uint32_t(i));
+  };
+  row.template each<NT>(
+      [&](int i) {
+        const float z = value_at(logits, i);
+        if (z >= cut) put(z, i, atomicAdd(&sh->mine, 1u));
+        else if (rest_counts && z > -INFINITY) behind += light(z);
+      },
+      [&](const uint4& x, int i) {
+        if (max_of<T>(x) < cut) {
+          if (rest_counts) behind += light(x);
+          return;
+        }
+        uint32_t hits = 0;
+        uint4 y = x;                         // without the hits
+#pragma unroll
+        for (int k = 0; k < Slice<T>::kPer; ++k)
+          if (value_of<T>(x, k) >= cut) {
+            hits |= 1u << k;
+            uint32_t& w = (k * int(sizeof(T)) / 4 == 0) ? y.x : (k * int(sizeof(T)) / 4 == 1) ? y.y : (k * int(sizeof(T)) / 4 == 2) ? y.z : y.w;
+            w = sizeof(T) == 4 ? 0xFF7FFFFFu : k & 1 ? (w & 0xFFFFu) | (kLowest2<T> & 0xFFFF0000u) : (w & 0xFFFF0000u) | (kLowest2<T> & 0xFFFFu);
+          }
+        if (rest_counts) behind += light(y);
+        if (hits) {
+          uint32_t k = atomicAdd(&sh->mine, uint32_t(__popc(hits)));
+          do {
+            const int e = __ffs(hits) - 1;
+            hits &= hits - 1;
+            put(value_at(logits, i + e), i + e, k++);
+          } while (hits);
+        }
+      });
+  bool planned = false;
+  for (;;) {
+    // ---- the list and the sums come together, and what they decide
+    uint64_t above = 0, below = 0;
+    if (S.tail) {
+      uint32_t z = 0, zz;
+      if (planned) scan<NT>(sh, z, before, zz, above);
+      scan<NT>(sh, z, behind, zz, below);
+    }
+    __syncthreads();
+    int n = int(min(sh->mine, uint32_t(2 * kList)));
+    if (kAll && ranks > 1) {
+      if (rank != 0) {
+        // hand it over: one place is asked for, then all entries are written
+        if (tid == 0) {
+          sh->at_count = add32(there(&sh->others, 0), uint32_t(n));
+          put64(there(&sh->tails[rank], 0), below);
+          put64(there(&sh->heads[rank], 0), above);
+        }
+        __syncthreads();
+        const uint32_t from = sh->at_count;
+        for (int i = tid; i < min(n, kList); i += NT)
+          if (from + i < uint32_t(kList)) put64(there(&cum[from + i], 0), list[i]);
+      }
+      sync();
+      if (rank == 0) {
+        const int others = int(sh->others);
+        if (n + others <= kList)
+          for (int i = tid; i < others; i += NT) list[n + i] = cum[i];
+        n += others;
+        for (uint32_t r = 1; r < ranks; ++r) {
+          below += sh->tails[r];
+          above += sh->heads[r];
+        }
+        __syncthreads();
+      }
+    }
+    const bool complete = cut <= lowest;
+    Verdict v = kGeneral;
+    if (rank == 0) {
+      const bool drawing = known != 0;
+      if (n <= kList && n > 0) {
+        sort_list<NT>(list, n);
+        uint64_t slack = 0;
+        if (S.tail && planned) slack = ((above + below + known) >> 28) + 2 * uint64_t(V);
+        else if (S.tail && !complete) slack = (below >> 17) + uint64_t(V);
+        v = decide<NT>(S, weigh, sh, list, cum, n, above, below, slack, complete && above == 0, known, &P.tokens[at],
+                       &P.probs[at]);
+      } else if (!planned && !(S.by_m && !S.by_p)) {
+        v = kPlan;                           // by what the histogram says
+        if (tid == 0) sh->want = S.by_k ? float(S.top_k) : -1.f;
+      }
+      // once more at most for the share, and once for the draw
+      if (v == kPlan && planned && (drawing || known == 0)) v = kGeneral;
+      if (v == kPlan && sizeof(T) == 2) v = kGeneral;        // whose histogram is quicker than what follows
+    }
+    // ---- how far down the list has to go: counts by distance from the largest
+    float from = 0.f, scale = float(kSteps);
+    uint64_t base = 0;                       // the weight before `from`, here in parts of 2^-30 of the largest
+    for (int level = 0;; ++level) {
+      if (kAll && ranks > 1) {
+        if (rank == 0 && tid < int(ranks)) {
+          put32(there(&sh->verdict, tid), v);
+          put32(there(&sh->from, tid), __float_as_uint(from));
+          put32(there(&sh->scale, tid), __float_as_uint(scale));
+        }
+        sync();
+        v = Verdict(sh->verdict);
+        from = sh->from;
+        scale = sh->scale;
+      }
+      if (v != kPlan && v != kRefine) break;
+      __syncthreads();
+      for (int i = tid; i < kList; i += NT) plan[i] = 0;
+      __syncthreads();
+      each_logit<NT>(row, [&](uint32_t, float z, int) {
+        const float y = ((z == top ? 0.f : (top - z) * weigh.c_hi) - from) * scale;
+        if (y >= 0.f && (level == 0 || y < float(kList))) atomicAdd(&plan[y < float(kList - 1) ? int(y) : kList - 1], 1u);
+      });
+      sync();
+      if (rank == 0) {
+        constexpr int kEach = kList / NT;
+        uint32_t count = 0, total, own[kEach];
+        uint64_t parts = 0, all_parts;
+        // a step's weight is off by half a step's 2^(1/scale) at most
+        auto weight = [&](uint32_t n, int e) {
+          return uint64_t(float(n) * ex2_approx(-from - (float(tid * kEach + e) + 0.5f) / scale) * 1073741824.f);
+        };
+        for (int e = 0; e < kEach; ++e) {
+          const int i = tid * kEach + e;
+          own[e] = plan[i];
+          for (uint32_t r = 1; r < ranks; ++r) own[e] += get32(there(&plan[i], r));
+          count += own[e];
+          parts += weight(own[e], e);
+        }
+        scan<NT>(sh, count, parts, total, all_parts);
+        const float want = sh->want;
+        const float share = want >= 0.f ? want : (S.by_p ? S.top_p : fminf(fmaxf(S.u, 0.f), 1.f)) * float(all_parts) * 0x1p-30f;
+        // the first step within 1/512 of the place, and the first that is behind it by as much
+        const uint64_t goal = uint64_t(share * 1073741824.f), off = (goal >> 9) + 1;
+        if (tid == 0) {
+          sh->at_bin = sh->at_count = 0;
+          sh->at_weight = base;
+          sh->at_end = uint32_t(kList - 1);
+          sh->end_count = total;
+        }
+        __syncthreads();
+        uint32_t c = count;
+        uint64_t w = base + parts;
+        for (int e = 0; e < kEach; ++e) {
+          const uint64_t next = w + weight(own[e], e);
+          const uint32_t upto = c + own[e];
+          if (S.by_k ? c < uint32_t(S.top_k) && upto >= uint32_t(S.top_k) : w <= goal + off && next > goal + off) {
+            sh->at_end = uint32_t(tid * kEach + e);
+            sh->end_count = upto;
+          }
+          if (!S.by_k && w + off <= goal && next + off > goal) {
+            sh->at_bin = uint32_t(tid * kEach + e);
+            sh->at_count = c;
+            sh->at_weight = w;
+          }
+          c = upto;
+          w = next;
+        }
+        __syncthreads();
+        const int end = int(sh->at_end);
+        int begin = int(sh->at_bin);
+        const bool beyond = end >= kList - 1;
+        v = kRead;
+        // from the largest on where the list can hold it, else around the place alone
+        bool from_top = level == 0 && sh->end_count <= uint32_t(kList);
+        float hi = NAN;                      // no logit is at least that
+        if (!from_top) {
+          if (S.by_k || S.by_m || begin > end) v = kGeneral;
+          else if (sh->end_count - sh->at_count > uint32_t(kList)) v = level == 0 && !beyond ? kRefine : kGeneral;
+          if (level > 0 || begin > 0) hi = top - (from + (float(begin) - 0.5f) / scale) * binary;
+        }
+        if (v == kRefine) {
+          // the same steps again, 2048 parts of them
+          base = sh->at_weight;
+          from += float(begin) / scale;
+          scale *= float(kList / (end + 1 - begin));
+        }
+        __syncthreads();
+        if (tid == 0) {
+          const float to = top - (from + (float(end) + 1.5f) / scale) * binary;
+          sh->cut = beyond && (level == 0) ? lowest : fmaxf(to, lowest);
+          sh->cut_above = hi;
+          sh->mine = 0;
+          sh->others = 0;
+        }
+        __syncthreads();
+        if (kAll && ranks > 1 && tid > 0 && tid < int(ranks)) {
+          put32(there(&sh->cut, tid), __float_as_uint(sh->cut));
+          put32(there(&sh->cut_above, tid), __float_as_uint(sh->cut_above));
+          put32(there(&sh->mine, tid), 0u);
+        }
+      }
+    }
+    if (v == kDone) return;
+    if (v == kGeneral) break;
+    // ---- the list again, around that place; the sums of the others to 2^-29
+    cut = sh->cut;
+    const float cut_above = sh->cut_above;
+    planned = true;
+    before = behind = 0;
+    each_logit<NT>(row, [&](uint32_t, float z, int i) {
+      if (z >= cut && !(z >= cut_above)) {
+        put(z, i, atomicAdd(&sh->mine, 1u));
+      } else if (S.tail) {
+        const uint64_t w = mid(z);
+        if (z < cut) behind += w;
+        else before += w;
+      }
+    });
+  }
+  if (rank != 0) return;
+  if constexpr (kAll) {
+    general<T>(P, logits, at, weigh, S, sh, reinterpret_cast<unsigned char*>(list));
+  } else if (tid == 0) {
+    P.tokens[at] = kUndecided;
+    P.probs[at] = top;
+  }
+}
+
+// The rows that sample_kernel left undecided.
+template <typename T>
+__global__ void __launch_bounds__(kThreads, 2) rest_kernel(const SampleParams P) {
+  asm volatile("griddepcontrol.wait;" ::: "memory");
+  extern __shared__ __align__(16) unsigned char smem[];
+  Shared* sh = reinterpret_cast<Shared*>(smem);
+  for (long long at = blockIdx.x; at < P.rows; at += gridDim.x) {
+    if (P.tokens[at] != kUndecided) continue;
+    __syncthreads();                         // the token is read before it is written, and the row before is done
+    const Asked asked = settings_of(P, at, P.V);
+    Settings S = asked.S;
+    Weigh weigh;
+    weigh.top = P.probs[at];
+    weigh.shift = P.shift;
+    weigh.table = sh->table;
+    weigh.c_hi = asked.c_hi;
+    weigh.c_lo = asked.c_lo;
+    fill_table(sh);
+    if (S.by_m && threadIdx.x == 0) sh->least = least_of(S, weigh.top);
+    __syncthreads();
+    if (S.by_m) S.least = sh->least;
+    general<T>(P, static_cast<const T*>(P.logits) + at * P.stride, at, weigh, S, sh, reinterpret_cast<unsigned char*>(sh + 1));
+    __syncthreads();
   }
 }
 
 template <typename T>
-cudaError_t launch(const SampleParams& P, long long rows, cudaStream_t s) {
+cudaError_t launch(SampleParams& P, cudaStream_t s) {
   using B = Bins<T>;
-  const int smem = int(sizeof(Shared)) + 8 * (B::kSingle ? 4 : B::kCount + 1) + 4 * B::kCount;
-  const cudaError_t e = settled(cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+  const int bins = int(sizeof(Parts)) + 8 * (B::kSingle ? 4 : B::kCount + 1) + 4 * B::kCount, lists = 16 * kList;
+  const int small = int(sizeof(Shared)) + lists, large = int(sizeof(Shared)) + (bins > lists ? bins : lists);
+  const int sms = device_sms() > 0 ? device_sms() : 152;
+  cudaLaunchAttribute at[1];
+  cudaLaunchConfig_t cfg = {};
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  if (P.rows <= 2 * sms) {
+    // Rows that do not fill the device are shared: as many CTAs a row as keep it to one round
+    // of two an SM, none with less than 4096 logits.
+    const auto kernel = sample_kernel<T, kThreads, 2, true>;
+    const cudaError_t e = settled(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, large));
+    if (e != cudaSuccess) return e;
+    P.ranks = 1;
+    while (P.ranks < kMaxRanks && P.rows * 2 * P.ranks <= 2ll * sms && P.V / (2 * P.ranks) >= 4096) P.ranks *= 2;
+    if (P.ranks == 1) return launch_kernel(kernel, unsigned(P.rows), kThreads, large, s, P);
+    at[0].id = cudaLaunchAttributeClusterDimension;
+    at[0].val.clusterDim.x = unsigned(P.ranks);
+    at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+    cfg.gridDim = dim3(unsigned(P.rows * P.ranks));
+    cfg.blockDim = dim3(kThreads);
+    cfg.dynamicSmemBytes = large;
+    return settled(cudaLaunchKernelEx(&cfg, kernel, static_cast<const SampleParams&>(P)));
+  }
+  // Many rows: smaller CTAs, more of them an SM, so that one's sums and barriers pass while
+  // others read; the few rows that their lists do not decide are left to a second kernel.
+  const auto kernel = sample_kernel<T, kManyThreads, kManyCtas, false>;
+  cudaError_t e = settled(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, small));
   if (e != cudaSuccess) return e;
-  return launch_kernel(sample_kernel<T>, unsigned(rows), kThreads, smem, s, P);
+  P.ranks = 1;
+  e = launch_kernel(kernel, unsigned(P.rows), kManyThreads, small, s, P);
+  if (e != cudaSuccess) return e;
+  e = settled(cudaFuncSetAttribute(rest_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, large));
+  if (e != cudaSuccess) return e;
+  at[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+  at[0].val.programmaticStreamSerializationAllowed = 1;
+  cfg.gridDim = dim3(unsigned(2 * sms));
+  cfg.blockDim = dim3(kThreads);
+  cfg.dynamicSmemBytes = large;
+  return settled(cudaLaunchKernelEx(&cfg, rest_kernel<T>, static_cast<const SampleParams&>(P)));
 }
 
 }  // namespace
@@ -599,11 +1399,11 @@ extern "C" int dart_logits_sample(const void* logits, int B, int R, int V, int64
   P.logits = logits; P.stride = row_stride;
   P.uniforms = uniforms; P.temperature = temperature; P.top_p = top_p; P.min_p = min_p; P.top_k = top_k;
   P.tokens = out_tokens; P.probs = out_probs;
-  P.R = R; P.V = V;
+  P.R = R; P.V = V; P.rows = rows;
   P.shift = 62 - bits;                       // the sum of V weights of 1 stays below 2^62
   cudaStream_t s = static_cast<cudaStream_t>(stream);
-  const cudaError_t e = dtype == DART_F32   ? launch<float>(P, rows, s)
-                        : dtype == DART_F16 ? launch<__half>(P, rows, s)
-                                            : launch<__nv_bfloat16>(P, rows, s);
+  const cudaError_t e = dtype == DART_F32   ? launch<float>(P, s)
+                        : dtype == DART_F16 ? launch<__half>(P, s)
+                                            : launch<__nv_bfloat16>(P, s);
   return e == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

@@ -532,8 +532,9 @@ int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * first top_k, n_m the number of w_i >= min_p.  The token drawn is the first
  * whose running sum exceeds u times the sum of the n kept; its probability is
  * w / that sum.  Weights are integers of 2^(62 - ceil(log2(V + 1))) parts of
- * the largest, exact to a few of them, and sums are exact, so a draw does not
- * depend on the order of summation.
+ * the largest, exact to a few of them, and a draw is what their exact sums say.
+ * The probability is rounded once; without any limit the sum in it holds the
+ * weights below 2^-12 to 2^-18 of theirs.
  * NaN and -inf are never drawn; a row without any other logit gives token -1
  * and probability 0.  +inf is drawn before anything finite.
  *  logits      device [B][R] rows of V elements, row_stride >= V apart (at most

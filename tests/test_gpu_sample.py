@@ -13,13 +13,13 @@ torch = pytest.importorskip("torch")
 DT = {"bf16": torch.bfloat16, "f16": torch.float16, "f32": torch.float32}
 
 
-def _near(V):
-    """How near to an edge, as a share of the sum, u may lie for another token to be drawn.
+def _near(V, total):
+    """How near to an edge a place may lie, in units of the largest weight, for another token to be drawn.
 
-    A weight is within one part of 2^-(62 - bits) of the largest, bits = the length of V, and within 2^-45 of itself; a
-    sum of up to V of them, at least the largest, within V parts and 2^-45.  The running sum and its total are both off
-    by that, the reference's own sums in 64 bits by less: four times it covers them."""
-    return 4.0 * (V * 2.0 ** -(62 - V.bit_length()) + 2.0 ** -45)
+    A weight is within half a part of 2^-(62 - bits), bits = the length of V, and within 2^-45 of itself, so the sum of
+    up to V of them, and a share of a sum, within V / 2 parts and 2^-45 of it.  The place and the edge are both off by
+    that, the reference's own sums in 64 bits by less."""
+    return 2.0 * (V / 2 * 2.0 ** -(62 - V.bit_length()) + 2.0 ** -45 * total)
 
 
 @pytest.fixture(scope="module")
@@ -46,13 +46,16 @@ def _check(D, z, u, heat=None, k=None, p=None, m=None):
         rows = z[b].double().numpy()
         one = lambda x, default: default if x is None else float(np.float32(x[b]))
         for r in range(R):
-            t, pr, near = refs.sample(rows[r], float(u[b, r]), one(heat, 1.0), int(one(k, 0)), one(p, 1.0), one(m, 0.0))
-            if near < _near(V):
+            t, pr, near, total = refs.sample(rows[r], float(u[b, r]), one(heat, 1.0), int(one(k, 0)), one(p, 1.0), one(m, 0.0))
+            if near < _near(V, total):
                 unsaid += 1
                 continue
             assert int(tokens[b, r]) == t, (b, r, near)
-            # a quotient of exact integers, rounded once
-            assert abs(float(probs[b, r]) - pr) <= 2.0 ** -23 * pr + 1e-30, (b, r)
+            # a quotient of integers, rounded once.  Without limits the sum has the weights that the draw did not have
+            # to list in fp32: an exponent y < 64 is off by 2^-24 y (its factor and the product, half a step each), the
+            # weight by 2^-24 64 ln 2 = 2^-18.5 of itself, 2^x by 2^-22, a sum of eight by 2^-22.
+            off = 2.0 ** -23 + (2.0 ** -18 if k is None and p is None and m is None else 0.0)
+            assert abs(float(probs[b, r]) - pr) <= off * pr + 1e-30, (b, r)
     assert unsaid <= max(1, B * R // 256)
     return tokens
 
@@ -125,9 +128,38 @@ def test_rows_with_nothing_and_with_infinities(D, dtype):
     z[0, 5, [3, 400]] = math.inf
     z[0, 6, :500] = -math.inf                 # one token left
     z[0, 7, 1:] = torch.finfo(DT[dtype]).min  # a mask of the type's lowest value
-    for kw in ({}, dict(p=[0.9]), dict(k=[3], m=[0.1]), dict(heat=[0.0]), dict(heat=[1e-30])):
+    for kw in ({}, dict(p=[0.9]), dict(k=[3], m=[0.1]), dict(heat=[0.0]), dict(heat=[1e-30]), dict(heat=[math.inf]),
+               dict(heat=[math.inf], m=[1.0]), dict(heat=[math.inf], p=[0.5])):
         tokens = _check(D, z, u, **kw)
         assert tokens[0, 0] == -1 and tokens[0, 1] == -1 and tokens[0, 4] == 7 and tokens[0, 6] == 500
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("V", [3000, 40000])
+def test_numbers_next_to_an_edge(D, dtype, V):
+    """Random numbers and shares that fall within some 2^-25 of an edge, where the sum of the many small weights counts
+    to its last bits."""
+    z = torch.full((1, 40, V), -5.0)
+    z[..., 5:V:V // 4] = 5.0
+    z = z.to(DT[dtype])
+    w = np.exp(z[0, 0].double().numpy() - 5.0)
+    large = np.sort(w)[::-1].cumsum()[:3] / w.sum()
+    steps = np.arange(40) - 20
+    for edge in large:
+        u = torch.from_numpy((np.float32(edge) * (1 + steps * 2.0 ** -23)).astype(np.float32))[None]
+        _check(D, z, u)
+        _check(D, z, torch.full((1, 40), 0.999), p=[float(u[0, 7])])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("spread", [0.5, 1.0, 2.0, 3.0, 6.0])
+def test_flat_and_peaked_rows(D, dtype, spread):
+    """From rows where a few tokens matter to rows where most do; few rows (shared by a cluster's CTAs) and many."""
+    for B, R, V in ((2, 2, 151936), (1, 6, 33333), (2, 80, 9001)):
+        z, u = _logits(B, R, V, dtype, seed=int(spread * 10), scale=spread)
+        for kw in ({}, dict(p=[0.95]), dict(p=[0.995], heat=[1.5]), dict(k=[1500]), dict(k=[3000], p=[0.9]),
+                   dict(m=[0.001]), dict(m=[0.0001], p=[0.9]), dict(heat=[8.0], k=[50])):
+            _check(D, z, u, **{key: x * B for key, x in kw.items()})
 
 
 def test_ends_of_the_uniforms(D):

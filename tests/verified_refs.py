@@ -8,38 +8,39 @@ from tests.steps_refs import U, unpack
 
 
 def sample(z, u, heat=1.0, k=0, p=1.0, m=0.0):
-    """(token, probability, distance) of one row: what sample_logits draws, and how far u lies from where another token
-    would be drawn, as a share of the sum."""
+    """(token, probability, distance, sum) of one row: what sample_logits draws, how far a share or u lies from where
+    another token would be drawn, and the sum of the weights, both in units of the largest."""
     z = np.asarray(z, np.float64)
     z = np.where(np.isnan(z), -np.inf, z)
     order = np.argsort(-z, kind="stable")
     total = int(np.sum(z > -np.inf))
     if total == 0:
-        return -1, 0.0, 1.0
+        return -1, 0.0, np.inf, 0.0
     order = order[:total]
     if not heat > 0:
-        return int(order[0]), 1.0, 1.0
+        return int(order[0]), 1.0, np.inf, 0.0
     x = z[order]
     with np.errstate(invalid="ignore", over="ignore"):
-        w = np.where(x == x[0], 1.0, np.exp((x - x[0]) / np.float64(heat)))
+        w = np.where(x == x[0], 1.0, 0.0 if np.isinf(x[0]) else np.exp((x - x[0]) / np.float64(heat)))
     n = total if k <= 0 else min(k, total)
     limit = n
     cum = np.cumsum(w)
-    near = 1.0
+    near = np.inf
     if p <= 0:
         limit = 1
     elif p < 1:
         limit = min(limit, int(np.searchsorted(cum[:n], p * cum[n - 1])) + 1)
-        near = float(np.min(np.abs(cum[:n] / cum[n - 1] - p)))
+        near = float(np.min(np.abs(cum[:n] - p * cum[n - 1])))
     if m > 0:
         limit = min(limit, int(np.sum(w >= m)))
     limit = max(limit, 1)
     t = u * cum[limit - 1]
     i = min(int(np.searchsorted(cum[:limit], t, side="right")), limit - 1)
-    edges = np.abs(cum[:limit - 1] - t) / cum[limit - 1]
+    edges = np.abs(cum[:limit - 1] - t)
     if np.all((w == 0.0) | (w == 1.0)):         # sums of whole numbers are exact on both sides
-        return int(order[i]), float(w[i] / cum[limit - 1]), 1.0
-    return int(order[i]), float(w[i] / cum[limit - 1]), min(near, float(edges.min()) if len(edges) else 1.0)
+        return int(order[i]), float(w[i] / cum[limit - 1]), np.inf, 0.0
+    near = min(near, float(edges.min()) if len(edges) else np.inf)
+    return int(order[i]), float(w[i] / cum[limit - 1]), near, float(cum[n - 1])
 
 
 def accept(picks, tokens, parents, depth):

@@ -77,7 +77,7 @@ class _LeaveAll:
     def adjust(*args):
         return None
 
-    append = attend = adjust
+    append = attend = sample = accept = keep = weights = evict = bind_verified = adjust
 
 
 def _load_native():

@@ -8,6 +8,7 @@ from __future__ import annotations
 
 import ctypes as C
 
+from . import _steps
 from . import DartError, _check, _check_error_word, _check_tensor, _mask_dtypes, _row_stride, _torch, lib
 from ._steps import (_at, _Cache, _cache, _check_inner, _codes, _enter, _heads, _leave, _one_device, _sequences,
                      _stream)
@@ -25,6 +26,24 @@ def declare(L):
         f.restype = i32
 
 
+# The usual calls are made by the native module, as those of the steps around a
+# tree are: it returns None for what it leaves to the code here.
+
+_bound = None
+
+
+def _native():
+    global _bound
+    module = _steps._native or _steps._load_native()
+    if module is not _bound:
+        L = lib()
+        module.bind_verified(*(C.cast(f, C.c_void_p).value for f in
+                               (L.dart_logits_sample, L.dart_tree_accept, L.dart_kv_keep, L.dart_attention_weights,
+                                L.dart_kv_evict)))
+        _bound = module
+    return module
+
+
 # ----------------------------------------------------------------- sampling
 
 def sample_logits(logits, uniforms, *, temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> dict:
@@ -40,6 +59,10 @@ def sample_logits(logits, uniforms, *, temperature=None, top_k=None, top_p=None,
     top_p counts from the top_k renormalised, min_p is relative to the largest.
     Returns tokens (int32 [B, R], -1 where a row has nothing to draw from) and
     probs (float32 [B, R], their probabilities among what was kept)."""
+    if stream is None and logits.is_cuda:
+        made = _native().sample(logits, uniforms, temperature, top_k, top_p, min_p)
+        if made is not None:
+            return {"tokens": made[0], "probs": made[1]}
     torch = _torch()
     dev = _one_device(("logits", "uniforms", "temperature", "top_k", "top_p", "min_p"),
                       (logits, uniforms, temperature, top_k, top_p, min_p))
@@ -82,6 +105,10 @@ def tree_accept(picks, tokens, parents, depth: int, *, stream=None) -> dict:
     row of each accepted node, -1 behind), counts (int32 [B], entries of the
     path) and tokens (int32 [B, depth + 1]: the accepted tokens and the one that
     follows them, -1 behind)."""
+    if stream is None and tokens.is_cuda:
+        made = _native().accept(picks, tokens, parents, depth)
+        if made is not None:
+            return {"path": made[0], "counts": made[1], "tokens": made[2]}
     torch = _torch()
     dev = _one_device(("picks", "tokens", "parents"), (picks, tokens, parents))
     if tokens.dim() != 2:
@@ -122,6 +149,10 @@ def kv_keep(k_cache, v_cache, pages, lengths, path, counts, *, device_err=None, 
     Returns the new lengths, lengths + counts: one call per layer reads the old
     ones.  device_err (int32 [>= 1], zeroed by the caller) collects the error
     bits of what is out of range or out of order."""
+    if stream is None and k_cache.is_cuda:
+        made = _native().keep(k_cache, v_cache, pages, lengths, path, counts, device_err)
+        if made is not None:
+            return made
     torch = _torch()
     dev = _one_device(("k_cache", "v_cache", "pages", "lengths", "path", "counts", "device_err"),
                       (k_cache, v_cache, pages, lengths, path, counts, device_err))
@@ -178,6 +209,10 @@ def attention_weights(q, k_cache, pages, lengths, starts, lse, scores, *, mask=N
     row whose lse is not finite adds nothing: set it to +inf to leave a row out.
     Returns scores.  device_err (int32 [>= 1], zeroed by the caller) collects
     error bits."""
+    if stream is None and q.is_cuda:
+        made = _native().weights(q, k_cache, pages, lengths, starts, lse, scores, mask, scale, device_err)
+        if made is not None:
+            return made
     torch = _torch()
     dev = _one_device(("q", "k_cache", "pages", "lengths", "starts", "lse", "scores", "mask", "device_err"),
                       (q, k_cache, pages, lengths, starts, lse, scores, mask, device_err))
@@ -224,6 +259,10 @@ def kv_evict(k_cache, v_cache, pages, lengths, scores, keep: int, *, first: int 
     shortened lengths.  Returns lengths (int32 [B], the new ones) and index
     (int32 [B, heads, keep], the old position of each slot, -1 from the length
     on).  device_err as for kv_keep."""
+    if stream is None and k_cache.is_cuda:
+        made = _native().evict(k_cache, v_cache, pages, lengths, scores, keep, first, last, device_err)
+        if made is not None:
+            return {"lengths": made[0], "index": made[1]}
     torch = _torch()
     dev = _one_device(("k_cache", "v_cache", "pages", "lengths", "scores", "device_err"),
                       (k_cache, v_cache, pages, lengths, scores, device_err))

@@ -1,5 +1,5 @@
-// dart_steps_py.cpp -- the usual calls of the steps around a tree, without the
-// interpreter: tensors in, the C entry point, tensors out.
+// dart_steps_py.cpp -- the usual calls of the steps around a tree and behind a
+// verified one, without the interpreter: tensors in, the C entry point, tensors out.
 //
 // Checks and arguments in Python cost 9 to 13 us a call on a Grace core (an
 // adjustment with everything 20), longer than many of these kernels run; here
@@ -32,6 +32,11 @@ decltype(&dart_logits_adjust) logits_adjust = nullptr;
 decltype(&dart_kv_append) kv_append = nullptr;
 decltype(&dart_tree_attention) tree_attention = nullptr;
 decltype(&dart_attention_workspace_bytes) workspace_bytes = nullptr;
+decltype(&dart_logits_sample) logits_sample = nullptr;            // these by bind_verified()
+decltype(&dart_tree_accept) tree_accept = nullptr;
+decltype(&dart_kv_keep) kv_keep = nullptr;
+decltype(&dart_attention_weights) attention_weights = nullptr;
+decltype(&dart_kv_evict) kv_evict = nullptr;
 PyObject* check = nullptr;          // check(code, name) raises the package's error; also from bind()
 
 PyObject* failed(int rc, const char* name) {
@@ -330,6 +335,213 @@ PyObject* attend(PyObject*, PyObject* const* args, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
+// -------------------------------------------------- behind a verified tree
+
+// An error word: absent, or at least one packed integer.
+bool error_word(const Tensor* t) { return !t || (packed(*t) && t->numel() >= 1 && t->is_contiguous()); }
+bool ints(const Tensor* t, int64_t B, int64_t n) {             // contiguous int32 [B, n]
+  return t && t->scalar_type() == at::kInt && t->dim() == 2 && t->size(0) == B && t->size(1) == n && t->is_contiguous();
+}
+
+// (logits, uniforms, temperature, top_k, top_p, min_p) -> (tokens, probs)
+PyObject* sample(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 6) Py_RETURN_NONE;
+  Taker take;
+  const Tensor *z = take(args[0]), *u = take(args[1]), *temperature = take(args[2]), *top_k = take(args[3]),
+               *top_p = take(args[4]), *min_p = take(args[5]);
+  if (!take.ok || !logits_sample || !z || !u || z->dim() != 3 || z->numel() == 0) Py_RETURN_NONE;
+  const int64_t B = z->size(0), R = z->size(1), V = z->size(2), stride = row_stride(*z);
+  const int code = dtype_code(z->scalar_type());
+  if (code < 0 || stride < 0 || B > INT_MAX || R > INT_MAX || V > INT_MAX || u->scalar_type() != at::kFloat ||
+      u->dim() != 2 || u->size(0) != B || u->size(1) != R || !u->is_contiguous() || !is(temperature, at::kFloat, B) ||
+      !is(top_k, at::kInt, B) || !is(top_p, at::kFloat, B) || !is(min_p, at::kFloat, B))
+    Py_RETURN_NONE;
+  Tensor tokens = at::empty({B, R}, u->options().dtype(at::kInt)), probs = at::empty({B, R}, u->options());
+  int rc;
+  void* const stream = current_stream(take.device);
+  Py_BEGIN_ALLOW_THREADS
+  rc = logits_sample(z->data_ptr(), int(B), int(R), int(V), stride, code, at_of<float>(u), at_of<float>(temperature),
+                     at_of<int32_t>(top_k), at_of<float>(top_p), at_of<float>(min_p), at_of<int32_t>(&tokens),
+                     at_of<float>(&probs), stream);
+  Py_END_ALLOW_THREADS
+  if (rc != DART_OK) return failed(rc, "dart_logits_sample");
+  return Py_BuildValue("NN", THPVariable_Wrap(tokens), THPVariable_Wrap(probs));
+  END_HANDLE_TH_ERRORS
+}
+
+// (picks, tokens, parents, depth) -> (path, counts, tokens)
+PyObject* accept(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 4) Py_RETURN_NONE;
+  Taker take;
+  const Tensor *picks = take(args[0]), *tokens = take(args[1]), *parents = take(args[2]);
+  if (!take.ok || !tree_accept || !picks || !tokens || !parents || tokens->dim() != 2 || tokens->numel() == 0 ||
+      !PyLong_Check(args[3]))
+    Py_RETURN_NONE;
+  const int64_t B = tokens->size(0), N = tokens->size(1);
+  const long depth = PyLong_AsLong(args[3]);
+  if (PyErr_Occurred()) {
+    PyErr_Clear();
+    Py_RETURN_NONE;
+  }
+  if (!ints(tokens, B, N) || !ints(parents, B, N) || !ints(picks, B, N + 1) || B > INT_MAX || N > INT_MAX ||
+      depth < 0 || depth > N)
+    Py_RETURN_NONE;
+  Tensor path = at::empty({B, depth + 1}, tokens->options()), counts = at::empty({B}, tokens->options()),
+         out = at::empty({B, depth + 1}, tokens->options());
+  int rc;
+  void* const stream = current_stream(take.device);
+  Py_BEGIN_ALLOW_THREADS
+  rc = tree_accept(at_of<int32_t>(picks), at_of<int32_t>(tokens), at_of<int32_t>(parents), int(B), int(N), int(depth),
+                   at_of<int32_t>(&path), at_of<int32_t>(&counts), at_of<int32_t>(&out), stream);
+  Py_END_ALLOW_THREADS
+  if (rc != DART_OK) return failed(rc, "dart_tree_accept");
+  return Py_BuildValue("NNN", THPVariable_Wrap(path), THPVariable_Wrap(counts), THPVariable_Wrap(out));
+  END_HANDLE_TH_ERRORS
+}
+
+// B of lengths [B], or -1.
+int64_t lengths_of(const Tensor* lengths) {
+  if (!lengths || lengths->dim() != 1) return -1;
+  const int64_t B = lengths->size(0);
+  return B > 0 && B < INT_MAX && is(lengths, at::kInt, B) && lengths->is_contiguous() ? B : -1;
+}
+
+// (k_cache, v_cache, pages, lengths, path, counts, device_err) -> lengths
+PyObject* keep(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 7) Py_RETURN_NONE;
+  Taker take;
+  const Tensor *k_cache = take(args[0]), *v_cache = take(args[1]), *pages = take(args[2]), *lengths = take(args[3]),
+               *path = take(args[4]), *counts = take(args[5]), *err = take(args[6]);
+  const int64_t B = lengths_of(lengths);
+  dart_cache_t c;
+  if (!take.ok || !kv_keep || B < 0 || !path || !counts || !cache_of(k_cache, v_cache, pages, B, &c) ||
+      !error_word(err) || !is(counts, at::kInt, B) || path->dim() != 2 || path->size(0) != B || path->size(1) < 1 ||
+      path->size(1) > INT_MAX || path->scalar_type() != at::kInt || (path->size(1) > 1 && path->stride(1) != 1))
+    Py_RETURN_NONE;
+  const int64_t width = path->size(1), step = B > 1 ? path->stride(0) : width;
+  if (step < width) Py_RETURN_NONE;
+  Tensor out = at::empty({B}, lengths->options());
+  int rc;
+  void* const stream = current_stream(take.device);
+  Py_BEGIN_ALLOW_THREADS
+  rc = kv_keep(&c, at_of<int32_t>(lengths), at_of<int32_t>(path), step, at_of<int32_t>(counts), int(B), int(width),
+               at_of<int32_t>(&out), at_of<uint32_t>(err), stream);
+  Py_END_ALLOW_THREADS
+  if (rc != DART_OK) return failed(rc, "dart_kv_keep");
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
+}
+
+// The (sequence, head) strides of scores [B, heads, width]: false where the binding has to look.
+bool scores_of(const Tensor* t, int64_t B, int64_t heads, int64_t* seq, int64_t* head) {
+  if (!t || t->dim() != 3 || t->size(0) != B || t->size(1) != heads || t->scalar_type() != at::kFloat ||
+      t->numel() == 0 || t->size(2) > INT_MAX || (t->size(2) > 1 && t->stride(2) != 1))
+    return false;
+  const int64_t width = t->size(2);
+  *head = heads > 1 ? t->stride(1) : width;
+  *seq = B > 1 ? t->stride(0) : heads * *head;
+  return *head >= width && (B <= 1 || *seq >= *head * (heads - 1) + width);
+}
+
+// (q, k_cache, pages, lengths, starts, lse, scores, mask, scale, device_err) -> scores
+PyObject* weights(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 10) Py_RETURN_NONE;
+  Taker take;
+  const Tensor *q = take(args[0]), *k_cache = take(args[1]), *pages = take(args[2]), *lengths = take(args[3]),
+               *starts = take(args[4]), *lse = take(args[5]), *scores = take(args[6]), *mask = take(args[7]),
+               *err = take(args[9]);
+  if (!take.ok || !attention_weights || !q || !lse || q->dim() != 3 || q->numel() == 0) Py_RETURN_NONE;
+  const int64_t B = sequences(lengths, starts), T = q->size(0), q_heads = q->size(1);
+  dart_cache_t c;
+  Heads hq;
+  int64_t s_seq, s_head;
+  if (B < 0 || T > INT_MAX || q_heads > INT_MAX || !cache_of(k_cache, k_cache, pages, B, &c) ||
+      !hq.fit(*q, T, q_heads, c.dim, k_cache->scalar_type()) || q_heads % c.heads != 0 ||
+      lse->scalar_type() != at::kFloat || lse->dim() != 2 || lse->size(0) != T || lse->size(1) != q_heads ||
+      !lse->is_contiguous() || !scores_of(scores, B, c.heads, &s_seq, &s_head) || !error_word(err))
+    Py_RETURN_NONE;
+  int64_t N = 0;
+  if (mask) {
+    if (!packed(*mask) || mask->dim() != 3 || mask->size(0) != B || mask->size(2) != (mask->size(1) + 31) / 32 ||
+        !mask->is_contiguous() || mask->size(1) > INT_MAX)
+      Py_RETURN_NONE;
+    N = mask->size(1);
+  }
+  double scale = std::pow(double(c.dim), -0.5);
+  if (args[8] != Py_None) {
+    scale = PyFloat_AsDouble(args[8]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  int rc;
+  void* const stream = current_stream(take.device);
+  Py_BEGIN_ALLOW_THREADS
+  rc = attention_weights(q->data_ptr(), hq.token, hq.head, int(q_heads), int(T), int(B), at_of<int32_t>(lengths),
+                         at_of<int32_t>(starts), at_of<uint32_t>(mask), int(N), float(scale), &c, at_of<float>(lse),
+                         at_of<float>(scores), s_seq, s_head, int(scores->size(2)), at_of<uint32_t>(err), stream);
+  Py_END_ALLOW_THREADS
+  if (rc != DART_OK) return failed(rc, "dart_attention_weights");
+  return Py_NewRef(args[6]);
+  END_HANDLE_TH_ERRORS
+}
+
+// (k_cache, v_cache, pages, lengths, scores, keep, first, last, device_err) -> (lengths, index)
+PyObject* evict(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 9) Py_RETURN_NONE;
+  Taker take;
+  const Tensor *k_cache = take(args[0]), *v_cache = take(args[1]), *pages = take(args[2]), *lengths = take(args[3]),
+               *scores = take(args[4]), *err = take(args[8]);
+  const int64_t B = lengths_of(lengths);
+  dart_cache_t c;
+  int64_t s_seq, s_head, n[3];
+  if (!take.ok || !kv_evict || B < 0 || !cache_of(k_cache, v_cache, pages, B, &c) ||
+      !scores_of(scores, B, c.heads, &s_seq, &s_head) || !error_word(err))
+    Py_RETURN_NONE;
+  for (int i = 0; i < 3; ++i) {
+    if (!PyLong_Check(args[5 + i])) Py_RETURN_NONE;
+    n[i] = PyLong_AsLongLong(args[5 + i]);
+    if (PyErr_Occurred()) {
+      PyErr_Clear();
+      Py_RETURN_NONE;
+    }
+  }
+  if (n[0] < 1 || n[0] > INT_MAX || n[1] < 0 || n[2] < 0 || n[1] > n[0] || n[2] > n[0] - n[1]) Py_RETURN_NONE;
+  Tensor out = at::empty({B}, lengths->options()), index = at::empty({B, c.heads, n[0]}, lengths->options());
+  int rc;
+  void* const stream = current_stream(take.device);
+  Py_BEGIN_ALLOW_THREADS
+  rc = kv_evict(&c, at_of<int32_t>(lengths), int(B), at_of<float>(scores), s_seq, s_head, int(scores->size(2)),
+                int(n[0]), int(n[1]), int(n[2]), at_of<int32_t>(&index), at_of<int32_t>(&out), at_of<uint32_t>(err),
+                stream);
+  Py_END_ALLOW_THREADS
+  if (rc != DART_OK) return failed(rc, "dart_kv_evict");
+  return Py_BuildValue("NN", THPVariable_Wrap(out), THPVariable_Wrap(index));
+  END_HANDLE_TH_ERRORS
+}
+
+// (the addresses of dart_logits_sample, dart_tree_accept, dart_kv_keep, dart_attention_weights and dart_kv_evict)
+PyObject* bind_verified(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  void* at[5];
+  if (count != 5) {
+    PyErr_SetString(PyExc_TypeError, "bind_verified takes five addresses");
+    return nullptr;
+  }
+  for (int i = 0; i < 5; ++i) {
+    at[i] = PyLong_AsVoidPtr(args[i]);
+    if (PyErr_Occurred()) return nullptr;
+  }
+  logits_sample = reinterpret_cast<decltype(logits_sample)>(at[0]);
+  tree_accept = reinterpret_cast<decltype(tree_accept)>(at[1]);
+  kv_keep = reinterpret_cast<decltype(kv_keep)>(at[2]);
+  attention_weights = reinterpret_cast<decltype(attention_weights)>(at[3]);
+  kv_evict = reinterpret_cast<decltype(kv_evict)>(at[4]);
+  Py_RETURN_NONE;
+}
+
 // (the addresses of dart_logits_adjust, dart_kv_append, dart_tree_attention and
 // dart_attention_workspace_bytes, then what raises the package's error)
 PyObject* bind(PyObject*, PyObject* const* args, Py_ssize_t count) {
@@ -356,7 +568,13 @@ template <typename F> PyCFunction method(F f) { return reinterpret_cast<PyCFunct
 PyMethodDef methods[] = {{"adjust", method(adjust), METH_FASTCALL, nullptr},
                          {"append", method(append), METH_FASTCALL, nullptr},
                          {"attend", method(attend), METH_FASTCALL, nullptr},
+                         {"sample", method(sample), METH_FASTCALL, nullptr},
+                         {"accept", method(accept), METH_FASTCALL, nullptr},
+                         {"keep", method(keep), METH_FASTCALL, nullptr},
+                         {"weights", method(weights), METH_FASTCALL, nullptr},
+                         {"evict", method(evict), METH_FASTCALL, nullptr},
                          {"bind", method(bind), METH_FASTCALL, nullptr},
+                         {"bind_verified", method(bind_verified), METH_FASTCALL, nullptr},
                          {nullptr, nullptr, 0, nullptr}};
 PyModuleDef module = {PyModuleDef_HEAD_INIT, "_steps_native", nullptr, -1, methods, nullptr, nullptr, nullptr, nullptr};
 

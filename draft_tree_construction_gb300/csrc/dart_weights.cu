@@ -13,13 +13,17 @@
 // One persistent CTA per SM (at most 152) takes an equal share of the list of
 // (sequence, key head, tile of 128 positions), a tile costing as many row blocks
 // as its sequence has.  Within a CTA:
-//   warps 8, 10  copy K tiles by TMA into a ring of swizzled stages, in turn
-//   warp 9       issues the tcgen05 products, one row block after the other
-//   warps 11, 12 copy the row blocks of Q (two buffers; a sequence with one or two
-//                blocks keeps them there for all of its tiles)
-//   warps 0-3, 4-7  add up the exponentials, each half of a block's rows
-// Blocks are 64 rows where sequences have few (then the ring takes the memory:
-// decoding is bound by the copy of K), else 256.
+//   warps 12, 13  copy K tiles by TMA into a ring of swizzled stages, in turn
+//   warp 14       issues the tcgen05 products, one row block after the other
+//   warp 15       copies the row blocks of Q (a sequence whose blocks fit in the
+//                 buffers keeps them there for all of its tiles)
+//   warps 0-11    add up the exponentials: three groups of four warps, each a third
+//                 of a block's rows, or, for sequences of up to 32 rows, each every
+//                 third tile (a tile's chain from the product to the stored score is
+//                 then longer than the copy of a tile)
+// Blocks have as many rows as make an average sequence's blocks equal, 256 at most;
+// what the buffers of Q leave of the shared memory goes to the ring (decoding is
+// bound by the copy of K).
 #include <cmath>
 #include <type_traits>
 
@@ -28,15 +32,15 @@
 namespace dart {
 namespace {
 
-constexpr int kSumWarps = 8;
-constexpr int kThreads = 13 * 32;
+constexpr int kGroups = 3, kSumWarps = 4 * kGroups, kSumThreads = kSumWarps * 32;
+constexpr int kThreads = kSumThreads + 4 * 32;
 constexpr int kCtas = 152;
 constexpr int kTile = 128;                           // positions of a tile
 constexpr int kTileBytes = kTile * kColBytes;        // 64 columns of them
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxBlock = 256, kMinBlock = 64;       // rows of a block
-constexpr int kMaxStages = 12, kMaxSums = 8;
-constexpr int kSumThreads = kSumWarps * 32;
+constexpr int kMaxBlock = 256;                       // rows of a block
+constexpr int kMaxStages = 12, kMaxSums = 8, kMaxQ = 4;
+constexpr int kFewRows = 32;                         // of a sequence whose tiles are dealt to the groups
 
 struct WeightParams {
   const void* q;
@@ -54,20 +58,21 @@ struct WeightParams {
   long long cap;                   // positions that a sequence's pages and scores can hold
   int page, pages, box;
   int k_slot[3];
-  int block, stages, sums;         // rows of a block, K stages, S buffers (512 / block)
+  int block, columns;              // rows of a block, tensor memory columns from one S buffer to the next
+  int stages, sums, queries;       // K stages, S buffers, Q buffers
   uint32_t* err;
   long long wait_limit;
 };
 
 struct Shared {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
-  uint64_t q_full[2], q_empty[2];
+  uint64_t q_full[kMaxQ], q_empty[kMaxQ];
   uint64_t s_full[kMaxSums], s_empty[kMaxSums];
   uint64_t drain;
   long long total, lo, hi, base;   // this CTA's share of the list, and the first unit of sequence `first`
   long long scan[kThreads / 32];
-  alignas(16) float minus_l[2][kMaxBlock];   // -L of the rows in either Q buffer, -inf for a row that adds nothing
-  float part[kTile];               // the second half's sums
+  alignas(16) float minus_l[kMaxQ][kMaxBlock];   // -L of the rows in a Q buffer, -inf for a row that adds nothing
+  float part[kGroups - 1][kTile];  // the other groups' sums
   uint4 see[kMaxBlock];            // what each row sees of a tile
   uint32_t tmem;
   int first;
@@ -186,15 +191,41 @@ struct Tour {
       lin = 0;
     }
   }
-  __device__ __forceinline__ bool resident() const { return c.blocks <= 2; }
+  __device__ __forceinline__ bool resident(const WeightParams& P) const { return c.blocks <= P.queries; }
   // Whether block j is taken for tile t: causal blocks that see nothing of it are left out,
   // unless the blocks stay in their buffers.
   __device__ __forceinline__ bool uses(const WeightParams& P, int t, int j) const {
-    return resident() || block_end(P, c, j) > t * kTile;
+    return resident(P) || block_end(P, c, j) > t * kTile;
   }
 };
 
-__device__ __forceinline__ void sum_barrier() { asm volatile("bar.sync 1, %0;" :: "n"(kSumThreads) : "memory"); }
+// A place in a ring of n, and the parity of its round.
+struct Ring {
+  uint32_t at = 0, round = 0;
+  __device__ __forceinline__ void next(int n) {
+    if (++at == uint32_t(n)) {
+      at = 0;
+      round ^= 1;
+    }
+  }
+  __device__ __forceinline__ Ring plus(int k, int n) const {       // k <= n
+    Ring r = *this;
+    r.at += k;
+    if (r.at >= uint32_t(n)) {
+      r.at -= n;
+      r.round ^= 1;
+    }
+    return r;
+  }
+};
+
+template <int ID, int N>
+__device__ __forceinline__ void named_barrier(int offset = 0) {
+  asm volatile("bar.sync %0, %1;" :: "r"(ID + offset), "n"(N) : "memory");
+}
+__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
+  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(smem_u32(bar)), "r"(n) : "memory");
+}
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
@@ -202,8 +233,8 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
   constexpr int kStageBytes = DH * kTileBytes;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int q_half = P.block * kColBytes, q_bytes = DH * q_half;
-  unsigned char* sq = smem;                              // two buffers of P.block rows
-  unsigned char* ring = smem + 2 * q_bytes;
+  unsigned char* sq = smem;                              // the buffers of Q
+  unsigned char* ring = smem + P.queries * q_bytes;
   Shared* sh = reinterpret_cast<Shared*>(ring + P.stages * kStageBytes);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -212,8 +243,8 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
       mbar_init(&sh->k_full[i], 1);
       mbar_init(&sh->k_empty[i], 1);
     }
-    for (int i = 0; i < 2; ++i) {
-      mbar_init(&sh->q_full[i], 2);                      // warps 11, 12
+    for (int i = 0; i < P.queries; ++i) {
+      mbar_init(&sh->q_full[i], 1);
       mbar_init(&sh->q_empty[i], 1 + kSumWarps);         // the products, and those who read -L
     }
     for (int i = 0; i < P.sums; ++i) {
@@ -226,7 +257,7 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
     sh->first = 0;
     sh->base = 0;
   }
-  if (warp == 9) {
+  if (warp == 14) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(&sh->tmem)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -241,13 +272,14 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
   Tour w;
   bool ok = true;
 
-  if (warp == 8 || warp == 10) {
+  if (warp == 12 || warp == 13) {
     // -------------------------------------------------------------- K tiles
-    const uint32_t pid = warp == 8 ? 0u : 1u;
+    const uint32_t pid = uint32_t(warp - 12);
     uint32_t idx = 0;
+    Ring stage;
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
       const int32_t* table = P.table + (long long)w.b * P.table_stride;
-      for (int t = w.t0; t < w.t1 && ok; ++t, ++idx) {
+      for (int t = w.t0; t < w.t1 && ok; ++t, ++idx, stage.next(P.stages)) {
         if ((idx & 1u) != pid) continue;
         const int p0 = t * kTile, boxes = (min(w.c.S - p0, kTile) + P.box - 1) / P.box;
         const int at = p0 + (lane / DH) * P.box;
@@ -260,16 +292,15 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
             page = P.pages;                  // out of the map's range: the box arrives as zeros
           }
         }
-        const uint32_t stage = idx % P.stages;
-        ok = wait_warp(&sh->k_empty[stage], ((idx / P.stages) & 1u) ^ 1u, sh, limit);
+        ok = wait_warp(&sh->k_empty[stage.at], stage.round ^ 1u, sh, limit);
         if (!ok) break;
-        if (lane == 0) mbar_expect_tx(&sh->k_full[stage], uint32_t(boxes * DH * P.box * kColBytes));
+        if (lane == 0) mbar_expect_tx(&sh->k_full[stage.at], uint32_t(boxes * DH * P.box * kColBytes));
         __syncwarp();
         if (mine) {
           const int half = lane % DH, row = at - P.by_page.div(at) * P.page;
           auto pick = [&](int i) { return P.k_slot[i] == 0 ? w.h : P.k_slot[i] == 1 ? row : page; };
-          tma_box(ring + stage * kStageBytes + half * kTileBytes + (lane / DH) * P.box * kColBytes, &kmap, 64 * half,
-                  pick(0), pick(1), pick(2), &sh->k_full[stage]);
+          tma_box(ring + stage.at * kStageBytes + half * kTileBytes + (lane / DH) * P.box * kColBytes, &kmap, 64 * half,
+                  pick(0), pick(1), pick(2), &sh->k_full[stage.at]);
         }
       }
     }
@@ -277,67 +308,65 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
     for (uint32_t i = idx > uint32_t(P.stages) ? idx - P.stages : 0; i < idx; ++i)
       if ((i & 1u) == pid) mbar_wait_bounded(&sh->k_full[i % P.stages], (i / P.stages) & 1u, kDrainLimit);
     __syncwarp();
-  } else if (warp == 9) {
+  } else if (warp == 14) {
     // ---------------------------------------------------------- tensor unit
     constexpr uint32_t type = kTypeCode<T>;
     const uint32_t id0 = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 4) << 24);
     const uint64_t q_desc = smem_desc(smem_u32(sq), 16), k_desc = smem_desc(smem_u32(ring), 16);
     const int k_steps = (P.D + 15) / 16;
-    uint32_t k_idx = 0, use = 0, load = 0;       // tiles, products and Q loads so far
+    Ring stage, s, load;
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
-      const bool stay = w.resident();
-      for (int t = w.t0; t < w.t1 && ok; ++t, ++k_idx) {
-        const uint32_t stage = k_idx % P.stages;
-        if (!(ok = wait_warp(&sh->k_full[stage], (k_idx / P.stages) & 1u, sh, limit))) break;
+      const bool stay = w.resident(P);
+      for (int t = w.t0; t < w.t1 && ok; ++t, stage.next(P.stages)) {
+        if (!(ok = wait_warp(&sh->k_full[stage.at], stage.round, sh, limit))) break;
         for (int j = 0; j < w.c.blocks; ++j) {
           if (!w.uses(P, t, j)) continue;
-          const uint32_t at = stay ? load + j : load;         // the Q load that this block came with
-          if (!stay || t == w.t0) ok = wait_warp(&sh->q_full[at & 1u], (at >> 1) & 1u, sh, limit);
-          const uint32_t s = use % P.sums;
-          ok = ok && wait_warp(&sh->s_empty[s], ((use / P.sums) & 1u) ^ 1u, sh, limit);
+          const Ring at = stay ? load.plus(j, P.queries) : load;       // the Q load that this block came with
+          if (!stay || t == w.t0) ok = wait_warp(&sh->q_full[at.at], at.round, sh, limit);
+          ok = ok && wait_warp(&sh->s_empty[s.at], s.round ^ 1u, sh, limit);
           if (!ok) break;
           tc_after();
           const int rows = min(w.c.rows - j * P.block, P.block);
           const uint32_t id = id0 | (uint32_t((rows + 15) / 16 * 2) << 17);
           if (elect()) {
-            const uint64_t kd = k_desc + uint64_t(stage * (kStageBytes >> 4));
-            const uint64_t qd = q_desc + uint64_t((at & 1u) * (q_bytes >> 4));
+            const uint64_t kd = k_desc + uint64_t(stage.at * (kStageBytes >> 4));
+            const uint64_t qd = q_desc + uint64_t(at.at * (q_bytes >> 4));
 #pragma unroll
             for (int k = 0; k < 4 * DH; ++k)
               if (k < k_steps)
-                mma_ss(tmem + s * P.block, kd + (((k >> 2) * kTileBytes + (k & 3) * 32) >> 4),
+                mma_ss(tmem + s.at * P.columns, kd + (((k >> 2) * kTileBytes + (k & 3) * 32) >> 4),
                        qd + (((k >> 2) * q_half + (k & 3) * 32) >> 4), id, k > 0);
-            tc_commit(&sh->s_full[s]);
-            if (!stay || t == w.t1 - 1) tc_commit(&sh->q_empty[at & 1u]);
+            tc_commit(&sh->s_full[s.at]);
+            if (!stay || t == w.t1 - 1) tc_commit(&sh->q_empty[at.at]);
           }
           __syncwarp();
-          ++use;
-          if (!stay) ++load;
+          s.next(P.sums);
+          if (!stay) load.next(P.queries);
         }
-        if (ok && elect()) tc_commit(&sh->k_empty[stage]);
+        if (ok && elect()) tc_commit(&sh->k_empty[stage.at]);
         __syncwarp();
       }
-      if (stay) load += w.c.blocks;
+      if (stay) load = load.plus(w.c.blocks, P.queries);
     }
     // every product has ended before the tensor memory is given back
     if (elect()) tc_commit(&sh->drain);
     mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
     __syncwarp();
-  } else if (warp >= 11) {
+  } else if (warp == 15) {
     // ------------------------------------------------------------ row blocks
     constexpr int kChunks = 8 * DH, kPer = 32 / kChunks;      // 16-byte chunks a row, rows a step
     const int chunk = lane % kChunks, sub = lane / kChunks;
     const bool inside = 8 * chunk < P.D;
-    uint32_t load = 0;
+    Ring load;
     auto bring = [&](int j) {
-      const uint32_t buf = load & 1u;
-      ok = wait_warp(&sh->q_empty[buf], ((load >> 1) & 1u) ^ 1u, sh, limit);
+      const uint32_t buf = load.at;
+      ok = wait_warp(&sh->q_empty[buf], load.round ^ 1u, sh, limit);
       if (!ok) return;
       const int rows = min(w.c.rows - j * P.block, P.block), padded = (rows + 15) / 16 * 16;
       const T* src = static_cast<const T*>(P.q) + (inside ? 8 * chunk : 0);
       unsigned char* dst = sq + buf * q_bytes + (chunk >> 3) * q_half;
       // groups of 32 rows in turn; lane r finds row r's place and sum for all
-      for (int r0 = (warp - 11) * 32; r0 < padded; r0 += 64) {
+      for (int r0 = 0; r0 < padded; r0 += 32) {
         const int g = j * P.block + min(r0 + lane, rows - 1);
         const int token = P.by_group.div(g), head = w.h * P.G + g - token * P.G;
         const long long at = (long long)(w.c.start + token) * P.q_ts + (long long)head * P.q_hs;
@@ -360,10 +389,10 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
       fence_async();
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh->q_full[buf]);
-      ++load;
+      load.next(P.queries);
     };
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
-      if (w.resident()) {
+      if (w.resident(P)) {
         for (int j = 0; j < w.c.blocks && ok; ++j) bring(j);
       } else {
         for (int t = w.t0; t < w.t1 && ok; ++t)
@@ -374,35 +403,53 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
     asm volatile("cp.async.wait_all;" ::: "memory");
   } else {
     // ------------------------------------------------------------------ sums
-    // The schedule alone decides which barriers of the two halves are met, so a wait
-    // that ran out cannot leave a warp behind: ok only turns the work off.
-    const int half = warp >> 2, mine = (warp & 3) * 32 + lane;      // lane of tensor memory: the position
+    // The schedule alone decides which barriers the groups meet at, so a wait that ran
+    // out cannot leave a warp behind: ok only turns the work off.
+    const int group = warp >> 2, mine = (warp & 3) * 32 + lane;     // lane of tensor memory: the position
     const uint32_t lane_base = uint32_t(warp & 3) << 21;
-    uint32_t use = 0, load = 0;
+    Ring s, load;
+    int turn = 0;                                  // the group whose turn the next tile of a short sequence is
     const uint64_t c2 = pair(P.c, P.c);
     for (bool more = w.begin(P, sh); more; more = w.next(P)) {
-      const bool stay = w.resident();
+      const bool stay = w.resident(P), few = w.c.rows <= kFewRows && w.c.blocks == 1;
       float* row = P.scores + w.b * P.s_seq + w.h * P.s_head;
       const int tree = w.c.len + w.c.lead;
-      const bool both = w.c.rows > 32;             // the second half has rows in some block
+      if (stay)                                    // -L is there; by all groups, so that none runs ahead of the others
+        for (int j = 0; j < w.c.blocks; ++j) {
+          const Ring at = load.plus(j, P.queries);
+          ok = ok && wait_warp(&sh->q_full[at.at], at.round, sh, limit);
+        }
       for (int t = w.t0; t < w.t1; ++t) {
         const int p0 = t * kTile, p = p0 + mine, end = min(p0 + kTile, w.c.S);
+        if (few) {
+          const bool here = turn == group;
+          turn = (turn + 1) % kGroups;
+          if (!here) {
+            s.next(P.sums);
+            continue;
+          }
+        }
+        const bool writes = (few || group == 0) && p < w.c.S;
         float old = 0.f;
-        if (half == 0 && p < w.c.S) old = row[p];
+        if (writes) old = row[p];
         uint64_t sum = 0ull;
         for (int j = 0; j < w.c.blocks; ++j) {
           if (!w.uses(P, t, j)) continue;
-          const uint32_t at = stay ? load + j : load, buf = at & 1u;
+          const Ring at = stay ? load.plus(j, P.queries) : load;
           const int rows = min(w.c.rows - j * P.block, P.block), cols = (rows + 15) / 16 * 16;
           const int first = P.by_group.div(j * P.block);
           // some row of the block does not see some position of the tile
           const bool masked = min(w.c.len + min(first + 1, w.c.lead), w.c.S) < end;
+          uint4* see_at = sh->see + (few ? group * kFewRows : 0);
           if (masked) {
-            sum_barrier();                         // the words of the masked block before have been read
-            if (tid < P.block) {
+            // the words of the masked block before have been read
+            if (few) named_barrier<2, 128>(group);
+            else named_barrier<1, kSumThreads>();
+            const int r = few ? mine : tid;
+            if (r < (few ? kFewRows : P.block)) {
               uint4 see = make_uint4(0, 0, 0, 0);
-              if (tid < rows) {
-                const int token = P.by_group.div(j * P.block + tid);
+              if (r < rows) {
+                const int token = P.by_group.div(j * P.block + r);
                 const int plain = min(w.c.len + min(token + 1, w.c.lead), w.c.S);
                 const int nodes = token >= w.c.lead ? min(min(P.N, w.c.n - w.c.lead), w.c.S - tree) : 0;
                 const uint32_t* bits = P.mask + ((long long)w.b * P.N + (token - w.c.lead)) * P.MW;
@@ -418,89 +465,108 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
                 }
                 see = make_uint4(out[0], out[1], out[2], out[3]);
               }
-              sh->see[tid] = see;
+              see_at[r] = see;
             }
-            sum_barrier();
+            if (few) named_barrier<2, 128>(group);
+            else named_barrier<1, kSumThreads>();
           }
-          // the first half's columns and the second's, in steps of 16
-          const int cut = cols <= 32 ? cols : (cols / 2 + 15) / 16 * 16;
-          const int c0 = half == 0 ? 0 : cut, c1 = half == 0 ? cut : cols;
-          const uint32_t s = use % P.sums;
-          if (!stay || t == w.t0) ok = ok && wait_warp(&sh->q_full[buf], (at >> 1) & 1u, sh, limit);   // -L is there
-          ok = ok && wait_warp(&sh->s_full[s], (use / P.sums) & 1u, sh, limit);
-          if (ok) {
+          // this group's columns, in steps of 16
+          const int steps = cols >> 4;
+          const int c0 = few ? 0 : (steps * group / kGroups) << 4, c1 = few ? cols : (steps * (group + 1) / kGroups) << 4;
+          if (!stay) ok = ok && wait_warp(&sh->q_full[at.at], at.round, sh, limit);
+          ok = ok && wait_warp(&sh->s_full[s.at], s.round, sh, limit);
+          if (ok && c0 < c1) {
             tc_after();
-            const uint32_t from = tmem + lane_base + s * P.block;
-            const float* l = sh->minus_l[buf];
-            const uint32_t* words = reinterpret_cast<const uint32_t*>(sh->see) + (warp & 3);
-            auto add_up = [&](auto by_bits, auto careful) {
-              uint64_t part[2] = {0ull, 0ull};
-              auto add = [&](const float* x, int col) {
-                const ulonglong2* l4 = reinterpret_cast<const ulonglong2*>(l + col);
+            const uint32_t from = tmem + lane_base + s.at * P.columns;
+            const float* l = sh->minus_l[at.at];
+            const uint32_t* words = reinterpret_cast<const uint32_t*>(see_at) + (warp & 3);
+            uint64_t part[2] = {0ull, 0ull};
+            auto fast = [&](const float* x, int col) {
+              const ulonglong2* l4 = reinterpret_cast<const ulonglong2*>(l + col);
 #pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                  const uint64_t lk = (k & 2) ? l4[k >> 2].y : l4[k >> 2].x;
-                  const uint64_t y = fma2(pair(x[k], x[k + 1]), c2, lk);
-                  float a = ex2_approx(low(y)), b = ex2_approx(high(y));
-                  if (decltype(by_bits)::value) {
-                    a = (words[4 * (col + k)] >> lane) & 1u ? a : 0.f;
-                    b = (words[4 * (col + k) + 4] >> lane) & 1u ? b : 0.f;
-                  }
-                  if (decltype(careful)::value) {
-                    a = low(lk) == -INFINITY ? 0.f : a;
-                    b = high(lk) == -INFINITY ? 0.f : b;
-                  }
-                  part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], pair(a, b));
-                }
-              };
+              for (int k = 0; k < 16; k += 4) {
+                const ulonglong2 lk = l4[k >> 2];
+                const uint64_t y0 = fma2(pair(x[k], x[k + 1]), c2, lk.x), y1 = fma2(pair(x[k + 2], x[k + 3]), c2, lk.y);
+                part[0] = add2(part[0], pair(ex2_approx(low(y0)), ex2_approx(high(y0))));
+                part[1] = add2(part[1], pair(ex2_approx(low(y1)), ex2_approx(high(y1))));
+              }
+            };
+            // what a row does not see and a row that adds nothing are left out whatever the product is
+            auto slow = [&](const float* x, int col) {
+#pragma unroll
+              for (int k = 0; k < 16; k += 2) {
+                const float l0 = l[col + k], l1 = l[col + k + 1];
+                const bool on0 = l0 > -INFINITY && (!masked || ((words[4 * (col + k)] >> lane) & 1u));
+                const bool on1 = l1 > -INFINITY && (!masked || ((words[4 * (col + k) + 4] >> lane) & 1u));
+                part[0] = add2(part[0], pair(on0 ? ex2_approx(fmaf(x[k], P.c, l0)) : 0.f,
+                                             on1 ? ex2_approx(fmaf(x[k + 1], P.c, l1)) : 0.f));
+              }
+            };
+            auto all_fast = [&]() {          // the next columns are on their way while these are added up
+              float x[2][16];
+              tmem_ld16(from + c0, x[0]);
               for (int col = c0; col < c1; col += 32) {
-                float x[32];
-                tmem_ld16(from + col, x);
-                const bool two = col + 16 < c1;
-                if (two) tmem_ld16(from + col + 16, x + 16);
-                loaded<16>(x);
-                add(x, col);
-                if (two) {
-                  loaded<16>(x + 16);
-                  add(x + 16, col + 16);
+                loaded<16>(x[0]);
+                if (col + 16 < c1) tmem_ld16(from + col + 16, x[1]);
+                fast(x[0], col);
+                if (col + 16 < c1) {
+                  loaded<16>(x[1]);
+                  if (col + 32 < c1) tmem_ld16(from + col + 32, x[0]);
+                  fast(x[1], col + 16);
                 }
               }
-              return add2(part[0], part[1]);
             };
-            uint64_t part = masked ? add_up(std::true_type{}, std::false_type{}) : add_up(std::false_type{}, std::false_type{});
-            // A row that adds nothing is zeros, and 0 * inf is NaN: where that may have
-            // happened the block is added up again without those rows.
-            const float both_halves = low(part) + high(part);
-            if (__any_sync(kFull, both_halves != both_halves))
-              part = masked ? add_up(std::true_type{}, std::true_type{}) : add_up(std::false_type{}, std::true_type{});
-            sum = add2(sum, part);
+            auto all_slow = [&]() {
+              part[0] = part[1] = 0ull;
+#pragma unroll 1
+              for (int col = c0; col < c1; col += 16) {
+                float x[16];
+                tmem_ld16(from + col, x);
+                loaded<16>(x);
+                slow(x, col);
+              }
+            };
+            bool again = masked;
+            if (!masked) {
+              all_fast();
+              // a row that adds nothing is zeros, and 0 * inf is NaN: then once more without those rows
+              const uint64_t both = add2(part[0], part[1]);
+              again = __any_sync(kFull, low(both) + high(both) != low(both) + high(both));
+            }
+            if (again) all_slow();
+            sum = add2(sum, add2(part[0], part[1]));
             tc_before();
           }
           __syncwarp();
-          if (lane == 0) {
-            mbar_arrive(&sh->s_empty[s]);
-            if (!stay || t == w.t1 - 1) mbar_arrive(&sh->q_empty[buf]);
-          }
-          ++use;
-          if (!stay) ++load;
+          if (lane == 0) mbar_arrive_n(&sh->s_empty[s.at], few ? kGroups : 1);
+          if (!stay && lane == 0) mbar_arrive(&sh->q_empty[at.at]);
+          s.next(P.sums);
+          if (!stay) load.next(P.queries);
         }
         float gathered = low(sum) + high(sum);
-        if (both) {
-          if (half == 1) sh->part[mine] = gathered;
-          sum_barrier();
-          if (half == 0) gathered += sh->part[mine];
-          sum_barrier();                           // read before the next tile's are written
+        if (!few) {
+          if (group > 0) sh->part[group - 1][mine] = gathered;
+          named_barrier<1, kSumThreads>();
+          if (group == 0)
+#pragma unroll
+            for (int i = 0; i < kGroups - 1; ++i) gathered += sh->part[i][mine];
+          named_barrier<1, kSumThreads>();         // read before the next tile's are written
         }
-        if (half == 0 && p < w.c.S && ok) row[p] = old + gathered;
+        if (writes && ok) row[p] = old + gathered;
       }
-      if (stay) load += w.c.blocks;
+      if (stay) {
+        __syncwarp();
+        if (lane == 0)
+          for (int j = 0; j < w.c.blocks; ++j) mbar_arrive(&sh->q_empty[load.plus(j, P.queries).at]);
+        load = load.plus(w.c.blocks, P.queries);
+      }
     }
   }
 
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 9) {
+  if (warp == 14) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
     if (lane == 0 && sh->dead) set_dev_error(P.err, DART_DEVERR_WAIT_TIMEOUT);
   }
@@ -509,10 +575,16 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
 template <typename T, int DH>
 cudaError_t launch(WeightParams& P, const CUtensorMap& km, cudaStream_t s) {
   constexpr int kStageBytes = DH * kTileBytes;
-  const int room = 227 * 1024 - int(sizeof(Shared)) - 2 * P.block * DH * kColBytes;
-  P.stages = room / kStageBytes < kMaxStages ? room / kStageBytes : kMaxStages;
-  P.sums = int(kTmemCols) / P.block;
-  const int smem = 2 * P.block * DH * kColBytes + P.stages * kStageBytes + int(sizeof(Shared));
+  // Three stages of K at least (two for the largest blocks), then buffers of Q so that
+  // the next head's blocks can come while this one's are used, then stages again.
+  const int room = 227 * 1024 - int(sizeof(Shared)), q = P.block * DH * kColBytes;
+  P.queries = (room - 3 * kStageBytes) / q;
+  P.queries = P.queries < 2 ? 2 : P.queries > kMaxQ ? kMaxQ : P.queries;
+  P.stages = (room - P.queries * q) / kStageBytes;
+  P.stages = P.stages < kMaxStages ? P.stages : kMaxStages;
+  P.columns = (P.block + 31) / 32 * 32;
+  P.sums = int(kTmemCols) / P.columns < kMaxSums ? int(kTmemCols) / P.columns : kMaxSums;
+  const int smem = P.queries * q + P.stages * kStageBytes + int(sizeof(Shared));
   const cudaError_t e =
       settled(cudaFuncSetAttribute(weights_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if (e != cudaSuccess) return e;
@@ -559,8 +631,9 @@ extern "C" int dart_attention_weights(const void* q, int64_t q_token_stride, int
   P.cap = (long long)c.table_width * c.page;
   if (P.cap > scores_width) P.cap = scores_width;
   P.page = c.page; P.pages = c.pages; P.box = gcd(c.page, kTile);
-  // few rows a sequence on average: small blocks, and the ring takes the memory
-  P.block = (long long)T * P.G <= (long long)kMinBlock * B ? kMinBlock : kMaxBlock;
+  // an average sequence's rows in equal blocks
+  const long long rows = ((long long)T * P.G + B - 1) / B, blocks = (rows + kMaxBlock - 1) / kMaxBlock;
+  P.block = int(((rows + blocks - 1) / blocks + 15) / 16 * 16);
   P.err = device_err;
   P.wait_limit = rows_wait_limit();
   CUtensorMap km;

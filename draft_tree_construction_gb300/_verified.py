@@ -10,8 +10,8 @@ import ctypes as C
 
 from . import _steps
 from . import DartError, _check, _check_error_word, _check_tensor, _mask_dtypes, _row_stride, _torch, lib
-from ._steps import (_at, _Cache, _cache, _check_inner, _codes, _enter, _heads, _leave, _one_device, _sequences,
-                     _stream)
+from ._steps import (_at, _Cache, _cache, _check_inner, _codes, _enter, _heads, _leave, _one_device, _output,
+                     _sequences, _stream)
 
 
 def declare(L):
@@ -221,7 +221,7 @@ def attention_weights(q, k_cache, pages, lengths, starts, lse, scores, *, mask=N
     if q.dim() != 3:
         raise DartError("q must be [T, q_heads, dim]")
     T, Hq, dim = q.shape
-    q0, q1 = _heads(q, "q", T, Hq, c.dim, k_cache.dtype)
+    q0, q1 = _output(q, "q", T, Hq, c.dim, k_cache.dtype)         # copied in boxes, which an expanded tensor has not
     if Hq < 1 or Hq % c.heads:
         raise DartError(f"{Hq} query heads do not share {c.heads} key heads evenly")
     _check_tensor(lse, "lse", torch.float32, (T, Hq))

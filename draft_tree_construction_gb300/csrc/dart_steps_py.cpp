@@ -460,7 +460,7 @@ PyObject* weights(PyObject*, PyObject* const* args, Py_ssize_t count) {
   Heads hq;
   int64_t s_seq, s_head;
   if (B < 0 || T > INT_MAX || q_heads > INT_MAX || !cache_of(k_cache, k_cache, pages, B, &c) ||
-      !hq.fit(*q, T, q_heads, c.dim, k_cache->scalar_type()) || q_heads % c.heads != 0 ||
+      !hq.fit(*q, T, q_heads, c.dim, k_cache->scalar_type(), true) || q_heads % c.heads != 0 ||
       lse->scalar_type() != at::kFloat || lse->dim() != 2 || lse->size(0) != T || lse->size(1) != q_heads ||
       !lse->is_contiguous() || !scores_of(scores, B, c.heads, &s_seq, &s_head) || !error_word(err))
     Py_RETURN_NONE;

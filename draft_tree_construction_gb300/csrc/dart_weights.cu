@@ -15,13 +15,14 @@
 // as its sequence has.  Within a CTA:
 //   warps 12, 13  copy K tiles by TMA into a ring of swizzled stages, in turn
 //   warp 14       issues the tcgen05 products, one row block after the other
-//   warp 15       copies the row blocks of Q (a sequence whose blocks fit in the
-//                 buffers keeps them there for all of its tiles)
+//   warp 15       copies the row blocks of Q by TMA, a box per 64 columns (a sequence
+//                 whose blocks fit in the buffers keeps them there for all of its tiles)
 //   warps 0-11    add up the exponentials: three groups of four warps, each a third
 //                 of a block's rows, or, for sequences of up to 32 rows, each every
 //                 third tile (a tile's chain from the product to the stored score is
 //                 then longer than the copy of a tile)
-// Blocks have as many rows as make an average sequence's blocks equal, 256 at most;
+// Blocks are whole tokens, as many as make an average sequence's blocks equal, 256 rows
+// at most (256 of a token's queries where a key head has more);
 // what the buffers of Q leave of the shared memory goes to the ring (decoding is
 // bound by the copy of K).
 #include <cmath>
@@ -48,7 +49,7 @@ struct WeightParams {
   float* scores;
   long long q_ts, q_hs, s_seq, s_head;
   int Hq, Hkv, G, D, T, B, N, MW;
-  FastDiv by_group, by_page;
+  FastDiv by_page;
   const int32_t* lengths;
   const int32_t* starts;
   const uint32_t* mask;
@@ -58,7 +59,10 @@ struct WeightParams {
   long long cap;                   // positions that a sequence's pages and scores can hold
   int page, pages, box;
   int k_slot[3];
-  int block, columns;              // rows of a block, tensor memory columns from one S buffer to the next
+  int tokens, queries_of;          // of a block: its tokens, the queries of each
+  int parts;                       // blocks that a token takes (more than one only with one token a block)
+  FastDiv by_part, by_queries;
+  int block, columns;              // rows of a buffer, tensor memory columns from one S buffer to the next
   int stages, sums, queries;       // K stages, S buffers, Q buffers
   uint32_t* err;
   long long wait_limit;
@@ -80,7 +84,7 @@ struct Shared {
 };
 
 struct Seq {
-  int start, n, len, lead, S, rows, blocks, tiles;
+  int start, n, len, lead, S, blocks, tiles;
 };
 __device__ __forceinline__ Seq load_seq(const WeightParams& P, int b) {
   Seq c;
@@ -90,18 +94,37 @@ __device__ __forceinline__ Seq load_seq(const WeightParams& P, int b) {
   c.len = int(min((long long)max(P.lengths[b], 0), P.cap));
   c.S = int(min((long long)c.len + c.n, P.cap));
   c.lead = max(c.n - P.N, 0);
-  c.rows = c.n * P.G;
-  c.blocks = int((unsigned(c.rows) + unsigned(P.block) - 1) / unsigned(P.block));
+  c.blocks = P.parts > 1 ? c.n * P.parts : (c.n + P.tokens - 1) / P.tokens;
   c.tiles = c.blocks > 0 ? (c.S + kTile - 1) / kTile : 0;
   return c;
 }
 __device__ __forceinline__ long long seq_cost(const WeightParams& P, const Seq& c) {
   return (long long)P.Hkv * c.tiles * c.blocks;
 }
+// A block of rows: row r is query q0 + r % queries of token t0 + r / queries.
+struct Block {
+  int t0, q0, tokens, queries, rows;
+};
+__device__ __forceinline__ Block block_of(const WeightParams& P, const Seq& c, int j) {
+  Block k;
+  if (P.parts == 1) {
+    k.t0 = j * P.tokens;
+    k.q0 = 0;
+    k.tokens = min(P.tokens, c.n - k.t0);
+    k.queries = P.G;
+  } else {
+    k.t0 = P.by_part.div(j);
+    k.q0 = (j - k.t0 * P.parts) * P.queries_of;
+    k.tokens = 1;
+    k.queries = min(P.queries_of, P.G - k.q0);
+  }
+  k.rows = k.tokens * k.queries;
+  return k;
+}
 // Positions that some row of block j sees end here.
 __device__ __forceinline__ int block_end(const WeightParams& P, const Seq& c, int j) {
-  const int r1 = min(c.rows - j * P.block, P.block) + j * P.block;
-  const int last = P.by_group.div(r1 - 1);
+  const Block k = block_of(P, c, j);
+  const int last = k.t0 + k.tokens - 1;
   return last >= c.lead ? c.S : min(c.len + last + 1, c.S);
 }
 
@@ -229,7 +252,7 @@ __device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
-weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
+weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
   constexpr int kStageBytes = DH * kTileBytes;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int q_half = P.block * kColBytes, q_bytes = DH * q_half;
@@ -326,7 +349,7 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
           ok = ok && wait_warp(&sh->s_empty[s.at], s.round ^ 1u, sh, limit);
           if (!ok) break;
           tc_after();
-          const int rows = min(w.c.rows - j * P.block, P.block);
+          const int rows = block_of(P, w.c, j).rows;
           const uint32_t id = id0 | (uint32_t((rows + 15) / 16 * 2) << 17);
           if (elect()) {
             const uint64_t kd = k_desc + uint64_t(stage.at * (kStageBytes >> 4));
@@ -354,42 +377,36 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
     __syncwarp();
   } else if (warp == 15) {
     // ------------------------------------------------------------ row blocks
-    constexpr int kChunks = 8 * DH, kPer = 32 / kChunks;      // 16-byte chunks a row, rows a step
-    const int chunk = lane % kChunks, sub = lane / kChunks;
-    const bool inside = 8 * chunk < P.D;
+    constexpr int kPer = kMaxBlock / 32;
     Ring load;
+    uint32_t loads = 0;
     auto bring = [&](int j) {
       const uint32_t buf = load.at;
+      const Block k = block_of(P, w.c, j);
+      // the rows' sums are on their way while the buffer is waited for
+      float l[kPer];
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int r = min(32 * i + lane, k.rows - 1);
+        const int token = P.parts == 1 ? P.by_queries.div(r) : 0, q = k.q0 + r - token * k.queries;
+        l[i] = 32 * i < k.rows ? P.lse[(long long)(w.c.start + k.t0 + token) * P.Hq + w.h * P.G + q] : 0.f;
+      }
       ok = wait_warp(&sh->q_empty[buf], load.round ^ 1u, sh, limit);
       if (!ok) return;
-      const int rows = min(w.c.rows - j * P.block, P.block), padded = (rows + 15) / 16 * 16;
-      const T* src = static_cast<const T*>(P.q) + (inside ? 8 * chunk : 0);
-      unsigned char* dst = sq + buf * q_bytes + (chunk >> 3) * q_half;
-      // groups of 32 rows in turn; lane r finds row r's place and sum for all
-      for (int r0 = 0; r0 < padded; r0 += 32) {
-        const int g = j * P.block + min(r0 + lane, rows - 1);
-        const int token = P.by_group.div(g), head = w.h * P.G + g - token * P.G;
-        const long long at = (long long)(w.c.start + token) * P.q_ts + (long long)head * P.q_hs;
-        float l = P.lse[(long long)(w.c.start + token) * P.Hq + head];
-        const bool adds = r0 + lane < rows && fabsf(l) < INFINITY;
-        if (r0 + lane < padded) sh->minus_l[buf][r0 + lane] = adds ? -l * 1.44269504088896341f : -INFINITY;
-        const uint32_t on = __ballot_sync(kFull, adds);
-#pragma unroll 4
-        for (int u = 0; u < 32 / kPer; ++u) {
-          const int r = u * kPer + sub;
-          const long long from = __shfl_sync(kFull, at, r);
-          // a row that adds nothing is zeros, and its exponent 0 - inf
-          if (r0 + r < padded)
-            cp_async16_or_zero(dst + (r0 + r) * kColBytes + (((chunk & 7) ^ (r & 7)) << 4), src + from,
-                               inside && ((on >> r) & 1u));
+#pragma unroll
+      for (int i = 0; i < kPer; ++i)
+        if (32 * i + lane < P.block) {
+          const bool adds = 32 * i + lane < k.rows && fabsf(l[i]) < INFINITY;
+          sh->minus_l[buf][32 * i + lane] = adds ? -l[i] * 1.44269504088896341f : -INFINITY;
         }
-      }
-      cp_async_commit();
-      cp_async_wait<0>();
-      fence_async();
       __syncwarp();
-      if (lane == 0) mbar_arrive(&sh->q_full[buf]);
+      // whole boxes: what lies behind the block's rows adds nothing
+      if (lane == 0) mbar_expect_tx(&sh->q_full[buf], uint32_t(DH * P.tokens * P.queries_of * kColBytes));
+      __syncwarp();
+      if (lane < DH)
+        tma_box(sq + buf * q_bytes + lane * q_half, &qmap, 64 * lane, w.h * P.G + k.q0, w.c.start + k.t0, 0, &sh->q_full[buf]);
       load.next(P.queries);
+      ++loads;
     };
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
       if (w.resident(P)) {
@@ -400,7 +417,9 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
             if (w.uses(P, t, j)) bring(j);
       }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
+    for (uint32_t i = loads > uint32_t(P.queries) ? loads - P.queries : 0; i < loads; ++i)
+      mbar_wait_bounded(&sh->q_full[i % P.queries], (i / P.queries) & 1u, kDrainLimit);
+    __syncwarp();
   } else {
     // ------------------------------------------------------------------ sums
     // The schedule alone decides which barriers the groups meet at, so a wait that ran
@@ -411,7 +430,7 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
     int turn = 0;                                  // the group whose turn the next tile of a short sequence is
     const uint64_t c2 = pair(P.c, P.c);
     for (bool more = w.begin(P, sh); more; more = w.next(P)) {
-      const bool stay = w.resident(P), few = w.c.rows <= kFewRows && w.c.blocks == 1;
+      const bool stay = w.resident(P), few = w.c.blocks == 1 && w.c.n * P.G <= kFewRows;
       float* row = P.scores + w.b * P.s_seq + w.h * P.s_head;
       const int tree = w.c.len + w.c.lead;
       if (stay)                                    // -L is there; by all groups, so that none runs ahead of the others
@@ -436,10 +455,10 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
         for (int j = 0; j < w.c.blocks; ++j) {
           if (!w.uses(P, t, j)) continue;
           const Ring at = stay ? load.plus(j, P.queries) : load;
-          const int rows = min(w.c.rows - j * P.block, P.block), cols = (rows + 15) / 16 * 16;
-          const int first = P.by_group.div(j * P.block);
+          const Block k = block_of(P, w.c, j);
+          const int cols = (k.rows + 15) / 16 * 16;
           // some row of the block does not see some position of the tile
-          const bool masked = min(w.c.len + min(first + 1, w.c.lead), w.c.S) < end;
+          const bool masked = min(w.c.len + min(k.t0 + 1, w.c.lead), w.c.S) < end;
           uint4* see_at = sh->see + (few ? group * kFewRows : 0);
           if (masked) {
             // the words of the masked block before have been read
@@ -448,8 +467,8 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
             const int r = few ? mine : tid;
             if (r < (few ? kFewRows : P.block)) {
               uint4 see = make_uint4(0, 0, 0, 0);
-              if (r < rows) {
-                const int token = P.by_group.div(j * P.block + r);
+              if (r < k.rows) {
+                const int token = k.t0 + (P.parts == 1 ? P.by_queries.div(r) : 0);
                 const int plain = min(w.c.len + min(token + 1, w.c.lead), w.c.S);
                 const int nodes = token >= w.c.lead ? min(min(P.N, w.c.n - w.c.lead), w.c.S - tree) : 0;
                 const uint32_t* bits = P.mask + ((long long)w.b * P.N + (token - w.c.lead)) * P.MW;
@@ -491,15 +510,19 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
                 part[1] = add2(part[1], pair(ex2_approx(low(y1)), ex2_approx(high(y1))));
               }
             };
-            // what a row does not see and a row that adds nothing are left out whatever the product is
+            // what a row does not see is left out whatever the product is, and a row that adds nothing
             auto slow = [&](const float* x, int col) {
+              const ulonglong2* l4 = reinterpret_cast<const ulonglong2*>(l + col);
 #pragma unroll
               for (int k = 0; k < 16; k += 2) {
-                const float l0 = l[col + k], l1 = l[col + k + 1];
-                const bool on0 = l0 > -INFINITY && (!masked || ((words[4 * (col + k)] >> lane) & 1u));
-                const bool on1 = l1 > -INFINITY && (!masked || ((words[4 * (col + k) + 4] >> lane) & 1u));
-                part[0] = add2(part[0], pair(on0 ? ex2_approx(fmaf(x[k], P.c, l0)) : 0.f,
-                                             on1 ? ex2_approx(fmaf(x[k + 1], P.c, l1)) : 0.f));
+                const uint64_t lk = (k & 2) ? l4[k >> 2].y : l4[k >> 2].x;
+                const uint64_t y = fma2(pair(x[k], x[k + 1]), c2, lk);
+                bool on0 = low(lk) > -INFINITY, on1 = high(lk) > -INFINITY;
+                if (masked) {
+                  on0 = on0 && ((words[4 * (col + k)] >> lane) & 1u);
+                  on1 = on1 && ((words[4 * (col + k) + 4] >> lane) & 1u);
+                }
+                part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], pair(on0 ? ex2_approx(low(y)) : 0.f, on1 ? ex2_approx(high(y)) : 0.f));
               }
             };
             auto all_fast = [&]() {          // the next columns are on their way while these are added up
@@ -572,8 +595,24 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap) {
   }
 }
 
+// The queries as a map (columns, query, token, one) with a box of a block's queries and tokens by 64 columns.
+bool query_map(const WeightParams& P, const dart_cache_t& c, CUtensorMap* map) {
+  const EncodeFn encode = tensor_map_encoder();
+  if (!encode) return false;
+  // a dimension of one is never stepped along: any valid stride serves
+  const cuuint64_t row = cuuint64_t(P.D) * 2;
+  const cuuint64_t dims[4] = {cuuint64_t(P.D), cuuint64_t(P.Hq), cuuint64_t(P.T), 1};
+  const cuuint64_t strides[3] = {P.Hq > 1 ? cuuint64_t(P.q_hs) * 2 : row, P.T > 1 ? cuuint64_t(P.q_ts) * 2 : row, row};
+  if (strides[0] == 0 || strides[1] == 0) return false;
+  const cuuint32_t boxes[4] = {64, cuuint32_t(P.queries_of), cuuint32_t(P.tokens), 1}, steps[4] = {1, 1, 1, 1};
+  return encode(map, c.dtype == DART_F16 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 4,
+                const_cast<void*>(P.q), dims, strides, boxes, steps, CU_TENSOR_MAP_INTERLEAVE_NONE,
+                CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 template <typename T, int DH>
-cudaError_t launch(WeightParams& P, const CUtensorMap& km, cudaStream_t s) {
+cudaError_t launch(WeightParams& P, const CUtensorMap& km, const CUtensorMap& qm, cudaStream_t s) {
   constexpr int kStageBytes = DH * kTileBytes;
   // Three stages of K at least (two for the largest blocks), then buffers of Q so that
   // the next head's blocks can come while this one's are used, then stages again.
@@ -589,7 +628,7 @@ cudaError_t launch(WeightParams& P, const CUtensorMap& km, cudaStream_t s) {
       settled(cudaFuncSetAttribute(weights_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if (e != cudaSuccess) return e;
   const int sms = device_sms(), ctas = sms > 0 && sms < kCtas ? sms : kCtas;
-  return launch_kernel(weights_kernel<T, DH>, ctas, kThreads, smem, s, P, km);
+  return launch_kernel(weights_kernel<T, DH>, ctas, kThreads, smem, s, P, km, qm);
 }
 
 }  // namespace
@@ -623,7 +662,6 @@ extern "C" int dart_attention_weights(const void* q, int64_t q_token_stride, int
   P.s_seq = scores_seq_stride; P.s_head = scores_head_stride;
   P.Hq = q_heads; P.Hkv = c.heads; P.G = q_heads / c.heads; P.D = c.dim;
   P.T = T; P.B = B; P.N = N; P.MW = (N + 31) / 32;
-  P.by_group = fast_div(uint32_t(P.G));
   P.by_page = fast_div(uint32_t(c.page));
   P.lengths = lengths; P.starts = starts; P.mask = mask;
   P.c = scale * 1.44269504088896341f;
@@ -631,19 +669,26 @@ extern "C" int dart_attention_weights(const void* q, int64_t q_token_stride, int
   P.cap = (long long)c.table_width * c.page;
   if (P.cap > scores_width) P.cap = scores_width;
   P.page = c.page; P.pages = c.pages; P.box = gcd(c.page, kTile);
-  // an average sequence's rows in equal blocks
-  const long long rows = ((long long)T * P.G + B - 1) / B, blocks = (rows + kMaxBlock - 1) / kMaxBlock;
-  P.block = int(((rows + blocks - 1) / blocks + 15) / 16 * 16);
+  // an average sequence's tokens in equal blocks
+  P.queries_of = P.G < kMaxBlock ? P.G : kMaxBlock;
+  P.parts = (P.G + P.queries_of - 1) / P.queries_of;
+  const int fit = kMaxBlock / P.queries_of, tokens = int(((long long)T + B - 1) / B), blocks = (tokens + fit - 1) / fit;
+  P.tokens = P.parts > 1 ? 1 : (tokens + blocks - 1) / blocks;
+  P.block = (P.tokens * P.queries_of + 15) / 16 * 16;
+  P.by_part = fast_div(uint32_t(P.parts));
+  P.by_queries = fast_div(uint32_t(P.G));
   P.err = device_err;
   P.wait_limit = rows_wait_limit();
   CUtensorMap km;
   if (!cache_map(c, c.k, c.k_page_stride, c.k_row_stride, c.k_head_stride, P.box, &km, P.k_slot))
     return DART_ERR_UNSUPPORTED;
+  CUtensorMap qm;
+  if (!query_map(P, c, &qm)) return DART_ERR_UNSUPPORTED;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (c.dtype == DART_F16)
-    e = c.dim <= 64 ? launch<__half, 1>(P, km, s) : launch<__half, 2>(P, km, s);
+    e = c.dim <= 64 ? launch<__half, 1>(P, km, qm, s) : launch<__half, 2>(P, km, qm, s);
   else
-    e = c.dim <= 64 ? launch<__nv_bfloat16, 1>(P, km, s) : launch<__nv_bfloat16, 2>(P, km, s);
+    e = c.dim <= 64 ? launch<__nv_bfloat16, 1>(P, km, qm, s) : launch<__nv_bfloat16, 2>(P, km, qm, s);
   return e == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

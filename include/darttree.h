@@ -600,7 +600,8 @@ int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, const int32_
  * not touched.  A row whose lse is not finite adds nothing (a caller sets +inf to
  * leave a row out, say of a node that was not accepted), and what a row does not
  * see does not reach a score.  Only the cache's k is read.
- *  q, lengths, starts, mask, N, scale   as for dart_tree_attention
+ *  q, lengths, starts, mask, N, scale   as for dart_tree_attention; q's strides
+ *              are not 0 where they are stepped along (DART_ERR_UNSUPPORTED)
  *  lse         device float [T][q_heads]
  *  scores      device float [B][heads] rows of scores_width elements with the
  *              given strides; positions from scores_width on are left out and

@@ -45,7 +45,8 @@ def _case(dtype, lengths, counts, Hq, Hkv, dim, page, tree=0, seed=0, extra=0, h
 def _run(D, s, scores, scale=None, err=None):
     k = s["k"].cuda()
     k = k.transpose(1, 2) if s["heads_first"] else k
-    return D.attention_weights(s["q"].cuda(), k, s["pages"].cuda(), _i32(s["lengths"]), _i32(s["starts"]),
+    q = s["q"].cuda() if s["q"].is_contiguous() else s["q"][:1].cuda().expand(s["q"].shape)
+    return D.attention_weights(q, k, s["pages"].cuda(), _i32(s["lengths"]), _i32(s["starts"]),
                                s["lse"].cuda(), scores, scale=scale, device_err=err,
                                mask=None if s["mask"] is None else torch.from_numpy(s["mask"]).cuda())
 
@@ -105,6 +106,24 @@ def test_chunks_shorter_than_the_tree(D):
 def test_many_row_blocks(D, n):
     """Chunks of one, two, three and more blocks of rows in one call, and sequences without a chunk."""
     _check(D, _case("bf16", [0, 500, 90, 1000, 3], [n, 1, 0, n // 2, n], 16, 2, 64, 64, seed=n, extra=3))
+
+
+@pytest.mark.parametrize("Hq,Hkv,n", [(300, 1, 3), (512, 1, 2), (514, 2, 4), (256, 1, 5)])
+def test_more_queries_than_a_block_has_rows(D, Hq, Hkv, n):
+    _check(D, _case("bf16", [200, 0, 130], [n, 1, n], Hq, Hkv, 64, 16, seed=Hq, extra=1))
+    _check(D, _case("f16", [90], [34], Hq, Hkv, 16, 16, tree=33, seed=n))
+
+
+def test_queries_with_strides(D):
+    """Queries that are a part of a projection's output."""
+    s = _case("bf16", [100, 300], [5, 1], 6, 2, 64, 16, seed=21)
+    want = _run(D, s, torch.zeros((2, 2, 310), device="cuda"))
+    wide = torch.randn(6, 10, 64).to(torch.bfloat16)
+    wide[:, 2:8] = s["q"]
+    got = torch.zeros((2, 2, 310), device="cuda")
+    D.attention_weights(wide.cuda()[:, 2:8], s["k"].cuda(), s["pages"].cuda(), _i32(s["lengths"]), _i32(s["starts"]),
+                        s["lse"].cuda(), got)
+    assert torch.equal(got, want)
 
 
 def test_many_tiles_a_head(D):
@@ -239,7 +258,7 @@ def test_refusals(D):
     for bad in (ok[:, :1], ok.double(), ok.cpu(), ok[0], ok[:, :1].expand(1, 2, 62)):
         with pytest.raises(D.DartError):
             _run(D, s, bad)
-    for key, bad in (("lse", s["lse"].double()), ("lse", s["lse"][:1]), ("q", s["q"].half()), ("q", s["q"][:, :3])):
+    for key, bad in (("q", s["q"][:1].expand(2, 4, 64)), ("lse", s["lse"].double()), ("lse", s["lse"][:1]), ("q", s["q"].half()), ("q", s["q"][:, :3])):
         t = dict(s)
         t[key] = bad
         with pytest.raises(D.DartError):

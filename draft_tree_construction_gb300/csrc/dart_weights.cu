@@ -17,10 +17,13 @@
 //   warp 14       issues the tcgen05 products, one row block after the other
 //   warp 15       copies the row blocks of Q by TMA, a box per 64 columns (a sequence
 //                 whose blocks fit in the buffers keeps them there for all of its tiles)
-//   warps 0-11    add up the exponentials: three groups of four warps, each a third
-//                 of a block's rows, or, for sequences of up to 32 rows, each every
-//                 third tile (a tile's chain from the product to the stored score is
-//                 then longer than the copy of a tile)
+//   warps 0-11    add up the exponentials: three groups of four warps with S buffers of
+//                 their own, each every third tile (a tile's chain from the product to
+//                 the stored score is longer than the copy of a tile, and groups that
+//                 share one wait for each other at every block)
+// Three tiles, a wave, are taken together: first each one's product with the first
+// block, then each one's with the second, so that the groups are all fed and a block
+// that does not stay is copied once for three tiles.
 // Blocks are whole tokens, as many as make an average sequence's blocks equal, 256 rows
 // at most (256 of a token's queries where a key head has more);
 // what the buffers of Q leave of the shared memory goes to the ring (decoding is
@@ -39,9 +42,8 @@ constexpr int kCtas = 152;
 constexpr int kTile = 128;                           // positions of a tile
 constexpr int kTileBytes = kTile * kColBytes;        // 64 columns of them
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxBlock = 256;                       // rows of a block
-constexpr int kMaxStages = 12, kMaxSums = 8, kMaxQ = 4;
-constexpr int kFewRows = 32;                         // of a sequence whose tiles are dealt to the groups
+constexpr int kMaxBlock = 160;                       // rows of a block: an S buffer for each group
+constexpr int kMaxStages = 12, kMaxSums = 4, kMaxQ = 4;
 
 struct WeightParams {
   const void* q;
@@ -63,7 +65,7 @@ struct WeightParams {
   int parts;                       // blocks that a token takes (more than one only with one token a block)
   FastDiv by_part, by_queries;
   int block, columns;              // rows of a buffer, tensor memory columns from one S buffer to the next
-  int stages, sums, queries;       // K stages, S buffers, Q buffers
+  int stages, sums, queries;       // K stages, S buffers of a group, Q buffers
   uint32_t* err;
   long long wait_limit;
 };
@@ -71,13 +73,12 @@ struct WeightParams {
 struct Shared {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
   uint64_t q_full[kMaxQ], q_empty[kMaxQ];
-  uint64_t s_full[kMaxSums], s_empty[kMaxSums];
+  uint64_t s_full[kGroups * kMaxSums], s_empty[kGroups * kMaxSums];
   uint64_t drain;
   long long total, lo, hi, base;   // this CTA's share of the list, and the first unit of sequence `first`
   long long scan[kThreads / 32];
   alignas(16) float minus_l[kMaxQ][kMaxBlock];   // -L of the rows in a Q buffer, -inf for a row that adds nothing
-  float part[kGroups - 1][kTile];  // the other groups' sums
-  uint4 see[kMaxBlock];            // what each row sees of a tile
+  alignas(16) uint32_t see[kGroups][4][kMaxBlock];   // what each row sees of a group's tile, 32 positions a word
   uint32_t tmem;
   int first;
   int dead;
@@ -215,11 +216,12 @@ struct Tour {
     }
   }
   __device__ __forceinline__ bool resident(const WeightParams& P) const { return c.blocks <= P.queries; }
-  // Whether block j is taken for tile t: causal blocks that see nothing of it are left out,
-  // unless the blocks stay in their buffers.
+  // Whether block j is taken for the wave from tile t on: causal blocks that see nothing of
+  // it are left out, unless the blocks stay in their buffers.
   __device__ __forceinline__ bool uses(const WeightParams& P, int t, int j) const {
     return resident(P) || block_end(P, c, j) > t * kTile;
   }
+  __device__ __forceinline__ int wave(int t) const { return min(kGroups, t1 - t); }
 };
 
 // A place in a ring of n, and the parity of its round.
@@ -246,13 +248,32 @@ template <int ID, int N>
 __device__ __forceinline__ void named_barrier(int offset = 0) {
   asm volatile("bar.sync %0, %1;" :: "r"(ID + offset), "n"(N) : "memory");
 }
-__device__ __forceinline__ void mbar_arrive_n(uint64_t* bar, uint32_t n) {
-  asm volatile("mbarrier.arrive.shared::cta.b64 _, [%0], %1;" :: "r"(smem_u32(bar)), "r"(n) : "memory");
+// What the rows of block k see of the positions from p0 on, by a group's 128 threads.  Not
+// inlined: it is rare, and the sums need the registers.
+__device__ __noinline__ void look(const WeightParams& P, Shared* sh, const Seq& c, const Block& k, int b, int group, int mine,
+                                  int p0, const float* minus_l) {
+  const int tree = c.len + c.lead, at0 = p0 - tree, wd0 = at0 >> 5;
+  for (int r = mine; r < (k.rows + 15) / 16 * 16; r += 128) {
+    const int token = k.t0 + (P.parts == 1 ? P.by_queries.div(r) : 0);
+    const bool on = r < k.rows && minus_l[r] > -INFINITY;        // a row that adds nothing sees nothing
+    const int plain = on ? min(c.len + min(token + 1, c.lead), c.S) : 0;
+    const int nodes = on && token >= c.lead ? min(min(P.N, c.n - c.lead), c.S - tree) : 0;
+    const uint32_t* bits = P.mask + ((long long)b * P.N + (token - c.lead)) * P.MW;
+    uint32_t word[5];
+#pragma unroll
+    for (int i = 0; i < 5; ++i) word[i] = wd0 + i >= 0 && 32 * (wd0 + i) < nodes ? bits[wd0 + i] : 0u;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int below = max(0, min(plain - p0 - 32 * i, 32)), left = max(0, min(nodes - at0 - 32 * i, 32));
+      const uint32_t x = __funnelshift_r(word[i], word[i + 1], at0 & 31);
+      sh->see[group][i][r] = (below >= 32 ? kFull : (1u << below) - 1u) | (x & (left >= 32 ? kFull : (1u << left) - 1u));
+    }
+  }
 }
 
 template <typename T, int DH>
 __global__ void __launch_bounds__(kThreads, 1)
-weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
+weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
   constexpr int kStageBytes = DH * kTileBytes;
   extern __shared__ __align__(1024) unsigned char smem[];
   const int q_half = P.block * kColBytes, q_bytes = DH * q_half;
@@ -270,9 +291,9 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, c
       mbar_init(&sh->q_full[i], 1);
       mbar_init(&sh->q_empty[i], 1 + kSumWarps);         // the products, and those who read -L
     }
-    for (int i = 0; i < P.sums; ++i) {
+    for (int i = 0; i < kGroups * P.sums; ++i) {
       mbar_init(&sh->s_full[i], 1);
-      mbar_init(&sh->s_empty[i], kSumWarps);
+      mbar_init(&sh->s_empty[i], 4);                     // the group's warps
     }
     mbar_init(&sh->drain, 1);
     fence_mbar_init();
@@ -280,6 +301,14 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, c
     sh->first = 0;
     sh->base = 0;
   }
+  // the rows that fill a block up to a multiple of 16 are never copied: zeros, so that they
+  // give no NaN
+  const int copied = P.tokens * P.queries_of;
+  for (int i = tid; i < P.queries * DH * (P.block - copied) * 8; i += kThreads) {
+    const int half = i / ((P.block - copied) * 8), at = i - half * (P.block - copied) * 8;
+    *reinterpret_cast<uint4*>(sq + half * q_half + copied * kColBytes + at * 16) = make_uint4(0, 0, 0, 0);
+  }
+  fence_async();
   if (warp == 14) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(&sh->tmem)), "r"(kTmemCols) : "memory");
@@ -337,37 +366,49 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, c
     const uint32_t id0 = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 4) << 24);
     const uint64_t q_desc = smem_desc(smem_u32(sq), 16), k_desc = smem_desc(smem_u32(ring), 16);
     const int k_steps = (P.D + 15) / 16;
-    Ring stage, s, load;
+    Ring stage, load, s[kGroups];
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
       const bool stay = w.resident(P);
-      for (int t = w.t0; t < w.t1 && ok; ++t, stage.next(P.stages)) {
-        if (!(ok = wait_warp(&sh->k_full[stage.at], stage.round, sh, limit))) break;
-        for (int j = 0; j < w.c.blocks; ++j) {
+      for (int t = w.t0; t < w.t1 && ok; t += kGroups) {
+        const int tiles = w.wave(t);
+        const bool ends = t + kGroups >= w.t1;               // the segment's last wave
+        int last = w.c.blocks - 1;
+        while (!w.uses(P, t, last)) --last;
+        bool first = true;
+        for (int j = 0; j <= last && ok; ++j) {
           if (!w.uses(P, t, j)) continue;
           const Ring at = stay ? load.plus(j, P.queries) : load;       // the Q load that this block came with
           if (!stay || t == w.t0) ok = wait_warp(&sh->q_full[at.at], at.round, sh, limit);
-          ok = ok && wait_warp(&sh->s_empty[s.at], s.round ^ 1u, sh, limit);
-          if (!ok) break;
-          tc_after();
           const int rows = block_of(P, w.c, j).rows;
           const uint32_t id = id0 | (uint32_t((rows + 15) / 16 * 2) << 17);
-          if (elect()) {
-            const uint64_t kd = k_desc + uint64_t(stage.at * (kStageBytes >> 4));
-            const uint64_t qd = q_desc + uint64_t(at.at * (q_bytes >> 4));
 #pragma unroll
-            for (int k = 0; k < 4 * DH; ++k)
-              if (k < k_steps)
-                mma_ss(tmem + s.at * P.columns, kd + (((k >> 2) * kTileBytes + (k & 3) * 32) >> 4),
-                       qd + (((k >> 2) * q_half + (k & 3) * 32) >> 4), id, k > 0);
-            tc_commit(&sh->s_full[s.at]);
-            if (!stay || t == w.t1 - 1) tc_commit(&sh->q_empty[at.at]);
+          for (int g = 0; g < kGroups; ++g) {
+            if (g >= tiles || !ok) break;
+            const Ring k_at = stage.plus(g, P.stages);
+            const uint32_t buf = uint32_t(g) * P.sums + s[g].at;
+            if (first) ok = wait_warp(&sh->k_full[k_at.at], k_at.round, sh, limit);
+            ok = ok && wait_warp(&sh->s_empty[buf], s[g].round ^ 1u, sh, limit);
+            if (!ok) break;
+            tc_after();
+            if (elect()) {
+              const uint64_t kd = k_desc + uint64_t(k_at.at * (kStageBytes >> 4));
+              const uint64_t qd = q_desc + uint64_t(at.at * (q_bytes >> 4));
+#pragma unroll
+              for (int k = 0; k < 4 * DH; ++k)
+                if (k < k_steps)
+                  mma_ss(tmem + buf * P.columns, kd + (((k >> 2) * kTileBytes + (k & 3) * 32) >> 4),
+                         qd + (((k >> 2) * q_half + (k & 3) * 32) >> 4), id, k > 0);
+              tc_commit(&sh->s_full[buf]);
+              if (j == last) tc_commit(&sh->k_empty[k_at.at]);
+              if (g == tiles - 1 && (!stay || ends)) tc_commit(&sh->q_empty[at.at]);
+            }
+            __syncwarp();
+            s[g].next(P.sums);
           }
-          __syncwarp();
-          s.next(P.sums);
+          first = false;
           if (!stay) load.next(P.queries);
         }
-        if (ok && elect()) tc_commit(&sh->k_empty[stage.at]);
-        __syncwarp();
+        stage = stage.plus(tiles, P.stages);
       }
       if (stay) load = load.plus(w.c.blocks, P.queries);
     }
@@ -412,7 +453,7 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, c
       if (w.resident(P)) {
         for (int j = 0; j < w.c.blocks && ok; ++j) bring(j);
       } else {
-        for (int t = w.t0; t < w.t1 && ok; ++t)
+        for (int t = w.t0; t < w.t1 && ok; t += kGroups)
           for (int j = 0; j < w.c.blocks && ok; ++j)
             if (w.uses(P, t, j)) bring(j);
       }
@@ -422,83 +463,48 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, c
     __syncwarp();
   } else {
     // ------------------------------------------------------------------ sums
-    // The schedule alone decides which barriers the groups meet at, so a wait that ran
-    // out cannot leave a warp behind: ok only turns the work off.
+    // The schedule alone decides which barriers a group's warps meet at, so a wait that
+    // ran out cannot leave a warp behind: ok only turns the work off.
     const int group = warp >> 2, mine = (warp & 3) * 32 + lane;     // lane of tensor memory: the position
     const uint32_t lane_base = uint32_t(warp & 3) << 21;
     Ring s, load;
-    int turn = 0;                                  // the group whose turn the next tile of a short sequence is
     const uint64_t c2 = pair(P.c, P.c);
     for (bool more = w.begin(P, sh); more; more = w.next(P)) {
-      const bool stay = w.resident(P), few = w.c.blocks == 1 && w.c.n * P.G <= kFewRows;
+      const bool stay = w.resident(P);
       float* row = P.scores + w.b * P.s_seq + w.h * P.s_head;
-      const int tree = w.c.len + w.c.lead;
-      if (stay)                                    // -L is there; by all groups, so that none runs ahead of the others
-        for (int j = 0; j < w.c.blocks; ++j) {
-          const Ring at = load.plus(j, P.queries);
-          ok = ok && wait_warp(&sh->q_full[at.at], at.round, sh, limit);
-        }
-      for (int t = w.t0; t < w.t1; ++t) {
-        const int p0 = t * kTile, p = p0 + mine, end = min(p0 + kTile, w.c.S);
-        if (few) {
-          const bool here = turn == group;
-          turn = (turn + 1) % kGroups;
-          if (!here) {
-            s.next(P.sums);
-            continue;
-          }
-        }
-        const bool writes = (few || group == 0) && p < w.c.S;
+      for (int t = w.t0; t < w.t1; t += kGroups) {
+        // all groups see every load of Q arrive, so that none gives one up before its time
+        const bool here = group < w.wave(t);
+        const int p0 = (t + group) * kTile, p = p0 + mine, end = min(p0 + kTile, w.c.S);
+        const bool writes = here && p < w.c.S;
         float old = 0.f;
         if (writes) old = row[p];
         uint64_t sum = 0ull;
         for (int j = 0; j < w.c.blocks; ++j) {
           if (!w.uses(P, t, j)) continue;
           const Ring at = stay ? load.plus(j, P.queries) : load;
+          if (!stay || t == w.t0) ok = ok && wait_warp(&sh->q_full[at.at], at.round, sh, limit);
+          if (!stay) load.next(P.queries);
+          if (!here) {
+            if (!stay && lane == 0) mbar_arrive(&sh->q_empty[at.at]);
+            continue;
+          }
           const Block k = block_of(P, w.c, j);
           const int cols = (k.rows + 15) / 16 * 16;
           // some row of the block does not see some position of the tile
           const bool masked = min(w.c.len + min(k.t0 + 1, w.c.lead), w.c.S) < end;
-          uint4* see_at = sh->see + (few ? group * kFewRows : 0);
           if (masked) {
-            // the words of the masked block before have been read
-            if (few) named_barrier<2, 128>(group);
-            else named_barrier<1, kSumThreads>();
-            const int r = few ? mine : tid;
-            if (r < (few ? kFewRows : P.block)) {
-              uint4 see = make_uint4(0, 0, 0, 0);
-              if (r < k.rows) {
-                const int token = k.t0 + (P.parts == 1 ? P.by_queries.div(r) : 0);
-                const int plain = min(w.c.len + min(token + 1, w.c.lead), w.c.S);
-                const int nodes = token >= w.c.lead ? min(min(P.N, w.c.n - w.c.lead), w.c.S - tree) : 0;
-                const uint32_t* bits = P.mask + ((long long)w.b * P.N + (token - w.c.lead)) * P.MW;
-                uint32_t word[5], out[4];
-                const int at0 = p0 - tree, wd0 = at0 >> 5;
-#pragma unroll
-                for (int i = 0; i < 5; ++i) word[i] = wd0 + i >= 0 && 32 * (wd0 + i) < nodes ? bits[wd0 + i] : 0u;
-#pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  const int below = max(0, min(plain - p0 - 32 * i, 32)), left = max(0, min(nodes - at0 - 32 * i, 32));
-                  const uint32_t x = __funnelshift_r(word[i], word[i + 1], at0 & 31);
-                  out[i] = (below >= 32 ? kFull : (1u << below) - 1u) | (x & (left >= 32 ? kFull : (1u << left) - 1u));
-                }
-                see = make_uint4(out[0], out[1], out[2], out[3]);
-              }
-              see_at[r] = see;
-            }
-            if (few) named_barrier<2, 128>(group);
-            else named_barrier<1, kSumThreads>();
+            named_barrier<1, 128>(group);          // the words of the masked block before have been read
+            look(P, sh, w.c, k, w.b, group, mine, p0, sh->minus_l[at.at]);
+            named_barrier<1, 128>(group);
           }
-          // this group's columns, in steps of 16
-          const int steps = cols >> 4;
-          const int c0 = few ? 0 : (steps * group / kGroups) << 4, c1 = few ? cols : (steps * (group + 1) / kGroups) << 4;
-          if (!stay) ok = ok && wait_warp(&sh->q_full[at.at], at.round, sh, limit);
-          ok = ok && wait_warp(&sh->s_full[s.at], s.round, sh, limit);
-          if (ok && c0 < c1) {
+          const uint32_t buf = uint32_t(group) * P.sums + s.at;
+          ok = ok && wait_warp(&sh->s_full[buf], s.round, sh, limit);
+          if (ok) {
             tc_after();
-            const uint32_t from = tmem + lane_base + s.at * P.columns;
+            const uint32_t from = tmem + lane_base + buf * P.columns;
             const float* l = sh->minus_l[at.at];
-            const uint32_t* words = reinterpret_cast<const uint32_t*>(see_at) + (warp & 3);
+            const uint32_t* words = sh->see[group][warp & 3];
             uint64_t part[2] = {0ull, 0ull};
             auto fast = [&](const float* x, int col) {
               const ulonglong2* l4 = reinterpret_cast<const ulonglong2*>(l + col);
@@ -510,72 +516,68 @@ weights_kernel(const WeightParams P, const __grid_constant__ CUtensorMap kmap, c
                 part[1] = add2(part[1], pair(ex2_approx(low(y1)), ex2_approx(high(y1))));
               }
             };
-            // what a row does not see is left out whatever the product is, and a row that adds nothing
-            auto slow = [&](const float* x, int col) {
+            // what a row does not see is left out whatever the product is
+            const uint32_t bit = 1u << lane;
+            auto seen = [&](const float* x, int col) {
               const ulonglong2* l4 = reinterpret_cast<const ulonglong2*>(l + col);
+              const uint4* w4 = reinterpret_cast<const uint4*>(words + col);
 #pragma unroll
-              for (int k = 0; k < 16; k += 2) {
-                const uint64_t lk = (k & 2) ? l4[k >> 2].y : l4[k >> 2].x;
-                const uint64_t y = fma2(pair(x[k], x[k + 1]), c2, lk);
-                bool on0 = low(lk) > -INFINITY, on1 = high(lk) > -INFINITY;
-                if (masked) {
-                  on0 = on0 && ((words[4 * (col + k)] >> lane) & 1u);
-                  on1 = on1 && ((words[4 * (col + k) + 4] >> lane) & 1u);
-                }
-                part[(k >> 1) & 1] = add2(part[(k >> 1) & 1], pair(on0 ? ex2_approx(low(y)) : 0.f, on1 ? ex2_approx(high(y)) : 0.f));
+              for (int k = 0; k < 16; k += 4) {
+                const ulonglong2 lk = l4[k >> 2];
+                const uint4 wk = w4[k >> 2];
+                const uint64_t y0 = fma2(pair(x[k], x[k + 1]), c2, lk.x), y1 = fma2(pair(x[k + 2], x[k + 3]), c2, lk.y);
+                const float a0 = wk.x & bit ? low(y0) : -INFINITY, a1 = wk.y & bit ? high(y0) : -INFINITY,
+                            a2 = wk.z & bit ? low(y1) : -INFINITY, a3 = wk.w & bit ? high(y1) : -INFINITY;
+                part[0] = add2(part[0], pair(ex2_approx(a0), ex2_approx(a1)));
+                part[1] = add2(part[1], pair(ex2_approx(a2), ex2_approx(a3)));
               }
             };
-            auto all_fast = [&]() {          // the next columns are on their way while these are added up
+            // the next columns are on their way while these are added up
+            auto all = [&](auto&& add) {
               float x[2][16];
-              tmem_ld16(from + c0, x[0]);
-              for (int col = c0; col < c1; col += 32) {
+              tmem_ld16(from, x[0]);
+              for (int col = 0; col < cols; col += 32) {
                 loaded<16>(x[0]);
-                if (col + 16 < c1) tmem_ld16(from + col + 16, x[1]);
-                fast(x[0], col);
-                if (col + 16 < c1) {
+                if (col + 16 < cols) tmem_ld16(from + col + 16, x[1]);
+                add(x[0], col);
+                if (col + 16 < cols) {
                   loaded<16>(x[1]);
-                  if (col + 32 < c1) tmem_ld16(from + col + 32, x[0]);
-                  fast(x[1], col + 16);
+                  if (col + 32 < cols) tmem_ld16(from + col + 32, x[0]);
+                  add(x[1], col + 16);
                 }
               }
             };
-            auto all_slow = [&]() {
-              part[0] = part[1] = 0ull;
-#pragma unroll 1
-              for (int col = c0; col < c1; col += 16) {
-                float x[16];
-                tmem_ld16(from + col, x);
-                loaded<16>(x);
-                slow(x, col);
-              }
-            };
-            bool again = masked;
-            if (!masked) {
-              all_fast();
-              // a row that adds nothing is zeros, and 0 * inf is NaN: then once more without those rows
+            if (masked) {
+              all(seen);
+            } else {
+              all(fast);
+              // a row that adds nothing is zeros or what lies behind the chunk, which may hold anything:
+              // where that gave NaN the block is added up once more without those rows
               const uint64_t both = add2(part[0], part[1]);
-              again = __any_sync(kFull, low(both) + high(both) != low(both) + high(both));
+              if (__any_sync(kFull, low(both) + high(both) != low(both) + high(both))) {
+                part[0] = part[1] = 0ull;
+#pragma unroll 1
+                for (int col = 0; col < cols; col += 16) {
+                  float x[16];
+                  tmem_ld16(from + col, x);
+                  loaded<16>(x);
+#pragma unroll
+                  for (int k = 0; k < 16; ++k)
+                    if (l[col + k] > -INFINITY) part[0] = add2(part[0], pair(ex2_approx(fmaf(x[k], P.c, l[col + k])), 0.f));
+                }
+              }
             }
-            if (again) all_slow();
             sum = add2(sum, add2(part[0], part[1]));
             tc_before();
           }
           __syncwarp();
-          if (lane == 0) mbar_arrive_n(&sh->s_empty[s.at], few ? kGroups : 1);
-          if (!stay && lane == 0) mbar_arrive(&sh->q_empty[at.at]);
+          if (lane == 0) {
+            mbar_arrive(&sh->s_empty[buf]);
+            if (!stay) mbar_arrive(&sh->q_empty[at.at]);
+          }
           s.next(P.sums);
-          if (!stay) load.next(P.queries);
         }
-        float gathered = low(sum) + high(sum);
-        if (!few) {
-          if (group > 0) sh->part[group - 1][mine] = gathered;
-          named_barrier<1, kSumThreads>();
-          if (group == 0)
-#pragma unroll
-            for (int i = 0; i < kGroups - 1; ++i) gathered += sh->part[i][mine];
-          named_barrier<1, kSumThreads>();         // read before the next tile's are written
-        }
-        if (writes && ok) row[p] = old + gathered;
+        if (writes && ok) row[p] = old + (low(sum) + high(sum));
       }
       if (stay) {
         __syncwarp();
@@ -614,15 +616,16 @@ bool query_map(const WeightParams& P, const dart_cache_t& c, CUtensorMap* map) {
 template <typename T, int DH>
 cudaError_t launch(WeightParams& P, const CUtensorMap& km, const CUtensorMap& qm, cudaStream_t s) {
   constexpr int kStageBytes = DH * kTileBytes;
-  // Three stages of K at least (two for the largest blocks), then buffers of Q so that
-  // the next head's blocks can come while this one's are used, then stages again.
+  // A wave's stages of K and one more at least, then buffers of Q so that the next head's
+  // blocks can come while this one's are used, then stages again.
   const int room = 227 * 1024 - int(sizeof(Shared)), q = P.block * DH * kColBytes;
-  P.queries = (room - 3 * kStageBytes) / q;
+  P.queries = (room - (kGroups + 1) * kStageBytes) / q;
   P.queries = P.queries < 2 ? 2 : P.queries > kMaxQ ? kMaxQ : P.queries;
   P.stages = (room - P.queries * q) / kStageBytes;
   P.stages = P.stages < kMaxStages ? P.stages : kMaxStages;
   P.columns = (P.block + 31) / 32 * 32;
-  P.sums = int(kTmemCols) / P.columns < kMaxSums ? int(kTmemCols) / P.columns : kMaxSums;
+  P.sums = int(kTmemCols) / P.columns / kGroups;
+  P.sums = P.sums < kMaxSums ? P.sums : kMaxSums;
   const int smem = P.queries * q + P.stages * kStageBytes + int(sizeof(Shared));
   const cudaError_t e =
       settled(cudaFuncSetAttribute(weights_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));

@@ -11,16 +11,21 @@
 // K9 (move_kernel): list entry i of a sequence moves position from(i) to base + i,
 // from(i) increasing and never below base + i.  So a store of entry i only ever
 // hits what an entry j <= i was read from: entries are taken in order, a batch is
-// read into registers by the whole CTA, and stored after a barrier.  A CTA owns some
-// 16-byte columns of one head of K or V, so no CTA reads what another one writes.
-// Columns are dealt to several CTAs (two columns, a 32-byte sector, at least) where
-// there are fewer (sequence, head)s than the device can run.  Memory bounds it: two
-// passes over the rows that move.
+// read into registers by the whole CTA, and stored after a barrier.  A CTA, or a cluster
+// of up to eight with a barrier of its own where lists are long and heads few, has one head
+// of K or V, so nobody reads what another one writes.  A lane finds where one of the
+// warp's 32 rows lies; then the warp moves them, whole rows at a time (when each thread
+// found its own 16 bytes, that was 150 instructions for each, and they bound it).  Memory
+// bounds it: two passes over the rows that move.
 //
-// K10 (select_kernel): one CTA per (sequence, head).  The m-th largest score is found
-// by a radix search over the ordered keys, 11 + 11 + 10 bits, each level one pass over
-// the scores with a histogram in shared memory; a last pass in position order counts
-// ties, writes the list and moves the scores up the same way as K9 moves rows.
+// K10 (select_kernel): the m-th largest score is found by a radix search over the
+// ordered keys, 11 + 11 + 10 bits.  One CTA per (sequence, head), or a cluster of up to
+// eight that share its positions where there are few or long ones.  A CTA reads its scores
+// once, into registers; each level is a histogram in shared memory, which the cluster's
+// CTAs read from one another, and a scan.  Then every warp counts what it keeps by ballots,
+// one scan gives all places, and the list and the scores, which have all been read by then,
+// are written.  Latency bounds it.  Sequences beyond what registers hold (131072 positions
+// a head) are read again at every level by one CTA (long_kernel).
 #include "dart_launch.h"
 
 namespace dart {
@@ -83,20 +88,26 @@ struct MoveParams {
   int32_t* out_lengths;             // [B] or nullptr
   int width, relative;              // relative: positions count from lengths[b]
   int cap;                          // positions that a sequence can have
-  int slices, vecs;                 // CTAs a row is dealt to, 16-byte columns of each
-  FastDiv by_page, by_slices;
+  int ranks;                        // CTAs that share a head's list
+  FastDiv by_page;
   uint32_t* err;
 };
 
-constexpr int kMoveUnroll = 4;
+__device__ __forceinline__ void cluster_sync() {
+  asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
+}
 
-__global__ void __launch_bounds__(512) move_kernel(const MoveParams P) {
-  const int head = P.by_slices.div(blockIdx.x), slice = blockIdx.x - head * P.slices, b = blockIdx.y;
+constexpr int kMoveThreads = 256;
+
+// COLS: 16-byte columns of a row, rounded up to a power of two; a warp moves 32 / COLS rows at once.
+template <int COLS>
+__global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const MoveParams P) {
+  const int head = int(blockIdx.x) / P.ranks, rank = int(blockIdx.x) - head * P.ranks, b = blockIdx.y;
   const int len = P.lengths[b], cap = P.cap;
   const int32_t* list = P.index + b * P.index_seq + head * P.index_head;
   const int32_t* table = P.c.table + (long long)b * P.c.table_stride;
   const int base = P.relative ? len : 0;
-  int count = P.counts ? P.counts[b] : min(len, P.width);
+  const int count = P.counts ? P.counts[b] : min(len, P.width);
   const bool wrong = len < 0 || count < 0 || count > P.width || len > cap || (P.relative && count > cap - len);
   const bool first = blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0;
   if (wrong) {
@@ -111,46 +122,61 @@ __global__ void __launch_bounds__(512) move_kernel(const MoveParams P) {
   const long long ps = blockIdx.z ? P.c.v_page_stride : P.c.k_page_stride,
                   rs = blockIdx.z ? P.c.v_row_stride : P.c.k_row_stride,
                   hs = blockIdx.z ? P.c.v_head_stride : P.c.k_head_stride;
-  const int all = P.c.dim >> 3;                      // columns of a head
-  const int per_row = P.vecs, rows = blockDim.x / per_row;
-  const int row = threadIdx.x / per_row, col = slice * per_row + threadIdx.x - row * per_row;
-  const bool mine = row < rows && col < all;
-  uint16_t* data = static_cast<uint16_t*>(blockIdx.z ? P.c.v : P.c.k) + head * hs + 8 * col;
-  auto place = [&](int p) -> uint16_t* {             // nullptr where there is no such position
-    if (p < 0 || p >= cap) return nullptr;
-    const int at = P.by_page.div(p), page = table[at];
-    if (page < 0 || page >= P.c.pages) return nullptr;
-    return data + page * ps + (p - at * P.c.page) * rs;
+  constexpr int kRows = 32 / COLS;                   // rows of a step, COLS steps for the warp's 32
+  const int lane = threadIdx.x & 31, warps = int(blockDim.x) >> 5, warp = int(threadIdx.x) >> 5;
+  const int sub = lane / COLS, col = lane % COLS;
+  const bool mine = col < (P.c.dim >> 3);
+  uint4* data = reinterpret_cast<uint4*>(static_cast<uint16_t*>(blockIdx.z ? P.c.v : P.c.k) + head * hs) + col;
+  // where position p's row begins, in 16-byte units from the head's first; -1 where there is none
+  auto place = [&](int p, int page) -> long long {
+    if (page < 0 || page >= P.c.pages) return -1;
+    return (page * ps + (p - P.by_page.div(p) * P.c.page) * rs) >> 3;
   };
   bool bad = false;
-  for (int i0 = 0; i0 < count; i0 += rows * kMoveUnroll) {
-    uint4 x[kMoveUnroll];
-    uint16_t* to[kMoveUnroll];
-#pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u) {
-      const int i = i0 + u * rows + row;
-      to[u] = nullptr;
-      if (!mine || i >= count) continue;
-      const int from = list[i], before = i > 0 ? list[i - 1] : -1;
-      if (from == i) continue;
-      // an entry out of order could be overwritten before it is read: it is left out
-      if (from < i || from <= before) {
+  const int stride = 32 * warps * P.ranks;           // entries of a batch
+  int next = (rank * warps + warp) * 32 + lane;      // this lane's entry
+  int from = next < count ? list[next] : next, before = next < count && next > 0 ? list[next - 1] : -1;
+  for (int i0 = 0; i0 < count; i0 += stride) {
+    const int i = next;
+    bool moves = from != i;
+    // an entry out of order could be overwritten before it is read: it is left out
+    if (moves && (from < i || from <= before || from >= cap - base)) {
+      bad = true;
+      moves = false;
+    }
+    long long src = -1, dst = -1;
+    if (moves) {
+      const int s = base + from, d = base + i, s_page = table[P.by_page.div(s)], d_page = table[P.by_page.div(d)];
+      src = place(s, s_page);
+      dst = place(d, d_page);
+      if (src < 0 || dst < 0) {
         bad = true;
-        continue;
-      }
-      const uint16_t* src = from < cap - base ? place(base + from) : nullptr;
-      to[u] = place(base + i);
-      if (src && to[u]) {
-        x[u] = *reinterpret_cast<const uint4*>(src);
-      } else {
-        to[u] = nullptr;
-        bad = true;
+        src = dst = -1;
       }
     }
-    __syncthreads();                                  // the batch is read before any of it is written
+    // the next batch's entry is on its way meanwhile
+    next += stride;
+    from = next < count ? list[next] : next;
+    before = next < count ? list[next - 1] : -1;
+    const bool any = __any_sync(kFull, src >= 0);
+    uint4 x[COLS];
+    if (any) {
 #pragma unroll
-    for (int u = 0; u < kMoveUnroll; ++u)
-      if (to[u]) *reinterpret_cast<uint4*>(to[u]) = x[u];
+      for (int u = 0; u < COLS; ++u) {
+        const long long at = __shfl_sync(kFull, src, u * kRows + sub);
+        if (at >= 0 && mine) x[u] = data[at];
+      }
+    }
+    // the batch is read before any of it is written
+    if (P.ranks > 1) cluster_sync();
+    else __syncthreads();
+    if (any) {
+#pragma unroll
+      for (int u = 0; u < COLS; ++u) {
+        const long long at = __shfl_sync(kFull, dst, u * kRows + sub);
+        if (at >= 0 && mine) data[at] = x[u];
+      }
+    }
   }
   if (bad) set_dev_error(P.err, DART_DEVERR_CACHE);
 }
@@ -194,7 +220,7 @@ __device__ __forceinline__ uint32_t block_exclusive(uint32_t x, uint32_t* warp_s
   return incl - x + (warp > 0 ? below : 0u);
 }
 
-__global__ void __launch_bounds__(kSelectThreads) select_positions_kernel(const SelectParams P) {
+__global__ void __launch_bounds__(kSelectThreads) long_kernel(const SelectParams P) {
   __shared__ uint32_t bins[2048];
   __shared__ uint32_t warp_sums[32];
   __shared__ uint32_t found[2];
@@ -279,20 +305,248 @@ __global__ void __launch_bounds__(kSelectThreads) select_positions_kernel(const 
   for (int p = P.keep + tid; p < len; p += kSelectThreads) scores[p] = 0.f;
 }
 
+// ---- a cluster's CTAs, a head's scores in their registers
+__device__ __forceinline__ uint32_t load_there(const uint32_t* p, uint32_t rank) {
+  uint32_t at, x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(x) : "r"(at) : "memory");
+  return x;
+}
+
+// Four words at once.
+__device__ __forceinline__ uint4 load_four_there(const uint32_t* p, uint32_t rank) {
+  uint32_t at;
+  uint4 x;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("ld.shared::cluster.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(x.x), "=r"(x.y), "=r"(x.z), "=r"(x.w) : "r"(at));
+  return x;
+}
+
+constexpr int kShareThreads = 512, kShareWarps = kShareThreads / 32, kMaxRanks = 8;
+
+// Exclusive prefix over 512 threads; total receives the sum.
+__device__ __forceinline__ uint32_t share_exclusive(uint32_t x, uint32_t* warp_sums, uint32_t& total) {
+  const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+  uint32_t incl = x;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const uint32_t y = __shfl_up_sync(kFull, incl, o);
+    if (lane >= o) incl += y;
+  }
+  __syncthreads();                                   // the sums of the call before have been read
+  if (lane == 31) warp_sums[warp] = incl;
+  __syncthreads();
+  uint32_t below = 0;
+  total = 0;
+#pragma unroll
+  for (int w = 0; w < kShareWarps; ++w) {
+    if (w == warp) below = total;
+    total += warp_sums[w];
+  }
+  return below + incl - x;
+}
+
+template <int KEYS>
+__global__ void __launch_bounds__(kShareThreads, KEYS <= 16 ? 2 : 1) select_kernel(const SelectParams P, int ranks) {
+  __shared__ alignas(16) uint32_t bins[2][2048];     // of a level and the next, which is cleared while others read the first
+  __shared__ uint32_t warp_sums[kShareWarps];
+  __shared__ uint32_t found[2], kept_here[2];
+  __shared__ uint32_t counts[KEYS * kShareWarps];    // kept below 16, ties above, of each batch and warp
+  const int rank = int(blockIdx.x) % ranks, h = int(blockIdx.x) / ranks, b = blockIdx.y;
+  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+  const int len = P.lengths[b];
+  int32_t* out = P.index + ((long long)b * P.heads + h) * P.keep;
+  const bool wrong = len < 0 || len > P.cap;
+  if (wrong || len <= P.keep) {
+    if (wrong && blockIdx.x == 0 && tid == 0) set_dev_error(P.err, DART_DEVERR_CACHE);
+    for (int i = rank * kShareThreads + tid; i < P.keep; i += ranks * kShareThreads) out[i] = !wrong && i < len ? i : -1;
+    return;
+  }
+  float* scores = P.scores + b * P.s_seq + h * P.s_head;
+  const int lo = P.first, hi = len - P.last;          // positions that have to earn their place
+  // this CTA's positions, in batches of 512
+  const int share = (len + ranks - 1) / ranks, p0 = min(rank * share, len), p1 = min(p0 + share, len);
+  float x[KEYS];
+#pragma unroll
+  for (int i = 0; i < KEYS; ++i) {
+    const int p = p0 + i * kShareThreads + tid;
+    x[i] = p < p1 ? scores[p] : 0.f;
+  }
+  for (int i = tid; i < 2048; i += kShareThreads) bins[0][i] = 0;
+  uint32_t want = uint32_t(P.keep - P.first - P.last), prefix = 0, ties = 0;
+  if (want > 0) {
+    const int shifts[3] = {21, 10, 0}, sizes[3] = {2048, 2048, 1024};
+#pragma unroll
+    for (int level = 0; level < 3; ++level) {
+      const int shift = shifts[level], size = sizes[level], above = level == 0 ? 32 : shifts[level - 1];
+      uint32_t* here = bins[level & 1];
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < KEYS; ++i) {
+        if (p0 + i * kShareThreads >= p1) break;
+        const int p = p0 + i * kShareThreads + tid;
+        const uint32_t key = score_key(x[i]);
+        const bool on = p < p1 && p >= lo && p < hi && (level == 0 || (key >> (above & 31)) == prefix);
+        const uint32_t bin = (key >> shift) & (size - 1), who = __ballot_sync(kFull, on);
+        if (who == 0) continue;
+        // scores that got nothing yet are equal: then one add for the warp
+        const uint32_t first = __shfl_sync(kFull, bin, __ffs(who) - 1);
+        if (__all_sync(kFull, !on || bin == first)) {
+          if (lane == 0) atomicAdd(&here[first], uint32_t(__popc(who)));
+        } else if (on) {
+          atomicAdd(&here[bin], 1u);
+        }
+      }
+      if (ranks > 1) cluster_sync();
+      else __syncthreads();
+      // from the largest bin down: thread t owns the four from 2047 - 4 t on
+      uint32_t n[4], sum = 0;
+      {
+        const uint32_t* four = &here[2044 - 4 * tid];
+        uint4 all = make_uint4(0, 0, 0, 0), part[kMaxRanks];
+        if (ranks > 1) {
+#pragma unroll
+          for (int r = 0; r < kMaxRanks; ++r)
+            if (r < ranks) part[r] = load_four_there(four, uint32_t(r));
+#pragma unroll
+          for (int r = 0; r < kMaxRanks; ++r)
+            if (r < ranks) all = make_uint4(all.x + part[r].x, all.y + part[r].y, all.z + part[r].z, all.w + part[r].w);
+        } else {
+          all = *reinterpret_cast<const uint4*>(four);
+        }
+        n[0] = all.w;
+        n[1] = all.z;
+        n[2] = all.y;
+        n[3] = all.x;
+        sum = all.x + all.y + all.z + all.w;
+      }
+      if (level < 2)
+        for (int i = tid; i < 2048; i += kShareThreads) bins[(level + 1) & 1][i] = 0;
+      uint32_t total;
+      uint32_t at = share_exclusive(sum, warp_sums, total);
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (at < want && want <= at + n[k]) {
+          found[0] = uint32_t(2047 - (tid * 4 + k));
+          found[1] = want - at;
+        }
+        at += n[k];
+      }
+      __syncthreads();
+      prefix = level == 0 ? found[0] : (prefix << (above - shift)) | found[0];
+      want = found[1];
+    }
+    ties = want;                                     // of the keys equal to prefix, the first `ties` positions stay
+  }
+  // what each warp keeps of each batch
+  auto sure_of = [&](int p, uint32_t key) { return p < p1 && (p < lo || p >= hi || (ties > 0 && key > prefix)); };
+  auto tie_of = [&](int p, uint32_t key) { return p < p1 && p >= lo && p < hi && ties > 0 && key == prefix; };
+#pragma unroll
+  for (int i = 0; i < KEYS; ++i) {
+    const int p = p0 + i * kShareThreads + tid;
+    const uint32_t key = score_key(x[i]);
+    const uint32_t sure = __ballot_sync(kFull, sure_of(p, key)), tie = __ballot_sync(kFull, tie_of(p, key));
+    if (lane == 0) counts[i * kShareWarps + warp] = uint32_t(__popc(sure)) | uint32_t(__popc(tie)) << 16;
+  }
+  __syncthreads();
+  // places of the batches' warps: both sums of at most 16384 in one word
+  constexpr int kEach = (KEYS * kShareWarps + kShareThreads - 1) / kShareThreads;
+  uint32_t own[kEach], sum = 0, total;
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = tid * kEach + e;
+    own[e] = i < KEYS * kShareWarps ? counts[i] : 0u;
+    sum += own[e];
+  }
+  uint32_t at = share_exclusive(sum, warp_sums, total);
+#pragma unroll
+  for (int e = 0; e < kEach; ++e) {
+    const int i = tid * kEach + e;
+    if (i < KEYS * kShareWarps) counts[i] = at;
+    at += own[e];
+  }
+  if (tid == 0) kept_here[0] = total;
+  uint32_t kept = 0, seen = 0;                       // before this CTA's positions
+  if (ranks > 1) {
+    cluster_sync();                                  // and every score has been read
+    for (int r = 0; r < rank; ++r) {
+      const uint32_t t = load_there(&kept_here[0], uint32_t(r));
+      kept += t & 0xFFFFu;
+      seen += t >> 16;
+    }
+  } else {
+    __syncthreads();
+  }
+  kept += min(seen, ties);
+#pragma unroll
+  for (int i = 0; i < KEYS; ++i) {
+    const int p = p0 + i * kShareThreads + tid;
+    const uint32_t key = score_key(x[i]);
+    const bool sure = sure_of(p, key), tie = tie_of(p, key);
+    const uint32_t below = (1u << lane) - 1u, before = counts[i * kShareWarps + warp];
+    const uint32_t sures = __popc(__ballot_sync(kFull, sure) & below), tied = __popc(__ballot_sync(kFull, tie) & below);
+    const uint32_t tie_rank = seen + (before >> 16) + tied;
+    if (sure || (tie && tie_rank < ties)) {
+      const uint32_t to = kept + (before & 0xFFFFu) + sures + min(tie_rank, ties) - min(seen, ties);
+      out[to] = p;
+      scores[to] = x[i];
+    }
+  }
+  // what lies behind the kept ones: nobody's place, so no order matters
+  for (int p = max(p0, P.keep) + tid; p < p1; p += kShareThreads) scores[p] = 0.f;
+  if (ranks > 1) cluster_sync();                     // the others have read this CTA's words
+}
+
+cudaError_t launch_select(const SelectParams& S, int B, cudaStream_t s) {
+  // As many CTAs a head as its positions need, and up to two an SM in all while each has
+  // 2048 positions at least.
+  const int sms = device_sms() > 0 ? device_sms() : 152;
+  int ranks = 1;
+  while (ranks < kMaxRanks && (S.cap > 8192ll * ranks ||
+                               (2ll * B * S.heads * ranks <= 2ll * sms && S.cap >= 4096ll * ranks)))
+    ranks *= 2;
+  if (S.cap > 16384ll * ranks) return launch_kernel(long_kernel, dim3(unsigned(S.heads), unsigned(B)), kSelectThreads, 0, s, S);
+  const auto kernel = S.cap <= 8192ll * ranks ? select_kernel<16> : select_kernel<32>;
+  if (ranks == 1) return launch_kernel(kernel, dim3(unsigned(S.heads), unsigned(B)), kShareThreads, 0, s, S, ranks);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(ranks);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = dim3(unsigned(S.heads * ranks), unsigned(B));
+  cfg.blockDim = dim3(kShareThreads);
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return settled(cudaLaunchKernelEx(&cfg, kernel, S, ranks));
+}
+
 cudaError_t launch_move(MoveParams& P, int B, cudaStream_t s) {
-  // A row's columns are dealt to several CTAs until there are about two for each SM; at
-  // least two columns each, so that whole 32-byte sectors move.
-  const int all = P.c.dim / 8, sms = device_sms() > 0 ? device_sms() : 152;
-  int vecs = all;
-  while (vecs > 2 && 2ll * B * P.c.heads * ((all + vecs - 1) / vecs) < 2ll * sms) vecs = (vecs + 1) / 2;
-  P.vecs = vecs;
-  P.slices = (all + vecs - 1) / vecs;
-  P.by_slices = fast_div(uint32_t(P.slices));
+  // A list of more than a CTA's batch is shared by a cluster while there is about one CTA for each SM.
+  const int sms = device_sms() > 0 ? device_sms() : 152, warps = (P.width + 31) / 32;
+  const int threads = warps < kMoveThreads / 32 ? 32 * warps : kMoveThreads;
+  P.ranks = 1;
+  while (P.ranks < kMaxRanks && 2ll * B * P.c.heads * P.ranks < sms && P.width > kMoveThreads * P.ranks) P.ranks *= 2;
   P.by_page = fast_div(uint32_t(P.c.page));
-  // as many threads as the list can use
-  long long threads = (long long)((P.width + kMoveUnroll - 1) / kMoveUnroll) * vecs;
-  threads = threads > 512 ? 512 : (threads + 31) / 32 * 32;
-  return launch_kernel(move_kernel, dim3(unsigned(P.c.heads * P.slices), unsigned(B), 2), dim3(unsigned(threads)), 0, s, P);
+  const int cols = P.c.dim / 8;
+  const auto kernel = cols <= 1   ? move_kernel<1>
+                      : cols <= 2 ? move_kernel<2>
+                      : cols <= 4 ? move_kernel<4>
+                      : cols <= 8 ? move_kernel<8>
+                                  : move_kernel<16>;
+  const dim3 grid(unsigned(P.c.heads * P.ranks), unsigned(B), 2);
+  if (P.ranks == 1) return launch_kernel(kernel, grid, dim3(unsigned(threads)), 0, s, P);
+  cudaLaunchAttribute at[1];
+  at[0].id = cudaLaunchAttributeClusterDimension;
+  at[0].val.clusterDim.x = unsigned(P.ranks);
+  at[0].val.clusterDim.y = at[0].val.clusterDim.z = 1;
+  cudaLaunchConfig_t cfg = {};
+  cfg.gridDim = grid;
+  cfg.blockDim = dim3(unsigned(threads));
+  cfg.stream = s;
+  cfg.attrs = at;
+  cfg.numAttrs = 1;
+  return settled(cudaLaunchKernelEx(&cfg, kernel, static_cast<const MoveParams&>(P)));
 }
 
 }  // namespace
@@ -354,8 +608,7 @@ extern "C" int dart_kv_evict(const dart_cache_t* cache, const int32_t* lengths, 
   S.keep = keep; S.first = first; S.last = last;
   S.cap = cap < scores_width ? cap : scores_width;
   S.err = device_err;
-  cudaError_t e = launch_kernel(select_positions_kernel, dim3(unsigned(cache->heads), unsigned(B)), kSelectThreads, 0, s, S);
-  if (e != cudaSuccess) return DART_ERR_CUDA;
+  if (launch_select(S, B, s) != cudaSuccess) return DART_ERR_CUDA;
   MoveParams P;
   P.c = *cache;
   P.lengths = lengths;

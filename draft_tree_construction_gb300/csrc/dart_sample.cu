@@ -50,8 +50,8 @@ struct SampleParams {
 
 // Which 16-bit magnitudes have bins of their own: kLow .. kHigh - 1.  bf16: 2^-8 .. 2^9;
 // f16: 2^-3 .. 2^6; f32 goes by its upper half, as bf16.
-template <typename T> struct Fine { static constexpr int kLow = 119 << 7, kHigh = 136 << 7; };
-template <> struct Fine<__half> { static constexpr int kLow = 12 << 10, kHigh = 21 << 10; };
+template <typename T> struct Fine { static constexpr int kLow = 119 << 7, kHigh = 136 << 7, kInf = 0x7F80; };
+template <> struct Fine<__half> { static constexpr int kLow = 12 << 10, kHigh = 21 << 10, kInf = 0x7C00; };
 
 // 2^-j/16 and 2^-j/256 in units of 2^-64.
 __constant__ uint64_t kSixteenths[16] = {
@@ -108,18 +108,44 @@ struct Bins {
 };
 
 // ------------------------------------------------------------------- weights
-// e^((z - max) / T) in units of 2^-shift.
-struct Weigh {
-  float top, c_hi, c_lo;                     // c = log2(e) / T
+// Two forms, the top and the factor c = log2(e) / T in two parts for both; `table` has
+// 2^-j/256 in units of 2^-63, `shift` says that 1 is 2^shift.
+struct Mid {                                 // 2^-y to 2^-29 of itself
+  float top, c_hi, c_lo;
   int shift;
-  const uint64_t* table;                     // 2^-j/256, units of 2^-63
+  const uint64_t* table;
+  // y = (top - z) c: the difference exactly in two parts, the product in two
+  __device__ __forceinline__ float distance(float z, float& rest) const {
+    const float d = top - z, v = d - top, e = (top - (d - v)) - (z + v), y = d * c_hi;
+    rest = fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi);
+    return y;
+  }
+  // y = whole + j / 256 + r, |r| <= 2^-9: 2^-r - 1 in fp32 (2^-33 of 1), 2^-j/256 and their
+  // product in parts of 2^-31
+  __device__ __forceinline__ uint64_t power(float y, float rest) const {
+    constexpr float kRound = 12582912.f;     // 1.5 2^23: a sum with it is a whole number
+    const float n = fmaf(y, 256.f, kRound);
+    const int steps = __float_as_int(n) - __float_as_int(kRound);
+    const float r = fmaf(n - kRound, -0.00390625f, y) + rest;
+    const float s = r * fmaf(r, fmaf(r, -0.05550410866f, 0.2402265070f), -0.6931471806f);     // 2^-r - 1
+    const int q = __float_as_int(fmaf(s, 2147483648.f, kRound)) - __float_as_int(kRound);
+    const int a = int(uint32_t(table[steps & 255] >> 32));
+    const uint32_t w = uint32_t(a) + uint32_t(int((long long)a * q >> 31));
+    return (uint64_t(w) << (shift - 31)) >> (steps >> 8);
+  }
+  __device__ __forceinline__ uint64_t operator()(float z) const {
+    float rest;
+    const float y = distance(z, rest);
+    return y < 62.f ? power(y, rest) : 0ull;
+  }
+};
+struct Weigh : Mid {                         // to 2^-45 of the largest
   __device__ __forceinline__ uint64_t operator()(float z) const {
     if (z == top) return 1ull << shift;
-    // y = (top - z) c: the difference exactly in two parts, the product in two
-    const float d = top - z, v = d - top, e = (top - (d - v)) - (z + v);
-    const float y = d * c_hi;
+    float rest;
+    const float y = distance(z, rest);
     if (!(y < 62.f)) return 0ull;            // also top = +inf
-    const float rest = fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi);
+    if (y >= 16.f) return power(y, rest);
     // y in units of 2^-48: whole part, 256ths, remainder r
     const long long Y = (long long)(y * 281474976710656.f) + __float2ll_rn(rest * 281474976710656.f);
     if (Y <= 0) return 1ull << shift;
@@ -293,6 +319,14 @@ __device__ __forceinline__ uint64_t share_of(uint64_t sum, float f, bool up) {
   return x + (up && rest ? 1ull : 0ull);
 }
 
+// w / sum, rounded once (to 2^-40 before that): both in two floats, one step of division.
+__device__ __forceinline__ float ratio(uint64_t w, uint64_t sum) {
+  const float a = __ull2float_rz(w), c = __ull2float_rz(sum);
+  const float b = __ull2float_rn(w - uint64_t(a)), d = __ull2float_rn(sum - uint64_t(c));
+  const float q = a / c, r = fmaf(-q, c, a) + fmaf(-q, d, b);
+  return q + r / c;
+}
+
 struct Settings {
   float heat, top_p, min_p, u;
   int top_k;
@@ -331,25 +365,27 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
   constexpr uint32_t kAside = sizeof(parts->weight) / 2;
   if (tid == 0) sh->mine = 0;
   __syncthreads();
-  auto count = [&](uint32_t bits, float z) {
-    if (z > -INFINITY) atomicAdd(&bin_count[B::of(bits)], 1u);
+  // the bin by integers alone; -inf and NaN, whose magnitudes are the largest, are left out
+  auto count = [&](uint32_t bits) {          // true: a shared bin's logit
+    const int magnitude = int(bits & 0x7FFFu), d = min(max(magnitude, B::F::kLow - 1), B::F::kHigh) - (B::F::kLow - 1);
+    if (magnitude >= B::F::kInf && bits != uint32_t(B::F::kInf)) return false;
+    atomicAdd(&bin_count[bits & 0x8000u ? B::kMiddle + d : B::kMiddle - d], 1u);
+    return B::kSingle && unsigned(d - 1) >= unsigned(B::kFine);
   };
-  auto shared_bin = [&](uint32_t bits, float z) { return B::kSingle && z > -INFINITY && !B::single(B::of(bits)); };
   row.template each<kThreads>(
       [&](int i) {
-        const uint32_t bits = bits_at(logits, i);
-        count(bits, value_at(logits, i));
-        if (shared_bin(bits, value_at(logits, i))) {
+        const float z = value_at(logits, i);
+        if (z > -INFINITY && count(bits_at(logits, i))) {
           const uint32_t k = atomicAdd(&sh->mine, 1u);
-          if (k < kAside) aside[k] = uint16_t(bits);
+          if (k < kAside) aside[k] = uint16_t(bits_at(logits, i));
         }
       },
       [&](const uint4& x, int) {
         uint32_t few = 0;
 #pragma unroll
         for (int k = 0; k < Slice<T>::kPer; ++k) {
-          count(bits_of<T>(x, k), value_of<T>(x, k));
-          few |= (shared_bin(bits_of<T>(x, k), value_of<T>(x, k)) ? 1u : 0u) << k;
+          if (sizeof(T) == 4 && !(value_of<T>(x, k) > -INFINITY)) continue;        // a NaN may show in the lower half alone
+          few |= (count(bits_of<T>(x, k)) ? 1u : 0u) << k;
         }
         if (few) {
           uint32_t k = atomicAdd(&sh->mine, uint32_t(__popc(few)));
@@ -642,7 +678,7 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
   }
   if (lane == 0) {
     P.tokens[at] = token;
-    P.probs[at] = float(double(weigh(unord_f32(drawn.key))) / double(sum));
+    P.probs[at] = ratio(weigh(unord_f32(drawn.key)), sum);
   }
 }
 
@@ -812,8 +848,123 @@ __device__ __forceinline__ Verdict decide(const Settings& S, const Weigh& weigh,
   if (tid == 0) {
     i = min(i, keep - 1);
     *token = int32_t(~uint32_t(list[i]));
-    *prob = float(double(cum[i] - (i > 0 ? cum[i - 1] : above)) / double(sum));
+    *prob = ratio(cum[i] - (i > 0 ? cum[i - 1] : above), sum);
   }
+  return kDone;
+}
+
+// decide() for a list of at most 128 tokens before which nothing lies, by one warp, in its
+// registers: token 32 e + lane is the lane's e-th.  Nothing waits for another warp.
+constexpr int kShort = 128;
+__device__ __forceinline__ Verdict decide_short(const Settings& S, const Weigh& weigh, Shared* sh, const uint64_t* list,
+                                                int n, uint64_t below, uint64_t slack, bool complete, int32_t* token,
+                                                float* prob) {
+  constexpr int E = kShort / 32;
+  const int lane = threadIdx.x & 31, used = (n + 31) / 32;
+  int N = 32;
+  while (N < n) N <<= 1;
+  uint64_t x[E], run[E];
+#pragma unroll
+  for (int e = 0; e < E; ++e) x[e] = 32 * e + lane < n ? list[32 * e + lane] : 0ull;
+  for (int size = 2; size <= N; size <<= 1) {
+    for (int stride = size >> 1; stride > 0; stride >>= 1) {
+      if (stride < 32) {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          if (32 * e >= N) break;
+          const uint64_t y = __shfl_xor_sync(kFull, x[e], stride);
+          const bool keep_max = ((lane & stride) == 0) == (((32 * e + lane) & size) == 0);
+          if ((x[e] < y) == keep_max) x[e] = y;
+        }
+      } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e) {
+          const int o = e ^ (stride >> 5);
+          if (o > e && 32 * o < N) {
+            // entries of this and the other register in one lane
+#pragma unroll
+            for (int f = 0; f < E; ++f)
+              if (f == o) {
+                const bool down = ((32 * e) & size) == 0;
+                const uint64_t a = x[e], b = x[f];
+                if ((a < b) == down) {
+                  x[e] = b;
+                  x[f] = a;
+                }
+              }
+          }
+        }
+      }
+    }
+  }
+  uint64_t head = 0;
+  int kept = 0;
+#pragma unroll
+  for (int e = 0; e < E; ++e) {
+    run[e] = 0;
+    if (e >= used) continue;
+    const bool on = 32 * e + lane < n;
+    const float z = unord_f32(uint32_t(x[e] >> 32));
+    uint64_t w = on ? weigh(z) : 0ull;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const uint64_t y = __shfl_up_sync(kFull, w, o);
+      if (lane >= o) w += y;
+    }
+    run[e] = head + w;
+    head += __shfl_sync(kFull, w, 31);
+    kept += __popc(__ballot_sync(kFull, on && z >= S.least));
+  }
+  auto upto = [&](uint64_t v) {
+    int k = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e < used) k += __popc(__ballot_sync(kFull, 32 * e + lane < n && run[e] <= v));
+    return k;
+  };
+  auto sum_at = [&](int i) {                 // the running sum with token i
+    uint64_t v = 0;
+#pragma unroll
+    for (int e = 0; e < E; ++e)
+      if (e == (i >> 5)) v = __shfl_sync(kFull, run[e], i & 31);
+    return v;
+  };
+  const float units = __uint_as_float(uint32_t(127 - weigh.shift) << 23);
+  auto place = [&](uint64_t v, int& i) {
+    i = upto(v);
+    bool sure = i < n;
+    if (slack > 0) sure = sure && v + slack < head && upto(v > slack ? v - slack : 0ull) == i && upto(v + slack) == i;
+    if (!sure && lane == 0) sh->want = float(v) * units;
+    return sure;
+  };
+  int keep = n, i;
+  uint64_t sum = head + below;
+  if (S.by_k) {
+    if (n < S.top_k && !complete && !(S.by_m && !S.by_p)) {
+      if (lane == 0) sh->want = float(S.top_k);
+      return kPlan;
+    }
+    keep = min(n, S.top_k);
+    sum = sum_at(keep - 1);
+  }
+  if (S.by_p) {
+    if (!place(share_of(sum, S.top_p, true) - 1, i)) return kPlan;     // at least 1: p > 0
+    keep = min(keep, i + 1);
+  }
+  if (S.by_m) keep = max(1, min(keep, kept));
+  if (S.by_p || S.by_m) {
+    sum = sum_at(keep - 1);
+    slack = 0;
+  }
+  if (!place(min(share_of(sum, S.u, false), sum - 1), i)) return kPlan;
+  i = min(i, keep - 1);
+  const uint64_t to = sum_at(i), w = to - (i > 0 ? sum_at(i - 1) : 0ull);
+#pragma unroll
+  for (int e = 0; e < E; ++e)
+    if (32 * e + lane == i) {
+      *token = int32_t(~uint32_t(x[e]));
+      *prob = ratio(w, sum);
+    }
   return kDone;
 }
 
@@ -876,28 +1027,6 @@ struct Tail {
     return __float2ull_rn((low(sum) + high(sum)) * one);
   }
   __device__ __forceinline__ uint64_t operator()(float z) const { return __float2ull_rn(ex2_approx((z - top) * c) * one); }
-};
-
-// A weight to 2^-29 of itself, for sums of tokens whose order does not matter.  2^-y with y in
-// two parts, y = whole + j / 256 + r, |r| <= 2^-9: 2^-r - 1 in fp32 (2^-33 of 1), 2^-j/256 and
-// their product in parts of 2^-31.
-struct Mid {
-  float top, c_hi, c_lo;
-  int shift;
-  const uint64_t* table;
-  __device__ __forceinline__ uint64_t operator()(float z) const {
-    const float d = top - z, v = d - top, e = (top - (d - v)) - (z + v), y = d * c_hi;
-    if (!(y < 62.f)) return 0ull;
-    constexpr float kRound = 12582912.f;     // 1.5 2^23: a sum with it is a whole number
-    const float n = fmaf(y, 256.f, kRound);
-    const int steps = __float_as_int(n) - __float_as_int(kRound);
-    const float r = fmaf(n - kRound, -0.00390625f, y) + (fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi));
-    const float s = r * fmaf(r, fmaf(r, -0.05550410866f, 0.2402265070f), -0.6931471806f);     // 2^-r - 1
-    const int q = __float_as_int(fmaf(s, 2147483648.f, kRound)) - __float_as_int(kRound);
-    const int a = int(uint32_t(table[steps & 255] >> 32));
-    const uint32_t w = uint32_t(a) + uint32_t(int((long long)a * q >> 31));
-    return (uint64_t(w) << (shift - 31)) >> (steps >> 8);
-  }
 };
 
 constexpr int kSteps = 64;                   // of a plan, in a binary order of weight
@@ -1081,7 +1210,7 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   else if (top == INFINITY) cut = top;
   else if (reach != 0) cut = unord_f32(reach);
   if (V > NT && S.by_m && !S.by_p) cut = fmaxf(S.by_k && reach != 0 ? fmaxf(cut, S.least) : S.least, lowest);
-  const Mid mid{top, weigh.c_hi, weigh.c_lo, P.shift, sh->table};
+  const Mid& mid = weigh;
   uint64_t known = 0;
 
   // ---- the tokens near the largest, and the weight of the others
@@ -1161,11 +1290,26 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
     Verdict v = kGeneral;
     if (rank == 0) {
       const bool drawing = known != 0;
-      if (n <= kList && n > 0) {
+      uint64_t slack = 0;
+      if (S.tail && planned) slack = ((above + below + known) >> 28) + 2 * uint64_t(V);
+      else if (S.tail && !complete) slack = (below >> 17) + uint64_t(V);
+      if (n <= kShort && !planned) {
+        if (warp == 0) {
+          v = decide_short(S, weigh, sh, list, n, below, slack, complete, &P.tokens[at], &P.probs[at]);
+          if (lane == 0) {
+            if (!kAll && sizeof(T) == 2 && v != kDone) {
+              P.tokens[at] = kUndecided;
+              P.probs[at] = top;
+            }
+            sh->verdict = v;
+          }
+        }
+        if (!kAll && sizeof(T) == 2) return;
+        __syncthreads();
+        v = Verdict(sh->verdict);
+        __syncthreads();                     // read before it is written again
+      } else if (n <= kList && n > 0) {
         sort_list<NT>(list, n);
-        uint64_t slack = 0;
-        if (S.tail && planned) slack = ((above + below + known) >> 28) + 2 * uint64_t(V);
-        else if (S.tail && !complete) slack = (below >> 17) + uint64_t(V);
         v = decide<NT>(S, weigh, sh, list, cum, n, above, below, slack, complete && above == 0, known, &P.tokens[at],
                        &P.probs[at]);
       } else if (!planned && !(S.by_m && !S.by_p)) {

@@ -90,6 +90,12 @@ struct Bins {
     return bin < kMiddle ? uint32_t(kMiddle - bin + F::kLow - 1) : 0x8000u | uint32_t(bin - kMiddle + F::kLow - 1);
   }
   static __device__ __forceinline__ float value(int bin) { return to_float<T>(bits(bin)); }
+  // The distance to the next logit of the same exponent, of 16-bit ones with normal magnitudes.
+  static __device__ __forceinline__ int exponent(uint32_t bits) { return int(bits) >> (F::kInf == 0x7C00 ? 10 : 7); }   // and sign
+  static __device__ __forceinline__ float step(uint32_t bits) {
+    const int e = exponent(bits & 0x7FFFu);
+    return __uint_as_float(uint32_t(F::kInf == 0x7C00 ? e - 25 + 127 : e - 7) << 23);
+  }
   // Ordered keys of the least and largest logit that a bin can hold.
   static __device__ __forceinline__ uint32_t low_key(int bin) {
     if (bin == 0) return ord_f32(to_float<T>(F::kHigh));
@@ -140,15 +146,11 @@ struct Mid {                                 // 2^-y to 2^-29 of itself
   }
 };
 struct Weigh : Mid {                         // to 2^-45 of the largest
-  __device__ __forceinline__ uint64_t operator()(float z) const {
-    if (z == top) return 1ull << shift;
-    float rest;
-    const float y = distance(z, rest);
-    if (!(y < 62.f)) return 0ull;            // also top = +inf
-    if (y >= 16.f) return power(y, rest);
+  // 2^-(y + rest) in units of 2^-63, 0 <= y < 62
+  __device__ __forceinline__ uint64_t exact(float y, float rest) const {
     // y in units of 2^-48: whole part, 256ths, remainder r
     const long long Y = (long long)(y * 281474976710656.f) + __float2ll_rn(rest * 281474976710656.f);
-    if (Y <= 0) return 1ull << shift;
+    if (Y <= 0) return 1ull << 63;
     const int whole = int(Y >> 48), j = int(Y >> 40) & 255;
     // 2^-r = 1 - (x - x^2/2 + x^3/6 - x^4/24), x = r ln 2 < 2^-8, in units of 2^-64; the
     // powers need their upper 32 bits
@@ -160,9 +162,28 @@ struct Weigh : Mid {                         // to 2^-45 of the largest
     // a third and a twelfth by 32-bit products, to 2^-47
     const uint64_t s = x - x2 + (uint64_t(__umulhi(uint32_t(x3 >> 16), 0x55555556u)) << 16) -
                        (uint64_t(__umulhi(uint32_t(x4 >> 8), 0x15555556u)) << 8);
-    const uint64_t t = table[j], w = t - __umul64hi(t, s);
-    const int down = 63 - shift + whole;
-    return down < 64 ? (w + (1ull << (down - 1))) >> down : 0ull;
+    const uint64_t t = table[j];
+    return (t - __umul64hi(t, s)) >> whole;
+  }
+  __device__ __forceinline__ uint64_t rounded(uint64_t w) const { return (w + (1ull << (62 - shift))) >> (63 - shift); }
+  __device__ __forceinline__ uint64_t operator()(float z) const {
+    if (z == top) return 1ull << shift;
+    float rest;
+    const float y = distance(z, rest);
+    if (!(y < 62.f)) return 0ull;            // also top = +inf
+    return y < 16.f ? rounded(exact(y, rest)) : power(y, rest);
+  }
+  // In units of 2^-63, and the factor from one logit to the next one `step` below, in 2^-64.
+  __device__ __forceinline__ uint64_t fine(float z) const {
+    float rest;
+    const float y = distance(z, rest);
+    return z == top ? 1ull << 63 : y < 62.f ? exact(y, rest) : 0ull;
+  }
+  __device__ __forceinline__ uint64_t ratio(float step) const {
+    const float y = step * c_hi;
+    if (!(y < 62.f)) return 0ull;
+    const uint64_t w = exact(y, fmaf(step, c_hi, -y) + step * c_lo);
+    return w >> 63 ? ~0ull : w << 1;
   }
 };
 
@@ -250,7 +271,7 @@ struct Shared {
   uint64_t table[256];
   uint64_t warp_weight[32];
   uint64_t tails[kMaxRanks], heads[kMaxRanks];   // by rank, with the first CTA: the sums of what is not listed
-  uint64_t at_weight;                        // what a search found
+  uint64_t at_weight, end_weight;            // what a search found
   uint32_t warp_count[32];
   uint64_t tops[kMaxRanks];                  // by rank, with every CTA: the largest logit, and what at least top_k reach
   uint32_t at_count, at_bin, end_count, at_end;
@@ -260,7 +281,7 @@ struct Shared {
   float cut, cut_above;                      // tokens from cut up to below cut_above are listed
   float from, scale;                         // a plan's first distance, and its steps a binary order
   float least;                               // the smallest logit that min-p keeps
-  float want;                                // how far a plan has to reach
+  float want, behind;                        // how far a plan has to reach: the weight up to there and behind it
 };
 // With the list: two arrays of kList words (tokens; running sums, or what the others hand over, or the plan's counts).
 // In general(): the parts of a bin, then the bins.
@@ -449,7 +470,7 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
   for (int i = bin0; i < min(bin1, last_bin + 1); ++i) several |= !B::single(i) && bin_count[i] > 0;
   if (__syncthreads_or(several)) {
     if constexpr (B::kSingle) {
-      // three sums: in registers, then one after the other over the CTA
+      // three sums: in registers, then a warp at a time
       uint64_t w[3] = {0ull, 0ull, 0ull};
       auto add = [&](uint32_t bits, float z, int) {
         const int i = B::of(bits);
@@ -465,10 +486,9 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
       else
         each_logit<kThreads>(row, add);
       for (int k = 0; k < 3; ++k) {
-        uint32_t c = 0, cc;
-        uint64_t sum;
-        scan<kThreads>(sh, c, w[k], cc, sum);
-        if (tid == 0) bin_weight[k] = sum;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) w[k] += __shfl_xor_sync(kFull, w[k], o);
+        if (lane == 0 && w[k]) atomicAdd(reinterpret_cast<unsigned long long*>(&bin_weight[k]), (unsigned long long)w[k]);
       }
     } else {
       each_logit<kThreads>(row, [&](uint32_t bits, float z, int) {
@@ -484,7 +504,36 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
     return B::single(i) ? n * weigh(B::value(i)) : bin_weight[slot(i)];
   };
   weight0 = 0;
-  for (int i = bin0; i < min(bin1, last_bin + 1); ++i) weight0 += weight_of(i);
+  if constexpr (B::kSingle) {
+    // Neighbours of one exponent lie one step apart, so each weight is the last one times the
+    // same factor: a product instead of a power.  Taken afresh at least every 16 bins, so that
+    // the factor's error, 2^-49, does not add up to 2^-45.
+    int exponent = -1, steps = 0;
+    uint64_t w = 0, factor = 0;
+    const int end = mine > 0 ? min(bin1, last_bin + 1) : bin0;
+    for (int i = bin0; i < end; ++i) {
+      const uint32_t n = bin_count[i];
+      if (!B::single(i)) {
+        if (n > 0) weight0 += bin_weight[slot(i)];
+        exponent = -1;
+        continue;
+      }
+      const uint32_t bits = B::bits(i);
+      const int e = B::exponent(bits);
+      if (e != exponent || ++steps == 16) {
+        if (B::value(i) > weigh.top) continue;     // nothing lies there, and no weight to go on from
+        w = weigh.fine(B::value(i));
+        if (e != exponent) factor = weigh.ratio(B::step(bits));
+        exponent = e;
+        steps = 0;
+      } else {
+        w = __umul64hi(w, factor);
+      }
+      weight0 += n * weigh.rounded(w);
+    }
+  } else {
+    for (int i = bin0; i < min(bin1, last_bin + 1); ++i) weight0 += weight_of(i);
+  }
   uint64_t own = weight0;
   {
     uint32_t c = 0, cc;
@@ -506,9 +555,14 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
     int bin = int(sh->at_bin);
     at.count = sh->at_count;
     at.weight = sh->at_weight;
-    // every warp looks at that thread's bins
+    // every warp looks at that thread's bins.  (The sum over a thread's bins may be some last
+    // bits more than that of its bins one by one: then the last of them takes what is left.)
     const int end = min(bin + kPer, B::kCount);
-    for (int i0 = bin; i0 < end; i0 += 32) {
+    int last = bin;
+    Place last_at = at;
+    uint64_t last_weight = 0;
+    bool found = false;
+    for (int i0 = bin; i0 < end && !found; i0 += 32) {
       const int i = i0 + lane;
       uint32_t c = i < end ? bin_count[i] : 0u;
       uint64_t w = i < end && i <= last_bin ? weight_of(i) : 0ull;
@@ -524,14 +578,21 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
         }
       }
       const uint32_t hit = __ballot_sync(kFull, by_count ? x < uint64_t(at.count) + c : x < at.weight + w);
-      const int l = hit ? __ffs(hit) - 1 : 31;
-      bin = i0 + l;
-      const uint32_t add_c = __shfl_sync(kFull, hit ? c - c1 : c, l);
-      const uint64_t add_w = __shfl_sync(kFull, hit ? w - w1 : w, l);
-      at.count += add_c;
-      at.weight += add_w;
-      if (hit) break;
+      const uint32_t some = __ballot_sync(kFull, by_count ? c1 > 0 : w1 > 0);
+      found = hit != 0;
+      if (hit || some) {
+        const int l = hit ? __ffs(hit) - 1 : 31 - __clz(some);
+        last = i0 + l;
+        last_at.count = at.count + __shfl_sync(kFull, c - c1, l);
+        last_at.weight = at.weight + __shfl_sync(kFull, w - w1, l);
+        last_weight = __shfl_sync(kFull, w1, l);
+      }
+      at.count += __shfl_sync(kFull, c, 31);
+      at.weight += __shfl_sync(kFull, w, 31);
     }
+    bin = last;
+    at = last_at;
+    if (!found) x = at.weight + last_weight - 1;
     at.key = B::high_key(bin);
     if (!B::single(bin)) {
       // divided again until a part is one value
@@ -815,7 +876,10 @@ __device__ __forceinline__ Verdict decide(const Settings& S, const Weigh& weigh,
     if (slack > 0)
       sure = sure && x + slack < head && (above == 0 || x >= above + slack) && upto(x > slack ? x - slack : 0ull) == i &&
              upto(x + slack) == i;
-    if (!sure && tid == 0) sh->want = float(x) * units;
+    if (!sure && tid == 0) {
+      sh->want = float(x) * units;
+      sh->behind = float(head + below - x) * units;
+    }
     return sure;
   };
   int keep = n, i;
@@ -934,7 +998,10 @@ __device__ __forceinline__ Verdict decide_short(const Settings& S, const Weigh& 
     i = upto(v);
     bool sure = i < n;
     if (slack > 0) sure = sure && v + slack < head && upto(v > slack ? v - slack : 0ull) == i && upto(v + slack) == i;
-    if (!sure && lane == 0) sh->want = float(v) * units;
+    if (!sure && lane == 0) {
+      sh->want = float(v) * units;
+      sh->behind = float(head + below - v) * units;
+    }
     return sure;
   };
   int keep = n, i;
@@ -1322,7 +1389,7 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
     }
     // ---- how far down the list has to go: counts by distance from the largest
     float from = 0.f, scale = float(kSteps);
-    uint64_t base = 0;                       // the weight before `from`, here in parts of 2^-30 of the largest
+    uint64_t base = 0, after = 0;            // the weights before and behind a plan's steps, here in parts of 2^-38 of the largest
     for (int level = 0;; ++level) {
       if (kAll && ranks > 1) {
         if (rank == 0 && tid < int(ranks)) {
@@ -1350,7 +1417,7 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
         uint64_t parts = 0, all_parts;
         // a step's weight is off by half a step's 2^(1/scale) at most
         auto weight = [&](uint32_t n, int e) {
-          return uint64_t(float(n) * ex2_approx(-from - (float(tid * kEach + e) + 0.5f) / scale) * 1073741824.f);
+          return uint64_t(float(n) * ex2_approx(-from - (float(tid * kEach + e) + 0.5f) / scale) * 0x1p38f);
         };
         for (int e = 0; e < kEach; ++e) {
           const int i = tid * kEach + e;
@@ -1360,15 +1427,23 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
           parts += weight(own[e], e);
         }
         scan<NT>(sh, count, parts, total, all_parts);
-        const float want = sh->want;
-        const float share = want >= 0.f ? want : (S.by_p ? S.top_p : fminf(fmaxf(S.u, 0.f), 1.f)) * float(all_parts) * 0x1p-30f;
-        // the first step within 1/512 of the place, and the first that is behind it by as much
-        const uint64_t goal = uint64_t(share * 1073741824.f), off = (goal >> 9) + 1;
+        // The first step that comes within 1/512 of the place, and the first that is behind it by
+        // as much: of the weight before it or of the weight behind it, whichever is less (both are
+        // known to more than the steps are).
+        const uint64_t whole = base + all_parts + after;
+        float want = sh->want, behind = sh->behind;
+        if (want < 0.f) {
+          want = (S.by_p ? S.top_p : fminf(fmaxf(S.u, 0.f), 1.f)) * float(whole) * 0x1p-38f;
+          behind = float(whole) * 0x1p-38f - want;
+        }
+        const bool low = behind < want;      // then places are told by what is behind them
+        const uint64_t goal = uint64_t(fmaxf(low ? behind : want, 0.f) * 0x1p38f), off = (goal >> 9) + 1;
         if (tid == 0) {
           sh->at_bin = sh->at_count = 0;
           sh->at_weight = base;
           sh->at_end = uint32_t(kList - 1);
           sh->end_count = total;
+          sh->end_weight = base + all_parts;
         }
         __syncthreads();
         uint32_t c = count;
@@ -1376,11 +1451,14 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
         for (int e = 0; e < kEach; ++e) {
           const uint64_t next = w + weight(own[e], e);
           const uint32_t upto = c + own[e];
-          if (S.by_k ? c < uint32_t(S.top_k) && upto >= uint32_t(S.top_k) : w <= goal + off && next > goal + off) {
+          const bool from_here = low ? whole - w >= goal + off && whole - next < goal + off : w + off <= goal && next + off > goal;
+          const bool to_here = low ? whole - w + off > goal && whole - next + off <= goal : w <= goal + off && next > goal + off;
+          if (S.by_k ? c < uint32_t(S.top_k) && upto >= uint32_t(S.top_k) : to_here) {
             sh->at_end = uint32_t(tid * kEach + e);
             sh->end_count = upto;
+            sh->end_weight = next;
           }
-          if (!S.by_k && w + off <= goal && next + off > goal) {
+          if (!S.by_k && from_here) {
             sh->at_bin = uint32_t(tid * kEach + e);
             sh->at_count = c;
             sh->at_weight = w;
@@ -1404,6 +1482,7 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
         if (v == kRefine) {
           // the same steps again, 2048 parts of them
           base = sh->at_weight;
+          after = whole - sh->end_weight;
           from += float(begin) / scale;
           scale *= float(kList / (end + 1 - begin));
         }

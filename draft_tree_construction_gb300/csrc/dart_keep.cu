@@ -322,6 +322,12 @@ __device__ __forceinline__ uint4 load_four_there(const uint32_t* p, uint32_t ran
   return x;
 }
 
+__device__ __forceinline__ void store_four_there(const uint32_t* p, uint32_t rank, const uint4& x) {
+  uint32_t at;
+  asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(at) : "r"(smem_u32(p)), "r"(rank));
+  asm volatile("st.shared::cluster.v4.u32 [%0], {%1,%2,%3,%4};" :: "r"(at), "r"(x.x), "r"(x.y), "r"(x.z), "r"(x.w) : "memory");
+}
+
 constexpr int kShareThreads = 512, kShareWarps = kShareThreads / 32, kMaxRanks = 8;
 
 // Exclusive prefix over 512 threads; total receives the sum.
@@ -349,6 +355,7 @@ __device__ __forceinline__ uint32_t share_exclusive(uint32_t x, uint32_t* warp_s
 template <int KEYS>
 __global__ void __launch_bounds__(kShareThreads, KEYS <= 16 ? 2 : 1) select_kernel(const SelectParams P, int ranks) {
   __shared__ alignas(16) uint32_t bins[2][2048];     // of a level and the next, which is cleared while others read the first
+  __shared__ alignas(16) uint32_t sums[2048];        // a cluster's bins together
   __shared__ uint32_t warp_sums[kShareWarps];
   __shared__ uint32_t found[2], kept_here[2];
   __shared__ uint32_t counts[KEYS * kShareWarps];    // kept below 16, ties above, of each batch and warp
@@ -399,27 +406,27 @@ __global__ void __launch_bounds__(kShareThreads, KEYS <= 16 ? 2 : 1) select_kern
       }
       if (ranks > 1) cluster_sync();
       else __syncthreads();
-      // from the largest bin down: thread t owns the four from 2047 - 4 t on
-      uint32_t n[4], sum = 0;
-      {
-        const uint32_t* four = &here[2044 - 4 * tid];
-        uint4 all = make_uint4(0, 0, 0, 0), part[kMaxRanks];
-        if (ranks > 1) {
+      // A cluster's CTAs each add up their part of the bins over all of them and hand the sums to
+      // all (when each added up all bins for itself, a level took twice as long).
+      if (ranks > 1) {
+        const int part = 2048 / ranks, first = rank * part;
+        for (int i = 4 * tid; i < part; i += 4 * kShareThreads) {
+          uint4 all = make_uint4(0, 0, 0, 0), from[kMaxRanks];
 #pragma unroll
           for (int r = 0; r < kMaxRanks; ++r)
-            if (r < ranks) part[r] = load_four_there(four, uint32_t(r));
+            if (r < ranks) from[r] = load_four_there(&here[first + i], uint32_t(r));
 #pragma unroll
           for (int r = 0; r < kMaxRanks; ++r)
-            if (r < ranks) all = make_uint4(all.x + part[r].x, all.y + part[r].y, all.z + part[r].z, all.w + part[r].w);
-        } else {
-          all = *reinterpret_cast<const uint4*>(four);
+            if (r < ranks) all = make_uint4(all.x + from[r].x, all.y + from[r].y, all.z + from[r].z, all.w + from[r].w);
+#pragma unroll
+          for (int r = 0; r < kMaxRanks; ++r)
+            if (r < ranks) store_four_there(&sums[first + i], uint32_t(r), all);
         }
-        n[0] = all.w;
-        n[1] = all.z;
-        n[2] = all.y;
-        n[3] = all.x;
-        sum = all.x + all.y + all.z + all.w;
+        cluster_sync();
       }
+      // from the largest bin down: thread t owns the four from 2047 - 4 t on
+      const uint4 four = *reinterpret_cast<const uint4*>(&(ranks > 1 ? sums : here)[2044 - 4 * tid]);
+      const uint32_t n[4] = {four.w, four.z, four.y, four.x}, sum = four.x + four.y + four.z + four.w;
       if (level < 2)
         for (int i = tid; i < 2048; i += kShareThreads) bins[(level + 1) & 1][i] = 0;
       uint32_t total;

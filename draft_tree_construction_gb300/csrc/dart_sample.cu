@@ -273,7 +273,7 @@ struct Shared {
   uint64_t tails[kMaxRanks], heads[kMaxRanks];   // by rank, with the first CTA: the sums of what is not listed
   uint64_t at_weight, end_weight;            // what a search found
   uint32_t warp_count[32];
-  uint64_t tops[kMaxRanks];                  // by rank, with every CTA: the largest logit, and what at least top_k reach
+  uint64_t tops[kMaxRanks];                  // by rank, with every CTA: the largest logit, and what its part of top_k reaches
   uint32_t at_count, at_bin, end_count, at_end;
   uint32_t mine, others;                     // tokens listed by this CTA, and handed over to it
   uint32_t first;                            // greedy: the first place of the largest logit
@@ -840,7 +840,7 @@ __device__ __forceinline__ uint32_t block_sum(Shared* sh, uint32_t x) {
 template <int NT>
 __device__ __forceinline__ Verdict decide(const Settings& S, const Weigh& weigh, Shared* sh, const uint64_t* list,
                                           uint64_t* cum, int n, uint64_t above, uint64_t below, uint64_t slack,
-                                          bool complete, uint64_t& known, int32_t* token, float* prob) {
+                                          bool complete, float cut, uint64_t& known, int32_t* token, float* prob) {
   constexpr int kEach = kList / NT;
   const int tid = threadIdx.x, each = (n + NT - 1) / NT, i0 = tid * each;
   uint64_t run[kEach], w = 0, head;
@@ -894,11 +894,15 @@ __device__ __forceinline__ Verdict decide(const Settings& S, const Weigh& weigh,
       __syncthreads();
       sum = cum[keep - 1];
     }
+    // tokens that min-p keeps; all of them are listed where the list goes down to its limit
+    const int most = S.by_m ? max(1, each <= 1 ? int(__syncthreads_count(kept)) : int(block_sum<NT>(sh, kept))) : n;
     if (S.by_p) {
-      if (!place(share_of(sum, S.top_p, true) - 1, i)) return kPlan;   // at least 1: p > 0
-      keep = min(keep, i + 1);
+      const uint64_t x = share_of(sum, S.top_p, true) - 1;             // at least 1: p > 0
+      if (place(x, i)) keep = min(keep, i + 1);
+      // wherever the share is reached, min-p ends before it
+      else if (!(S.by_m && S.least >= cut && above == 0 && x >= slack && upto(x - slack) >= most)) return kPlan;
     }
-    if (S.by_m) keep = max(1, min(keep, each <= 1 ? int(__syncthreads_count(kept)) : int(block_sum<NT>(sh, kept))));
+    if (S.by_m) keep = min(keep, most);
     if (S.by_p || S.by_m) {
       __syncthreads();
       sum = cum[keep - 1];
@@ -921,8 +925,8 @@ __device__ __forceinline__ Verdict decide(const Settings& S, const Weigh& weigh,
 // registers: token 32 e + lane is the lane's e-th.  Nothing waits for another warp.
 constexpr int kShort = 128;
 __device__ __forceinline__ Verdict decide_short(const Settings& S, const Weigh& weigh, Shared* sh, const uint64_t* list,
-                                                int n, uint64_t below, uint64_t slack, bool complete, int32_t* token,
-                                                float* prob) {
+                                                int n, uint64_t below, uint64_t slack, bool complete, float cut,
+                                                int32_t* token, float* prob) {
   constexpr int E = kShort / 32;
   const int lane = threadIdx.x & 31, used = (n + 31) / 32;
   int N = 32;
@@ -1014,11 +1018,13 @@ __device__ __forceinline__ Verdict decide_short(const Settings& S, const Weigh& 
     keep = min(n, S.top_k);
     sum = sum_at(keep - 1);
   }
-  if (S.by_p) {
-    if (!place(share_of(sum, S.top_p, true) - 1, i)) return kPlan;     // at least 1: p > 0
-    keep = min(keep, i + 1);
+  const int most = S.by_m ? max(1, kept) : n;
+  if (S.by_p) {                              // as in decide()
+    const uint64_t v = share_of(sum, S.top_p, true) - 1;
+    if (place(v, i)) keep = min(keep, i + 1);
+    else if (!(S.by_m && S.least >= cut && v >= slack && upto(v - slack) >= most)) return kPlan;
   }
-  if (S.by_m) keep = max(1, min(keep, kept));
+  if (S.by_m) keep = min(keep, most);
   if (S.by_p || S.by_m) {
     sum = sum_at(keep - 1);
     slack = 0;
@@ -1197,13 +1203,15 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   __syncthreads();
   best = __reduce_max_sync(kFull, sh->warp_count[lane % (NT / 32)]);
   // Each thread has the maxima of two disjoint parts of the row, so what top_k of those
-  // maxima reach is reached by top_k tokens: the list need not go further down.
+  // maxima reach is reached by top_k tokens: the list need not go further down.  CTAs that
+  // share a row each look for their part of top_k, and the lowest answer holds for all.
   uint32_t reach = 0;
-  if (!greedy && S.by_k && S.top_k <= 2 * NT) {
+  const int enough_here = (S.top_k + int(ranks) - 1) / int(ranks);
+  if (!greedy && S.by_k && enough_here <= 2 * NT) {
     float lo = unord_f32(best) - 32.f * binary, hi = unord_f32(best);
-    const bool two = S.top_k > NT / 2;       // for few the larger one of each thread serves
+    const bool two = enough_here > NT / 2;   // for few the larger one of each thread serves
     auto enough = [&](float x) {
-      return __syncthreads_count(mine >= x) + (two ? __syncthreads_count(rest >= x) : 0) >= S.top_k;
+      return __syncthreads_count(mine >= x) + (two ? __syncthreads_count(rest >= x) : 0) >= enough_here;
     };
     if (enough(fmaxf(lo, lowest))) {
       lo = fmaxf(lo, lowest);
@@ -1221,7 +1229,7 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
     sync();
     const uint64_t x = sh->tops[lane % ranks];
     best = __reduce_max_sync(kFull, uint32_t(x >> 32));
-    reach = __reduce_max_sync(kFull, uint32_t(x));
+    reach = __reduce_min_sync(kFull, uint32_t(x));       // 0 where one of them has none
   }
   top = unord_f32(best);
   if (top == -INFINITY) {                    // nothing is left to draw from
@@ -1316,6 +1324,10 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
           } while (hits);
         }
       });
+  // Whether a list that does not decide is made again where a plan says: of 16-bit logits
+  // general() is quicker (100 thousand cycles for 200 with 32000 of them), but for the first
+  // top_k of a large vocabulary (4 x 497 rows of 151936, top_k 1000 for some: 424 us for 362).
+  const bool plans = sizeof(T) == 4 || (ranks == 1 && S.by_k && V > 65536);
   bool planned = false;
   for (;;) {
     // ---- the list and the sums come together, and what they decide
@@ -1341,6 +1353,8 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
           if (from + i < uint32_t(kList)) put64(there(&cum[from + i], 0), list[i]);
       }
       sync();
+      // what a row of 16-bit logits needs beyond its list, the first CTA does alone
+      if (rank != 0 && sizeof(T) == 2) return;
       if (rank == 0) {
         const int others = int(sh->others);
         if (n + others <= kList)
@@ -1362,22 +1376,22 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
       else if (S.tail && !complete) slack = (below >> 17) + uint64_t(V);
       if (n <= kShort && !planned) {
         if (warp == 0) {
-          v = decide_short(S, weigh, sh, list, n, below, slack, complete, &P.tokens[at], &P.probs[at]);
+          v = decide_short(S, weigh, sh, list, n, below, slack, complete, cut, &P.tokens[at], &P.probs[at]);
           if (lane == 0) {
-            if (!kAll && sizeof(T) == 2 && v != kDone) {
+            if (!kAll && !plans && v != kDone) {
               P.tokens[at] = kUndecided;
               P.probs[at] = top;
             }
             sh->verdict = v;
           }
         }
-        if (!kAll && sizeof(T) == 2) return;
+        if (!kAll && !plans) return;
         __syncthreads();
         v = Verdict(sh->verdict);
         __syncthreads();                     // read before it is written again
       } else if (n <= kList && n > 0) {
         sort_list<NT>(list, n);
-        v = decide<NT>(S, weigh, sh, list, cum, n, above, below, slack, complete && above == 0, known, &P.tokens[at],
+        v = decide<NT>(S, weigh, sh, list, cum, n, above, below, slack, complete && above == 0, cut, known, &P.tokens[at],
                        &P.probs[at]);
       } else if (!planned && !(S.by_m && !S.by_p)) {
         v = kPlan;                           // by what the histogram says
@@ -1385,13 +1399,13 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
       }
       // once more at most for the share, and once for the draw
       if (v == kPlan && planned && (drawing || known == 0)) v = kGeneral;
-      if (v == kPlan && sizeof(T) == 2) v = kGeneral;        // whose histogram is quicker than what follows
+      if (v == kPlan && !plans) v = kGeneral;
     }
     // ---- how far down the list has to go: counts by distance from the largest
     float from = 0.f, scale = float(kSteps);
     uint64_t base = 0, after = 0;            // the weights before and behind a plan's steps, here in parts of 2^-38 of the largest
     for (int level = 0;; ++level) {
-      if (kAll && ranks > 1) {
+      if (kAll && ranks > 1 && sizeof(T) != 2) {
         if (rank == 0 && tid < int(ranks)) {
           put32(there(&sh->verdict, tid), v);
           put32(there(&sh->from, tid), __float_as_uint(from));

@@ -158,7 +158,8 @@ def test_flat_and_peaked_rows(D, dtype, spread):
     for B, R, V in ((2, 2, 151936), (1, 6, 33333), (2, 80, 9001)):
         z, u = _logits(B, R, V, dtype, seed=int(spread * 10), scale=spread)
         for kw in ({}, dict(p=[0.95]), dict(p=[0.995], heat=[1.5]), dict(k=[1500]), dict(k=[3000], p=[0.9]),
-                   dict(m=[0.001]), dict(m=[0.0001], p=[0.9]), dict(heat=[8.0], k=[50])):
+                   dict(m=[0.001]), dict(m=[0.0001], p=[0.9]), dict(heat=[8.0], k=[50]), dict(m=[0.02], p=[0.99]),
+                   dict(m=[0.05], p=[0.999], heat=[1.5]), dict(k=[1000], p=[0.95], m=[0.001])):
             _check(D, z, u, **{key: x * B for key, x in kw.items()})
 
 

@@ -1184,37 +1184,44 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   // a binary order of weight in logits
   const float binary = fminf(0.69314718055994531f * S.heat, 3.4028235e38f);
 
-  // ---- the largest logit
-  float top = -INFINITY, part = -INFINITY;   // of the thread's odd vectors, of its even ones
-  {
-    bool odd = false;
-    row.template each<NT>([&](int i) { top = fmaxf(top, value_at(logits, i)); },
-                          [&](const uint4& x, int) {
-                            const float m = max_of<T>(x);
-                            if (odd) top = fmaxf(top, m);
-                            else part = fmaxf(part, m);
-                            odd = !odd;
-                          });
+  // ---- the largest logit, and those of the thread's eight parts of the row
+  constexpr int kGroups = 8;
+  float most[kGroups], mine = -INFINITY;
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) most[u] = -INFINITY;
+  if (row.first && tid < row.head) most[0] = fmaxf(most[0], value_at(logits, tid));
+  if (row.last && row.tail + tid < V) most[0] = fmaxf(most[0], value_at(logits, row.tail + tid));
+  for (int v = row.v0 + tid; v < row.v1; v += NT * kGroups) {
+    uint4 x[kGroups];
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u)
+      if (v + u * NT < row.v1) x[u] = __ldg(row.body + v + u * NT);
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u)
+      if (v + u * NT < row.v1) most[u] = fmaxf(most[u], max_of<T>(x[u]));
   }
-  const float mine = fmaxf(top, part), rest = fminf(top, part);
+#pragma unroll
+  for (int u = 0; u < kGroups; ++u) mine = fmaxf(mine, most[u]);
+  float top;
   uint32_t best = __reduce_max_sync(kFull, ord_f32(mine));
   if (lane == 0) sh->warp_count[warp] = best;
   if (!greedy) fill_table(sh);
   __syncthreads();
   best = __reduce_max_sync(kFull, sh->warp_count[lane % (NT / 32)]);
-  // Each thread has the maxima of two disjoint parts of the row, so what top_k of those
-  // maxima reach is reached by top_k tokens: the list need not go further down.  CTAs that
-  // share a row each look for their part of top_k, and the lowest answer holds for all.
+  // What top_k of the maxima of disjoint parts of the row reach is reached by top_k tokens:
+  // the list need not go further down.  CTAs that share a row each look for their part of
+  // top_k, and the lowest answer holds for all.
   uint32_t reach = 0;
   const int enough_here = (S.top_k + int(ranks) - 1) / int(ranks);
-  if (!greedy && S.by_k && enough_here <= 2 * NT) {
-    float lo = unord_f32(best) - 32.f * binary, hi = unord_f32(best);
-    const bool two = enough_here > NT / 2;   // for few the larger one of each thread serves
+  if (!greedy && S.by_k && enough_here <= kGroups / 2 * NT) {
+    float lo = fmaxf(unord_f32(best) - 32.f * binary, lowest), hi = unord_f32(best);
     auto enough = [&](float x) {
-      return __syncthreads_count(mine >= x) + (two ? __syncthreads_count(rest >= x) : 0) >= enough_here;
+      uint32_t n = 0;
+#pragma unroll
+      for (int u = 0; u < kGroups; ++u) n += most[u] >= x;
+      return int(block_sum<NT>(sh, n)) >= enough_here;
     };
-    if (enough(fmaxf(lo, lowest))) {
-      lo = fmaxf(lo, lowest);
+    if (enough(lo)) {
       for (int i = 0; i < 10; ++i) {
         const float mid = 0.5f * (lo + hi);
         if (enough(mid)) lo = mid;

@@ -1104,7 +1104,7 @@ struct Tail {
 
 constexpr int kSteps = 64;                   // of a plan, in a binary order of weight
 constexpr float kNear = 12.f;                // binary orders that are listed at first
-constexpr int32_t kUndecided = -2;           // a row's token until general() has drawn it
+constexpr int32_t kUndecided = -2, kTaken = -3;    // a row's token until general() has drawn it
 
 // The settings of a row's sequence, and the weights' factor: log2(e) / heat in two parts,
 // each step's remainder carried on.
@@ -1549,29 +1549,59 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   }
 }
 
-// The rows that sample_kernel left undecided.
+// The rows that sample_kernel left undecided.  They come in runs (a sequence's settings are
+// those of all of its rows), so a CTA takes one at a time, from the part of the rows that is
+// its own at first and then from the others', and marks it as taken in its token; of a part's
+// open rows each CTA tries another one.
 template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) rest_kernel(const SampleParams P) {
   asm volatile("griddepcontrol.wait;" ::: "memory");
   extern __shared__ __align__(16) unsigned char smem[];
+  __shared__ long long row;
   Shared* sh = reinterpret_cast<Shared*>(smem);
-  for (long long at = blockIdx.x; at < P.rows; at += gridDim.x) {
-    if (P.tokens[at] != kUndecided) continue;
-    __syncthreads();                         // the token is read before it is written, and the row before is done
-    const Asked asked = settings_of(P, at, P.V);
-    Settings S = asked.S;
-    Weigh weigh;
-    weigh.top = P.probs[at];
-    weigh.shift = P.shift;
-    weigh.table = sh->table;
-    weigh.c_hi = asked.c_hi;
-    weigh.c_lo = asked.c_lo;
-    fill_table(sh);
-    if (S.by_m && threadIdx.x == 0) sh->least = least_of(S, weigh.top);
-    __syncthreads();
-    if (S.by_m) S.least = sh->least;
-    general<T>(P, static_cast<const T*>(P.logits) + at * P.stride, at, weigh, S, sh, reinterpret_cast<unsigned char*>(sh + 1));
-    __syncthreads();
+  constexpr int kEach = 4, kPart = kThreads * kEach;
+  const int tid = threadIdx.x;
+  const long long parts = (P.rows + kPart - 1) / kPart;
+  for (long long i = 0; i < parts; ++i) {
+    const long long at0 = (blockIdx.x + i) % parts * kPart;
+    for (uint32_t turn = blockIdx.x;; ++turn) {
+      uint32_t open = 0;
+#pragma unroll
+      for (int e = 0; e < kEach; ++e) {
+        const long long at = at0 + tid * kEach + e;
+        if (at < P.rows && __ldcg(P.tokens + at) == kUndecided) open |= 1u << e;
+      }
+      const uint32_t here = __popc(open);
+      uint32_t rank = here, total;
+      uint64_t none = 0, zero;
+      scan<kThreads>(sh, rank, none, total, zero);
+      if (total == 0) break;
+      uint32_t want = turn * 2654435761u % total;
+      if (rank <= want && want < rank + here) {
+        for (want -= rank; want > 0; --want) open &= open - 1;
+        const long long at = at0 + tid * kEach + __ffs(open) - 1;
+        row = atomicCAS(P.tokens + at, kUndecided, kTaken) == kUndecided ? at : -1;
+      }
+      __syncthreads();
+      const long long at = row;
+      if (at >= 0) {
+        const Asked asked = settings_of(P, at, P.V);
+        Settings S = asked.S;
+        Weigh weigh;
+        weigh.top = P.probs[at];
+        weigh.shift = P.shift;
+        weigh.table = sh->table;
+        weigh.c_hi = asked.c_hi;
+        weigh.c_lo = asked.c_lo;
+        fill_table(sh);
+        if (S.by_m && tid == 0) sh->least = least_of(S, weigh.top);
+        __syncthreads();
+        if (S.by_m) S.least = sh->least;
+        general<T>(P, static_cast<const T*>(P.logits) + at * P.stride, at, weigh, S, sh,
+                   reinterpret_cast<unsigned char*>(sh + 1));
+      }
+      __syncthreads();
+    }
   }
 }
 

@@ -24,7 +24,7 @@
 // once, into registers; each level is a histogram in shared memory, which the cluster's
 // CTAs read from one another, and a scan.  Then every warp counts what it keeps by ballots,
 // one scan gives all places, and the list and the scores, which have all been read by then,
-// are written.  Latency bounds it.  Sequences beyond what registers hold (131072 positions
+// are written.  Latency bounds it.  Sequences beyond what registers hold (163840 positions
 // a head) are read again at every level by one CTA (long_kernel).
 #include "dart_launch.h"
 
@@ -353,7 +353,7 @@ __device__ __forceinline__ uint32_t share_exclusive(uint32_t x, uint32_t* warp_s
 }
 
 template <int KEYS>
-__global__ void __launch_bounds__(kShareThreads, KEYS <= 16 ? 2 : 1) select_kernel(const SelectParams P, int ranks) {
+__global__ void __launch_bounds__(kShareThreads, KEYS <= 20 ? 2 : 1) select_kernel(const SelectParams P, int ranks) {
   __shared__ alignas(16) uint32_t bins[2][2048];     // of a level and the next, which is cleared while others read the first
   __shared__ alignas(16) uint32_t sums[2048];        // a cluster's bins together
   __shared__ uint32_t warp_sums[kShareWarps];
@@ -450,13 +450,17 @@ __global__ void __launch_bounds__(kShareThreads, KEYS <= 16 ? 2 : 1) select_kern
   auto tie_of = [&](int p, uint32_t key) { return p < p1 && p >= lo && p < hi && ties > 0 && key == prefix; };
 #pragma unroll
   for (int i = 0; i < KEYS; ++i) {
+    if (p0 + i * kShareThreads >= p1) {
+      if (lane == 0) counts[i * kShareWarps + warp] = 0;
+      continue;
+    }
     const int p = p0 + i * kShareThreads + tid;
     const uint32_t key = score_key(x[i]);
     const uint32_t sure = __ballot_sync(kFull, sure_of(p, key)), tie = __ballot_sync(kFull, tie_of(p, key));
     if (lane == 0) counts[i * kShareWarps + warp] = uint32_t(__popc(sure)) | uint32_t(__popc(tie)) << 16;
   }
   __syncthreads();
-  // places of the batches' warps: both sums of at most 16384 in one word
+  // places of the batches' warps: both sums of at most 20480 in one word
   constexpr int kEach = (KEYS * kShareWarps + kShareThreads - 1) / kShareThreads;
   uint32_t own[kEach], sum = 0, total;
 #pragma unroll
@@ -487,6 +491,7 @@ __global__ void __launch_bounds__(kShareThreads, KEYS <= 16 ? 2 : 1) select_kern
   kept += min(seen, ties);
 #pragma unroll
   for (int i = 0; i < KEYS; ++i) {
+    if (p0 + i * kShareThreads >= p1) break;
     const int p = p0 + i * kShareThreads + tid;
     const uint32_t key = score_key(x[i]);
     const bool sure = sure_of(p, key), tie = tie_of(p, key);
@@ -509,11 +514,11 @@ cudaError_t launch_select(const SelectParams& S, int B, cudaStream_t s) {
   // 2048 positions at least.
   const int sms = device_sms() > 0 ? device_sms() : 152;
   int ranks = 1;
-  while (ranks < kMaxRanks && (S.cap > 8192ll * ranks ||
+  while (ranks < kMaxRanks && (S.cap > kShareThreads * 20ll * ranks ||
                                (2ll * B * S.heads * ranks <= 2ll * sms && S.cap >= 4096ll * ranks)))
     ranks *= 2;
-  if (S.cap > 16384ll * ranks) return launch_kernel(long_kernel, dim3(unsigned(S.heads), unsigned(B)), kSelectThreads, 0, s, S);
-  const auto kernel = S.cap <= 8192ll * ranks ? select_kernel<16> : select_kernel<32>;
+  if (S.cap > kShareThreads * 40ll * ranks) return launch_kernel(long_kernel, dim3(unsigned(S.heads), unsigned(B)), kSelectThreads, 0, s, S);
+  const auto kernel = S.cap <= kShareThreads * 20ll * ranks ? select_kernel<20> : select_kernel<40>;
   if (ranks == 1) return launch_kernel(kernel, dim3(unsigned(S.heads), unsigned(B)), kShareThreads, 0, s, S, ranks);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;

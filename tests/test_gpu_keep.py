@@ -176,7 +176,10 @@ def test_evict_unusual_scores(D, kind):
     _evict(D, "bf16", [3000, 2500], 2, 16, 8, s, 1100, 3, 10)
 
 
-@pytest.mark.parametrize("B,heads,keep,length", [(1, 1, 20000, 40000), (1, 8, 4096, 9001), (40, 4, 300, 1000)])
+# one CTA a head and clusters of them, either number of scores a thread, and more than the registers of eight hold
+@pytest.mark.parametrize("B,heads,keep,length", [(1, 1, 20000, 40000), (1, 8, 4096, 9001), (40, 4, 300, 1000),
+                                                 (1, 2, 50000, 100001), (1, 1, 1000, 163840), (1, 1, 70000, 163900),
+                                                 (100, 2, 5000, 10235), (40, 8, 700, 10300)])
 def test_evict_sizes(D, B, heads, keep, length):
     g = torch.Generator().manual_seed(keep)
     _evict(D, "f16", [length - 3 * b for b in range(B)], heads, 32, 64,

@@ -163,6 +163,78 @@ def test_flat_and_peaked_rows(D, dtype, spread):
             _check(D, z, u, **{key: x * B for key, x in kw.items()})
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows", [1, 2, 18, 19, 20, 37, 38, 39, 75, 77, 151, 153, 303, 304, 305, 400])
+def test_numbers_of_rows(D, dtype, rows):
+    """Rows shared by eight CTAs and by fewer, rows with a CTA each, and rows that CTAs take one after another."""
+    z, u = _logits(1, rows, 33000, dtype, seed=rows, scale=1.0)
+    _check(D, z, u, p=[0.9])
+
+
+# rows that their largest tokens decide, rows whose sums reach far down, and both next to one another
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("kind", ["peaked", "flat", "both", "constant", "quantised"])
+def test_many_rows(D, dtype, kind):
+    B, R, V = 8, 61, 4001
+    z, u = _logits(B, R, V, dtype, seed=11, scale={"peaked": 4.0, "quantised": 2.0}.get(kind, 0.7), pad=3)
+    if kind == "both":
+        z[:, ::3] *= 5.0
+    elif kind == "constant":
+        z = torch.full_like(z, -1.5)
+    elif kind == "quantised":
+        z = z.round()
+    _check(D, z, u)
+    _check(D, z, u, heat=[0.0, 0.3, 0.8, 1.0, 1.3, 3.0, 50.0, math.inf], k=[0, 40, 2500, 0, 0, 1, 900, 0],
+           p=[1.0, 0.9, 1.0, 0.999, 0.95, 0.5, 0.9999, 0.3], m=[0.0, 0.0, 0.0, 0.01, 0.0, 0.2, 1e-5, 0.0])
+    _check(D, z, u, heat=[1.0, 0.7] * 4, m=[0.001, 0.05, 0.0, 1.0] * 2)
+    _check(D, z, u, k=[1, 7, 129, 500, 1024, 1025, 2048, 4001])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_many_long_rows(D, dtype):
+    """Vocabularies beyond 2^16, and more rows than are in flight at once."""
+    B, R, V = 2, 153, 70001
+    z, u = _logits(B, R, V, dtype, seed=12, scale=0.8)
+    _check(D, z, u, heat=[1.0, 2.0], p=[0.9, 0.99])
+    _check(D, z, u, heat=[1.0, 1.2], k=[30000, 200], p=[0.98, 1.0])
+    _check(D, z, u, m=[0.0, 0.01])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+def test_many_rows_with_nothing_and_with_infinities(D, dtype):
+    z, u = _logits(1, 320, 601, dtype, seed=13, scale=0.7)
+    z[0, 0::7] = -math.inf
+    z[0, 1::7] = math.nan
+    z[0, 2::7, ::2] = -math.inf
+    z[0, 3::7, 5] = math.inf
+    z[0, 4::7, :600] = -math.inf
+    z[0, 5::7, 1:] = torch.finfo(DT[dtype]).min
+    for kw in ({}, dict(p=[0.9]), dict(k=[3], m=[0.1]), dict(k=[400]), dict(heat=[0.0]), dict(heat=[math.inf], p=[0.5])):
+        tokens = _check(D, z, u, **kw)
+        assert tokens[0, 0] == -1 and tokens[0, 1] == -1 and tokens[0, 3] == 5 and tokens[0, 4] == 600
+
+
+def test_many_rows_replayed(D):
+    """A captured call of rows of both sorts follows its inputs, and draws the same every time."""
+    z, u = _logits(2, 200, 9001, "bf16", seed=14, scale=0.7)
+    z, u = z.cuda(), u.cuda()
+    p = torch.tensor([0.95, 0.5], device="cuda")
+    heat = torch.ones(2, device="cuda")
+    g = torch.cuda.CUDAGraph()
+    D.sample_logits(z, u, temperature=heat, top_p=p)
+    with torch.cuda.graph(g):
+        out = D.sample_logits(z, u, temperature=heat, top_p=p)
+    for turn in range(4):
+        u.copy_(u.roll(1, 1))
+        z.mul_(1.25)
+        heat.mul_(0.9)
+        want = D.sample_logits(z, u, temperature=heat, top_p=p)
+        g.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out["tokens"], want["tokens"]) and torch.equal(out["probs"], want["probs"])
+        assert int(out["tokens"].min()) >= 0
+
+
 def test_ends_of_the_uniforms(D):
     z, _ = _logits(1, 6, 4000, "bf16", seed=3)
     u = torch.tensor([[0.0, 1.0 - 2.0 ** -24, 1.0, -1.0, 2.0, math.nan]])

@@ -552,7 +552,8 @@ cudaError_t launch_move(MoveParams& P, int B, cudaStream_t s) {
                       : cols <= 4 ? move_kernel<4>
                       : cols <= 8 ? move_kernel<8>
                                   : move_kernel<16>;
-  const dim3 grid(unsigned(P.c.heads * P.ranks), unsigned(B), 2);
+  // values that are the keys themselves move once
+  const dim3 grid(unsigned(P.c.heads * P.ranks), unsigned(B), P.c.k == P.c.v ? 1 : 2);
   if (P.ranks == 1) return launch_kernel(kernel, grid, dim3(unsigned(threads)), 0, s, P);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -565,6 +566,11 @@ cudaError_t launch_move(MoveParams& P, int B, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   return settled(cudaLaunchKernelEx(&cfg, kernel, static_cast<const MoveParams&>(P)));
+}
+
+// One memory for keys and values is one set of rows.
+bool same_or_apart(const dart_cache_t& c) {
+  return c.k != c.v || (c.k_page_stride == c.v_page_stride && c.k_row_stride == c.v_row_stride && c.k_head_stride == c.v_head_stride);
 }
 
 }  // namespace
@@ -589,7 +595,7 @@ extern "C" int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, c
   if (B < 0 || B > 65535 || width < 1 || width > (1 << 30)) return DART_ERR_INVALID_ARG;
   const int rc = check_cache(cache, B);
   if (rc) return rc;
-  if (path_stride < 0 || (B > 1 && path_stride < width)) return DART_ERR_INVALID_ARG;
+  if (path_stride < 0 || (B > 1 && path_stride < width) || !same_or_apart(*cache)) return DART_ERR_INVALID_ARG;
   if (B == 0) return DART_OK;
   if (!lengths || !path || !counts || cache->pages < 1 || cache->table_width < 1) return DART_ERR_INVALID_ARG;
   MoveParams P;
@@ -614,7 +620,7 @@ extern "C" int dart_kv_evict(const dart_cache_t* cache, const int32_t* lengths, 
   const int rc = check_cache(cache, B);
   if (rc) return rc;
   if (scores_seq_stride < 0 || scores_head_stride < 0 || (cache->heads > 1 && scores_head_stride < scores_width) ||
-      (B > 1 && scores_seq_stride < scores_width))
+      (B > 1 && scores_seq_stride < scores_width) || !same_or_apart(*cache))
     return DART_ERR_INVALID_ARG;
   if (B == 0) return DART_OK;
   if (!lengths || !scores || !out_index || cache->pages < 1 || cache->table_width < 1) return DART_ERR_INVALID_ARG;

@@ -576,7 +576,8 @@ int dart_tree_accept(const int32_t* picks, const int32_t* tokens, const int32_t*
 /* Moves the rows of a path up behind one another: position lengths[b] +
  * path[b][i] of K and V, all heads, goes to lengths[b] + i for i < counts[b].
  * In place; nothing else of the cache is written.  The pages of the positions
- * written belong to one sequence only.
+ * written belong to one sequence only.  k and v are one memory, with the same
+ * strides, or do not overlap.
  *  lengths     device [B], tokens in the cache before the chunk, >= 0
  *  path        device int32 [B] rows of `width` >= 1, path_stride apart,
  *              increasing, path[i] >= i
@@ -625,7 +626,8 @@ int dart_attention_weights(const void* q, int64_t q_token_stride, int64_t q_head
  * length, become 0.  The heads of a position part ways: slot i of two heads may
  * hold different tokens, which attention does not mind.  Keys keep the rotary
  * positions they were written with, so later calls of dart_kv_append give
- * offsets from the shortened length.  A sequence's pages belong to it alone.
+ * offsets from the shortened length.  A sequence's pages belong to it alone; k
+ * and v as for dart_kv_keep.
  *  lengths     device [B], tokens in the cache
  *  scores      device float, as for dart_attention_weights
  *  keep        >= 1; first, last >= 0, first + last <= keep
@@ -678,9 +680,9 @@ int dart_device_error(const void* workspace, uint32_t* out_flags, void* stream);
 int dart_noalloc_device_error(uint32_t* out_flags, void* stream);
 
 /* Sets the number of SM clock cycles any one wait of the row pass (a bulk
- * copy landing, a slot freeing, a barrier of the CTA), of dart_tree_attention or
- * of dart_attention_weights
- * (a tile landing, a product or its operands) may take before the kernel
+ * copy landing, a slot freeing, a barrier of the CTA), of dart_tree_attention
+ * or of dart_attention_weights (a tile landing, a product or its operands) may
+ * take before the kernel
  * gives up: the CTA then ends every other wait, lets its copies in flight
  * land, sets DART_DEVERR_WAIT_TIMEOUT and returns, and its outputs are
  * invalid.  cycles <= 0 restores the default (4e9, about two seconds).  For

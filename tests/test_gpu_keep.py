@@ -112,6 +112,22 @@ def test_keep_leaves_out_what_is_wrong(D):
     assert torch.equal(kc.cpu(), want_k)
 
 
+def test_keep_of_values_that_are_the_keys(D):
+    """One memory for both moves once."""
+    rng = np.random.default_rng(6)
+    page, n = 16, 600
+    k, _, pages = refs.paged(torch.bfloat16, [900] * 3, 4, 64, page, seed=6)
+    path = np.stack([np.sort(rng.choice(n, 300, replace=False)) for _ in range(3)])
+    want = k.clone()
+    for b in range(3):
+        src, dst = 100 + torch.from_numpy(path[b]), 100 + torch.arange(300)
+        want[pages[b, dst // page].long(), dst % page] = k[pages[b, src // page].long(), src % page]
+    for _ in range(20):
+        kc = k.cuda()
+        D.kv_keep(kc, kc, pages.cuda(), _i32([100] * 3), _i32(path), _i32([300] * 3))
+        assert torch.equal(kc.cpu(), want)
+
+
 # -------------------------------------------------------------------- evict
 
 def _evict(D, dtype, lengths, heads, dim, page, scores, keep, first, last, seed=0, heads_first=False):
@@ -198,6 +214,22 @@ def test_evict_of_scores_with_strides(D):
     assert torch.equal(a["index"], b["index"]) and torch.equal(part, plain)
     before[:, 1:, 4:112] = plain
     assert torch.equal(big, before)
+
+
+def test_evict_of_values_that_are_the_keys(D):
+    lengths, keep, page = [3000, 100, 2500], 1000, 16
+    k, _, pages = refs.paged(torch.float16, lengths, 2, 128, page, seed=7)
+    scores = torch.rand((3, 2, 3000), generator=torch.Generator().manual_seed(7))
+    want = k.clone()
+    for b, x in enumerate(lengths):
+        for h in range(2):
+            kept = torch.tensor(refs.evict(scores[b, h].numpy(), x, keep, 4, 8), dtype=torch.long)
+            new = torch.arange(len(kept))
+            want[pages[b, new // page].long(), new % page, h] = k[pages[b, kept // page].long(), kept % page, h]
+    for _ in range(20):
+        kc = k.cuda()
+        D.kv_evict(kc, kc, pages.cuda(), _i32(lengths), scores.cuda(), keep, first=4, last=8)
+        assert torch.equal(kc.cpu(), want)
 
 
 def test_evict_lengths_out_of_range(D):

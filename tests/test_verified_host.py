@@ -113,6 +113,20 @@ def test_keep_argument_checks(L):
         assert _keep(L, _cache(**over), B=1) == INVALID
 
 
+def test_values_that_are_the_keys_lie_like_them(L):
+    same = _cache()
+    same.v, same.v_page_stride, same.v_row_stride, same.v_head_stride = \
+        same.k, same.k_page_stride, same.k_row_stride, same.k_head_stride
+    assert _keep(L, same) == OK and _evict(L, same) == OK
+    for name in ("v_page_stride", "v_row_stride", "v_head_stride"):
+        other = _cache()
+        other.v = other.k
+        for n in ("page", "row", "head"):
+            setattr(other, f"v_{n}_stride", getattr(other, f"k_{n}_stride"))
+        setattr(other, name, getattr(other, name) + 8)
+        assert _keep(L, other) == INVALID and _evict(L, other) == INVALID
+
+
 def test_evict_argument_checks(L):
     assert _evict(L, _cache()) == OK and _evict(L, None) == INVALID
     for kw in (dict(B=-1), dict(B=65536), dict(width=-1), dict(keep=0), dict(first=-1), dict(last=-1), dict(first=11),

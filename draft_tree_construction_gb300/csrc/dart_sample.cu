@@ -1298,7 +1298,8 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   const Tail<T> light{top, weigh.c_hi, __uint_as_float(uint32_t(127 + P.shift) << 23)};
   // short rows are listed whole; min-p alone says itself what is kept
   float cut = fmaxf(top - kNear * binary, lowest);
-  if (V <= NT || binary > 1e30f) cut = lowest;       // so the lowest value weighs nothing where it stands for none
+  // the type's lowest value, which stands for none below, has to weigh nothing
+  if (V <= NT || top - to_float<T>(kLowest2<T> & 0xFFFFu) < 64.f * binary) cut = lowest;
   else if (top == INFINITY) cut = top;
   else if (reach != 0) cut = unord_f32(reach);
   if (V > NT && S.by_m && !S.by_p) cut = fmaxf(S.by_k && reach != 0 ? fmaxf(cut, S.least) : S.least, lowest);

@@ -536,14 +536,16 @@ int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * The probability is rounded once; without any limit the sum in it holds the
  * weights below 2^-12 to 2^-18 of theirs.
  * NaN and -inf are never drawn; a row without any other logit gives token -1
- * and probability 0.  +inf is drawn before anything finite.
+ * and probability 0.  +inf is drawn before anything finite, and a difference
+ * beyond FLT_MAX counts as infinite, at any temperature.
  *  logits      device [B][R] rows of V elements, row_stride >= V apart (at most
  *              2^30), element aligned; the padding is not read.  V < 2^24,
  *              B * R < 2^31
  *  uniforms    device float [B][R], in [0, 1) (smaller counts as 0, larger draws
  *              the last kept token)
  *  temperature device float [B] or NULL (1); <= 0 or NaN: the first token of the
- *              order, probability 1
+ *              order, probability 1.  A positive one below 1.5e-30 counts as
+ *              that; above 1e30 weights are good to 2^-20 of themselves
  *  top_k       device int32 [B] or NULL; <= 0: no limit
  *  top_p       device float [B] or NULL; >= 1 or NaN: no limit, <= 0: one token
  *  min_p       device float [B] or NULL; <= 0 or NaN: no limit

@@ -214,6 +214,23 @@ def test_many_rows_with_nothing_and_with_infinities(D, dtype):
         assert tokens[0, 0] == -1 and tokens[0, 1] == -1 and tokens[0, 3] == 5 and tokens[0, 4] == 600
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("rows", [5, 310])
+def test_ends_of_the_temperatures(D, dtype, rows):
+    """The least and largest temperatures, over logits of every size; largest ones that several tokens share."""
+    g = torch.Generator().manual_seed(15)
+    n = torch.randn((1, rows, 700), generator=g)
+    n[..., ::50] = n.max()
+    u = torch.rand((1, rows), generator=g)
+    for scale in (1.0, 1e4, 1e-4) + (() if dtype == "f16" else (3e37, 1e-30)):
+        z = (n * scale).to(DT[dtype])
+        for heat in (1e-45, 1e-38, 2e-30, 1e-12, 1e12, 1e30, 3e38, math.inf):
+            if (scale < 1e-20 and heat < 1e-20) or (scale > 1e20 and 1e30 < heat < math.inf):
+                continue                      # a temperature below 1.5e-30 counts as that, above 1e30 fewer bits are right
+            _check(D, z, u, heat=[heat])
+            _check(D, z, u, heat=[heat], p=[0.7], k=[300])
+
+
 def test_many_rows_replayed(D):
     """A captured call of rows of both sorts follows its inputs, and draws the same every time."""
     z, u = _logits(2, 200, 9001, "bf16", seed=14, scale=0.7)

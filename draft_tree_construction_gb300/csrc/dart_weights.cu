@@ -24,9 +24,9 @@
 // Three tiles, a wave, are taken together: first each one's product with the first
 // block, then each one's with the second, so that the groups are all fed and a block
 // that does not stay is copied once for three tiles.
-// Blocks are whole tokens, as many as make an average sequence's blocks equal, 256 rows
-// at most (256 of a token's queries where a key head has more);
-// what the buffers of Q leave of the shared memory goes to the ring (decoding is
+// Blocks are whole tokens, as many as make an average sequence's blocks equal, 160 rows
+// at most, for which each group has an S buffer (160 of a token's queries where a key head
+// has more); what the buffers of Q leave of the shared memory goes to the ring (decoding is
 // bound by the copy of K).
 //
 // Measured (GB300, bf16, 32 + 8 heads of 128, graph-replayed):

@@ -29,15 +29,24 @@
 // has more); what the buffers of Q leave of the shared memory goes to the ring (decoding is
 // bound by the copy of K).
 //
+// -L of a block's rows lies in slots of its own, so that the next head's queries are copied
+// as soon as this head's products have ended, while its last tiles are added up.
+//
 // Measured (GB300, bf16, 32 + 8 heads of 128, graph-replayed):
 //   1 token over 4098 positions                 12.6 us: the share, the first tile and block, one chain
 //   64 x 1 token over 4100..8200 positions      140..146 us, 5.7 TB/s: the keys, once
-//   64 trees of 79 rows over ~1600 positions    106 us (floor 39): 90 without the masked tiles, 70 without
-//     the exponentials; the tensor unit and the exponential unit are each busy a third of it, for a group
-//     has one S buffer of 160 rows and waits for its next product
-//   2 x 2048 rows over 32768 positions          973 us, 1.0 PFLOP/s
-// Tried: waves of two tiles with the groups in rotation, so that the next wave's keys fit in the ring too
-// (117 us on the trees); all groups on every block, each a third of its rows (166 us).
+//   64 trees of 79 rows over ~1600 positions    101 us (floor 39): 85 without the masked tiles, 67 without
+//     the exponentials
+//   2 x 2048 rows over 32768 positions          926 us, 1.05 PFLOP/s
+// What bounds the last two: a group takes 4500 cycles for 160 rows of a tile, 3050 of them adding up
+// (three warps an SM quarter; 1920 if the exponential unit never waited), 800 waiting for the
+// product; the warp of the products is busy 670 cycles a block, for the issue waits for the
+// tensor unit, and needs 400 more between blocks.
+// Tried: waves of two tiles with the groups in rotation (117 us on the trees for 106 then), a group
+// for each block of a tile, the sums handed on (114 for 106), four S buffers of 128 rows that
+// the groups share (118 for 101: what a block costs hardly depends on its rows), all groups on every
+// block, each a third of its rows (166), lanes with four positions and a quarter of the columns,
+// which read a quarter of -L (112 for 101), one thread for all products (108 for 103).
 #include <cmath>
 #include <type_traits>
 
@@ -53,7 +62,7 @@ constexpr int kTile = 128;                           // positions of a tile
 constexpr int kTileBytes = kTile * kColBytes;        // 64 columns of them
 constexpr uint32_t kTmemCols = 512;
 constexpr int kMaxBlock = 160;                       // rows of a block: an S buffer for each group
-constexpr int kMaxStages = 12, kMaxSums = 4, kMaxQ = 4;
+constexpr int kMaxStages = 12, kMaxSums = 4, kMaxQ = 4, kSlots = 8;
 
 struct WeightParams {
   const void* q;
@@ -83,11 +92,12 @@ struct WeightParams {
 struct Shared {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
   uint64_t q_full[kMaxQ], q_empty[kMaxQ];
+  uint64_t l_full[kSlots], l_empty[kSlots];
   uint64_t s_full[kGroups * kMaxSums], s_empty[kGroups * kMaxSums];
   uint64_t drain;
   long long total, lo, hi, base;   // this CTA's share of the list, and the first unit of sequence `first`
   long long scan[kThreads / 32];
-  alignas(16) float minus_l[kMaxQ][kMaxBlock];   // -L of the rows in a Q buffer, -inf for a row that adds nothing
+  alignas(16) float minus_l[kSlots][kMaxBlock];  // -L of the rows of a block, -inf for a row that adds nothing
   alignas(16) uint32_t see[kGroups][4][kMaxBlock];   // what each row sees of a group's tile, 32 positions a word
   uint32_t tmem;
   int first;
@@ -132,11 +142,10 @@ __device__ __forceinline__ Block block_of(const WeightParams& P, const Seq& c, i
   k.rows = k.tokens * k.queries;
   return k;
 }
-// Positions that some row of block j sees end here.
-__device__ __forceinline__ int block_end(const WeightParams& P, const Seq& c, int j) {
-  const Block k = block_of(P, c, j);
-  const int last = k.t0 + k.tokens - 1;
-  return last >= c.lead ? c.S : min(c.len + last + 1, c.S);
+// The first block of which some row sees positions from p on (p < S): they all do from there.
+__device__ __forceinline__ int first_block(const WeightParams& P, const Seq& c, int p) {
+  const int token = min(max(p - c.len, 0), c.lead);       // sees p, and so do those behind it
+  return P.parts > 1 ? token * P.parts : token / P.tokens;
 }
 
 // x * c / n for c <= n <= kCtas.
@@ -226,10 +235,10 @@ struct Tour {
     }
   }
   __device__ __forceinline__ bool resident(const WeightParams& P) const { return c.blocks <= P.queries; }
-  // Whether block j is taken for the wave from tile t on: causal blocks that see nothing of
+  // The first block taken for the wave from tile t on: causal blocks that see nothing of
   // it are left out, unless the blocks stay in their buffers.
-  __device__ __forceinline__ bool uses(const WeightParams& P, int t, int j) const {
-    return resident(P) || block_end(P, c, j) > t * kTile;
+  __device__ __forceinline__ int begin_block(const WeightParams& P, int t) const {
+    return resident(P) ? 0 : first_block(P, c, t * kTile);
   }
   __device__ __forceinline__ int wave(int t) const { return min(kGroups, t1 - t); }
 };
@@ -299,7 +308,11 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
     }
     for (int i = 0; i < P.queries; ++i) {
       mbar_init(&sh->q_full[i], 1);
-      mbar_init(&sh->q_empty[i], 1 + kSumWarps);         // the products, and those who read -L
+      mbar_init(&sh->q_empty[i], 1);
+    }
+    for (int i = 0; i < kSlots; ++i) {
+      mbar_init(&sh->l_full[i], 1);
+      mbar_init(&sh->l_empty[i], kSumWarps);
     }
     for (int i = 0; i < kGroups * P.sums; ++i) {
       mbar_init(&sh->s_full[i], 1);
@@ -376,51 +389,51 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
     const uint32_t id0 = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 4) << 24);
     const uint64_t q_desc = smem_desc(smem_u32(sq), 16), k_desc = smem_desc(smem_u32(ring), 16);
     const int k_steps = (P.D + 15) / 16;
+    const uint64_t half = uint64_t(q_half >> 4);
     Ring stage, load, s[kGroups];
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
       const bool stay = w.resident(P);
+      const int blocks = w.c.blocks;
       for (int t = w.t0; t < w.t1 && ok; t += kGroups) {
-        const int tiles = w.wave(t);
+        const int tiles = w.wave(t), begin = w.begin_block(P, t);
         const bool ends = t + kGroups >= w.t1;               // the segment's last wave
-        int last = w.c.blocks - 1;
-        while (!w.uses(P, t, last)) --last;
-        bool first = true;
-        for (int j = 0; j <= last && ok; ++j) {
-          if (!w.uses(P, t, j)) continue;
+        for (int j = begin; j < blocks && ok; ++j) {
           const Ring at = stay ? load.plus(j, P.queries) : load;       // the Q load that this block came with
-          if (!stay || t == w.t0) ok = wait_warp(&sh->q_full[at.at], at.round, sh, limit);
-          const int rows = block_of(P, w.c, j).rows;
+          const int rows = P.parts == 1 && j + 1 < blocks ? P.tokens * P.G : block_of(P, w.c, j).rows;
           const uint32_t id = id0 | (uint32_t((rows + 15) / 16 * 2) << 17);
+          const uint64_t qd = q_desc + uint64_t(at.at * (q_bytes >> 4));
+          if (!stay || t == w.t0) ok = wait_warp(&sh->q_full[at.at], at.round, sh, limit);
 #pragma unroll
           for (int g = 0; g < kGroups; ++g) {
             if (g >= tiles || !ok) break;
             const Ring k_at = stage.plus(g, P.stages);
-            const uint32_t buf = uint32_t(g) * P.sums + s[g].at;
-            if (first) ok = wait_warp(&sh->k_full[k_at.at], k_at.round, sh, limit);
+            const uint32_t buf = uint32_t(g) * P.sums + s[g].at, d = tmem + buf * P.columns;
+            const uint64_t kd = k_desc + uint64_t(k_at.at * (kStageBytes >> 4));
+            if (j == begin) ok = wait_warp(&sh->k_full[k_at.at], k_at.round, sh, limit);
             ok = ok && wait_warp(&sh->s_empty[buf], s[g].round ^ 1u, sh, limit);
             if (!ok) break;
             tc_after();
             if (elect()) {
-              const uint64_t kd = k_desc + uint64_t(k_at.at * (kStageBytes >> 4));
-              const uint64_t qd = q_desc + uint64_t(at.at * (q_bytes >> 4));
+              if (k_steps == 4 * DH) {
 #pragma unroll
-              for (int k = 0; k < 4 * DH; ++k)
-                if (k < k_steps)
-                  mma_ss(tmem + buf * P.columns, kd + (((k >> 2) * kTileBytes + (k & 3) * 32) >> 4),
-                         qd + (((k >> 2) * q_half + (k & 3) * 32) >> 4), id, k > 0);
+                for (int k = 0; k < 4 * DH; ++k)
+                  mma_ss(d, kd + (((k >> 2) * kTileBytes + (k & 3) * 32) >> 4), qd + (k < 4 ? 0 : half) + (((k & 3) * 32) >> 4), id, k > 0);
+              } else {
+                for (int k = 0; k < k_steps; ++k)
+                  mma_ss(d, kd + (((k >> 2) * kTileBytes + (k & 3) * 32) >> 4), qd + (k < 4 ? 0 : half) + (((k & 3) * 32) >> 4), id, k > 0);
+              }
               tc_commit(&sh->s_full[buf]);
-              if (j == last) tc_commit(&sh->k_empty[k_at.at]);
+              if (j + 1 == blocks) tc_commit(&sh->k_empty[k_at.at]);
               if (g == tiles - 1 && (!stay || ends)) tc_commit(&sh->q_empty[at.at]);
             }
             __syncwarp();
             s[g].next(P.sums);
           }
-          first = false;
           if (!stay) load.next(P.queries);
         }
         stage = stage.plus(tiles, P.stages);
       }
-      if (stay) load = load.plus(w.c.blocks, P.queries);
+      if (stay) load = load.plus(blocks, P.queries);
     }
     // every product has ended before the tensor memory is given back
     if (elect()) tc_commit(&sh->drain);
@@ -429,7 +442,7 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
   } else if (warp == 15) {
     // ------------------------------------------------------------ row blocks
     constexpr int kPer = kMaxBlock / 32;
-    Ring load;
+    Ring load, slot;
     uint32_t loads = 0;
     auto bring = [&](int j) {
       const uint32_t buf = load.at;
@@ -442,15 +455,19 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
         const int token = P.parts == 1 ? P.by_queries.div(r) : 0, q = k.q0 + r - token * k.queries;
         l[i] = 32 * i < k.rows ? P.lse[(long long)(w.c.start + k.t0 + token) * P.Hq + w.h * P.G + q] : 0.f;
       }
-      ok = wait_warp(&sh->q_empty[buf], load.round ^ 1u, sh, limit);
+      ok = wait_warp(&sh->l_empty[slot.at], slot.round ^ 1u, sh, limit);
       if (!ok) return;
 #pragma unroll
       for (int i = 0; i < kPer; ++i)
         if (32 * i + lane < P.block) {
           const bool adds = 32 * i + lane < k.rows && fabsf(l[i]) < INFINITY;
-          sh->minus_l[buf][32 * i + lane] = adds ? -l[i] * 1.44269504088896341f : -INFINITY;
+          sh->minus_l[slot.at][32 * i + lane] = adds ? -l[i] * 1.44269504088896341f : -INFINITY;
         }
       __syncwarp();
+      if (lane == 0) mbar_arrive(&sh->l_full[slot.at]);
+      slot.next(kSlots);
+      ok = wait_warp(&sh->q_empty[buf], load.round ^ 1u, sh, limit);
+      if (!ok) return;
       // whole boxes: what lies behind the block's rows adds nothing
       if (lane == 0) mbar_expect_tx(&sh->q_full[buf], uint32_t(DH * P.tokens * P.queries_of * kColBytes));
       __syncwarp();
@@ -464,8 +481,7 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
         for (int j = 0; j < w.c.blocks && ok; ++j) bring(j);
       } else {
         for (int t = w.t0; t < w.t1 && ok; t += kGroups)
-          for (int j = 0; j < w.c.blocks && ok; ++j)
-            if (w.uses(P, t, j)) bring(j);
+          for (int j = w.begin_block(P, t); j < w.c.blocks && ok; ++j) bring(j);
       }
     }
     for (uint32_t i = loads > uint32_t(P.queries) ? loads - P.queries : 0; i < loads; ++i)
@@ -483,20 +499,19 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
       const bool stay = w.resident(P);
       float* row = P.scores + w.b * P.s_seq + w.h * P.s_head;
       for (int t = w.t0; t < w.t1; t += kGroups) {
-        // all groups see every load of Q arrive, so that none gives one up before its time
+        // all groups see every block's rows arrive, so that none gives them up before their time
         const bool here = group < w.wave(t);
         const int p0 = (t + group) * kTile, p = p0 + mine, end = min(p0 + kTile, w.c.S);
         const bool writes = here && p < w.c.S;
         float old = 0.f;
         if (writes) old = row[p];
         uint64_t sum = 0ull;
-        for (int j = 0; j < w.c.blocks; ++j) {
-          if (!w.uses(P, t, j)) continue;
-          const Ring at = stay ? load.plus(j, P.queries) : load;
-          if (!stay || t == w.t0) ok = ok && wait_warp(&sh->q_full[at.at], at.round, sh, limit);
-          if (!stay) load.next(P.queries);
+        for (int j = w.begin_block(P, t); j < w.c.blocks; ++j) {
+          const Ring at = stay ? load.plus(j, kSlots) : load;
+          if (!stay || t == w.t0) ok = ok && wait_warp(&sh->l_full[at.at], at.round, sh, limit);
+          if (!stay) load.next(kSlots);
           if (!here) {
-            if (!stay && lane == 0) mbar_arrive(&sh->q_empty[at.at]);
+            if (!stay && lane == 0) mbar_arrive(&sh->l_empty[at.at]);
             continue;
           }
           const Block k = block_of(P, w.c, j);
@@ -583,7 +598,7 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
           __syncwarp();
           if (lane == 0) {
             mbar_arrive(&sh->s_empty[buf]);
-            if (!stay) mbar_arrive(&sh->q_empty[at.at]);
+            if (!stay) mbar_arrive(&sh->l_empty[at.at]);
           }
           s.next(P.sums);
         }
@@ -592,8 +607,8 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
       if (stay) {
         __syncwarp();
         if (lane == 0)
-          for (int j = 0; j < w.c.blocks; ++j) mbar_arrive(&sh->q_empty[load.plus(j, P.queries).at]);
-        load = load.plus(w.c.blocks, P.queries);
+          for (int j = 0; j < w.c.blocks; ++j) mbar_arrive(&sh->l_empty[load.plus(j, kSlots).at]);
+        load = load.plus(w.c.blocks, kSlots);
       }
     }
   }

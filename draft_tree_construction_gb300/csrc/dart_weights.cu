@@ -13,40 +13,41 @@
 // One persistent CTA per SM (at most 152) takes an equal share of the list of
 // (sequence, key head, tile of 128 positions), a tile costing as many row blocks
 // as its sequence has.  Within a CTA:
-//   warps 12, 13  copy K tiles by TMA into a ring of swizzled stages, in turn
-//   warp 14       issues the tcgen05 products, one row block after the other
-//   warp 15       copies the row blocks of Q by TMA, a box per 64 columns (a sequence
-//                 whose blocks fit in the buffers keeps them there for all of its tiles)
-//   warps 0-11    add up the exponentials: three groups of four warps with S buffers of
-//                 their own, each every third tile (a tile's chain from the product to
+//   12 or 16 warps  add up the exponentials: three or four groups of four warps with S buffers
+//                 of their own, each every third (fourth) tile (a tile's chain from the product to
 //                 the stored score is longer than the copy of a tile, and groups that
 //                 share one wait for each other at every block)
-// Three tiles, a wave, are taken together: first each one's product with the first
+//   one warp      copies K tiles by TMA into a ring of swizzled stages
+//   two warps     issue the tcgen05 products, one row block after the other, each of every other
+//                 group: an issue waits for the tensor unit, so that one warp's barriers would pass
+//                 while nothing is computed
+//   one warp      copies the row blocks of Q by TMA, a box per 64 columns (a sequence
+//                 whose blocks fit in the buffers keeps them there for all of its tiles)
+// Three or four tiles, a wave, are taken together: first each one's product with the first
 // block, then each one's with the second, so that the groups are all fed and a block
-// that does not stay is copied once for three tiles.
+// that does not stay is copied once for all of them.
 // Blocks are whole tokens, as many as make an average sequence's blocks equal, 160 rows
-// at most, for which each group has an S buffer (160 of a token's queries where a key head
-// has more); what the buffers of Q leave of the shared memory goes to the ring (decoding is
-// bound by the copy of K).
-//
+// at most (128 with four groups), for which each group has an S buffer (or as many of a
+// token's queries where a key head has more); what the buffers of Q leave of the shared
+// memory goes to the ring (decoding is bound by the copy of K).
 // -L of a block's rows lies in slots of its own, so that the next head's queries are copied
 // as soon as this head's products have ended, while its last tiles are added up.
 //
 // Measured (GB300, bf16, 32 + 8 heads of 128, graph-replayed):
 //   1 token over 4098 positions                 12.6 us: the share, the first tile and block, one chain
-//   64 x 1 token over 4100..8200 positions      140..146 us, 5.7 TB/s: the keys, once
-//   64 trees of 79 rows over ~1600 positions    101 us (floor 39): 85 without the masked tiles, 67 without
+//   64 x 1 token over 4100..8200 positions      138..141 us, 5.85 TB/s: the keys, once
+//   64 trees of 79 rows over ~1600 positions    103 us (floor 39): 85 without the masked tiles, 68 without
 //     the exponentials
-//   2 x 2048 rows over 32768 positions          926 us, 1.05 PFLOP/s
-// What bounds the last two: a group takes 4500 cycles for 160 rows of a tile, 3050 of them adding up
-// (three warps an SM quarter; 1920 if the exponential unit never waited), 800 waiting for the
-// product; the warp of the products is busy 670 cycles a block, for the issue waits for the
-// tensor unit, and needs 400 more between blocks.
+//   32 trees of 497 rows over ~3100 positions   517 us (floor 210)
+//   2 x 2048 rows over 32768 positions          780 us, 1.24 PFLOP/s
+// What bounds the last three: adding up.  With three groups it takes one 3050 cycles for 160 rows of a
+// tile where the exponential unit alone would need 1920 for all three, and the next product comes 800
+// later; a fourth group and the second warp of products brought 925 us down to 780.
 // Tried: waves of two tiles with the groups in rotation (117 us on the trees for 106 then), a group
-// for each block of a tile, the sums handed on (114 for 106), four S buffers of 128 rows that
-// the groups share (118 for 101: what a block costs hardly depends on its rows), all groups on every
-// block, each a third of its rows (166), lanes with four positions and a quarter of the columns,
-// which read a quarter of -L (112 for 101), one thread for all products (108 for 103).
+// for each block of a tile, the sums handed on (114 for 106), four S buffers of 128 rows that three
+// groups share (118 for 103: with one warp of products a block cost much the same for any rows), all
+// groups on every block, each a third of its rows (166), lanes with four positions and a quarter of the
+// columns, which read a quarter of -L (112 for 103), one thread for all products (108 for 103).
 #include <cmath>
 #include <type_traits>
 
@@ -55,13 +56,13 @@
 namespace dart {
 namespace {
 
-constexpr int kGroups = 3, kSumWarps = 4 * kGroups, kSumThreads = kSumWarps * 32;
-constexpr int kThreads = kSumThreads + 4 * 32;
+// By groups: the threads of a CTA, and the rows of a block, an S buffer for each group.
+__host__ __device__ constexpr int threads_of(int groups) { return (4 * groups + 4) * 32; }
+__host__ __device__ constexpr int rows_of(int groups) { return groups == 3 ? 160 : 128; }
 constexpr int kCtas = 152;
 constexpr int kTile = 128;                           // positions of a tile
 constexpr int kTileBytes = kTile * kColBytes;        // 64 columns of them
 constexpr uint32_t kTmemCols = 512;
-constexpr int kMaxBlock = 160;                       // rows of a block: an S buffer for each group
 constexpr int kMaxStages = 12, kMaxSums = 4, kMaxQ = 4, kSlots = 8;
 
 struct WeightParams {
@@ -89,16 +90,17 @@ struct WeightParams {
   long long wait_limit;
 };
 
+template <int G>
 struct Shared {
   uint64_t k_full[kMaxStages], k_empty[kMaxStages];
   uint64_t q_full[kMaxQ], q_empty[kMaxQ];
   uint64_t l_full[kSlots], l_empty[kSlots];
-  uint64_t s_full[kGroups * kMaxSums], s_empty[kGroups * kMaxSums];
+  uint64_t s_full[G * kMaxSums], s_empty[G * kMaxSums];
   uint64_t drain;
   long long total, lo, hi, base;   // this CTA's share of the list, and the first unit of sequence `first`
-  long long scan[kThreads / 32];
-  alignas(16) float minus_l[kSlots][kMaxBlock];  // -L of the rows of a block, -inf for a row that adds nothing
-  alignas(16) uint32_t see[kGroups][4][kMaxBlock];   // what each row sees of a group's tile, 32 positions a word
+  long long scan[threads_of(G) / 32];
+  alignas(16) float minus_l[kSlots][rows_of(G)];  // -L of the rows of a block, -inf for a row that adds nothing
+  alignas(16) uint32_t see[G][4][rows_of(G)];   // what each row sees of a group's tile, 32 positions a word
   uint32_t tmem;
   int first;
   int dead;
@@ -154,7 +156,9 @@ __device__ __forceinline__ long long share(long long x, int c, int n) {
 }
 
 // All threads: the cost of all sequences, this CTA's share, the sequence it begins in.
-__device__ void find_share(const WeightParams& P, Shared* sh) {
+template <int G>
+__device__ void find_share(const WeightParams& P, Shared<G>* sh) {
+  constexpr int kThreads = threads_of(G);
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   long long before = 0, lo = 0;
   bool bad = false;
@@ -202,11 +206,12 @@ __device__ void find_share(const WeightParams& P, Shared* sh) {
 
 // A CTA's walk over its share, consecutive tiles of one head at a time.  A tile
 // belongs to the CTA in whose share its first block lies.
+template <int G>
 struct Tour {
   long long lin, base, hi;
   int b, h, t0, t1;
   Seq c;
-  __device__ __forceinline__ bool begin(const WeightParams& P, const Shared* sh) {
+  __device__ __forceinline__ bool begin(const WeightParams& P, const Shared<G>* sh) {
     hi = sh->hi;
     if (sh->lo >= hi) return false;
     b = sh->first;
@@ -240,7 +245,7 @@ struct Tour {
   __device__ __forceinline__ int begin_block(const WeightParams& P, int t) const {
     return resident(P) ? 0 : first_block(P, c, t * kTile);
   }
-  __device__ __forceinline__ int wave(int t) const { return min(kGroups, t1 - t); }
+  __device__ __forceinline__ int wave(int t) const { return min(G, t1 - t); }
 };
 
 // A place in a ring of n, and the parity of its round.
@@ -269,7 +274,8 @@ __device__ __forceinline__ void named_barrier(int offset = 0) {
 }
 // What the rows of block k see of the positions from p0 on, by a group's 128 threads.  Not
 // inlined: it is rare, and the sums need the registers.
-__device__ __noinline__ void look(const WeightParams& P, Shared* sh, const Seq& c, const Block& k, int b, int group, int mine,
+template <int G>
+__device__ __noinline__ void look(const WeightParams& P, Shared<G>* sh, const Seq& c, const Block& k, int b, int group, int mine,
                                   int p0, const float* minus_l) {
   const int tree = c.len + c.lead, at0 = p0 - tree, wd0 = at0 >> 5;
   for (int r = mine; r < (k.rows + 15) / 16 * 16; r += 128) {
@@ -290,35 +296,35 @@ __device__ __noinline__ void look(const WeightParams& P, Shared* sh, const Seq& 
   }
 }
 
-template <typename T, int DH>
-__global__ void __launch_bounds__(kThreads, 1)
+template <typename T, int DH, int G>
+__global__ void __launch_bounds__(threads_of(G), 1)
 weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ CUtensorMap kmap, const __grid_constant__ CUtensorMap qmap) {
-  constexpr int kStageBytes = DH * kTileBytes;
+  constexpr int kStageBytes = DH * kTileBytes, kSumWarps = 4 * G, kThreads = threads_of(G);
   extern __shared__ __align__(1024) unsigned char smem[];
   const int q_half = P.block * kColBytes, q_bytes = DH * q_half;
   unsigned char* sq = smem;                              // the buffers of Q
   unsigned char* ring = smem + P.queries * q_bytes;
-  Shared* sh = reinterpret_cast<Shared*>(ring + P.stages * kStageBytes);
+  Shared<G>* sh = reinterpret_cast<Shared<G>*>(ring + P.stages * kStageBytes);
 
   const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
   if (tid == 0) {
     for (int i = 0; i < P.stages; ++i) {
       mbar_init(&sh->k_full[i], 1);
-      mbar_init(&sh->k_empty[i], 1);
+      mbar_init(&sh->k_empty[i], 2);                     // both warps of products, the one that has none of the tile too
     }
     for (int i = 0; i < P.queries; ++i) {
       mbar_init(&sh->q_full[i], 1);
-      mbar_init(&sh->q_empty[i], 1);
+      mbar_init(&sh->q_empty[i], 2);                     // both warps of products
     }
     for (int i = 0; i < kSlots; ++i) {
       mbar_init(&sh->l_full[i], 1);
       mbar_init(&sh->l_empty[i], kSumWarps);
     }
-    for (int i = 0; i < kGroups * P.sums; ++i) {
+    for (int i = 0; i < G * P.sums; ++i) {
       mbar_init(&sh->s_full[i], 1);
       mbar_init(&sh->s_empty[i], 4);                     // the group's warps
     }
-    mbar_init(&sh->drain, 1);
+    mbar_init(&sh->drain, 2);
     fence_mbar_init();
     sh->dead = 0;
     sh->first = 0;
@@ -332,7 +338,7 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
     *reinterpret_cast<uint4*>(sq + half * q_half + copied * kColBytes + at * 16) = make_uint4(0, 0, 0, 0);
   }
   fence_async();
-  if (warp == 14) {
+  if (warp == kSumWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;"
                  :: "r"(smem_u32(&sh->tmem)), "r"(kTmemCols) : "memory");
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
@@ -344,59 +350,59 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
   tc_after();
   const uint32_t tmem = sh->tmem;
   const long long limit = P.wait_limit;
-  Tour w;
+  Tour<G> w;
   bool ok = true;
 
-  if (warp == 12 || warp == 13) {
+  if (warp == kSumWarps) {
     // -------------------------------------------------------------- K tiles
-    const uint32_t pid = uint32_t(warp - 12);
     uint32_t idx = 0;
     Ring stage;
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
       const int32_t* table = P.table + (long long)w.b * P.table_stride;
+      const int at = (lane / DH) * P.box;                  // this lane's box in a tile
+      int next = w.t0 * kTile + at < w.c.S && at < kTile ? table[P.by_page.div(w.t0 * kTile + at)] : 0;
       for (int t = w.t0; t < w.t1 && ok; ++t, ++idx, stage.next(P.stages)) {
-        if ((idx & 1u) != pid) continue;
         const int p0 = t * kTile, boxes = (min(w.c.S - p0, kTile) + P.box - 1) / P.box;
-        const int at = p0 + (lane / DH) * P.box;
         const bool mine = lane / DH < boxes;
-        int page = 0;
-        if (mine) {
-          page = table[P.by_page.div(at)];
-          if (page < 0 || page >= P.pages) {
-            set_dev_error(P.err, DART_DEVERR_CACHE);
-            page = P.pages;                  // out of the map's range: the box arrives as zeros
-          }
+        int page = next;
+        // the next tile's page is on its way meanwhile
+        if (t + 1 < w.t1 && at < kTile && p0 + kTile + at < w.c.S) next = table[P.by_page.div(p0 + kTile + at)];
+        if (mine && (page < 0 || page >= P.pages)) {
+          set_dev_error(P.err, DART_DEVERR_CACHE);
+          page = P.pages;                    // out of the map's range: the box arrives as zeros
         }
         ok = wait_warp(&sh->k_empty[stage.at], stage.round ^ 1u, sh, limit);
         if (!ok) break;
         if (lane == 0) mbar_expect_tx(&sh->k_full[stage.at], uint32_t(boxes * DH * P.box * kColBytes));
         __syncwarp();
         if (mine) {
-          const int half = lane % DH, row = at - P.by_page.div(at) * P.page;
+          const int half = lane % DH, row = p0 + at - P.by_page.div(p0 + at) * P.page;
           auto pick = [&](int i) { return P.k_slot[i] == 0 ? w.h : P.k_slot[i] == 1 ? row : page; };
-          tma_box(ring + stage.at * kStageBytes + half * kTileBytes + (lane / DH) * P.box * kColBytes, &kmap, 64 * half,
+          tma_box(ring + stage.at * kStageBytes + half * kTileBytes + at * kColBytes, &kmap, 64 * half,
                   pick(0), pick(1), pick(2), &sh->k_full[stage.at]);
         }
       }
     }
     // no copy may land after the CTA has left: the last load of each stage is waited for
     for (uint32_t i = idx > uint32_t(P.stages) ? idx - P.stages : 0; i < idx; ++i)
-      if ((i & 1u) == pid) mbar_wait_bounded(&sh->k_full[i % P.stages], (i / P.stages) & 1u, kDrainLimit);
+      mbar_wait_bounded(&sh->k_full[i % P.stages], (i / P.stages) & 1u, kDrainLimit);
     __syncwarp();
-  } else if (warp == 14) {
+  } else if (warp == kSumWarps + 1 || warp == kSumWarps + 2) {
     // ---------------------------------------------------------- tensor unit
     constexpr uint32_t type = kTypeCode<T>;
     const uint32_t id0 = (1u << 4) | (type << 7) | (type << 10) | (uint32_t(kTile >> 4) << 24);
     const uint64_t q_desc = smem_desc(smem_u32(sq), 16), k_desc = smem_desc(smem_u32(ring), 16);
     const int k_steps = (P.D + 15) / 16;
     const uint64_t half = uint64_t(q_half >> 4);
-    Ring stage, load, s[kGroups];
+    constexpr int kOwn = (G + 1) / 2;                        // this warp has every other group
+    const int own = warp - kSumWarps - 1;
+    Ring stage, load, s[kOwn];
     for (bool more = w.begin(P, sh); more && ok; more = w.next(P)) {
       const bool stay = w.resident(P);
       const int blocks = w.c.blocks;
-      for (int t = w.t0; t < w.t1 && ok; t += kGroups) {
+      for (int t = w.t0; t < w.t1 && ok; t += G) {
         const int tiles = w.wave(t), begin = w.begin_block(P, t);
-        const bool ends = t + kGroups >= w.t1;               // the segment's last wave
+        const bool ends = t + G >= w.t1;               // the segment's last wave
         for (int j = begin; j < blocks && ok; ++j) {
           const Ring at = stay ? load.plus(j, P.queries) : load;       // the Q load that this block came with
           const int rows = P.parts == 1 && j + 1 < blocks ? P.tokens * P.G : block_of(P, w.c, j).rows;
@@ -404,13 +410,14 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
           const uint64_t qd = q_desc + uint64_t(at.at * (q_bytes >> 4));
           if (!stay || t == w.t0) ok = wait_warp(&sh->q_full[at.at], at.round, sh, limit);
 #pragma unroll
-          for (int g = 0; g < kGroups; ++g) {
+          for (int i = 0; i < kOwn; ++i) {
+            const int g = 2 * i + own;
             if (g >= tiles || !ok) break;
             const Ring k_at = stage.plus(g, P.stages);
-            const uint32_t buf = uint32_t(g) * P.sums + s[g].at, d = tmem + buf * P.columns;
+            const uint32_t buf = uint32_t(g) * P.sums + s[i].at, d = tmem + buf * P.columns;
             const uint64_t kd = k_desc + uint64_t(k_at.at * (kStageBytes >> 4));
             if (j == begin) ok = wait_warp(&sh->k_full[k_at.at], k_at.round, sh, limit);
-            ok = ok && wait_warp(&sh->s_empty[buf], s[g].round ^ 1u, sh, limit);
+            ok = ok && wait_warp(&sh->s_empty[buf], s[i].round ^ 1u, sh, limit);
             if (!ok) break;
             tc_after();
             if (elect()) {
@@ -424,11 +431,20 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
               }
               tc_commit(&sh->s_full[buf]);
               if (j + 1 == blocks) tc_commit(&sh->k_empty[k_at.at]);
-              if (g == tiles - 1 && (!stay || ends)) tc_commit(&sh->q_empty[at.at]);
             }
             __syncwarp();
-            s[g].next(P.sums);
+            s[i].next(P.sums);
           }
+          if (ok && (!stay || ends) && elect()) tc_commit(&sh->q_empty[at.at]);
+          // this warp sees the other's tiles arrive and gives them up too: a stage's round is told by one
+          // bit, so neither may miss one
+          for (int g = 1 - own; j == begin && g < tiles && ok; g += 2) {
+            const Ring k_at = stage.plus(g, P.stages);
+            ok = wait_warp(&sh->k_full[k_at.at], k_at.round, sh, limit);
+            if (ok && lane == 0) mbar_arrive(&sh->k_empty[k_at.at]);
+            __syncwarp();
+          }
+          __syncwarp();
           if (!stay) load.next(P.queries);
         }
         stage = stage.plus(tiles, P.stages);
@@ -439,9 +455,9 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
     if (elect()) tc_commit(&sh->drain);
     mbar_wait_bounded(&sh->drain, 0, kDrainLimit);
     __syncwarp();
-  } else if (warp == 15) {
+  } else if (warp == kSumWarps + 3) {
     // ------------------------------------------------------------ row blocks
-    constexpr int kPer = kMaxBlock / 32;
+    constexpr int kPer = rows_of(G) / 32;
     Ring load, slot;
     uint32_t loads = 0;
     auto bring = [&](int j) {
@@ -480,7 +496,7 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
       if (w.resident(P)) {
         for (int j = 0; j < w.c.blocks && ok; ++j) bring(j);
       } else {
-        for (int t = w.t0; t < w.t1 && ok; t += kGroups)
+        for (int t = w.t0; t < w.t1 && ok; t += G)
           for (int j = w.begin_block(P, t); j < w.c.blocks && ok; ++j) bring(j);
       }
     }
@@ -498,7 +514,7 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
     for (bool more = w.begin(P, sh); more; more = w.next(P)) {
       const bool stay = w.resident(P);
       float* row = P.scores + w.b * P.s_seq + w.h * P.s_head;
-      for (int t = w.t0; t < w.t1; t += kGroups) {
+      for (int t = w.t0; t < w.t1; t += G) {
         // all groups see every block's rows arrive, so that none gives them up before their time
         const bool here = group < w.wave(t);
         const int p0 = (t + group) * kTile, p = p0 + mine, end = min(p0 + kTile, w.c.S);
@@ -557,18 +573,28 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
                 part[1] = add2(part[1], pair(ex2_approx(a2), ex2_approx(a3)));
               }
             };
-            // the next columns are on their way while these are added up
+            // with three groups the next columns are on their way while these are added up
             auto all = [&](auto&& add) {
-              float x[2][16];
-              tmem_ld16(from, x[0]);
-              for (int col = 0; col < cols; col += 32) {
-                loaded<16>(x[0]);
-                if (col + 16 < cols) tmem_ld16(from + col + 16, x[1]);
-                add(x[0], col);
-                if (col + 16 < cols) {
-                  loaded<16>(x[1]);
-                  if (col + 32 < cols) tmem_ld16(from + col + 32, x[0]);
-                  add(x[1], col + 16);
+              if constexpr (G < 4) {
+                float x[2][16];
+                tmem_ld16(from, x[0]);
+                for (int col = 0; col < cols; col += 32) {
+                  loaded<16>(x[0]);
+                  if (col + 16 < cols) tmem_ld16(from + col + 16, x[1]);
+                  add(x[0], col);
+                  if (col + 16 < cols) {
+                    loaded<16>(x[1]);
+                    if (col + 32 < cols) tmem_ld16(from + col + 32, x[0]);
+                    add(x[1], col + 16);
+                  }
+                }
+              } else {
+#pragma unroll 1
+                for (int col = 0; col < cols; col += 16) {
+                  float x[16];
+                  tmem_ld16(from + col, x);
+                  loaded<16>(x);
+                  add(x, col);
                 }
               }
             };
@@ -616,7 +642,7 @@ weights_kernel(const __grid_constant__ WeightParams P, const __grid_constant__ C
   tc_before();
   __syncthreads();
   tc_after();
-  if (warp == 14) {
+  if (warp == kSumWarps + 1) {
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" :: "r"(tmem), "r"(kTmemCols));
     if (lane == 0 && sh->dead) set_dev_error(P.err, DART_DEVERR_WAIT_TIMEOUT);
   }
@@ -638,25 +664,31 @@ bool query_map(const WeightParams& P, const dart_cache_t& c, CUtensorMap* map) {
                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <typename T, int DH>
+template <typename T, int DH, int G>
 cudaError_t launch(WeightParams& P, const CUtensorMap& km, const CUtensorMap& qm, cudaStream_t s) {
   constexpr int kStageBytes = DH * kTileBytes;
   // A wave's stages of K and one more at least, then buffers of Q so that the next head's
   // blocks can come while this one's are used, then stages again.
-  const int room = 227 * 1024 - int(sizeof(Shared)), q = P.block * DH * kColBytes;
-  P.queries = (room - (kGroups + 1) * kStageBytes) / q;
+  const int room = 227 * 1024 - int(sizeof(Shared<G>)), q = P.block * DH * kColBytes;
+  P.queries = (room - 4 * kStageBytes) / q;
   P.queries = P.queries < 2 ? 2 : P.queries > kMaxQ ? kMaxQ : P.queries;
   P.stages = (room - P.queries * q) / kStageBytes;
   P.stages = P.stages < kMaxStages ? P.stages : kMaxStages;
   P.columns = (P.block + 31) / 32 * 32;
-  P.sums = int(kTmemCols) / P.columns / kGroups;
+  P.sums = int(kTmemCols) / P.columns / G;
   P.sums = P.sums < kMaxSums ? P.sums : kMaxSums;
-  const int smem = P.queries * q + P.stages * kStageBytes + int(sizeof(Shared));
+  const int smem = P.queries * q + P.stages * kStageBytes + int(sizeof(Shared<G>));
   const cudaError_t e =
-      settled(cudaFuncSetAttribute(weights_kernel<T, DH>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      settled(cudaFuncSetAttribute(weights_kernel<T, DH, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
   if (e != cudaSuccess) return e;
   const int sms = device_sms(), ctas = sms > 0 && sms < kCtas ? sms : kCtas;
-  return launch_kernel(weights_kernel<T, DH>, ctas, kThreads, smem, s, P, km, qm);
+  return launch_kernel(weights_kernel<T, DH, G>, ctas, threads_of(G), smem, s, P, km, qm);
+}
+
+template <typename T>
+cudaError_t launch_type(WeightParams& P, int groups, const CUtensorMap& km, const CUtensorMap& qm, cudaStream_t s) {
+  if (groups == 3) return P.D <= 64 ? launch<T, 1, 3>(P, km, qm, s) : launch<T, 2, 3>(P, km, qm, s);
+  return P.D <= 64 ? launch<T, 1, 4>(P, km, qm, s) : launch<T, 2, 4>(P, km, qm, s);
 }
 
 }  // namespace
@@ -697,10 +729,15 @@ extern "C" int dart_attention_weights(const void* q, int64_t q_token_stride, int
   P.cap = (long long)c.table_width * c.page;
   if (P.cap > scores_width) P.cap = scores_width;
   P.page = c.page; P.pages = c.pages; P.box = gcd(c.page, kTile);
+  // Three groups of warps where an average sequence's rows stay in shared memory, four where they are
+  // copied again for each wave (64 trees of 79 rows 103 us for 108, 2 x 2048 rows 925 for 785).
+  const long long rows = ((long long)T + B - 1) / B * (q_heads / c.heads);
+  const int groups = rows <= (c.dim <= 64 ? 4 : 2) * rows_of(3) ? 3 : 4;
   // an average sequence's tokens in equal blocks
-  P.queries_of = P.G < kMaxBlock ? P.G : kMaxBlock;
+  const int most = rows_of(groups);
+  P.queries_of = P.G < most ? P.G : most;
   P.parts = (P.G + P.queries_of - 1) / P.queries_of;
-  const int fit = kMaxBlock / P.queries_of, tokens = int(((long long)T + B - 1) / B), blocks = (tokens + fit - 1) / fit;
+  const int fit = most / P.queries_of, tokens = int(((long long)T + B - 1) / B), blocks = (tokens + fit - 1) / fit;
   P.tokens = P.parts > 1 ? 1 : (tokens + blocks - 1) / blocks;
   P.block = (P.tokens * P.queries_of + 15) / 16 * 16;
   P.by_part = fast_div(uint32_t(P.parts));
@@ -715,8 +752,8 @@ extern "C" int dart_attention_weights(const void* q, int64_t q_token_stride, int
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   cudaError_t e;
   if (c.dtype == DART_F16)
-    e = c.dim <= 64 ? launch<__half, 1>(P, km, qm, s) : launch<__half, 2>(P, km, qm, s);
+    e = launch_type<__half>(P, groups, km, qm, s);
   else
-    e = c.dim <= 64 ? launch<__nv_bfloat16, 1>(P, km, qm, s) : launch<__nv_bfloat16, 2>(P, km, qm, s);
+    e = launch_type<__nv_bfloat16>(P, groups, km, qm, s);
   return e == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

@@ -218,13 +218,15 @@ struct Slice {
     last = rank == ranks - 1;
   }
   // All threads; one(i) of the single elements, vec(x, i) of the vectors, i the place of the (first) element.
+  // From the end on, for a row that has just been read from its beginning: the rows of all CTAs
+  // may be more than the L2 holds, and what was read last is still there (4 x 497 rows of 151936).
   template <int NT, typename F, typename G>
   __device__ __forceinline__ void each(F&& one, G&& vec) const {
-    constexpr int kUnroll = 4;
+    constexpr int kUnroll = 4, kStep = NT * kUnroll;
     const int t = threadIdx.x;
     if (first && t < head) one(t);
     if (last && tail + t < V) one(tail + t);
-    for (int v = v0 + t; v < v1; v += NT * kUnroll) {
+    for (int v = v0 + (max(v1 - v0 - 1, 0) / kStep) * kStep + t; v >= v0; v -= kStep) {
       uint4 x[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)

@@ -28,14 +28,12 @@
 // Measured (GB300, graph-replayed; the floor is one reading at the copy rate):
 //   one row of 151936 bf16, top-k and top-p      15..21 us (90 where it goes by general()): three
 //     cluster barriers, two readings, the list
-//   4 x 497 rows of 151936 bf16, all limits      176..368 us, floor 90; 148 where all rows are greedy
-//   64 x 79 rows of 32000 fp16, top-p 0.7..0.99  300..442 us, floor 48: half of it in the tenth of the
-//     rows whose sums reach far down (an integer add in shared memory takes 16 cycles a warp); 80 where
-//     all are greedy, 125 with min-p alone
-//   500 rows of 32000 fp32, temperature alone    111..203 us, floor 9.6: one wave of rows, as long as its
-//     longest; 25 with min-p alone
-#include <cmath>
-
+//   4 x 497 rows of 151936 bf16, all limits      127..349 us, floor 90; 116 where all rows are greedy
+//   64 x 79 rows of 32000 fp16, top-p 0.7..0.99  308..451 us, floor 48: half of it in the tenth of the
+//     rows whose sums reach far down (an integer add in shared memory takes 16 cycles a warp); 77 where
+//     all are greedy, 120 with min-p alone
+//   500 rows of 32000 fp32, temperature alone    109..198 us, floor 9.6: one wave of rows, as long as its
+//     longest; 22 with min-p alone
 #include "dart_launch.h"
 
 namespace dart {
@@ -218,15 +216,13 @@ struct Slice {
     last = rank == ranks - 1;
   }
   // All threads; one(i) of the single elements, vec(x, i) of the vectors, i the place of the (first) element.
-  // From the end on, for a row that has just been read from its beginning: the rows of all CTAs
-  // may be more than the L2 holds, and what was read last is still there (4 x 497 rows of 151936).
   template <int NT, typename F, typename G>
   __device__ __forceinline__ void each(F&& one, G&& vec) const {
-    constexpr int kUnroll = 4, kStep = NT * kUnroll;
+    constexpr int kUnroll = 4;
     const int t = threadIdx.x;
     if (first && t < head) one(t);
     if (last && tail + t < V) one(tail + t);
-    for (int v = v0 + (max(v1 - v0 - 1, 0) / kStep) * kStep + t; v >= v0; v -= kStep) {
+    for (int v = v0 + t; v < v1; v += NT * kUnroll) {
       uint4 x[kUnroll];
 #pragma unroll
       for (int u = 0; u < kUnroll; ++u)
@@ -1073,6 +1069,8 @@ template <> __device__ __forceinline__ uint32_t max2<__half>(uint32_t a, uint32_
 }
 template <typename T> constexpr uint32_t kLowest2 = 0xFF7FFF7Fu;        // the lowest finite value, twice
 template <> constexpr uint32_t kLowest2<__half> = 0xFBFFFBFFu;
+template <typename T> constexpr uint32_t kNone2 = 0xFF80FF80u;          // -inf, twice
+template <> constexpr uint32_t kNone2<__half> = 0xFC00FC00u;
 template <typename T>
 __device__ __forceinline__ float max_of(const uint4& x) {
   if constexpr (sizeof(T) == 2) {
@@ -1199,10 +1197,12 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   // ---- the largest logit, and those of the thread's eight parts of the row
   constexpr int kGroups = 8;
   float most[kGroups], mine = -INFINITY;
+  uint32_t most2[kGroups];                   // two at a time where they have 16 bits
 #pragma unroll
-  for (int u = 0; u < kGroups; ++u) most[u] = -INFINITY;
-  if (row.first && tid < row.head) most[0] = fmaxf(most[0], value_at(logits, tid));
-  if (row.last && row.tail + tid < V) most[0] = fmaxf(most[0], value_at(logits, row.tail + tid));
+  for (int u = 0; u < kGroups; ++u) {
+    most[u] = -INFINITY;
+    most2[u] = kNone2<T>;
+  }
   for (int v = row.v0 + tid; v < row.v1; v += NT * kGroups) {
     uint4 x[kGroups];
 #pragma unroll
@@ -1210,8 +1210,17 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
       if (v + u * NT < row.v1) x[u] = __ldg(row.body + v + u * NT);
 #pragma unroll
     for (int u = 0; u < kGroups; ++u)
-      if (v + u * NT < row.v1) most[u] = fmaxf(most[u], max_of<T>(x[u]));
+      if (v + u * NT < row.v1) {
+        if constexpr (sizeof(T) == 2) most2[u] = max2<T>(most2[u], max2<T>(max2<T>(x[u].x, x[u].y), max2<T>(x[u].z, x[u].w)));
+        else most[u] = fmaxf(most[u], max_of<T>(x[u]));
+      }
   }
+  if constexpr (sizeof(T) == 2) {
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) most[u] = fmaxf(to_float<T>(most2[u] & 0xFFFFu), to_float<T>(most2[u] >> 16));
+  }
+  if (row.first && tid < row.head) most[0] = fmaxf(most[0], value_at(logits, tid));
+  if (row.last && row.tail + tid < V) most[0] = fmaxf(most[0], value_at(logits, row.tail + tid));
 #pragma unroll
   for (int u = 0; u < kGroups; ++u) mine = fmaxf(mine, most[u]);
   float top;
@@ -1259,16 +1268,41 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
     return;
   }
 
+  // The row again, from its end on (the rows of all CTAs may be more than the L2 holds, and what was
+  // read last is still there); where what lies below z does not count, only those of the thread's
+  // eight parts of it that have a logit from z on (4 x 497 rows of 151936: top-k 210 us for 180).
+  auto again = [&](bool whole, float z, auto&& one, auto&& vec) {
+    constexpr int kUnroll = 4;
+    if (row.first && tid < row.head) one(tid);
+    if (row.last && row.tail + tid < V) one(row.tail + tid);
+    uint32_t parts = whole ? 1u : 0u;
+#pragma unroll
+    for (int u = 0; u < kGroups; ++u) parts |= (!whole && most[u] >= z ? 1u : 0u) << u;
+    const int stride = whole ? NT : NT * kGroups, step = kUnroll * stride;
+    while (parts) {
+      const int from = row.v0 + (__ffs(parts) - 1) * NT + tid;
+      parts &= parts - 1;
+      for (int v = from + (max(row.v1 - from - 1, 0) / step) * step; v >= from; v -= step) {
+        uint4 x[kUnroll];
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+          if (v + i * stride < row.v1) x[i] = __ldg(row.body + v + i * stride);
+#pragma unroll
+        for (int i = 0; i < kUnroll; ++i)
+          if (v + i * stride < row.v1) vec(x[i], row.head + (v + i * stride) * Slice<T>::kPer);
+      }
+    }
+  };
+
   if (greedy) {
     uint32_t first = 0xFFFFFFFFu;
-    if (mine == top)
-      row.template each<NT>([&](int i) { if (value_at(logits, i) == top) first = min(first, uint32_t(i)); },
-                            [&](const uint4& x, int i) {
-                              if (max_of<T>(x) != top) return;
+    again(false, top, [&](int i) { if (value_at(logits, i) == top) first = min(first, uint32_t(i)); },
+              [&](const uint4& x, int i) {
+                if (max_of<T>(x) != top) return;
 #pragma unroll
-                              for (int k = Slice<T>::kPer - 1; k >= 0; --k)
-                                if (value_of<T>(x, k) == top) first = min(first, uint32_t(i + k));
-                            });
+                for (int k = Slice<T>::kPer - 1; k >= 0; --k)
+                  if (value_of<T>(x, k) == top) first = min(first, uint32_t(i + k));
+              });
     if (first != 0xFFFFFFFFu) atomicMin(&sh->first, first);
     __syncthreads();
     first = sh->first;
@@ -1314,36 +1348,36 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   auto put = [&](float z, int i, uint32_t k) {
     if (k < uint32_t(kList)) list[k] = elem_key(z, uint32_t(i));
   };
-  row.template each<NT>(
-      [&](int i) {
-        const float z = value_at(logits, i);
-        if (z >= cut) put(z, i, atomicAdd(&sh->mine, 1u));
-        else if (rest_counts && z > -INFINITY) behind += light(z);
-      },
-      [&](const uint4& x, int i) {
-        if (max_of<T>(x) < cut) {
-          if (rest_counts) behind += light(x);
-          return;
-        }
-        uint32_t hits = 0;
-        uint4 y = x;                         // without the hits
+  auto list_one = [&](int i) {
+    const float z = value_at(logits, i);
+    if (z >= cut) put(z, i, atomicAdd(&sh->mine, 1u));
+    else if (rest_counts && z > -INFINITY) behind += light(z);
+  };
+  auto list_vec = [&](const uint4& x, int i) {
+    if (max_of<T>(x) < cut) {
+      if (rest_counts) behind += light(x);
+      return;
+    }
+    uint32_t hits = 0;
+    uint4 y = x;                         // without the hits
 #pragma unroll
-        for (int k = 0; k < Slice<T>::kPer; ++k)
-          if (value_of<T>(x, k) >= cut) {
-            hits |= 1u << k;
-            uint32_t& w = (k * int(sizeof(T)) / 4 == 0) ? y.x : (k * int(sizeof(T)) / 4 == 1) ? y.y : (k * int(sizeof(T)) / 4 == 2) ? y.z : y.w;
-            w = sizeof(T) == 4 ? 0xFF7FFFFFu : k & 1 ? (w & 0xFFFFu) | (kLowest2<T> & 0xFFFF0000u) : (w & 0xFFFF0000u) | (kLowest2<T> & 0xFFFFu);
-          }
-        if (rest_counts) behind += light(y);
-        if (hits) {
-          uint32_t k = atomicAdd(&sh->mine, uint32_t(__popc(hits)));
-          do {
-            const int e = __ffs(hits) - 1;
-            hits &= hits - 1;
-            put(value_at(logits, i + e), i + e, k++);
-          } while (hits);
-        }
-      });
+    for (int k = 0; k < Slice<T>::kPer; ++k)
+      if (value_of<T>(x, k) >= cut) {
+        hits |= 1u << k;
+        uint32_t& w = (k * int(sizeof(T)) / 4 == 0) ? y.x : (k * int(sizeof(T)) / 4 == 1) ? y.y : (k * int(sizeof(T)) / 4 == 2) ? y.z : y.w;
+        w = sizeof(T) == 4 ? 0xFF7FFFFFu : k & 1 ? (w & 0xFFFFu) | (kLowest2<T> & 0xFFFF0000u) : (w & 0xFFFF0000u) | (kLowest2<T> & 0xFFFFu);
+      }
+    if (rest_counts) behind += light(y);
+    if (hits) {
+      uint32_t k = atomicAdd(&sh->mine, uint32_t(__popc(hits)));
+      do {
+        const int e = __ffs(hits) - 1;
+        hits &= hits - 1;
+        put(value_at(logits, i + e), i + e, k++);
+      } while (hits);
+    }
+  };
+  again(rest_counts, cut, list_one, list_vec);
   // Whether a list that does not decide is made again where a plan says: of 16-bit logits
   // general() is quicker (100 thousand cycles for 200 with 32000 of them), but for the first
   // top_k of a large vocabulary (4 x 497 rows of 151936, top_k 1000 for some: 424 us for 362).

@@ -28,11 +28,11 @@
 // Measured (GB300, graph-replayed; the floor is one reading at the copy rate):
 //   one row of 151936 bf16, top-k and top-p      15..21 us (90 where it goes by general()): three
 //     cluster barriers, two readings, the list
-//   4 x 497 rows of 151936 bf16, all limits      127..349 us, floor 90; 116 where all rows are greedy
-//   64 x 79 rows of 32000 fp16, top-p 0.7..0.99  308..451 us, floor 48: half of it in the tenth of the
+//   4 x 497 rows of 151936 bf16, all limits      126..349 us, floor 90; 115 where all rows are greedy
+//   64 x 79 rows of 32000 fp16, top-p 0.7..0.99  311..457 us, floor 48: half of it in the tenth of the
 //     rows whose sums reach far down (an integer add in shared memory takes 16 cycles a warp); 77 where
 //     all are greedy, 120 with min-p alone
-//   500 rows of 32000 fp32, temperature alone    109..198 us, floor 9.6: one wave of rows, as long as its
+//   500 rows of 32000 fp32, temperature alone    110..199 us, floor 9.6: one wave of rows, as long as its
 //     longest; 22 with min-p alone
 #include "dart_launch.h"
 

@@ -35,8 +35,8 @@
 //
 // Measured (GB300, bf16, 32 + 8 heads of 128, graph-replayed):
 //   1 token over 4098 positions                 12.6 us: the share, the first tile and block, one chain
-//   64 x 1 token over 4100..8200 positions      138..141 us, 5.85 TB/s: the keys, once
-//   64 trees of 79 rows over ~1600 positions    103 us (floor 39): 85 without the masked tiles, 68 without
+//   64 x 1 token over 4100..8200 positions      135..138 us, 6.0 TB/s: the keys, once
+//   64 trees of 79 rows over ~1600 positions    102 us (floor 39): 85 without the masked tiles, 68 without
 //     the exponentials
 //   32 trees of 497 rows over ~3100 positions   517 us (floor 210)
 //   2 x 2048 rows over 32768 positions          780 us, 1.24 PFLOP/s

@@ -32,8 +32,8 @@
 //   64 x 79 rows of 32000 fp16, top-p 0.7..0.99  311..457 us, floor 48: half of it in the tenth of the
 //     rows whose sums reach far down (an integer add in shared memory takes 16 cycles a warp); 77 where
 //     all are greedy, 120 with min-p alone
-//   500 rows of 32000 fp32, temperature alone    110..199 us, floor 9.6: one wave of rows, as long as its
-//     longest; 22 with min-p alone
+//   500 rows of 32000 fp32, temperature alone    89..155 us, floor 9.6: two rounds of rows, as long as their
+//     longest; 29 with min-p alone
 #include "dart_launch.h"
 
 namespace dart {
@@ -1663,9 +1663,14 @@ cudaError_t launch(SampleParams& P, cudaStream_t s) {
   cfg.stream = s;
   cfg.attrs = at;
   cfg.numAttrs = 1;
-  if (P.rows <= 2 * sms) {
+  if (P.rows <= (sizeof(T) == 4 ? 4 : 2) * sms) {
+    // Large CTAs that do all for their rows.  Up to two rows an SM: 304 bf16 rows of 32000 83 us for 106
+    // by the kernels below, 64 x 79 fp16 ones 368 for 311.  Up to four where logits have 32 bits and
+    // plans take long: 500 rows of 32000 114 us for 139, 608 with top-p 292 for 391 (with top-k 40
+    // for 27), 5000 of 2000 668 for 550.
     // Rows that do not fill the device are shared: as many CTAs a row as keep it to one round
-    // of two an SM, none with less than 4096 logits.
+    // of two an SM, none with less than 4096 logits (one row of 151936 60 us for 72 by one CTA, where
+    // it goes by general(); 20 rows 110 for 109).
     const auto kernel = sample_kernel<T, kThreads, 2, true>;
     const cudaError_t e = settled(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, large));
     if (e != cudaSuccess) return e;
@@ -1680,7 +1685,7 @@ cudaError_t launch(SampleParams& P, cudaStream_t s) {
     cfg.dynamicSmemBytes = large;
     return settled(cudaLaunchKernelEx(&cfg, kernel, static_cast<const SampleParams&>(P)));
   }
-  // Many rows: smaller CTAs, more of them an SM, so that one's sums and barriers pass while
+  // More rows: smaller CTAs, more of them an SM, so that one's sums and barriers pass while
   // others read; the few rows that their lists do not decide are left to a second kernel.
   const auto kernel = sample_kernel<T, kManyThreads, kManyCtas, false>;
   cudaError_t e = settled(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, small));

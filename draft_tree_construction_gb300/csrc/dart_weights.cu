@@ -730,7 +730,8 @@ extern "C" int dart_attention_weights(const void* q, int64_t q_token_stride, int
   if (P.cap > scores_width) P.cap = scores_width;
   P.page = c.page; P.pages = c.pages; P.box = gcd(c.page, kTile);
   // Three groups of warps where an average sequence's rows stay in shared memory, four where they are
-  // copied again for each wave (64 trees of 79 rows 103 us for 108, 2 x 2048 rows 925 for 785).
+  // copied again for each wave (three for four: 64 trees of 79 rows 103 us for 111, 2 x 512 rows over
+  // 16384 positions 124 for 108, 2 x 2048 over 32768 922 for 780).
   const long long rows = ((long long)T + B - 1) / B * (q_heads / c.heads);
   const int groups = rows <= (c.dim <= 64 ? 4 : 2) * rows_of(3) ? 3 : 4;
   // an average sequence's tokens in equal blocks

@@ -191,6 +191,17 @@ def test_many_rows(D, dtype, kind):
 
 
 @pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
+@pytest.mark.parametrize("scale", [0.7, 4.0])
+def test_more_rows_than_are_in_flight(D, dtype, scale):
+    z, u = _logits(8, 81, 4001, dtype, seed=16, scale=scale, pad=1)
+    _check(D, z, u)
+    _check(D, z, u, heat=[0.0, 0.3, 0.8, 1.0, 1.3, 3.0, 50.0, math.inf], k=[0, 40, 2500, 0, 0, 1, 900, 0],
+           p=[1.0, 0.9, 1.0, 0.999, 0.95, 0.5, 0.9999, 0.3], m=[0.0, 0.0, 0.0, 0.01, 0.0, 0.2, 1e-5, 0.0])
+    z[:, ::9] = -math.inf
+    _check(D, z, u, p=[0.98] * 8)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f16", "f32"])
 def test_many_long_rows(D, dtype):
     """Vocabularies beyond 2^16, and more rows than are in flight at once."""
     B, R, V = 2, 153, 70001

@@ -1,8 +1,8 @@
 """The steps behind a verified tree: sampling, the walk along the drawn tokens, what stays in the cache.
 
 Bindings of dart_logits_sample, dart_tree_accept, dart_kv_keep,
-dart_attention_weights and dart_kv_evict (include/darttree.h); the package
-exports the public names.
+dart_kv_keep_scored, dart_attention_weights and dart_kv_evict
+(include/darttree.h); the package exports the public names.
 """
 from __future__ import annotations
 
@@ -19,10 +19,12 @@ def declare(L):
     L.dart_logits_sample.argtypes = [P, i32, i32, i32, i64, i32, P, P, P, P, P, P, P, P]
     L.dart_tree_accept.argtypes = [P, P, P, i32, i32, i32, P, P, P, P]
     L.dart_kv_keep.argtypes = [C.POINTER(_Cache), P, P, i64, P, i32, i32, P, P, P]
+    L.dart_kv_keep_scored.argtypes = [C.POINTER(_Cache), P, P, i64, P, i32, i32, P, P, i64, i64, i32, P, P, P]
     L.dart_attention_weights.argtypes = [P, i64, i64, i32, i32, i32, P, P, P, i32, f32, C.POINTER(_Cache), P, P, i64,
                                          i64, i32, P, P]
     L.dart_kv_evict.argtypes = [C.POINTER(_Cache), P, i32, P, i64, i64, i32, i32, i32, i32, P, P, P, P]
-    for f in (L.dart_logits_sample, L.dart_tree_accept, L.dart_kv_keep, L.dart_attention_weights, L.dart_kv_evict):
+    for f in (L.dart_logits_sample, L.dart_tree_accept, L.dart_kv_keep, L.dart_kv_keep_scored, L.dart_attention_weights,
+              L.dart_kv_evict):
         f.restype = i32
 
 
@@ -39,7 +41,7 @@ def _native():
         L = lib()
         module.bind_verified(*(C.cast(f, C.c_void_p).value for f in
                                (L.dart_logits_sample, L.dart_tree_accept, L.dart_kv_keep, L.dart_attention_weights,
-                                L.dart_kv_evict)))
+                                L.dart_kv_evict, L.dart_kv_keep_scored)))
         _bound = module
     return module
 
@@ -140,22 +142,26 @@ def _one_length(lengths):
     return lengths.shape[0]
 
 
-def kv_keep(k_cache, v_cache, pages, lengths, path, counts, *, device_err=None, stream=None):
+def kv_keep(k_cache, v_cache, pages, lengths, path, counts, *, scores=None, starts=None, device_err=None, stream=None):
     """Moves a path's keys and values up behind one another (dart_kv_keep).
 
     k_cache, v_cache, pages, lengths as for kv_append (lengths: the tokens in
     the cache before the chunk), the caches written in place; path (int32 [B,
     width], increasing) and counts (int32 [B]) as tree_accept returns them.
-    Returns the new lengths, lengths + counts: one call per layer reads the old
-    ones.  device_err (int32 [>= 1], zeroed by the caller) collects the error
-    bits of what is out of range or out of order."""
+    scores (float32 [B, heads, width], from attention_weights) move with their
+    positions, in place, and become 0 from the new lengths to the chunk's end,
+    which starts (int32 [B + 1], the chunk's) tell: a cache that is ever given to
+    kv_evict needs them here (dart_kv_keep_scored).  Returns the new lengths,
+    lengths + counts: one call per layer reads the old ones.  device_err (int32
+    [>= 1], zeroed by the caller) collects the error bits of what is out of range
+    or out of order."""
     if stream is None and k_cache.is_cuda:
-        made = _native().keep(k_cache, v_cache, pages, lengths, path, counts, device_err)
+        made = _native().keep(k_cache, v_cache, pages, lengths, path, counts, scores, starts, device_err)
         if made is not None:
             return made
     torch = _torch()
-    dev = _one_device(("k_cache", "v_cache", "pages", "lengths", "path", "counts", "device_err"),
-                      (k_cache, v_cache, pages, lengths, path, counts, device_err))
+    dev = _one_device(("k_cache", "v_cache", "pages", "lengths", "path", "counts", "scores", "starts", "device_err"),
+                      (k_cache, v_cache, pages, lengths, path, counts, scores, starts, device_err))
     B = _one_length(lengths)
     c = _cache(k_cache, v_cache, pages, B)
     if path.dim() != 2 or path.shape[0] != B or path.shape[1] < 1:
@@ -167,17 +173,24 @@ def kv_keep(k_cache, v_cache, pages, lengths, path, counts, *, device_err=None, 
     if step < width:
         raise DartError("the rows of path overlap")
     _check_tensor(counts, "counts", torch.int32, (B,))
+    if (scores is None) != (starts is None):
+        raise DartError("scores need the chunk's starts, and starts are of use with scores alone")
+    if scores is not None:
+        s0, s1 = _scores(scores, B, c.heads)
+        _check_tensor(starts, "starts", torch.int32, (B + 1,))
     if device_err is not None:
         _check_error_word(device_err)
+    name = "dart_kv_keep" if scores is None else "dart_kv_keep_scored"
     scope = _enter(dev, stream)
     try:
         out = torch.empty(B, dtype=torch.int32, device=dev)
-        rc = lib().dart_kv_keep(C.byref(c), lengths.data_ptr(), path.data_ptr(), step, counts.data_ptr(), B, width,
-                                out.data_ptr(), _at(device_err), _stream(stream, dev))
+        gathered = () if scores is None else (starts.data_ptr(), scores.data_ptr(), s0, s1, scores.shape[2])
+        rc = getattr(lib(), name)(C.byref(c), lengths.data_ptr(), path.data_ptr(), step, counts.data_ptr(), B, width,
+                                  *gathered, out.data_ptr(), _at(device_err), _stream(stream, dev))
     finally:
         _leave(scope)
     if rc:
-        _check(rc, "dart_kv_keep")
+        _check(rc, name)
     return out
 
 

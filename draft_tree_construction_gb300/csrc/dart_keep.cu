@@ -16,7 +16,8 @@
 // of K or V, so nobody reads what another one writes.  A lane finds where one of the
 // warp's 32 rows lies; then the warp moves them, whole rows at a time (when each thread
 // found its own 16 bytes, that was 150 instructions for each, and they bound it).  Memory
-// bounds it: two passes over the rows that move.
+// bounds it: two passes over the rows that move.  What the positions have gathered goes with
+// them in one more layer of the grid, a CTA a head.
 //
 // K10 (select_kernel): the m-th largest score is found by a radix search over the
 // ordered keys, 11 + 11 + 10 bits.  One CTA per (sequence, head), or a cluster of up to
@@ -95,6 +96,11 @@ struct MoveParams {
   int width, relative;              // relative: positions count from lengths[b]
   int cap;                          // positions that a sequence can have
   int ranks;                        // CTAs that share a head's list
+  // what each position has gathered, moved with it by the CTAs of grid layer `scored` (-1: none)
+  int scored, s_width;
+  float* scores;
+  long long s_seq, s_head;
+  const int32_t* starts;            // [B + 1]: the chunk's end
   FastDiv by_page;
   uint32_t* err;
 };
@@ -104,6 +110,30 @@ __device__ __forceinline__ void cluster_sync() {
 }
 
 constexpr int kMoveThreads = 256;
+
+// The scores of one head, by one CTA: those of the list's positions move up as the rows do, those from
+// there to the chunk's end become 0, so that the next chunk's positions begin with nothing.
+__device__ __forceinline__ void move_scores(const MoveParams& P, const int32_t* list, int b, int head, int base, int count) {
+  const int tid = threadIdx.x, threads = blockDim.x;
+  float* row = P.scores + b * P.s_seq + head * P.s_head;
+  const long long end = (long long)base + ((long long)P.starts[b + 1] - P.starts[b]);
+  bool bad = end > P.s_width;
+  for (int i0 = 0; i0 < count; i0 += threads) {
+    const int i = i0 + tid, from = i < count ? list[i] : i, before = i < count && i > 0 ? list[i - 1] : -1;
+    bool moves = from != i;
+    if (moves && (from < i || from <= before || from >= P.cap - base)) {
+      bad = true;
+      moves = false;
+    }
+    if (moves && base + from >= P.s_width) bad = true;         // has no score: what it leaves is 0
+    const float x = moves && base + from < P.s_width ? row[base + from] : 0.f;
+    __syncthreads();                                           // as for the rows: a batch is read before it is written
+    if (moves && base + i < P.s_width) row[base + i] = x;
+  }
+  const int stop = int(max(min(end, (long long)P.s_width), 0ll));
+  for (int p = base + count + tid; p < stop; p += threads) row[p] = 0.f;
+  if (bad) set_dev_error(P.err, DART_DEVERR_CACHE);
+}
 
 // COLS: 16-byte columns of a row, rounded up to a power of two; a warp moves 32 / COLS rows at once.
 template <int COLS>
@@ -124,6 +154,10 @@ __global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const MoveParams 
     return;
   }
   if (first && P.out_lengths) P.out_lengths[b] = P.relative ? len + count : count;
+  if (int(blockIdx.z) == P.scored) {
+    if (rank == 0) move_scores(P, list, b, head, base, count);
+    return;
+  }
   if (!P.relative && count == len) return;          // everything stays where it is
   const long long ps = blockIdx.z ? P.c.v_page_stride : P.c.k_page_stride,
                   rs = blockIdx.z ? P.c.v_row_stride : P.c.k_row_stride,
@@ -555,7 +589,9 @@ cudaError_t launch_move(MoveParams& P, int B, cudaStream_t s) {
                       : cols <= 8 ? move_kernel<8>
                                   : move_kernel<16>;
   // values that are the keys themselves move once
-  const dim3 grid(unsigned(P.c.heads * P.ranks), unsigned(B), P.c.k == P.c.v ? 1 : 2);
+  const unsigned layers = P.c.k == P.c.v ? 1 : 2;
+  P.scored = P.scores ? int(layers) : -1;
+  const dim3 grid(unsigned(P.c.heads * P.ranks), unsigned(B), layers + (P.scores ? 1 : 0));
   if (P.ranks == 1) return launch_kernel(kernel, grid, dim3(unsigned(threads)), 0, s, P);
   cudaLaunchAttribute at[1];
   at[0].id = cudaLaunchAttributeClusterDimension;
@@ -590,10 +626,12 @@ extern "C" int dart_tree_accept(const int32_t* picks, const int32_t* tokens, con
   return e == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }
 
-extern "C" int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, const int32_t* path, int64_t path_stride,
-                            const int32_t* counts, int B, int width, int32_t* out_lengths, uint32_t* device_err,
-                            void* stream) {
-  using namespace dart;
+namespace dart {
+namespace {
+
+int keep(const dart_cache_t* cache, const int32_t* lengths, const int32_t* path, int64_t path_stride,
+         const int32_t* counts, int B, int width, const int32_t* starts, float* scores, int64_t scores_seq_stride,
+         int64_t scores_head_stride, int scores_width, int32_t* out_lengths, uint32_t* device_err, void* stream) {
   if (B < 0 || B > 65535 || width < 1 || width > (1 << 30)) return DART_ERR_INVALID_ARG;
   const int rc = check_cache(cache, B);
   if (rc) return rc;
@@ -608,8 +646,36 @@ extern "C" int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, c
   P.out_lengths = out_lengths;
   P.width = width; P.relative = 1;
   P.cap = cache->table_width * cache->page;
+  P.scores = scores; P.s_seq = scores_seq_stride; P.s_head = scores_head_stride; P.s_width = scores_width;
+  P.starts = starts;
   P.err = device_err;
   return launch_move(P, B, static_cast<cudaStream_t>(stream)) == cudaSuccess ? DART_OK : DART_ERR_CUDA;
+}
+
+bool scores_fit(const dart_cache_t& c, int B, int64_t seq_stride, int64_t head_stride, int width) {
+  return width >= 0 && seq_stride >= 0 && head_stride >= 0 && (c.heads <= 1 || head_stride >= width) &&
+         (B <= 1 || seq_stride >= width);
+}
+
+}  // namespace
+}  // namespace dart
+
+extern "C" int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, const int32_t* path, int64_t path_stride,
+                            const int32_t* counts, int B, int width, int32_t* out_lengths, uint32_t* device_err,
+                            void* stream) {
+  return dart::keep(cache, lengths, path, path_stride, counts, B, width, nullptr, nullptr, 0, 0, 0, out_lengths,
+                    device_err, stream);
+}
+
+extern "C" int dart_kv_keep_scored(const dart_cache_t* cache, const int32_t* lengths, const int32_t* path,
+                                   int64_t path_stride, const int32_t* counts, int B, int width, const int32_t* starts,
+                                   float* scores, int64_t scores_seq_stride, int64_t scores_head_stride,
+                                   int scores_width, int32_t* out_lengths, uint32_t* device_err, void* stream) {
+  using namespace dart;
+  if (cache && !scores_fit(*cache, B, scores_seq_stride, scores_head_stride, scores_width)) return DART_ERR_INVALID_ARG;
+  if (B > 0 && (!starts || !scores)) return DART_ERR_INVALID_ARG;
+  return keep(cache, lengths, path, path_stride, counts, B, width, starts, scores, scores_seq_stride,
+              scores_head_stride, scores_width, out_lengths, device_err, stream);
 }
 
 extern "C" int dart_kv_evict(const dart_cache_t* cache, const int32_t* lengths, int B, float* scores,
@@ -621,8 +687,7 @@ extern "C" int dart_kv_evict(const dart_cache_t* cache, const int32_t* lengths, 
     return DART_ERR_INVALID_ARG;
   const int rc = check_cache(cache, B);
   if (rc) return rc;
-  if (scores_seq_stride < 0 || scores_head_stride < 0 || (cache->heads > 1 && scores_head_stride < scores_width) ||
-      (B > 1 && scores_seq_stride < scores_width) || !same_or_apart(*cache))
+  if (!scores_fit(*cache, B, scores_seq_stride, scores_head_stride, scores_width) || !same_or_apart(*cache))
     return DART_ERR_INVALID_ARG;
   if (B == 0) return DART_OK;
   if (!lengths || !scores || !out_index || cache->pages < 1 || cache->table_width < 1) return DART_ERR_INVALID_ARG;
@@ -643,6 +708,7 @@ extern "C" int dart_kv_evict(const dart_cache_t* cache, const int32_t* lengths, 
   P.out_lengths = out_lengths;
   P.width = keep; P.relative = 0;
   P.cap = int(S.cap);
+  P.scores = nullptr;
   P.err = device_err;
   return launch_move(P, B, s) == cudaSuccess ? DART_OK : DART_ERR_CUDA;
 }

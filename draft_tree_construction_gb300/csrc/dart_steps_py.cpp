@@ -37,6 +37,7 @@ decltype(&dart_tree_accept) tree_accept = nullptr;
 decltype(&dart_kv_keep) kv_keep = nullptr;
 decltype(&dart_attention_weights) attention_weights = nullptr;
 decltype(&dart_kv_evict) kv_evict = nullptr;
+decltype(&dart_kv_keep_scored) kv_keep_scored = nullptr;
 PyObject* check = nullptr;          // check(code, name) raises the package's error; also from bind()
 
 PyObject* failed(int rc, const char* name) {
@@ -408,33 +409,6 @@ int64_t lengths_of(const Tensor* lengths) {
   return B > 0 && B < INT_MAX && is(lengths, at::kInt, B) && lengths->is_contiguous() ? B : -1;
 }
 
-// (k_cache, v_cache, pages, lengths, path, counts, device_err) -> lengths
-PyObject* keep(PyObject*, PyObject* const* args, Py_ssize_t count) {
-  HANDLE_TH_ERRORS
-  if (count != 7) Py_RETURN_NONE;
-  Taker take;
-  const Tensor *k_cache = take(args[0]), *v_cache = take(args[1]), *pages = take(args[2]), *lengths = take(args[3]),
-               *path = take(args[4]), *counts = take(args[5]), *err = take(args[6]);
-  const int64_t B = lengths_of(lengths);
-  dart_cache_t c;
-  if (!take.ok || !kv_keep || B < 0 || !path || !counts || !cache_of(k_cache, v_cache, pages, B, &c) ||
-      !error_word(err) || !is(counts, at::kInt, B) || path->dim() != 2 || path->size(0) != B || path->size(1) < 1 ||
-      path->size(1) > INT_MAX || path->scalar_type() != at::kInt || (path->size(1) > 1 && path->stride(1) != 1))
-    Py_RETURN_NONE;
-  const int64_t width = path->size(1), step = B > 1 ? path->stride(0) : width;
-  if (step < width) Py_RETURN_NONE;
-  Tensor out = at::empty({B}, lengths->options());
-  int rc;
-  void* const stream = current_stream(take.device);
-  Py_BEGIN_ALLOW_THREADS
-  rc = kv_keep(&c, at_of<int32_t>(lengths), at_of<int32_t>(path), step, at_of<int32_t>(counts), int(B), int(width),
-               at_of<int32_t>(&out), at_of<uint32_t>(err), stream);
-  Py_END_ALLOW_THREADS
-  if (rc != DART_OK) return failed(rc, "dart_kv_keep");
-  return THPVariable_Wrap(out);
-  END_HANDLE_TH_ERRORS
-}
-
 // The (sequence, head) strides of scores [B, heads, width]: false where the binding has to look.
 bool scores_of(const Tensor* t, int64_t B, int64_t heads, int64_t* seq, int64_t* head) {
   if (!t || t->dim() != 3 || t->size(0) != B || t->size(1) != heads || t->scalar_type() != at::kFloat ||
@@ -444,6 +418,42 @@ bool scores_of(const Tensor* t, int64_t B, int64_t heads, int64_t* seq, int64_t*
   *head = heads > 1 ? t->stride(1) : width;
   *seq = B > 1 ? t->stride(0) : heads * *head;
   return *head >= width && (B <= 1 || *seq >= *head * (heads - 1) + width);
+}
+
+// (k_cache, v_cache, pages, lengths, path, counts, scores, starts, device_err) -> lengths
+PyObject* keep(PyObject*, PyObject* const* args, Py_ssize_t count) {
+  HANDLE_TH_ERRORS
+  if (count != 9) Py_RETURN_NONE;
+  Taker take;
+  const Tensor *k_cache = take(args[0]), *v_cache = take(args[1]), *pages = take(args[2]), *lengths = take(args[3]),
+               *path = take(args[4]), *counts = take(args[5]), *scores = take(args[6]), *starts = take(args[7]),
+               *err = take(args[8]);
+  const int64_t B = lengths_of(lengths);
+  dart_cache_t c;
+  int64_t s_seq = 0, s_head = 0;
+  if (!take.ok || !kv_keep || !kv_keep_scored || B < 0 || !path || !counts ||
+      !cache_of(k_cache, v_cache, pages, B, &c) || !error_word(err) || !is(counts, at::kInt, B) || path->dim() != 2 ||
+      path->size(0) != B || path->size(1) < 1 || path->size(1) > INT_MAX || path->scalar_type() != at::kInt ||
+      (path->size(1) > 1 && path->stride(1) != 1) || (scores == nullptr) != (starts == nullptr) ||
+      (scores && (!scores_of(scores, B, c.heads, &s_seq, &s_head) || !is(starts, at::kInt, B + 1))))
+    Py_RETURN_NONE;
+  const int64_t width = path->size(1), step = B > 1 ? path->stride(0) : width;
+  if (step < width) Py_RETURN_NONE;
+  Tensor out = at::empty({B}, lengths->options());
+  int rc;
+  void* const stream = current_stream(take.device);
+  Py_BEGIN_ALLOW_THREADS
+  if (scores)
+    rc = kv_keep_scored(&c, at_of<int32_t>(lengths), at_of<int32_t>(path), step, at_of<int32_t>(counts), int(B),
+                        int(width), at_of<int32_t>(starts), at_of<float>(scores), s_seq, s_head, int(scores->size(2)),
+                        at_of<int32_t>(&out), at_of<uint32_t>(err), stream);
+  else
+    rc = kv_keep(&c, at_of<int32_t>(lengths), at_of<int32_t>(path), step, at_of<int32_t>(counts), int(B), int(width),
+                 at_of<int32_t>(&out), at_of<uint32_t>(err), stream);
+  Py_END_ALLOW_THREADS
+  if (rc != DART_OK) return failed(rc, scores ? "dart_kv_keep_scored" : "dart_kv_keep");
+  return THPVariable_Wrap(out);
+  END_HANDLE_TH_ERRORS
 }
 
 // (q, k_cache, pages, lengths, starts, lse, scores, mask, scale, device_err) -> scores
@@ -523,14 +533,15 @@ PyObject* evict(PyObject*, PyObject* const* args, Py_ssize_t count) {
   END_HANDLE_TH_ERRORS
 }
 
-// (the addresses of dart_logits_sample, dart_tree_accept, dart_kv_keep, dart_attention_weights and dart_kv_evict)
+// (the addresses of dart_logits_sample, dart_tree_accept, dart_kv_keep, dart_attention_weights, dart_kv_evict and
+// dart_kv_keep_scored)
 PyObject* bind_verified(PyObject*, PyObject* const* args, Py_ssize_t count) {
-  void* at[5];
-  if (count != 5) {
-    PyErr_SetString(PyExc_TypeError, "bind_verified takes five addresses");
+  void* at[6];
+  if (count != 6) {
+    PyErr_SetString(PyExc_TypeError, "bind_verified takes six addresses");
     return nullptr;
   }
-  for (int i = 0; i < 5; ++i) {
+  for (int i = 0; i < 6; ++i) {
     at[i] = PyLong_AsVoidPtr(args[i]);
     if (PyErr_Occurred()) return nullptr;
   }
@@ -539,6 +550,7 @@ PyObject* bind_verified(PyObject*, PyObject* const* args, Py_ssize_t count) {
   kv_keep = reinterpret_cast<decltype(kv_keep)>(at[2]);
   attention_weights = reinterpret_cast<decltype(attention_weights)>(at[3]);
   kv_evict = reinterpret_cast<decltype(kv_evict)>(at[4]);
+  kv_keep_scored = reinterpret_cast<decltype(kv_keep_scored)>(at[5]);
   Py_RETURN_NONE;
 }
 

@@ -521,8 +521,9 @@ int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * is drawn at every row (dart_logits_sample), the tree is walked along the
  * drawn tokens (dart_tree_accept), the path's keys and values move up behind
  * the root (dart_kv_keep); and, where a cache has to stay within a budget, the
- * attention that each position gets is added up (dart_attention_weights) and
- * the positions that got most stay (dart_kv_evict). */
+ * attention that each position gets is added up (dart_attention_weights) before
+ * the path moves up, moves with it (dart_kv_keep_scored), and the positions that
+ * got most stay (dart_kv_evict). */
 
 /* Draws a token from each row of logits.  With the row's tokens in descending
  * order of their logits, the lower id first where they are equal, and
@@ -594,6 +595,24 @@ int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, const int32_
                  const int32_t* counts, int B, int width, int32_t* out_lengths, uint32_t* device_err,
                  void* stream);
 
+/* dart_kv_keep of a cache whose positions gather scores (dart_attention_weights):
+ * the scores move with their positions, scores[b][h][lengths[b] + path[b][i]] to
+ * lengths[b] + i for every head, and those from lengths[b] + counts[b] to the
+ * chunk's end, lengths[b] + starts[b + 1] - starts[b], become 0.  Without it a
+ * position keeps what another node had at its place, and the next chunk's
+ * tokens begin with what rejected nodes had.
+ *  starts      device [B + 1], as for the chunk's dart_tree_attention
+ *  scores      as for dart_attention_weights, written in place.  What has no
+ *              score, from scores_width on, gives 0 where it moves to; a chunk
+ *              that reaches there sets DART_DEVERR_CACHE
+ * The scores of a sequence, or an entry, that is left out stay as they are (not
+ * those of an entry whose page id is out of range: no page is looked up for
+ * them).  Everything else as for dart_kv_keep. */
+int dart_kv_keep_scored(const dart_cache_t* cache, const int32_t* lengths, const int32_t* path,
+                        int64_t path_stride, const int32_t* counts, int B, int width, const int32_t* starts,
+                        float* scores, int64_t scores_seq_stride, int64_t scores_head_stride,
+                        int scores_width, int32_t* out_lengths, uint32_t* device_err, void* stream);
+
 /* Adds to each cached position the attention weights that a chunk's rows give
  * it: for position p and key head h,
  *   scores[b][h][p] += sum exp(scale * q.k_p - lse)
@@ -602,7 +621,9 @@ int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, const int32_
  * the same call.  fp32, summed in a fixed order; scores of other positions are
  * not touched.  A row whose lse is not finite adds nothing (a caller sets +inf to
  * leave a row out, say of a node that was not accepted), and what a row does not
- * see does not reach a score.  Only the cache's k is read.
+ * see does not reach a score.  Only the cache's k is read.  A tree's rows gather at
+ * the places of its chunk: the path's scores move with its keys and values
+ * (dart_kv_keep_scored), before the next chunk takes those places.
  *  q, lengths, starts, mask, N, scale   as for dart_tree_attention; q's strides
  *              are not 0 where they are stepped along (DART_ERR_UNSUPPORTED)
  *  lse         device float [T][q_heads]

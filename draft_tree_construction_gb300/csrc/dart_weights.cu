@@ -669,7 +669,8 @@ cudaError_t launch(WeightParams& P, const CUtensorMap& km, const CUtensorMap& qm
   constexpr int kStageBytes = DH * kTileBytes;
   // A wave's stages of K and one more at least, then buffers of Q so that the next head's
   // blocks can come while this one's are used, then stages again.
-  const int room = 227 * 1024 - int(sizeof(Shared<G>)), q = P.block * DH * kColBytes;
+  constexpr int kMost = 227 * 1024;
+  const int room = kMost - int(sizeof(Shared<G>)), q = P.block * DH * kColBytes;
   P.queries = (room - 4 * kStageBytes) / q;
   P.queries = P.queries < 2 ? 2 : P.queries > kMaxQ ? kMaxQ : P.queries;
   P.stages = (room - P.queries * q) / kStageBytes;
@@ -678,8 +679,10 @@ cudaError_t launch(WeightParams& P, const CUtensorMap& km, const CUtensorMap& qm
   P.sums = int(kTmemCols) / P.columns / G;
   P.sums = P.sums < kMaxSums ? P.sums : kMaxSums;
   const int smem = P.queries * q + P.stages * kStageBytes + int(sizeof(Shared<G>));
+  // the same limit from every call: it is the kernel's, not the launch's, and a call of another shape
+  // in another thread may come between this line and the launch
   const cudaError_t e =
-      settled(cudaFuncSetAttribute(weights_kernel<T, DH, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, smem));
+      settled(cudaFuncSetAttribute(weights_kernel<T, DH, G>, cudaFuncAttributeMaxDynamicSharedMemorySize, kMost));
   if (e != cudaSuccess) return e;
   const int sms = device_sms(), ctas = sms > 0 && sms < kCtas ? sms : kCtas;
   return launch_kernel(weights_kernel<T, DH, G>, ctas, threads_of(G), smem, s, P, km, qm);

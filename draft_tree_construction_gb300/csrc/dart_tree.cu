@@ -627,13 +627,16 @@ cudaError_t launch_tree(const TreeArgs& a, cudaStream_t stream) {
   if (a.B == 0) return cudaSuccess;
   const size_t smem = tree_smem_bytes(a.d, a.W, a.k, a.MW, a.N, a.M > 0);
   const int threads = tree_threads(a.W, a.k, a.B, device_sms());
+  // The largest tree's, from every call: the limit is the kernel's, not the launch's, and a call of
+  // another shape in another thread may come between setting it and the launch.
+  const int most = int(tree_smem_bytes(kMaxD, kMaxW, kMaxK, kMaxMW, kMaxN, true));
   cudaError_t e;
   if (a.W <= 32) {
-    e = settled(cudaFuncSetAttribute(tree_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    e = settled(cudaFuncSetAttribute(tree_kernel<1>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     if (e != cudaSuccess) return e;
     tree_kernel<1><<<a.B, threads, smem, stream>>>(a);
   } else {
-    e = settled(cudaFuncSetAttribute(tree_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, int(smem)));
+    e = settled(cudaFuncSetAttribute(tree_kernel<2>, cudaFuncAttributeMaxDynamicSharedMemorySize, most));
     if (e != cudaSuccess) return e;
     tree_kernel<2><<<a.B, threads, smem, stream>>>(a);
   }

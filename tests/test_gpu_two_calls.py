@@ -71,3 +71,30 @@ def test_attention_weights_of_other_shapes(D, dim):
     torch.cuda.synchronize()
     _together(calls, 1000)
     assert all(torch.equal(got, want) for got, want in checks)
+
+
+@pytest.mark.parametrize("shapes", [[(3, 4, 4), (32, 32, 32)], [(4, 5, 40), (15, 32, 64)]])
+def test_trees_of_other_shapes(D, shapes):
+    """Frontiers up to 32 and beyond are two kernels; trees of one kernel need other amounts of shared memory.  The C
+    entry point by itself: the binding's host work would leave the threads little to meet in."""
+    calls, checks = [], []
+    for d, k, W in shapes:
+        rng = np.random.default_rng(d)
+        ids = _i32(np.argsort(rng.random((1, d, 100)), axis=-1)[..., :k])
+        logp = torch.from_numpy(np.sort(rng.normal(size=(1, d, k)))[..., ::-1].copy()).cuda()
+        want = D.tree_from_topk(ids, logp, W, 0.0, 0.0)
+        out = {key: torch.zeros_like(x) for key, x in want.items()}
+        outs = [out[key].data_ptr() for key in ("tokens", "parents", "pos", "mask", "scores")]
+        build = D.lib().dart_tree_from_topk
+
+        def call(args=(ids.data_ptr(), logp.data_ptr(), 1, d, k, W, 0.0, 0.0, None, None, *outs)):
+            stream = torch.cuda.current_stream().cuda_stream
+            for _ in range(200):
+                rc = build(*args, stream)
+                assert rc == 0, rc
+        calls.append(call)
+        checks.append((out, want))
+    torch.cuda.synchronize()
+    _together(calls, 100)
+    for out, want in checks:
+        assert all(torch.equal(out[key], want[key]) for key in want)

@@ -111,6 +111,12 @@ __device__ __forceinline__ void cluster_sync() {
 
 constexpr int kMoveThreads = 256;
 
+// Whether entry i, `from`, may be moved: one out of order could be overwritten before it is read, or
+// name a row that another entry has.  before: the entry in front of it, -1 for the first.
+__device__ __forceinline__ bool in_order(int from, int before, int i, int end) {
+  return from >= i && from > before && from < end;
+}
+
 // The scores of one head, by one CTA: those of the list's positions move up as the rows do, those from
 // there to the chunk's end become 0, so that the next chunk's positions begin with nothing.
 __device__ __forceinline__ void move_scores(const MoveParams& P, const int32_t* list, int b, int head, int base, int count) {
@@ -121,7 +127,7 @@ __device__ __forceinline__ void move_scores(const MoveParams& P, const int32_t* 
   for (int i0 = 0; i0 < count; i0 += threads) {
     const int i = i0 + tid, from = i < count ? list[i] : i, before = i < count && i > 0 ? list[i - 1] : -1;
     bool moves = from != i;
-    if (moves && (from < i || from <= before || from >= P.cap - base)) {
+    if (i < count && !in_order(from, before, i, P.cap - base)) {
       bad = true;
       moves = false;
     }
@@ -179,8 +185,7 @@ __global__ void __launch_bounds__(kMoveThreads, 2) move_kernel(const MoveParams 
   for (int i0 = 0; i0 < count; i0 += stride) {
     const int i = next;
     bool moves = from != i;
-    // an entry out of order could be overwritten before it is read: it is left out
-    if (moves && (from < i || from <= before || from >= cap - base)) {
+    if (i < count && !in_order(from, before, i, cap - base)) {
       bad = true;
       moves = false;
     }

@@ -587,10 +587,12 @@ int dart_tree_accept(const int32_t* picks, const int32_t* tokens, const int32_t*
  *  counts      device int32 [B], 0..width
  *  out_lengths device int32 [B] or NULL: lengths[b] + counts[b].  Not lengths
  *              itself: every layer's call reads that.
+ *  B           at most 65535
  * A length or count out of range leaves the sequence and its length as they
- * are; an entry out of order, a position or a page id out of range is left out;
- * each sets DART_DEVERR_CACHE in *device_err (device uint32 or NULL).  Returns
- * DART_OK or an error code. */
+ * are; an entry out of order (not above the one before it, or below its place),
+ * a position or a page id out of range is left out; each sets DART_DEVERR_CACHE
+ * in *device_err (device uint32 or NULL).  No page is looked up for an entry that
+ * stays where it is.  Returns DART_OK or an error code. */
 int dart_kv_keep(const dart_cache_t* cache, const int32_t* lengths, const int32_t* path, int64_t path_stride,
                  const int32_t* counts, int B, int width, int32_t* out_lengths, uint32_t* device_err,
                  void* stream);
@@ -657,10 +659,11 @@ int dart_attention_weights(const void* q, int64_t q_token_stride, int64_t q_head
  *  out_index   device int32 [B][heads][keep]: the old position of each slot; -1
  *              from the length on
  *  out_lengths device int32 [B] or NULL: min(length, keep).  Not lengths itself.
+ *  B           at most 65535
  * A length beyond the table's pages or scores_width leaves the sequence and its
- * length as they are, a page id out of range the rows in it; either sets
- * DART_DEVERR_CACHE in *device_err (device uint32 or NULL).  Returns DART_OK or
- * an error code. */
+ * length as they are, a page id out of range the rows that would move from it or
+ * to it; either sets DART_DEVERR_CACHE in *device_err (device uint32 or NULL).
+ * Returns DART_OK or an error code. */
 int dart_kv_evict(const dart_cache_t* cache, const int32_t* lengths, int B, float* scores,
                   int64_t scores_seq_stride, int64_t scores_head_stride, int scores_width, int keep,
                   int first, int last, int32_t* out_index, int32_t* out_lengths, uint32_t* device_err,

@@ -284,6 +284,8 @@ def _cache(k_cache, v_cache, pages, B):
     elif step < width:
         raise DartError("the rows of pages overlap")
     count, page, heads, dim = shape
+    if (width | count | page | heads) >> 31:       # the descriptor holds them in 32 bits
+        raise DartError(f"{max(width, count, page, heads)} is more than a cache can have of anything")
     if page < 8 or page & 7:
         raise DartError(f"pages must hold a multiple of 8 positions, got {page}")
     if not 8 <= dim <= 128 or dim & 7:

@@ -46,6 +46,15 @@ def _native():
     return module
 
 
+_MOST = 2 ** 31 - 1
+
+
+def _sizes(*counts):
+    """Sizes that the entry points take as 32-bit integers, which ctypes would cut to their lower half."""
+    if max(counts) > _MOST:
+        raise DartError(f"sizes must be at most {_MOST}, got {max(counts)}")
+
+
 # ----------------------------------------------------------------- sampling
 
 def sample_logits(logits, uniforms, *, temperature=None, top_k=None, top_p=None, min_p=None, stream=None) -> dict:
@@ -74,6 +83,7 @@ def sample_logits(logits, uniforms, *, temperature=None, top_k=None, top_p=None,
     B, R, V = logits.shape
     if V < 1:
         raise DartError("logits must have at least one token")
+    _sizes(B, R, V)
     stride = V if logits.is_contiguous() else _row_stride(logits)
     _check_tensor(uniforms, "uniforms", torch.float32, (B, R))
     for t, name in ((temperature, "temperature"), (top_p, "top_p"), (min_p, "min_p")):
@@ -116,6 +126,7 @@ def tree_accept(picks, tokens, parents, depth: int, *, stream=None) -> dict:
     if tokens.dim() != 2:
         raise DartError("tokens must be [B, N]")
     B, N = tokens.shape
+    _sizes(B, N)
     _check_tensor(tokens, "tokens", torch.int32)
     _check_tensor(parents, "parents", torch.int32, (B, N))
     _check_tensor(picks, "picks", torch.int32, (B, N + 1))
@@ -169,6 +180,7 @@ def kv_keep(k_cache, v_cache, pages, lengths, path, counts, *, scores=None, star
     _check_tensor(path, "path", torch.int32, contiguous=False)
     _check_inner(path, "path")
     width = path.shape[1]
+    _sizes(B, width)
     step = path.stride(0) if B > 1 else width
     if step < width:
         raise DartError("the rows of path overlap")
@@ -203,6 +215,7 @@ def _scores(scores, B, heads):
     _check_tensor(scores, "scores", _torch().float32, contiguous=False)
     _check_inner(scores, "scores")
     width = scores.shape[2]
+    _sizes(B, width)
     a, b = scores.stride(0) if B > 1 else heads * width, scores.stride(1) if heads > 1 else width
     low, high = sorted(((a, B), (b, heads)))
     if width and ((heads > 1 and b < width) or (B > 1 and a < width) or
@@ -234,6 +247,7 @@ def attention_weights(q, k_cache, pages, lengths, starts, lse, scores, *, mask=N
     if q.dim() != 3:
         raise DartError("q must be [T, q_heads, dim]")
     T, Hq, dim = q.shape
+    _sizes(T, Hq)
     q0, q1 = _output(q, "q", T, Hq, c.dim, k_cache.dtype)         # copied in boxes, which an expanded tensor has not
     if Hq < 1 or Hq % c.heads:
         raise DartError(f"{Hq} query heads do not share {c.heads} key heads evenly")
@@ -244,6 +258,7 @@ def attention_weights(q, k_cache, pages, lengths, starts, lse, scores, *, mask=N
         if mask.dim() != 3 or mask.shape[0] != B or mask.shape[2] != (mask.shape[1] + 31) // 32:
             raise DartError(f"mask must be [{B}, N, ceil(N / 32)]")
         N = mask.shape[1]
+        _sizes(N)
         _check_tensor(mask, "mask", _mask_dtypes())
     if device_err is not None:
         _check_error_word(device_err)
@@ -282,6 +297,7 @@ def kv_evict(k_cache, v_cache, pages, lengths, scores, keep: int, *, first: int 
     B = _one_length(lengths)
     c = _cache(k_cache, v_cache, pages, B)
     s0, s1 = _scores(scores, B, c.heads)
+    _sizes(keep)
     if keep < 1 or first < 0 or last < 0 or first + last > keep:
         raise DartError(f"keep ({keep}) must hold the first {first} and the last {last} positions, and be at least 1")
     if device_err is not None:

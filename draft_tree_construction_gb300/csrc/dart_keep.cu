@@ -25,14 +25,16 @@
 // once, into registers; each level is a histogram in shared memory, which the cluster's
 // CTAs read from one another, and a scan.  Then every warp counts what it keeps by ballots,
 // one scan gives all places, and the list and the scores, which have all been read by then,
-// are written.  Latency bounds it.  Sequences beyond what registers hold (163840 positions
-// a head) are read again at every level by one CTA (long_kernel).
+// are written.  Latency bounds it.  Where the page table and the scores have room for more than
+// registers hold (163840 positions a head), whatever the lengths are, one CTA a head reads them
+// again at every level (long_kernel).
 //
 // Measured (GB300, graph-replayed): a tree walked and its path moved, 8 heads of 128, 6.4 us
 // for one tree of 78 nodes, 8.4 for 64 of 496 (two launches).  Eviction of fresh scores: 32
 // sequences of about 6000 positions to 2048, 105 us, 80 of them the moves (6.7 TB/s); one of
-// 32768 to 16384, 50 us: 20 the selection (three cluster barriers a level), 30 the moves of
-// 128 CTAs (4.5 TB/s).  Where hardly any row moves: 36 and 28.
+// 32768 to 16384, 50 us: 20 the selection (eight cluster barriers in a chain: two a level, one before
+// the places, one at the end), 30 the moves of 128 CTAs (4.5 TB/s).  Where hardly any row moves: 36 and
+// 28.  A path's scores moved and cleared with its rows add nothing to the 4.1 and 6.2 us of the move.
 #include "dart_launch.h"
 
 namespace dart {
@@ -558,6 +560,9 @@ cudaError_t launch_select(const SelectParams& S, int B, cudaStream_t s) {
   // As many CTAs a head as its positions need, and up to two an SM in all while each has
   // 2048 positions at least; the moves below likewise (both together, with and without: one
   // sequence of 32768 to 16384, 8 heads 48 us for 127, one head 35 for 119; 4 of 8192 to 4096 34 for 45).
+  // Lengths are on the device, so the positions are those that the table and the scores have room for:
+  // a table much wider than its sequences costs (32 sequences of 6016 to 2048: 103 us in tables for 8192
+  // positions, 190 for 65536, eight CTAs a head that each find little; 112 for 262144, long_kernel).
   const int sms = device_sms() > 0 ? device_sms() : 152;
   int ranks = 1;
   while (ranks < kMaxRanks && (S.cap > kShareThreads * 20ll * ranks ||

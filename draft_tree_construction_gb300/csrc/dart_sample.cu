@@ -17,10 +17,11 @@
 // equal values, several limits far down) goes by general(), a histogram of the values.
 //
 // Which token a random number falls on is a matter of the last bits of sums over the
-// whole vocabulary, so weights are 64-bit integers, good to 2^-45, and their sums exact in
-// any order.  Only sums of what is not listed are taken with less (the bounds are at Tail
-// and Mid); where a place lies so near to an edge that this could matter, the next form
-// decides, general() at last.  Results are the same bits every time.
+// whole vocabulary, so weights are 64-bit integers, good to 2^-42 of themselves (to 2^-28
+// below 2^-16 of the largest) and to a part, and their sums exact in any order.  Only sums of
+// what is not listed are taken with less (the bounds are at Tail and Mid); where a place lies
+// so near to an edge that this could matter, the next form decides, general() at last.  A
+// call gives the same bits every time.
 //
 // Rows that are fewer than the SMs are shared by up to eight CTAs of a cluster, which hand
 // their largest logit, list and sum to the first one through distributed shared memory.
@@ -124,7 +125,7 @@ struct Bins {
 // ------------------------------------------------------------------- weights
 // Two forms, the top and the factor c = log2(e) / T in two parts for both; `table` has
 // 2^-j/256 in units of 2^-63, `shift` says that 1 is 2^shift.
-struct Mid {                                 // 2^-y to 2^-29 of itself
+struct Mid {                                 // 2^-y to 2^-28 of itself, less a part
   float top, c_hi, c_lo;
   int shift;
   const uint64_t* table;
@@ -134,8 +135,9 @@ struct Mid {                                 // 2^-y to 2^-29 of itself
     rest = fmaf(d, c_hi, -y) + fmaf(d, c_lo, e * c_hi);
     return y;
   }
-  // y = whole + j / 256 + r, |r| <= 2^-9: 2^-r - 1 in fp32 (2^-33 of 1), 2^-j/256 and their
-  // product in parts of 2^-31
+  // y = whole + j / 256 + r, |r| <= 2^-9: 2^-r - 1 in fp32 (half a unit of 2^-31), rounded to such
+  // units (half of one), 2^-j/256 and the product cut to them (one each): 3 units of at least
+  // 2^30 (1 - 2^-9), less than 2^-28 (2^-28.9 is the most that was seen)
   __device__ __forceinline__ uint64_t power(float y, float rest) const {
     constexpr float kRound = 12582912.f;     // 1.5 2^23: a sum with it is a whole number
     const float n = fmaf(y, 256.f, kRound);
@@ -153,8 +155,9 @@ struct Mid {                                 // 2^-y to 2^-29 of itself
     return y < 62.f ? power(y, rest) : 0ull;
   }
 };
-struct Weigh : Mid {                         // to 2^-45 of the largest
-  // 2^-(y + rest) in units of 2^-63, 0 <= y < 62
+struct Weigh : Mid {                         // to 2^-42 of itself, below 2^-16 as Mid
+  // 2^-(y + rest) in units of 2^-63, 0 <= y < 62.  Where its terms are cut costs 2^-46.5 of itself,
+  // y's own error, 2^-47 y ln 2 by the factor in two parts, 2^-43.5 at y = 16
   __device__ __forceinline__ uint64_t exact(float y, float rest) const {
     // y in units of 2^-48: whole part, 256ths, remainder r
     const long long Y = (long long)(y * 281474976710656.f) + __float2ll_rn(rest * 281474976710656.f);
@@ -515,7 +518,7 @@ __device__ __noinline__ void general(const SampleParams& P, const T* logits, lon
   if constexpr (B::kSingle) {
     // Neighbours of one exponent lie one step apart, so each weight is the last one times the
     // same factor: a product instead of a power.  Taken afresh at least every 16 bins, so that
-    // the factor's error, 2^-49, does not add up to 2^-45.
+    // the factor's error, 2^-46.5, does not add up to more than 2^-42.5 (2^-43.8 is the most seen).
     int exponent = -1, steps = 0;
     uint64_t w = 0, factor = 0;
     const int end = mine > 0 ? min(bin1, last_bin + 1) : bin0;
@@ -1081,10 +1084,15 @@ __device__ __forceinline__ float max_of(const uint4& x) {
   }
 }
 
-// Weights of tokens that are not listed, 2^-12 at most, in fp32.  The exponent y < 64 (what
-// lies beyond adds less than a part) is off by (2^-25 + 2^-25) y, the factor c and the
-// product, so the weight by 2^-24 64 ln 2 < 2^-18 of itself; ex2 and the sum of a vector's
-// eight add 2^-21; a vector's sum is rounded to a whole part.
+// Weights of tokens that are not listed, 2^-12 at most, in fp32 (u = 2^-24, half a step).  The
+// exponent y is a rounded difference (u) times a factor (u by its rounding, 0.23 u by the part of
+// log2(e) that is left out) in a rounded product (u), so off by 3.23 u y, and the weight by
+// ln 2 of that, 2.24 u y of itself; ex2 is off by 4 u, a sum of eight by 4 u.  Together
+// (2.24 y + 8) u: 2^-17 of the weight up to y = 53.  A weight beyond that is less than a part, because
+// rows with a list have more than 256 tokens and parts of 2^-53 or more, and its error, 2^-16.7 of it up
+// to y = 64, next to nothing.  A vector's sum is rounded to a whole part, half of one for four tokens or
+// more (the few outside vectors one by one), and what stands in for a listed token weighs less than 2^-10 of a part.  So a row's sum is
+// within 2^-17 of itself and V parts: the guard band of a list that is not complete.
 template <typename T>
 struct Tail {
   float top, c, one;                         // one: 2^shift
@@ -1379,8 +1387,11 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
   };
   again(rest_counts, cut, list_one, list_vec);
   // Whether a list that does not decide is made again where a plan says: of 16-bit logits
-  // general() is quicker (100 thousand cycles for 200 with 32000 of them), but for the first
-  // top_k of a large vocabulary (4 x 497 rows of 151936, top_k 1000 for some: 424 us for 362).
+  // general() is quicker (100 thousand cycles for 200 with 32000 of them).  It was not for the first
+  // top_k of a large vocabulary before the maxima bounded lists up to 1024, which need no plan now.
+  // What is left for this rule, top_k above that, mostly loses by it (plan for general(); 1988 rows of
+  // 151936: bf16, top_k 2000 1250..1286 us for 944..986, fp16 1129..1312 for 1214..1271, top_k 8000
+  // 1499..1547 for 1227..1270; of 66000, bf16 738..815 for 519..540; top_k 1000 473..476 for 468..472).
   const bool plans = sizeof(T) == 4 || (ranks == 1 && S.by_k && V > 65536);
   bool planned = false;
   for (;;) {
@@ -1572,7 +1583,7 @@ __global__ void __launch_bounds__(NT, kCtas) sample_kernel(const SampleParams P)
     }
     if (v == kDone) return;
     if (v == kGeneral) break;
-    // ---- the list again, around that place; the sums of the others to 2^-29
+    // ---- the list again, around that place; the sums of the others to 2^-28 and a part each
     cut = sh->cut;
     const float cut_above = sh->cut_above;
     planned = true;
@@ -1664,13 +1675,17 @@ cudaError_t launch(SampleParams& P, cudaStream_t s) {
   cfg.attrs = at;
   cfg.numAttrs = 1;
   if (P.rows <= (sizeof(T) == 4 ? 4 : 2) * sms) {
-    // Large CTAs that do all for their rows.  Up to two rows an SM: 304 bf16 rows of 32000 83 us for 106
-    // by the kernels below, 64 x 79 fp16 ones 368 for 311.  Up to four where logits have 32 bits and
-    // plans take long: 500 rows of 32000 114 us for 139, 608 with top-p 292 for 391 (with top-k 40
-    // for 27), 5000 of 2000 668 for 550.
+    // Large CTAs that do all for their rows, against the kernels below (us, in that order).  16 bits: 304
+    // rows of 32000 83 for 106, 64 x 79 fp16 ones 368 for 311, 1988 of 151936 with all limits 189..365 for
+    // 127..349.  32 bits: 500 rows of 32000 114 for 139, 608 with top-p 292 for 391, 5000 of 2000 668 for
+    // 550.  The number of rows alone decides, and is not right for all: flat 16-bit rows of 32000 with
+    // top-p alone would go better by the large CTAs far beyond two an SM (320 rows 90 for 111, 608 140 for
+    // 175, 1988 379 for 421), 32-bit rows without top-k beyond four (2000 of 32000 476 for 589, 700 of
+    // 151936 629 for 1153, with top-p 1202 for 1680; peaked ones of 32000 347 for 325), those with top-k by
+    // the small ones from one an SM on (320 of 32000 31 for 23, 608 39 for 27).
     // Rows that do not fill the device are shared: as many CTAs a row as keep it to one round
     // of two an SM, none with less than 4096 logits (one row of 151936 60 us for 72 by one CTA, where
-    // it goes by general(); 20 rows 110 for 109).
+    // it goes by general(); 20 rows 110 for 109; 76 rows 115 for 107, where one CTA a row is quicker).
     const auto kernel = sample_kernel<T, kThreads, 2, true>;
     const cudaError_t e = settled(cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, large));
     if (e != cudaSuccess) return e;

@@ -533,9 +533,11 @@ int dart_tree_attention(const void* q, int64_t q_token_stride, int64_t q_head_st
  * first top_k, n_m the number of w_i >= min_p.  The token drawn is the first
  * whose running sum exceeds u times the sum of the n kept; its probability is
  * w / that sum.  Weights are integers of 2^(62 - ceil(log2(V + 1))) parts of
- * the largest, exact to a few of them, and a draw is what their exact sums say.
- * The probability is rounded once; without any limit the sum in it holds the
- * weights below 2^-12 to 2^-18 of theirs.
+ * the largest, each good to 2^-42 of itself (2^-28 below 2^-16 of the largest)
+ * and a part, and their sums are exact: a draw is that of exact weights unless its
+ * place, or that of top_p, lies so near an edge between two tokens.  The
+ * probability is rounded once; without any limit the sum in it holds the
+ * weights below 2^-12 to 2^-17 of theirs and a part each.
  * NaN and -inf are never drawn; a row without any other logit gives token -1
  * and probability 0.  +inf is drawn before anything finite, and a difference
  * beyond FLT_MAX counts as infinite, at any temperature.

@@ -1088,11 +1088,12 @@ __device__ __forceinline__ float max_of(const uint4& x) {
 // exponent y is a rounded difference (u) times a factor (u by its rounding, 0.23 u by the part of
 // log2(e) that is left out) in a rounded product (u), so off by 3.23 u y, and the weight by
 // ln 2 of that, 2.24 u y of itself; ex2 is off by 4 u, a sum of eight by 4 u.  Together
-// (2.24 y + 8) u: 2^-17 of the weight up to y = 53.  A weight beyond that is less than a part, because
-// rows with a list have more than 256 tokens and parts of 2^-53 or more, and its error, 2^-16.7 of it up
-// to y = 64, next to nothing.  A vector's sum is rounded to a whole part, half of one for four tokens or
-// more (the few outside vectors one by one), and what stands in for a listed token weighs less than 2^-10 of a part.  So a row's sum is
-// within 2^-17 of itself and V parts: the guard band of a list that is not complete.
+// (2.24 y + 8) u: 2^-17 of the weight up to y = 53.  A weight beyond that is less than a part, as
+// rows with a list have more than 256 tokens and parts of 2^-53 or more, and its error, 2^-16.7 of
+// it up to y = 64, next to nothing.  A vector's sum is rounded to a whole part, half of one for
+// four tokens or more (the few outside vectors one by one), and what stands in for a listed token
+// weighs less than 2^-10 of a part.  So a row's sum is within 2^-17 of itself and V parts: the guard
+// band of a list that is not complete.
 template <typename T>
 struct Tail {
   float top, c, one;                         // one: 2^shift
